@@ -281,6 +281,40 @@ int tlb_linear_backward(int32_t wtype, const void *W, float scale, const float *
 int tlb_adamw(float *p, const float *g, float *m, float *v, int64_t n,
               const tlb_adamw_cfg *cfg, float lr_mult, double *sumsq, void *stream);
 
+/* ---------------------------------------------------------------- the loss above the stack */
+
+/* Softmax cross entropy of a linear head without the logits in memory, and its gradient,
+ * the dOut that enters the top layer ([RS] backward_through_layers takes it as given):
+ *   z[i, v] = sum_d hidden[i, d] W[v, d]     lse[i] = log sum_v exp z[i, v]
+ *   forward:   loss[i] = lse[i] - z[i, targets[i]]
+ *   backward:  dz[i, v] = d_loss[i] (exp(z[i, v] - lse[i]) - [v = targets[i]])
+ *              d_hidden = dz W,   d_w = dz^T hidden (where d_w is not NULL)
+ * hidden [rows, dim] and W [vocab, dim] (one row per vocabulary entry, the layout of an
+ * embedding table), both dense and 16-byte aligned; targets [rows] int64; loss, lse, d_loss
+ * [rows] float32.  A target outside [0, vocab) marks a row without one (prompt, padding):
+ * its loss is 0, its d_hidden row 0, and it adds nothing to d_w, whatever its hidden row and
+ * lse hold; its lse is that of its logits all the same.
+ *
+ * Types (TLB_W_F32, TLB_W_BF16): hidden and W both bf16; hidden f32 with W bf16 or f32.
+ * d_hidden and d_w (both overwritten) have hidden's type.  All run on the tcgen05 tensor
+ * cores with fp32 sums.  bf16 hidden: dz is rounded to bf16 once as the operand of the
+ * gradient products.  f32 hidden: every float32 operand, dz included, is taken apart into
+ * three bf16 terms that hold all its 24 bits, for results of float32 precision at a third
+ * (W bf16) or a sixth (W f32) of the speed.
+ *
+ * rows >= 0 (0 rows: no-op, d_w set to 0), vocab >= 1, dim >= 1, of any size up to 2^24,
+ * 2^24 and 2^20 (dim % 8 != 0 costs a padded copy of the operands).  The backward pass walks
+ * through the vocabulary in pieces whose dz stays in the workspace (512 MB at most; at
+ * least 2048 columns).  Same inputs, same bits: no sum depends on timing.
+ * ws: zero-filled once, 256-byte aligned, tlb_xent_workspace_bytes() bytes (enough for both
+ * calls; 0 for sizes or types that the calls refuse).  grad_w: whether d_w will be asked for. */
+size_t tlb_xent_workspace_bytes(int32_t htype, int32_t wtype, int64_t rows, int64_t vocab, int64_t dim, int32_t grad_w);
+int tlb_xent_forward(int32_t htype, const void *hidden, int32_t wtype, const void *W, const int64_t *targets, int64_t rows,
+                     int64_t vocab, int64_t dim, float *loss, float *lse, void *ws, size_t ws_bytes, void *stream);
+int tlb_xent_backward(int32_t htype, const void *hidden, int32_t wtype, const void *W, const int64_t *targets,
+                      const float *lse, const float *d_loss, int64_t rows, int64_t vocab, int64_t dim, void *d_hidden,
+                      void *d_w, void *ws, size_t ws_bytes, void *stream);
+
 /* ---------------------------------------------------------------- layer pieces */
 
 /* Workspace bytes needed by tlb_ffn_backward / tlb_attn_backward /

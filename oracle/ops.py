@@ -177,3 +177,35 @@ def adamw(p, g, m, v, lr, beta1, beta2, eps, wd, step: int):
     v = beta2 * v + (1.0 - beta2) * g * g
     p = p - lr * ((m * bc1) / (np.sqrt(v * bc2) + eps) + wd * p)
     return p, m, v
+
+
+def xent_forward(hidden, w, targets):
+    """Softmax cross entropy of the linear head w [vocab, dim] on hidden [rows, dim].
+
+    z = hidden w^T;  lse[i] = log sum_v exp z[i, v];  loss[i] = lse[i] - z[i, targets[i]].
+    A target outside [0, vocab) marks a row without one: loss 0.  Returns (loss, lse).
+    """
+    z = f64(hidden) @ f64(w).T
+    top = z.max(axis=1, keepdims=True)
+    lse = (top + np.log(np.sum(np.exp(z - top), axis=1, keepdims=True)))[:, 0]
+    t = np.asarray(targets)
+    has = (t >= 0) & (t < z.shape[1])
+    at = z[np.arange(len(t)), np.where(has, t, 0)]
+    return np.where(has, lse - at, 0.0), lse
+
+
+def xent_dlogits(hidden, w, targets, lse, d_loss):
+    """dz[i, v] = d_loss[i] (exp(z[i, v] - lse[i]) - [v = targets[i]]), 0 in rows without a target."""
+    z = f64(hidden) @ f64(w).T
+    t = np.asarray(targets)
+    has = (t >= 0) & (t < z.shape[1])
+    dz = np.exp(z - f64(lse)[:, None])
+    dz[np.arange(len(t))[has], t[has]] -= 1.0
+    return np.where(has[:, None], dz * f64(d_loss)[:, None], 0.0)
+
+
+def xent_backward(hidden, w, targets, lse, d_loss):
+    """Gradient of sum_i d_loss[i] loss[i]: (d_hidden, d_w) = (dz w, dz^T hidden)."""
+    dz = xent_dlogits(hidden, w, targets, lse, d_loss)
+    has = (np.asarray(targets) >= 0) & (np.asarray(targets) < np.shape(w)[0])
+    return dz @ f64(w), dz.T @ np.where(has[:, None], f64(hidden), 0.0)

@@ -70,6 +70,9 @@ SIGNATURES = {
     "tlb_rmsnorm_backward": (C.c_int, [vp, vp, vp, vp, i64, i64, f32, i32, vp]),
     "tlb_rope_backward": (C.c_int, [vp, vp, i64, i32, i32, i64, f32, vp]),
     "tlb_adamw": (C.c_int, [vp, vp, vp, vp, i64, P(AdamwCfg), f32, vp, vp]),
+    "tlb_xent_workspace_bytes": (sz, [i32, i32, i64, i64, i64, i32]),
+    "tlb_xent_forward": (C.c_int, [i32, vp, i32, vp, vp, i64, i64, i64, vp, vp, vp, sz, vp]),
+    "tlb_xent_backward": (C.c_int, [i32, vp, i32, vp, vp, vp, vp, i64, i64, i64, vp, vp, vp, sz, vp]),
     "tlb_workspace_bytes": (sz, [P(LayerCfg), i64, i64]),
     "tlb_workspace_status": (C.c_int, [vp, sz, vp]),
     "tlb_ffn_backward": (C.c_int, [P(LayerCfg), i64, vp, P(LayerWeights), P(LayerActs), vp, vp,

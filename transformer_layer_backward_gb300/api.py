@@ -6,6 +6,7 @@ here; every step runs in the CUDA kernels of ``lib/libtlb.so``.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes as C
 import math
 
@@ -16,6 +17,11 @@ from . import _abi as A
 _WDTYPE = {A.W_F32: torch.float32, A.W_BF16: torch.bfloat16, A.W_TERNARY_I8: torch.int8,
            A.W_TERNARY_2B: torch.uint8}
 _WCODE = {"f32": A.W_F32, "bf16": A.W_BF16, "ternary": A.W_TERNARY_I8, "ternary2": A.W_TERNARY_2B}
+
+
+def _on_device(t):
+    """Guard that makes the tensor's device the current one, for the launch and the stream."""
+    return torch.cuda.device(t.device) if t.is_cuda else contextlib.nullcontext()
 
 
 def _stream(stream):
@@ -141,6 +147,75 @@ def adamw(p, g, m, v, cfg: A.AdamwCfg, lr_mult=1.0, sumsq=None, stream=None):
     A.call("tlb_adamw", _ptr(p, name="p"), _ptr(g, name="g"), _ptr(m, name="m"),
            _ptr(v, name="v"), p.numel(), C.byref(cfg), float(lr_mult),
            _ptr(sumsq, torch.float64, "sumsq"), _stream(stream))
+
+
+# ------------------------------------------------------------------ the loss above the stack
+
+_XENT_CODE = {torch.float32: A.W_F32, torch.bfloat16: A.W_BF16}
+
+
+def _xent_code(dtype, name):
+    if dtype not in _XENT_CODE:
+        raise TypeError("%s must be float32 or bfloat16, got %s" % (name, dtype))
+    return _XENT_CODE[dtype]
+
+
+def _xent_shapes(hidden, W, targets, **per_row):
+    if hidden.dim() != 2 or W.dim() != 2 or hidden.shape[1] != W.shape[1]:
+        raise ValueError("hidden [rows, dim] and W [vocab, dim] expected, got %s and %s"
+                         % (tuple(hidden.shape), tuple(W.shape)))
+    rows = hidden.shape[0]
+    for name, t in dict(per_row, targets=targets).items():
+        if t is not None and tuple(t.shape) != (rows,):
+            raise ValueError("%s must have shape (%d,), got %s" % (name, rows, tuple(t.shape)))
+    for name, t in dict(per_row, W=W, targets=targets).items():
+        if t is not None and t.device != hidden.device:
+            raise ValueError("%s is on %s, hidden on %s" % (name, t.device, hidden.device))
+    return rows, W.shape[0], W.shape[1]
+
+
+def xent_workspace(hidden_dtype, weight_dtype, rows, vocab, dim, grad_w=False, device="cuda"):
+    """A zeroed workspace tensor for xent_forward and xent_backward (grad_w: with the head's
+    gradient) of these sizes."""
+    n = int(A.load().tlb_xent_workspace_bytes(_xent_code(hidden_dtype, "hidden"), _xent_code(weight_dtype, "W"),
+                                              int(rows), int(vocab), int(dim), 1 if grad_w else 0))
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
+
+
+def xent_forward(hidden, W, targets, loss=None, lse=None, ws=None, stream=None):
+    """Per-row cross entropy of the linear head W [vocab, dim] on hidden [rows, dim], without
+    the logits: (loss, lse).  Targets (int64) outside [0, vocab) mark rows without one."""
+    rows, vocab, dim = _xent_shapes(hidden, W, targets, loss=loss, lse=lse)
+    ht, wt = _xent_code(hidden.dtype, "hidden"), _xent_code(W.dtype, "W")
+    loss = torch.empty(rows, device=hidden.device) if loss is None else loss
+    lse = torch.empty(rows, device=hidden.device) if lse is None else lse
+    ws = xent_workspace(hidden.dtype, W.dtype, rows, vocab, dim, device=hidden.device) if ws is None else ws
+    with _on_device(hidden):
+        A.call("tlb_xent_forward", ht, _ptr(hidden, None, "hidden"), wt, _ptr(W, None, "W"),
+               _ptr(targets, torch.int64, "targets"), rows, vocab, dim, _ptr(loss, name="loss"), _ptr(lse, name="lse"),
+               _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream))
+    return loss, lse
+
+
+def xent_backward(hidden, W, targets, lse, d_loss, d_hidden=None, d_w=None, grad_w=False, ws=None, stream=None):
+    """Gradient of sum(d_loss * loss): (d_hidden, d_w), in hidden's dtype; d_w [vocab, dim] is
+    None unless grad_w is set or a tensor for it is given.  lse as xent_forward returned it."""
+    rows, vocab, dim = _xent_shapes(hidden, W, targets, lse=lse, d_loss=d_loss)
+    ht, wt = _xent_code(hidden.dtype, "hidden"), _xent_code(W.dtype, "W")
+    d_hidden = torch.empty_like(hidden) if d_hidden is None else d_hidden
+    if d_w is None and grad_w:
+        d_w = torch.empty(vocab, dim, dtype=hidden.dtype, device=hidden.device)
+    for name, t, shape in (("d_hidden", d_hidden, hidden.shape), ("d_w", d_w, W.shape)):
+        if t is not None and (t.shape != shape or t.device != hidden.device):
+            raise ValueError("%s must have shape %s on %s" % (name, tuple(shape), hidden.device))
+    if ws is None:
+        ws = xent_workspace(hidden.dtype, W.dtype, rows, vocab, dim, d_w is not None, hidden.device)
+    with _on_device(hidden):
+        A.call("tlb_xent_backward", ht, _ptr(hidden, None, "hidden"), wt, _ptr(W, None, "W"),
+               _ptr(targets, torch.int64, "targets"), _ptr(lse, name="lse"), _ptr(d_loss, name="d_loss"), rows, vocab,
+               dim, _ptr(d_hidden, hidden.dtype, "d_hidden"), _ptr(d_w, hidden.dtype, "d_w"),
+               _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream))
+    return d_hidden, d_w
 
 
 # ------------------------------------------------------------------ layer pieces

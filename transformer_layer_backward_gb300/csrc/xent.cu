@@ -1,0 +1,1014 @@
+// Softmax cross entropy of a linear head, and its gradient, without the logits in memory:
+//   z[i, v] = <hidden[i], W[v]>,  lse[i] = log sum_v exp z[i, v],  loss[i] = lse[i] - z[i, t_i]
+//   dz[i, v] = d_loss[i] (exp(z[i, v] - lse[i]) - [v = t_i])
+//   d_hidden = dz W,  d_w = dz^T hidden
+// with hidden [N, D] (token rows), W [V, D] (one row per vocabulary entry) and t_i a column
+// of [0, V) or outside it (no target: loss 0, dz = 0).
+//
+// Every product runs on one tcgen05 kernel.  Its modes differ in what becomes of an
+// accumulator tile (rows x columns of z or of a gradient):
+//   kStats  running maximum and sum of exponentials of each row over the tile's columns, and
+//           the target's logit; the logits never leave tensor memory.  A second kernel joins
+//           the tiles' pairs in column order.
+//   kGrad   dz of the tile, rounded to bf16, by TMA into a piece of the vocabulary's dz
+//           [N, piece] in the workspace
+//   kOut    d_hidden (+)= dz W over one piece, or d_w of the piece: fp32 sums, stream-K
+// Operands of either order: a K-major operand has the summed index along its rows (hidden
+// and W in z), an MN-major one across them (W in dz W, dz and hidden in dz^T hidden); both
+// are staged by TMA with 128-byte swizzle, so nothing is transposed in memory.
+//
+// Float32 operands are taken apart into three bf16 terms of 8 bits each, x = x0 + x1 + x2
+// exactly, and the product is the sum of the term products down to 2^-24 of the first: three
+// with a bf16 partner (exact), six between two float32 operands (x_i y_j with i + j <= 2).
+// With bf16 operands dz is rounded to bf16 once (2^-8 at most, relative to each dz; the sums
+// of it are in fp32): its own error in d_hidden is that of d_hidden's rounding to bf16.
+//
+// The tensor core cuts its fp32 sum after every MMA of 16 products (measured: a sum of 160
+// MMAs comes out about 1.2e-6 of its size short, one of 6144 3e-5).  Results of float32
+// precision are therefore summed in chunks of kChunk k blocks, which the epilogue adds up in
+// registers, and the smaller term products come first, while the sum is small.
+//
+// Bounds: N >= 512 rows is bound by the tensor pipe (2 N V D flops a product), few rows by
+// the read of W.
+#include <cuda.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "async.cuh"
+#include "common.cuh"
+#include "kernels.cuh"
+#include "tc.cuh"
+
+namespace tlb {
+
+namespace {
+
+constexpr int kBM = 128, kBK = 64;          // rows of a CTA's tile; k block (64 bf16 = 128 bytes)
+constexpr int kThreads = 320;               // 10 warps: TMA producer, MMA issuer, 8 epilogue warps
+constexpr int kEpiWarps = 8;                // two per 32 TMEM lanes (rows), each half of the columns
+constexpr int kMaxTerms = 3, kMaxProd = 6;
+constexpr int kChunk = 20;                  // k blocks (80 MMAs) of one tensor-memory sum of a float32 result
+constexpr int kGroupM = 16;                 // row tiles that share a column tile before the next one
+constexpr int kBox = 4096;                  // bytes of a 32 x 64 bf16 box of dz
+constexpr float kLog2e = 1.4426950408889634f;
+
+enum Mode { kStats = 0, kGrad = 1, kOut = 2 };
+
+struct XParams {
+    CUtensorMap a[kMaxTerms], b[kMaxTerms];  // operand terms
+    CUtensorMap d[kMaxTerms];                // kGrad: dz terms [rows, piece], boxes of 64 x 32
+    int nprod;                               // the product is the sum of a[pa[i]] b[pb[i]]
+    int8_t pa[kMaxProd + 2], pb[kMaxProd + 2];
+    int kb;                                  // k blocks of one term product
+    int M, N;                                // rows and columns of the result
+    int tiles_m, tiles_n;
+    int units;                               // CTAs (pairs): unit u does the whole tiles u, u + units, ...
+    int64_t whole;                           // ... below `whole`, then its share of the other tiles'
+    int64_t sk_work;                         // k blocks (kOut: split evenly over sk_units units)
+    int sk_units;
+    // kStats, kGrad
+    const int64_t *targets;
+    int64_t vocab, v0;                       // columns in all, first column of this piece
+    float2 *part;                            // kStats: (max, sum) [slot0 + 2 tile_n + half][ld_part]
+    int64_t ld_part;
+    float *zt;                               // kStats: logit of the target
+    const float *lse, *dloss;                // kGrad
+    // kOut
+    const float *acc;                        // sum of the earlier pieces [M, N], or null
+    float *out32;                            // one of the two is written
+    __nv_bfloat16 *out16;
+    int vec;                                 // N % 4 == 0 and 16-byte rows: four columns an access
+    float *partial;                          // [CTA][2][kBM][BN]
+    uint32_t *status;
+};
+
+__host__ __device__ __forceinline__ int64_t sk_start(int64_t work, int units, int c) { return work * c / units; }
+
+// Result tile number t: groups of kGroupM row tiles, inside a group the row tiles of one
+// column tile first.  The CTAs that run together so share a few column tiles of one operand
+// and 16 row tiles of the other (21 MB of 2560-wide rows), which stay in L2.
+__device__ __forceinline__ void tile_of(const XParams &p, int64_t t, int &m, int &n) {
+    const int64_t group = int64_t(kGroupM) * p.tiles_n;
+    const int g = int(t / group);
+    const int64_t r = t - g * group;
+    const int rows = min(kGroupM, p.tiles_m - g * kGroupM);
+    n = int(r / rows);
+    m = g * kGroupM + int(r - int64_t(n) * rows);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// Shared-memory descriptor of an MN-major tile written by TMA boxes of 64 (MN) x kBK (K)
+// with 128-byte swizzle: 128-byte rows, one per k; 8-row groups along k are 1024 bytes apart
+// (stride offset), blocks of 64 along MN one box (leading offset).
+__device__ __forceinline__ uint64_t sw128_desc_mn(const void *p) {
+    uint64_t d = (uint64_t(smem_u32(p)) >> 4) & 0x3FFFull;
+    d |= uint64_t((kBK * 128) >> 4) << 16;
+    d |= uint64_t(1024 >> 4) << 32;
+    d |= uint64_t(1) << 46;
+    d |= uint64_t(2) << 61;
+    return d;
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int x, int y) {
+    asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];" ::"l"(
+                     reinterpret_cast<uint64_t>(map)),
+                 "r"(x), "r"(y), "r"(smem_u32(src))
+                 : "memory");
+}
+__device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_read() { asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory"); }
+__device__ __forceinline__ void bulk_wait_all() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// The next bf16 term of x: its 8 highest significant bits (cut, so that three terms hold
+// all 24 exactly), removed from x.  Infinities and NaN go whole into the first term.
+__device__ __forceinline__ uint32_t next_term(float &x) {
+    const uint32_t u = __float_as_uint(x);
+    if ((u & 0x7F800000u) == 0x7F800000u) {
+        x = 0.f;
+        return (u >> 16) | ((u & 0x007FFFFFu) ? 0x40u : 0u);
+    }
+    x -= __uint_as_float(u & 0xFFFF0000u);
+    return u >> 16;
+}
+
+// ---------------------------------------------------------------- epilogues of a warp
+
+// Columns [col0, col0 + BN / 2) of this thread's row, in registers: z[j] is column col0 + j.
+
+// kStats: running maximum and sum of exponentials, and the target's logit.
+template <int BN>
+__device__ __forceinline__ void stats_row(const XParams &p, float (&z)[BN / 2], int row, int col0, int slot) {
+    const int64_t t = row < p.M ? p.targets[row] : -1;
+    const int tc = (t >= p.v0 && t < p.v0 + p.N && t < p.vocab) ? int(t - p.v0) - col0 : -1;
+    if (col0 + BN / 2 > p.N) {
+#pragma unroll
+        for (int c = 0; c < BN / 2; ++c)
+            if (col0 + c >= p.N) z[c] = -INFINITY;
+    }
+    float m[4] = {z[0], z[1], z[2], z[3]};
+#pragma unroll
+    for (int c = 4; c < BN / 2; ++c) m[c & 3] = fmaxf(m[c & 3], z[c]);
+    const float mx = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
+    // nothing but -inf (columns past the last): exponents against 0 give sums of 0
+    const float ref = (mx == -INFINITY ? 0.f : mx) * kLog2e;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < BN / 2; ++c) sum[c & 3] += ex2(fmaf(z[c], kLog2e, -ref));
+    if (row < p.M) p.part[int64_t(slot) * p.ld_part + row] = make_float2(mx, (sum[0] + sum[1]) + (sum[2] + sum[3]));
+    if (unsigned(tc) < unsigned(BN / 2)) {
+#pragma unroll
+        for (int c = 0; c < BN / 2; ++c)
+            if (c == tc) p.zt[row] = z[c];
+    }
+}
+
+// kGrad: what dz needs of this thread's row.
+struct GradRow {
+    float lse, g;
+    bool has;
+    int tc;                                                // the target's column in this piece, or -1
+};
+__device__ __forceinline__ GradRow grad_row(const XParams &p, int row) {
+    const int64_t t = row < p.M ? p.targets[row] : -1;
+    GradRow r;
+    r.has = t >= 0 && t < p.vocab;
+    r.tc = (r.has && t >= p.v0 && t < p.v0 + p.N) ? int(t - p.v0) : -1;
+    r.lse = r.has ? p.lse[row] : 0.f;
+    r.g = r.has ? p.dloss[row] : 0.f;
+    return r;
+}
+
+// kGrad: dz of this warp's 32 rows row0.. and columns col0 .. col0 + 63, from z in y: one
+// 4 KB box of each term through the warp's shared buffer and out by TMA, which leaves out
+// what lies past the last row or column.
+template <int TERMS>
+__device__ __forceinline__ void grad_box(const XParams &p, const GradRow &r, float *y, int row0, int col0, uint8_t *box,
+                                         int lane) {
+    if (row0 >= p.M || col0 >= p.N) return;
+#pragma unroll
+    for (int c = 0; c < 64; ++c) y[c] = ex2((y[c] - r.lse) * kLog2e);
+    if (unsigned(r.tc - col0) < 64u && r.tc >= 0) {
+#pragma unroll
+        for (int c = 0; c < 64; ++c)
+            if (c == r.tc - col0) y[c] -= 1.f;
+    }
+#pragma unroll
+    for (int c = 0; c < 64; ++c) y[c] = r.has ? y[c] * r.g : 0.f;
+    if (lane == 0) bulk_wait_read();                       // the box's last store has read it
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < TERMS; ++k) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+            uint4 w;
+            if constexpr (TERMS == 1) {
+                const uint2 lo = pack_bf16x4(y[8 * c], y[8 * c + 1], y[8 * c + 2], y[8 * c + 3]);
+                const uint2 hi = pack_bf16x4(y[8 * c + 4], y[8 * c + 5], y[8 * c + 6], y[8 * c + 7]);
+                w = make_uint4(lo.x, lo.y, hi.x, hi.y);
+            } else {
+                uint32_t u[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) u[i] = next_term(y[8 * c + i]);
+                w = make_uint4(u[0] | (u[1] << 16), u[2] | (u[3] << 16), u[4] | (u[5] << 16), u[6] | (u[7] << 16));
+            }
+            *reinterpret_cast<uint4 *>(box + k * kBox + lane * 128 + ((c ^ (lane & 7)) << 4)) = w;
+        }
+    }
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) {
+#pragma unroll
+        for (int k = 0; k < TERMS; ++k) tma_store_2d(&p.d[k], box + k * kBox, col0, row0);
+        bulk_commit();
+    }
+}
+
+// Four columns col.. of one row of a result: the earlier pieces' sum is added, the value
+// stored in the result's type.
+__device__ __forceinline__ void store4(const XParams &p, int row, int col, const float (&v)[4]) {
+    const int64_t e = int64_t(row) * p.N + col;
+    if (p.vec) {
+        float4 y = make_float4(v[0], v[1], v[2], v[3]);
+        if (p.acc != nullptr) {
+            const float4 c = *reinterpret_cast<const float4 *>(p.acc + e);
+            y.x += c.x; y.y += c.y; y.z += c.z; y.w += c.w;
+        }
+        if (p.out32 != nullptr) *reinterpret_cast<float4 *>(p.out32 + e) = y;
+        else *reinterpret_cast<uint2 *>(p.out16 + e) = pack_bf16x4(y.x, y.y, y.z, y.w);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (col + i >= p.N) break;
+        const float y = v[i] + (p.acc != nullptr ? p.acc[e + i] : 0.f);
+        if (p.out32 != nullptr) p.out32[e + i] = y;
+        else p.out16[e + i] = __float2bfloat16(y);
+    }
+}
+
+// kOut: columns col0 .. col0 + 31 of a warp's 32 rows row0.. (one row a thread), turned in
+// shared memory so that lanes run along the columns (8 column quads x 4 rows an access):
+// into the result, or into a partial tile (rows of `ld` floats) where there is one.
+__device__ __forceinline__ void out_block(const XParams &p, const float *z, int row0, int col0, float *partial, int ld,
+                                          float *blk, int lane) {
+    if (row0 >= p.M || col0 >= p.N) return;
+#pragma unroll
+    for (int t = 0; t < 32; ++t) blk[lane * 33 + t] = z[t];
+    __syncwarp();
+    const int c4 = (lane & 7) * 4, rl = lane >> 3;
+#pragma unroll 4
+    for (int k = 0; k < 8; ++k) {
+        const int r = 4 * k + rl;
+        if (row0 + r >= p.M || col0 + c4 >= p.N) continue;
+        const float *a = blk + r * 33 + c4;
+        if (partial != nullptr) {
+            *reinterpret_cast<float4 *>(partial + int64_t(r) * ld + c4) = make_float4(a[0], a[1], a[2], a[3]);
+        } else {
+            const float v[4] = {a[0], a[1], a[2], a[3]};
+            store4(p, row0 + r, col0 + c4, v);
+        }
+    }
+    __syncwarp();
+}
+
+// ---------------------------------------------------------------- the kernel
+
+template <int BN, bool PAIR>
+struct Shape {
+    static constexpr int TM = PAIR ? 2 * kBM : kBM;          // rows of a tile of the schedule
+    static constexpr int BH = PAIR ? BN / 2 : BN;            // columns' operand rows that a CTA stages
+    static constexpr int A_BYTES = kBM * kBK * 2, B_BYTES = BH * kBK * 2, STAGE = A_BYTES + B_BYTES;
+};
+// Ring depth: what shared memory leaves beside the epilogue's buffers (8 x 12 KB boxes for
+// three dz terms, 8 x 4 KB for one, 8 x 4.2 KB for the turn of kOut, none for kStats).
+template <int BN, bool PAIR, int MODE>
+constexpr int epi_bytes(int terms) {
+    return MODE == kStats ? 0 : MODE == kGrad ? kEpiWarps * kBox * terms : kEpiWarps * 32 * 33 * 4;
+}
+template <int BN, bool PAIR, int MODE, int TERMS>
+constexpr int stages_of() {
+    const int room = 226 * 1024 - 1024 - epi_bytes<BN, PAIR, MODE>(TERMS);
+    const int n = room / Shape<BN, PAIR>::STAGE;
+    return n > 6 ? 6 : n;
+}
+
+// TERMS: bf16 terms of dz (kGrad; 1 otherwise).  FINE: sums in chunks of kChunk k blocks.
+template <int BN, bool PAIR, int MODE, int TERMS, bool FINE, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_constant__ XParams p) {
+    using S = Shape<BN, PAIR>;
+    constexpr int kStages = stages_of<BN, PAIR, MODE, TERMS>();
+    constexpr int TM = S::TM, BH = S::BH, A_BYTES = S::A_BYTES, STAGE = S::STAGE;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ uint64_t full[kStages], empty[kStages], accfull[2], accempty[2], done;
+    __shared__ uint32_t tmem_base;
+    __shared__ int s_abort, s_issued, s_consumed;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = PAIR ? int(cluster_rank()) : 0;         // this CTA's half of a tile's rows
+    const int unit = PAIR ? int(blockIdx.x >> 1) : int(blockIdx.x);
+    const bool leader = rank == 0;                           // issues the MMAs
+
+    // this unit's segments: its whole tiles, then its share of the split tiles, cut at tiles
+    const int KB = p.nprod * p.kb;
+    const int chunk = FINE ? kChunk : KB;                    // k blocks of one accumulator
+    const int64_t nwhole = p.whole > unit ? (p.whole - unit + p.units - 1) / p.units : 0;
+    const bool splits = MODE == kOut && p.sk_work > 0 && unit < p.sk_units;
+    const int64_t b0 = splits ? sk_start(p.sk_work, p.sk_units, unit) : 0;
+    const int64_t b1 = splits ? sk_start(p.sk_work, p.sk_units, unit + 1) : 0;
+    struct Seg {
+        int m0, n0, tn, kb0, kb1, slot;
+    };
+    // segment i; `at` walks through [b0, b1) after the whole tiles
+    auto next_seg = [&](int64_t i, int64_t &at, Seg &s) {
+        int64_t t;
+        if (i < nwhole) {
+            t = i * p.units + unit;
+            s.kb0 = 0;
+            s.kb1 = KB;
+            s.slot = 0;
+        } else {
+            if (at >= b1) return false;
+            const int64_t tl = at / KB;
+            s.kb0 = int(at - tl * KB);
+            s.kb1 = int(min(int64_t(KB), b1 - tl * KB));
+            s.slot = at == b0 ? 0 : 1;
+            at += s.kb1 - s.kb0;
+            t = p.whole + tl;
+        }
+        int m;
+        tile_of(p, t, m, s.tn);
+        s.m0 = m * TM + rank * kBM;
+        s.n0 = s.tn * BN;
+        return true;
+    };
+
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        s_issued = s_consumed = 0;
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&accfull[b], 1);
+            mbar_init(&accempty[b], (PAIR ? 2 : 1) * kEpiWarps);
+        }
+        mbar_init(&done, 1);
+    }
+    if (warp == 1) {
+        if constexpr (PAIR) {
+            tmem_alloc_pair(&tmem_base, 2 * BN);
+            tmem_relinquish_pair();
+        } else {
+            tmem_alloc(&tmem_base, 2 * BN);
+            tmem_relinquish();
+        }
+    }
+    fence_mbar_init();
+    tc_fence_before();
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync();              // the peer's barriers exist before any remote arrive
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int g = 0;
+            bool ok = true;
+            int64_t at = b0;
+            Seg sg;
+            for (int64_t i = 0; ok && next_seg(i, at, sg); ++i) {
+                for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++g) {
+                    const int s = g % kStages;
+                    if (g >= kStages && !mbar_wait(&empty[s], ((g / kStages) - 1) & 1, p.status, 20u)) {
+                        ok = false;
+                        break;
+                    }
+                    const int prod = kb / p.kb, k0 = (kb - prod * p.kb) * kBK;
+                    const CUtensorMap *ma = &p.a[p.pa[prod]], *mb = &p.b[p.pb[prod]];
+                    uint8_t *sa = smem + s * STAGE, *sb = sa + A_BYTES;
+                    const int nb = sg.n0 + rank * BH;
+                    if constexpr (PAIR) {
+                        if (leader) mbar_arrive_expect_tx(&full[s], 2 * STAGE);   // both CTAs' copies
+                        const uint32_t fb = cluster_addr(&full[s], 0);
+                        if constexpr (A_MN) {
+                            for (int c = 0; c < kBM / 64; ++c)
+                                tma_load_2d_pair(sa + c * kBK * 128, ma, sg.m0 + c * 64, k0, fb);
+                        } else {
+                            tma_load_2d_pair(sa, ma, k0, sg.m0, fb);
+                        }
+                        if constexpr (B_MN) {
+                            for (int c = 0; c < BH / 64; ++c)
+                                tma_load_2d_pair(sb + c * kBK * 128, mb, nb + c * 64, k0, fb);
+                        } else {
+                            tma_load_2d_pair(sb, mb, k0, nb, fb);
+                        }
+                    } else {
+                        mbar_arrive_expect_tx(&full[s], STAGE);
+                        if constexpr (A_MN) {
+                            for (int c = 0; c < kBM / 64; ++c)
+                                tma_load_2d(sa + c * kBK * 128, ma, sg.m0 + c * 64, k0, &full[s]);
+                        } else {
+                            tma_load_2d(sa, ma, k0, sg.m0, &full[s]);
+                        }
+                        if constexpr (B_MN) {
+                            for (int c = 0; c < BH / 64; ++c)
+                                tma_load_2d(sb + c * kBK * 128, mb, nb + c * 64, k0, &full[s]);
+                        } else {
+                            tma_load_2d(sb, mb, k0, nb, &full[s]);
+                        }
+                    }
+                    s_issued = g + 1;
+                }
+            }
+            if (!ok) s_abort = 1;
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer, accumulators alternate
+        if (lane == 0 && leader) {
+            constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (A_MN ? 1u << 15 : 0u) |
+                                       (B_MN ? 1u << 16 : 0u) | (uint32_t(BN >> 3) << 17) | (uint32_t(TM >> 4) << 24);
+            // 16 k: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major tile
+            constexpr int ka = A_MN ? 128 : 2, kbs = B_MN ? 128 : 2;
+            int g = 0, f = 0;                                // k blocks, accumulators so far
+            bool ok = true;
+            int64_t at = b0;
+            Seg sg;
+            for (int64_t i = 0; ok && next_seg(i, at, sg); ++i) {
+                for (int k0 = sg.kb0; ok && k0 < sg.kb1; k0 += chunk, ++f) {
+                    const int b = f & 1, k1 = min(sg.kb1, k0 + chunk);
+                    const uint32_t acc = tmem + uint32_t(b * BN);
+                    if (f >= 2 && !mbar_wait(&accempty[b], uint32_t(((f >> 1) - 1) & 1), p.status, 23u)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    for (int kb = k0; kb < k1; ++kb, ++g) {
+                        const int s = g % kStages;
+                        if (!mbar_wait(&full[s], (g / kStages) & 1, p.status, 21u)) { ok = false; break; }
+                        tc_fence_after();
+                        const uint8_t *sa = smem + s * STAGE;
+                        const uint64_t ad = A_MN ? sw128_desc_mn(sa) : sw128_desc(sa);
+                        const uint64_t bd = B_MN ? sw128_desc_mn(sa + A_BYTES) : sw128_desc(sa + A_BYTES);
+#pragma unroll
+                        for (int k = 0; k < kBK / 16; ++k) {
+                            const uint32_t add = (kb > k0 || k > 0) ? 1u : 0u;
+                            if constexpr (PAIR) mma_bf16_pair(acc, ad + ka * k, bd + kbs * k, idesc, add);
+                            else mma_bf16(acc, ad + ka * k, bd + kbs * k, idesc, add);
+                        }
+                        if constexpr (PAIR) mma_commit_pair(&empty[s], 3);   // frees the stage in both CTAs
+                        else mma_commit(&empty[s]);
+                        s_consumed = g + 1;
+                    }
+                    if (ok) {
+                        if constexpr (PAIR) mma_commit_pair(&accfull[b], 3);
+                        else mma_commit(&accfull[b]);
+                    }
+                }
+            }
+            if (!ok) s_abort = 1;
+            if constexpr (PAIR) mma_commit_pair(&done, 1);
+            else mma_commit(&done);
+            mbar_wait(&done, 0, nullptr, 0u);
+        }
+    } else {
+        // ------------------------------------------------ epilogue (warps 2..9)
+        const int q = warp & 3, half = (warp - 2) >> 2;       // TMEM lane quarter, half of the columns
+        // A fine sum is gathered whole in registers; any other stays in tensor memory while it
+        // is read a block at a time.
+        constexpr int WN = MODE == kGrad ? 64 : 32, ZN = FINE ? BN / 2 : WN;
+        uint8_t *buf = smem + kStages * STAGE;
+        uint8_t *box = buf + (warp - 2) * (kBox * TERMS);                              // kGrad
+        float *blk = reinterpret_cast<float *>(buf) + (warp - 2) * 32 * 33;            // kOut
+        int f = 0;
+        bool ok = true;
+        int64_t at = b0;
+        Seg sg;
+        for (int64_t i = 0; ok && next_seg(i, at, sg); ++i) {
+            const int row0 = sg.m0 + q * 32, colh = sg.n0 + half * (BN / 2);
+            float *part = nullptr;                            // kOut: this warp's part of a partial tile
+            if (MODE == kOut && (sg.kb0 != 0 || sg.kb1 != KB))
+                part = p.partial + ((int64_t(blockIdx.x) * 2 + sg.slot) * kBM + q * 32) * BN + half * (BN / 2);
+            GradRow gr;
+            if constexpr (MODE == kGrad) gr = grad_row(p, row0 + lane);
+            float z[ZN];                                      // this thread's row
+            auto block = [&](float *y, int c0) {              // WN columns from colh + c0
+                if constexpr (MODE == kGrad) grad_box<TERMS>(p, gr, y, row0, colh + c0, box, lane);
+                if constexpr (MODE == kOut) out_block(p, y, row0, colh + c0, part != nullptr ? part + c0 : nullptr, BN, blk, lane);
+            };
+            for (int k0 = sg.kb0; k0 < sg.kb1; k0 += chunk, ++f) {
+                const int b = f & 1;
+                if (!mbar_wait(&accfull[b], uint32_t((f >> 1) & 1), p.status, 22u)) {
+                    s_abort = 1;
+                    ok = false;
+                    break;
+                }
+                tc_fence_after();
+                const uint32_t tm = tmem + uint32_t(b * BN + half * (BN / 2)) + (uint32_t(q * 32) << 16);
+                if constexpr (FINE) {
+#pragma unroll
+                    for (int j = 0; j < BN / 64; ++j) {
+                        uint32_t v[32];
+                        tmem_ld32(tm + uint32_t(j * 32), v);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int c = 0; c < 32; ++c)
+                            z[j * 32 + c] = (k0 > sg.kb0 ? z[j * 32 + c] : 0.f) + __uint_as_float(v[c]);
+                    }
+                } else {
+#pragma unroll 1
+                    for (int c0 = 0; c0 < BN / 2; c0 += WN) {
+#pragma unroll
+                        for (int j = 0; j < WN / 32; ++j) {
+                            uint32_t v[32];
+                            tmem_ld32(tm + uint32_t(c0 + j * 32), v);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int c = 0; c < 32; ++c) z[j * 32 + c] = __uint_as_float(v[c]);
+                        }
+                        block(z, c0);
+                    }
+                }
+                tc_fence_before();                            // the accumulator is free again
+                __syncwarp();
+                if (lane == 0) {
+                    if constexpr (PAIR) mbar_arrive_cluster(cluster_addr(&accempty[b], 0));
+                    else mbar_arrive(&accempty[b]);
+                }
+            }
+            if (!ok) break;
+            if constexpr (MODE == kStats) {
+                stats_row<BN>(p, z, row0 + lane, colh, 2 * sg.tn + half);
+            } else if constexpr (FINE) {
+#pragma unroll
+                for (int c0 = 0; c0 < BN / 2; c0 += WN) block(z + c0, c0);
+            }
+        }
+        if (MODE == kGrad && lane == 0) bulk_wait_all();
+    }
+    // wind down.  The MMA thread waited for its last commit; after an abort (a wait ran out)
+    // the copies that were issued and not consumed are awaited too, and every CTA then stays
+    // for 20 us so that its peer's last copies and arrivals land while it lives.
+    tc_fence_before();
+    __syncthreads();
+    if (s_abort && threadIdx.x == 0) {
+        if (leader)
+            for (int g = s_consumed; g < s_issued; ++g) mbar_wait(&full[g % kStages], (g / kStages) & 1, nullptr, 0u);
+        const long long t0 = clock64();
+        while (clock64() - t0 < 40000) {}
+    }
+    __syncthreads();
+    if constexpr (PAIR) cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        if constexpr (PAIR) tmem_dealloc_pair(tmem, 2 * BN);
+        else tmem_dealloc(tmem, 2 * BN);
+    }
+}
+
+// A split tile (number whole + blockIdx.x) is the sum, in unit order, of its units' partial
+// tiles; block y does rows [y TM / gridDim.y, ...).  A tile of one unit was written by it.
+template <int BN, bool PAIR>
+__global__ void __launch_bounds__(256) xent_fixup_kernel(const __grid_constant__ XParams p) {
+    constexpr int TM = PAIR ? 2 * kBM : kBM;
+    const int64_t KB = int64_t(p.nprod) * p.kb, ta = int64_t(blockIdx.x) * KB, tb = ta + KB;
+    int c0 = int(ta * p.sk_units / p.sk_work);
+    while (c0 > 0 && sk_start(p.sk_work, p.sk_units, c0) > ta) --c0;
+    while (c0 + 1 < p.sk_units && sk_start(p.sk_work, p.sk_units, c0 + 1) <= ta) ++c0;
+    int c1 = c0;
+    while (c1 + 1 < p.sk_units && sk_start(p.sk_work, p.sk_units, c1 + 1) < tb) ++c1;
+    if (c1 == c0) return;
+    const int s0 = sk_start(p.sk_work, p.sk_units, c0) < ta ? 1 : 0;
+    int m, n;
+    tile_of(p, p.whole + blockIdx.x, m, n);
+    const int m0 = m * TM, n0 = n * BN;
+    const int rows = TM / gridDim.y, r0 = blockIdx.y * rows;
+    for (int e = threadIdx.x; e < rows * (BN / 4); e += blockDim.x) {
+        const int r = r0 + e / (BN / 4), c4 = (e % (BN / 4)) * 4;
+        const int row = m0 + r, col = n0 + c4;
+        if (row >= p.M || col >= p.N) continue;
+        const int h = r / kBM, lr = r % kBM;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = c0; c <= c1; c += 8) {                  // eight loads in flight
+            float4 v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (c + u <= c1) {
+                    const int64_t cta = PAIR ? 2 * int64_t(c + u) + h : c + u;
+                    const int slot = c + u == c0 ? s0 : 0;
+                    v[u] = *reinterpret_cast<const float4 *>(p.partial + ((cta * 2 + slot) * kBM + lr) * BN + c4);
+                }
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (c + u <= c1) {
+                    acc.x += v[u].x; acc.y += v[u].y; acc.z += v[u].z; acc.w += v[u].w;
+                }
+        }
+        const float v[4] = {acc.x, acc.y, acc.z, acc.w};
+        store4(p, row, col, v);
+    }
+}
+
+// Joins the (max, sum) pairs of a row's tiles: `rx` rows x 256 / rx threads a block; each
+// thread joins slots y, y + 256 / rx, ..., then the block joins its threads' pairs in order.
+__global__ void __launch_bounds__(256) xent_join_kernel(const float2 *__restrict__ part, int64_t ld, int slots, int rows,
+                                                        int rx, const float *__restrict__ zt,
+                                                        const int64_t *__restrict__ targets, int64_t vocab,
+                                                        float *__restrict__ loss, float *__restrict__ lse) {
+    __shared__ float2 sh[256];
+    const int x = threadIdx.x % rx, y = threadIdx.x / rx, ny = 256 / rx;
+    const int row = blockIdx.x * rx + x;
+    auto join = [](float2 a, float2 b) {
+        const float m = fmaxf(a.x, b.x), ref = (m == -INFINITY ? 0.f : m);
+        return make_float2(m, a.y * expf(a.x - ref) + b.y * expf(b.x - ref));
+    };
+    float2 a = make_float2(-INFINITY, 0.f);
+    if (row < rows)
+        for (int s = y; s < slots; s += ny) a = join(a, part[int64_t(s) * ld + row]);
+    sh[threadIdx.x] = a;
+    for (int h = ny / 2; h > 0; h /= 2) {
+        __syncthreads();
+        if (y < h) sh[threadIdx.x] = join(sh[threadIdx.x], sh[threadIdx.x + h * rx]);
+    }
+    if (y == 0 && row < rows) {
+        const float2 r = sh[threadIdx.x];
+        const float l = r.x + logf(r.y);
+        const int64_t t = targets[row];
+        lse[row] = l;
+        loss[row] = (t >= 0 && t < vocab) ? l - zt[row] : 0.f;
+    }
+}
+
+// Rows of float32 or bf16 -> T bf16 terms [T][rows][ld], columns past `cols` zero; with
+// `targets`, rows without a target are zero (what padding holds must not reach a sum over
+// the rows).
+template <typename SRC>
+__global__ void __launch_bounds__(256) xent_pack_kernel(const SRC *__restrict__ x, int64_t rows, int cols, int ld, int terms,
+                                                        const int64_t *__restrict__ targets, int64_t vocab,
+                                                        __nv_bfloat16 *__restrict__ y) {
+    const int64_t quads = ld / 4, n = rows * quads, plane = rows * int64_t(ld);
+    for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += int64_t(gridDim.x) * blockDim.x) {
+        const int64_t r = i / quads;
+        const int c = int(i - r * quads) * 4;
+        bool on = true;
+        if (targets != nullptr) {
+            const int64_t t = targets[r];
+            on = t >= 0 && t < vocab;
+        }
+        float v[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) v[k] = on && c + k < cols ? float(x[r * cols + c + k]) : 0.f;
+        for (int t = 0; t < terms; ++t) {
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = next_term(v[k]);
+            *reinterpret_cast<uint2 *>(y + t * plane + r * ld + c) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host side
+
+// bf16 [rows, cols] with rows `ld` elements apart, boxes of 64 columns x `box_rows`, 128-byte
+// swizzle, zero fill past the edges.
+int make_map(CUtensorMap *m, const void *base, int64_t rows, int64_t cols, int64_t ld, int box_rows) {
+    EncodeTiled enc = encode_fn();
+    TLB_REQUIRE(enc != nullptr, TLB_ECUDA, "xent: cuTensorMapEncodeTiled unavailable");
+    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(ld) * 2};
+    const cuuint32_t box[2] = {cuuint32_t(kBK), cuuint32_t(box_rows)};
+    const cuuint32_t estr[2] = {1, 1};
+    CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(base), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    TLB_REQUIRE(r == CUDA_SUCCESS, TLB_ECUDA, "xent: tensor map encoding failed (%d)", int(r));
+    return TLB_OK;
+}
+
+// A matrix operand: `terms` bf16 planes [rows, cols], `plane` elements apart, rows ld apart.
+struct Mat {
+    const __nv_bfloat16 *p;
+    int64_t rows, cols, ld, plane;
+    int terms;
+};
+
+template <int BN, bool PAIR, int MODE, int TERMS, bool FINE, bool A_MN, bool B_MN>
+int launch(XParams &p, const Mat &a, const Mat &b, cudaStream_t st) {
+    using S = Shape<BN, PAIR>;
+    constexpr int stages = stages_of<BN, PAIR, MODE, TERMS>();
+    constexpr int smem = stages * S::STAGE + epi_bytes<BN, PAIR, MODE>(TERMS) + 1024;
+    static_assert(stages >= 3 && smem <= 227 * 1024 - 512, "shared memory of one CTA");
+    for (int t = 0; t < a.terms; ++t)
+        TLB_TRY(make_map(&p.a[t], a.p + t * a.plane, a.rows, a.cols, a.ld, A_MN ? kBK : kBM));
+    for (int t = 0; t < b.terms; ++t)
+        TLB_TRY(make_map(&p.b[t], b.p + t * b.plane, b.rows, b.cols, b.ld, B_MN ? kBK : S::BH));
+    // term products, the smallest first: i + j <= 2 of three and three, all of one and three
+    p.nprod = 0;
+    for (int sum = kMaxTerms - 1; sum >= 0; --sum)
+        for (int i = 0; i < a.terms; ++i) {
+            const int j = sum - i;
+            if (j < 0 || j >= b.terms) continue;
+            p.pa[p.nprod] = int8_t(i);
+            p.pb[p.nprod] = int8_t(j);
+            ++p.nprod;
+        }
+    const int64_t K = A_MN ? a.rows : a.cols;
+    p.kb = int(ceil_div(K, kBK));
+    p.tiles_m = int(ceil_div(p.M, S::TM));
+    p.tiles_n = int(ceil_div(p.N, BN));
+    const int64_t tiles = int64_t(p.tiles_m) * p.tiles_n, KB = int64_t(p.nprod) * p.kb;
+    const int most = PAIR ? num_sms() / 2 : num_sms();
+    p.whole = tiles;
+    p.sk_work = 0;
+    p.sk_units = 1;
+    p.units = int(std::min<int64_t>(tiles, most));
+    if (MODE == kOut) {
+        // The tiles past the last full wave are split along K over all units unless a wave of
+        // them costs less: a split ends in partial tiles and a second kernel, about 24 k blocks
+        const int64_t rest = tiles % most;
+        if (rest > 0 && KB > KB * rest / most + 24) {
+            p.whole = tiles - rest;
+            p.sk_work = rest * KB;
+            p.sk_units = int(std::max<int64_t>(1, std::min<int64_t>(most, p.sk_work / 8)));
+            p.units = p.whole > 0 ? most : p.sk_units;
+        }
+    }
+    auto k = xent_gemm_kernel<BN, PAIR, MODE, TERMS, FINE, A_MN, B_MN>;
+    TLB_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned((PAIR ? 2 : 1) * p.units));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = PAIR ? 2 : 1;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    TLB_CUDA(cudaLaunchKernelEx(&cfg, k, p));
+    TLB_TRY(check_launch(MODE == kStats ? "xent_stats" : MODE == kGrad ? "xent_grad" : A_MN ? "xent_dw" : "xent_dh"));
+    if (p.sk_work > 0) {
+        const int64_t rest = p.sk_work / KB;
+        xent_fixup_kernel<BN, PAIR><<<dim3(unsigned(rest), PAIR ? 64 : 32), 256, 0, st>>>(p);
+        TLB_TRY(check_launch("xent_fixup"));
+    }
+    return TLB_OK;
+}
+
+// Tile form.  More than 128 rows: CTA pairs on 256 x 256 tiles.  Up to 128 rows there is one
+// row tile, and 128 columns a tile even out the few tiles over the SMs better than 256 when
+// their last wave is fuller; the boxes of three dz terms leave room for 128 columns only.
+template <int MODE, int TERMS>
+int launch_z(XParams &p, const Mat &h, const Mat &w, cudaStream_t st) {
+    constexpr bool fine = MODE == kStats || TERMS > 1;       // the loss is float32 whatever the operands
+    if (p.M > kBM) return launch<256, true, MODE, TERMS, fine, false, false>(p, h, w, st);
+    const int64_t n = num_sms(), t256 = ceil_div(p.N, 256), t128 = ceil_div(p.N, 128);
+    if constexpr (TERMS == 1)
+        if (2 * ceil_div(t256, n) <= ceil_div(t128, n)) return launch<256, false, MODE, TERMS, fine, false, false>(p, h, w, st);
+    return launch<128, false, MODE, TERMS, fine, false, false>(p, h, w, st);
+}
+
+template <bool A_MN, bool FINE>
+int launch_out(XParams &p, const Mat &a, const Mat &b, cudaStream_t st) {
+    if (p.M > kBM) return launch<256, true, kOut, 1, FINE, A_MN, true>(p, a, b, st);
+    return launch<256, false, kOut, 1, FINE, A_MN, true>(p, a, b, st);
+}
+
+constexpr int64_t kPieceBytes = int64_t(512) << 20;   // of dz, and of packed head rows, in the workspace
+constexpr int64_t kRowChunk = 16384;                  // rows of one pass of the loss (its pairs' buffer)
+
+struct Plan {
+    int h_terms, w_terms, z_terms;
+    bool pack_h, pack_w;
+    int64_t dp;                  // packed row length
+    int64_t piece;               // vocabulary rows of one piece (multiple of 256)
+    int64_t part_ld, slots;
+    size_t h, w, dz, part, zt, acc, partial, total;
+};
+
+Plan plan_of(int htype, int wtype, int64_t N, int64_t V, int64_t D, bool grad, bool grad_w) {
+    Plan q;
+    q.h_terms = htype == TLB_W_F32 ? 3 : 1;
+    q.w_terms = wtype == TLB_W_F32 ? 3 : 1;
+    q.z_terms = htype == TLB_W_F32 ? 3 : 1;
+    q.dp = ceil_div(D, 8) * 8;
+    // d_w sums over the rows: those without a target are zeroed in a copy
+    q.pack_h = htype == TLB_W_F32 || D % 8 != 0 || grad_w;
+    q.pack_w = wtype == TLB_W_F32 || D % 8 != 0;
+    int64_t piece = ceil_div(V, 256) * 256;
+    if (grad) piece = std::min(piece, kPieceBytes / (2 * q.z_terms * std::max<int64_t>(N, 1)));
+    if (q.pack_w) piece = std::min(piece, kPieceBytes / (2 * q.w_terms * q.dp));
+    piece = std::min(std::max<int64_t>(piece / 256 * 256, 2048), ceil_div(V, 256) * 256);
+    q.piece = ceil_div(ceil_div(V, ceil_div(V, piece)), 256) * 256;      // pieces of nearly one size
+    WsPlan w;
+    q.h = q.pack_h ? w.take(size_t(q.h_terms) * N * q.dp * 2) : 0;
+    q.w = q.pack_w ? w.take(size_t(q.w_terms) * q.piece * q.dp * 2) : 0;
+    q.part_ld = q.slots = 0;
+    q.part = q.zt = q.dz = q.acc = q.partial = 0;
+    if (!grad) {
+        q.part_ld = ceil_div(std::min(N, kRowChunk), 32) * 32;
+        q.slots = 2 * (ceil_div(V, 128) + ceil_div(V, q.piece));           // 128-wide tiles: the most slots
+        q.part = w.take(size_t(q.part_ld) * q.slots * 8);
+        q.zt = w.take(size_t(N) * 4);
+    } else {
+        q.dz = w.take(size_t(q.z_terms) * N * q.piece * 2);
+        if (htype != TLB_W_F32 && q.piece < V) q.acc = w.take(size_t(N) * D * 4);
+        q.partial = w.take(size_t(num_sms() + 1) * 2 * kBM * 256 * 4);
+    }
+    q.total = w.off;
+    return q;
+}
+
+int pack(const void *x, int type, int64_t rows, int64_t cols, int64_t ld, int terms, const int64_t *targets, int64_t vocab,
+         __nv_bfloat16 *y, cudaStream_t st) {
+    const unsigned grid = stream_grid(rows * (ld / 4), 256);
+    if (type == TLB_W_F32)
+        xent_pack_kernel<float><<<grid, 256, 0, st>>>(static_cast<const float *>(x), rows, int(cols), int(ld), terms, targets,
+                                                      vocab, y);
+    else
+        xent_pack_kernel<__nv_bfloat16><<<grid, 256, 0, st>>>(static_cast<const __nv_bfloat16 *>(x), rows, int(cols), int(ld),
+                                                              terms, targets, vocab, y);
+    return check_launch("xent_pack");
+}
+
+size_t elem(int type) { return type == TLB_W_F32 ? 4 : 2; }
+
+int check_types(const char *fn, int htype, int wtype, int64_t N, int64_t V, int64_t D) {
+    TLB_REQUIRE((htype == TLB_W_F32 || htype == TLB_W_BF16) && (wtype == TLB_W_F32 || wtype == TLB_W_BF16), TLB_EINVAL,
+                "%s: hidden and head are float32 or bfloat16", fn);
+    TLB_REQUIRE(!(htype == TLB_W_BF16 && wtype == TLB_W_F32), TLB_EUNSUPPORTED,
+                "%s: bfloat16 hidden rows with a float32 head", fn);
+    TLB_REQUIRE(N >= 0 && V >= 1 && D >= 1, TLB_EINVAL, "%s: needs rows >= 0, vocab >= 1, dim >= 1", fn);
+    TLB_REQUIRE(N <= (int64_t(1) << 24) && V <= (int64_t(1) << 24) && D <= (int64_t(1) << 20), TLB_EUNSUPPORTED,
+                "%s: rows and vocab up to 2^24, dim up to 2^20", fn);
+    return TLB_OK;
+}
+
+// hidden rows as an operand, packed into the workspace where its plan asks for it
+int hidden_operand(const Plan &q, int htype, const void *hidden, int64_t N, int64_t D, const int64_t *mask, int64_t V,
+                   void *ws, cudaStream_t st, Mat &h) {
+    if (!q.pack_h) {
+        h = Mat{static_cast<const __nv_bfloat16 *>(hidden), N, D, D, 0, 1};
+        return TLB_OK;
+    }
+    __nv_bfloat16 *y = ws_at<__nv_bfloat16>(ws, q.h);
+    h = Mat{y, N, D, q.dp, N * q.dp, q.h_terms};
+    return pack(hidden, htype, N, D, q.dp, q.h_terms, mask, V, y, st);
+}
+
+// rows v0 .. v0 + n of the head as an operand
+int head_operand(const Plan &q, int wtype, const void *W, int64_t v0, int64_t n, int64_t D, void *ws, cudaStream_t st,
+                 Mat &w) {
+    const char *src = static_cast<const char *>(W) + size_t(v0) * D * elem(wtype);
+    if (!q.pack_w) {
+        w = Mat{reinterpret_cast<const __nv_bfloat16 *>(src), n, D, D, 0, 1};
+        return TLB_OK;
+    }
+    __nv_bfloat16 *y = ws_at<__nv_bfloat16>(ws, q.w);
+    w = Mat{y, n, D, q.dp, n * q.dp, q.w_terms};
+    return pack(src, wtype, n, D, q.dp, q.w_terms, nullptr, 0, y, st);
+}
+
+}  // namespace
+
+}  // namespace tlb
+
+using namespace tlb;
+
+extern "C" {
+
+size_t tlb_xent_workspace_bytes(int32_t htype, int32_t wtype, int64_t rows, int64_t vocab, int64_t dim, int32_t grad_w) {
+    clear_error();
+    if (check_types("xent_workspace_bytes", htype, wtype, rows, vocab, dim) != TLB_OK) return 0;
+    return std::max(plan_of(htype, wtype, rows, vocab, dim, false, false).total,
+                    plan_of(htype, wtype, rows, vocab, dim, true, grad_w != 0).total);
+}
+
+int tlb_xent_forward(int32_t htype, const void *hidden, int32_t wtype, const void *W, const int64_t *targets, int64_t rows,
+                     int64_t vocab, int64_t dim, float *loss, float *lse, void *ws, size_t ws_bytes, void *stream) {
+    clear_error();
+    TLB_TRY(check_types("xent_forward", htype, wtype, rows, vocab, dim));
+    if (rows == 0) return TLB_OK;
+    TLB_REQUIRE(hidden && W && targets && loss && lse, TLB_EINVAL, "xent_forward: null pointer");
+    TLB_REQUIRE(aligned16(hidden) && aligned16(W), TLB_EINVAL, "xent_forward: hidden and W must be 16-byte aligned");
+    const Plan q = plan_of(htype, wtype, rows, vocab, dim, false, false);
+    TLB_REQUIRE(ws != nullptr && (reinterpret_cast<uintptr_t>(ws) & 255) == 0 && ws_bytes >= q.total, TLB_EINVAL,
+                "xent_forward: needs a 256-byte aligned workspace of %zu bytes", q.total);
+    cudaStream_t st = as_stream(stream);
+    Mat h;
+    TLB_TRY(hidden_operand(q, htype, hidden, rows, dim, nullptr, vocab, ws, st, h));
+    const int64_t step = q.pack_w ? q.piece : vocab;
+    for (int64_t r0 = 0; r0 < rows; r0 += kRowChunk) {
+        const int64_t n = std::min(kRowChunk, rows - r0);
+        Mat hr = h;
+        hr.p += r0 * h.ld;
+        hr.rows = n;
+        int slot = 0;
+        for (int64_t v0 = 0; v0 < vocab; v0 += step) {
+            Mat w;
+            const int64_t nv = std::min(step, vocab - v0);
+            TLB_TRY(head_operand(q, wtype, W, v0, nv, dim, ws, st, w));
+            XParams p;
+            memset(&p, 0, sizeof(p));
+            p.M = int(n);
+            p.N = int(nv);
+            p.targets = targets + r0;
+            p.vocab = vocab;
+            p.v0 = v0;
+            p.part = ws_at<float2>(ws, q.part) + int64_t(slot) * q.part_ld;
+            p.ld_part = q.part_ld;
+            p.zt = ws_at<float>(ws, q.zt) + r0;
+            p.status = ws_at<uint32_t>(ws, 0);
+            TLB_TRY((launch_z<kStats, 1>(p, hr, w, st)));
+            slot += 2 * p.tiles_n;
+        }
+        int rx = 1;
+        while (rx < 32 && rx < n) rx *= 2;
+        xent_join_kernel<<<unsigned(ceil_div(n, rx)), 256, 0, st>>>(ws_at<float2>(ws, q.part), q.part_ld, slot, int(n), rx,
+                                                                    ws_at<float>(ws, q.zt) + r0, targets + r0, vocab,
+                                                                    loss + r0, lse + r0);
+        TLB_TRY(check_launch("xent_join"));
+    }
+    return TLB_OK;
+}
+
+int tlb_xent_backward(int32_t htype, const void *hidden, int32_t wtype, const void *W, const int64_t *targets,
+                      const float *lse, const float *d_loss, int64_t rows, int64_t vocab, int64_t dim, void *d_hidden,
+                      void *d_w, void *ws, size_t ws_bytes, void *stream) {
+    clear_error();
+    TLB_TRY(check_types("xent_backward", htype, wtype, rows, vocab, dim));
+    cudaStream_t st = as_stream(stream);
+    if (rows == 0) {
+        if (d_w != nullptr) TLB_CUDA(cudaMemsetAsync(d_w, 0, size_t(vocab) * dim * elem(htype), st));
+        return TLB_OK;
+    }
+    TLB_REQUIRE(hidden && W && targets && lse && d_loss && d_hidden, TLB_EINVAL, "xent_backward: null pointer");
+    TLB_REQUIRE(aligned16(hidden) && aligned16(W), TLB_EINVAL, "xent_backward: hidden and W must be 16-byte aligned");
+    const Plan q = plan_of(htype, wtype, rows, vocab, dim, true, d_w != nullptr);
+    TLB_REQUIRE(ws != nullptr && (reinterpret_cast<uintptr_t>(ws) & 255) == 0 && ws_bytes >= q.total, TLB_EINVAL,
+                "xent_backward: needs a 256-byte aligned workspace of %zu bytes", q.total);
+    Mat h;
+    TLB_TRY(hidden_operand(q, htype, hidden, rows, dim, d_w != nullptr ? targets : nullptr, vocab, ws, st, h));
+    const bool wide = htype == TLB_W_F32;
+    for (int64_t v0 = 0; v0 < vocab; v0 += q.piece) {
+        const int64_t nv = std::min(q.piece, vocab - v0);
+        Mat w;
+        TLB_TRY(head_operand(q, wtype, W, v0, nv, dim, ws, st, w));
+        const Mat dz{ws_at<__nv_bfloat16>(ws, q.dz), rows, nv, q.piece, rows * q.piece, q.z_terms};
+        {
+            XParams p;
+            memset(&p, 0, sizeof(p));
+            p.M = int(rows);
+            p.N = int(nv);
+            p.targets = targets;
+            p.vocab = vocab;
+            p.v0 = v0;
+            p.lse = lse;
+            p.dloss = d_loss;
+            for (int t = 0; t < q.z_terms; ++t)
+                TLB_TRY(make_map(&p.d[t], dz.p + t * dz.plane, rows, nv, dz.ld, 32));
+            p.status = ws_at<uint32_t>(ws, 0);
+            if (wide) TLB_TRY((launch_z<kGrad, 3>(p, h, w, st)));
+            else TLB_TRY((launch_z<kGrad, 1>(p, h, w, st)));
+        }
+        {
+            XParams p;
+            memset(&p, 0, sizeof(p));
+            p.M = int(rows);
+            p.N = int(dim);
+            float *sum = wide ? static_cast<float *>(d_hidden) : ws_at<float>(ws, q.acc);
+            const bool last = v0 + nv == vocab;
+            p.acc = v0 > 0 ? sum : nullptr;
+            if (wide || !last) p.out32 = sum;
+            else p.out16 = static_cast<__nv_bfloat16 *>(d_hidden);
+            p.vec = dim % 4 == 0 && aligned16(d_hidden);
+            p.partial = ws_at<float>(ws, q.partial);
+            p.status = ws_at<uint32_t>(ws, 0);
+            TLB_TRY((wide ? launch_out<false, true>(p, dz, w, st) : launch_out<false, false>(p, dz, w, st)));
+        }
+        if (d_w != nullptr) {
+            XParams p;
+            memset(&p, 0, sizeof(p));
+            p.M = int(nv);
+            p.N = int(dim);
+            char *out = static_cast<char *>(d_w) + size_t(v0) * dim * elem(htype);
+            if (wide) p.out32 = reinterpret_cast<float *>(out);
+            else p.out16 = reinterpret_cast<__nv_bfloat16 *>(out);
+            p.vec = dim % 4 == 0 && aligned16(d_w);
+            p.partial = ws_at<float>(ws, q.partial);
+            p.status = ws_at<uint32_t>(ws, 0);
+            TLB_TRY((wide ? launch_out<true, true>(p, dz, h, st) : launch_out<true, false>(p, dz, h, st)));
+        }
+    }
+    return TLB_OK;
+}
+
+}  // extern "C"
