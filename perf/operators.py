@@ -134,11 +134,11 @@ def prepare(case, seed):
         state = {"case": case, "groups": _muon_inputs(case, seed)}
         if own:
             import transformer_layer_backward_gb300 as tlb
-            params, grads, momenta = ([m for group in state["groups"] for m in group[i].unbind(0)] for i in range(3))
-            state["lists"] = params, grads, momenta
+            state["mats"] = tlb.muon_mats(*([m for group in state["groups"] for m in group[i].unbind(0)]
+                                            for i in range(3)))
             state["cfg"] = tlb.muon_cfg(MUON["lr"], MUON["momentum"], MUON["weight_decay"], MUON["eps"],
                                         MUON["coefficients"], case["steps"], case["nesterov"])
-            state["ws"] = tlb.muon_workspace([p.shape for p in params])
+            state["ws"] = tlb.muon_workspace(state["mats"])
         return state
     hidden, weight, targets, d_loss = _head_inputs(case, seed)
     state = {"case": case, "hidden": hidden, "weight": weight, "targets": targets, "d_loss": d_loss}
@@ -200,7 +200,7 @@ def run(state):
     if own:
         import transformer_layer_backward_gb300 as tlb
         if case["op"] == "muon":
-            tlb.muon(*state["lists"], state["cfg"], state["ws"])
+            tlb.muon(state["mats"], state["cfg"], state["ws"])
             return [(param, momentum) for param, _, momentum in state["groups"]]
         hidden, weight, targets, ws = state["hidden"], state["weight"], state["targets"], state["ws"]
         if case["op"] == "xent_forward":
