@@ -281,6 +281,36 @@ int tlb_linear_backward(int32_t wtype, const void *W, float scale, const float *
 int tlb_adamw(float *p, const float *g, float *m, float *v, int64_t n,
               const tlb_adamw_cfg *cfg, float lr_mult, double *sumsq, void *stream);
 
+/* One matrix of a Muon step: parameter, gradient and momentum [rows, cols] float32 (p and m
+ * are updated in place), with a learning rate of cfg.lr * lr_mult and an orthogonal update
+ * of `scale` (sqrt(max(1, rows / cols)) is usual). */
+typedef struct {
+    float *p;
+    const float *g;
+    float *m;
+    int32_t rows, cols;      /* min(rows, cols) <= 64, the adapters' largest rank; max <= 2^24 */
+    float lr_mult, scale;
+} tlb_muon_mat;
+
+typedef struct {
+    double lr, momentum, weight_decay, eps;
+    double a, b, c;          /* Newton-Schulz coefficients: 3.4445, -4.7750, 2.0315 are usual */
+    int32_t steps;           /* Newton-Schulz steps, 1 .. 100 (5 is usual) */
+    int32_t nesterov;
+} tlb_muon_cfg;
+
+/* The Muon optimiser's step, the other step for the adapters' gradients beside tlb_adamw, on
+ * `n` matrices of any shapes at once (host array), each by itself:
+ *   m <- momentum m + g;   u = nesterov ? g + momentum m : m;   X = u / (|u|_F + eps)
+ *   X <- a X + b (X X^T) X + c (X X^T)^2 X     `steps` times
+ *   p <- p - lr lr_mult (weight_decay p + scale X)
+ * All in float32; a zero update gives X = 0.  The matrices must not overlap, within the call
+ * or with one another; any alignment of 4 bytes goes (16 is faster).  Same inputs, same bits.
+ * ws: 256-byte aligned, tlb_muon_workspace_bytes() of these shapes (their pointers are not
+ * looked at; 0 for shapes that the call refuses). */
+size_t tlb_muon_workspace_bytes(const tlb_muon_mat *mats, int32_t n);
+int tlb_muon(const tlb_muon_mat *mats, int32_t n, const tlb_muon_cfg *cfg, void *ws, size_t ws_bytes, void *stream);
+
 /* ---------------------------------------------------------------- the loss above the stack */
 
 /* Softmax cross entropy of a linear head without the logits in memory, and its gradient,

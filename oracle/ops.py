@@ -209,3 +209,24 @@ def xent_backward(hidden, w, targets, lse, d_loss):
     dz = xent_dlogits(hidden, w, targets, lse, d_loss)
     has = (np.asarray(targets) >= 0) & (np.asarray(targets) < np.shape(w)[0])
     return dz @ f64(w), dz.T @ np.where(has[:, None], f64(hidden), 0.0)
+
+
+def newton_schulz(x, coefficients, steps: int):
+    """X <- a X + b (X X^T) X + c (X X^T)^2 X, `steps` times: with X = U S V^T every singular
+    value s goes to a s + b s^3 + c s^5 and U, V stay."""
+    a, b, c = (float(v) for v in coefficients)
+    u, s, vt = np.linalg.svd(f64(x), full_matrices=False)
+    for _ in range(int(steps)):
+        s = s * (a + s * s * (b + s * s * c))
+    return (u * s) @ vt
+
+
+def muon(p, g, m, lr, momentum, wd, eps, coefficients, steps: int, nesterov: bool, scale: float):
+    """One Muon step of a matrix: m = momentum m + g; u = g + momentum m or m; the update is
+    newton_schulz(u / (|u|_F + eps)); p -= lr (wd p + scale update).  Returns (p, m)."""
+    p, g, m = f64(p), f64(g), f64(m)
+    m = momentum * m + g
+    u = g + momentum * m if nesterov else m
+    norm = np.sqrt(np.sum(u * u)) + eps
+    x = newton_schulz(u / norm if norm > 0 else u, coefficients, steps)
+    return p - lr * (wd * p + scale * x), m

@@ -54,6 +54,15 @@ class AdamwCfg(C.Structure):
                 ("step", i32)]
 
 
+class MuonMat(C.Structure):
+    _fields_ = [("p", vp), ("g", vp), ("m", vp), ("rows", i32), ("cols", i32), ("lr_mult", f32), ("scale", f32)]
+
+
+class MuonCfg(C.Structure):
+    _fields_ = [("lr", C.c_double), ("momentum", C.c_double), ("weight_decay", C.c_double), ("eps", C.c_double),
+                ("a", C.c_double), ("b", C.c_double), ("c", C.c_double), ("steps", i32), ("nesterov", i32)]
+
+
 P = C.POINTER
 SIGNATURES = {
     "tlb_last_error": (C.c_char_p, []),
@@ -70,6 +79,8 @@ SIGNATURES = {
     "tlb_rmsnorm_backward": (C.c_int, [vp, vp, vp, vp, i64, i64, f32, i32, vp]),
     "tlb_rope_backward": (C.c_int, [vp, vp, i64, i32, i32, i64, f32, vp]),
     "tlb_adamw": (C.c_int, [vp, vp, vp, vp, i64, P(AdamwCfg), f32, vp, vp]),
+    "tlb_muon_workspace_bytes": (sz, [P(MuonMat), i32]),
+    "tlb_muon": (C.c_int, [P(MuonMat), i32, P(MuonCfg), vp, sz, vp]),
     "tlb_xent_workspace_bytes": (sz, [i32, i32, i64, i64, i64, i32]),
     "tlb_xent_forward": (C.c_int, [i32, vp, i32, vp, vp, i64, i64, i64, vp, vp, vp, sz, vp]),
     "tlb_xent_backward": (C.c_int, [i32, vp, i32, vp, vp, vp, vp, i64, i64, i64, vp, vp, vp, sz, vp]),

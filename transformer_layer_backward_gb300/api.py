@@ -149,6 +149,51 @@ def adamw(p, g, m, v, cfg: A.AdamwCfg, lr_mult=1.0, sumsq=None, stream=None):
            _ptr(sumsq, torch.float64, "sumsq"), _stream(stream))
 
 
+def muon_cfg(lr, momentum=0.95, weight_decay=0.0, eps=1e-7, coefficients=(3.4445, -4.7750, 2.0315), steps=5,
+             nesterov=True):
+    a, b, c = coefficients
+    return A.MuonCfg(lr, momentum, weight_decay, eps, a, b, c, int(steps), 1 if nesterov else 0)
+
+
+def muon_mats(params, grads, momenta, lr_mults=None, scales=None):
+    """The matrices of a Muon step, for muon() and muon_workspace(): equally long lists of
+    float32 matrices [rows, cols], min(rows, cols) <= 64.  lr_mults (1) multiply the learning
+    rate, scales (sqrt(max(1, rows / cols))) the orthogonal update.  Holds device pointers:
+    the tensors must stay alive and where they are while it is used."""
+    n = len(params)
+    if not (len(grads) == len(momenta) == n and (lr_mults is None or len(lr_mults) == n)
+            and (scales is None or len(scales) == n)):
+        raise ValueError("muon_mats: the lists differ in length")
+    mats = (A.MuonMat * max(n, 1))()
+    for i, (p, g, m) in enumerate(zip(params, grads, momenta)):
+        if p.dim() != 2 or g.shape != p.shape or m.shape != p.shape:
+            raise ValueError("muon_mats: matrix %d: param, grad and momentum must be matrices of one shape" % i)
+        if any(t.device != params[0].device for t in (p, g, m)):
+            raise ValueError("muon_mats: matrix %d is on another device" % i)
+        rows, cols = p.shape
+        mats[i] = A.MuonMat(_ptr(p, name="param"), _ptr(g, name="grad"), _ptr(m, name="momentum"), rows, cols,
+                            1.0 if lr_mults is None else float(lr_mults[i]),
+                            math.sqrt(max(1.0, rows / max(cols, 1))) if scales is None else float(scales[i]))
+    written = [q for mat in mats[:n] for q in (mat.p, mat.m) if q]
+    if len(set(written)) != len(written):
+        raise ValueError("muon_mats: the same tensor twice")
+    mats.n, mats.device = n, params[0].device if n else None
+    return mats
+
+
+def muon_workspace(mats, device="cuda"):
+    """A zeroed workspace tensor for muon() on these matrices (or on others of their shapes)."""
+    n = int(A.load().tlb_muon_workspace_bytes(mats, mats.n))
+    return torch.zeros(max(n, 256), dtype=torch.uint8, device=mats.device or device)
+
+
+def muon(mats, cfg: A.MuonCfg, ws, stream=None):
+    """One Muon step in place on the params and momenta of muon_mats(): momentum, the update
+    made orthogonal by Newton-Schulz steps, weight decay.  The counterpart of adamw()."""
+    with _on_device(ws):
+        A.call("tlb_muon", mats, mats.n, C.byref(cfg), _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream))
+
+
 # ------------------------------------------------------------------ the loss above the stack
 
 _XENT_CODE = {torch.float32: A.W_F32, torch.bfloat16: A.W_BF16}
