@@ -91,6 +91,20 @@ def test_xent(lib, rows, vocab, dim, types):
     check_gradient("d_hidden alone", host(only), rdh, np.abs(dz) @ np.abs(w), bf)
 
 
+@pytest.mark.parametrize("types", TYPES, ids="-".join)
+@pytest.mark.parametrize("rows,vocab,dim", [(1, 1, 2), (1, 9, 6000), (1, 30011, 1026), (2, 8, 64), (2, 1237, 2560),
+                                            (3, 1000, 320), (3, 5, 2), (4, 4099, 2560), (4, 12, 1022), (4, 300, 3074),
+                                            (5, 2000, 2560)])
+def test_few_rows(lib, rows, vocab, dim, types):
+    """Up to four rows of an even length take the one-pass kernel; a block of head rows that is
+    not full, one longer than the registers hold, and five rows beside it."""
+    n0 = lib.launch_count()
+    test_xent(lib, rows, vocab, dim, types)
+    names = lib.launch_names(n0)
+    one_pass = rows <= 4 and (rows == 1 or dim < 3073)
+    assert ("xent_token_loss" in names and "xent_token_grad" in names) == one_pass, names
+
+
 @pytest.mark.parametrize("types,rows,vocab,dim", [(("f32", "bf16"), 2048, 50001, 64),     # pieces of dz
                                                   (("f32", "f32"), 3, 36000, 2560),      # pieces of the packed head
                                                   (("bf16", "bf16"), 6000, 50001, 40),

@@ -68,6 +68,16 @@ int tc_gemm(const TcOperand *seg, int nseg, int64_t M, int64_t N, float alpha, f
 int act_backward_bf16_launch(int act, const float *gate, const float *up, const float *silu_gate, const float *dh,
                              void *dgate, void *dup, int64_t n, cudaStream_t st);
 
+// Cross entropy of a linear head for up to four rows (xent_token.cu): one pass over the head.
+bool xent_token_supported(int64_t N, int64_t D);
+// (max, sum) pairs of every row in *slots slots of part [slot][ld_part], and the targets' logits.
+int xent_token_loss(int htype, const void *hidden, int wtype, const void *W, const int64_t *targets, int64_t N, int64_t V,
+                    int64_t D, float2 *part, int64_t ld_part, float *zt, uint32_t *status, int *slots, cudaStream_t st);
+// partial: N D floats for every SM.
+int xent_token_grad(int htype, const void *hidden, int wtype, const void *W, const int64_t *targets, const float *lse,
+                    const float *d_loss, int64_t N, int64_t V, int64_t D, void *d_hidden, void *d_w, float *partial,
+                    uint32_t *status, cudaStream_t st);
+
 // Attention backward from dCtx to dQ(pre) and dV (attention.cu).
 struct AttnArgs {
     const float *dctx;       // [S, q_dim]

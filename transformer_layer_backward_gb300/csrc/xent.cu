@@ -25,7 +25,7 @@
 //
 // The tensor core cuts its fp32 sum after every MMA of 16 products (measured: a sum of 160
 // MMAs comes out about 1.2e-6 of its size short, one of 6144 3e-5).  Results of float32
-// precision are therefore summed in chunks of kChunk k blocks, which the epilogue adds up in
+// precision are therefore summed in chunks of a few k blocks, which the epilogue adds up in
 // registers, and the smaller term products come first, while the sum is small.
 //
 // Bounds: N >= 512 rows is bound by the tensor pipe (2 N V D flops a product), few rows by
@@ -48,7 +48,10 @@ constexpr int kBM = 128, kBK = 64;          // rows of a CTA's tile; k block (64
 constexpr int kThreads = 320;               // 10 warps: TMA producer, MMA issuer, 8 epilogue warps
 constexpr int kEpiWarps = 8;                // two per 32 TMEM lanes (rows), each half of the columns
 constexpr int kMaxTerms = 3, kMaxProd = 6;
-constexpr int kChunk = 20;                  // k blocks (80 MMAs) of one tensor-memory sum of a float32 result
+// k blocks (4 MMAs each) of one tensor-memory sum of a float32 result.  Reading a sum out takes
+// the tensor pipe about 300 cycles, and its error grows with its length: the loss of 2048 x
+// 2560 x 131072 is 3.7e-7 off at 8 k blocks (812 us), 9e-7 at 20 (787 us).
+constexpr int kChunkLoss = 14, kChunkGrad = 10;
 constexpr int kGroupM = 16;                 // row tiles that share a column tile before the next one
 constexpr int kBox = 4096;                  // bytes of a 32 x 64 bf16 box of dz
 constexpr float kLog2e = 1.4426950408889634f;
@@ -298,7 +301,7 @@ constexpr int stages_of() {
     return n > 6 ? 6 : n;
 }
 
-// TERMS: bf16 terms of dz (kGrad; 1 otherwise).  FINE: sums in chunks of kChunk k blocks.
+// TERMS: bf16 terms of dz (kGrad; 1 otherwise).  FINE: sums in chunks of k blocks.
 template <int BN, bool PAIR, int MODE, int TERMS, bool FINE, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_constant__ XParams p) {
     using S = Shape<BN, PAIR>;
@@ -316,7 +319,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
 
     // this unit's segments: its whole tiles, then its share of the split tiles, cut at tiles
     const int KB = p.nprod * p.kb;
-    const int chunk = FINE ? kChunk : KB;                    // k blocks of one accumulator
+    const int chunk = !FINE ? KB : MODE == kStats ? kChunkLoss : kChunkGrad;                    // k blocks of one accumulator
     const int64_t nwhole = p.whole > unit ? (p.whole - unit + p.units - 1) / p.units : 0;
     const bool splits = MODE == kOut && p.sk_work > 0 && unit < p.sk_units;
     const int64_t b0 = splits ? sk_start(p.sk_work, p.sk_units, unit) : 0;
@@ -616,8 +619,9 @@ __global__ void __launch_bounds__(256) xent_fixup_kernel(const __grid_constant__
     }
 }
 
-// Joins the (max, sum) pairs of a row's tiles: `rx` rows x 256 / rx threads a block; each
-// thread joins slots y, y + 256 / rx, ..., then the block joins its threads' pairs in order.
+// Joins the (max, sum) pairs of a row's tiles: rx rows x 256 / rx threads a block.  Each
+// thread joins slots y, y + 256 / rx, ..., eight at a time, then the block its threads' pairs
+// in a fixed tree.
 __global__ void __launch_bounds__(256) xent_join_kernel(const float2 *__restrict__ part, int64_t ld, int slots, int rows,
                                                         int rx, const float *__restrict__ zt,
                                                         const int64_t *__restrict__ targets, int64_t vocab,
@@ -625,17 +629,30 @@ __global__ void __launch_bounds__(256) xent_join_kernel(const float2 *__restrict
     __shared__ float2 sh[256];
     const int x = threadIdx.x % rx, y = threadIdx.x / rx, ny = 256 / rx;
     const int row = blockIdx.x * rx + x;
-    auto join = [](float2 a, float2 b) {
-        const float m = fmaxf(a.x, b.x), ref = (m == -INFINITY ? 0.f : m);
-        return make_float2(m, a.y * expf(a.x - ref) + b.y * expf(b.x - ref));
-    };
+    auto scaled = [](float2 a, float ref) { return a.y * ex2((a.x - ref) * kLog2e); };
     float2 a = make_float2(-INFINITY, 0.f);
-    if (row < rows)
-        for (int s = y; s < slots; s += ny) a = join(a, part[int64_t(s) * ld + row]);
+    for (int s = y; s < slots && row < rows; s += 8 * ny) {
+        float2 v[8];
+        float m = a.x;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+            v[u] = s + u * ny < slots ? part[int64_t(s + u * ny) * ld + row] : make_float2(-INFINITY, 0.f);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) m = fmaxf(m, v[u].x);
+        const float ref = m == -INFINITY ? 0.f : m;
+        float sum = scaled(a, ref);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) sum += scaled(v[u], ref);
+        a = make_float2(m, sum);
+    }
     sh[threadIdx.x] = a;
     for (int h = ny / 2; h > 0; h /= 2) {
         __syncthreads();
-        if (y < h) sh[threadIdx.x] = join(sh[threadIdx.x], sh[threadIdx.x + h * rx]);
+        if (y < h) {
+            const float2 b = sh[threadIdx.x + h * rx], c = sh[threadIdx.x];
+            const float m = fmaxf(b.x, c.x), ref = m == -INFINITY ? 0.f : m;
+            sh[threadIdx.x] = make_float2(m, scaled(c, ref) + scaled(b, ref));
+        }
     }
     if (y == 0 && row < rows) {
         const float2 r = sh[threadIdx.x];
@@ -815,7 +832,8 @@ Plan plan_of(int htype, int wtype, int64_t N, int64_t V, int64_t D, bool grad, b
     q.part = q.zt = q.dz = q.acc = q.partial = 0;
     if (!grad) {
         q.part_ld = ceil_div(std::min(N, kRowChunk), 32) * 32;
-        q.slots = 2 * (ceil_div(V, 128) + ceil_div(V, q.piece));           // 128-wide tiles: the most slots
+        // 128-wide tiles: the most slots; a slot an SM for up to four rows
+        q.slots = std::max<int64_t>(2 * (ceil_div(V, 128) + ceil_div(V, q.piece)), num_sms());
         q.part = w.take(size_t(q.part_ld) * q.slots * 8);
         q.zt = w.take(size_t(N) * 4);
     } else {
@@ -877,6 +895,16 @@ int head_operand(const Plan &q, int wtype, const void *W, int64_t v0, int64_t n,
     return pack(src, wtype, n, D, q.dp, q.w_terms, nullptr, 0, y, st);
 }
 
+int join(const Plan &q, void *ws, int64_t r0, int64_t n, int slots, const int64_t *targets, int64_t vocab, float *loss,
+         float *lse, cudaStream_t st) {
+    int rx = 1;                                              // a block for every SM first, then whole sectors
+    while (rx < 8 && 2 * rx * int64_t(num_sms()) <= n) rx *= 2;
+    xent_join_kernel<<<unsigned(ceil_div(n, rx)), 256, 0, st>>>(ws_at<float2>(ws, q.part), q.part_ld, slots, int(n), rx,
+                                                                ws_at<float>(ws, q.zt) + r0, targets + r0, vocab, loss + r0,
+                                                                lse + r0);
+    return check_launch("xent_join");
+}
+
 }  // namespace
 
 }  // namespace tlb
@@ -903,6 +931,12 @@ int tlb_xent_forward(int32_t htype, const void *hidden, int32_t wtype, const voi
     TLB_REQUIRE(ws != nullptr && (reinterpret_cast<uintptr_t>(ws) & 255) == 0 && ws_bytes >= q.total, TLB_EINVAL,
                 "xent_forward: needs a 256-byte aligned workspace of %zu bytes", q.total);
     cudaStream_t st = as_stream(stream);
+    if (xent_token_supported(rows, dim)) {
+        int slots = 0;
+        TLB_TRY(xent_token_loss(htype, hidden, wtype, W, targets, rows, vocab, dim, ws_at<float2>(ws, q.part), q.part_ld,
+                                ws_at<float>(ws, q.zt), ws_at<uint32_t>(ws, 0), &slots, st));
+        return join(q, ws, 0, rows, slots, targets, vocab, loss, lse, st);
+    }
     Mat h;
     TLB_TRY(hidden_operand(q, htype, hidden, rows, dim, nullptr, vocab, ws, st, h));
     const int64_t step = q.pack_w ? q.piece : vocab;
@@ -930,12 +964,7 @@ int tlb_xent_forward(int32_t htype, const void *hidden, int32_t wtype, const voi
             TLB_TRY((launch_z<kStats, 1>(p, hr, w, st)));
             slot += 2 * p.tiles_n;
         }
-        int rx = 1;
-        while (rx < 32 && rx < n) rx *= 2;
-        xent_join_kernel<<<unsigned(ceil_div(n, rx)), 256, 0, st>>>(ws_at<float2>(ws, q.part), q.part_ld, slot, int(n), rx,
-                                                                    ws_at<float>(ws, q.zt) + r0, targets + r0, vocab,
-                                                                    loss + r0, lse + r0);
-        TLB_TRY(check_launch("xent_join"));
+        TLB_TRY(join(q, ws, r0, n, slot, targets, vocab, loss, lse, st));
     }
     return TLB_OK;
 }
@@ -955,6 +984,9 @@ int tlb_xent_backward(int32_t htype, const void *hidden, int32_t wtype, const vo
     const Plan q = plan_of(htype, wtype, rows, vocab, dim, true, d_w != nullptr);
     TLB_REQUIRE(ws != nullptr && (reinterpret_cast<uintptr_t>(ws) & 255) == 0 && ws_bytes >= q.total, TLB_EINVAL,
                 "xent_backward: needs a 256-byte aligned workspace of %zu bytes", q.total);
+    if (xent_token_supported(rows, dim) && aligned16(d_w))
+        return xent_token_grad(htype, hidden, wtype, W, targets, lse, d_loss, rows, vocab, dim, d_hidden, d_w,
+                               ws_at<float>(ws, q.partial), ws_at<uint32_t>(ws, 0), st);
     Mat h;
     TLB_TRY(hidden_operand(q, htype, hidden, rows, dim, d_w != nullptr ? targets : nullptr, vocab, ws, st, h));
     const bool wide = htype == TLB_W_F32;
