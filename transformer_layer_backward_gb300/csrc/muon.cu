@@ -28,6 +28,7 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.cuh"
@@ -39,8 +40,8 @@ namespace {
 
 constexpr int kMaxMats = 256;            // matrices of one launch (their table is a kernel parameter)
 constexpr int kFirstRun = 2, kRun = 3;    // steps from the first and from each later Gram matrix
-constexpr int kCluster = 8;              // CTAs that hold one matrix
-constexpr int kPassThreads = 128, kPolyThreads = 256, kClusterThreads = 256;
+constexpr int kCluster = 8;              // CTAs of a cluster; 1, 2, 4 or 8 of them hold one matrix
+constexpr int NT = 256;                  // threads of every kernel
 
 struct Mat {
     float *p, *m;
@@ -49,7 +50,7 @@ struct Mat {
     int32_t r, n;
     int32_t tall;                        // stored [n, r] (else [r, n])
     int32_t vec;                         // 16-byte accesses (aligned; r % 4 == 0 of a tall one, n % 4 == 0 of a wide one)
-    int32_t block0;                      // first block of this matrix (multi-pass)
+    int32_t block0, ctas;                // first block of this matrix, and (clusters) how many
     float lr, lr_scale;                  // lr lr_mult, and times scale
 };
 
@@ -68,20 +69,19 @@ struct Params {
 enum Source { kMomentum = 0, kUpdate = 1, kY = 2 };   // m' and u; u from g and m'; Y
 enum Sink { kGram = 0, kGramY = 1, kParam = 2 };      // Gram matrix; X to Y and its Gram matrix; p
 
-// A tile of up to JT columns of X [r, n], in shared memory as [RP][LD]: 33 KB for r <= 16, 66
-// KB above.  LD = JT + 4: the same column of eight neighbouring rows lies in eight different
+// A tile of up to JT columns of X [r, n], in shared memory as [RP][LD]: 33 to 66 KB.  LD = JT + 4: the same column of eight neighbouring rows lies in eight different
 // groups of four banks.
 template <int RP> struct Tile {
-    static constexpr int JT = RP == 8 ? 1024 : RP == 64 ? 256 : 512;
+    static constexpr int JT = RP == 8 ? 1024 : RP == 16 ? 640 : RP == 32 ? 512 : 256;
     static constexpr int LD = JT + 4, XF = RP * LD;
     static constexpr int LM = RP + 4;                       // row length of an r x r matrix in shared memory
     // Gram blocks of B x B a thread (row k of block b is b + NB k); the upper PAIRS of them
     static constexpr int B = RP == 64 ? 8 : 4, NB = RP / B, PAIRS = NB * (NB + 1) / 2;
     static constexpr int GSIZE = PAIRS * B * B;             // floats of a Gram matrix's upper blocks
 };
-// NT threads form a Gram matrix in GROUPS groups, each with every GROUPS-th column quad; RG of
-// them at a time meet in a buffer of at most 9 KB.
-template <int RP, int NT> struct Gram {
+// The threads form a Gram matrix in GROUPS groups, each with every GROUPS-th column quad.  Where
+// the tile has to stay, RG of them at a time meet in a buffer of at most 9 KB.
+template <int RP> struct Gram {
     static constexpr int G0 = NT / Tile<RP>::PAIRS, GROUPS = G0 > 32 ? 32 : G0;
     static constexpr int R0 = 9216 / (Tile<RP>::GSIZE * 4), RG = R0 < 1 ? 1 : R0 > GROUPS ? GROUPS : R0;
     static constexpr int RF = RG * Tile<RP>::GSIZE;         // floats of the buffer
@@ -99,169 +99,208 @@ __device__ __forceinline__ void pair_of(int q, int &bi, int &bk) {
     bk = bi + q;
 }
 
-// Walks through a tile's elements (columns j0 .. j0 + jn) in pieces of cnt <= 4 that are
-// contiguous in memory: f(offset of the first, its place in the tile, places' step, cnt) for U
-// pieces at once, so that their loads are in flight together.
-template <int RP, int NT, int U, typename F>
+// Walks through a tile's elements (columns j0 .. j0 + jn): f(C, S, e, de, at, dat, n) for runs of
+// n pieces of this thread.  A piece is C::value contiguous elements; piece s starts at element
+// e + s de of the matrix and stands at at + s dat of the tile, its elements S::value places
+// apart.  Addresses go by increments only.
+template <int RP, typename F>
 __device__ __forceinline__ void visit(const Mat &a, int j0, int jn, F f) {
-    constexpr int LD = Tile<RP>::LD;
-    int64_t e[U];
-    int at[U], cnt[U];
-    auto divide = [](uint32_t x, uint32_t magic, int d) { return d > 1 ? int(__umulhi(x, magic)) : int(x); };
-    auto magic_of = [](int d) { return 0xFFFFFFFFu / uint32_t(d) + 1u; };           // exact below 2^16
-    if (a.tall && a.vec) {
-        // a warp takes 8 columns x 16 rows: 64 contiguous bytes a column
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        const int rq = a.r / 4, rb = (rq + 3) / 4, units = ((jn + 7) / 8) * rb;
-        for (int q0 = warp; q0 < units; q0 += U * (NT / 32)) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int q = q0 + u * (NT / 32), jb = q / rb;
-                const int j = jb * 8 + (lane >> 2), iq = (q - jb * rb) * 4 + (lane & 3);
-                cnt[u] = q < units && j < jn && iq < rq ? 4 : 0;
-                e[u] = int64_t(j0 + j) * a.r + iq * 4;
-                at[u] = iq * 4 * LD + j;
-            }
-            f(e, at, LD, cnt);
-        }
-    } else if (a.tall) {
-        const int total = jn * a.r;
-        const uint32_t magic = magic_of(a.r);
-        for (int q0 = threadIdx.x; q0 < total; q0 += U * NT) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int q = q0 + u * NT, j = divide(uint32_t(q), magic, a.r);
-                cnt[u] = q < total ? 1 : 0;
-                e[u] = int64_t(j0) * a.r + q;
-                at[u] = (q - j * a.r) * LD + j;
-            }
-            f(e, at, 0, cnt);
-        }
-    } else {
-        const int step = a.vec ? 4 : 1, w = (jn + step - 1) / step, total = w * a.r;   // vec: jn % 4 == 0
-        const uint32_t magic = magic_of(w);
-        for (int q0 = threadIdx.x; q0 < total; q0 += U * NT) {
-#pragma unroll
-            for (int u = 0; u < U; ++u) {
-                const int q = q0 + u * NT, i = divide(uint32_t(q), magic, w), j = (q - i * w) * step;
-                cnt[u] = q < total ? step : 0;
-                e[u] = int64_t(i) * a.n + j0 + j;
-                at[u] = i * LD + j;
-            }
-            f(e, at, 1, cnt);
-        }
+    constexpr int LD = Tile<RP>::LD, WARPS = NT / 32;
+    constexpr std::integral_constant<int, 1> one{};
+    constexpr std::integral_constant<int, 4> four{};
+    constexpr std::integral_constant<int, LD> ld{};
+    constexpr std::integral_constant<int, 32> k32{};
+    constexpr std::integral_constant<int, 8 * WARPS> k64{};
+    constexpr std::integral_constant<int, 128> k128{};
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (!a.tall && a.vec) {                                  // a warp a row, a lane four columns
+        const int n = (jn / 4 - lane + 31) >> 5;             // jn % 4 == 0
+#pragma unroll 1
+        for (int i = warp; i < a.r; i += WARPS)
+            f(four, one, int64_t(i) * a.n + j0 + 4 * lane, k128, i * LD + 4 * lane, k128, n);
+    } else if (!a.tall) {
+        const int n = (jn - lane + 31) >> 5;
+#pragma unroll 1
+        for (int i = warp; i < a.r; i += WARPS)
+            f(one, one, int64_t(i) * a.n + j0 + lane, k32, i * LD + lane, k32, n);
+    } else if (a.vec) {                                      // a warp 8 columns x 16 rows: 64 contiguous bytes a column
+        const int j = warp * 8 + (lane >> 2), n = (jn - j + 8 * WARPS - 1) / (8 * WARPS);
+#pragma unroll 1
+        for (int i = (lane & 3) * 4; i < a.r; i += 16)
+            f(four, ld, int64_t(j0 + j) * a.r + i, 8 * WARPS * a.r, i * LD + j, k64, n);
+    } else {                                                 // a thread a column
+#pragma unroll 1
+        for (int j = threadIdx.x; j < jn; j += NT) f(one, ld, int64_t(j0 + j) * a.r, one, j, ld, a.r);
     }
 }
 
-__device__ __forceinline__ void load4(const float *p, int64_t e, int cnt, float (&v)[4]) {
-    if (cnt == 4) {
-        const float4 x = *reinterpret_cast<const float4 *>(p + e);
+template <int C>
+__device__ __forceinline__ void load_piece(const float *p, float (&v)[C]) {
+    if constexpr (C == 4) {
+        const float4 x = *reinterpret_cast<const float4 *>(p);
         v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
     } else {
-        v[0] = cnt > 0 ? p[e] : 0.f;
+        v[0] = *p;
     }
 }
-__device__ __forceinline__ void keep4(float *p, int64_t e, int cnt, const float (&v)[4]) {
-    if (cnt == 4) *reinterpret_cast<float4 *>(p + e) = make_float4(v[0], v[1], v[2], v[3]);
-    else if (cnt > 0) p[e] = v[0];
+template <int C>
+__device__ __forceinline__ void keep_piece(float *p, const float (&v)[C]) {
+    if constexpr (C == 4) *reinterpret_cast<float4 *>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    else *p = v[0];
+}
+// To and from the tile, S places apart.
+template <int C, int S>
+__device__ __forceinline__ void put_piece(float *x, const float (&v)[C]) {
+    if constexpr (S == 1) {
+        keep_piece<C>(x, v);
+    } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c) x[c * S] = v[c];
+    }
+}
+template <int C, int S>
+__device__ __forceinline__ void take_piece(const float *x, float (&v)[C]) {
+    if constexpr (S == 1) {
+        load_piece<C>(x, v);
+    } else {
+#pragma unroll
+        for (int c = 0; c < C; ++c) v[c] = x[c * S];
+    }
 }
 
 // Rows past r, and columns jn .. up to a whole quad, count as 0.
-template <int RP, int NT>
+template <int RP>
 __device__ __forceinline__ void clear_rest(const Mat &a, float *x, int jn) {
     constexpr int LD = Tile<RP>::LD;
     const int j4 = (jn + 3) & ~3;
+#pragma unroll 1
     for (int k = threadIdx.x; k < (RP - a.r) * j4; k += NT) x[(a.r + k / j4) * LD + k % j4] = 0.f;
     if (j4 > jn)
+#pragma unroll 1
         for (int k = threadIdx.x; k < a.r * (j4 - jn); k += NT) x[(k / (j4 - jn)) * LD + jn + k % (j4 - jn)] = 0.f;
 }
 
+constexpr int kFlight = 4;               // pieces of a thread whose loads are in flight together
+
 // The tile of u, from g and the momentum, which FIRST brings up to date.
-template <int RP, int NT, bool FIRST>
+template <int RP, bool FIRST>
 __device__ __forceinline__ void load_update(const Params &p, const Mat &a, float *x, int j0, int jn) {
-    constexpr int U = 4;
-    clear_rest<RP, NT>(a, x, jn);
-    visit<RP, NT, U>(a, j0, jn, [&](const int64_t (&e)[U], const int (&at)[U], int step, const int (&cnt)[U]) {
-        float g[U][4], m[U][4];
+    constexpr int U = kFlight;
+    const float mu = p.mu;
+    const bool nesterov = p.nesterov != 0;
+    clear_rest<RP>(a, x, jn);
+    visit<RP>(a, j0, jn, [&](auto cc, auto ss, int64_t e, auto de, int at, auto dat, int n) {
+        constexpr int C = decltype(cc)::value, S = decltype(ss)::value;
+        const float *gp = a.g + e;
+        float *mp = a.m + e, *xp = x + at;
+#pragma unroll 1
+        for (int s = 0; s < n; s += U, gp += U * de, mp += U * de, xp += U * dat) {
+            float g[U][C], m[U][C];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            load4(a.g, e[u], cnt[u], g[u]);
-            load4(a.m, e[u], cnt[u], m[u]);
-        }
+            for (int u = 0; u < U; ++u)
+                {
+                    const int o = min(u, n - 1 - s) * de;
+                    load_piece<C>(gp + o, g[u]);
+                    load_piece<C>(mp + o, m[u]);
+                }
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            if constexpr (FIRST) {
+            for (int u = 0; u < U; ++u)
+                if (s + u < n) {
+                    if constexpr (FIRST) {
 #pragma unroll
-                for (int c = 0; c < 4; ++c) m[u][c] = fmaf(p.mu, m[u][c], g[u][c]);
-                keep4(a.m, e[u], cnt[u], m[u]);
-            }
+                        for (int c = 0; c < C; ++c) m[u][c] = fmaf(mu, m[u][c], g[u][c]);
+                        keep_piece<C>(mp + u * de, m[u]);
+                    }
+                    if (nesterov) {
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (c < cnt[u]) x[at[u] + c * step] = p.nesterov ? fmaf(p.mu, m[u][c], g[u][c]) : m[u][c];
+                        for (int c = 0; c < C; ++c) m[u][c] = fmaf(mu, m[u][c], g[u][c]);
+                    }
+                    put_piece<C, S>(xp + u * dat, m[u]);
+                }
         }
     });
 }
 
 // p moved along the tile.
-template <int RP, int NT>
+template <int RP>
 __device__ __forceinline__ void move_params(const Params &p, const Mat &a, const float *x, int j0, int jn) {
-    constexpr int U = 4;
-    visit<RP, NT, U>(a, j0, jn, [&](const int64_t (&e)[U], const int (&at)[U], int step, const int (&cnt)[U]) {
-        float v[U][4];
+    constexpr int U = kFlight;
+    const float decay = a.lr * p.wd, move = a.lr_scale;
+    visit<RP>(a, j0, jn, [&](auto cc, auto ss, int64_t e, auto de, int at, auto dat, int n) {
+        constexpr int C = decltype(cc)::value, S = decltype(ss)::value;
+        float *pp = a.p + e;
+        const float *xp = x + at;
+#pragma unroll 1
+        for (int s = 0; s < n; s += U, pp += U * de, xp += U * dat) {
+            float v[U][C];
 #pragma unroll
-        for (int u = 0; u < U; ++u) load4(a.p, e[u], cnt[u], v[u]);
+            for (int u = 0; u < U; ++u)
+                load_piece<C>(pp + min(u, n - 1 - s) * de, v[u]);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+            for (int u = 0; u < U; ++u)
+                if (s + u < n) {
+                    float o[C];
+                    take_piece<C, S>(xp + u * dat, o);
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-                if (c < cnt[u]) v[u][c] -= a.lr * p.wd * v[u][c] + a.lr_scale * x[at[u] + c * step];
-            keep4(a.p, e[u], cnt[u], v[u]);
+                    for (int c = 0; c < C; ++c) v[u][c] -= fmaf(move, o[c], __fmul_rn(decay, v[u][c]));
+                    keep_piece<C>(pp + u * de, v[u]);
+                }
         }
     });
 }
 
-// X <- M X on the shared tile: a thread takes two columns whole into registers, so the product
-// goes back in place without a barrier.  mt: M's columns as rows (the same for all threads).
-template <int RP, int NT>
+// X <- M X on the shared tile: a thread owns a column pair (for r > 32 half of its rows), so
+// the product goes back in place, past one barrier where two threads share a column.  mt: M's
+// columns as rows; the same for all threads, as x is for the rows of a column.
+template <int RP>
 __device__ __forceinline__ void apply(float *x, const float *mt, int jn) {
     constexpr int LD = Tile<RP>::LD, LM = Tile<RP>::LM;
+    constexpr int RH = RP > 32 ? 32 : RP, HALVES = RP / RH, W = NT / HALVES;
+    static_assert(HALVES == 1 || 2 * W >= Tile<RP>::JT, "all columns at once where a barrier stands between");
+    const int i0 = HALVES == 1 ? 0 : (threadIdx.x / W) * RH;
 #pragma unroll 1
-    for (int j = 2 * threadIdx.x; j < jn; j += 2 * NT) {
-        float2 v[RP];
+    for (int jb = 0; jb < jn; jb += 2 * W) {
+        const int j = jb + 2 * (threadIdx.x % W);
+        float2 y[RH];
 #pragma unroll
-        for (int k = 0; k < RP; ++k) v[k] = *reinterpret_cast<const float2 *>(x + k * LD + j);
-#pragma unroll 1
-        for (int i = 0; i < RP; i += 4) {
-            float2 y[4];
-#pragma unroll
-            for (int d = 0; d < 4; ++d) y[d] = make_float2(0.f, 0.f);
-#pragma unroll
+        for (int i = 0; i < RH; ++i) y[i] = make_float2(0.f, 0.f);
+        if (j < jn) {
+#pragma unroll 2
             for (int k = 0; k < RP; ++k) {
-                const float4 w = *reinterpret_cast<const float4 *>(mt + k * LM + i);
-                y[0].x = fmaf(w.x, v[k].x, y[0].x); y[0].y = fmaf(w.x, v[k].y, y[0].y);
-                y[1].x = fmaf(w.y, v[k].x, y[1].x); y[1].y = fmaf(w.y, v[k].y, y[1].y);
-                y[2].x = fmaf(w.z, v[k].x, y[2].x); y[2].y = fmaf(w.z, v[k].y, y[2].y);
-                y[3].x = fmaf(w.w, v[k].x, y[3].x); y[3].y = fmaf(w.w, v[k].y, y[3].y);
-            }
+                const float2 v = *reinterpret_cast<const float2 *>(x + k * LD + j);
 #pragma unroll
-            for (int d = 0; d < 4; ++d) *reinterpret_cast<float2 *>(x + (i + d) * LD + j) = y[d];
+                for (int i = 0; i < RH; i += 4) {
+                    const float4 w = *reinterpret_cast<const float4 *>(mt + k * LM + i0 + i);
+                    y[i].x = fmaf(w.x, v.x, y[i].x); y[i].y = fmaf(w.x, v.y, y[i].y);
+                    y[i + 1].x = fmaf(w.y, v.x, y[i + 1].x); y[i + 1].y = fmaf(w.y, v.y, y[i + 1].y);
+                    y[i + 2].x = fmaf(w.z, v.x, y[i + 2].x); y[i + 2].y = fmaf(w.z, v.y, y[i + 2].y);
+                    y[i + 3].x = fmaf(w.w, v.x, y[i + 3].x); y[i + 3].y = fmaf(w.w, v.y, y[i + 3].y);
+                }
+            }
+        }
+        if constexpr (HALVES > 1) __syncthreads();
+        if (j < jn) {
+#pragma unroll
+            for (int i = 0; i < RH; ++i) *reinterpret_cast<float2 *>(x + (i0 + i) * LD + j) = y[i];
         }
     }
 }
 
-// This thread's share of the tile's Gram matrix added to acc: block (bi, bk) over the column
+// This thread's share of the tile's Gram matrix: block (bi, bk) over the column
 // quads grp, grp + GROUPS, ...
-template <int RP, int NT>
-__device__ __forceinline__ void gram_add(const float *x, int jn, float (&acc)[Tile<RP>::B][Tile<RP>::B]) {
+template <int RP>
+__device__ __forceinline__ void gram_tile(const float *x, int jn, float (&acc)[Tile<RP>::B][Tile<RP>::B]) {
     using T = Tile<RP>;
     constexpr int B = T::B, NB = T::NB, LD = T::LD;
     const int grp = threadIdx.x / T::PAIRS;
-    if (grp >= Gram<RP, NT>::GROUPS) return;
+#pragma unroll
+    for (int k = 0; k < B * B; ++k) acc[k / B][k % B] = 0.f;
+    if (grp >= Gram<RP>::GROUPS) return;
     int bi, bk;
     pair_of<NB>(threadIdx.x % T::PAIRS, bi, bk);
     const int quads = (jn + 3) / 4;
 #pragma unroll 1
-    for (int q = grp; q < quads; q += Gram<RP, NT>::GROUPS) {
+    for (int q = grp; q < quads; q += Gram<RP>::GROUPS) {
         float4 s[B];
 #pragma unroll
         for (int k = 0; k < B; ++k) s[k] = *reinterpret_cast<const float4 *>(x + (bi + NB * k) * LD + 4 * q);
@@ -275,26 +314,23 @@ __device__ __forceinline__ void gram_add(const float *x, int jn, float (&acc)[Ti
     }
 }
 
-// The groups' shares added up in group order: out[e] = sum of element e (e < GSIZE, in the
-// order [pair][B * B]); red: Gram::RF floats.
-template <int RP, int NT>
-__device__ __forceinline__ void gram_sum(const float (&acc)[Tile<RP>::B][Tile<RP>::B], float *red, float *out) {
+// The groups' shares added up in group order, RG at a time through red (RG GSIZE floats), onto
+// s: this thread's elements threadIdx.x + o NT of the order [B * B][pair].
+template <int RP, int RG>
+__device__ __forceinline__ void gram_sum(const float (&acc)[Tile<RP>::B][Tile<RP>::B], float *red, float (&s)[Gram<RP>::OWN]) {
     using T = Tile<RP>;
-    using G = Gram<RP, NT>;
+    using G = Gram<RP>;
     constexpr int B = T::B;
     const int grp = threadIdx.x / T::PAIRS, pair = threadIdx.x % T::PAIRS;
-    float s[G::OWN];
-#pragma unroll
-    for (int o = 0; o < G::OWN; ++o) s[o] = 0.f;
 #pragma unroll 1
-    for (int g0 = 0; g0 < G::GROUPS; g0 += G::RG) {
+    for (int g0 = 0; g0 < G::GROUPS; g0 += RG) {
         __syncthreads();
-        if (grp >= g0 && grp < g0 + G::RG && grp < G::GROUPS) {
+        if (grp >= g0 && grp < g0 + RG && grp < G::GROUPS) {
 #pragma unroll
             for (int k = 0; k < B * B; ++k) red[(grp - g0) * T::GSIZE + k * T::PAIRS + pair] = acc[k / B][k % B];
         }
         __syncthreads();
-        const int n = min(G::RG, G::GROUPS - g0);
+        const int n = min(RG, G::GROUPS - g0);
 #pragma unroll
         for (int o = 0; o < G::OWN; ++o) {
             const int e = threadIdx.x + o * NT;
@@ -302,10 +338,13 @@ __device__ __forceinline__ void gram_sum(const float (&acc)[Tile<RP>::B][Tile<RP
                 for (int k = 0; k < n; ++k) s[o] += red[k * T::GSIZE + e];
         }
     }
+}
+template <int RP>
+__device__ __forceinline__ void gram_keep(const float (&s)[Gram<RP>::OWN], float *out) {
 #pragma unroll
-    for (int o = 0; o < G::OWN; ++o) {
+    for (int o = 0; o < Gram<RP>::OWN; ++o) {
         const int e = threadIdx.x + o * NT;
-        if (e < T::GSIZE) out[e] = s[o];
+        if (e < Tile<RP>::GSIZE) out[e] = s[o];
     }
 }
 
@@ -321,87 +360,110 @@ __device__ __forceinline__ void gram_place(int e, int &i, int &k) {
 }
 
 // The product of `steps` Newton-Schulz polynomials P of G, times `scale`, in mm.  gm: G
-// (symmetric; changed); sq, pm: scratch; all [RP][LM].  G and P are symmetric: a row stands
-// for a column.  Called by NT threads, D x D elements each.
-template <int RP, int NT>
+// (symmetric; changed); sq, pm: scratch; all [RP][LM].  G and P are kept symmetric (the upper
+// triangle, mirrored), so that a row stands for a column.  r <= 16: one warp, without block
+// barriers, while the others wait; else all threads.
+template <int RP>
 __device__ __forceinline__ void polynomial(float *gm, float *sq, float *pm, float *mm, int steps, float a, float b, float c,
                                            float scale) {
     constexpr int LM = Tile<RP>::LM;
-    constexpr int D = RP == 64 ? 4 : RP == 32 ? 2 : 1, W = RP / D;
-    static_assert(W * W <= NT, "threads of a product");
-    const int tid = threadIdx.x, r0 = (tid / W) * D, c0 = (tid % W) * D;
-    const bool on = tid < W * W;
-    // out = f(sum_k x[k][r] y[k][c])
-    auto product = [&](const float *x, const float *y, float *out, auto f) {
-        float acc[D][D];
+    constexpr bool WARP = RP <= 16;
+    // a thread's DR x DC elements
+    constexpr int DC = RP == 64 ? 4 : RP == 8 ? 1 : 2, DR = RP == 64 || RP == 16 ? 4 : 2, W = RP / DC;
+    static_assert(W * (RP / DR) <= (WARP ? 32 : NT), "threads of a product");
+    const int tid = threadIdx.x, r0 = (tid / W) * DR, c0 = (tid % W) * DC;
+    const bool on = r0 < RP;
+    auto sync = [] {
+        if constexpr (WARP) __syncwarp();
+        else __syncthreads();
+    };
+    // out = sum_k x[k][r] y[k][c]; SYM: only the upper triangle counts and is mirrored
+    enum { PLAIN, SYM, POLY };
+    auto product = [&](const float *x, const float *y, float *out, auto kind) {
+        constexpr int KIND = decltype(kind)::value;
+        float acc[DR][DC];
 #pragma unroll
-        for (int s = 0; s < D; ++s)
+        for (int s = 0; s < DR; ++s)
 #pragma unroll
-            for (int t = 0; t < D; ++t) acc[s][t] = 0.f;
-        if (on) {
-#pragma unroll 8
+            for (int t = 0; t < DC; ++t) acc[s][t] = 0.f;
+        const bool mine = on && (KIND == PLAIN || r0 < c0 + DC);
+        if (mine) {
+#pragma unroll 16
             for (int k = 0; k < RP; ++k) {
-                float u[D], v[D];
-                if constexpr (D == 4) {
-                    const float4 q = *reinterpret_cast<const float4 *>(x + k * LM + r0), w = *reinterpret_cast<const float4 *>(y + k * LM + c0);
+                float u[DR], v[DC];
+                if constexpr (DR == 4) {
+                    const float4 q = *reinterpret_cast<const float4 *>(x + k * LM + r0);
                     u[0] = q.x; u[1] = q.y; u[2] = q.z; u[3] = q.w;
-                    v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
-                } else if constexpr (D == 2) {
-                    const float2 q = *reinterpret_cast<const float2 *>(x + k * LM + r0), w = *reinterpret_cast<const float2 *>(y + k * LM + c0);
-                    u[0] = q.x; u[1] = q.y;
-                    v[0] = w.x; v[1] = w.y;
                 } else {
-                    u[0] = x[k * LM + r0];
+                    const float2 q = *reinterpret_cast<const float2 *>(x + k * LM + r0);
+                    u[0] = q.x; u[1] = q.y;
+                }
+                if constexpr (DC == 4) {
+                    const float4 q = *reinterpret_cast<const float4 *>(y + k * LM + c0);
+                    v[0] = q.x; v[1] = q.y; v[2] = q.z; v[3] = q.w;
+                } else if constexpr (DC == 2) {
+                    const float2 q = *reinterpret_cast<const float2 *>(y + k * LM + c0);
+                    v[0] = q.x; v[1] = q.y;
+                } else {
                     v[0] = y[k * LM + c0];
                 }
 #pragma unroll
-                for (int s = 0; s < D; ++s)
+                for (int s = 0; s < DR; ++s)
 #pragma unroll
-                    for (int t = 0; t < D; ++t) acc[s][t] = fmaf(u[s], v[t], acc[s][t]);
+                    for (int t = 0; t < DC; ++t) acc[s][t] = fmaf(u[s], v[t], acc[s][t]);
+            }
+            if constexpr (KIND == POLY) {                    // a I + b x + c x^2
+#pragma unroll
+                for (int s = 0; s < DR; ++s)
+#pragma unroll
+                    for (int t = 0; t < DC; ++t)
+                        acc[s][t] = fmaf(c, acc[s][t], fmaf(b, x[(r0 + s) * LM + c0 + t], r0 + s == c0 + t ? a : 0.f));
             }
         }
-        __syncthreads();                                     // out may be x or y
-        if (on) {
+        sync();                                              // out may be x or y
+        if (mine) {
 #pragma unroll
-            for (int s = 0; s < D; ++s)
+            for (int s = 0; s < DR; ++s)
 #pragma unroll
-                for (int t = 0; t < D; ++t) out[(r0 + s) * LM + c0 + t] = f(acc[s][t], r0 + s, c0 + t);
+                for (int t = 0; t < DC; ++t) {
+                    const int i = r0 + s, k = c0 + t;
+                    if (KIND == PLAIN || i <= k) out[i * LM + k] = acc[s][t];
+                    if (KIND != PLAIN && i < k) out[k * LM + i] = acc[s][t];
+                }
         }
-        __syncthreads();
+        sync();
     };
-    auto same = [](float v, int, int) { return v; };
-    for (int s = 0; s < steps; ++s) {
-        // the first P is the product so far, and carries the scale; P itself is needed without
-        // it while G goes on
-        product(gm, gm, pm, [&](float v, int i, int k) { return fmaf(c, v, fmaf(b, gm[i * LM + k], i == k ? a : 0.f)); });
-        if (s == 0) {
-            if (on) {
+    constexpr std::integral_constant<int, PLAIN> plain{};
+    constexpr std::integral_constant<int, SYM> sym{};
+    constexpr std::integral_constant<int, POLY> poly{};
+    if (!WARP || tid < 32) {
+        for (int s = 0; s < steps; ++s) {
+            product(gm, gm, pm, poly);
+            if (s == 0) {
+                if (on) {
 #pragma unroll
-                for (int u = 0; u < D; ++u)
+                    for (int u = 0; u < DR; ++u)
 #pragma unroll
-                    for (int t = 0; t < D; ++t) mm[(r0 + u) * LM + c0 + t] = pm[(r0 + u) * LM + c0 + t] * scale;
+                        for (int t = 0; t < DC; ++t) mm[(r0 + u) * LM + c0 + t] = pm[(r0 + u) * LM + c0 + t] * scale;
+                }
+                sync();
+            } else {
+                product(pm, mm, mm, plain);
             }
-            __syncthreads();
-        } else {
-            product(pm, mm, mm, same);
-        }
-        if (s + 1 < steps) {
-            // G of the next X: P G P with one factor on either side, made symmetric again
-            // (G P P, equal but for rounding, or a G left unsymmetric, cost a digit in X)
-            product(gm, pm, sq, same);                       // G P
-            product(sq, pm, gm, same);                       // (G P)^T P
-            for (int e = tid; e < RP * RP; e += NT) {
-                const int i = e / RP, k = e % RP;
-                if (i < k) gm[i * LM + k] = gm[k * LM + i] = 0.5f * (gm[i * LM + k] + gm[k * LM + i]);
+            if (s + 1 < steps) {
+                // G of the next X: P G P with one factor on either side (G P P, equal but for
+                // rounding, or a G left unsymmetric, cost a digit in X)
+                product(gm, pm, sq, plain);                  // G P
+                product(sq, pm, gm, sym);                    // (G P)^T P
             }
-            __syncthreads();
         }
     }
+    __syncthreads();
 }
 
 // 1 / (|u|_F + eps) from the Gram matrix of u, which becomes that of X0.  A zero update stays
 // zero, also for eps = 0.
-template <int RP, int NT>
+template <int RP>
 __device__ __forceinline__ float normalise(float *gm, float *s_inv, float eps) {
     constexpr int LM = Tile<RP>::LM;
     if (threadIdx.x < 32) {
@@ -425,41 +487,56 @@ __device__ __forceinline__ float ld_cluster(const float *p, int rank) {
 
 // ---------------------------------------------------------------- one matrix a cluster
 
-// The whole step of a matrix whose X fits the shared memory of kCluster CTAs: CTA c holds
-// columns [c w, (c + 1) w).  X never leaves the SMs: 20 bytes an element cross, as they must.
-// Gram matrices are summed over the cluster through distributed shared memory, by every CTA in
-// rank order, and every CTA forms the r x r products for itself.
+// The whole step of a matrix whose X fits the shared memory of a.ctas CTAs of a cluster: CTA c
+// of them holds columns [c w, (c + 1) w).  X never leaves the SMs: 20 bytes an element cross,
+// as they must.  Gram matrices are summed through distributed shared memory, by every CTA in
+// rank order, and every CTA forms the r x r products for itself.  A cluster holds 8 / a.ctas
+// matrices, which all meet at its barriers; CTAs left over (block0 is a multiple of 8 where
+// a.ctas changes) only do that.
 template <int RP> constexpr int cluster_floats() {
-    return Tile<RP>::XF + Gram<RP, kClusterThreads>::RF + 2 * Tile<RP>::GSIZE + 4 * RP * Tile<RP>::LM;
+    return Tile<RP>::XF + Gram<RP>::RF + 2 * Tile<RP>::GSIZE + 4 * RP * Tile<RP>::LM;
 }
 
 template <int RP>
-__global__ void __launch_bounds__(kClusterThreads) muon_cluster_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(NT, RP <= 16 ? 4 : 1) muon_cluster_kernel(const __grid_constant__ Params p) {
     using T = Tile<RP>;
-    constexpr int NT = kClusterThreads, LM = T::LM, B = T::B;
+    constexpr int LM = T::LM, B = T::B;
     extern __shared__ __align__(16) float sh[];
     float *x = sh, *gm = x + T::XF, *sq = gm + RP * LM, *pm = sq + RP * LM, *mm = pm + RP * LM;
     float *part = mm + RP * LM, *red = part + 2 * T::GSIZE;  // part: two, for alternate runs
     __shared__ float s_inv;
-    const Mat &a = p.mat[blockIdx.x / kCluster];
-    const int rank = int(cluster_rank());
-    const int w = ((a.n + kCluster - 1) / kCluster + 3) & ~3;
+    int lo = 0, hi = p.nmat - 1;                            // this CTA's matrix
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (p.mat[mid].block0 <= int(blockIdx.x)) lo = mid;
+        else hi = mid - 1;
+    }
+    const Mat &a = p.mat[lo];
+    const int rank = int(blockIdx.x) - a.block0, ctas = a.ctas;
+    if (rank >= ctas) {
+        for (int done = 0; done < p.steps; done += done == 0 ? kFirstRun : kRun) cluster_sync();
+        cluster_sync();
+        return;
+    }
+    const int peer0 = int(cluster_rank()) - rank;
+    const int w = ((a.n + ctas - 1) / ctas + 3) & ~3;
     const int j0 = min(a.n, rank * w), jn = min(w, a.n - j0);
-    load_update<RP, NT, true>(p, a, x, j0, jn);
+    load_update<RP, true>(p, a, x, j0, jn);
     float scale = 1.f;
     for (int done = 0, run = 0; done < p.steps; ++run) {
         __syncthreads();
-        float acc[B][B];
-#pragma unroll
-        for (int k = 0; k < B * B; ++k) acc[k / B][k % B] = 0.f;
-        gram_add<RP, NT>(x, jn, acc);
         float *mine = part + (run & 1) * T::GSIZE;
-        gram_sum<RP, NT>(acc, red, mine);
+        {
+            float acc[B][B], s[Gram<RP>::OWN] = {};
+            gram_tile<RP>(x, jn, acc);
+            gram_sum<RP, Gram<RP>::RG>(acc, red, s);
+            gram_keep<RP>(s, mine);
+        }
         cluster_sync();
         for (int e = threadIdx.x; e < T::GSIZE; e += NT) {
             float v[kCluster], s = 0.f;
 #pragma unroll
-            for (int c = 0; c < kCluster; ++c) v[c] = ld_cluster(mine + e, c);
+            for (int c = 0; c < kCluster; ++c) v[c] = c < ctas ? ld_cluster(mine + e, peer0 + c) : 0.f;
 #pragma unroll
             for (int c = 0; c < kCluster; ++c) s += v[c];
             int i, k;
@@ -468,29 +545,30 @@ __global__ void __launch_bounds__(kClusterThreads) muon_cluster_kernel(const __g
             gm[k * LM + i] = s;
         }
         __syncthreads();
-        if (run == 0) scale = normalise<RP, NT>(gm, &s_inv, p.eps);
+        if (run == 0) scale = normalise<RP>(gm, &s_inv, p.eps);
         const int steps = min(run == 0 ? kFirstRun : kRun, p.steps - done);
-        polynomial<RP, NT>(gm, sq, pm, mm, steps, p.a, p.b, p.c, run == 0 ? scale : 1.f);
+        polynomial<RP>(gm, sq, pm, mm, steps, p.a, p.b, p.c, run == 0 ? scale : 1.f);
         done += steps;
-        apply<RP, NT>(x, mm, jn);
+        apply<RP>(x, mm, jn);
     }
     __syncthreads();
-    move_params<RP, NT>(p, a, x, j0, jn);
+    move_params<RP>(p, a, x, j0, jn);
     cluster_sync();                                          // peers have read the last partial sums
 }
 
 // ---------------------------------------------------------------- passes over longer matrices
 
 template <int RP> constexpr int pass_floats() {
-    return Tile<RP>::XF + Gram<RP, kPassThreads>::RF + RP * Tile<RP>::LM;
+    static_assert(Gram<RP>::GROUPS * Tile<RP>::GSIZE <= Tile<RP>::XF, "the groups meet in the tile's place");
+    return Tile<RP>::XF + RP * Tile<RP>::LM;
 }
 
 template <int RP, int SOURCE, int SINK>
-__global__ void __launch_bounds__(kPassThreads) muon_pass_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(NT, RP == 64 ? 2 : 1) muon_pass_kernel(const __grid_constant__ Params p) {
     using T = Tile<RP>;
-    constexpr int NT = kPassThreads, JT = T::JT, LD = T::LD, LM = T::LM, B = T::B;
+    constexpr int JT = T::JT, LD = T::LD, LM = T::LM, B = T::B;
     extern __shared__ __align__(16) float sh[];
-    float *x = sh, *mt = x + T::XF, *red = mt + RP * LM;
+    float *x = sh, *mt = x + T::XF;
     int lo = 0, hi = p.nmat - 1;                            // this block's matrix
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
@@ -504,9 +582,7 @@ __global__ void __launch_bounds__(kPassThreads) muon_pass_kernel(const __grid_co
         const float *src = p.ws + p.mpoly + int64_t(lo) * RP * RP;
         for (int k = threadIdx.x; k < RP * RP; k += NT) mt[(k / RP) * LM + k % RP] = src[k];
     }
-    float acc[B][B];
-#pragma unroll
-    for (int k = 0; k < B * B; ++k) acc[k / B][k % B] = 0.f;
+    float s[Gram<RP>::OWN] = {};
     for (int t = t0; t < t1; ++t) {
         const int j0 = t * JT, jn = min(JT, a.n - j0);
         float *y = p.ws + a.y + int64_t(t) * RP * JT;       // this tile of Y: [RP][JT]
@@ -515,15 +591,15 @@ __global__ void __launch_bounds__(kPassThreads) muon_pass_kernel(const __grid_co
             for (int k = threadIdx.x; k < RP * (JT / 4); k += NT)
                 *reinterpret_cast<float4 *>(x + (k / (JT / 4)) * LD + (k % (JT / 4)) * 4) = reinterpret_cast<const float4 *>(y)[k];
         } else {
-            load_update<RP, NT, SOURCE == kMomentum>(p, a, x, j0, jn);
+            load_update<RP, SOURCE == kMomentum>(p, a, x, j0, jn);
         }
         __syncthreads();
         if constexpr (SOURCE != kMomentum) {
-            apply<RP, NT>(x, mt, jn);
+            apply<RP>(x, mt, jn);
             __syncthreads();
         }
         if constexpr (SINK == kParam) {
-            move_params<RP, NT>(p, a, x, j0, jn);
+            move_params<RP>(p, a, x, j0, jn);
         } else {
             if constexpr (SINK == kGramY) {
                 const int jq = (jn + 3) / 4;
@@ -531,23 +607,25 @@ __global__ void __launch_bounds__(kPassThreads) muon_pass_kernel(const __grid_co
                     *reinterpret_cast<float4 *>(y + (k / jq) * JT + (k % jq) * 4) =
                         *reinterpret_cast<const float4 *>(x + (k / jq) * LD + (k % jq) * 4);
             }
-            gram_add<RP, NT>(x, jn, acc);
+            float acc[B][B];
+            gram_tile<RP>(x, jn, acc);
+            gram_sum<RP, Gram<RP>::GROUPS>(acc, x, s);       // the tile is used up
         }
     }
-    if constexpr (SINK != kParam) gram_sum<RP, NT>(acc, red, p.ws + a.part + int64_t(bl) * T::GSIZE);
+    if constexpr (SINK != kParam) gram_keep<RP>(s, p.ws + a.part + int64_t(bl) * T::GSIZE);
 }
 
 // One matrix a block: G from its partial sums in block order, then M.
 template <int RP>
-__global__ void __launch_bounds__(kPolyThreads) muon_poly_kernel(const __grid_constant__ Params p, int done, int steps) {
+__global__ void __launch_bounds__(NT) muon_poly_kernel(const __grid_constant__ Params p, int done, int steps) {
     using T = Tile<RP>;
-    constexpr int LM = T::LM, NT = kPolyThreads;
+    constexpr int LM = T::LM;
     extern __shared__ __align__(16) float sh[];
     float *gm = sh, *sq = gm + RP * LM, *pm = sq + RP * LM, *mm = pm + RP * LM;
     __shared__ float s_inv;
     const Mat &a = p.mat[blockIdx.x];
     const float *part = p.ws + a.part;
-    const int nb = ((a.n + T::JT - 1) / T::JT + p.tiles_per_block - 1) / p.tiles_per_block;
+    const int nb = a.ctas;
     for (int e = threadIdx.x; e < T::GSIZE; e += NT) {
         float s = 0.f;
         for (int k = 0; k < nb; k += 8) {
@@ -563,8 +641,8 @@ __global__ void __launch_bounds__(kPolyThreads) muon_poly_kernel(const __grid_co
         gm[k * LM + i] = s;
     }
     __syncthreads();
-    const float scale = done == 0 ? normalise<RP, NT>(gm, &s_inv, p.eps) : 1.f;
-    polynomial<RP, NT>(gm, sq, pm, mm, steps, p.a, p.b, p.c, scale);
+    const float scale = done == 0 ? normalise<RP>(gm, &s_inv, p.eps) : 1.f;
+    polynomial<RP>(gm, sq, pm, mm, steps, p.a, p.b, p.c, scale);
     float *out = p.ws + p.mpoly + int64_t(blockIdx.x) * RP * RP;
     for (int e = threadIdx.x; e < RP * RP; e += NT) out[e] = mm[(e / RP) * LM + e % RP];
 }
@@ -581,6 +659,17 @@ int64_t tiles_of(int64_t n) { return ceil_div(n, Tile<RP>::JT); }
 int tiles_per_block(int64_t tiles) {
     const int64_t want = tiles / (int64_t(num_sms()) * 8);
     return int(std::min<int64_t>(8, std::max<int64_t>(1, want)));
+}
+
+// CTAs that hold a matrix of a cluster launch of n matrices: all eight while that leaves SMs
+// free, for the shortest time; else as few as its columns fit, for the least work on the r x r
+// products.
+template <int RP>
+int ctas_of(int64_t len, int n) {
+    int c = kCluster;
+    if (int64_t(n) * kCluster > 2 * num_sms())
+        while (c > 1 && len <= int64_t(c / 2) * Tile<RP>::JT) c /= 2;
+    return c;
 }
 
 // Workspace floats of a group of matrices (the passes'): Y, the partial Gram matrices (as many
@@ -600,16 +689,19 @@ int pass(const Params &p, unsigned blocks, cudaStream_t st) {
     constexpr int smem = pass_floats<RP>() * 4;
     auto k = muon_pass_kernel<RP, SOURCE, SINK>;
     TLB_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    k<<<blocks, kPassThreads, smem, st>>>(p);
+    k<<<blocks, NT, smem, st>>>(p);
     return check_launch("muon_pass");
 }
 
 template <int RP>
-int group(const tlb_muon_mat *mats, const int *idx, int n, bool clusters, const tlb_muon_cfg &cfg, float *ws, cudaStream_t st) {
+int group(const tlb_muon_mat *mats, int *idx, int n, bool clusters, const tlb_muon_cfg &cfg, float *ws, cudaStream_t st) {
     Params p;
     memset(&p, 0, sizeof(p));
     int64_t tiles = 0, off = 0, blocks = 0;
     for (int k = 0; k < n; ++k) tiles += tiles_of<RP>(std::max(mats[idx[k]].rows, mats[idx[k]].cols));
+    auto len_of = [&](int i) { return int64_t(std::max(mats[i].rows, mats[i].cols)); };
+    if (clusters)                                            // longest first; a stable order
+        std::sort(idx, idx + n, [&](int x, int y) { return len_of(x) != len_of(y) ? len_of(x) > len_of(y) : x < y; });
     p.tiles_per_block = tiles_per_block(tiles);
     p.nmat = n;
     p.ws = ws;
@@ -633,8 +725,12 @@ int group(const tlb_muon_mat *mats, const int *idx, int n, bool clusters, const 
         a.vec = aligned16(s.p) && aligned16(s.g) && aligned16(s.m) && (a.tall ? a.r : a.n) % 4 == 0;
         a.lr = float(cfg.lr * double(s.lr_mult));
         a.lr_scale = float(cfg.lr * double(s.lr_mult) * double(s.scale));
+        a.ctas = clusters ? ctas_of<RP>(a.n, n) : int(ceil_div(tiles_of<RP>(a.n), p.tiles_per_block));
+        // matrices of one number of CTAs stand together, so they fill clusters; the first of
+        // another number begins a cluster
+        if (clusters && k > 0 && a.ctas != p.mat[k - 1].ctas) blocks = ceil_div(blocks, kCluster) * kCluster;
         a.block0 = int(blocks);
-        blocks += ceil_div(tiles_of<RP>(a.n), p.tiles_per_block);
+        blocks += a.ctas;
         a.y = off;
         off += tiles_of<RP>(a.n) * RP * Tile<RP>::JT;
         a.part = off;
@@ -646,8 +742,8 @@ int group(const tlb_muon_mat *mats, const int *idx, int n, bool clusters, const 
         auto k = muon_cluster_kernel<RP>;
         TLB_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
         cudaLaunchConfig_t lc = {};
-        lc.gridDim = dim3(unsigned(n * kCluster));
-        lc.blockDim = dim3(kClusterThreads);
+        lc.gridDim = dim3(unsigned(ceil_div(blocks, kCluster) * kCluster));
+        lc.blockDim = dim3(NT);
         lc.dynamicSmemBytes = smem;
         lc.stream = st;
         cudaLaunchAttribute attr[1];
@@ -666,7 +762,7 @@ int group(const tlb_muon_mat *mats, const int *idx, int n, bool clusters, const 
     for (int done = 0; done < cfg.steps;) {
         const bool first = done == 0;
         const int steps = std::min(first ? kFirstRun : kRun, cfg.steps - done);
-        muon_poly_kernel<RP><<<unsigned(n), kPolyThreads, poly_smem, st>>>(p, done, steps);
+        muon_poly_kernel<RP><<<unsigned(n), NT, poly_smem, st>>>(p, done, steps);
         TLB_TRY(check_launch("muon_poly"));
         done += steps;
         const bool last = done == cfg.steps;
@@ -772,7 +868,7 @@ int tlb_muon(const tlb_muon_mat *mats, int32_t n, const tlb_muon_cfg *cfg, void 
                 "muon: needs a 256-byte aligned workspace of %zu bytes", kStatusBytes + f * 4);
     float *w = ws_at<float>(ws, kStatusBytes);
     cudaStream_t st = as_stream(stream);
-    return for_groups(mats, n, [&](int rp, bool clusters, const int *idx, int k) {
+    return for_groups(mats, n, [&](int rp, bool clusters, int *idx, int k) {
         return by_class(rp, [&] { return group<8>(mats, idx, k, clusters, *cfg, w, st); },
                         [&] { return group<16>(mats, idx, k, clusters, *cfg, w, st); },
                         [&] { return group<32>(mats, idx, k, clusters, *cfg, w, st); },
