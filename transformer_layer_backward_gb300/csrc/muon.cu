@@ -40,7 +40,7 @@ namespace {
 
 constexpr int kMaxMats = 256;            // matrices of one launch (their table is a kernel parameter)
 constexpr int kFirstRun = 2, kRun = 3;    // steps from the first and from each later Gram matrix
-constexpr int kCluster = 8;              // CTAs of a cluster; 1, 2, 4 or 8 of them hold one matrix
+constexpr int kCluster = 8;              // CTAs of a cluster; one to all of them hold one matrix
 constexpr int NT = 256;                  // threads of every kernel
 
 struct Mat {
@@ -72,20 +72,33 @@ enum Sink { kGram = 0, kGramY = 1, kParam = 2 };      // Gram matrix; X to Y and
 // A tile of up to JT columns of X [r, n], in shared memory as [RP][LD]: 33 to 66 KB.  LD = JT + 4: the same column of eight neighbouring rows lies in eight different
 // groups of four banks.
 template <int RP> struct Tile {
-    static constexpr int JT = RP == 8 ? 1024 : RP == 16 ? 640 : RP == 32 ? 512 : 256;
+    static constexpr int JT = RP == 8 ? 1024 : RP == 16 ? 704 : RP == 32 ? 512 : 256;
     static constexpr int LD = JT + 4, XF = RP * LD;
     static constexpr int LM = RP + 4;                       // row length of an r x r matrix in shared memory
     // Gram blocks of B x B a thread (row k of block b is b + NB k); the upper PAIRS of them
     static constexpr int B = RP == 64 ? 8 : 4, NB = RP / B, PAIRS = NB * (NB + 1) / 2;
     static constexpr int GSIZE = PAIRS * B * B;             // floats of a Gram matrix's upper blocks
 };
-// The threads form a Gram matrix in GROUPS groups, each with every GROUPS-th column quad.  Where
-// the tile has to stay, RG of them at a time meet in a buffer of at most 9 KB.
+// The threads form a Gram matrix in GROUPS groups, each with every GROUPS-th column quad.  A
+// warp holds GW whole groups, which it adds up itself, for r <= 16; groups of 36 pairs run
+// across warps.  PARTS shares then meet in shared memory.
 template <int RP> struct Gram {
-    static constexpr int G0 = NT / Tile<RP>::PAIRS, GROUPS = G0 > 32 ? 32 : G0;
-    static constexpr int R0 = 9216 / (Tile<RP>::GSIZE * 4), RG = R0 < 1 ? 1 : R0 > GROUPS ? GROUPS : R0;
-    static constexpr int RF = RG * Tile<RP>::GSIZE;         // floats of the buffer
+    static constexpr int GW = RP == 8 ? 8 : RP == 16 ? 3 : 0;
+    static constexpr int GROUPS = GW ? GW * (NT / 32) : NT / Tile<RP>::PAIRS, PARTS = GW ? NT / 32 : GROUPS;
+    static constexpr int RF = PARTS * Tile<RP>::GSIZE;      // floats where they meet
     static constexpr int OWN = (Tile<RP>::GSIZE + NT - 1) / NT;
+    // this thread's group (GROUPS: none) and pair
+    __device__ static void mine(int &grp, int &pair) {
+        constexpr int PAIRS = Tile<RP>::PAIRS;
+        if constexpr (GW > 0) {
+            const int lane = threadIdx.x & 31, g = lane / PAIRS;
+            grp = g < GW ? int(threadIdx.x >> 5) * GW + g : GROUPS;
+            pair = lane % PAIRS;
+        } else {
+            grp = min(int(threadIdx.x) / PAIRS, GROUPS);
+            pair = threadIdx.x % PAIRS;
+        }
+    }
 };
 
 // Row block and column block of upper pair `q` of an NB x NB grid.
@@ -292,12 +305,12 @@ template <int RP>
 __device__ __forceinline__ void gram_tile(const float *x, int jn, float (&acc)[Tile<RP>::B][Tile<RP>::B]) {
     using T = Tile<RP>;
     constexpr int B = T::B, NB = T::NB, LD = T::LD;
-    const int grp = threadIdx.x / T::PAIRS;
+    int grp, pair, bi, bk;
+    Gram<RP>::mine(grp, pair);
 #pragma unroll
     for (int k = 0; k < B * B; ++k) acc[k / B][k % B] = 0.f;
     if (grp >= Gram<RP>::GROUPS) return;
-    int bi, bk;
-    pair_of<NB>(threadIdx.x % T::PAIRS, bi, bk);
+    pair_of<NB>(pair, bi, bk);
     const int quads = (jn + 3) / 4;
 #pragma unroll 1
     for (int q = grp; q < quads; q += Gram<RP>::GROUPS) {
@@ -314,28 +327,41 @@ __device__ __forceinline__ void gram_tile(const float *x, int jn, float (&acc)[T
     }
 }
 
-// The groups' shares added up in group order, RG at a time through red (RG GSIZE floats), onto
-// s: this thread's elements threadIdx.x + o NT of the order [B * B][pair].
-template <int RP, int RG>
-__device__ __forceinline__ void gram_sum(const float (&acc)[Tile<RP>::B][Tile<RP>::B], float *red, float (&s)[Gram<RP>::OWN]) {
+// The groups' shares added up in a fixed order, through red (RF floats), onto s: this thread's
+// elements threadIdx.x + o NT of the order [B * B][pair].
+template <int RP>
+__device__ __forceinline__ void gram_sum(float (&acc)[Tile<RP>::B][Tile<RP>::B], float *red, float (&s)[Gram<RP>::OWN]) {
     using T = Tile<RP>;
     using G = Gram<RP>;
     constexpr int B = T::B;
-    const int grp = threadIdx.x / T::PAIRS, pair = threadIdx.x % T::PAIRS;
-#pragma unroll 1
-    for (int g0 = 0; g0 < G::GROUPS; g0 += RG) {
-        __syncthreads();
-        if (grp >= g0 && grp < g0 + RG && grp < G::GROUPS) {
+    int grp, pair;
+    G::mine(grp, pair);
+    const int part = G::GW ? int(threadIdx.x >> 5) : grp;
+    if constexpr (G::GW == 3) {
 #pragma unroll
-            for (int k = 0; k < B * B; ++k) red[(grp - g0) * T::GSIZE + k * T::PAIRS + pair] = acc[k / B][k % B];
+        for (int k = 0; k < B * B; ++k) {
+            const float v = acc[k / B][k % B];
+            acc[k / B][k % B] = v + __shfl_down_sync(0xffffffffu, v, T::PAIRS) + __shfl_down_sync(0xffffffffu, v, 2 * T::PAIRS);
         }
-        __syncthreads();
-        const int n = min(RG, G::GROUPS - g0);
+    } else if constexpr (G::GW == 8) {
 #pragma unroll
-        for (int o = 0; o < G::OWN; ++o) {
-            const int e = threadIdx.x + o * NT;
-            if (e < T::GSIZE)
-                for (int k = 0; k < n; ++k) s[o] += red[k * T::GSIZE + e];
+        for (int o = 4; o > 0; o /= 2)
+#pragma unroll
+            for (int k = 0; k < B * B; ++k)
+                acc[k / B][k % B] += __shfl_down_sync(0xffffffffu, acc[k / B][k % B], o * T::PAIRS);
+    }
+    __syncthreads();
+    if (G::GW ? int(threadIdx.x & 31) < T::PAIRS : grp < G::GROUPS) {
+#pragma unroll
+        for (int k = 0; k < B * B; ++k) red[part * T::GSIZE + k * T::PAIRS + pair] = acc[k / B][k % B];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int o = 0; o < G::OWN; ++o) {
+        const int e = threadIdx.x + o * NT;
+        if (e < T::GSIZE) {
+#pragma unroll
+            for (int k = 0; k < G::PARTS; ++k) s[o] += red[k * T::GSIZE + e];
         }
     }
 }
@@ -363,14 +389,14 @@ __device__ __forceinline__ void gram_place(int e, int &i, int &k) {
 // (symmetric; changed); sq, pm: scratch; all [RP][LM].  G and P are kept symmetric (the upper
 // triangle, mirrored), so that a row stands for a column.  r <= 16: one warp, without block
 // barriers, while the others wait; else all threads.
-template <int RP>
+template <int RP, int PT = NT>
 __device__ __forceinline__ void polynomial(float *gm, float *sq, float *pm, float *mm, int steps, float a, float b, float c,
                                            float scale) {
     constexpr int LM = Tile<RP>::LM;
     constexpr bool WARP = RP <= 16;
     // a thread's DR x DC elements
-    constexpr int DC = RP == 64 ? 4 : RP == 8 ? 1 : 2, DR = RP == 64 || RP == 16 ? 4 : 2, W = RP / DC;
-    static_assert(W * (RP / DR) <= (WARP ? 32 : NT), "threads of a product");
+    constexpr int DC = RP == 64 ? 1024 / PT : RP == 8 ? 1 : 2, DR = RP == 64 || RP == 16 ? 4 : 2, W = RP / DC;
+    static_assert(W * (RP / DR) <= (WARP ? 32 : PT), "threads of a product");
     const int tid = threadIdx.x, r0 = (tid / W) * DR, c0 = (tid % W) * DC;
     const bool on = r0 < RP;
     auto sync = [] {
@@ -463,7 +489,7 @@ __device__ __forceinline__ void polynomial(float *gm, float *sq, float *pm, floa
 
 // 1 / (|u|_F + eps) from the Gram matrix of u, which becomes that of X0.  A zero update stays
 // zero, also for eps = 0.
-template <int RP>
+template <int RP, int PT = NT>
 __device__ __forceinline__ float normalise(float *gm, float *s_inv, float eps) {
     constexpr int LM = Tile<RP>::LM;
     if (threadIdx.x < 32) {
@@ -474,7 +500,7 @@ __device__ __forceinline__ float normalise(float *gm, float *s_inv, float eps) {
     }
     __syncthreads();
     const float inv = *s_inv;
-    for (int e = threadIdx.x; e < RP * RP; e += NT) gm[(e / RP) * LM + e % RP] *= inv * inv;
+    for (int e = threadIdx.x; e < RP * RP; e += PT) gm[(e / RP) * LM + e % RP] *= inv * inv;
     __syncthreads();
     return inv;
 }
@@ -490,9 +516,10 @@ __device__ __forceinline__ float ld_cluster(const float *p, int rank) {
 // The whole step of a matrix whose X fits the shared memory of a.ctas CTAs of a cluster: CTA c
 // of them holds columns [c w, (c + 1) w).  X never leaves the SMs: 20 bytes an element cross,
 // as they must.  Gram matrices are summed through distributed shared memory, by every CTA in
-// rank order, and every CTA forms the r x r products for itself.  A cluster holds 8 / a.ctas
-// matrices, which all meet at its barriers; CTAs left over (block0 is a multiple of 8 where
-// a.ctas changes) only do that.
+// rank order, and every CTA forms the r x r products for itself.  Several matrices share a
+// cluster and meet at its barriers; CTAs left over in it only do that.  r <= 16: 57 KB and 64
+// registers, four CTAs an SM, so that the 576 CTAs of a 36-layer stack's rank-16 adapters run
+// at once.
 template <int RP> constexpr int cluster_floats() {
     return Tile<RP>::XF + Gram<RP>::RF + 2 * Tile<RP>::GSIZE + 4 * RP * Tile<RP>::LM;
 }
@@ -529,7 +556,7 @@ __global__ void __launch_bounds__(NT, RP <= 16 ? 4 : 1) muon_cluster_kernel(cons
         {
             float acc[B][B], s[Gram<RP>::OWN] = {};
             gram_tile<RP>(x, jn, acc);
-            gram_sum<RP, Gram<RP>::RG>(acc, red, s);
+            gram_sum<RP>(acc, red, s);
             gram_keep<RP>(s, mine);
         }
         cluster_sync();
@@ -559,7 +586,7 @@ __global__ void __launch_bounds__(NT, RP <= 16 ? 4 : 1) muon_cluster_kernel(cons
 // ---------------------------------------------------------------- passes over longer matrices
 
 template <int RP> constexpr int pass_floats() {
-    static_assert(Gram<RP>::GROUPS * Tile<RP>::GSIZE <= Tile<RP>::XF, "the groups meet in the tile's place");
+    static_assert(Gram<RP>::RF <= Tile<RP>::XF, "the groups meet in the tile's place");
     return Tile<RP>::XF + RP * Tile<RP>::LM;
 }
 
@@ -609,24 +636,26 @@ __global__ void __launch_bounds__(NT, RP == 64 ? 2 : 1) muon_pass_kernel(const _
             }
             float acc[B][B];
             gram_tile<RP>(x, jn, acc);
-            gram_sum<RP, Gram<RP>::GROUPS>(acc, x, s);       // the tile is used up
+            gram_sum<RP>(acc, x, s);       // the tile is used up
         }
     }
     if constexpr (SINK != kParam) gram_keep<RP>(s, p.ws + a.part + int64_t(bl) * T::GSIZE);
 }
 
 // One matrix a block: G from its partial sums in block order, then M.
+template <int RP> constexpr int kPolyThreads = RP == 64 ? 512 : NT;   // 8 of 64 x 64 elements a thread: the products
+                                                                    // are bound by latency
 template <int RP>
-__global__ void __launch_bounds__(NT) muon_poly_kernel(const __grid_constant__ Params p, int done, int steps) {
+__global__ void __launch_bounds__(kPolyThreads<RP>) muon_poly_kernel(const __grid_constant__ Params p, int done, int steps) {
     using T = Tile<RP>;
-    constexpr int LM = T::LM;
+    constexpr int LM = T::LM, PT = kPolyThreads<RP>;
     extern __shared__ __align__(16) float sh[];
     float *gm = sh, *sq = gm + RP * LM, *pm = sq + RP * LM, *mm = pm + RP * LM;
     __shared__ float s_inv;
     const Mat &a = p.mat[blockIdx.x];
     const float *part = p.ws + a.part;
     const int nb = a.ctas;
-    for (int e = threadIdx.x; e < T::GSIZE; e += NT) {
+    for (int e = threadIdx.x; e < T::GSIZE; e += PT) {
         float s = 0.f;
         for (int k = 0; k < nb; k += 8) {
             float v[8];
@@ -641,10 +670,10 @@ __global__ void __launch_bounds__(NT) muon_poly_kernel(const __grid_constant__ P
         gm[k * LM + i] = s;
     }
     __syncthreads();
-    const float scale = done == 0 ? normalise<RP>(gm, &s_inv, p.eps) : 1.f;
-    polynomial<RP>(gm, sq, pm, mm, steps, p.a, p.b, p.c, scale);
+    const float scale = done == 0 ? normalise<RP, PT>(gm, &s_inv, p.eps) : 1.f;
+    polynomial<RP, PT>(gm, sq, pm, mm, steps, p.a, p.b, p.c, scale);
     float *out = p.ws + p.mpoly + int64_t(blockIdx.x) * RP * RP;
-    for (int e = threadIdx.x; e < RP * RP; e += NT) out[e] = mm[(e / RP) * LM + e % RP];
+    for (int e = threadIdx.x; e < RP * RP; e += PT) out[e] = mm[(e / RP) * LM + e % RP];
 }
 
 // ---------------------------------------------------------------- host side
@@ -661,15 +690,36 @@ int tiles_per_block(int64_t tiles) {
     return int(std::min<int64_t>(8, std::max<int64_t>(1, want)));
 }
 
-// CTAs that hold a matrix of a cluster launch of n matrices: all eight while that leaves SMs
-// free, for the shortest time; else as few as its columns fit, for the least work on the r x r
-// products.
+// Puts the matrices `idx` into clusters: ctas[k], block0[k] for idx[k], which is sorted by
+// block0.  All eight CTAs for a matrix while that leaves SMs free, for the shortest time; else
+// as few as its columns fit, for the least work on the r x r products, the largest first, each
+// into the first cluster with room.  Returns the CTAs in all.
 template <int RP>
-int ctas_of(int64_t len, int n) {
-    int c = kCluster;
-    if (int64_t(n) * kCluster > 2 * num_sms())
-        while (c > 1 && len <= int64_t(c / 2) * Tile<RP>::JT) c /= 2;
-    return c;
+int place(const tlb_muon_mat *mats, int *idx, int n, int32_t *ctas, int32_t *block0) {
+    auto need = [&](int i) { return int(ceil_div(std::max(mats[i].rows, mats[i].cols), Tile<RP>::JT)); };
+    const bool all = int64_t(n) * kCluster <= 2 * num_sms();
+    std::sort(idx, idx + n, [&](int x, int y) { return need(x) != need(y) ? need(x) > need(y) : x < y; });
+    int used[kMaxMats], clusters = 0, order[kMaxMats];
+    int32_t at[kMaxMats], size[kMaxMats];
+    for (int k = 0; k < n; ++k) {
+        const int c = all ? kCluster : need(idx[k]);
+        int j = 0;
+        while (j < clusters && used[j] + c > kCluster) ++j;
+        if (j == clusters) used[clusters++] = 0;
+        at[k] = j * kCluster + used[j];
+        size[k] = c;
+        used[j] += c;
+        order[k] = k;
+    }
+    std::sort(order, order + n, [&](int x, int y) { return at[x] < at[y]; });
+    int sorted[kMaxMats];
+    for (int k = 0; k < n; ++k) {
+        sorted[k] = idx[order[k]];
+        ctas[k] = size[order[k]];
+        block0[k] = at[order[k]];
+    }
+    std::copy(sorted, sorted + n, idx);
+    return clusters * kCluster;
 }
 
 // Workspace floats of a group of matrices (the passes'): Y, the partial Gram matrices (as many
@@ -699,9 +749,8 @@ int group(const tlb_muon_mat *mats, int *idx, int n, bool clusters, const tlb_mu
     memset(&p, 0, sizeof(p));
     int64_t tiles = 0, off = 0, blocks = 0;
     for (int k = 0; k < n; ++k) tiles += tiles_of<RP>(std::max(mats[idx[k]].rows, mats[idx[k]].cols));
-    auto len_of = [&](int i) { return int64_t(std::max(mats[i].rows, mats[i].cols)); };
-    if (clusters)                                            // longest first; a stable order
-        std::sort(idx, idx + n, [&](int x, int y) { return len_of(x) != len_of(y) ? len_of(x) > len_of(y) : x < y; });
+    int32_t ctas[kMaxMats], block0[kMaxMats];
+    if (clusters) blocks = place<RP>(mats, idx, n, ctas, block0);
     p.tiles_per_block = tiles_per_block(tiles);
     p.nmat = n;
     p.ws = ws;
@@ -725,12 +774,14 @@ int group(const tlb_muon_mat *mats, int *idx, int n, bool clusters, const tlb_mu
         a.vec = aligned16(s.p) && aligned16(s.g) && aligned16(s.m) && (a.tall ? a.r : a.n) % 4 == 0;
         a.lr = float(cfg.lr * double(s.lr_mult));
         a.lr_scale = float(cfg.lr * double(s.lr_mult) * double(s.scale));
-        a.ctas = clusters ? ctas_of<RP>(a.n, n) : int(ceil_div(tiles_of<RP>(a.n), p.tiles_per_block));
-        // matrices of one number of CTAs stand together, so they fill clusters; the first of
-        // another number begins a cluster
-        if (clusters && k > 0 && a.ctas != p.mat[k - 1].ctas) blocks = ceil_div(blocks, kCluster) * kCluster;
-        a.block0 = int(blocks);
-        blocks += a.ctas;
+        if (clusters) {
+            a.ctas = ctas[k];
+            a.block0 = block0[k];
+        } else {
+            a.ctas = int(ceil_div(tiles_of<RP>(a.n), p.tiles_per_block));
+            a.block0 = int(blocks);
+            blocks += a.ctas;
+        }
         a.y = off;
         off += tiles_of<RP>(a.n) * RP * Tile<RP>::JT;
         a.part = off;
@@ -742,7 +793,7 @@ int group(const tlb_muon_mat *mats, int *idx, int n, bool clusters, const tlb_mu
         auto k = muon_cluster_kernel<RP>;
         TLB_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
         cudaLaunchConfig_t lc = {};
-        lc.gridDim = dim3(unsigned(ceil_div(blocks, kCluster) * kCluster));
+        lc.gridDim = dim3(unsigned(blocks));
         lc.blockDim = dim3(NT);
         lc.dynamicSmemBytes = smem;
         lc.stream = st;
@@ -762,7 +813,7 @@ int group(const tlb_muon_mat *mats, int *idx, int n, bool clusters, const tlb_mu
     for (int done = 0; done < cfg.steps;) {
         const bool first = done == 0;
         const int steps = std::min(first ? kFirstRun : kRun, cfg.steps - done);
-        muon_poly_kernel<RP><<<unsigned(n), NT, poly_smem, st>>>(p, done, steps);
+        muon_poly_kernel<RP><<<unsigned(n), kPolyThreads<RP>, poly_smem, st>>>(p, done, steps);
         TLB_TRY(check_launch("muon_poly"));
         done += steps;
         const bool last = done == cfg.steps;
