@@ -26,7 +26,8 @@
 // The tensor core cuts its fp32 sum after every MMA of 16 products (measured: a sum of 160
 // MMAs comes out about 1.2e-6 of its size short, one of 6144 3e-5).  Results of float32
 // precision are therefore summed in chunks of a few k blocks, which the epilogue adds up in
-// registers, and the smaller term products come first, while the sum is small.
+// registers.  The term products of a k block follow one another, so that its operand tiles
+// come from memory once and from L2 then.
 //
 // Bounds: N >= 512 rows is bound by the tensor pipe (2 N V D flops a product), few rows by
 // the read of W.
@@ -51,7 +52,7 @@ constexpr int kMaxTerms = 3, kMaxProd = 6;
 // k blocks (4 MMAs each) of one tensor-memory sum of a float32 result.  Reading a sum out takes
 // the tensor pipe about 300 cycles, and its error grows with its length: the loss of 2048 x
 // 2560 x 131072 is 3.7e-7 off at 8 k blocks (812 us), 9e-7 at 20 (787 us).
-constexpr int kChunkLoss = 14, kChunkGrad = 10;
+constexpr int kChunkLoss = 14, kChunkTerms = 8, kChunkGrad = 10;   // loss of bf16, of float32 terms; gradient
 constexpr int kGroupM = 16;                 // row tiles that share a column tile before the next one
 constexpr int kBox = 4096;                  // bytes of a 32 x 64 bf16 box of dz
 constexpr float kLog2e = 1.4426950408889634f;
@@ -187,8 +188,8 @@ __device__ __forceinline__ GradRow grad_row(const XParams &p, int row) {
     return r;
 }
 
-// kGrad: dz of this warp's 32 rows row0.. and columns col0 .. col0 + 63, from z in y: one
-// 4 KB box of each term through the warp's shared buffer and out by TMA, which leaves out
+// kGrad: dz of this warp's 32 rows row0.. and columns col0 .. col0 + 63, from z in y: term by
+// term through the warp's 4 KB box and out by TMA, which leaves out
 // what lies past the last row or column.
 template <int TERMS>
 __device__ __forceinline__ void grad_box(const XParams &p, const GradRow &r, float *y, int row0, int col0, uint8_t *box,
@@ -203,10 +204,10 @@ __device__ __forceinline__ void grad_box(const XParams &p, const GradRow &r, flo
     }
 #pragma unroll
     for (int c = 0; c < 64; ++c) y[c] = r.has ? y[c] * r.g : 0.f;
-    if (lane == 0) bulk_wait_read();                       // the box's last store has read it
-    __syncwarp();
 #pragma unroll
     for (int k = 0; k < TERMS; ++k) {
+        if (lane == 0) bulk_wait_read();                   // the box's last store has read it
+        __syncwarp();
 #pragma unroll
         for (int c = 0; c < 8; ++c) {
             uint4 w;
@@ -215,20 +216,24 @@ __device__ __forceinline__ void grad_box(const XParams &p, const GradRow &r, flo
                 const uint2 hi = pack_bf16x4(y[8 * c + 4], y[8 * c + 5], y[8 * c + 6], y[8 * c + 7]);
                 w = make_uint4(lo.x, lo.y, hi.x, hi.y);
             } else {
+                // the 8 highest significant bits, cut; what is left goes on to the next term
                 uint32_t u[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) u[i] = next_term(y[8 * c + i]);
-                w = make_uint4(u[0] | (u[1] << 16), u[2] | (u[3] << 16), u[4] | (u[5] << 16), u[6] | (u[7] << 16));
+                for (int i = 0; i < 8; ++i) {
+                    u[i] = __float_as_uint(y[8 * c + i]);
+                    y[8 * c + i] -= __uint_as_float(u[i] & 0xFFFF0000u);
+                }
+                w = make_uint4(__byte_perm(u[0], u[1], 0x7632), __byte_perm(u[2], u[3], 0x7632),
+                               __byte_perm(u[4], u[5], 0x7632), __byte_perm(u[6], u[7], 0x7632));
             }
-            *reinterpret_cast<uint4 *>(box + k * kBox + lane * 128 + ((c ^ (lane & 7)) << 4)) = w;
+            *reinterpret_cast<uint4 *>(box + lane * 128 + ((c ^ (lane & 7)) << 4)) = w;
         }
-    }
-    fence_proxy_async();
-    __syncwarp();
-    if (lane == 0) {
-#pragma unroll
-        for (int k = 0; k < TERMS; ++k) tma_store_2d(&p.d[k], box + k * kBox, col0, row0);
-        bulk_commit();
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+            tma_store_2d(&p.d[k], box, col0, row0);
+            bulk_commit();
+        }
     }
 }
 
@@ -288,16 +293,15 @@ struct Shape {
     static constexpr int BH = PAIR ? BN / 2 : BN;            // columns' operand rows that a CTA stages
     static constexpr int A_BYTES = kBM * kBK * 2, B_BYTES = BH * kBK * 2, STAGE = A_BYTES + B_BYTES;
 };
-// Ring depth: what shared memory leaves beside the epilogue's buffers (8 x 12 KB boxes for
-// three dz terms, 8 x 4 KB for one, 8 x 4.2 KB for the turn of kOut, none for kStats).
-template <int BN, bool PAIR, int MODE>
-constexpr int epi_bytes(int terms) {
-    return MODE == kStats ? 0 : MODE == kGrad ? kEpiWarps * kBox * terms : kEpiWarps * 32 * 33 * 4;
+// Ring depth: what shared memory leaves beside the epilogue's buffers (8 x 4 KB boxes of dz, 8 x
+// 4.2 KB for the turn of kOut, none for kStats).
+template <int MODE>
+constexpr int epi_bytes() {
+    return MODE == kStats ? 0 : MODE == kGrad ? kEpiWarps * kBox : kEpiWarps * 32 * 33 * 4;
 }
-template <int BN, bool PAIR, int MODE, int TERMS>
+template <int BN, bool PAIR, int MODE>
 constexpr int stages_of() {
-    const int room = 226 * 1024 - 1024 - epi_bytes<BN, PAIR, MODE>(TERMS);
-    const int n = room / Shape<BN, PAIR>::STAGE;
+    const int n = (226 * 1024 - 1024 - epi_bytes<MODE>()) / Shape<BN, PAIR>::STAGE;
     return n > 6 ? 6 : n;
 }
 
@@ -305,7 +309,7 @@ constexpr int stages_of() {
 template <int BN, bool PAIR, int MODE, int TERMS, bool FINE, bool A_MN, bool B_MN>
 __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_constant__ XParams p) {
     using S = Shape<BN, PAIR>;
-    constexpr int kStages = stages_of<BN, PAIR, MODE, TERMS>();
+    constexpr int kStages = stages_of<BN, PAIR, MODE>();
     constexpr int TM = S::TM, BH = S::BH, A_BYTES = S::A_BYTES, STAGE = S::STAGE;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -319,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
 
     // this unit's segments: its whole tiles, then its share of the split tiles, cut at tiles
     const int KB = p.nprod * p.kb;
-    const int chunk = !FINE ? KB : MODE == kStats ? kChunkLoss : kChunkGrad;                    // k blocks of one accumulator
+    const int chunk = !FINE ? KB : MODE != kStats ? kChunkGrad : p.nprod > 1 ? kChunkTerms : kChunkLoss;                    // k blocks of one accumulator
     const int64_t nwhole = p.whole > unit ? (p.whole - unit + p.units - 1) / p.units : 0;
     const bool splits = MODE == kOut && p.sk_work > 0 && unit < p.sk_units;
     const int64_t b0 = splits ? sk_start(p.sk_work, p.sk_units, unit) : 0;
@@ -394,7 +398,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
                         ok = false;
                         break;
                     }
-                    const int prod = kb / p.kb, k0 = (kb - prod * p.kb) * kBK;
+                    const int kq = kb / p.nprod, prod = kb - kq * p.nprod, k0 = kq * kBK;
                     const CUtensorMap *ma = &p.a[p.pa[prod]], *mb = &p.b[p.pb[prod]];
                     uint8_t *sa = smem + s * STAGE, *sb = sa + A_BYTES;
                     const int nb = sg.n0 + rank * BH;
@@ -488,7 +492,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
         // is read a block at a time.
         constexpr int WN = MODE == kGrad ? 64 : 32, ZN = FINE ? BN / 2 : WN;
         uint8_t *buf = smem + kStages * STAGE;
-        uint8_t *box = buf + (warp - 2) * (kBox * TERMS);                              // kGrad
+        uint8_t *box = buf + (warp - 2) * kBox;                                        // kGrad
         float *blk = reinterpret_cast<float *>(buf) + (warp - 2) * 32 * 33;            // kOut
         int f = 0;
         bool ok = true;
@@ -670,23 +674,26 @@ template <typename SRC>
 __global__ void __launch_bounds__(256) xent_pack_kernel(const SRC *__restrict__ x, int64_t rows, int cols, int ld, int terms,
                                                         const int64_t *__restrict__ targets, int64_t vocab,
                                                         __nv_bfloat16 *__restrict__ y) {
-    const int64_t quads = ld / 4, n = rows * quads, plane = rows * int64_t(ld);
+    const int64_t n = rows * (ld / 8), plane = rows * int64_t(ld);
+    const uint32_t per = uint32_t(ld / 8);
     for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += int64_t(gridDim.x) * blockDim.x) {
-        const int64_t r = i / quads;
-        const int c = int(i - r * quads) * 4;
+        const int64_t r = n >> 32 ? i / per : int64_t(uint32_t(i) / per);
+        const int c = int(i - r * per) * 8;
         bool on = true;
         if (targets != nullptr) {
             const int64_t t = targets[r];
             on = t >= 0 && t < vocab;
         }
-        float v[4];
+        const SRC *src = x + r * cols + c;
+        float v[8];
 #pragma unroll
-        for (int k = 0; k < 4; ++k) v[k] = on && c + k < cols ? float(x[r * cols + c + k]) : 0.f;
+        for (int k = 0; k < 8; ++k) v[k] = on && c + k < cols ? float(src[k]) : 0.f;
         for (int t = 0; t < terms; ++t) {
-            uint32_t w[4];
+            uint32_t w[8];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) w[k] = next_term(v[k]);
-            *reinterpret_cast<uint2 *>(y + t * plane + r * ld + c) = make_uint2(w[0] | (w[1] << 16), w[2] | (w[3] << 16));
+            for (int k = 0; k < 8; ++k) w[k] = next_term(v[k]);
+            *reinterpret_cast<uint4 *>(y + t * plane + r * ld + c) =
+                make_uint4(w[0] | (w[1] << 16), w[2] | (w[3] << 16), w[4] | (w[5] << 16), w[6] | (w[7] << 16));
         }
     }
 }
@@ -719,8 +726,8 @@ struct Mat {
 template <int BN, bool PAIR, int MODE, int TERMS, bool FINE, bool A_MN, bool B_MN>
 int launch(XParams &p, const Mat &a, const Mat &b, cudaStream_t st) {
     using S = Shape<BN, PAIR>;
-    constexpr int stages = stages_of<BN, PAIR, MODE, TERMS>();
-    constexpr int smem = stages * S::STAGE + epi_bytes<BN, PAIR, MODE>(TERMS) + 1024;
+    constexpr int stages = stages_of<BN, PAIR, MODE>();
+    constexpr int smem = stages * S::STAGE + epi_bytes<MODE>() + 1024;
     static_assert(stages >= 3 && smem <= 227 * 1024 - 512, "shared memory of one CTA");
     for (int t = 0; t < a.terms; ++t)
         TLB_TRY(make_map(&p.a[t], a.p + t * a.plane, a.rows, a.cols, a.ld, A_MN ? kBK : kBM));
@@ -782,14 +789,13 @@ int launch(XParams &p, const Mat &a, const Mat &b, cudaStream_t st) {
 
 // Tile form.  More than 128 rows: CTA pairs on 256 x 256 tiles.  Up to 128 rows there is one
 // row tile, and 128 columns a tile even out the few tiles over the SMs better than 256 when
-// their last wave is fuller; the boxes of three dz terms leave room for 128 columns only.
+// their last wave is fuller.
 template <int MODE, int TERMS>
 int launch_z(XParams &p, const Mat &h, const Mat &w, cudaStream_t st) {
     constexpr bool fine = MODE == kStats || TERMS > 1;       // the loss is float32 whatever the operands
     if (p.M > kBM) return launch<256, true, MODE, TERMS, fine, false, false>(p, h, w, st);
     const int64_t n = num_sms(), t256 = ceil_div(p.N, 256), t128 = ceil_div(p.N, 128);
-    if constexpr (TERMS == 1)
-        if (2 * ceil_div(t256, n) <= ceil_div(t128, n)) return launch<256, false, MODE, TERMS, fine, false, false>(p, h, w, st);
+    if (2 * ceil_div(t256, n) <= ceil_div(t128, n)) return launch<256, false, MODE, TERMS, fine, false, false>(p, h, w, st);
     return launch<128, false, MODE, TERMS, fine, false, false>(p, h, w, st);
 }
 
@@ -832,8 +838,8 @@ Plan plan_of(int htype, int wtype, int64_t N, int64_t V, int64_t D, bool grad, b
     q.part = q.zt = q.dz = q.acc = q.partial = 0;
     if (!grad) {
         q.part_ld = ceil_div(std::min(N, kRowChunk), 32) * 32;
-        // 128-wide tiles: the most slots; a slot an SM for up to four rows
-        q.slots = std::max<int64_t>(2 * (ceil_div(V, 128) + ceil_div(V, q.piece)), num_sms());
+        // 128-wide tiles: the most slots; two an SM for up to four rows
+        q.slots = std::max<int64_t>(2 * (ceil_div(V, 128) + ceil_div(V, q.piece)), 2 * num_sms());
         q.part = w.take(size_t(q.part_ld) * q.slots * 8);
         q.zt = w.take(size_t(N) * 4);
     } else {
@@ -847,7 +853,7 @@ Plan plan_of(int htype, int wtype, int64_t N, int64_t V, int64_t D, bool grad, b
 
 int pack(const void *x, int type, int64_t rows, int64_t cols, int64_t ld, int terms, const int64_t *targets, int64_t vocab,
          __nv_bfloat16 *y, cudaStream_t st) {
-    const unsigned grid = stream_grid(rows * (ld / 4), 256);
+    const unsigned grid = stream_grid(rows * (ld / 8), 256);
     if (type == TLB_W_F32)
         xent_pack_kernel<float><<<grid, 256, 0, st>>>(static_cast<const float *>(x), rows, int(cols), int(ld), terms, targets,
                                                       vocab, y);

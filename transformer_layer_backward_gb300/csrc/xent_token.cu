@@ -7,7 +7,7 @@
 // and used for both z and dz W (and the block's rows of d_w), so W crosses once.  All
 // arithmetic is fp32: z, the softmax and dz are never rounded to fewer bits.
 //
-// One CTA per SM, 16 warps.  A thread owns the same column pairs of every head row: its part
+// One CTA of 16 warps an SM, or two of 8.  A thread owns the same column pairs of every head row: its part
 // of the hidden rows and of d_hidden stays in registers.  Per block of 8 rows (4 of float32):
 //   the thread's W values into registers; its share of the 8 N dot products
 //   warp sums by exchange (a lane ends with one of the 8 N values), 16 warps' sums in shared
@@ -30,7 +30,6 @@ namespace tlb {
 
 namespace {
 
-constexpr int kThreads = 512, kWarps = 16;
 constexpr int kMaxStages = 6;
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -71,8 +70,11 @@ __device__ __forceinline__ float2 unpack(const Pair<W32> &p) {
     else return make_float2(bf16_lo(p.v), bf16_hi(p.v));
 }
 
-template <int N, int R, bool W32, bool GRAD>
-__global__ void __launch_bounds__(kThreads, 1) xent_token_kernel(const __grid_constant__ TokenParams p) {
+// TH threads: 512, one CTA an SM, or 256, two CTAs, where a thread's registers hold twice the
+// columns; the two then wait at barriers of their own.
+template <int TH, int N, int R, bool W32, bool GRAD>
+__global__ void __launch_bounds__(TH, 512 / TH) xent_token_kernel(const __grid_constant__ TokenParams p) {
+    constexpr int kThreads = TH, kWarps = TH / 32;
     constexpr int VB = block_rows<W32>(), NV = VB * N;
     constexpr int SH = NV == 32 ? 0 : NV == 16 ? 1 : NV == 8 ? 2 : 3;      // lane >> SH: the lane's value
     static_assert((NV << SH) == 32, "values a warp reduces");
@@ -303,37 +305,43 @@ __global__ void __launch_bounds__(256) xent_token_sum_kernel(const float *__rest
     }
 }
 
-template <int N, int R, bool W32, bool GRAD>
+template <int TH, int N, int R, bool W32, bool GRAD>
 int launch(TokenParams &p, int grid, cudaStream_t st) {
-    p.stages = std::min(kMaxStages, (220 * 1024) / (16 * p.D));
+    constexpr int room = (TH == 512 ? 220 : 108) * 1024;
+    p.stages = std::min(kMaxStages, room / (16 * p.D));
     const int smem = p.stages * 16 * p.D;
-    auto k = xent_token_kernel<N, R, W32, GRAD>;
-    TLB_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 220 * 1024));
-    k<<<grid, kThreads, smem, st>>>(p);
+    auto k = xent_token_kernel<TH, N, R, W32, GRAD>;
+    TLB_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, room));
+    k<<<grid, TH, smem, st>>>(p);
     return check_launch(GRAD ? "xent_token_grad" : "xent_token_loss");
 }
 
-// Column pairs a thread holds: registers allow 6 rounds of 512 pairs for one row, 3 for two and
-// four.
-constexpr int kRounds1 = 6, kRounds = 3;
+// Column pairs a thread holds: registers allow 6 rounds of 512 pairs for one row, 3 for two to
+// four; of 256 pairs 5 for up to two rows.
+constexpr int kRounds1 = 6, kRounds = 3, kRounds256 = 5;
+
+// Two CTAs an SM where the rows allow it: the gradient of one token over 32768 x 2560 takes
+// 43 us with one CTA (its warps wait for one another at every block of head rows).
+bool two_ctas(int64_t N, int64_t D) { return N <= 2 && D <= kRounds256 * 2 * 256; }
 
 template <bool W32, bool GRAD>
 int by_rows(TokenParams &p, int64_t N, int grid, cudaStream_t st) {
-    const bool few = p.D <= kRounds * 2 * kThreads;
-    if (N == 1) return few ? launch<1, kRounds, W32, GRAD>(p, grid, st) : launch<1, kRounds1, W32, GRAD>(p, grid, st);
-    if (N == 2) return launch<2, kRounds, W32, GRAD>(p, grid, st);
-    return launch<4, kRounds, W32, GRAD>(p, grid, st);
+    if (two_ctas(N, p.D))
+        return N == 1 ? launch<256, 1, kRounds256, W32, GRAD>(p, grid, st) : launch<256, 2, kRounds256, W32, GRAD>(p, grid, st);
+    if (N == 1) return p.D <= kRounds * 1024 ? launch<512, 1, kRounds, W32, GRAD>(p, grid, st) : launch<512, 1, kRounds1, W32, GRAD>(p, grid, st);
+    if (N == 2) return launch<512, 2, kRounds, W32, GRAD>(p, grid, st);
+    return launch<512, 4, kRounds, W32, GRAD>(p, grid, st);
 }
 
-int token_grid(int wtype, int64_t vocab) {
-    return int(std::min<int64_t>(num_sms(), ceil_div(vocab, wtype == TLB_W_F32 ? 4 : 8)));
+int token_grid(int wtype, int64_t N, int64_t vocab, int64_t D) {
+    return int(std::min<int64_t>((two_ctas(N, D) ? 2 : 1) * num_sms(), ceil_div(vocab, wtype == TLB_W_F32 ? 4 : 8)));
 }
 
 }  // namespace
 
 // Up to four rows of an even length whose share fits a thread's registers.
 bool xent_token_supported(int64_t N, int64_t D) {
-    return N >= 1 && N <= 4 && D % 2 == 0 && D <= (N == 1 ? kRounds1 : kRounds) * 2 * kThreads;
+    return N >= 1 && N <= 4 && D % 2 == 0 && D <= (N == 1 ? kRounds1 : kRounds) * 1024;
 }
 
 int xent_token_loss(int htype, const void *hidden, int wtype, const void *W, const int64_t *targets, int64_t N, int64_t V,
@@ -351,7 +359,7 @@ int xent_token_loss(int htype, const void *hidden, int wtype, const void *W, con
     p.ld_part = ld_part;
     p.zt = zt;
     p.status = status;
-    *slots = token_grid(wtype, V);
+    *slots = token_grid(wtype, N, V, D);
     return wtype == TLB_W_F32 ? by_rows<true, false>(p, N, *slots, st) : by_rows<false, false>(p, N, *slots, st);
 }
 
@@ -372,7 +380,7 @@ int xent_token_grad(int htype, const void *hidden, int wtype, const void *W, con
     p.partial = partial;
     p.dw = d_w;
     p.status = status;
-    const int grid = token_grid(wtype, V), n = int(N * D);
+    const int grid = token_grid(wtype, N, V, D), n = int(N * D);
     TLB_TRY((wtype == TLB_W_F32 ? by_rows<true, true>(p, N, grid, st) : by_rows<false, true>(p, N, grid, st)));
     xent_token_sum_kernel<<<unsigned(ceil_div(n, 32)), 256, 0, st>>>(
         partial, grid, n, htype == TLB_W_F32 ? static_cast<float *>(d_hidden) : nullptr,
