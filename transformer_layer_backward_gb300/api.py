@@ -19,9 +19,14 @@ _WDTYPE = {A.W_F32: torch.float32, A.W_BF16: torch.bfloat16, A.W_TERNARY_I8: tor
 _WCODE = {"f32": A.W_F32, "bf16": A.W_BF16, "ternary": A.W_TERNARY_I8, "ternary2": A.W_TERNARY_2B}
 
 
+_NO_GUARD = contextlib.nullcontext()
+
+
 def _on_device(t):
     """Guard that makes the tensor's device the current one, for the launch and the stream."""
-    return torch.cuda.device(t.device) if t.is_cuda else contextlib.nullcontext()
+    if not t.is_cuda or t.device.index == torch.cuda.current_device():
+        return _NO_GUARD
+    return torch.cuda.device(t.device)
 
 
 def _stream(stream):

@@ -383,6 +383,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
     if constexpr (PAIR) cluster_sync();              // the peer's barriers exist before any remote arrive
     tc_fence_after();
     const uint32_t tmem = tmem_base;
+    pdl_trigger();                                           // the kernel that joins the parts may be scheduled
 
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
@@ -586,6 +587,7 @@ template <int BN, bool PAIR>
 __global__ void __launch_bounds__(256) xent_fixup_kernel(const __grid_constant__ XParams p) {
     constexpr int TM = PAIR ? 2 * kBM : kBM;
     const int64_t KB = int64_t(p.nprod) * p.kb, ta = int64_t(blockIdx.x) * KB, tb = ta + KB;
+    pdl_wait();
     int c0 = int(ta * p.sk_units / p.sk_work);
     while (c0 > 0 && sk_start(p.sk_work, p.sk_units, c0) > ta) --c0;
     while (c0 + 1 < p.sk_units && sk_start(p.sk_work, p.sk_units, c0 + 1) <= ta) ++c0;
@@ -633,6 +635,7 @@ __global__ void __launch_bounds__(256) xent_join_kernel(const float2 *__restrict
     __shared__ float2 sh[256];
     const int x = threadIdx.x % rx, y = threadIdx.x / rx, ny = 256 / rx;
     const int row = blockIdx.x * rx + x;
+    pdl_wait();
     auto scaled = [](float2 a, float ref) { return a.y * ex2((a.x - ref) * kLog2e); };
     float2 a = make_float2(-INFINITY, 0.f);
     for (int s = y; s < slots && row < rows; s += 8 * ny) {
@@ -781,7 +784,7 @@ int launch(XParams &p, const Mat &a, const Mat &b, cudaStream_t st) {
     TLB_TRY(check_launch(MODE == kStats ? "xent_stats" : MODE == kGrad ? "xent_grad" : A_MN ? "xent_dw" : "xent_dh"));
     if (p.sk_work > 0) {
         const int64_t rest = p.sk_work / KB;
-        xent_fixup_kernel<BN, PAIR><<<dim3(unsigned(rest), PAIR ? 64 : 32), 256, 0, st>>>(p);
+        TLB_CUDA(launch_dependent(xent_fixup_kernel<BN, PAIR>, dim3(unsigned(rest), PAIR ? 64 : 32), dim3(256), 0, st, p));
         TLB_TRY(check_launch("xent_fixup"));
     }
     return TLB_OK;
@@ -905,9 +908,9 @@ int join(const Plan &q, void *ws, int64_t r0, int64_t n, int slots, const int64_
          float *lse, cudaStream_t st) {
     int rx = 1;                                              // a block for every SM first, then whole sectors
     while (rx < 8 && 2 * rx * int64_t(num_sms()) <= n) rx *= 2;
-    xent_join_kernel<<<unsigned(ceil_div(n, rx)), 256, 0, st>>>(ws_at<float2>(ws, q.part), q.part_ld, slots, int(n), rx,
-                                                                ws_at<float>(ws, q.zt) + r0, targets + r0, vocab, loss + r0,
-                                                                lse + r0);
+    TLB_CUDA(launch_dependent(xent_join_kernel, dim3(unsigned(ceil_div(n, rx))), dim3(256), 0, st,
+                              ws_at<float2>(ws, q.part), q.part_ld, slots, int(n), rx, ws_at<float>(ws, q.zt) + r0,
+                              targets + r0, vocab, loss + r0, lse + r0));
     return check_launch("xent_join");
 }
 

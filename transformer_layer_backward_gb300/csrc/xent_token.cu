@@ -101,6 +101,7 @@ __global__ void __launch_bounds__(TH, 512 / TH) xent_token_kernel(const __grid_c
     };
     if (tid == 0)
         for (int i = 0; i < stages; ++i) fetch(i);
+    pdl_trigger();                                          // the kernel that joins the parts may be scheduled
 
     // the lane's value: head row vr of the block, hidden row vn
     const int vi = lane >> SH, vn = vi % N, vr = vi / N;
@@ -287,6 +288,7 @@ __global__ void __launch_bounds__(256) xent_token_sum_kernel(const float *__rest
                                                              __nv_bfloat16 *out16) {
     __shared__ float sh[8][32];
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5, e = blockIdx.x * 32 + x;
+    pdl_wait();
     float s = 0.f;
     for (int k = y; k < parts && e < n; k += 64) {
         float v[8];
@@ -382,9 +384,9 @@ int xent_token_grad(int htype, const void *hidden, int wtype, const void *W, con
     p.status = status;
     const int grid = token_grid(wtype, N, V, D), n = int(N * D);
     TLB_TRY((wtype == TLB_W_F32 ? by_rows<true, true>(p, N, grid, st) : by_rows<false, true>(p, N, grid, st)));
-    xent_token_sum_kernel<<<unsigned(ceil_div(n, 32)), 256, 0, st>>>(
-        partial, grid, n, htype == TLB_W_F32 ? static_cast<float *>(d_hidden) : nullptr,
-        htype == TLB_W_F32 ? nullptr : static_cast<__nv_bfloat16 *>(d_hidden));
+    TLB_CUDA(launch_dependent(xent_token_sum_kernel, dim3(unsigned(ceil_div(n, 32))), dim3(256), 0, st, partial, grid, n,
+                              htype == TLB_W_F32 ? static_cast<float *>(d_hidden) : nullptr,
+                              htype == TLB_W_F32 ? nullptr : static_cast<__nv_bfloat16 *>(d_hidden)));
     return check_launch("xent_token_sum");
 }
 
