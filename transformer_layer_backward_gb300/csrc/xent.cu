@@ -68,7 +68,7 @@ struct XParams {
     int M, N;                                // rows and columns of the result
     int tiles_m, tiles_n;
     int units;                               // CTAs (pairs): unit u does the whole tiles u, u + units, ...
-    int64_t whole;                           // ... below `whole`, then its share of the other tiles'
+    int whole;                               // ... below `whole`, then its share of the other tiles'
     int64_t sk_work;                         // k blocks (kOut: split evenly over sk_units units)
     int sk_units;
     // kStats, kGrad
@@ -92,13 +92,12 @@ __host__ __device__ __forceinline__ int64_t sk_start(int64_t work, int units, in
 // Result tile number t: groups of kGroupM row tiles, inside a group the row tiles of one
 // column tile first.  The CTAs that run together so share a few column tiles of one operand
 // and 16 row tiles of the other (21 MB of 2560-wide rows), which stay in L2.
-__device__ __forceinline__ void tile_of(const XParams &p, int64_t t, int &m, int &n) {
-    const int64_t group = int64_t(kGroupM) * p.tiles_n;
-    const int g = int(t / group);
-    const int64_t r = t - g * group;
-    const int rows = min(kGroupM, p.tiles_m - g * kGroupM);
-    n = int(r / rows);
-    m = g * kGroupM + int(r - int64_t(n) * rows);
+// (Fewer than 2^31 tiles: 2^24 rows by 2^20 columns at most.)
+__device__ __forceinline__ void tile_of(const XParams &p, uint32_t t, int &m, int &n) {
+    const uint32_t group = uint32_t(kGroupM) * p.tiles_n, g = t / group, r = t - g * group;
+    const uint32_t rows = min(kGroupM, p.tiles_m - int(g) * kGroupM), c = r / rows;
+    n = int(c);
+    m = int(g * kGroupM + (r - c * rows));
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -324,35 +323,37 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
     // this unit's segments: its whole tiles, then its share of the split tiles, cut at tiles
     const int KB = p.nprod * p.kb;
     const int chunk = !FINE ? KB : MODE != kStats ? kChunkGrad : p.nprod > 1 ? kChunkTerms : kChunkLoss;                    // k blocks of one accumulator
-    const int64_t nwhole = p.whole > unit ? (p.whole - unit + p.units - 1) / p.units : 0;
+    const int nwhole = p.whole > unit ? (p.whole - unit + p.units - 1) / p.units : 0;
     const bool splits = MODE == kOut && p.sk_work > 0 && unit < p.sk_units;
-    const int64_t b0 = splits ? sk_start(p.sk_work, p.sk_units, unit) : 0;
-    const int64_t b1 = splits ? sk_start(p.sk_work, p.sk_units, unit + 1) : 0;
+    const int b0 = splits ? int(sk_start(p.sk_work, p.sk_units, unit)) : 0;       // sk_work < units KB < 2^31
+    const int b1 = splits ? int(sk_start(p.sk_work, p.sk_units, unit + 1)) : 0;
     struct Seg {
-        int m0, n0, tn, kb0, kb1, slot;
+        int tile, kb0, kb1, slot;
     };
     // segment i; `at` walks through [b0, b1) after the whole tiles
-    auto next_seg = [&](int64_t i, int64_t &at, Seg &s) {
-        int64_t t;
+    auto next_seg = [&](int i, int &at, Seg &s) {
         if (i < nwhole) {
-            t = i * p.units + unit;
+            s.tile = i * p.units + unit;
             s.kb0 = 0;
             s.kb1 = KB;
             s.slot = 0;
         } else {
             if (at >= b1) return false;
-            const int64_t tl = at / KB;
-            s.kb0 = int(at - tl * KB);
-            s.kb1 = int(min(int64_t(KB), b1 - tl * KB));
+            const int tl = at / KB;
+            s.kb0 = at - tl * KB;
+            s.kb1 = min(KB, b1 - tl * KB);
             s.slot = at == b0 ? 0 : 1;
             at += s.kb1 - s.kb0;
-            t = p.whole + tl;
+            s.tile = p.whole + tl;
         }
-        int m;
-        tile_of(p, t, m, s.tn);
-        s.m0 = m * TM + rank * kBM;
-        s.n0 = s.tn * BN;
         return true;
+    };
+    // this CTA's first row, the first column and the column tile of a tile
+    auto place = [&](int tile, int &m0, int &n0, int &tn) {
+        int m;
+        tile_of(p, uint32_t(tile), m, tn);
+        m0 = m * TM + rank * kBM;
+        n0 = tn * BN;
     };
 
     if (threadIdx.x == 0) {
@@ -388,12 +389,23 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
     if (warp == 0) {
         // ------------------------------------------------ TMA producer
         if (lane == 0) {
-            int g = 0;
+            int g = 0, at = b0;
             bool ok = true;
-            int64_t at = b0;
             Seg sg;
-            for (int64_t i = 0; ok && next_seg(i, at, sg); ++i) {
-                for (int kb = sg.kb0; kb < sg.kb1; ++kb, ++g) {
+            for (int i = 0; ok && next_seg(i, at, sg); ++i) {
+                int m0, n0, tn;
+                place(sg.tile, m0, n0, tn);
+                const int nb = n0 + rank * BH;
+                // A part of a tile starts at a multiple of the units' share and wraps round, so
+                // that the units are at the same k of different tiles at the same time and
+                // share its operand tiles in L2
+                int kb = sg.kb0;
+                if (splits && i >= nwhole && sg.kb1 - sg.kb0 == b1 - b0) {
+                    const int share = int((p.sk_work + p.sk_units - 1) / p.sk_units);
+                    kb = (sg.kb0 + share - 1) / share * share;
+                    if (kb >= sg.kb1) kb = sg.kb0;
+                }
+                for (int j = sg.kb0; j < sg.kb1; ++j, ++g, kb = kb + 1 < sg.kb1 ? kb + 1 : sg.kb0) {
                     const int s = g % kStages;
                     if (g >= kStages && !mbar_wait(&empty[s], ((g / kStages) - 1) & 1, p.status, 20u)) {
                         ok = false;
@@ -402,15 +414,14 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
                     const int kq = kb / p.nprod, prod = kb - kq * p.nprod, k0 = kq * kBK;
                     const CUtensorMap *ma = &p.a[p.pa[prod]], *mb = &p.b[p.pb[prod]];
                     uint8_t *sa = smem + s * STAGE, *sb = sa + A_BYTES;
-                    const int nb = sg.n0 + rank * BH;
                     if constexpr (PAIR) {
                         if (leader) mbar_arrive_expect_tx(&full[s], 2 * STAGE);   // both CTAs' copies
                         const uint32_t fb = cluster_addr(&full[s], 0);
                         if constexpr (A_MN) {
                             for (int c = 0; c < kBM / 64; ++c)
-                                tma_load_2d_pair(sa + c * kBK * 128, ma, sg.m0 + c * 64, k0, fb);
+                                tma_load_2d_pair(sa + c * kBK * 128, ma, m0 + c * 64, k0, fb);
                         } else {
-                            tma_load_2d_pair(sa, ma, k0, sg.m0, fb);
+                            tma_load_2d_pair(sa, ma, k0, m0, fb);
                         }
                         if constexpr (B_MN) {
                             for (int c = 0; c < BH / 64; ++c)
@@ -422,9 +433,9 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
                         mbar_arrive_expect_tx(&full[s], STAGE);
                         if constexpr (A_MN) {
                             for (int c = 0; c < kBM / 64; ++c)
-                                tma_load_2d(sa + c * kBK * 128, ma, sg.m0 + c * 64, k0, &full[s]);
+                                tma_load_2d(sa + c * kBK * 128, ma, m0 + c * 64, k0, &full[s]);
                         } else {
-                            tma_load_2d(sa, ma, k0, sg.m0, &full[s]);
+                            tma_load_2d(sa, ma, k0, m0, &full[s]);
                         }
                         if constexpr (B_MN) {
                             for (int c = 0; c < BH / 64; ++c)
@@ -445,11 +456,10 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
                                        (B_MN ? 1u << 16 : 0u) | (uint32_t(BN >> 3) << 17) | (uint32_t(TM >> 4) << 24);
             // 16 k: 32 bytes along a K-major row, 16 rows of 128 bytes of an MN-major tile
             constexpr int ka = A_MN ? 128 : 2, kbs = B_MN ? 128 : 2;
-            int g = 0, f = 0;                                // k blocks, accumulators so far
+            int g = 0, f = 0, at = b0;                       // k blocks, accumulators so far
             bool ok = true;
-            int64_t at = b0;
             Seg sg;
-            for (int64_t i = 0; ok && next_seg(i, at, sg); ++i) {
+            for (int i = 0; ok && next_seg(i, at, sg); ++i) {
                 for (int k0 = sg.kb0; ok && k0 < sg.kb1; k0 += chunk, ++f) {
                     const int b = f & 1, k1 = min(sg.kb1, k0 + chunk);
                     const uint32_t acc = tmem + uint32_t(b * BN);
@@ -495,12 +505,13 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
         uint8_t *buf = smem + kStages * STAGE;
         uint8_t *box = buf + (warp - 2) * kBox;                                        // kGrad
         float *blk = reinterpret_cast<float *>(buf) + (warp - 2) * 32 * 33;            // kOut
-        int f = 0;
+        int f = 0, at = b0;
         bool ok = true;
-        int64_t at = b0;
         Seg sg;
-        for (int64_t i = 0; ok && next_seg(i, at, sg); ++i) {
-            const int row0 = sg.m0 + q * 32, colh = sg.n0 + half * (BN / 2);
+        for (int i = 0; ok && next_seg(i, at, sg); ++i) {
+            int m0, n0, tn;
+            place(sg.tile, m0, n0, tn);
+            const int row0 = m0 + q * 32, colh = n0 + half * (BN / 2);
             float *part = nullptr;                            // kOut: this warp's part of a partial tile
             if (MODE == kOut && (sg.kb0 != 0 || sg.kb1 != KB))
                 part = p.partial + ((int64_t(blockIdx.x) * 2 + sg.slot) * kBM + q * 32) * BN + half * (BN / 2);
@@ -553,7 +564,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
             }
             if (!ok) break;
             if constexpr (MODE == kStats) {
-                stats_row<BN>(p, z, row0 + lane, colh, 2 * sg.tn + half);
+                stats_row<BN>(p, z, row0 + lane, colh, 2 * tn + half);
             } else if constexpr (FINE) {
 #pragma unroll
                 for (int c0 = 0; c0 < BN / 2; c0 += WN) block(z + c0, c0);
@@ -596,7 +607,7 @@ __global__ void __launch_bounds__(256) xent_fixup_kernel(const __grid_constant__
     if (c1 == c0) return;
     const int s0 = sk_start(p.sk_work, p.sk_units, c0) < ta ? 1 : 0;
     int m, n;
-    tile_of(p, p.whole + blockIdx.x, m, n);
+    tile_of(p, uint32_t(p.whole + blockIdx.x), m, n);
     const int m0 = m * TM, n0 = n * BN;
     const int rows = TM / gridDim.y, r0 = blockIdx.y * rows;
     for (int e = threadIdx.x; e < rows * (BN / 4); e += blockDim.x) {
@@ -752,7 +763,8 @@ int launch(XParams &p, const Mat &a, const Mat &b, cudaStream_t st) {
     p.tiles_n = int(ceil_div(p.N, BN));
     const int64_t tiles = int64_t(p.tiles_m) * p.tiles_n, KB = int64_t(p.nprod) * p.kb;
     const int most = PAIR ? num_sms() / 2 : num_sms();
-    p.whole = tiles;
+    TLB_REQUIRE(tiles < (int64_t(1) << 31), TLB_EUNSUPPORTED, "xent: too many tiles");
+    p.whole = int(tiles);
     p.sk_work = 0;
     p.sk_units = 1;
     p.units = int(std::min<int64_t>(tiles, most));
@@ -761,7 +773,7 @@ int launch(XParams &p, const Mat &a, const Mat &b, cudaStream_t st) {
         // them costs less: a split ends in partial tiles and a second kernel, about 24 k blocks
         const int64_t rest = tiles % most;
         if (rest > 0 && KB > KB * rest / most + 24) {
-            p.whole = tiles - rest;
+            p.whole = int(tiles - rest);
             p.sk_work = rest * KB;
             p.sk_units = int(std::max<int64_t>(1, std::min<int64_t>(most, p.sk_work / 8)));
             p.units = p.whole > 0 ? most : p.sk_units;
