@@ -59,6 +59,7 @@ struct Params {
     int nmat, tiles_per_block;
     float *ws;
     int64_t mpoly;                       // offset of the products M [nmat][RP * RP]
+    uint32_t *status;
     float mu, wd;
     int nesterov;
     float a, b, c, eps;                  // Newton-Schulz
@@ -591,7 +592,7 @@ template <int RP> constexpr int pass_floats() {
 }
 
 template <int RP, int SOURCE, int SINK>
-__global__ void __launch_bounds__(NT, RP == 64 ? 2 : 1) muon_pass_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(NT) muon_pass_kernel(const __grid_constant__ Params p) {
     using T = Tile<RP>;
     constexpr int JT = T::JT, LD = T::LD, LM = T::LM, B = T::B;
     extern __shared__ __align__(16) float sh[];
@@ -642,6 +643,319 @@ __global__ void __launch_bounds__(NT, RP == 64 ? 2 : 1) muon_pass_kernel(const _
     if constexpr (SINK != kParam) gram_keep<RP>(s, p.ws + a.part + int64_t(bl) * T::GSIZE);
 }
 
+// ---------------------------------------------------------------- the passes for r > 32, on the tensor cores
+
+// With r near 64 the passes' 3 r FMAs an element would bound them on the CUDA cores (180 us for
+// one pass over the 94 MB of a rank-64 36-layer stack).  Here both products run on tcgen05
+// with every float taken apart into three bf16 terms of 8 bits (x = x0 + x1 + x2 exactly):
+//   Y^T = X^T M^T     128 columns as the MMA's rows, K = 64 rows of X, the six term products
+//                     x_a m_b with a + b <= 2, the smallest first; fp32 in tensor memory
+//   G = D1 + D2 + D2^T, D1 = x1 x1^T + x0 x0^T, D2 = x0 x2^T + x0 x1^T, over the columns
+// What is left out is 2^-24 of a product.  A term of X lies in shared memory as [64 rows][64
+// columns] blocks of 128-byte rows with 128-byte swizzle, which is an MN-major operand for the
+// first product and a K-major one for the second.
+constexpr int kTcJ = 128;                                   // columns of a tile
+constexpr int kXPlane = 64 * kTcJ * 2, kMPlane = 64 * 64 * 2;
+// 3 planes of X and of M; the rest keeps a third CTA off the SM (tensor memory: two of 256
+// columns).  An MMA of G reads 128 rows: 64 of a block and the 64 rows behind it, whose
+// results are not looked at; behind the last block of X lies M.
+constexpr int kTcSmem = 84 * 1024;
+static_assert(3 * kXPlane + 3 * kMPlane + 1024 <= kTcSmem, "shared memory of the planes");
+
+// Byte offset of element (i, j) in a plane of X (blocks of 64 columns), or of M with j < 64.
+__device__ __forceinline__ int plane_at(int i, int j) {
+    return (j >> 6) * (64 * 128) + i * 128 + ((((j & 63) >> 3) ^ (i & 7)) << 4) + (j & 7) * 2;
+}
+// Cuts the 8 highest significant bits off x.
+__device__ __forceinline__ uint32_t cut_term(float &x) {
+    const uint32_t u = __float_as_uint(x);
+    x -= __uint_as_float(u & 0xFFFF0000u);
+    return u;
+}
+// Values into the planes: C = 4 along the columns (S = 1) or down the rows (S = 0), or one.
+template <int C, int S>
+__device__ __forceinline__ void put_terms(uint8_t *planes, int plane, int i, int j, float (&v)[C]) {
+#pragma unroll
+    for (int t = 0; t < 3; ++t, planes += plane) {
+        uint32_t u[C];
+#pragma unroll
+        for (int c = 0; c < C; ++c) u[c] = cut_term(v[c]);
+        if constexpr (C == 4 && S == 1) {
+            *reinterpret_cast<uint2 *>(planes + plane_at(i, j)) =
+                make_uint2(__byte_perm(u[0], u[1], 0x7632), __byte_perm(u[2], u[3], 0x7632));
+        } else {
+#pragma unroll
+            for (int c = 0; c < C; ++c)
+                *reinterpret_cast<uint16_t *>(planes + plane_at(i + (S == 0 ? c : 0), j + (S == 1 ? c : 0))) = uint16_t(u[c] >> 16);
+        }
+    }
+}
+
+// This thread's pieces of a tile of u, or of p: f(C, S, N, item) with item(k) the k-th of N
+// pieces, {whether it exists, element offset, row, column}; S as in put_terms.
+struct Piece {
+    bool on;
+    int64_t e;
+    int i, j;
+};
+template <typename F>
+__device__ __forceinline__ void tc_visit(const Mat &a, int j0, int jn, F f) {
+    constexpr std::integral_constant<int, 0> down{};
+    constexpr std::integral_constant<int, 1> one{};
+    constexpr std::integral_constant<int, 4> four{};
+    constexpr std::integral_constant<int, 8> n8{};
+    constexpr std::integral_constant<int, 32> n32{};
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (!a.tall && a.vec) {                                  // a warp a row, a lane four columns
+        f(four, one, n8, [&](int k) {
+            const int i = warp + 8 * k, j = 4 * lane;
+            return Piece{i < a.r && j < jn, int64_t(i) * a.n + j0 + j, i, j};
+        });
+    } else if (!a.tall) {
+        f(one, one, n32, [&](int k) {
+            const int i = warp + 8 * (k >> 2), j = lane + 32 * (k & 3);
+            return Piece{i < a.r && j < jn, int64_t(i) * a.n + j0 + j, i, j};
+        });
+    } else if (a.vec) {                                      // a warp 8 columns x 16 rows
+        f(four, down, n8, [&](int k) {
+            const int j = (warp + 8 * (k >> 2)) * 8 + (lane >> 2), i = (k & 3) * 16 + (lane & 3) * 4;
+            return Piece{i < a.r && j < jn, int64_t(j0 + j) * a.r + i, i, j};
+        });
+    } else {                                                 // a thread half a column
+        f(one, down, n32, [&](int k) {
+            const int j = threadIdx.x & 127, i = (threadIdx.x >> 7) * 32 + k;
+            return Piece{i < a.r && j < jn, int64_t(j0 + j) * a.r + i, i, j};
+        });
+    }
+}
+
+// The terms of u into the planes, from g and the momentum, which FIRST brings up to date.
+template <bool FIRST>
+__device__ __forceinline__ void tc_load_update(const Params &p, const Mat &a, uint8_t *planes, int j0, int jn) {
+    const float mu = p.mu;
+    const bool nesterov = p.nesterov != 0;
+    tc_visit(a, j0, jn, [&](auto cc, auto ss, auto nn, auto item) {
+        constexpr int C = decltype(cc)::value, S = decltype(ss)::value, U = 4;
+#pragma unroll 1
+        for (int k = 0; k < decltype(nn)::value; k += U) {
+            float g[U][C], m[U][C];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const Piece q = item(k + u);
+                const int64_t e = q.on ? q.e : 0;
+                load_piece<C>(a.g + e, g[u]);
+                load_piece<C>(a.m + e, m[u]);
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const Piece q = item(k + u);
+                if (!q.on) continue;
+                if constexpr (FIRST) {
+#pragma unroll
+                    for (int c = 0; c < C; ++c) m[u][c] = fmaf(mu, m[u][c], g[u][c]);
+                    keep_piece<C>(a.m + q.e, m[u]);
+                }
+                if (nesterov) {
+#pragma unroll
+                    for (int c = 0; c < C; ++c) m[u][c] = fmaf(mu, m[u][c], g[u][c]);
+                }
+                put_terms<C, S>(planes, kXPlane, q.i, q.j, m[u]);
+            }
+        }
+    });
+}
+
+template <int SOURCE, int SINK>
+__global__ void __launch_bounds__(NT, 2) muon_tc_pass_kernel(const __grid_constant__ Params p) {
+    using T = Tile<64>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *planes = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint8_t *mplanes = planes + 3 * kXPlane;
+    __shared__ uint64_t bar_y, bar_g;
+    __shared__ uint32_t tmem_base;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int lo = 0, hi = p.nmat - 1;                            // this block's matrix
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if (p.mat[mid].block0 <= int(blockIdx.x)) lo = mid;
+        else hi = mid - 1;
+    }
+    const Mat &a = p.mat[lo];
+    const int bl = blockIdx.x - a.block0, t0 = bl * p.tiles_per_block;
+    const int t1 = min((a.n + kTcJ - 1) / kTcJ, t0 + p.tiles_per_block);
+    if (warp == 0) {
+        tmem_alloc(&tmem_base, 256);
+        tmem_relinquish();
+    }
+    if (tid == 0) {
+        mbar_init(&bar_y, 1);
+        mbar_init(&bar_g, 1);
+    }
+    fence_mbar_init();
+    tc_fence_before();
+    auto clear = [&] {
+        for (int k = tid; k < 3 * kXPlane / 16; k += NT) reinterpret_cast<uint4 *>(planes)[k] = make_uint4(0, 0, 0, 0);
+    };
+    clear();                                                 // rows past r stay 0
+    if constexpr (SOURCE != kMomentum) {
+        const float *src = p.ws + p.mpoly + int64_t(lo) * 64 * 64;
+        for (int k = tid; k < 64 * 16; k += NT) {
+            float v[4];
+            load_piece<4>(src + 4 * k, v);
+            put_terms<4, 1>(mplanes, kMPlane, k / 16, (k % 16) * 4, v);
+        }
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base, ty = tmem, td1 = tmem + 64, td2 = tmem + 128;
+    // D f32, A and B bf16, 128 x 64; A MN-major for Y
+    constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(64 >> 3) << 17) | (uint32_t(128 >> 4) << 24);
+    const int q = warp & 3, half = warp >> 2;               // TMEM lanes (columns of X), half of the rows
+    int done = 0;
+    for (int t = t0; t < t1; ++t, ++done) {
+        const int j0 = t * kTcJ, jn = min(kTcJ, a.n - j0);
+        float *y = p.ws + a.y + int64_t(t) * 64 * kTcJ;      // this tile of Y: [64][128]
+        if (SINK != kParam && done > 0) mbar_wait(&bar_g, (done - 1) & 1, p.status, 40u);   // the planes are read
+        if (jn < kTcJ) {                                     // columns past the last count as 0
+            clear();
+            __syncthreads();
+        }
+        if constexpr (SOURCE == kY) {
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                float v[4];
+                const int i = warp + 8 * k;
+                load_piece<4>(y + i * kTcJ + 4 * lane, v);
+                put_terms<4, 1>(planes, kXPlane, i, 4 * lane, v);
+            }
+        } else {
+            tc_load_update<SOURCE == kMomentum>(p, a, planes, j0, jn);
+        }
+        fence_proxy_async();
+        tc_fence_before();
+        __syncthreads();
+        if constexpr (SOURCE != kMomentum) {
+            if (tid == 0) {
+                tc_fence_after();
+                uint32_t add = 0;
+#pragma unroll
+                for (int sum = 2; sum >= 0; --sum)
+#pragma unroll
+                    for (int ta = 0; ta <= sum; ++ta) {
+                        uint64_t ad = sw128_desc(planes + ta * kXPlane);
+                        // MN-major: blocks of 64 columns 8192 bytes apart (leading offset)
+                        ad = (ad & ~(0x3FFFull << 16)) | (uint64_t(8192 >> 4) << 16);
+                        const uint64_t bd = sw128_desc(mplanes + (sum - ta) * kMPlane);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {        // 16 rows of X: 2048 bytes; of M: 32
+                            mma_bf16(ty, ad + 128 * k, bd + 2 * k, idesc | (1u << 15), add);
+                            add = 1;
+                        }
+                    }
+                mma_commit(&bar_y);
+            }
+            mbar_wait(&bar_y, done & 1, p.status, 41u);
+            tc_fence_after();
+            uint32_t v[32];
+            tmem_ld32(ty + (uint32_t(q * 32) << 16) + uint32_t(half * 32), v);
+            tmem_wait_ld();
+            const int j = q * 32 + lane, i0 = half * 32;
+            if constexpr (SINK == kParam) {
+                const float decay = a.lr * p.wd, move = a.lr_scale;
+                if (j < jn) {
+                    if (a.tall && a.vec) {
+                        float *pp = a.p + int64_t(j0 + j) * a.r + i0;
+#pragma unroll
+                        for (int c = 0; c < 32; c += 4) {
+                            if (i0 + c >= a.r) continue;
+                            float x[4];
+                            load_piece<4>(pp + c, x);
+#pragma unroll
+                            for (int d = 0; d < 4; ++d) x[d] -= fmaf(move, __uint_as_float(v[c + d]), __fmul_rn(decay, x[d]));
+                            keep_piece<4>(pp + c, x);
+                        }
+                    } else {
+                        const int64_t step = a.tall ? 1 : a.n;
+                        float *pp = a.tall ? a.p + int64_t(j0 + j) * a.r + i0 : a.p + int64_t(i0) * a.n + j0 + j;
+#pragma unroll
+                        for (int c0 = 0; c0 < 32; c0 += 8) {
+                            float x[8];
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) x[c] = i0 + c0 + c < a.r ? pp[(c0 + c) * step] : 0.f;
+#pragma unroll
+                            for (int c = 0; c < 8; ++c)
+                                if (i0 + c0 + c < a.r)
+                                    pp[(c0 + c) * step] = x[c] - fmaf(move, __uint_as_float(v[c0 + c]), __fmul_rn(decay, x[c]));
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncthreads();                             // the planes and Y are read by all
+            } else {
+#pragma unroll
+                for (int c = 0; c < 32; ++c) y[(i0 + c) * kTcJ + j] = __uint_as_float(v[c]);
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    float x[1] = {__uint_as_float(v[c])};
+                    put_terms<1, 1>(planes, kXPlane, i0 + c, j, x);
+                }
+                fence_proxy_async();
+                tc_fence_before();
+                __syncthreads();
+            }
+        }
+        if constexpr (SINK != kParam) {
+            if (tid == 0) {
+                tc_fence_after();
+                auto gram = [&](uint32_t d, int ta, int tb, uint32_t first) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {            // 16 columns: 32 bytes, 64 a block
+                        const int off = (k >> 2) * (64 * 128);
+                        mma_bf16(d, sw128_desc(planes + ta * kXPlane + off) + 2 * (k & 3),
+                                 sw128_desc(planes + tb * kXPlane + off) + 2 * (k & 3), idesc, first | uint32_t(k > 0));
+                    }
+                };
+                const uint32_t add = done > 0 ? 1u : 0u;
+                gram(td1, 1, 1, add);
+                gram(td1, 0, 0, 1u);
+                gram(td2, 0, 2, add);
+                gram(td2, 0, 1, 1u);
+                mma_commit(&bar_g);
+            }
+        }
+    }
+    if constexpr (SINK != kParam) {
+        if (done > 0) mbar_wait(&bar_g, (done - 1) & 1, p.status, 42u);
+        tc_fence_after();
+        float *s1 = reinterpret_cast<float *>(planes), *s2 = s1 + 64 * 65;    // in the planes' place
+        if (q < 2) {
+            uint32_t v[32], w[32];
+            const uint32_t at = (uint32_t(q * 32) << 16) + uint32_t(half * 32);
+            tmem_ld32(td1 + at, v);
+            tmem_ld32(td2 + at, w);
+            tmem_wait_ld();
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+                s1[(q * 32 + lane) * 65 + half * 32 + c] = __uint_as_float(v[c]);
+                s2[(q * 32 + lane) * 65 + half * 32 + c] = __uint_as_float(w[c]);
+            }
+        }
+        tc_fence_before();
+        __syncthreads();
+        float *out = p.ws + a.part + int64_t(bl) * T::GSIZE;
+        for (int e = tid; e < T::GSIZE; e += NT) {
+            int i, k;
+            gram_place<64>(e, i, k);
+            out[e] = s1[i * 65 + k] + (s2[i * 65 + k] + s2[k * 65 + i]);
+        }
+    }
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 256);
+    }
+}
+
 // One matrix a block: G from its partial sums in block order, then M.
 template <int RP> constexpr int kPolyThreads = RP == 64 ? 512 : NT;   // 8 of 64 x 64 elements a thread: the products
                                                                     // are bound by latency
@@ -680,8 +994,10 @@ __global__ void __launch_bounds__(kPolyThreads<RP>) muon_poly_kernel(const __gri
 
 int rank_class(int64_t r) { return r <= 8 ? 8 : r <= 16 ? 16 : r <= 32 ? 32 : 64; }
 
+// Columns of a pass's tile, and a matrix's tiles.
+template <int RP> constexpr int pass_columns() { return RP == 64 ? kTcJ : Tile<RP>::JT; }
 template <int RP>
-int64_t tiles_of(int64_t n) { return ceil_div(n, Tile<RP>::JT); }
+int64_t tiles_of(int64_t n) { return ceil_div(n, pass_columns<RP>()); }
 
 // Column tiles a block takes: one, until that makes more than about 8 blocks an SM (fewer
 // partial Gram matrices then), 8 at most.
@@ -729,18 +1045,25 @@ size_t group_floats(const tlb_muon_mat *mats, const int *idx, int n) {
     size_t f = 0;
     for (int k = 0; k < n; ++k) {
         const int64_t tiles = tiles_of<RP>(std::max(mats[idx[k]].rows, mats[idx[k]].cols));
-        f += size_t(tiles) * (RP * Tile<RP>::JT + Tile<RP>::GSIZE) + size_t(RP) * RP;
+        f += size_t(tiles) * (RP * pass_columns<RP>() + Tile<RP>::GSIZE) + size_t(RP) * RP;
     }
     return f;
 }
 
 template <int RP, int SOURCE, int SINK>
 int pass(const Params &p, unsigned blocks, cudaStream_t st) {
-    constexpr int smem = pass_floats<RP>() * 4;
-    auto k = muon_pass_kernel<RP, SOURCE, SINK>;
-    TLB_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    k<<<blocks, NT, smem, st>>>(p);
-    return check_launch("muon_pass");
+    if constexpr (RP == 64) {
+        auto k = muon_tc_pass_kernel<SOURCE, SINK>;
+        TLB_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem));
+        k<<<blocks, NT, kTcSmem, st>>>(p);
+        return check_launch("muon_tc_pass");
+    } else {
+        constexpr int smem = pass_floats<RP>() * 4;
+        auto k = muon_pass_kernel<RP, SOURCE, SINK>;
+        TLB_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+        k<<<blocks, NT, smem, st>>>(p);
+        return check_launch("muon_pass");
+    }
 }
 
 template <int RP>
@@ -754,6 +1077,7 @@ int group(const tlb_muon_mat *mats, int *idx, int n, bool clusters, const tlb_mu
     p.tiles_per_block = tiles_per_block(tiles);
     p.nmat = n;
     p.ws = ws;
+    p.status = reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(ws) - kStatusBytes);
     p.mu = float(cfg.momentum);
     p.wd = float(cfg.weight_decay);
     p.nesterov = cfg.nesterov != 0;
@@ -783,7 +1107,7 @@ int group(const tlb_muon_mat *mats, int *idx, int n, bool clusters, const tlb_mu
             blocks += a.ctas;
         }
         a.y = off;
-        off += tiles_of<RP>(a.n) * RP * Tile<RP>::JT;
+        off += tiles_of<RP>(a.n) * RP * pass_columns<RP>();
         a.part = off;
         off += tiles_of<RP>(a.n) * Tile<RP>::GSIZE;
     }
