@@ -127,6 +127,7 @@ __device__ __forceinline__ void visit(const Mat &a, int j0, int jn, F f) {
     constexpr std::integral_constant<int, 8 * WARPS> k64{};
     constexpr std::integral_constant<int, 128> k128{};
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    if (jn <= 0) return;                                     // a CTA past the last column
     if (!a.tall && a.vec) {                                  // a warp a row, a lane four columns
         const int n = (jn / 4 - lane + 31) >> 5;             // jn % 4 == 0
 #pragma unroll 1
@@ -142,9 +143,12 @@ __device__ __forceinline__ void visit(const Mat &a, int j0, int jn, F f) {
 #pragma unroll 1
         for (int i = (lane & 3) * 4; i < a.r; i += 16)
             f(four, ld, int64_t(j0 + j) * a.r + i, 8 * WARPS * a.r, i * LD + j, k64, n);
-    } else {                                                 // a thread a column
+    } else {                                                 // a thread a column, or some of its rows
+        const int w = (jn + 31) & ~31, parts = max(1, NT / w), rows = (a.r + parts - 1) / parts;
+        const int i0 = parts > 1 ? int(threadIdx.x) / w * rows : 0, n = min(rows, a.r - i0);
 #pragma unroll 1
-        for (int j = threadIdx.x; j < jn; j += NT) f(one, ld, int64_t(j0 + j) * a.r, one, j, ld, a.r);
+        for (int j = parts > 1 ? int(threadIdx.x) % w : int(threadIdx.x); j < jn; j += NT)
+            f(one, ld, int64_t(j0 + j) * a.r + i0, one, i0 * LD + j, ld, n);
     }
 }
 
@@ -199,12 +203,11 @@ constexpr int kFlight = 4;               // pieces of a thread whose loads are i
 // The tile of u, from g and the momentum, which FIRST brings up to date.
 template <int RP, bool FIRST>
 __device__ __forceinline__ void load_update(const Params &p, const Mat &a, float *x, int j0, int jn) {
-    constexpr int U = kFlight;
     const float mu = p.mu;
     const bool nesterov = p.nesterov != 0;
     clear_rest<RP>(a, x, jn);
     visit<RP>(a, j0, jn, [&](auto cc, auto ss, int64_t e, auto de, int at, auto dat, int n) {
-        constexpr int C = decltype(cc)::value, S = decltype(ss)::value;
+        constexpr int C = decltype(cc)::value, S = decltype(ss)::value, U = kFlight;
         const float *gp = a.g + e;
         float *mp = a.m + e, *xp = x + at;
 #pragma unroll 1
@@ -238,10 +241,9 @@ __device__ __forceinline__ void load_update(const Params &p, const Mat &a, float
 // p moved along the tile.
 template <int RP>
 __device__ __forceinline__ void move_params(const Params &p, const Mat &a, const float *x, int j0, int jn) {
-    constexpr int U = kFlight;
     const float decay = a.lr * p.wd, move = a.lr_scale;
     visit<RP>(a, j0, jn, [&](auto cc, auto ss, int64_t e, auto de, int at, auto dat, int n) {
-        constexpr int C = decltype(cc)::value, S = decltype(ss)::value;
+        constexpr int C = decltype(cc)::value, S = decltype(ss)::value, U = kFlight;
         float *pp = a.p + e;
         const float *xp = x + at;
 #pragma unroll 1
@@ -389,9 +391,10 @@ __device__ __forceinline__ void gram_place(int e, int &i, int &k) {
 // The product of `steps` Newton-Schulz polynomials P of G, times `scale`, in mm.  gm: G
 // (symmetric; changed); sq, pm: scratch; all [RP][LM].  G and P are kept symmetric (the upper
 // triangle, mirrored), so that a row stands for a column.  r <= 16: one warp, without block
-// barriers, while the others wait; else all threads.
+// barriers, while the others wait; else all threads.  Then only the first kr rows and
+// columns (r rounded up to 8) are formed; mm is 0 outside.
 template <int RP, int PT = NT>
-__device__ __forceinline__ void polynomial(float *gm, float *sq, float *pm, float *mm, int steps, float a, float b, float c,
+__device__ __forceinline__ void polynomial(float *gm, float *sq, float *pm, float *mm, int steps, int kr, float a, float b, float c,
                                            float scale) {
     constexpr int LM = Tile<RP>::LM;
     constexpr bool WARP = RP <= 16;
@@ -399,7 +402,8 @@ __device__ __forceinline__ void polynomial(float *gm, float *sq, float *pm, floa
     constexpr int DC = RP == 64 ? 1024 / PT : RP == 8 ? 1 : 2, DR = RP == 64 || RP == 16 ? 4 : 2, W = RP / DC;
     static_assert(W * (RP / DR) <= (WARP ? 32 : PT), "threads of a product");
     const int tid = threadIdx.x, r0 = (tid / W) * DR, c0 = (tid % W) * DC;
-    const bool on = r0 < RP;
+    if constexpr (WARP) kr = RP;                             // unrolled whole
+    const bool on = r0 < kr && c0 < kr;
     auto sync = [] {
         if constexpr (WARP) __syncwarp();
         else __syncthreads();
@@ -415,8 +419,11 @@ __device__ __forceinline__ void polynomial(float *gm, float *sq, float *pm, floa
             for (int t = 0; t < DC; ++t) acc[s][t] = 0.f;
         const bool mine = on && (KIND == PLAIN || r0 < c0 + DC);
         if (mine) {
-#pragma unroll 16
-            for (int k = 0; k < RP; ++k) {
+            constexpr int KU = WARP ? RP : 8;
+#pragma unroll 1
+            for (int k0 = 0; k0 < kr; k0 += KU)
+#pragma unroll
+            for (int k = k0; k < k0 + KU; ++k) {
                 float u[DR], v[DC];
                 if constexpr (DR == 4) {
                     const float4 q = *reinterpret_cast<const float4 *>(x + k * LM + r0);
@@ -463,6 +470,8 @@ __device__ __forceinline__ void polynomial(float *gm, float *sq, float *pm, floa
     constexpr std::integral_constant<int, PLAIN> plain{};
     constexpr std::integral_constant<int, SYM> sym{};
     constexpr std::integral_constant<int, POLY> poly{};
+    for (int e = threadIdx.x; e < RP * LM; e += PT) mm[e] = 0.f;
+    __syncthreads();
     if (!WARP || tid < 32) {
         for (int s = 0; s < steps; ++s) {
             product(gm, gm, pm, poly);
@@ -506,6 +515,13 @@ __device__ __forceinline__ float normalise(float *gm, float *s_inv, float eps) {
     return inv;
 }
 
+// Every thread of the cluster meets here.  The cluster's barrier wants whole warps, whose
+// threads come apart in the loops over ragged tiles: the block's barrier brings them together.
+__device__ __forceinline__ void cluster_meet() {
+    __syncthreads();
+    cluster_sync();
+}
+
 __device__ __forceinline__ float ld_cluster(const float *p, int rank) {
     float v;
     asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr(p, uint32_t(rank))) : "memory");
@@ -542,8 +558,8 @@ __global__ void __launch_bounds__(NT, RP <= 16 ? 4 : 1) muon_cluster_kernel(cons
     const Mat &a = p.mat[lo];
     const int rank = int(blockIdx.x) - a.block0, ctas = a.ctas;
     if (rank >= ctas) {
-        for (int done = 0; done < p.steps; done += done == 0 ? kFirstRun : kRun) cluster_sync();
-        cluster_sync();
+        for (int done = 0; done < p.steps; done += done == 0 ? kFirstRun : kRun) cluster_meet();
+        cluster_meet();
         return;
     }
     const int peer0 = int(cluster_rank()) - rank;
@@ -560,7 +576,7 @@ __global__ void __launch_bounds__(NT, RP <= 16 ? 4 : 1) muon_cluster_kernel(cons
             gram_sum<RP>(acc, red, s);
             gram_keep<RP>(s, mine);
         }
-        cluster_sync();
+        cluster_meet();
         for (int e = threadIdx.x; e < T::GSIZE; e += NT) {
             float v[kCluster], s = 0.f;
 #pragma unroll
@@ -575,13 +591,13 @@ __global__ void __launch_bounds__(NT, RP <= 16 ? 4 : 1) muon_cluster_kernel(cons
         __syncthreads();
         if (run == 0) scale = normalise<RP>(gm, &s_inv, p.eps);
         const int steps = min(run == 0 ? kFirstRun : kRun, p.steps - done);
-        polynomial<RP>(gm, sq, pm, mm, steps, p.a, p.b, p.c, run == 0 ? scale : 1.f);
+        polynomial<RP>(gm, sq, pm, mm, steps, (a.r + 7) & ~7, p.a, p.b, p.c, run == 0 ? scale : 1.f);
         done += steps;
         apply<RP>(x, mm, jn);
     }
     __syncthreads();
     move_params<RP>(p, a, x, j0, jn);
-    cluster_sync();                                          // peers have read the last partial sums
+    cluster_meet();                                          // peers have read the last partial sums
 }
 
 // ---------------------------------------------------------------- passes over longer matrices
@@ -656,11 +672,15 @@ __global__ void __launch_bounds__(NT) muon_pass_kernel(const __grid_constant__ P
 // first product and a K-major one for the second.
 constexpr int kTcJ = 128;                                   // columns of a tile
 constexpr int kXPlane = 64 * kTcJ * 2, kMPlane = 64 * 64 * 2;
-// 3 planes of X and of M; the rest keeps a third CTA off the SM (tensor memory: two of 256
-// columns).  An MMA of G reads 128 rows: 64 of a block and the 64 rows behind it, whose
-// results are not looked at; behind the last block of X lies M.
-constexpr int kTcSmem = 84 * 1024;
-static_assert(3 * kXPlane + 3 * kMPlane + 1024 <= kTcSmem, "shared memory of the planes");
+// Shared memory: 3 planes of X, then 3 of M.  An MMA of G reads 128 rows: 64 of a block and the
+// 64 rows behind it, whose results are not looked at, so 8 KB have to lie behind X's last
+// block.  Tensor memory: 64 columns each for Y, D1 and D2.  Three CTAs an SM (registers), two
+// of the pass that has all of it.
+template <int SOURCE, int SINK> constexpr int tc_smem() {
+    return 1024 + 3 * kXPlane + (SOURCE == kMomentum ? 64 * 128 : SINK == kParam ? 3 * kMPlane : 84 * 1024 - 1024 - 3 * kXPlane);
+}
+template <int SOURCE, int SINK> constexpr int tc_columns() { return SINK == kParam ? 64 : SOURCE == kMomentum ? 128 : 256; }
+template <int SOURCE, int SINK> constexpr int tc_ctas() { return SOURCE == kMomentum || SINK == kParam ? 3 : 2; }
 
 // Byte offset of element (i, j) in a plane of X (blocks of 64 columns), or of M with j < 64.
 __device__ __forceinline__ int plane_at(int i, int j) {
@@ -766,7 +786,7 @@ __device__ __forceinline__ void tc_load_update(const Params &p, const Mat &a, ui
 }
 
 template <int SOURCE, int SINK>
-__global__ void __launch_bounds__(NT, 2) muon_tc_pass_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(NT, tc_ctas<SOURCE, SINK>()) muon_tc_pass_kernel(const __grid_constant__ Params p) {
     using T = Tile<64>;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *planes = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -784,7 +804,7 @@ __global__ void __launch_bounds__(NT, 2) muon_tc_pass_kernel(const __grid_consta
     const int bl = blockIdx.x - a.block0, t0 = bl * p.tiles_per_block;
     const int t1 = min((a.n + kTcJ - 1) / kTcJ, t0 + p.tiles_per_block);
     if (warp == 0) {
-        tmem_alloc(&tmem_base, 256);
+        tmem_alloc(&tmem_base, tc_columns<SOURCE, SINK>());
         tmem_relinquish();
     }
     if (tid == 0) {
@@ -807,7 +827,7 @@ __global__ void __launch_bounds__(NT, 2) muon_tc_pass_kernel(const __grid_consta
     }
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_base, ty = tmem, td1 = tmem + 64, td2 = tmem + 128;
+    const uint32_t tmem = tmem_base, td1 = tmem, td2 = tmem + 64, ty = SINK == kParam ? tmem : tmem + 128;
     // D f32, A and B bf16, 128 x 64; A MN-major for Y
     constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(64 >> 3) << 17) | (uint32_t(128 >> 4) << 24);
     const int q = warp & 3, half = warp >> 2;               // TMEM lanes (columns of X), half of the rows
@@ -854,39 +874,44 @@ __global__ void __launch_bounds__(NT, 2) muon_tc_pass_kernel(const __grid_consta
                     }
                 mma_commit(&bar_y);
             }
+            // this thread's column j of X, rows i0 ..; p is fetched while the product runs
+            const int j = q * 32 + lane, i0 = half * 32;
+            const int64_t step = a.tall ? 1 : a.n;
+            float *pp = a.tall ? a.p + int64_t(j0 + j) * a.r + i0 : a.p + int64_t(i0) * a.n + j0 + j;
+            const bool quads = a.tall && a.vec;
+            const int rows = j < jn ? a.r - i0 : 0;
+            float x[SINK == kParam ? 32 : 1];
+            if constexpr (SINK == kParam) {
+#pragma unroll
+                for (int c = 0; c < 32; c += 4) {
+                    float *x4 = x + c;
+                    if (quads) {
+                        const float4 t = c < rows ? *reinterpret_cast<const float4 *>(pp + c) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        x4[0] = t.x; x4[1] = t.y; x4[2] = t.z; x4[3] = t.w;
+                    } else {
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) x4[d] = c + d < rows ? pp[(c + d) * step] : 0.f;
+                    }
+                }
+            }
             mbar_wait(&bar_y, done & 1, p.status, 41u);
+            __syncwarp();                                    // tensor memory is read by whole warps
             tc_fence_after();
             uint32_t v[32];
             tmem_ld32(ty + (uint32_t(q * 32) << 16) + uint32_t(half * 32), v);
             tmem_wait_ld();
-            const int j = q * 32 + lane, i0 = half * 32;
             if constexpr (SINK == kParam) {
                 const float decay = a.lr * p.wd, move = a.lr_scale;
-                if (j < jn) {
-                    if (a.tall && a.vec) {
-                        float *pp = a.p + int64_t(j0 + j) * a.r + i0;
 #pragma unroll
-                        for (int c = 0; c < 32; c += 4) {
-                            if (i0 + c >= a.r) continue;
-                            float x[4];
-                            load_piece<4>(pp + c, x);
+                for (int c = 0; c < 32; ++c) x[c] -= fmaf(move, __uint_as_float(v[c]), __fmul_rn(decay, x[c]));
 #pragma unroll
-                            for (int d = 0; d < 4; ++d) x[d] -= fmaf(move, __uint_as_float(v[c + d]), __fmul_rn(decay, x[d]));
-                            keep_piece<4>(pp + c, x);
-                        }
+                for (int c = 0; c < 32; c += 4) {
+                    if (quads) {
+                        if (c < rows) *reinterpret_cast<float4 *>(pp + c) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
                     } else {
-                        const int64_t step = a.tall ? 1 : a.n;
-                        float *pp = a.tall ? a.p + int64_t(j0 + j) * a.r + i0 : a.p + int64_t(i0) * a.n + j0 + j;
 #pragma unroll
-                        for (int c0 = 0; c0 < 32; c0 += 8) {
-                            float x[8];
-#pragma unroll
-                            for (int c = 0; c < 8; ++c) x[c] = i0 + c0 + c < a.r ? pp[(c0 + c) * step] : 0.f;
-#pragma unroll
-                            for (int c = 0; c < 8; ++c)
-                                if (i0 + c0 + c < a.r)
-                                    pp[(c0 + c) * step] = x[c] - fmaf(move, __uint_as_float(v[c0 + c]), __fmul_rn(decay, x[c]));
-                        }
+                        for (int d = 0; d < 4; ++d)
+                            if (c + d < rows) pp[(c + d) * step] = x[c + d];
                     }
                 }
                 tc_fence_before();
@@ -926,6 +951,7 @@ __global__ void __launch_bounds__(NT, 2) muon_tc_pass_kernel(const __grid_consta
     }
     if constexpr (SINK != kParam) {
         if (done > 0) mbar_wait(&bar_g, (done - 1) & 1, p.status, 42u);
+        __syncwarp();
         tc_fence_after();
         float *s1 = reinterpret_cast<float *>(planes), *s2 = s1 + 64 * 65;    // in the planes' place
         if (q < 2) {
@@ -952,7 +978,7 @@ __global__ void __launch_bounds__(NT, 2) muon_tc_pass_kernel(const __grid_consta
     __syncthreads();
     if (warp == 0) {
         tc_fence_after();
-        tmem_dealloc(tmem, 256);
+        tmem_dealloc(tmem, tc_columns<SOURCE, SINK>());
     }
 }
 
@@ -969,23 +995,35 @@ __global__ void __launch_bounds__(kPolyThreads<RP>) muon_poly_kernel(const __gri
     const Mat &a = p.mat[blockIdx.x];
     const float *part = p.ws + a.part;
     const int nb = a.ctas;
-    for (int e = threadIdx.x; e < T::GSIZE; e += PT) {
-        float s = 0.f;
-        for (int k = 0; k < nb; k += 8) {
-            float v[8];
+    constexpr int OWN = (T::GSIZE + PT - 1) / PT, U = 6;     // U blocks of all own elements in flight
+    float g[OWN] = {};
+    for (int k = 0; k < nb; k += U) {
+        float v[U][OWN];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) v[u] = k + u < nb ? part[int64_t(k + u) * T::GSIZE + e] : 0.f;
+        for (int u = 0; u < U; ++u)
 #pragma unroll
-            for (int u = 0; u < 8; ++u) s += v[u];
+            for (int o = 0; o < OWN; ++o) {
+                const int e = threadIdx.x + o * PT;
+                v[u][o] = k + u < nb && e < T::GSIZE ? part[int64_t(k + u) * T::GSIZE + e] : 0.f;
+            }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int o = 0; o < OWN; ++o) g[o] += v[u][o];
+    }
+#pragma unroll
+    for (int o = 0; o < OWN; ++o) {
+        const int e = threadIdx.x + o * PT;
+        if (e < T::GSIZE) {
+            int i, k;
+            gram_place<RP>(e, i, k);
+            gm[i * LM + k] = g[o];
+            gm[k * LM + i] = g[o];
         }
-        int i, k;
-        gram_place<RP>(e, i, k);
-        gm[i * LM + k] = s;
-        gm[k * LM + i] = s;
     }
     __syncthreads();
     const float scale = done == 0 ? normalise<RP, PT>(gm, &s_inv, p.eps) : 1.f;
-    polynomial<RP, PT>(gm, sq, pm, mm, steps, p.a, p.b, p.c, scale);
+    polynomial<RP, PT>(gm, sq, pm, mm, steps, (a.r + 7) & ~7, p.a, p.b, p.c, scale);
     float *out = p.ws + p.mpoly + int64_t(blockIdx.x) * RP * RP;
     for (int e = threadIdx.x; e < RP * RP; e += PT) out[e] = mm[(e / RP) * LM + e % RP];
 }
@@ -1054,8 +1092,9 @@ template <int RP, int SOURCE, int SINK>
 int pass(const Params &p, unsigned blocks, cudaStream_t st) {
     if constexpr (RP == 64) {
         auto k = muon_tc_pass_kernel<SOURCE, SINK>;
-        TLB_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem));
-        k<<<blocks, NT, kTcSmem, st>>>(p);
+        constexpr int smem = tc_smem<SOURCE, SINK>();
+        TLB_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+        k<<<blocks, NT, smem, st>>>(p);
         return check_launch("muon_tc_pass");
     } else {
         constexpr int smem = pass_floats<RP>() * 4;

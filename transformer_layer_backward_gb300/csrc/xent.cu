@@ -529,6 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
                     ok = false;
                     break;
                 }
+                __syncwarp();                                 // tensor memory is read by whole warps
                 tc_fence_after();
                 const uint32_t tm = tmem + uint32_t(b * BN + half * (BN / 2)) + (uint32_t(q * 32) << 16);
                 if constexpr (FINE) {
@@ -553,6 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
                             for (int c = 0; c < 32; ++c) z[j * 32 + c] = __uint_as_float(v[c]);
                         }
                         block(z, c0);
+                        __syncwarp();
                     }
                 }
                 tc_fence_before();                            // the accumulator is free again
