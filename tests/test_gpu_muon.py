@@ -181,6 +181,9 @@ def test_muon_refusals(lib):
     with pytest.raises(ValueError, match="twice"):
         a = z(4, 4)
         lib.muon_mats([a, a], [z(4, 4), z(4, 4)], [z(4, 4), z(4, 4)])
+    with pytest.raises(ValueError, match="also a param"):
+        a = z(4, 4)
+        lib.muon_mats([a], [a], [z(4, 4)])
     with pytest.raises(ValueError, match="length"):
         lib.muon_mats([z(4, 4)], [], [z(4, 4)])
     with pytest.raises(ValueError, match="one shape"):

@@ -163,8 +163,8 @@ def muon_cfg(lr, momentum=0.95, weight_decay=0.0, eps=1e-7, coefficients=(3.4445
 def muon_mats(params, grads, momenta, lr_mults=None, scales=None):
     """The matrices of a Muon step, for muon() and muon_workspace(): equally long lists of
     float32 matrices [rows, cols], min(rows, cols) <= 64.  lr_mults (1) multiply the learning
-    rate, scales (sqrt(max(1, rows / cols))) the orthogonal update.  Holds device pointers:
-    the tensors must stay alive and where they are while it is used."""
+    rate, scales (sqrt(max(1, rows / cols))) the orthogonal update.  Holds the tensors,
+    whose memory must stay where it is (a gradient is written into, not replaced)."""
     n = len(params)
     if not (len(grads) == len(momenta) == n and (lr_mults is None or len(lr_mults) == n)
             and (scales is None or len(scales) == n)):
@@ -182,7 +182,10 @@ def muon_mats(params, grads, momenta, lr_mults=None, scales=None):
     written = [q for mat in mats[:n] for q in (mat.p, mat.m) if q]
     if len(set(written)) != len(written):
         raise ValueError("muon_mats: the same tensor twice")
+    if set(written) & {mat.g for mat in mats[:n] if mat.g}:
+        raise ValueError("muon_mats: a gradient that is also a param or momentum")
     mats.n, mats.device = n, params[0].device if n else None
+    mats.tensors = list(params), list(grads), list(momenta)
     return mats
 
 
@@ -195,6 +198,8 @@ def muon_workspace(mats, device="cuda"):
 def muon(mats, cfg: A.MuonCfg, ws, stream=None):
     """One Muon step in place on the params and momenta of muon_mats(): momentum, the update
     made orthogonal by Newton-Schulz steps, weight decay.  The counterpart of adamw()."""
+    if mats.device is not None and ws.device != mats.device:
+        raise ValueError("ws is on %s, the matrices on %s" % (ws.device, mats.device))
     with _on_device(ws):
         A.call("tlb_muon", mats, mats.n, C.byref(cfg), _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream))
 
@@ -210,7 +215,7 @@ def _xent_code(dtype, name):
     return _XENT_CODE[dtype]
 
 
-def _xent_shapes(hidden, W, targets, **per_row):
+def _xent_shapes(hidden, W, targets, ws, **per_row):
     if hidden.dim() != 2 or W.dim() != 2 or hidden.shape[1] != W.shape[1]:
         raise ValueError("hidden [rows, dim] and W [vocab, dim] expected, got %s and %s"
                          % (tuple(hidden.shape), tuple(W.shape)))
@@ -218,7 +223,7 @@ def _xent_shapes(hidden, W, targets, **per_row):
     for name, t in dict(per_row, targets=targets).items():
         if t is not None and tuple(t.shape) != (rows,):
             raise ValueError("%s must have shape (%d,), got %s" % (name, rows, tuple(t.shape)))
-    for name, t in dict(per_row, W=W, targets=targets).items():
+    for name, t in dict(per_row, W=W, targets=targets, ws=ws).items():
         if t is not None and t.device != hidden.device:
             raise ValueError("%s is on %s, hidden on %s" % (name, t.device, hidden.device))
     return rows, W.shape[0], W.shape[1]
@@ -235,7 +240,7 @@ def xent_workspace(hidden_dtype, weight_dtype, rows, vocab, dim, grad_w=False, d
 def xent_forward(hidden, W, targets, loss=None, lse=None, ws=None, stream=None):
     """Per-row cross entropy of the linear head W [vocab, dim] on hidden [rows, dim], without
     the logits: (loss, lse).  Targets (int64) outside [0, vocab) mark rows without one."""
-    rows, vocab, dim = _xent_shapes(hidden, W, targets, loss=loss, lse=lse)
+    rows, vocab, dim = _xent_shapes(hidden, W, targets, ws, loss=loss, lse=lse)
     ht, wt = _xent_code(hidden.dtype, "hidden"), _xent_code(W.dtype, "W")
     loss = torch.empty(rows, device=hidden.device) if loss is None else loss
     lse = torch.empty(rows, device=hidden.device) if lse is None else lse
@@ -250,7 +255,7 @@ def xent_forward(hidden, W, targets, loss=None, lse=None, ws=None, stream=None):
 def xent_backward(hidden, W, targets, lse, d_loss, d_hidden=None, d_w=None, grad_w=False, ws=None, stream=None):
     """Gradient of sum(d_loss * loss): (d_hidden, d_w), in hidden's dtype; d_w [vocab, dim] is
     None unless grad_w is set or a tensor for it is given.  lse as xent_forward returned it."""
-    rows, vocab, dim = _xent_shapes(hidden, W, targets, lse=lse, d_loss=d_loss)
+    rows, vocab, dim = _xent_shapes(hidden, W, targets, ws, lse=lse, d_loss=d_loss)
     ht, wt = _xent_code(hidden.dtype, "hidden"), _xent_code(W.dtype, "W")
     d_hidden = torch.empty_like(hidden) if d_hidden is None else d_hidden
     if d_w is None and grad_w:

@@ -171,19 +171,14 @@ __device__ __forceinline__ void stats_row(const XParams &p, float (&z)[BN / 2], 
     }
 }
 
-// kGrad: what dz needs of this thread's row.
+// kGrad: what dz needs of this thread's row; fetched a tile ahead.
 struct GradRow {
+    int64_t t;
     float lse, g;
-    bool has;
-    int tc;                                                // the target's column in this piece, or -1
 };
 __device__ __forceinline__ GradRow grad_row(const XParams &p, int row) {
-    const int64_t t = row < p.M ? p.targets[row] : -1;
-    GradRow r;
-    r.has = t >= 0 && t < p.vocab;
-    r.tc = (r.has && t >= p.v0 && t < p.v0 + p.N) ? int(t - p.v0) : -1;
-    r.lse = r.has ? p.lse[row] : 0.f;
-    r.g = r.has ? p.dloss[row] : 0.f;
+    GradRow r{-1, 0.f, 0.f};
+    if (row < p.M) r = GradRow{p.targets[row], p.lse[row], p.dloss[row]};
     return r;
 }
 
@@ -194,15 +189,19 @@ template <int TERMS>
 __device__ __forceinline__ void grad_box(const XParams &p, const GradRow &r, float *y, int row0, int col0, uint8_t *box,
                                          int lane) {
     if (row0 >= p.M || col0 >= p.N) return;
+    const bool has = r.t >= 0 && r.t < p.vocab;
 #pragma unroll
     for (int c = 0; c < 64; ++c) y[c] = ex2((y[c] - r.lse) * kLog2e);
-    if (unsigned(r.tc - col0) < 64u && r.tc >= 0) {
+    const int64_t tc = has ? r.t - p.v0 - col0 : -1;       // the target's column in this box
+    if (tc >= 0 && tc < min(64, p.N - col0)) {
+        int k = int(tc);
+        asm("" : "+r"(k));                                 // compared, never an index: y stays in registers
 #pragma unroll
         for (int c = 0; c < 64; ++c)
-            if (c == r.tc - col0) y[c] -= 1.f;
+            if (c == k) y[c] -= 1.f;
     }
 #pragma unroll
-    for (int c = 0; c < 64; ++c) y[c] = r.has ? y[c] * r.g : 0.f;
+    for (int c = 0; c < 64; ++c) y[c] = has ? y[c] * r.g : 0.f;
 #pragma unroll
     for (int k = 0; k < TERMS; ++k) {
         if (lane == 0) bulk_wait_read();                   // the box's last store has read it
@@ -507,16 +506,26 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
         float *blk = reinterpret_cast<float *>(buf) + (warp - 2) * 32 * 33;            // kOut
         int f = 0, at = b0;
         bool ok = true;
-        Seg sg;
-        for (int i = 0; ok && next_seg(i, at, sg); ++i) {
-            int m0, n0, tn;
-            place(sg.tile, m0, n0, tn);
-            const int row0 = m0 + q * 32, colh = n0 + half * (BN / 2);
+        Seg sg, next;
+        bool more = next_seg(0, at, next);
+        int m0 = 0, n0 = 0, tn = 0;
+        GradRow grn{-1, 0.f, 0.f};
+        if (more) {
+            place(next.tile, m0, n0, tn);
+            if constexpr (MODE == kGrad) grn = grad_row(p, m0 + q * 32 + lane);
+        }
+        for (int i = 0; ok && more; ++i) {
+            sg = next;
+            const int row0 = m0 + q * 32, colh = n0 + half * (BN / 2), tile_n = tn;
+            const GradRow gr = grn;
+            more = next_seg(i + 1, at, next);
+            if (more) {
+                place(next.tile, m0, n0, tn);
+                if constexpr (MODE == kGrad) grn = grad_row(p, m0 + q * 32 + lane);
+            }
             float *part = nullptr;                            // kOut: this warp's part of a partial tile
             if (MODE == kOut && (sg.kb0 != 0 || sg.kb1 != KB))
                 part = p.partial + ((int64_t(blockIdx.x) * 2 + sg.slot) * kBM + q * 32) * BN + half * (BN / 2);
-            GradRow gr;
-            if constexpr (MODE == kGrad) gr = grad_row(p, row0 + lane);
             float z[ZN];                                      // this thread's row
             auto block = [&](float *y, int c0) {              // WN columns from colh + c0
                 if constexpr (MODE == kGrad) grad_box<TERMS>(p, gr, y, row0, colh + c0, box, lane);
@@ -545,14 +554,12 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
                 } else {
 #pragma unroll 1
                     for (int c0 = 0; c0 < BN / 2; c0 += WN) {
+                        uint32_t v[WN / 32][32];
 #pragma unroll
-                        for (int j = 0; j < WN / 32; ++j) {
-                            uint32_t v[32];
-                            tmem_ld32(tm + uint32_t(c0 + j * 32), v);
-                            tmem_wait_ld();
+                        for (int j = 0; j < WN / 32; ++j) tmem_ld32(tm + uint32_t(c0 + j * 32), v[j]);
+                        tmem_wait_ld();
 #pragma unroll
-                            for (int c = 0; c < 32; ++c) z[j * 32 + c] = __uint_as_float(v[c]);
-                        }
+                        for (int c = 0; c < WN; ++c) z[c] = __uint_as_float(v[c / 32][c % 32]);
                         block(z, c0);
                         __syncwarp();
                     }
@@ -566,7 +573,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
             }
             if (!ok) break;
             if constexpr (MODE == kStats) {
-                stats_row<BN>(p, z, row0 + lane, colh, 2 * tn + half);
+                stats_row<BN>(p, z, row0 + lane, colh, 2 * tile_n + half);
             } else if constexpr (FINE) {
 #pragma unroll
                 for (int c0 = 0; c0 < BN / 2; c0 += WN) block(z + c0, c0);
