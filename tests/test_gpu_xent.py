@@ -94,15 +94,47 @@ def test_xent(lib, rows, vocab, dim, types):
 @pytest.mark.parametrize("types", TYPES, ids="-".join)
 @pytest.mark.parametrize("rows,vocab,dim", [(1, 1, 2), (1, 9, 6000), (1, 30011, 1026), (2, 8, 64), (2, 1237, 2560),
                                             (3, 1000, 320), (3, 5, 2), (4, 4099, 2560), (4, 12, 1022), (4, 300, 3074),
-                                            (5, 2000, 2560)])
+                                            (5, 2000, 2560), (1, 50, 1001), (1, 700, 2085), (2, 1003, 333), (4, 77, 5),
+                                            (3, 2001, 1999), (4, 900, 511), (6, 1500, 513), (9, 500, 1216), (16, 3001, 130),
+                                            (15, 600, 1025), (17, 400, 130), (12, 999, 3073)])
 def test_few_rows(lib, rows, vocab, dim, types):
-    """Up to four rows of an even length take the one-pass kernel; a block of head rows that is
-    not full, one longer than the registers hold, and five rows beside it."""
+    """Up to four rows take the one-pass kernel, up to sixteen take it in turns where the head
+    would have to be packed (float32, odd lengths); blocks of head rows that are not full,
+    lengths past what the registers hold, and one row more beside them."""
     n0 = lib.launch_count()
     test_xent(lib, rows, vocab, dim, types)
     names = lib.launch_names(n0)
-    one_pass = rows <= 4 and (rows == 1 or dim < 3073)
-    assert ("xent_token_loss" in names and "xent_token_grad" in names) == one_pass, names
+    fits = dim <= (6144 if rows == 1 else 1024 * 3)
+    packed = types[1] == "f32" or dim % 8 != 0
+    assert ("xent_token_loss" in names) == (fits and rows <= (16 if packed else 4)), names
+    if types[0] == "bf16" and rows > 4:                      # d_w of several turns is summed in float32 only
+        assert "xent_dw" in names
+
+
+@pytest.mark.parametrize("types", TYPES, ids="-".join)
+@pytest.mark.parametrize("rows,dim", [(1, 512), (3, 511), (40, 512), (200, 264)])
+def test_confident_rows(lib, rows, dim, types):
+    """Targets of probability 1 - 1e-3 and nearer: p - 1 and the loss are small differences of
+    large numbers.  lse carries half a step of its own, 2^-24 x 16 = 1e-6, so 1 - p of 1e-3 is
+    known to 1e-3 at best: the gradient is compared for the lse that it is given, where expm1
+    leaves the target's logit: sums of 512 products in fp32, at most 2^-22 of |h| |w| = 20 in
+    the terms' absolute sum, 5e-6 of p, 5e-3 of 1 - p = 1e-3."""
+    import torch
+    vocab = 900
+    th, tw, h, w, t, g = problem(rows, vocab, dim, types)
+    t[:] = np.arange(rows) % vocab
+    h = h * 0.1
+    h += w[t] / np.sum(w[t] ** 2, 1, keepdims=True) * 15.0     # the target's logit near 15, the others' near 0
+    th = dev(h.astype(np.float32), types[0])
+    h, tt = host(th), torch.from_numpy(t).cuda()
+    rlse = ops.xent_forward(h, w, t)[1].astype(np.float32)
+    loss, lse = lib.xent_forward(th, tw, tt)
+    # half a step of lse and of the logit, 2^-24 x 16 each, and the sum's 5e-6
+    assert np.max(np.abs(host(loss) - ops.xent_forward(h, w, t)[0])) <= 1e-5
+    dh, _ = lib.xent_backward(th, tw, tt, dev(rlse), dev(g))
+    rdh, _ = ops.xent_backward(h, w, t, host(dev(rlse)), g)
+    rel, _ = errors(host(dh), rdh)
+    assert rel <= (5e-3 if types[0] == "f32" else 1e-2), rel
 
 
 @pytest.mark.parametrize("types,rows,vocab,dim", [(("f32", "bf16"), 2048, 50001, 64),     # pieces of dz

@@ -73,10 +73,10 @@ bool xent_token_supported(int64_t N, int64_t D);
 // (max, sum) pairs of every row in *slots slots of part [slot][ld_part], and the targets' logits.
 int xent_token_loss(int htype, const void *hidden, int wtype, const void *W, const int64_t *targets, int64_t N, int64_t V,
                     int64_t D, float2 *part, int64_t ld_part, float *zt, uint32_t *status, int *slots, cudaStream_t st);
-// partial: N D floats for every slot, two an SM at most.
+// partial: N (D + 1) floats for every slot, four an SM at most.  dw_add (float32): d_w += .
 int xent_token_grad(int htype, const void *hidden, int wtype, const void *W, const int64_t *targets, const float *lse,
                     const float *d_loss, int64_t N, int64_t V, int64_t D, void *d_hidden, void *d_w, float *partial,
-                    uint32_t *status, cudaStream_t st);
+                    uint32_t *status, bool dw_add, cudaStream_t st);
 
 // Attention backward from dCtx to dQ(pre) and dV (attention.cu).
 struct AttnArgs {

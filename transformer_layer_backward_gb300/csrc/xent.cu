@@ -7,9 +7,8 @@
 //
 // Every product runs on one tcgen05 kernel.  Its modes differ in what becomes of an
 // accumulator tile (rows x columns of z or of a gradient):
-//   kStats  running maximum and sum of exponentials of each row over the tile's columns, and
-//           the target's logit; the logits never leave tensor memory.  A second kernel joins
-//           the tiles' pairs in column order.
+//   kStats  maximum and sum of exponentials of each row over the tile's columns; the logits
+//           never leave tensor memory.  A second kernel joins the tiles' pairs in a fixed order.
 //   kGrad   dz of the tile, rounded to bf16, by TMA into a piece of the vocabulary's dz
 //           [N, piece] in the workspace
 //   kOut    d_hidden (+)= dz W over one piece, or d_w of the piece: fp32 sums, stream-K
@@ -28,6 +27,13 @@
 // precision are therefore summed in chunks of a few k blocks, which the epilogue adds up in
 // registers.  The term products of a k block follow one another, so that its operand tiles
 // come from memory once and from L2 then.
+//
+// The logit of a row's own target decides how exact the loss and p - 1 of a confident row are
+// (1 - p may be 1e-3 of p): a kernel of its own sums it in fp32 on the CUDA cores, and both
+// epilogues put it in the place of the accumulator's.
+//
+// Up to 64 bf16 rows give too few roundings of dz to even out (one row's largest dz alone sets
+// its error), and the read of W hides a second product: dz is kept in two terms there.
 //
 // Bounds: N >= 512 rows is bound by the tensor pipe (2 N V D flops a product), few rows by
 // the read of W.
@@ -50,9 +56,9 @@ constexpr int kThreads = 320;               // 10 warps: TMA producer, MMA issue
 constexpr int kEpiWarps = 8;                // two per 32 TMEM lanes (rows), each half of the columns
 constexpr int kMaxTerms = 3, kMaxProd = 6;
 // k blocks (4 MMAs each) of one tensor-memory sum of a float32 result.  Reading a sum out takes
-// the tensor pipe about 300 cycles, and its error grows with its length: the loss of 2048 x
-// 2560 x 131072 is 3.7e-7 off at 8 k blocks (812 us), 9e-7 at 20 (787 us).
-constexpr int kChunkLoss = 14, kChunkTerms = 8, kChunkGrad = 10;   // loss of bf16, of float32 terms; gradient
+// the tensor pipe about 300 cycles (the loss of 2048 x 2560 x 131072: 812 us at 8 k blocks, 787
+// at 20), and its error grows with its length.
+constexpr int kChunkLoss = 20, kChunkGrad = 10;
 constexpr int kGroupM = 16;                 // row tiles that share a column tile before the next one
 constexpr int kBox = 4096;                  // bytes of a 32 x 64 bf16 box of dz
 constexpr float kLog2e = 1.4426950408889634f;
@@ -76,7 +82,7 @@ struct XParams {
     int64_t vocab, v0;                       // columns in all, first column of this piece
     float2 *part;                            // kStats: (max, sum) [slot0 + 2 tile_n + half][ld_part]
     int64_t ld_part;
-    float *zt;                               // kStats: logit of the target
+    const float *zt;                         // logit of each row's target, from xent_target_kernel
     const float *lse, *dloss;                // kGrad
     // kOut
     const float *acc;                        // sum of the earlier pieces [M, N], or null
@@ -144,7 +150,7 @@ __device__ __forceinline__ uint32_t next_term(float &x) {
 
 // Columns [col0, col0 + BN / 2) of this thread's row, in registers: z[j] is column col0 + j.
 
-// kStats: running maximum and sum of exponentials, and the target's logit.
+// kStats: maximum and sum of exponentials, with the target's logit as p.zt has it.
 template <int BN>
 __device__ __forceinline__ void stats_row(const XParams &p, float (&z)[BN / 2], int row, int col0, int slot) {
     const int64_t t = row < p.M ? p.targets[row] : -1;
@@ -153,6 +159,14 @@ __device__ __forceinline__ void stats_row(const XParams &p, float (&z)[BN / 2], 
 #pragma unroll
         for (int c = 0; c < BN / 2; ++c)
             if (col0 + c >= p.N) z[c] = -INFINITY;
+    }
+    if (tc >= 0 && tc < BN / 2) {
+        const float zt = p.zt[row];
+        int k = tc;
+        asm("" : "+r"(k));                                 // compared, never an index: z stays in registers
+#pragma unroll
+        for (int c = 0; c < BN / 2; ++c)
+            if (c == k) z[c] = zt;
     }
     float m[4] = {z[0], z[1], z[2], z[3]};
 #pragma unroll
@@ -164,21 +178,16 @@ __device__ __forceinline__ void stats_row(const XParams &p, float (&z)[BN / 2], 
 #pragma unroll
     for (int c = 0; c < BN / 2; ++c) sum[c & 3] += ex2(fmaf(z[c], kLog2e, -ref));
     if (row < p.M) p.part[int64_t(slot) * p.ld_part + row] = make_float2(mx, (sum[0] + sum[1]) + (sum[2] + sum[3]));
-    if (unsigned(tc) < unsigned(BN / 2)) {
-#pragma unroll
-        for (int c = 0; c < BN / 2; ++c)
-            if (c == tc) p.zt[row] = z[c];
-    }
 }
 
 // kGrad: what dz needs of this thread's row; fetched a tile ahead.
 struct GradRow {
     int64_t t;
-    float lse, g;
+    float lse, g, zt;
 };
 __device__ __forceinline__ GradRow grad_row(const XParams &p, int row) {
-    GradRow r{-1, 0.f, 0.f};
-    if (row < p.M) r = GradRow{p.targets[row], p.lse[row], p.dloss[row]};
+    GradRow r{-1, 0.f, 0.f, 0.f};
+    if (row < p.M) r = GradRow{p.targets[row], p.lse[row], p.dloss[row], p.zt[row]};
     return r;
 }
 
@@ -196,9 +205,10 @@ __device__ __forceinline__ void grad_box(const XParams &p, const GradRow &r, flo
     if (tc >= 0 && tc < min(64, p.N - col0)) {
         int k = int(tc);
         asm("" : "+r"(k));                                 // compared, never an index: y stays in registers
+        const float pt1 = expm1f(r.zt - r.lse);            // p - 1 of the target, exact also where p is near 1
 #pragma unroll
         for (int c = 0; c < 64; ++c)
-            if (c == k) y[c] -= 1.f;
+            if (c == k) y[c] = pt1;
     }
 #pragma unroll
     for (int c = 0; c < 64; ++c) y[c] = has ? y[c] * r.g : 0.f;
@@ -321,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
 
     // this unit's segments: its whole tiles, then its share of the split tiles, cut at tiles
     const int KB = p.nprod * p.kb;
-    const int chunk = !FINE ? KB : MODE != kStats ? kChunkGrad : p.nprod > 1 ? kChunkTerms : kChunkLoss;                    // k blocks of one accumulator
+    const int chunk = !FINE ? KB : MODE == kStats ? kChunkLoss : kChunkGrad;                    // k blocks of one accumulator
     const int nwhole = p.whole > unit ? (p.whole - unit + p.units - 1) / p.units : 0;
     const bool splits = MODE == kOut && p.sk_work > 0 && unit < p.sk_units;
     const int b0 = splits ? int(sk_start(p.sk_work, p.sk_units, unit)) : 0;       // sk_work < units KB < 2^31
@@ -504,12 +514,13 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
         uint8_t *buf = smem + kStages * STAGE;
         uint8_t *box = buf + (warp - 2) * kBox;                                        // kGrad
         float *blk = reinterpret_cast<float *>(buf) + (warp - 2) * 32 * 33;            // kOut
+        if constexpr (MODE != kOut) pdl_wait();               // the targets' logits, where their kernel comes just before
         int f = 0, at = b0;
         bool ok = true;
         Seg sg, next;
         bool more = next_seg(0, at, next);
         int m0 = 0, n0 = 0, tn = 0;
-        GradRow grn{-1, 0.f, 0.f};
+        GradRow grn{-1, 0.f, 0.f, 0.f};
         if (more) {
             place(next.tile, m0, n0, tn);
             if constexpr (MODE == kGrad) grn = grad_row(p, m0 + q * 32 + lane);
@@ -645,6 +656,44 @@ __global__ void __launch_bounds__(256) xent_fixup_kernel(const __grid_constant__
     }
 }
 
+// zt[i] = <hidden[i], W[t_i]> in fp32: a warp a row.
+template <typename HT, typename WT>
+__global__ void __launch_bounds__(256) xent_target_kernel(const HT *__restrict__ hidden, const WT *__restrict__ W,
+                                                          const int64_t *__restrict__ targets, int64_t rows, int64_t vocab,
+                                                          int64_t dim, float *__restrict__ zt) {
+    pdl_trigger();
+    const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int lane = threadIdx.x & 31;
+    if (row >= rows) return;
+    const int64_t t = targets[row];
+    if (t < 0 || t >= vocab) {
+        if (lane == 0) zt[row] = 0.f;
+        return;
+    }
+    const HT *h = hidden + row * dim;
+    const WT *w = W + t * dim;
+    float s[4] = {0.f, 0.f, 0.f, 0.f};
+    if (dim % 8 == 0) {                                      // rows of whole 16 bytes
+        for (int64_t c = lane * 8; c < dim; c += 256) {
+            alignas(16) HT a[8];
+            alignas(16) WT b[8];
+#pragma unroll
+            for (int k = 0; k < int(sizeof(a) / 16); ++k) reinterpret_cast<uint4 *>(a)[k] = reinterpret_cast<const uint4 *>(h + c)[k];
+#pragma unroll
+            for (int k = 0; k < int(sizeof(b) / 16); ++k) reinterpret_cast<uint4 *>(b)[k] = reinterpret_cast<const uint4 *>(w + c)[k];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) s[k & 3] = fmaf(float(a[k]), float(b[k]), s[k & 3]);
+        }
+    } else {
+        for (int64_t c = lane; c < dim; c += 128)
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (c + 32 * k < dim) s[k] = fmaf(float(h[c + 32 * k]), float(w[c + 32 * k]), s[k]);
+    }
+    const float v = warp_sum((s[0] + s[1]) + (s[2] + s[3]));
+    if (lane == 0) zt[row] = v;
+}
+
 // Joins the (max, sum) pairs of a row's tiles: rx rows x 256 / rx threads a block.  Each
 // thread joins slots y, y + 256 / rx, ..., eight at a time, then the block its threads' pairs
 // in a fixed tree.
@@ -747,7 +796,7 @@ struct Mat {
 };
 
 template <int BN, bool PAIR, int MODE, int TERMS, bool FINE, bool A_MN, bool B_MN>
-int launch(XParams &p, const Mat &a, const Mat &b, cudaStream_t st) {
+int launch(XParams &p, const Mat &a, const Mat &b, cudaStream_t st, bool dependent = false) {
     using S = Shape<BN, PAIR>;
     constexpr int stages = stages_of<BN, PAIR, MODE>();
     constexpr int smem = stages * S::STAGE + epi_bytes<MODE>() + 1024;
@@ -795,12 +844,14 @@ int launch(XParams &p, const Mat &a, const Mat &b, cudaStream_t st) {
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = PAIR ? 2 : 1;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = dependent ? 2 : 1;
     TLB_CUDA(cudaLaunchKernelEx(&cfg, k, p));
     TLB_TRY(check_launch(MODE == kStats ? "xent_stats" : MODE == kGrad ? "xent_grad" : A_MN ? "xent_dw" : "xent_dh"));
     if (p.sk_work > 0) {
@@ -814,13 +865,16 @@ int launch(XParams &p, const Mat &a, const Mat &b, cudaStream_t st) {
 // Tile form.  More than 128 rows: CTA pairs on 256 x 256 tiles.  Up to 128 rows there is one
 // row tile, and 128 columns a tile even out the few tiles over the SMs better than 256 when
 // their last wave is fuller.
+// after_targets: the kernel before it in the stream is xent_target_kernel, beside which it may start.
 template <int MODE, int TERMS>
-int launch_z(XParams &p, const Mat &h, const Mat &w, cudaStream_t st) {
+int launch_z(XParams &p, const Mat &h, const Mat &w, bool after_targets, cudaStream_t st) {
     constexpr bool fine = MODE == kStats || TERMS > 1;       // the loss is float32 whatever the operands
-    if (p.M > kBM) return launch<256, true, MODE, TERMS, fine, false, false>(p, h, w, st);
+    if constexpr (TERMS != 2)                                // two terms: up to 64 rows
+        if (p.M > kBM) return launch<256, true, MODE, TERMS, fine, false, false>(p, h, w, st, after_targets);
     const int64_t n = num_sms(), t256 = ceil_div(p.N, 256), t128 = ceil_div(p.N, 128);
-    if (2 * ceil_div(t256, n) <= ceil_div(t128, n)) return launch<256, false, MODE, TERMS, fine, false, false>(p, h, w, st);
-    return launch<128, false, MODE, TERMS, fine, false, false>(p, h, w, st);
+    if (2 * ceil_div(t256, n) <= ceil_div(t128, n))
+        return launch<256, false, MODE, TERMS, fine, false, false>(p, h, w, st, after_targets);
+    return launch<128, false, MODE, TERMS, fine, false, false>(p, h, w, st, after_targets);
 }
 
 template <bool A_MN, bool FINE>
@@ -830,6 +884,7 @@ int launch_out(XParams &p, const Mat &a, const Mat &b, cudaStream_t st) {
 }
 
 constexpr int64_t kPieceBytes = int64_t(512) << 20;   // of dz, and of packed head rows, in the workspace
+constexpr int64_t kFewRows = 64;                      // bf16 rows up to which dz has two terms
 constexpr int64_t kRowChunk = 16384;                  // rows of one pass of the loss (its pairs' buffer)
 
 struct Plan {
@@ -845,7 +900,7 @@ Plan plan_of(int htype, int wtype, int64_t N, int64_t V, int64_t D, bool grad, b
     Plan q;
     q.h_terms = htype == TLB_W_F32 ? 3 : 1;
     q.w_terms = wtype == TLB_W_F32 ? 3 : 1;
-    q.z_terms = htype == TLB_W_F32 ? 3 : 1;
+    q.z_terms = htype == TLB_W_F32 ? 3 : N <= kFewRows ? 2 : 1;
     q.dp = ceil_div(D, 8) * 8;
     // d_w sums over the rows: those without a target are zeroed in a copy
     q.pack_h = htype == TLB_W_F32 || D % 8 != 0 || grad_w;
@@ -862,12 +917,13 @@ Plan plan_of(int htype, int wtype, int64_t N, int64_t V, int64_t D, bool grad, b
     q.part = q.zt = q.dz = q.acc = q.partial = 0;
     if (!grad) {
         q.part_ld = ceil_div(std::min(N, kRowChunk), 32) * 32;
-        // 128-wide tiles: the most slots; two an SM for up to four rows
-        q.slots = std::max<int64_t>(2 * (ceil_div(V, 128) + ceil_div(V, q.piece)), 2 * num_sms());
+        // 128-wide tiles: the most slots; four an SM for up to four rows
+        q.slots = std::max<int64_t>(2 * (ceil_div(V, 128) + ceil_div(V, q.piece)), 4 * num_sms());
         q.part = w.take(size_t(q.part_ld) * q.slots * 8);
         q.zt = w.take(size_t(N) * 4);
     } else {
         q.dz = w.take(size_t(q.z_terms) * N * q.piece * 2);
+        q.zt = w.take(size_t(N) * 4);
         if (htype != TLB_W_F32 && q.piece < V) q.acc = w.take(size_t(N) * D * 4);
         q.partial = w.take(size_t(num_sms() + 1) * 2 * kBM * 256 * 4);
     }
@@ -925,6 +981,32 @@ int head_operand(const Plan &q, int wtype, const void *W, int64_t v0, int64_t n,
     return pack(src, wtype, n, D, q.dp, q.w_terms, nullptr, 0, y, st);
 }
 
+// Few rows take the kernel that reads the head once for up to four rows, in turns of four: one
+// turn, or up to four where the tensor-core route would read and write the head again to pack
+// it (measured at 8 rows, 1216 x 36096 float32: see the table of cases).
+bool by_tokens(const Plan &q, int64_t rows, int64_t dim) {
+    const int64_t turns = ceil_div(rows, 4), last = rows - 4 * (turns - 1);
+    return turns <= (q.pack_w ? 4 : 1) && xent_token_supported(std::min<int64_t>(rows, 4), dim) && xent_token_supported(last, dim);
+}
+
+int target_logits(int htype, const void *hidden, int wtype, const void *W, const int64_t *targets, int64_t rows, int64_t vocab,
+                  int64_t dim, float *zt, cudaStream_t st) {
+    const unsigned grid = unsigned(ceil_div(rows, 8));
+    const float *hf = static_cast<const float *>(hidden);
+    const __nv_bfloat16 *hb = static_cast<const __nv_bfloat16 *>(hidden), *wb = static_cast<const __nv_bfloat16 *>(W);
+    if (wtype == TLB_W_F32)
+        xent_target_kernel<<<grid, 256, 0, st>>>(hf, static_cast<const float *>(W), targets, rows, vocab, dim, zt);
+    else if (htype == TLB_W_F32)
+        xent_target_kernel<<<grid, 256, 0, st>>>(hf, wb, targets, rows, vocab, dim, zt);
+    else
+        xent_target_kernel<<<grid, 256, 0, st>>>(hb, wb, targets, rows, vocab, dim, zt);
+    return check_launch("xent_target");
+}
+
+const void *row_of(const void *x, int type, int64_t r, int64_t dim) {
+    return static_cast<const char *>(x) + size_t(r) * dim * elem(type);
+}
+
 int join(const Plan &q, void *ws, int64_t r0, int64_t n, int slots, const int64_t *targets, int64_t vocab, float *loss,
          float *lse, cudaStream_t st) {
     int rx = 1;                                              // a block for every SM first, then whole sectors
@@ -961,11 +1043,16 @@ int tlb_xent_forward(int32_t htype, const void *hidden, int32_t wtype, const voi
     TLB_REQUIRE(ws != nullptr && (reinterpret_cast<uintptr_t>(ws) & 255) == 0 && ws_bytes >= q.total, TLB_EINVAL,
                 "xent_forward: needs a 256-byte aligned workspace of %zu bytes", q.total);
     cudaStream_t st = as_stream(stream);
-    if (xent_token_supported(rows, dim)) {
-        int slots = 0;
-        TLB_TRY(xent_token_loss(htype, hidden, wtype, W, targets, rows, vocab, dim, ws_at<float2>(ws, q.part), q.part_ld,
-                                ws_at<float>(ws, q.zt), ws_at<uint32_t>(ws, 0), &slots, st));
-        return join(q, ws, 0, rows, slots, targets, vocab, loss, lse, st);
+    if (by_tokens(q, rows, dim)) {
+        for (int64_t r0 = 0; r0 < rows; r0 += 4) {
+            const int64_t n = std::min<int64_t>(4, rows - r0);
+            int slots = 0;
+            TLB_TRY(xent_token_loss(htype, row_of(hidden, htype, r0, dim), wtype, W, targets + r0, n, vocab, dim,
+                                    ws_at<float2>(ws, q.part), q.part_ld, ws_at<float>(ws, q.zt) + r0,
+                                    ws_at<uint32_t>(ws, 0), &slots, st));
+            TLB_TRY(join(q, ws, r0, n, slots, targets, vocab, loss, lse, st));
+        }
+        return TLB_OK;
     }
     Mat h;
     TLB_TRY(hidden_operand(q, htype, hidden, rows, dim, nullptr, vocab, ws, st, h));
@@ -980,6 +1067,9 @@ int tlb_xent_forward(int32_t htype, const void *hidden, int32_t wtype, const voi
             Mat w;
             const int64_t nv = std::min(step, vocab - v0);
             TLB_TRY(head_operand(q, wtype, W, v0, nv, dim, ws, st, w));
+            if (v0 == 0)
+                TLB_TRY(target_logits(htype, row_of(hidden, htype, r0, dim), wtype, W, targets + r0, n, vocab, dim,
+                                      ws_at<float>(ws, q.zt) + r0, st));
             XParams p;
             memset(&p, 0, sizeof(p));
             p.M = int(n);
@@ -991,7 +1081,7 @@ int tlb_xent_forward(int32_t htype, const void *hidden, int32_t wtype, const voi
             p.ld_part = q.part_ld;
             p.zt = ws_at<float>(ws, q.zt) + r0;
             p.status = ws_at<uint32_t>(ws, 0);
-            TLB_TRY((launch_z<kStats, 1>(p, hr, w, st)));
+            TLB_TRY((launch_z<kStats, 1>(p, hr, w, v0 == 0, st)));
             slot += 2 * p.tiles_n;
         }
         TLB_TRY(join(q, ws, r0, n, slot, targets, vocab, loss, lse, st));
@@ -1014,9 +1104,15 @@ int tlb_xent_backward(int32_t htype, const void *hidden, int32_t wtype, const vo
     const Plan q = plan_of(htype, wtype, rows, vocab, dim, true, d_w != nullptr);
     TLB_REQUIRE(ws != nullptr && (reinterpret_cast<uintptr_t>(ws) & 255) == 0 && ws_bytes >= q.total, TLB_EINVAL,
                 "xent_backward: needs a 256-byte aligned workspace of %zu bytes", q.total);
-    if (xent_token_supported(rows, dim) && aligned16(d_w))
-        return xent_token_grad(htype, hidden, wtype, W, targets, lse, d_loss, rows, vocab, dim, d_hidden, d_w,
-                               ws_at<float>(ws, q.partial), ws_at<uint32_t>(ws, 0), st);
+    // several turns add to d_w, which only float32 can hold
+    if (by_tokens(q, rows, dim) && aligned16(d_w) && (d_w == nullptr || rows <= 4 || htype == TLB_W_F32)) {
+        for (int64_t r0 = 0; r0 < rows; r0 += 4)
+            TLB_TRY(xent_token_grad(htype, row_of(hidden, htype, r0, dim), wtype, W, targets + r0, lse + r0, d_loss + r0,
+                                    std::min<int64_t>(4, rows - r0), vocab, dim,
+                                    const_cast<void *>(row_of(d_hidden, htype, r0, dim)), d_w, ws_at<float>(ws, q.partial),
+                                    ws_at<uint32_t>(ws, 0), r0 > 0, st));
+        return TLB_OK;
+    }
     Mat h;
     TLB_TRY(hidden_operand(q, htype, hidden, rows, dim, d_w != nullptr ? targets : nullptr, vocab, ws, st, h));
     const bool wide = htype == TLB_W_F32;
@@ -1024,6 +1120,7 @@ int tlb_xent_backward(int32_t htype, const void *hidden, int32_t wtype, const vo
         const int64_t nv = std::min(q.piece, vocab - v0);
         Mat w;
         TLB_TRY(head_operand(q, wtype, W, v0, nv, dim, ws, st, w));
+        if (v0 == 0) TLB_TRY(target_logits(htype, hidden, wtype, W, targets, rows, vocab, dim, ws_at<float>(ws, q.zt), st));
         const Mat dz{ws_at<__nv_bfloat16>(ws, q.dz), rows, nv, q.piece, rows * q.piece, q.z_terms};
         {
             XParams p;
@@ -1035,11 +1132,13 @@ int tlb_xent_backward(int32_t htype, const void *hidden, int32_t wtype, const vo
             p.v0 = v0;
             p.lse = lse;
             p.dloss = d_loss;
+            p.zt = ws_at<float>(ws, q.zt);
             for (int t = 0; t < q.z_terms; ++t)
                 TLB_TRY(make_map(&p.d[t], dz.p + t * dz.plane, rows, nv, dz.ld, 32));
             p.status = ws_at<uint32_t>(ws, 0);
-            if (wide) TLB_TRY((launch_z<kGrad, 3>(p, h, w, st)));
-            else TLB_TRY((launch_z<kGrad, 1>(p, h, w, st)));
+            if (q.z_terms == 3) TLB_TRY((launch_z<kGrad, 3>(p, h, w, v0 == 0, st)));
+            else if (q.z_terms == 2) TLB_TRY((launch_z<kGrad, 2>(p, h, w, v0 == 0, st)));
+            else TLB_TRY((launch_z<kGrad, 1>(p, h, w, v0 == 0, st)));
         }
         {
             XParams p;

@@ -46,8 +46,9 @@ struct TokenParams {
     float *zt;
     // gradient
     const float *lse, *dloss;
-    float *partial;              // [CTA][n][D]
+    float *partial;              // [CTA][n][D, made even]
     void *dw;                    // [V, D] in hidden's type, or null
+    int dw_add;                  // add to it (float32)
     uint32_t *status;
 };
 
@@ -70,8 +71,8 @@ __device__ __forceinline__ float2 unpack(const Pair<W32> &p) {
     else return make_float2(bf16_lo(p.v), bf16_hi(p.v));
 }
 
-// TH threads: 512, one CTA an SM, or 256, two CTAs, where a thread's registers hold twice the
-// columns; the two then wait at barriers of their own.
+// TH threads: 512, one CTA an SM, or 256 or 128, two or four CTAs, which wait at barriers of
+// their own: as few threads as hold the columns in R pairs each.
 template <int TH, int N, int R, bool W32, bool GRAD>
 __global__ void __launch_bounds__(TH, 512 / TH) xent_token_kernel(const __grid_constant__ TokenParams p) {
     constexpr int kThreads = TH, kWarps = TH / 32;
@@ -83,6 +84,7 @@ __global__ void __launch_bounds__(TH, 512 / TH) xent_token_kernel(const __grid_c
     __shared__ float red[2][kWarps][NV];
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int D = p.D, stages = p.stages;
+    const bool odd = D & 1;                                 // pairs start at odd elements: loads by element
     const int64_t blocks = (p.vocab + VB - 1) / VB, nfull = p.vocab / VB;  // the last may be short
     const uint32_t bytes = 16u * uint32_t(D);
     const char *w = static_cast<const char *>(p.w);
@@ -124,7 +126,12 @@ __global__ void __launch_bounds__(TH, 512 / TH) xent_token_kernel(const __grid_c
             h[n][r] = acc[n][r] = make_float2(0.f, 0.f);
             if (c < D && on) {
                 const int64_t e = int64_t(n) * D + c;
-                if (p.hidden_f32) {
+                if (odd) {
+                    h[n][r].x = p.hidden_f32 ? static_cast<const float *>(p.hidden)[e] : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.hidden)[e]);
+                    if (c + 1 < D)
+                        h[n][r].y = p.hidden_f32 ? static_cast<const float *>(p.hidden)[e + 1]
+                                                 : __bfloat162float(static_cast<const __nv_bfloat16 *>(p.hidden)[e + 1]);
+                } else if (p.hidden_f32) {
                     h[n][r] = *reinterpret_cast<const float2 *>(static_cast<const float *>(p.hidden) + e);
                 } else {
                     const uint32_t v = *reinterpret_cast<const uint32_t *>(static_cast<const __nv_bfloat16 *>(p.hidden) + e);
@@ -133,6 +140,22 @@ __global__ void __launch_bounds__(TH, 512 / TH) xent_token_kernel(const __grid_c
             }
         }
     }
+    // the pair of columns c, c + 1 of head row v of a block
+    auto pair_at = [&](const void *src, int v, int c) {
+        Pair<W32> x = {};
+        if (!odd) {
+            x = *reinterpret_cast<const Pair<W32> *>(static_cast<const char *>(src) + (size_t(v) * D + c) * (W32 ? 4 : 2));
+        } else if constexpr (W32) {
+            const float *q = static_cast<const float *>(src) + size_t(v) * D + c;
+            x.v.x = q[0];
+            if (c + 1 < D) x.v.y = q[1];
+        } else {
+            const uint16_t *q = static_cast<const uint16_t *>(src) + size_t(v) * D + c;
+            x.v = q[0];
+            if (c + 1 < D) x.v |= uint32_t(q[1]) << 16;
+        }
+        return x;
+    };
     float m = -INFINITY, sum = 0.f;
     bool ok = true;
     int i = 0;
@@ -149,7 +172,7 @@ __global__ void __launch_bounds__(TH, 512 / TH) xent_token_kernel(const __grid_c
                 for (int r = 0; r < R; ++r) {
                     const int c = 2 * (tid + r * kThreads);
                     x[v][r] = {};
-                    if (c < D) x[v][r] = *reinterpret_cast<const Pair<W32> *>(src + (size_t(v) * D + c) * (W32 ? 4 : 2));
+                    if (c < D) x[v][r] = pair_at(src, v, c);
                 }
         } else {
             const char *src = w + b * bytes;
@@ -159,8 +182,7 @@ __global__ void __launch_bounds__(TH, 512 / TH) xent_token_kernel(const __grid_c
                 for (int r = 0; r < R; ++r) {
                     const int c = 2 * (tid + r * kThreads);
                     x[v][r] = {};
-                    if (c < D && v < rows)
-                        x[v][r] = *reinterpret_cast<const Pair<W32> *>(src + (size_t(v) * D + c) * (W32 ? 4 : 2));
+                    if (c < D && v < rows) x[v][r] = pair_at(src, v, c);
                 }
         }
         float s[NV];
@@ -210,7 +232,7 @@ __global__ void __launch_bounds__(TH, 512 / TH) xent_token_kernel(const __grid_c
                 if (row == t && (lane & ((1 << SH) - 1)) == 0) p.zt[vn] = z;
             }
         } else {
-            float dz = ex2((z - lse) * kLog2e) - (row == t ? 1.f : 0.f);
+            float dz = row == t ? expm1f(z - lse) : ex2((z - lse) * kLog2e);    // p - 1, exact also where p is near 1
             dz = has && vr < rows ? dz * g : 0.f;
 #pragma unroll
             for (int v = 0; v < VB; ++v) {
@@ -239,7 +261,21 @@ __global__ void __launch_bounds__(TH, 512 / TH) xent_token_kernel(const __grid_c
                         }
                         const int64_t e = (b * VB + v) * D + c;
                         if (p.hidden_f32) {
-                            *reinterpret_cast<float2 *>(static_cast<float *>(p.dw) + e) = o;
+                            float *q = static_cast<float *>(p.dw) + e;
+                            if (p.dw_add) {
+                                o.x += q[0];
+                                if (c + 1 < D) o.y += q[1];
+                            }
+                            if (odd) {
+                                q[0] = o.x;
+                                if (c + 1 < D) q[1] = o.y;
+                            } else {
+                                *reinterpret_cast<float2 *>(q) = o;
+                            }
+                        } else if (odd) {
+                            __nv_bfloat16 *q = static_cast<__nv_bfloat16 *>(p.dw) + e;
+                            q[0] = __float2bfloat16(o.x);
+                            if (c + 1 < D) q[1] = __float2bfloat16(o.y);
                         } else {
                             const __nv_bfloat162 q = __floats2bfloat162_rn(o.x, o.y);
                             *reinterpret_cast<__nv_bfloat162 *>(static_cast<__nv_bfloat16 *>(p.dw) + e) = q;
@@ -278,22 +314,24 @@ __global__ void __launch_bounds__(TH, 512 / TH) xent_token_kernel(const __grid_c
             for (int r = 0; r < R; ++r) {
                 const int c = 2 * (tid + r * kThreads);
                 if (c < D && n < p.n)
-                    *reinterpret_cast<float2 *>(p.partial + (int64_t(blockIdx.x) * p.n + n) * D + c) = acc[n][r];
+                    *reinterpret_cast<float2 *>(p.partial + (int64_t(blockIdx.x) * p.n + n) * (D + (D & 1)) + c) = acc[n][r];
             }
     }
 }
 
 // d_hidden: the CTAs' parts added up, 32 elements x 8 threads a block, in a fixed order.
-__global__ void __launch_bounds__(256) xent_token_sum_kernel(const float *__restrict__ partial, int parts, int n, float *out32,
-                                                             __nv_bfloat16 *out16) {
+__global__ void __launch_bounds__(256) xent_token_sum_kernel(const float *__restrict__ partial, int parts, int rows, int D,
+                                                             float *out32, __nv_bfloat16 *out16) {
     __shared__ float sh[8][32];
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5, e = blockIdx.x * 32 + x;
+    const int ld = D + (D & 1), n = rows * D, row = e / D;
+    const float *src = partial + row * ld + (e - row * D);
     pdl_wait();
     float s = 0.f;
     for (int k = y; k < parts && e < n; k += 64) {
         float v[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = k + 8 * u < parts ? partial[int64_t(k + 8 * u) * n + e] : 0.f;
+        for (int u = 0; u < 8; ++u) v[u] = k + 8 * u < parts ? src[int64_t(k + 8 * u) * rows * ld] : 0.f;
 #pragma unroll
         for (int u = 0; u < 8; ++u) s += v[u];
     }
@@ -309,7 +347,7 @@ __global__ void __launch_bounds__(256) xent_token_sum_kernel(const float *__rest
 
 template <int TH, int N, int R, bool W32, bool GRAD>
 int launch(TokenParams &p, int grid, cudaStream_t st) {
-    constexpr int room = (TH == 512 ? 220 : 108) * 1024;
+    constexpr int room = (TH == 512 ? 220 : TH == 256 ? 108 : 52) * 1024;
     p.stages = std::min(kMaxStages, room / (16 * p.D));
     const int smem = p.stages * 16 * p.D;
     auto k = xent_token_kernel<TH, N, R, W32, GRAD>;
@@ -318,33 +356,37 @@ int launch(TokenParams &p, int grid, cudaStream_t st) {
     return check_launch(GRAD ? "xent_token_grad" : "xent_token_loss");
 }
 
-// Column pairs a thread holds: registers allow 6 rounds of 512 pairs for one row, 3 for two to
-// four; of 256 pairs 5 for up to two rows.
-constexpr int kRounds1 = 6, kRounds = 3, kRounds256 = 5;
-
-// Two CTAs an SM where the rows allow it: the gradient of one token over 32768 x 2560 takes
-// 43 us with one CTA (its warps wait for one another at every block of head rows).
-bool two_ctas(int64_t N, int64_t D) { return N <= 2 && D <= kRounds256 * 2 * 256; }
+// Threads of a CTA for N rows (1, 2 or 4) of length D; 0: none.  A thread's registers hold 4 to 6
+// pairs of columns of one row, 3 to 5 of two, 2 or 3 of four.  Smaller CTAs first: the warps of
+// a CTA wait for one another at every block of head rows (the gradient of one token over 32768
+// x 2560 takes 43 us with one CTA of 512 threads an SM, 30 us with two of 256).
+int token_threads(int64_t N, int64_t D) {
+    if (N == 4) return D <= 512 ? 128 : D <= 1024 ? 256 : D <= 3 * 1024 ? 512 : 0;
+    return D <= 1024 ? 128 : D <= 2560 ? 256 : D <= (N == 1 ? 6 : 3) * 1024 ? 512 : 0;
+}
+int64_t row_class(int64_t N) { return N <= 2 ? N : 4; }
 
 template <bool W32, bool GRAD>
 int by_rows(TokenParams &p, int64_t N, int grid, cudaStream_t st) {
-    if (two_ctas(N, p.D))
-        return N == 1 ? launch<256, 1, kRounds256, W32, GRAD>(p, grid, st) : launch<256, 2, kRounds256, W32, GRAD>(p, grid, st);
-    if (N == 1) return p.D <= kRounds * 1024 ? launch<512, 1, kRounds, W32, GRAD>(p, grid, st) : launch<512, 1, kRounds1, W32, GRAD>(p, grid, st);
-    if (N == 2) return launch<512, 2, kRounds, W32, GRAD>(p, grid, st);
-    return launch<512, 4, kRounds, W32, GRAD>(p, grid, st);
+    const int th = token_threads(row_class(N), p.D);
+    if (N == 1)
+        return th == 128 ? launch<128, 1, 4, W32, GRAD>(p, grid, st) : th == 256 ? launch<256, 1, 5, W32, GRAD>(p, grid, st)
+                                                                                 : launch<512, 1, 6, W32, GRAD>(p, grid, st);
+    if (N == 2)
+        return th == 128 ? launch<128, 2, 4, W32, GRAD>(p, grid, st) : th == 256 ? launch<256, 2, 5, W32, GRAD>(p, grid, st)
+                                                                                 : launch<512, 2, 3, W32, GRAD>(p, grid, st);
+    return th == 128 ? launch<128, 4, 2, W32, GRAD>(p, grid, st) : th == 256 ? launch<256, 4, 2, W32, GRAD>(p, grid, st)
+                                                                             : launch<512, 4, 3, W32, GRAD>(p, grid, st);
 }
 
 int token_grid(int wtype, int64_t N, int64_t vocab, int64_t D) {
-    return int(std::min<int64_t>((two_ctas(N, D) ? 2 : 1) * num_sms(), ceil_div(vocab, wtype == TLB_W_F32 ? 4 : 8)));
+    const int ctas = 512 / token_threads(row_class(N), D);
+    return int(std::min<int64_t>(ctas * num_sms(), ceil_div(vocab, wtype == TLB_W_F32 ? 4 : 8)));
 }
 
 }  // namespace
 
-// Up to four rows of an even length whose share fits a thread's registers.
-bool xent_token_supported(int64_t N, int64_t D) {
-    return N >= 1 && N <= 4 && D % 2 == 0 && D <= (N == 1 ? kRounds1 : kRounds) * 1024;
-}
+bool xent_token_supported(int64_t N, int64_t D) { return N >= 1 && N <= 4 && token_threads(row_class(N), D) > 0; }
 
 int xent_token_loss(int htype, const void *hidden, int wtype, const void *W, const int64_t *targets, int64_t N, int64_t V,
                     int64_t D, float2 *part, int64_t ld_part, float *zt, uint32_t *status, int *slots, cudaStream_t st) {
@@ -367,7 +409,7 @@ int xent_token_loss(int htype, const void *hidden, int wtype, const void *W, con
 
 int xent_token_grad(int htype, const void *hidden, int wtype, const void *W, const int64_t *targets, const float *lse,
                     const float *d_loss, int64_t N, int64_t V, int64_t D, void *d_hidden, void *d_w, float *partial,
-                    uint32_t *status, cudaStream_t st) {
+                    uint32_t *status, bool dw_add, cudaStream_t st) {
     TokenParams p;
     memset(&p, 0, sizeof(p));
     p.hidden = hidden;
@@ -381,10 +423,11 @@ int xent_token_grad(int htype, const void *hidden, int wtype, const void *W, con
     p.dloss = d_loss;
     p.partial = partial;
     p.dw = d_w;
+    p.dw_add = dw_add;
     p.status = status;
     const int grid = token_grid(wtype, N, V, D), n = int(N * D);
     TLB_TRY((wtype == TLB_W_F32 ? by_rows<true, true>(p, N, grid, st) : by_rows<false, true>(p, N, grid, st)));
-    TLB_CUDA(launch_dependent(xent_token_sum_kernel, dim3(unsigned(ceil_div(n, 32))), dim3(256), 0, st, partial, grid, n,
+    TLB_CUDA(launch_dependent(xent_token_sum_kernel, dim3(unsigned(ceil_div(n, 32))), dim3(256), 0, st, partial, grid, int(N), int(D),
                               htype == TLB_W_F32 ? static_cast<float *>(d_hidden) : nullptr,
                               htype == TLB_W_F32 ? nullptr : static_cast<__nv_bfloat16 *>(d_hidden)));
     return check_launch("xent_token_sum");
