@@ -96,17 +96,20 @@ def test_xent(lib, rows, vocab, dim, types):
                                             (3, 1000, 320), (3, 5, 2), (4, 4099, 2560), (4, 12, 1022), (4, 300, 3074),
                                             (5, 2000, 2560), (1, 50, 1001), (1, 700, 2085), (2, 1003, 333), (4, 77, 5),
                                             (3, 2001, 1999), (4, 900, 511), (6, 1500, 513), (9, 500, 1216), (16, 3001, 130),
-                                            (15, 600, 1025), (17, 400, 130), (12, 999, 3073)])
+                                            (15, 600, 1025), (17, 400, 130), (12, 999, 3073), (12, 700, 832),
+                                            (13, 700, 832), (10, 20011, 832)])
 def test_few_rows(lib, rows, vocab, dim, types):
-    """Up to four rows take the one-pass kernel, up to sixteen take it in turns where the head
-    would have to be packed (float32, odd lengths); blocks of head rows that are not full,
+    """Up to four rows take the one-pass kernel, up to twelve float32 rows take it in turns, and
+    sixteen where the head would have to be packed (float32, odd lengths); blocks of head rows that are not full,
     lengths past what the registers hold, and one row more beside them."""
     n0 = lib.launch_count()
     test_xent(lib, rows, vocab, dim, types)
     names = lib.launch_names(n0)
-    fits = dim <= (6144 if rows == 1 else 1024 * 3)
+    turns = [min(4, rows - r) for r in range(0, rows, 4)]
     packed = types[1] == "f32" or dim % 8 != 0
-    assert ("xent_token_loss" in names) == (fits and rows <= (16 if packed else 4)), names
+    for name, four in (("xent_token_loss", 5), ("xent_token_grad", 3)):
+        fits = all(dim <= 1024 * {1: 6, 2: 5}.get(n, four) for n in turns)
+        assert (name in names) == (fits and rows <= (16 if packed else 12 if types[0] == "f32" else 4)), names
     if types[0] == "bf16" and rows > 4:                      # d_w of several turns is summed in float32 only
         assert "xent_dw" in names
 

@@ -69,7 +69,7 @@ int act_backward_bf16_launch(int act, const float *gate, const float *up, const 
                              void *dgate, void *dup, int64_t n, cudaStream_t st);
 
 // Cross entropy of a linear head for up to four rows (xent_token.cu): one pass over the head.
-bool xent_token_supported(int64_t N, int64_t D);
+bool xent_token_supported(int64_t N, int64_t D, bool grad);
 // (max, sum) pairs of every row in *slots slots of part [slot][ld_part], and the targets' logits.
 int xent_token_loss(int htype, const void *hidden, int wtype, const void *W, const int64_t *targets, int64_t N, int64_t V,
                     int64_t D, float2 *part, int64_t ld_part, float *zt, uint32_t *status, int *slots, cudaStream_t st);

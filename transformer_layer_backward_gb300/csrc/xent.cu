@@ -41,6 +41,7 @@
 
 #include <algorithm>
 #include <cstring>
+#include <type_traits>
 
 #include "async.cuh"
 #include "common.cuh"
@@ -756,6 +757,26 @@ __global__ void __launch_bounds__(256) xent_pack_kernel(const SRC *__restrict__ 
             const int64_t t = targets[r];
             on = t >= 0 && t < vocab;
         }
+        if constexpr (std::is_same<SRC, __nv_bfloat16>::value) {
+            // bf16 into one term: the bits as they are, by words, half a word apart in odd places
+            const int64_t e = r * cols + c, total = rows * cols;
+            const uint16_t *half = reinterpret_cast<const uint16_t *>(x);
+            const uint32_t *word = reinterpret_cast<const uint32_t *>(x) + (e >> 1);
+            uint32_t w[5], o[4];
+#pragma unroll
+            for (int k = 0; k < 5; ++k) {
+                const int64_t at = (e & ~int64_t(1)) + 2 * k;
+                w[k] = !on || at >= total || 2 * k > 8 + int(e & 1) - 1 ? 0u : at + 1 < total ? word[k] : uint32_t(half[at]);
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                o[k] = e & 1 ? __byte_perm(w[k], w[k + 1], 0x5432) : w[k];
+                const int left = cols - c - 2 * k;           // columns from here to the row's end
+                if (left < 2) o[k] = left == 1 ? o[k] & 0xFFFFu : 0u;
+            }
+            *reinterpret_cast<uint4 *>(y + r * ld + c) = make_uint4(o[0], o[1], o[2], o[3]);
+            continue;
+        }
         const SRC *src = x + r * cols + c;
         float v[8];
 #pragma unroll
@@ -982,11 +1003,13 @@ int head_operand(const Plan &q, int wtype, const void *W, int64_t v0, int64_t n,
 }
 
 // Few rows take the kernel that reads the head once for up to four rows, in turns of four: one
-// turn, or up to four where the tensor-core route would read and write the head again to pack
-// it (measured at 8 rows, 1216 x 36096 float32: see the table of cases).
-bool by_tokens(const Plan &q, int64_t rows, int64_t dim) {
+// turn beside bf16 tensor-core products (which read the head once for a loss), up to three
+// beside float32 rows' (three products of every tile: 10 rows x 832 x 110656, gradient, 130
+// against 186 us), up to four where the tensor-core route would write the head again to pack it.
+bool by_tokens(const Plan &q, int64_t rows, int64_t dim, bool grad) {
     const int64_t turns = ceil_div(rows, 4), last = rows - 4 * (turns - 1);
-    return turns <= (q.pack_w ? 4 : 1) && xent_token_supported(std::min<int64_t>(rows, 4), dim) && xent_token_supported(last, dim);
+    return turns <= (q.pack_w ? 4 : q.h_terms > 1 ? 3 : 1) && xent_token_supported(std::min<int64_t>(rows, 4), dim, grad) &&
+           xent_token_supported(last, dim, grad);
 }
 
 int target_logits(int htype, const void *hidden, int wtype, const void *W, const int64_t *targets, int64_t rows, int64_t vocab,
@@ -1043,7 +1066,7 @@ int tlb_xent_forward(int32_t htype, const void *hidden, int32_t wtype, const voi
     TLB_REQUIRE(ws != nullptr && (reinterpret_cast<uintptr_t>(ws) & 255) == 0 && ws_bytes >= q.total, TLB_EINVAL,
                 "xent_forward: needs a 256-byte aligned workspace of %zu bytes", q.total);
     cudaStream_t st = as_stream(stream);
-    if (by_tokens(q, rows, dim)) {
+    if (by_tokens(q, rows, dim, false)) {
         for (int64_t r0 = 0; r0 < rows; r0 += 4) {
             const int64_t n = std::min<int64_t>(4, rows - r0);
             int slots = 0;
@@ -1105,7 +1128,7 @@ int tlb_xent_backward(int32_t htype, const void *hidden, int32_t wtype, const vo
     TLB_REQUIRE(ws != nullptr && (reinterpret_cast<uintptr_t>(ws) & 255) == 0 && ws_bytes >= q.total, TLB_EINVAL,
                 "xent_backward: needs a 256-byte aligned workspace of %zu bytes", q.total);
     // several turns add to d_w, which only float32 can hold
-    if (by_tokens(q, rows, dim) && aligned16(d_w) && (d_w == nullptr || rows <= 4 || htype == TLB_W_F32)) {
+    if (by_tokens(q, rows, dim, true) && aligned16(d_w) && (d_w == nullptr || rows <= 4 || htype == TLB_W_F32)) {
         for (int64_t r0 = 0; r0 < rows; r0 += 4)
             TLB_TRY(xent_token_grad(htype, row_of(hidden, htype, r0, dim), wtype, W, targets + r0, lse + r0, d_loss + r0,
                                     std::min<int64_t>(4, rows - r0), vocab, dim,

@@ -71,11 +71,15 @@ __device__ __forceinline__ float2 unpack(const Pair<W32> &p) {
     else return make_float2(bf16_lo(p.v), bf16_hi(p.v));
 }
 
+// Pairs of columns a thread's registers hold: of the hidden rows, and for the gradient of
+// d_hidden's rows and of a block of head rows too.
+template <int N, bool GRAD> constexpr int rounds() { return N == 1 ? 6 : N == 2 || !GRAD ? 5 : 3; }
+
 // TH threads: 512, one CTA an SM, or 256 or 128, two or four CTAs, which wait at barriers of
 // their own: as few threads as hold the columns in R pairs each.
-template <int TH, int N, int R, bool W32, bool GRAD>
+template <int TH, int N, bool W32, bool GRAD>
 __global__ void __launch_bounds__(TH, 512 / TH) xent_token_kernel(const __grid_constant__ TokenParams p) {
-    constexpr int kThreads = TH, kWarps = TH / 32;
+    constexpr int kThreads = TH, kWarps = TH / 32, R = rounds<N, GRAD>();
     constexpr int VB = block_rows<W32>(), NV = VB * N;
     constexpr int SH = NV == 32 ? 0 : NV == 16 ? 1 : NV == 8 ? 2 : 3;      // lane >> SH: the lane's value
     static_assert((NV << SH) == 32, "values a warp reduces");
@@ -345,48 +349,48 @@ __global__ void __launch_bounds__(256) xent_token_sum_kernel(const float *__rest
     }
 }
 
-template <int TH, int N, int R, bool W32, bool GRAD>
+template <int TH, int N, bool W32, bool GRAD>
 int launch(TokenParams &p, int grid, cudaStream_t st) {
     constexpr int room = (TH == 512 ? 220 : TH == 256 ? 108 : 52) * 1024;
     p.stages = std::min(kMaxStages, room / (16 * p.D));
     const int smem = p.stages * 16 * p.D;
-    auto k = xent_token_kernel<TH, N, R, W32, GRAD>;
+    auto k = xent_token_kernel<TH, N, W32, GRAD>;
     TLB_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, room));
     k<<<grid, TH, smem, st>>>(p);
     return check_launch(GRAD ? "xent_token_grad" : "xent_token_loss");
 }
 
-// Threads of a CTA for N rows (1, 2 or 4) of length D; 0: none.  A thread's registers hold 4 to 6
-// pairs of columns of one row, 3 to 5 of two, 2 or 3 of four.  Smaller CTAs first: the warps of
-// a CTA wait for one another at every block of head rows (the gradient of one token over 32768
-// x 2560 takes 43 us with one CTA of 512 threads an SM, 30 us with two of 256).
-int token_threads(int64_t N, int64_t D) {
-    if (N == 4) return D <= 512 ? 128 : D <= 1024 ? 256 : D <= 3 * 1024 ? 512 : 0;
-    return D <= 1024 ? 128 : D <= 2560 ? 256 : D <= (N == 1 ? 6 : 3) * 1024 ? 512 : 0;
+// Threads of a CTA for N rows of length D; 0: too long.  The smallest CTA whose registers hold the
+// rows, and 512 / threads of them an SM: the warps of a CTA wait for one another at every block
+// of head rows (the gradient of one token over 32768 x 2560 takes 43 us with one CTA of 512
+// threads an SM, 30 us with two of 256).
+int token_threads(int64_t N, int64_t D, bool grad) {
+    const int r = N == 1 ? 6 : N == 2 || !grad ? 5 : 3;
+    for (int th = 128; th <= 512; th *= 2)
+        if (D <= int64_t(2) * th * r) return th;
+    return 0;
 }
-int64_t row_class(int64_t N) { return N <= 2 ? N : 4; }
+
+template <int N, bool W32, bool GRAD>
+int by_threads(TokenParams &p, int th, int grid, cudaStream_t st) {
+    return th == 128 ? launch<128, N, W32, GRAD>(p, grid, st) : th == 256 ? launch<256, N, W32, GRAD>(p, grid, st)
+                                                                          : launch<512, N, W32, GRAD>(p, grid, st);
+}
+
+// Up to 4 CTAs an SM, each with a block of head rows at least.
+int token_grid(int wtype, int th, int64_t vocab) {
+    return int(std::min<int64_t>(512 / th * num_sms(), ceil_div(vocab, wtype == TLB_W_F32 ? 4 : 8)));
+}
 
 template <bool W32, bool GRAD>
-int by_rows(TokenParams &p, int64_t N, int grid, cudaStream_t st) {
-    const int th = token_threads(row_class(N), p.D);
-    if (N == 1)
-        return th == 128 ? launch<128, 1, 4, W32, GRAD>(p, grid, st) : th == 256 ? launch<256, 1, 5, W32, GRAD>(p, grid, st)
-                                                                                 : launch<512, 1, 6, W32, GRAD>(p, grid, st);
-    if (N == 2)
-        return th == 128 ? launch<128, 2, 4, W32, GRAD>(p, grid, st) : th == 256 ? launch<256, 2, 5, W32, GRAD>(p, grid, st)
-                                                                                 : launch<512, 2, 3, W32, GRAD>(p, grid, st);
-    return th == 128 ? launch<128, 4, 2, W32, GRAD>(p, grid, st) : th == 256 ? launch<256, 4, 2, W32, GRAD>(p, grid, st)
-                                                                             : launch<512, 4, 3, W32, GRAD>(p, grid, st);
-}
-
-int token_grid(int wtype, int64_t N, int64_t vocab, int64_t D) {
-    const int ctas = 512 / token_threads(row_class(N), D);
-    return int(std::min<int64_t>(ctas * num_sms(), ceil_div(vocab, wtype == TLB_W_F32 ? 4 : 8)));
+int by_rows(TokenParams &p, int th, int grid, cudaStream_t st) {
+    return p.n == 1 ? by_threads<1, W32, GRAD>(p, th, grid, st) : p.n == 2 ? by_threads<2, W32, GRAD>(p, th, grid, st)
+                                                                           : by_threads<4, W32, GRAD>(p, th, grid, st);
 }
 
 }  // namespace
 
-bool xent_token_supported(int64_t N, int64_t D) { return N >= 1 && N <= 4 && token_threads(row_class(N), D) > 0; }
+bool xent_token_supported(int64_t N, int64_t D, bool grad) { return N >= 1 && N <= 4 && token_threads(N, D, grad) > 0; }
 
 int xent_token_loss(int htype, const void *hidden, int wtype, const void *W, const int64_t *targets, int64_t N, int64_t V,
                     int64_t D, float2 *part, int64_t ld_part, float *zt, uint32_t *status, int *slots, cudaStream_t st) {
@@ -403,8 +407,9 @@ int xent_token_loss(int htype, const void *hidden, int wtype, const void *W, con
     p.ld_part = ld_part;
     p.zt = zt;
     p.status = status;
-    *slots = token_grid(wtype, N, V, D);
-    return wtype == TLB_W_F32 ? by_rows<true, false>(p, N, *slots, st) : by_rows<false, false>(p, N, *slots, st);
+    const int th = token_threads(N, D, false);
+    *slots = token_grid(wtype, th, V);
+    return wtype == TLB_W_F32 ? by_rows<true, false>(p, th, *slots, st) : by_rows<false, false>(p, th, *slots, st);
 }
 
 int xent_token_grad(int htype, const void *hidden, int wtype, const void *W, const int64_t *targets, const float *lse,
@@ -425,8 +430,8 @@ int xent_token_grad(int htype, const void *hidden, int wtype, const void *W, con
     p.dw = d_w;
     p.dw_add = dw_add;
     p.status = status;
-    const int grid = token_grid(wtype, N, V, D), n = int(N * D);
-    TLB_TRY((wtype == TLB_W_F32 ? by_rows<true, true>(p, N, grid, st) : by_rows<false, true>(p, N, grid, st)));
+    const int th = token_threads(N, D, true), grid = token_grid(wtype, th, V), n = int(N * D);
+    TLB_TRY((wtype == TLB_W_F32 ? by_rows<true, true>(p, th, grid, st) : by_rows<false, true>(p, th, grid, st)));
     TLB_CUDA(launch_dependent(xent_token_sum_kernel, dim3(unsigned(ceil_div(n, 32))), dim3(256), 0, st, partial, grid, int(N), int(D),
                               htype == TLB_W_F32 ? static_cast<float *>(d_hidden) : nullptr,
                               htype == TLB_W_F32 ? nullptr : static_cast<__nv_bfloat16 *>(d_hidden)));
