@@ -20,7 +20,8 @@
 // exactly, and the product is the sum of the term products down to 2^-24 of the first: three
 // with a bf16 partner (exact), six between two float32 operands (x_i y_j with i + j <= 2).
 // With bf16 operands dz is rounded to bf16 once (2^-8 at most, relative to each dz; the sums
-// of it are in fp32): its own error in d_hidden is that of d_hidden's rounding to bf16.
+// of it are in fp32): its error in d_hidden stays below that of d_hidden's rounding to bf16,
+// since the largest dz of most rows, the target's, is kept whole by a factor of the row.
 //
 // The tensor core cuts its fp32 sum after every MMA of 16 products (measured: a sum of 160
 // MMAs comes out about 1.2e-6 of its size short, one of 6144 3e-5).  Results of float32
@@ -85,6 +86,7 @@ struct XParams {
     int64_t ld_part;
     const float *zt;                         // logit of each row's target, from xent_target_kernel
     const float *lse, *dloss;                // kGrad
+    const float2 *scale;                     // (factor of a row of dz, its inverse), or null
     // kOut
     const float *acc;                        // sum of the earlier pieces [M, N], or null
     float *out32;                            // one of the two is written
@@ -184,11 +186,11 @@ __device__ __forceinline__ void stats_row(const XParams &p, float (&z)[BN / 2], 
 // kGrad: what dz needs of this thread's row; fetched a tile ahead.
 struct GradRow {
     int64_t t;
-    float lse, g, zt;
+    float lse, g, zt;                                      // g with the row's factor
 };
 __device__ __forceinline__ GradRow grad_row(const XParams &p, int row) {
     GradRow r{-1, 0.f, 0.f, 0.f};
-    if (row < p.M) r = GradRow{p.targets[row], p.lse[row], p.dloss[row], p.zt[row]};
+    if (row < p.M) r = GradRow{p.targets[row], p.lse[row], p.dloss[row] * (p.scale != nullptr ? p.scale[row].x : 1.f), p.zt[row]};
     return r;
 }
 
@@ -248,7 +250,12 @@ __device__ __forceinline__ void grad_box(const XParams &p, const GradRow &r, flo
 
 // Four columns col.. of one row of a result: the earlier pieces' sum is added, the value
 // stored in the result's type.
-__device__ __forceinline__ void store4(const XParams &p, int row, int col, const float (&v)[4]) {
+__device__ __forceinline__ void store4(const XParams &p, int row, int col, float (&v)[4]) {
+    if (p.scale != nullptr) {
+        const float f = p.scale[row].y;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] *= f;
+    }
     const int64_t e = int64_t(row) * p.N + col;
     if (p.vec) {
         float4 y = make_float4(v[0], v[1], v[2], v[3]);
@@ -287,7 +294,7 @@ __device__ __forceinline__ void out_block(const XParams &p, const float *z, int 
         if (partial != nullptr) {
             *reinterpret_cast<float4 *>(partial + int64_t(r) * ld + c4) = make_float4(a[0], a[1], a[2], a[3]);
         } else {
-            const float v[4] = {a[0], a[1], a[2], a[3]};
+            float v[4] = {a[0], a[1], a[2], a[3]};
             store4(p, row0 + r, col0 + c4, v);
         }
     }
@@ -652,23 +659,29 @@ __global__ void __launch_bounds__(256) xent_fixup_kernel(const __grid_constant__
                     acc.x += v[u].x; acc.y += v[u].y; acc.z += v[u].z; acc.w += v[u].w;
                 }
         }
-        const float v[4] = {acc.x, acc.y, acc.z, acc.w};
+        float v[4] = {acc.x, acc.y, acc.z, acc.w};
         store4(p, row, col, v);
     }
 }
 
-// zt[i] = <hidden[i], W[t_i]> in fp32: a warp a row.
+// zt[i] = <hidden[i], W[t_i]> in fp32: a warp a row.  scale (dz of one bf16 term): the factor, near
+// 1, that makes the target's dz, the largest of most rows, a bf16 number, and its inverse, which
+// goes onto the row's products: so its rounding drops out of the row's gradient.
 template <typename HT, typename WT>
 __global__ void __launch_bounds__(256) xent_target_kernel(const HT *__restrict__ hidden, const WT *__restrict__ W,
                                                           const int64_t *__restrict__ targets, int64_t rows, int64_t vocab,
-                                                          int64_t dim, float *__restrict__ zt) {
+                                                          int64_t dim, float *__restrict__ zt, const float *__restrict__ lse,
+                                                          const float *__restrict__ dloss, float2 *__restrict__ scale) {
     pdl_trigger();
     const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
     if (row >= rows) return;
     const int64_t t = targets[row];
     if (t < 0 || t >= vocab) {
-        if (lane == 0) zt[row] = 0.f;
+        if (lane == 0) {
+            zt[row] = 0.f;
+            if (scale != nullptr) scale[row] = make_float2(1.f, 1.f);
+        }
         return;
     }
     const HT *h = hidden + row * dim;
@@ -692,7 +705,14 @@ __global__ void __launch_bounds__(256) xent_target_kernel(const HT *__restrict__
                 if (c + 32 * k < dim) s[k] = fmaf(float(h[c + 32 * k]), float(w[c + 32 * k]), s[k]);
     }
     const float v = warp_sum((s[0] + s[1]) + (s[2] + s[3]));
-    if (lane == 0) zt[row] = v;
+    if (lane == 0) {
+        zt[row] = v;
+        if (scale != nullptr) {
+            const float dz = expm1f(v - lse[row]) * dloss[row], r = __bfloat162float(__float2bfloat16(dz));
+            const float f = r / dz, inv = dz / r;
+            scale[row] = isfinite(f) && isfinite(inv) && f > 0.f ? make_float2(f, inv) : make_float2(1.f, 1.f);
+        }
+    }
 }
 
 // Joins the (max, sum) pairs of a row's tiles: rx rows x 256 / rx threads a block.  Each
@@ -914,7 +934,7 @@ struct Plan {
     int64_t dp;                  // packed row length
     int64_t piece;               // vocabulary rows of one piece (multiple of 256)
     int64_t part_ld, slots;
-    size_t h, w, dz, part, zt, acc, partial, total;
+    size_t h, w, dz, part, zt, scale, acc, partial, total;
 };
 
 Plan plan_of(int htype, int wtype, int64_t N, int64_t V, int64_t D, bool grad, bool grad_w) {
@@ -935,7 +955,7 @@ Plan plan_of(int htype, int wtype, int64_t N, int64_t V, int64_t D, bool grad, b
     q.h = q.pack_h ? w.take(size_t(q.h_terms) * N * q.dp * 2) : 0;
     q.w = q.pack_w ? w.take(size_t(q.w_terms) * q.piece * q.dp * 2) : 0;
     q.part_ld = q.slots = 0;
-    q.part = q.zt = q.dz = q.acc = q.partial = 0;
+    q.part = q.zt = q.scale = q.dz = q.acc = q.partial = 0;
     if (!grad) {
         q.part_ld = ceil_div(std::min(N, kRowChunk), 32) * 32;
         // 128-wide tiles: the most slots; four an SM for up to four rows
@@ -945,6 +965,7 @@ Plan plan_of(int htype, int wtype, int64_t N, int64_t V, int64_t D, bool grad, b
     } else {
         q.dz = w.take(size_t(q.z_terms) * N * q.piece * 2);
         q.zt = w.take(size_t(N) * 4);
+        q.scale = w.take(size_t(N) * 8);
         if (htype != TLB_W_F32 && q.piece < V) q.acc = w.take(size_t(N) * D * 4);
         q.partial = w.take(size_t(num_sms() + 1) * 2 * kBM * 256 * 4);
     }
@@ -1013,16 +1034,16 @@ bool by_tokens(const Plan &q, int64_t rows, int64_t dim, bool grad) {
 }
 
 int target_logits(int htype, const void *hidden, int wtype, const void *W, const int64_t *targets, int64_t rows, int64_t vocab,
-                  int64_t dim, float *zt, cudaStream_t st) {
+                  int64_t dim, float *zt, const float *lse, const float *dloss, float2 *scale, cudaStream_t st) {
     const unsigned grid = unsigned(ceil_div(rows, 8));
     const float *hf = static_cast<const float *>(hidden);
     const __nv_bfloat16 *hb = static_cast<const __nv_bfloat16 *>(hidden), *wb = static_cast<const __nv_bfloat16 *>(W);
     if (wtype == TLB_W_F32)
-        xent_target_kernel<<<grid, 256, 0, st>>>(hf, static_cast<const float *>(W), targets, rows, vocab, dim, zt);
+        xent_target_kernel<<<grid, 256, 0, st>>>(hf, static_cast<const float *>(W), targets, rows, vocab, dim, zt, lse, dloss, scale);
     else if (htype == TLB_W_F32)
-        xent_target_kernel<<<grid, 256, 0, st>>>(hf, wb, targets, rows, vocab, dim, zt);
+        xent_target_kernel<<<grid, 256, 0, st>>>(hf, wb, targets, rows, vocab, dim, zt, lse, dloss, scale);
     else
-        xent_target_kernel<<<grid, 256, 0, st>>>(hb, wb, targets, rows, vocab, dim, zt);
+        xent_target_kernel<<<grid, 256, 0, st>>>(hb, wb, targets, rows, vocab, dim, zt, lse, dloss, scale);
     return check_launch("xent_target");
 }
 
@@ -1092,7 +1113,7 @@ int tlb_xent_forward(int32_t htype, const void *hidden, int32_t wtype, const voi
             TLB_TRY(head_operand(q, wtype, W, v0, nv, dim, ws, st, w));
             if (v0 == 0)
                 TLB_TRY(target_logits(htype, row_of(hidden, htype, r0, dim), wtype, W, targets + r0, n, vocab, dim,
-                                      ws_at<float>(ws, q.zt) + r0, st));
+                                      ws_at<float>(ws, q.zt) + r0, nullptr, nullptr, nullptr, st));
             XParams p;
             memset(&p, 0, sizeof(p));
             p.M = int(n);
@@ -1139,11 +1160,15 @@ int tlb_xent_backward(int32_t htype, const void *hidden, int32_t wtype, const vo
     Mat h;
     TLB_TRY(hidden_operand(q, htype, hidden, rows, dim, d_w != nullptr ? targets : nullptr, vocab, ws, st, h));
     const bool wide = htype == TLB_W_F32;
+    // factors of dz's rows would stay in d_w's sums over the rows
+    float2 *scale = q.z_terms == 1 && d_w == nullptr ? ws_at<float2>(ws, q.scale) : nullptr;
     for (int64_t v0 = 0; v0 < vocab; v0 += q.piece) {
         const int64_t nv = std::min(q.piece, vocab - v0);
         Mat w;
         TLB_TRY(head_operand(q, wtype, W, v0, nv, dim, ws, st, w));
-        if (v0 == 0) TLB_TRY(target_logits(htype, hidden, wtype, W, targets, rows, vocab, dim, ws_at<float>(ws, q.zt), st));
+        if (v0 == 0)
+            TLB_TRY(target_logits(htype, hidden, wtype, W, targets, rows, vocab, dim, ws_at<float>(ws, q.zt), lse, d_loss, scale,
+                                  st));
         const Mat dz{ws_at<__nv_bfloat16>(ws, q.dz), rows, nv, q.piece, rows * q.piece, q.z_terms};
         {
             XParams p;
@@ -1156,6 +1181,7 @@ int tlb_xent_backward(int32_t htype, const void *hidden, int32_t wtype, const vo
             p.lse = lse;
             p.dloss = d_loss;
             p.zt = ws_at<float>(ws, q.zt);
+            p.scale = scale;
             for (int t = 0; t < q.z_terms; ++t)
                 TLB_TRY(make_map(&p.d[t], dz.p + t * dz.plane, rows, nv, dz.ld, 32));
             p.status = ws_at<uint32_t>(ws, 0);
@@ -1171,6 +1197,7 @@ int tlb_xent_backward(int32_t htype, const void *hidden, int32_t wtype, const vo
             float *sum = wide ? static_cast<float *>(d_hidden) : ws_at<float>(ws, q.acc);
             const bool last = v0 + nv == vocab;
             p.acc = v0 > 0 ? sum : nullptr;
+            p.scale = scale;
             if (wide || !last) p.out32 = sum;
             else p.out16 = static_cast<__nv_bfloat16 *>(d_hidden);
             p.vec = dim % 4 == 0 && aligned16(d_hidden);
