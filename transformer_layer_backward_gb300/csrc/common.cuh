@@ -167,6 +167,25 @@ __device__ __forceinline__ void l2_prefetch(const void *p, uint32_t bytes) {
     asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
 }
 
+// exp(x) - 1.  Near 0 the Taylor series, so that a small difference keeps its digits: eight
+// terms leave 0.5^8 / 9! x 2 = 2e-8 of the result at |x| = 1/2; beyond, the difference itself,
+// of a power of two that is 2^-22 off: 6e-7 of the result at most.
+__device__ __forceinline__ float exp_minus_1(float x) {
+    if (fabsf(x) < 0.5f) {
+        float s = fmaf(x, 1.f / 8.f, 1.f);
+        s = fmaf(s * x, 1.f / 7.f, 1.f);
+        s = fmaf(s * x, 1.f / 6.f, 1.f);
+        s = fmaf(s * x, 1.f / 5.f, 1.f);
+        s = fmaf(s * x, 1.f / 4.f, 1.f);
+        s = fmaf(s * x, 1.f / 3.f, 1.f);
+        s = fmaf(s * x, 1.f / 2.f, 1.f);
+        return s * x;
+    }
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    return y - 1.f;
+}
+
 __device__ __forceinline__ float dot4(float4 a, float4 b) {
     return a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
 }

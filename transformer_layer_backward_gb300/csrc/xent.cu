@@ -208,7 +208,7 @@ __device__ __forceinline__ void grad_box(const XParams &p, const GradRow &r, flo
     if (tc >= 0 && tc < min(64, p.N - col0)) {
         int k = int(tc);
         asm("" : "+r"(k));                                 // compared, never an index: y stays in registers
-        const float pt1 = expm1f(r.zt - r.lse);            // p - 1 of the target, exact also where p is near 1
+        const float pt1 = exp_minus_1(r.zt - r.lse);            // p - 1 of the target, exact also where p is near 1
 #pragma unroll
         for (int c = 0; c < 64; ++c)
             if (c == k) y[c] = pt1;
@@ -708,7 +708,7 @@ __global__ void __launch_bounds__(256) xent_target_kernel(const HT *__restrict__
     if (lane == 0) {
         zt[row] = v;
         if (scale != nullptr) {
-            const float dz = expm1f(v - lse[row]) * dloss[row], r = __bfloat162float(__float2bfloat16(dz));
+            const float dz = exp_minus_1(v - lse[row]) * dloss[row], r = __bfloat162float(__float2bfloat16(dz));
             const float f = r / dz, inv = dz / r;
             scale[row] = isfinite(f) && isfinite(inv) && f > 0.f ? make_float2(f, inv) : make_float2(1.f, 1.f);
         }

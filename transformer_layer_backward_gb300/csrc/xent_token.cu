@@ -73,13 +73,14 @@ __device__ __forceinline__ float2 unpack(const Pair<W32> &p) {
 
 // Pairs of columns a thread's registers hold: of the hidden rows, and for the gradient of
 // d_hidden's rows and of a block of head rows too.
-template <int N, bool GRAD> constexpr int rounds() { return N == 1 ? 6 : N == 2 || !GRAD ? 5 : 3; }
+// (A round that no column needs costs as much: 256 threads with 6 take 45 us for 2560, with 5 38.)
+constexpr int rounds(int64_t N, bool grad, int threads) { return N == 1 && threads == 512 ? 6 : N <= 2 || !grad ? 5 : 3; }
 
 // TH threads: 512, one CTA an SM, or 256 or 128, two or four CTAs, which wait at barriers of
 // their own: as few threads as hold the columns in R pairs each.
 template <int TH, int N, bool W32, bool GRAD>
 __global__ void __launch_bounds__(TH, 512 / TH) xent_token_kernel(const __grid_constant__ TokenParams p) {
-    constexpr int kThreads = TH, kWarps = TH / 32, R = rounds<N, GRAD>();
+    constexpr int kThreads = TH, kWarps = TH / 32, R = rounds(N, GRAD, TH);
     constexpr int VB = block_rows<W32>(), NV = VB * N;
     constexpr int SH = NV == 32 ? 0 : NV == 16 ? 1 : NV == 8 ? 2 : 3;      // lane >> SH: the lane's value
     static_assert((NV << SH) == 32, "values a warp reduces");
@@ -144,21 +145,37 @@ __global__ void __launch_bounds__(TH, 512 / TH) xent_token_kernel(const __grid_c
             }
         }
     }
-    // the pair of columns c, c + 1 of head row v of a block
-    auto pair_at = [&](const void *src, int v, int c) {
-        Pair<W32> x = {};
+    // x[v][r]: this thread's pairs of the first `rows` head rows at src
+    auto take = [&](const void *src, int rows, Pair<W32> (&x)[VB][R]) {
         if (!odd) {
-            x = *reinterpret_cast<const Pair<W32> *>(static_cast<const char *>(src) + (size_t(v) * D + c) * (W32 ? 4 : 2));
-        } else if constexpr (W32) {
-            const float *q = static_cast<const float *>(src) + size_t(v) * D + c;
-            x.v.x = q[0];
-            if (c + 1 < D) x.v.y = q[1];
-        } else {
-            const uint16_t *q = static_cast<const uint16_t *>(src) + size_t(v) * D + c;
-            x.v = q[0];
-            if (c + 1 < D) x.v |= uint32_t(q[1]) << 16;
+#pragma unroll
+            for (int v = 0; v < VB; ++v)
+#pragma unroll
+                for (int r = 0; r < R; ++r) {
+                    const int c = 2 * (tid + r * kThreads);
+                    x[v][r] = {};
+                    if (c < D && v < rows)
+                        x[v][r] = *reinterpret_cast<const Pair<W32> *>(static_cast<const char *>(src) + (size_t(v) * D + c) * (W32 ? 4 : 2));
+                }
+            return;
         }
-        return x;
+#pragma unroll
+        for (int v = 0; v < VB; ++v)
+#pragma unroll
+            for (int r = 0; r < R; ++r) {
+                const int c = 2 * (tid + r * kThreads);
+                x[v][r] = {};
+                if (c >= D || v >= rows) continue;
+                if constexpr (W32) {
+                    const float *q = static_cast<const float *>(src) + size_t(v) * D + c;
+                    x[v][r].v.x = q[0];
+                    if (c + 1 < D) x[v][r].v.y = q[1];
+                } else {
+                    const uint16_t *q = static_cast<const uint16_t *>(src) + size_t(v) * D + c;
+                    x[v][r].v = q[0];
+                    if (c + 1 < D) x[v][r].v |= uint32_t(q[1]) << 16;
+                }
+            }
     };
     float m = -INFINITY, sum = 0.f;
     bool ok = true;
@@ -169,25 +186,9 @@ __global__ void __launch_bounds__(TH, 512 / TH) xent_token_kernel(const __grid_c
         Pair<W32> x[VB][R];
         if (staged) {
             ok = mbar_wait(&full[i % stages], (i / stages) & 1, p.status, 30u);
-            const uint8_t *src = smem + size_t(i % stages) * bytes;
-#pragma unroll
-            for (int v = 0; v < VB; ++v)
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const int c = 2 * (tid + r * kThreads);
-                    x[v][r] = {};
-                    if (c < D) x[v][r] = pair_at(src, v, c);
-                }
+            take(smem + size_t(i % stages) * bytes, VB, x);
         } else {
-            const char *src = w + b * bytes;
-#pragma unroll
-            for (int v = 0; v < VB; ++v)
-#pragma unroll
-                for (int r = 0; r < R; ++r) {
-                    const int c = 2 * (tid + r * kThreads);
-                    x[v][r] = {};
-                    if (c < D && v < rows) x[v][r] = pair_at(src, v, c);
-                }
+            take(w + b * bytes, rows, x);
         }
         float s[NV];
 #pragma unroll
@@ -236,7 +237,9 @@ __global__ void __launch_bounds__(TH, 512 / TH) xent_token_kernel(const __grid_c
                 if (row == t && (lane & ((1 << SH) - 1)) == 0) p.zt[vn] = z;
             }
         } else {
-            float dz = row == t ? expm1f(z - lse) : ex2((z - lse) * kLog2e);    // p - 1, exact also where p is near 1
+            float dz = ex2((z - lse) * kLog2e);
+            if (__any_sync(0xffffffffu, row == t))
+                dz = row == t ? exp_minus_1(z - lse) : dz;       // p - 1, exact also where p is near 1
             dz = has && vr < rows ? dz * g : 0.f;
 #pragma unroll
             for (int v = 0; v < VB; ++v) {
@@ -323,29 +326,29 @@ __global__ void __launch_bounds__(TH, 512 / TH) xent_token_kernel(const __grid_c
     }
 }
 
-// d_hidden: the CTAs' parts added up, 32 elements x 8 threads a block, in a fixed order.
-__global__ void __launch_bounds__(256) xent_token_sum_kernel(const float *__restrict__ partial, int parts, int rows, int D,
-                                                             float *out32, __nv_bfloat16 *out16) {
-    __shared__ float sh[8][32];
+// d_hidden: the CTAs' parts added up, 32 elements x 32 threads a block, in a fixed order.
+__global__ void __launch_bounds__(1024) xent_token_sum_kernel(const float *__restrict__ partial, int parts, int rows, int D,
+                                                              float *out32, __nv_bfloat16 *out16) {
+    __shared__ float sh[32][33];
     const int x = threadIdx.x & 31, y = threadIdx.x >> 5, e = blockIdx.x * 32 + x;
-    const int ld = D + (D & 1), n = rows * D, row = e / D;
+    const int ld = D + (D & 1), n = rows * D, row = e / D, step = rows * ld;
     const float *src = partial + row * ld + (e - row * D);
     pdl_wait();
     float s = 0.f;
-    for (int k = y; k < parts && e < n; k += 64) {
+    for (int k = y; k < parts && e < n; k += 256) {
         float v[8];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) v[u] = k + 8 * u < parts ? src[int64_t(k + 8 * u) * rows * ld] : 0.f;
+        for (int u = 0; u < 8; ++u) v[u] = k + 32 * u < parts ? src[int64_t(k + 32 * u) * step] : 0.f;
 #pragma unroll
         for (int u = 0; u < 8; ++u) s += v[u];
     }
     sh[y][x] = s;
     __syncthreads();
-    if (y == 0 && e < n) {
-#pragma unroll
-        for (int k = 1; k < 8; ++k) s += sh[k][x];
-        if (out32 != nullptr) out32[e] = s;
-        else out16[e] = __float2bfloat16(s);
+    s = warp_sum(sh[x][y]);                                 // a warp an element
+    const int o = blockIdx.x * 32 + y;
+    if (x == 0 && o < n) {
+        if (out32 != nullptr) out32[o] = s;
+        else out16[o] = __float2bfloat16(s);
     }
 }
 
@@ -365,9 +368,8 @@ int launch(TokenParams &p, int grid, cudaStream_t st) {
 // of head rows (the gradient of one token over 32768 x 2560 takes 43 us with one CTA of 512
 // threads an SM, 30 us with two of 256).
 int token_threads(int64_t N, int64_t D, bool grad) {
-    const int r = N == 1 ? 6 : N == 2 || !grad ? 5 : 3;
     for (int th = 128; th <= 512; th *= 2)
-        if (D <= int64_t(2) * th * r) return th;
+        if (D <= int64_t(2) * th * rounds(N, grad, th)) return th;
     return 0;
 }
 
@@ -432,7 +434,7 @@ int xent_token_grad(int htype, const void *hidden, int wtype, const void *W, con
     p.status = status;
     const int th = token_threads(N, D, true), grid = token_grid(wtype, th, V), n = int(N * D);
     TLB_TRY((wtype == TLB_W_F32 ? by_rows<true, true>(p, th, grid, st) : by_rows<false, true>(p, th, grid, st)));
-    TLB_CUDA(launch_dependent(xent_token_sum_kernel, dim3(unsigned(ceil_div(n, 32))), dim3(256), 0, st, partial, grid, int(N), int(D),
+    TLB_CUDA(launch_dependent(xent_token_sum_kernel, dim3(unsigned(ceil_div(n, 32))), dim3(1024), 0, st, partial, grid, int(N), int(D),
                               htype == TLB_W_F32 ? static_cast<float *>(d_hidden) : nullptr,
                               htype == TLB_W_F32 ? nullptr : static_cast<__nv_bfloat16 *>(d_hidden)));
     return check_launch("xent_token_sum");
