@@ -304,9 +304,10 @@ typedef struct {
  *   m <- momentum m + g;   u = nesterov ? g + momentum m : m;   X = u / (|u|_F + eps)
  *   X <- a X + b (X X^T) X + c (X X^T)^2 X     `steps` times
  *   p <- p - lr lr_mult (weight_decay p + scale X)
- * All in float32; a zero update gives X = 0.  The matrices must not overlap, within the call
- * or with one another; any alignment of 4 bytes goes (16 is faster).  Same inputs, same bits.
- * ws: 256-byte aligned, tlb_muon_workspace_bytes() of these shapes (their pointers are not
+ * All in float32; a zero update gives X = 0.  |u|_F comes from float32 squares: it should lie
+ * between 1e-18 and 1e18 (or be 0).  The matrices must not overlap, within the call or with
+ * one another; any alignment of 4 bytes goes (16 is faster).  Same inputs, same bits.
+ * ws: zero-filled once, 256-byte aligned, tlb_muon_workspace_bytes() of these shapes (their pointers are not
  * looked at; 0 for shapes that the call refuses). */
 size_t tlb_muon_workspace_bytes(const tlb_muon_mat *mats, int32_t n);
 int tlb_muon(const tlb_muon_mat *mats, int32_t n, const tlb_muon_cfg *cfg, void *ws, size_t ws_bytes, void *stream);
@@ -326,16 +327,20 @@ int tlb_muon(const tlb_muon_mat *mats, int32_t n, const tlb_muon_cfg *cfg, void 
  * lse hold; its lse is that of its logits all the same.
  *
  * Types (TLB_W_F32, TLB_W_BF16): hidden and W both bf16; hidden f32 with W bf16 or f32.
- * d_hidden and d_w (both overwritten) have hidden's type.  All run on the tcgen05 tensor
- * cores with fp32 sums.  bf16 hidden: dz is rounded to bf16 once as the operand of the
- * gradient products.  f32 hidden: every float32 operand, dz included, is taken apart into
- * three bf16 terms that hold all its 24 bits, for results of float32 precision at a third
- * (W bf16) or a sixth (W f32) of the speed.
+ * d_hidden and d_w (both overwritten) have hidden's type.  Up to four rows (sixteen with a
+ * float32 head) run on a kernel that reads the head once, in fp32 throughout (dim up to a few
+ * thousand), more on the tcgen05 tensor cores with fp32 sums.  On the tensor cores:
+ * bf16 hidden: dz is rounded to bf16 as the operand of the gradient products, for up to 64
+ * rows to two bf16 terms (16 bits); beyond, where d_w is NULL, a factor of each row keeps its
+ * target's dz free of rounding.  f32 hidden: every float32 operand, dz included, is taken
+ * apart into three bf16 terms that hold all its 24 bits, for results of float32 precision at
+ * a third (W bf16) or a sixth (W f32) of the speed.  The target's own logit is summed in fp32.
  *
  * rows >= 0 (0 rows: no-op, d_w set to 0), vocab >= 1, dim >= 1, of any size up to 2^24,
  * 2^24 and 2^20 (dim % 8 != 0 costs a padded copy of the operands).  The backward pass walks
  * through the vocabulary in pieces whose dz stays in the workspace (512 MB at most; at
- * least 2048 columns).  Same inputs, same bits: no sum depends on timing.
+ * least 2048 columns).  Same inputs, same bits: no sum depends on timing.  d_hidden may be
+ * hidden itself; no other output may overlap an input or another output.
  * ws: zero-filled once, 256-byte aligned, tlb_xent_workspace_bytes() bytes (enough for both
  * calls; 0 for sizes or types that the calls refuse).  grad_w: whether d_w will be asked for. */
 size_t tlb_xent_workspace_bytes(int32_t htype, int32_t wtype, int64_t rows, int64_t vocab, int64_t dim, int32_t grad_w);

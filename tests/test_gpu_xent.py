@@ -99,19 +99,17 @@ def test_xent(lib, rows, vocab, dim, types):
                                             (15, 600, 1025), (17, 400, 130), (12, 999, 3073), (12, 700, 832),
                                             (13, 700, 832), (10, 20011, 832)])
 def test_few_rows(lib, rows, vocab, dim, types):
-    """Up to four rows take the one-pass kernel, up to twelve float32 rows take it in turns, and
-    sixteen where the head would have to be packed (float32, odd lengths); blocks of head rows that are not full,
-    lengths past what the registers hold, and one row more beside them."""
+    """Up to four rows take the one-pass kernel, and with a float32 head up to sixteen, in turns;
+    blocks of head rows that are not full, lengths past what the registers hold, and one row
+    more beside them."""
     n0 = lib.launch_count()
     test_xent(lib, rows, vocab, dim, types)
     names = lib.launch_names(n0)
     turns = [min(4, rows - r) for r in range(0, rows, 4)]
-    packed = types[1] == "f32" or dim % 8 != 0
     for name, four in (("xent_token_loss", 5), ("xent_token_grad", 3)):
         fits = all(dim <= 1024 * {1: 6, 2: 5}.get(n, four) for n in turns)
-        assert (name in names) == (fits and rows <= (16 if packed else 12 if types[0] == "f32" else 4)), names
-    if types[0] == "bf16" and rows > 4:                      # d_w of several turns is summed in float32 only
-        assert "xent_dw" in names
+        assert (name in names) == (fits and rows <= (16 if types[1] == "f32" else 4)), names
+    assert ("xent_dw" in names) == ("xent_token_grad" not in names)
 
 
 @pytest.mark.parametrize("types", TYPES, ids="-".join)
@@ -327,3 +325,41 @@ def test_empty_and_refused(lib):
         lib.xent_forward(flat[1:].view(3, 16), w.bfloat16(), t)
     with pytest.raises(lib.TlbError, match="workspace"):
         lib.xent_forward(h, w.bfloat16(), t, ws=torch.zeros(256, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("types,rows,grad_w", [(("bf16", "bf16"), 3, True), (("bf16", "bf16"), 70, True),
+                                               (("bf16", "bf16"), 300, False), (("f32", "bf16"), 10, True),
+                                               (("f32", "f32"), 40, True)])
+def test_gradient_in_place_of_the_hidden_rows(lib, types, rows, grad_w):
+    """d_hidden may be hidden itself: the same bits, in one piece of the vocabulary or several."""
+    import torch
+    for vocab, dim in ((700, 96), (2100 if rows < 100 else 900000, 33)):
+        th, tw, _, _, t, g = problem(rows, vocab, dim, types)
+        tt, tg = torch.from_numpy(t).cuda(), dev(g)
+        _, lse = lib.xent_forward(th, tw, tt)
+        dh, dw = lib.xent_backward(th, tw, tt, lse, tg, grad_w=grad_w)
+        same, dw2 = lib.xent_backward(th, tw, tt, lse, tg, d_hidden=th, grad_w=grad_w)
+        assert same is th and torch.equal(th, dh)
+        assert not grad_w or torch.equal(dw, dw2)
+
+
+def test_what_is_allocated_belongs_to_the_given_stream(lib, monkeypatch):
+    import torch
+    th, tw, _, _, t, g = problem(20, 600, 64, ("bf16", "bf16"))
+    tt, tg = torch.from_numpy(t).cuda(), dev(g)
+    loss, lse = lib.xent_forward(th, tw, tt)
+    dh, _ = lib.xent_backward(th, tw, tt, lse, tg)
+    side, seen = torch.cuda.Stream(), []
+    make = lib.api.xent_workspace
+
+    def recorded(*args, **kw):
+        seen.append(torch.cuda.current_stream())
+        return make(*args, **kw)
+
+    monkeypatch.setattr(lib.api, "xent_workspace", recorded)
+    side.wait_stream(torch.cuda.current_stream())
+    loss2, lse2 = lib.xent_forward(th, tw, tt, stream=side)
+    dh2, _ = lib.xent_backward(th, tw, tt, lse2, tg, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert seen == [side, side]
+    assert torch.equal(loss, loss2) and torch.equal(lse, lse2) and torch.equal(dh, dh2)

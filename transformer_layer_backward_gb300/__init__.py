@@ -15,6 +15,7 @@ from .api import (act_backward, adamw, adamw_cfg, adamw_cfg_of, attn_backward, d
 
 __all__ = ["TlbError", "load", "act_backward", "adamw", "adamw_cfg", "adamw_cfg_of", "attn_backward", "debug_skip_barrier_arrival",
            "ffn_backward", "layer_acts", "layer_backward", "layer_cfg", "layer_cfg_of", "layer_weights", "launch_count", "launch_names", "linear_backward", "linear_workspace", "lora",
-           "lora_grad_adamw", "lora_grad_adamw_noalloc", "muon", "muon_cfg", "muon_mats", "muon_workspace", "profile_events", "rmsnorm_backward", "rope_backward", "softmax_backward",
+           "lora_grad_adamw", "lora_grad_adamw_noalloc", "muon", "muon_cfg", "muon_mats", "muon_workspace", "profile_events",
+           "rmsnorm_backward", "rope_backward", "softmax_backward",
            "stack_backward", "stack_workspace", "workspace", "workspace_bytes", "workspace_status",
            "xent_backward", "xent_forward", "xent_workspace", "_abi"]

@@ -22,9 +22,16 @@ _WCODE = {"f32": A.W_F32, "bf16": A.W_BF16, "ternary": A.W_TERNARY_I8, "ternary2
 _NO_GUARD = contextlib.nullcontext()
 
 
-def _on_device(t):
-    """Guard that makes the tensor's device the current one, for the launch and the stream."""
-    if not t.is_cuda or t.device.index == torch.cuda.current_device():
+def _queued(t, stream=None):
+    """Guard for work on t: its device is the current one, and so is the stream that the work is
+    queued on, to which what is allocated meanwhile then belongs."""
+    if not t.is_cuda:
+        return _NO_GUARD
+    if isinstance(stream, torch.cuda.Stream):
+        if stream.device != t.device:
+            raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, t.device))
+        return torch.cuda.stream(stream)
+    if t.device.index == torch.cuda.current_device():
         return _NO_GUARD
     return torch.cuda.device(t.device)
 
@@ -200,7 +207,7 @@ def muon(mats, cfg: A.MuonCfg, ws, stream=None):
     made orthogonal by Newton-Schulz steps, weight decay.  The counterpart of adamw()."""
     if mats.device is not None and ws.device != mats.device:
         raise ValueError("ws is on %s, the matrices on %s" % (ws.device, mats.device))
-    with _on_device(ws):
+    with _queued(ws, stream):
         A.call("tlb_muon", mats, mats.n, C.byref(cfg), _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream))
 
 
@@ -242,10 +249,10 @@ def xent_forward(hidden, W, targets, loss=None, lse=None, ws=None, stream=None):
     the logits: (loss, lse).  Targets (int64) outside [0, vocab) mark rows without one."""
     rows, vocab, dim = _xent_shapes(hidden, W, targets, ws, loss=loss, lse=lse)
     ht, wt = _xent_code(hidden.dtype, "hidden"), _xent_code(W.dtype, "W")
-    loss = torch.empty(rows, device=hidden.device) if loss is None else loss
-    lse = torch.empty(rows, device=hidden.device) if lse is None else lse
-    ws = xent_workspace(hidden.dtype, W.dtype, rows, vocab, dim, device=hidden.device) if ws is None else ws
-    with _on_device(hidden):
+    with _queued(hidden, stream):
+        loss = torch.empty(rows, device=hidden.device) if loss is None else loss
+        lse = torch.empty(rows, device=hidden.device) if lse is None else lse
+        ws = xent_workspace(hidden.dtype, W.dtype, rows, vocab, dim, device=hidden.device) if ws is None else ws
         A.call("tlb_xent_forward", ht, _ptr(hidden, None, "hidden"), wt, _ptr(W, None, "W"),
                _ptr(targets, torch.int64, "targets"), rows, vocab, dim, _ptr(loss, name="loss"), _ptr(lse, name="lse"),
                _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream))
@@ -257,15 +264,15 @@ def xent_backward(hidden, W, targets, lse, d_loss, d_hidden=None, d_w=None, grad
     None unless grad_w is set or a tensor for it is given.  lse as xent_forward returned it."""
     rows, vocab, dim = _xent_shapes(hidden, W, targets, ws, lse=lse, d_loss=d_loss)
     ht, wt = _xent_code(hidden.dtype, "hidden"), _xent_code(W.dtype, "W")
-    d_hidden = torch.empty_like(hidden) if d_hidden is None else d_hidden
-    if d_w is None and grad_w:
-        d_w = torch.empty(vocab, dim, dtype=hidden.dtype, device=hidden.device)
-    for name, t, shape in (("d_hidden", d_hidden, hidden.shape), ("d_w", d_w, W.shape)):
-        if t is not None and (t.shape != shape or t.device != hidden.device):
-            raise ValueError("%s must have shape %s on %s" % (name, tuple(shape), hidden.device))
-    if ws is None:
-        ws = xent_workspace(hidden.dtype, W.dtype, rows, vocab, dim, d_w is not None, hidden.device)
-    with _on_device(hidden):
+    with _queued(hidden, stream):
+        d_hidden = torch.empty_like(hidden) if d_hidden is None else d_hidden
+        if d_w is None and grad_w:
+            d_w = torch.empty(vocab, dim, dtype=hidden.dtype, device=hidden.device)
+        for name, t, shape in (("d_hidden", d_hidden, hidden.shape), ("d_w", d_w, W.shape)):
+            if t is not None and (t.shape != shape or t.device != hidden.device):
+                raise ValueError("%s must have shape %s on %s" % (name, tuple(shape), hidden.device))
+        if ws is None:
+            ws = xent_workspace(hidden.dtype, W.dtype, rows, vocab, dim, d_w is not None, hidden.device)
         A.call("tlb_xent_backward", ht, _ptr(hidden, None, "hidden"), wt, _ptr(W, None, "W"),
                _ptr(targets, torch.int64, "targets"), _ptr(lse, name="lse"), _ptr(d_loss, name="d_loss"), rows, vocab,
                dim, _ptr(d_hidden, hidden.dtype, "d_hidden"), _ptr(d_w, hidden.dtype, "d_w"),

@@ -16,15 +16,28 @@
 // by 1e2, emulated in fp32: 3e-7 to 3e-6, as five steps each with a Gram matrix of its own have
 // (4e-7 to 1e-6); three steps before two give up to 1.3e-5, five in one run up to 5e-5.
 //
-// Launches for five steps, over all matrices of a rank class together (class: r rounded up to
-// 8, 16, 32 or 64):
-//   pass   m', u = f(g, m); partial Gram matrices of column chunks
-//   poly   sums them in order, |u|_F from the trace, two steps' product M
-//   pass   u again from g and m'; Y = M u to the workspace; partial Gram matrices of Y
-//   poly   three steps' product M
-//   pass   X = M Y; p updated
-// Bounds: HBM for r <= 16 (20 bytes an element that must move; g and m' a second time and Y
-// come from L2 while they fit it), fp32 FMAs for r = 64 (3 r of them an element and pass pair).
+// Two ways, chosen by shape; all matrices of one rank class (r rounded up to 8, 16, 32 or 64) and
+// way go in one launch (of each kind):
+//   cluster  X fits the shared memory of up to eight CTAs (n <= 8192, 5632, 4096, 2048 by class; a
+//            class 64 of few matrices only, see in_cluster): one launch, X never leaves the SMs
+//   passes   five launches for five steps, with r x r work between reads of the matrix:
+//     pass   m', u = f(g, m); partial Gram matrices of column chunks
+//     poly   sums them in order, |u|_F from the trace, two steps' product M
+//     pass   u again from g and m'; Y = M u to the workspace; partial Gram matrices of Y
+//     poly   three steps' product M
+//     pass   X = M Y; p updated
+//   The passes run on the CUDA cores for r <= 32, on tcgen05 with every float as three bf16 terms
+//   for r > 32, where 3 r FMAs an element would bound them.
+//
+// Bounds, and measured (five steps):
+//   one 16 x 2560 matrix: latency of the phases, 16 us in one launch (20 bytes an element are 0.1 us)
+//   144 rank-16 matrices of a 36-layer stack, 118 MB to move (17.4 us): 53 us in one launch.  Its CTAs
+//     go through reading, r x r products and writing in step, so that HBM idles in the middle:
+//     two reads and two Gram sums of X in shared memory, then two chains of r x r products
+//   seven 5 x 1001 and three 999 x 33 matrices: 74 us in two launches, chains of 14 r x r products
+//   144 rank-64 matrices, 472 MB (69.6 us; 189 MB read by each pass): 349 us = passes of 70, 118 and
+//     98 us and r x r products of 20 and 29 us; the passes wait for loads and for taking floats
+//     apart (DRAM 28 to 44 % busy, tensor pipe 16 %)
 #include <algorithm>
 #include <cmath>
 #include <cstring>

@@ -37,7 +37,10 @@
 // its error), and the read of W hides a second product: dz is kept in two terms there.
 //
 // Bounds: N >= 512 rows is bound by the tensor pipe (2 N V D flops a product), few rows by
-// the read of W.
+// the read of W.  Measured at 2048 x 2560 x 131072 in bf16 (727 us a product at the rate of a large
+// library product, 1.89 PFLOP/s): loss 771 us, dz 780 us, dz W 784 us each alone, 1.78 PFLOP/s;
+// 862 and 1755 us for the calls back to back, where the power limit sets the clock.  4096 x 2560 x
+// 65536 with d_w: 2.70 ms (2.18).  Float32 rows, 512 x 2560 x 32768: 400 us (273: three products).
 #include <cuda.h>
 
 #include <algorithm>
@@ -1023,13 +1026,15 @@ int head_operand(const Plan &q, int wtype, const void *W, int64_t v0, int64_t n,
     return pack(src, wtype, n, D, q.dp, q.w_terms, nullptr, 0, y, st);
 }
 
-// Few rows take the kernel that reads the head once for up to four rows, in turns of four: one
-// turn beside bf16 tensor-core products (which read the head once for a loss), up to three
-// beside float32 rows' (three products of every tile: 10 rows x 832 x 110656, gradient, 130
-// against 186 us), up to four where the tensor-core route would write the head again to pack it.
+// Up to four rows take the kernel that reads the head once, and with a float32 head, which the
+// tensor-core route writes again as three terms, up to sixteen, in turns of four.  Measured, loss
+// and gradient in us, 32768 x 2560 | 110656 x 832, turns against tensor cores:
+//   bf16                 4 rows: 40, 77 against 44, 91 | 1024 wide, 151936: 75, 153 against 78, 154
+//   float32 and bf16     4 rows: 38, 76 against 82, 147 | 56, 114 against 77, 162;   8 rows: 75, 152 | 111, 226
+//   float32             12 rows: 165, 284 | 204, 419;   13: 219, 342 | 269, 488 against 294, 410 | 430, 598
 bool by_tokens(const Plan &q, int64_t rows, int64_t dim, bool grad) {
     const int64_t turns = ceil_div(rows, 4), last = rows - 4 * (turns - 1);
-    return turns <= (q.pack_w ? 4 : q.h_terms > 1 ? 3 : 1) && xent_token_supported(std::min<int64_t>(rows, 4), dim, grad) &&
+    return turns <= (q.w_terms > 1 ? 4 : 1) && xent_token_supported(std::min<int64_t>(rows, 4), dim, grad) &&
            xent_token_supported(last, dim, grad);
 }
 
@@ -1148,8 +1153,8 @@ int tlb_xent_backward(int32_t htype, const void *hidden, int32_t wtype, const vo
     const Plan q = plan_of(htype, wtype, rows, vocab, dim, true, d_w != nullptr);
     TLB_REQUIRE(ws != nullptr && (reinterpret_cast<uintptr_t>(ws) & 255) == 0 && ws_bytes >= q.total, TLB_EINVAL,
                 "xent_backward: needs a 256-byte aligned workspace of %zu bytes", q.total);
-    // several turns add to d_w, which only float32 can hold
-    if (by_tokens(q, rows, dim, true) && aligned16(d_w) && (d_w == nullptr || rows <= 4 || htype == TLB_W_F32)) {
+    // (several turns add to d_w, in float32: a float32 head goes with float32 rows)
+    if (by_tokens(q, rows, dim, true) && aligned16(d_w)) {
         for (int64_t r0 = 0; r0 < rows; r0 += 4)
             TLB_TRY(xent_token_grad(htype, row_of(hidden, htype, r0, dim), wtype, W, targets + r0, lse + r0, d_loss + r0,
                                     std::min<int64_t>(4, rows - r0), vocab, dim,

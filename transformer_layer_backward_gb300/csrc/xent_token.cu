@@ -7,8 +7,9 @@
 // and used for both z and dz W (and the block's rows of d_w), so W crosses once.  All
 // arithmetic is fp32: z, the softmax and dz are never rounded to fewer bits.
 //
-// One CTA of 16 warps an SM, or two of 8.  A thread owns the same column pairs of every head row: its part
-// of the hidden rows and of d_hidden stays in registers.  Per block of 8 rows (4 of float32):
+// One CTA of 16 warps an SM, two of 8 or four of 4.  A thread owns the same column pairs of every
+// head row: its part of the hidden rows and of d_hidden stays in registers.  Per block of 8 head
+// rows (4 of float32):
 //   the thread's W values into registers; its share of the 8 N dot products
 //   warp sums by exchange (a lane ends with one of the 8 N values), 16 warps' sums in shared
 //   memory, one barrier: the slot is free for the copy of a later block, and every warp
@@ -17,8 +18,9 @@
 //   shuffles, times the W values still in registers
 // A CTA's statistics, or its part of d_hidden, are joined in CTA order by a second kernel.
 //
-// Measured: one token, 32768 x 2560 bf16 (168 MB, 24.7 us of reading at the copy rate): see
-// the launchers.
+// Measured: one token, 32768 x 2560 bf16 (168 MB, 24.7 us of reading at the copy rate): loss 28 us
+// (70 % of DRAM's time busy; 33 us with the join), gradient 31 us (63 %; 37 us with the sum).  The
+// first blocks' way from DRAM and the last CTA's end are the rest.
 #include <algorithm>
 #include <cstring>
 
@@ -75,6 +77,24 @@ __device__ __forceinline__ float2 unpack(const Pair<W32> &p) {
 // d_hidden's rows and of a block of head rows too.
 // (A round that no column needs costs as much: 256 threads with 6 take 45 us for 2560, with 5 38.)
 constexpr int rounds(int64_t N, bool grad, int threads) { return N == 1 && threads == 512 ? 6 : N <= 2 || !grad ? 5 : 3; }
+
+// Sums of the first CNT values over the warp: each exchange halves the values that a lane holds,
+// then plain sums, so that s[0] of lane l is the sum of value l >> (5 - log2 CNT).
+template <int CNT, int OFF>
+__device__ __forceinline__ void warp_sums(float *s, int lane) {
+    if constexpr (CNT > 1) {
+        const bool up = lane & OFF;
+#pragma unroll
+        for (int k = 0; k < CNT / 2; ++k) {
+            float x0 = s[k], x1 = s[k + CNT / 2];
+            asm("" : "+f"(x0), "+f"(x1));                   // values, not places, are chosen: s stays in registers
+            s[k] = (up ? x1 : x0) + __shfl_xor_sync(0xffffffffu, up ? x0 : x1, OFF);
+        }
+    } else {
+        s[0] += __shfl_xor_sync(0xffffffffu, s[0], OFF);
+    }
+    if constexpr (OFF > 1) warp_sums<(CNT > 1 ? CNT / 2 : 1), OFF / 2>(s, lane);
+}
 
 // TH threads: 512, one CTA an SM, or 256 or 128, two or four CTAs, which wait at barriers of
 // their own: as few threads as hold the columns in R pairs each.
@@ -203,21 +223,7 @@ __global__ void __launch_bounds__(TH, 512 / TH) xent_token_kernel(const __grid_c
                 }
                 s[v * N + n] = a;
             }
-        // each exchange halves the values a lane holds; then plain sums
-#pragma unroll
-        for (int cnt = NV, off = 16; off > 0; off /= 2) {
-            if (cnt > 1) {
-                cnt /= 2;
-                const bool up = lane & off;
-#pragma unroll
-                for (int k = 0; k < cnt; ++k) {
-                    const float give = up ? s[k] : s[k + cnt], keep = up ? s[k + cnt] : s[k];
-                    s[k] = keep + __shfl_xor_sync(0xffffffffu, give, off);
-                }
-            } else {
-                s[0] += __shfl_xor_sync(0xffffffffu, s[0], off);
-            }
-        }
+        warp_sums<NV, 16>(s, lane);
         if ((lane & ((1 << SH) - 1)) == 0) red[i & 1][warp][vi] = s[0];
         if (__syncthreads_or(!ok)) {                        // a copy did not arrive: leave together
             ok = false;
