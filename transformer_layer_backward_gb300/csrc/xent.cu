@@ -18,7 +18,9 @@
 //
 // Float32 operands are taken apart into three bf16 terms of 8 bits each, x = x0 + x1 + x2
 // exactly, and the product is the sum of the term products down to 2^-24 of the first: three
-// with a bf16 partner (exact), six between two float32 operands (x_i y_j with i + j <= 2).
+// with a bf16 partner (exact), six between two float32 operands (x_i y_j with i + j <= 2).  The
+// terms are written to the workspace, or (a float32 head, up to 512 rows) made from the float32
+// values on their way into shared memory.
 // With bf16 operands dz is rounded to bf16 once (2^-8 at most, relative to each dz; the sums
 // of it are in fp32): its error in d_hidden stays below that of d_hidden's rounding to bf16,
 // since the largest dz of most rows, the target's, is kept whole by a factor of the row.
@@ -58,12 +60,15 @@ namespace {
 
 constexpr int kBM = 128, kBK = 64;          // rows of a CTA's tile; k block (64 bf16 = 128 bytes)
 constexpr int kThreads = 320;               // 10 warps: TMA producer, MMA issuer, 8 epilogue warps
+constexpr int kConvWarps = 8;               // ... and those that take a float32 operand apart
+constexpr int kConvThreads = kThreads + 32 * kConvWarps;
 constexpr int kEpiWarps = 8;                // two per 32 TMEM lanes (rows), each half of the columns
 constexpr int kMaxTerms = 3, kMaxProd = 6;
 // k blocks (4 MMAs each) of one tensor-memory sum of a float32 result.  Reading a sum out takes
 // the tensor pipe about 300 cycles (the loss of 2048 x 2560 x 131072: 812 us at 8 k blocks, 787
 // at 20), and its error grows with its length.
 constexpr int kChunkLoss = 20, kChunkGrad = 10;
+constexpr int kConvLoss = 3, kConvGrad = 2;  // of six term products each
 constexpr int kGroupM = 16;                 // row tiles that share a column tile before the next one
 constexpr int kBox = 4096;                  // bytes of a 32 x 64 bf16 box of dz
 constexpr float kLog2e = 1.4426950408889634f;
@@ -95,6 +100,8 @@ struct XParams {
     float *out32;                            // one of the two is written
     __nv_bfloat16 *out16;
     int vec;                                 // N % 4 == 0 and 16-byte rows: four columns an access
+    const float *bw;                         // CONV: columns' operand, float32 [b_rows, b_cols], rows b_cols apart
+    int b_rows, b_cols, b_vec;               // b_vec: four columns an access
     float *partial;                          // [CTA][2][kBM][BN]
     uint32_t *status;
 };
@@ -312,24 +319,117 @@ struct Shape {
     static constexpr int BH = PAIR ? BN / 2 : BN;            // columns' operand rows that a CTA stages
     static constexpr int A_BYTES = kBM * kBK * 2, B_BYTES = BH * kBK * 2, STAGE = A_BYTES + B_BYTES;
 };
+// CONV: a stage holds the three terms of both operands.
+constexpr int kConvStage = 3 * (kBM * kBK * 2 + 128 * kBK * 2);
 // Ring depth: what shared memory leaves beside the epilogue's buffers (8 x 4 KB boxes of dz, 8 x
 // 4.2 KB for the turn of kOut, none for kStats).
 template <int MODE>
 constexpr int epi_bytes() {
     return MODE == kStats ? 0 : MODE == kGrad ? kEpiWarps * kBox : kEpiWarps * 32 * 33 * 4;
 }
-template <int BN, bool PAIR, int MODE>
+template <int BN, bool PAIR, int MODE, bool CONV>
 constexpr int stages_of() {
-    const int n = (226 * 1024 - 1024 - epi_bytes<MODE>()) / Shape<BN, PAIR>::STAGE;
+    const int n = (226 * 1024 - 1024 - epi_bytes<MODE>()) / (CONV ? kConvStage : Shape<BN, PAIR>::STAGE);
     return n > 6 ? 6 : n;
 }
 
+// A float32 head's 64 x 64 block in registers, loaded and taken apart by the converting warps.
+// vec: two rows of 16 lanes x 4 columns; else a row of 32 lanes x 2 columns.
+constexpr int kConvRows = 64 / kConvWarps, kAhead = 2;
+template <bool INSIDE>
+__device__ __forceinline__ void conv_fetch(const XParams &p, int row0, int col0, int cw, int lane, float (&v)[2 * kConvRows]) {
+    if (p.b_vec) {
+        const int c = col0 + 4 * (lane & 15), r = row0 + cw * kConvRows + (lane >> 4);
+        const float *src = p.bw + int64_t(r) * p.b_cols + c;
+#pragma unroll
+        for (int u = 0; u < kConvRows / 2; ++u, src += 2 * p.b_cols) {
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (INSIDE || (r + 2 * u < p.b_rows && c < p.b_cols)) x = __ldg(reinterpret_cast<const float4 *>(src));
+            v[4 * u] = x.x; v[4 * u + 1] = x.y; v[4 * u + 2] = x.z; v[4 * u + 3] = x.w;
+        }
+    } else {
+        const int c = col0 + 2 * lane, r = row0 + cw * kConvRows;
+        const float *src = p.bw + int64_t(r) * p.b_cols + c;
+#pragma unroll
+        for (int u = 0; u < kConvRows; ++u, src += p.b_cols)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                v[2 * u + k] = 0.f;
+                if (INSIDE || (r + u < p.b_rows && c + k < p.b_cols)) v[2 * u + k] = __ldg(src + k);
+            }
+    }
+}
+__device__ __forceinline__ void conv_load(const XParams &p, int row0, int col0, int cw, int lane, float (&v)[2 * kConvRows]) {
+    if (row0 + 64 <= p.b_rows && col0 + 64 <= p.b_cols) conv_fetch<true>(p, row0, col0, cw, lane, v);
+    else conv_fetch<false>(p, row0, col0, cw, lane, v);
+}
+// A block's lines on their way to L2: 64 x 128 floats (MN) or 128 x 64, a line a thread.
+template <bool B_MN>
+__device__ __forceinline__ void conv_prefetch(const XParams &p, int row0, int col0, int t) {
+    static_assert(kConvWarps == 8, "256 lines");
+    const int r = row0 + (B_MN ? t >> 2 : t >> 1), c = col0 + 32 * (B_MN ? t & 3 : t & 1);
+    if (r < p.b_rows && c < p.b_cols) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.bw + int64_t(r) * p.b_cols + c));
+}
+// Two neighbours' next terms as a word, removed from them.
+template <bool FINITE>
+__device__ __forceinline__ uint32_t next_terms(float &x, float &y) {
+    if constexpr (!FINITE) {
+        const uint32_t a = next_term(x), b = next_term(y);
+        return a | (b << 16);
+    }
+    const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+    x -= __uint_as_float(a & 0xFFFF0000u);
+    y -= __uint_as_float(b & 0xFFFF0000u);
+    return __byte_perm(a, b, 0x7632);
+}
+// ... into the three planes `plane` bytes apart (rows of 128 bytes, 128-byte swizzle).
+template <bool FINITE>
+__device__ __forceinline__ void conv_terms(bool vec, uint8_t *dst, int plane, int cw, int lane, float (&v)[2 * kConvRows]) {
+    if (vec) {
+#pragma unroll
+        for (int u = 0; u < kConvRows / 2; ++u) {
+            const int r = cw * kConvRows + 2 * u + (lane >> 4), c = lane & 15;
+            uint8_t *at = dst + r * 128 + (((c >> 1) ^ (r & 7)) << 4) + (c & 1) * 8;
+#pragma unroll
+            for (int t = 0; t < 3; ++t) {
+                uint2 w;
+                w.x = next_terms<FINITE>(v[4 * u], v[4 * u + 1]);
+                w.y = next_terms<FINITE>(v[4 * u + 2], v[4 * u + 3]);
+                *reinterpret_cast<uint2 *>(at + t * plane) = w;
+            }
+        }
+    } else {
+#pragma unroll
+        for (int u = 0; u < kConvRows; ++u) {
+            const int r = cw * kConvRows + u;
+            uint8_t *at = dst + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
+#pragma unroll
+            for (int t = 0; t < 3; ++t) *reinterpret_cast<uint32_t *>(at + t * plane) = next_terms<FINITE>(v[2 * u], v[2 * u + 1]);
+        }
+    }
+}
+__device__ __forceinline__ void conv_store(bool vec, uint8_t *dst, int plane, int cw, int lane, float (&v)[2 * kConvRows]) {
+    uint32_t big = 0;
+#pragma unroll
+    for (int k = 0; k < 2 * kConvRows; ++k) big = max(big, __float_as_uint(v[k]) & 0x7FFFFFFFu);
+    // one branch for all: a test at every value takes longer than the rest
+    if (__all_sync(0xffffffffu, big < 0x7F800000u)) conv_terms<true>(vec, dst, plane, cw, lane, v);
+    else conv_terms<false>(vec, dst, plane, cw, lane, v);
+}
+
 // TERMS: bf16 terms of dz (kGrad; 1 otherwise).  FINE: sums in chunks of k blocks.
-template <int BN, bool PAIR, int MODE, int TERMS, bool FINE, bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_constant__ XParams p) {
+// CONV: the columns' operand is float32 in memory, and 8 more warps take it apart into the three
+// planes of a stage, beside TMA's three of the rows' operand; a k block is then all six term
+// products (24 MMAs, 1536 cycles), and two stages fill shared memory.  It is bound by the
+// converting warps' loads: 32 KB in flight an SM, asked for in L2 two k blocks before (about 2300
+// cycles a k block).  8 warps against 4: 139 against 176 us (128 rows, loss), although the
+// epilogue then spills some registers.
+template <int BN, bool PAIR, int MODE, int TERMS, bool FINE, bool A_MN, bool B_MN, bool CONV>
+__global__ void __launch_bounds__(CONV ? kConvThreads : kThreads, 1) xent_gemm_kernel(const __grid_constant__ XParams p) {
     using S = Shape<BN, PAIR>;
-    constexpr int kStages = stages_of<BN, PAIR, MODE>();
-    constexpr int TM = S::TM, BH = S::BH, A_BYTES = S::A_BYTES, STAGE = S::STAGE;
+    static_assert(!CONV || (BN == 128 && !PAIR && FINE && !A_MN), "one form");
+    constexpr int kStages = stages_of<BN, PAIR, MODE, CONV>();
+    constexpr int TM = S::TM, BH = S::BH, A_BYTES = (CONV ? 3 : 1) * S::A_BYTES, STAGE = CONV ? kConvStage : S::STAGE;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t full[kStages], empty[kStages], accfull[2], accempty[2], done;
@@ -342,7 +442,8 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
 
     // this unit's segments: its whole tiles, then its share of the split tiles, cut at tiles
     const int KB = p.nprod * p.kb;
-    const int chunk = !FINE ? KB : MODE == kStats ? kChunkLoss : kChunkGrad;                    // k blocks of one accumulator
+    // k blocks of one accumulator
+    const int chunk = !FINE ? KB : MODE == kStats ? (CONV ? kConvLoss : kChunkLoss) : (CONV ? kConvGrad : kChunkGrad);
     const int nwhole = p.whole > unit ? (p.whole - unit + p.units - 1) / p.units : 0;
     const bool splits = MODE == kOut && p.sk_work > 0 && unit < p.sk_units;
     const int b0 = splits ? int(sk_start(p.sk_work, p.sk_units, unit)) : 0;       // sk_work < units KB < 2^31
@@ -376,11 +477,23 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
         n0 = tn * BN;
     };
 
+    // A part of a tile starts at a multiple of the units' share and wraps round, so that the units
+    // are at the same k of different tiles at the same time and share its operand tiles in L2
+    auto first_kb = [&](int i, const Seg &s) {
+        int kb = s.kb0;
+        if (splits && i >= nwhole && s.kb1 - s.kb0 == b1 - b0) {
+            const int share = int((p.sk_work + p.sk_units - 1) / p.sk_units);
+            kb = (s.kb0 + share - 1) / share * share;
+            if (kb >= s.kb1) kb = s.kb0;
+        }
+        return kb;
+    };
+
     if (threadIdx.x == 0) {
         s_abort = 0;
         s_issued = s_consumed = 0;
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], CONV ? 1 + kConvWarps : 1);
             mbar_init(&empty[s], 1);
         }
         for (int b = 0; b < 2; ++b) {
@@ -416,15 +529,7 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
                 int m0, n0, tn;
                 place(sg.tile, m0, n0, tn);
                 const int nb = n0 + rank * BH;
-                // A part of a tile starts at a multiple of the units' share and wraps round, so
-                // that the units are at the same k of different tiles at the same time and
-                // share its operand tiles in L2
-                int kb = sg.kb0;
-                if (splits && i >= nwhole && sg.kb1 - sg.kb0 == b1 - b0) {
-                    const int share = int((p.sk_work + p.sk_units - 1) / p.sk_units);
-                    kb = (sg.kb0 + share - 1) / share * share;
-                    if (kb >= sg.kb1) kb = sg.kb0;
-                }
+                int kb = first_kb(i, sg);
                 for (int j = sg.kb0; j < sg.kb1; ++j, ++g, kb = kb + 1 < sg.kb1 ? kb + 1 : sg.kb0) {
                     const int s = g % kStages;
                     if (g >= kStages && !mbar_wait(&empty[s], ((g / kStages) - 1) & 1, p.status, 20u)) {
@@ -434,7 +539,10 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
                     const int kq = kb / p.nprod, prod = kb - kq * p.nprod, k0 = kq * kBK;
                     const CUtensorMap *ma = &p.a[p.pa[prod]], *mb = &p.b[p.pb[prod]];
                     uint8_t *sa = smem + s * STAGE, *sb = sa + A_BYTES;
-                    if constexpr (PAIR) {
+                    if constexpr (CONV) {
+                        mbar_arrive_expect_tx(&full[s], A_BYTES);
+                        for (int t = 0; t < 3; ++t) tma_load_2d(sa + t * S::A_BYTES, &p.a[t], k0, m0, &full[s]);
+                    } else if constexpr (PAIR) {
                         if (leader) mbar_arrive_expect_tx(&full[s], 2 * STAGE);   // both CTAs' copies
                         const uint32_t fb = cluster_addr(&full[s], 0);
                         if constexpr (A_MN) {
@@ -493,14 +601,21 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
                         if (!mbar_wait(&full[s], (g / kStages) & 1, p.status, 21u)) { ok = false; break; }
                         tc_fence_after();
                         const uint8_t *sa = smem + s * STAGE;
-                        const uint64_t ad = A_MN ? sw128_desc_mn(sa) : sw128_desc(sa);
-                        const uint64_t bd = B_MN ? sw128_desc_mn(sa + A_BYTES) : sw128_desc(sa + A_BYTES);
+                        // CONV: the six products of three terms each, the smallest first
 #pragma unroll
-                        for (int k = 0; k < kBK / 16; ++k) {
-                            const uint32_t add = (kb > k0 || k > 0) ? 1u : 0u;
-                            if constexpr (PAIR) mma_bf16_pair(acc, ad + ka * k, bd + kbs * k, idesc, add);
-                            else mma_bf16(acc, ad + ka * k, bd + kbs * k, idesc, add);
-                        }
+                        for (int sum = CONV ? 2 : 0; sum >= 0; --sum)
+#pragma unroll
+                            for (int ta = 0; ta <= sum; ++ta) {
+                                const uint8_t *pa = sa + ta * S::A_BYTES, *pb = sa + A_BYTES + (sum - ta) * S::B_BYTES;
+                                const uint64_t ad = A_MN ? sw128_desc_mn(pa) : sw128_desc(pa);
+                                const uint64_t bd = B_MN ? sw128_desc_mn(pb) : sw128_desc(pb);
+#pragma unroll
+                                for (int k = 0; k < kBK / 16; ++k) {
+                                    const uint32_t add = (kb > k0 || k > 0 || (CONV && !(sum == 2 && ta == 0))) ? 1u : 0u;
+                                    if constexpr (PAIR) mma_bf16_pair(acc, ad + ka * k, bd + kbs * k, idesc, add);
+                                    else mma_bf16(acc, ad + ka * k, bd + kbs * k, idesc, add);
+                                }
+                            }
                         if constexpr (PAIR) mma_commit_pair(&empty[s], 3);   // frees the stage in both CTAs
                         else mma_commit(&empty[s]);
                         s_consumed = g + 1;
@@ -515,6 +630,58 @@ __global__ void __launch_bounds__(kThreads, 1) xent_gemm_kernel(const __grid_con
             if constexpr (PAIR) mma_commit_pair(&done, 1);
             else mma_commit(&done);
             mbar_wait(&done, 0, nullptr, 0u);
+        }
+    } else if (CONV && warp >= 2 + kEpiWarps) {
+        // ------------------------------------------------ float32 operand -> three terms
+        if constexpr (CONV) {
+            const int cw = warp - 2 - kEpiWarps;
+            int i = 0, at = b0, j = 0, kb = 0, m0, n0 = 0, tn;
+            Seg sg;
+            // k blocks in the producer's order
+            auto enter = [&] {
+                if (!next_seg(i, at, sg)) return false;
+                place(sg.tile, m0, n0, tn);
+                kb = first_kb(i, sg);
+                j = sg.kb0;
+                return true;
+            };
+            auto step = [&] {
+                if (++j < sg.kb1) {
+                    kb = kb + 1 < sg.kb1 ? kb + 1 : sg.kb0;
+                    return true;
+                }
+                ++i;
+                return enter();
+            };
+            float v[2][2 * kConvRows];                                   // the two halves of the k block that comes next
+            // DRAM takes longer than a k block does: the block after the next is asked for too
+            auto load = [&](int h) {
+                if (h == 0) conv_prefetch<B_MN>(p, B_MN ? (kb + kAhead) * kBK : n0, B_MN ? n0 : (kb + kAhead) * kBK, cw * 32 + lane);
+                if constexpr (B_MN) conv_load(p, kb * kBK, n0 + 64 * h, cw, lane, v[h]);
+                else conv_load(p, n0 + 64 * h, kb * kBK, cw, lane, v[h]);
+            };
+            bool more = enter();
+            if (more) {
+                load(0);
+                load(1);
+            }
+            for (int g = 0; more; ++g) {
+                const int s = g % kStages;
+                if (g >= kStages && !mbar_wait(&empty[s], ((g / kStages) - 1) & 1, p.status, 24u)) {
+                    s_abort = 1;
+                    break;
+                }
+                uint8_t *sb = smem + s * STAGE + A_BYTES;
+                more = step();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    conv_store(p.b_vec != 0, sb + h * 64 * 128, S::B_BYTES, cw, lane, v[h]);
+                    if (more) load(h);
+                }
+                fence_proxy_async();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&full[s]);
+            }
         }
     } else {
         // ------------------------------------------------ epilogue (warps 2..9)
@@ -837,18 +1004,25 @@ struct Mat {
     const __nv_bfloat16 *p;
     int64_t rows, cols, ld, plane;
     int terms;
+    const float *f32 = nullptr;  // instead: the float32 matrix, rows cols apart, taken apart by the product
 };
 
-template <int BN, bool PAIR, int MODE, int TERMS, bool FINE, bool A_MN, bool B_MN>
+template <int BN, bool PAIR, int MODE, int TERMS, bool FINE, bool A_MN, bool B_MN, bool CONV = false>
 int launch(XParams &p, const Mat &a, const Mat &b, cudaStream_t st, bool dependent = false) {
     using S = Shape<BN, PAIR>;
-    constexpr int stages = stages_of<BN, PAIR, MODE>();
-    constexpr int smem = stages * S::STAGE + epi_bytes<MODE>() + 1024;
-    static_assert(stages >= 3 && smem <= 227 * 1024 - 512, "shared memory of one CTA");
+    constexpr int stages = stages_of<BN, PAIR, MODE, CONV>();
+    constexpr int smem = stages * (CONV ? kConvStage : S::STAGE) + epi_bytes<MODE>() + 1024;
+    static_assert(stages >= (CONV ? 2 : 3) && smem <= 227 * 1024 - 512, "shared memory of one CTA");
     for (int t = 0; t < a.terms; ++t)
         TLB_TRY(make_map(&p.a[t], a.p + t * a.plane, a.rows, a.cols, a.ld, A_MN ? kBK : kBM));
-    for (int t = 0; t < b.terms; ++t)
+    for (int t = 0; t < b.terms && !CONV; ++t)
         TLB_TRY(make_map(&p.b[t], b.p + t * b.plane, b.rows, b.cols, b.ld, B_MN ? kBK : S::BH));
+    if (CONV) {
+        p.bw = b.f32;
+        p.b_rows = int(b.rows);
+        p.b_cols = int(b.cols);
+        p.b_vec = b.cols % 4 == 0;
+    }
     // term products, the smallest first: i + j <= 2 of three and three, all of one and three
     p.nprod = 0;
     for (int sum = kMaxTerms - 1; sum >= 0; --sum)
@@ -859,6 +1033,7 @@ int launch(XParams &p, const Mat &a, const Mat &b, cudaStream_t st, bool depende
             p.pb[p.nprod] = int8_t(j);
             ++p.nprod;
         }
+    if (CONV) p.nprod = 1;                                   // all six are a k block's
     const int64_t K = A_MN ? a.rows : a.cols;
     p.kb = int(ceil_div(K, kBK));
     p.tiles_m = int(ceil_div(p.M, S::TM));
@@ -874,18 +1049,18 @@ int launch(XParams &p, const Mat &a, const Mat &b, cudaStream_t st, bool depende
         // The tiles past the last full wave are split along K over all units unless a wave of
         // them costs less: a split ends in partial tiles and a second kernel, about 24 k blocks
         const int64_t rest = tiles % most;
-        if (rest > 0 && KB > KB * rest / most + 24) {
+        if (rest > 0 && KB > KB * rest / most + (CONV ? 4 : 24)) {
             p.whole = int(tiles - rest);
             p.sk_work = rest * KB;
-            p.sk_units = int(std::max<int64_t>(1, std::min<int64_t>(most, p.sk_work / 8)));
+            p.sk_units = int(std::max<int64_t>(1, std::min<int64_t>(most, p.sk_work / (CONV ? 2 : 8))));
             p.units = p.whole > 0 ? most : p.sk_units;
         }
     }
-    auto k = xent_gemm_kernel<BN, PAIR, MODE, TERMS, FINE, A_MN, B_MN>;
+    auto k = xent_gemm_kernel<BN, PAIR, MODE, TERMS, FINE, A_MN, B_MN, CONV>;
     TLB_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned((PAIR ? 2 : 1) * p.units));
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(CONV ? kConvThreads : kThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
@@ -913,6 +1088,8 @@ int launch(XParams &p, const Mat &a, const Mat &b, cudaStream_t st, bool depende
 template <int MODE, int TERMS>
 int launch_z(XParams &p, const Mat &h, const Mat &w, bool after_targets, cudaStream_t st) {
     constexpr bool fine = MODE == kStats || TERMS > 1;       // the loss is float32 whatever the operands
+    if constexpr (MODE == kStats || TERMS == 3)
+        if (w.f32 != nullptr) return launch<128, false, MODE, TERMS, true, false, false, true>(p, h, w, st, after_targets);
     if constexpr (TERMS != 2)                                // two terms: up to 64 rows
         if (p.M > kBM) return launch<256, true, MODE, TERMS, fine, false, false>(p, h, w, st, after_targets);
     const int64_t n = num_sms(), t256 = ceil_div(p.N, 256), t128 = ceil_div(p.N, 128);
@@ -923,17 +1100,25 @@ int launch_z(XParams &p, const Mat &h, const Mat &w, bool after_targets, cudaStr
 
 template <bool A_MN, bool FINE>
 int launch_out(XParams &p, const Mat &a, const Mat &b, cudaStream_t st) {
+    if constexpr (FINE && !A_MN)
+        if (b.f32 != nullptr) return launch<128, false, kOut, 1, true, false, true, true>(p, a, b, st);
     if (p.M > kBM) return launch<256, true, kOut, 1, FINE, A_MN, true>(p, a, b, st);
     return launch<256, false, kOut, 1, FINE, A_MN, true>(p, a, b, st);
 }
 
 constexpr int64_t kPieceBytes = int64_t(512) << 20;   // of dz, and of packed head rows, in the workspace
 constexpr int64_t kFewRows = 64;                      // bf16 rows up to which dz has two terms
+// Rows up to which a float32 head is taken apart by the product itself, once for every 128 rows,
+// instead of being written as three terms (2.5 times its bytes) before.  Loss, gradient in us:
+//   32768 x 2560    128 rows: 127, 259 against 269, 395   333: 319, 677 against 489, 852   512: 387, 867 against 496, 871
+//   50021 x 1001    128 rows:  97, 194 against 207, 297   333: 217, 461 against 309, 564   512: 293, 616 against 315, 578
+// (2048 rows: 1403, 3311 against 1338, 2815: the larger tiles of the other form pay.)
+constexpr int64_t kConvMost = 512;
 constexpr int64_t kRowChunk = 16384;                  // rows of one pass of the loss (its pairs' buffer)
 
 struct Plan {
     int h_terms, w_terms, z_terms;
-    bool pack_h, pack_w;
+    bool pack_h, pack_w, conv_w;
     int64_t dp;                  // packed row length
     int64_t piece;               // vocabulary rows of one piece (multiple of 256)
     int64_t part_ld, slots;
@@ -948,7 +1133,8 @@ Plan plan_of(int htype, int wtype, int64_t N, int64_t V, int64_t D, bool grad, b
     q.dp = ceil_div(D, 8) * 8;
     // d_w sums over the rows: those without a target are zeroed in a copy
     q.pack_h = htype == TLB_W_F32 || D % 8 != 0 || grad_w;
-    q.pack_w = wtype == TLB_W_F32 || D % 8 != 0;
+    q.conv_w = wtype == TLB_W_F32 && N <= kConvMost;
+    q.pack_w = !q.conv_w && (wtype == TLB_W_F32 || D % 8 != 0);
     int64_t piece = ceil_div(V, 256) * 256;
     if (grad) piece = std::min(piece, kPieceBytes / (2 * q.z_terms * std::max<int64_t>(N, 1)));
     if (q.pack_w) piece = std::min(piece, kPieceBytes / (2 * q.w_terms * q.dp));
@@ -1017,6 +1203,10 @@ int hidden_operand(const Plan &q, int htype, const void *hidden, int64_t N, int6
 int head_operand(const Plan &q, int wtype, const void *W, int64_t v0, int64_t n, int64_t D, void *ws, cudaStream_t st,
                  Mat &w) {
     const char *src = static_cast<const char *>(W) + size_t(v0) * D * elem(wtype);
+    if (q.conv_w) {
+        w = Mat{nullptr, n, D, D, 0, q.w_terms, reinterpret_cast<const float *>(src)};
+        return TLB_OK;
+    }
     if (!q.pack_w) {
         w = Mat{reinterpret_cast<const __nv_bfloat16 *>(src), n, D, D, 0, 1};
         return TLB_OK;
@@ -1026,15 +1216,14 @@ int head_operand(const Plan &q, int wtype, const void *W, int64_t v0, int64_t n,
     return pack(src, wtype, n, D, q.dp, q.w_terms, nullptr, 0, y, st);
 }
 
-// Up to four rows take the kernel that reads the head once, and with a float32 head, which the
-// tensor-core route writes again as three terms, up to sixteen, in turns of four.  Measured, loss
-// and gradient in us, 32768 x 2560 | 110656 x 832, turns against tensor cores:
-//   bf16                 4 rows: 40, 77 against 44, 91 | 1024 wide, 151936: 75, 153 against 78, 154
-//   float32 and bf16     4 rows: 38, 76 against 82, 147 | 56, 114 against 77, 162;   8 rows: 75, 152 | 111, 226
-//   float32             12 rows: 165, 284 | 204, 419;   13: 219, 342 | 269, 488 against 294, 410 | 430, 598
+// Up to four rows take the kernel that reads the head once, and with a float32 head up to eight,
+// in two turns.  Measured, loss and gradient in us, 32768 x 2560 | 110656 x 832, against tensor cores:
+//   bf16                4 rows: 40, 77 against 44, 91 | 1024 wide, 151936: 75, 153 against 78, 154
+//   float32 and bf16    4 rows: 38, 76 against 82, 147 | 56, 114 against 77, 162;   8 rows: 75, 152 | 111, 226
+//   float32             8 rows: 111, 189 | 137, 280;   12: 165, 284 | 204, 419 against 125, 250 | 130, 285
 bool by_tokens(const Plan &q, int64_t rows, int64_t dim, bool grad) {
     const int64_t turns = ceil_div(rows, 4), last = rows - 4 * (turns - 1);
-    return turns <= (q.w_terms > 1 ? 4 : 1) && xent_token_supported(std::min<int64_t>(rows, 4), dim, grad) &&
+    return turns <= (q.w_terms > 1 ? 2 : 1) && xent_token_supported(std::min<int64_t>(rows, 4), dim, grad) &&
            xent_token_supported(last, dim, grad);
 }
 
