@@ -335,6 +335,7 @@ int tlb_muon(const tlb_muon_mat *mats, int32_t n, const tlb_muon_cfg *cfg, void 
  * target's dz free of rounding.  f32 hidden: every float32 operand, dz included, is taken
  * apart into three bf16 terms that hold all its 24 bits, for results of float32 precision at
  * a third (W bf16) or a sixth (W f32) of the speed.  The target's own logit is summed in fp32.
+ * (An infinity in a float32 operand counts as NaN.)
  *
  * rows >= 0 (0 rows: no-op, d_w set to 0), vocab >= 1, dim >= 1, of any size up to 2^24,
  * 2^24 and 2^20 (dim % 8 != 0 costs a padded copy of the operands).  The backward pass walks

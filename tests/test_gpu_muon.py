@@ -175,6 +175,22 @@ def test_muon_misaligned_repeats_and_graphs(lib, rows, cols):
         assert all(torch.equal(a, b) for a, b in zip(results[0], v))
 
 
+@pytest.mark.parametrize("rows,cols,copies", [(64, 110000, 4), (90001, 40, 4), (64, 2560, 150)])
+def test_muon_beside_others(lib, rows, cols, copies):
+    """The same bits for a matrix by itself and beside others, where a block takes several of its
+    column tiles: their Gram matrices are summed tile by tile either way."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(5)
+    one = [torch.randn(rows, cols, generator=gen, device="cuda") * 0.02 for _ in range(3)]
+    cfg = lib.muon_cfg(0.02, 0.95, 0.1, 1e-7, COEF, 5, True)
+    many = [[x.clone() for _ in range(copies)] for x in one]
+    for lists in ([[x] for x in one], many):
+        mats = lib.muon_mats(*([lists[k] for k in range(3)]))
+        lib.muon(mats, cfg, lib.muon_workspace(mats))
+    for k in (0, 2):
+        assert all(torch.equal(one[k], x) for x in many[k])
+
+
 def test_muon_refusals(lib):
     import torch
     z = lambda *s: torch.zeros(*s, device="cuda")

@@ -233,7 +233,8 @@ def test_far_rows_of_a_large_head(lib):
     check("d_w", host(dw[tail]), host(dz[:, tail].T @ th.double()), BF16_REL_L2, None)
 
 
-@pytest.mark.parametrize("types,rows", [(("bf16", "bf16"), 130), (("f32", "bf16"), 9), (("bf16", "bf16"), 3)])
+@pytest.mark.parametrize("types,rows", [(("bf16", "bf16"), 130), (("f32", "bf16"), 9), (("bf16", "bf16"), 3),
+                                        (("f32", "f32"), 140), (("f32", "f32"), 7)])
 def test_repeats_streams_and_neighbours(lib, types, rows):
     """The same bits on a second run, on another stream, in a captured graph that is replayed
     on new inputs, beside a second graph on the same workspace; memory behind the outputs

@@ -35,9 +35,10 @@
 //     go through reading, r x r products and writing in step, so that HBM idles in the middle:
 //     two reads and two Gram sums of X in shared memory, then two chains of r x r products
 //   seven 5 x 1001 and three 999 x 33 matrices: 74 us in two launches, chains of 14 r x r products
-//   144 rank-64 matrices, 472 MB (69.6 us; 189 MB read by each pass): 349 us = passes of 70, 118 and
-//     98 us and r x r products of 20 and 29 us; the passes wait for loads and for taking floats
-//     apart (DRAM 28 to 44 % busy, tensor pipe 16 %)
+//   144 rank-64 matrices, 472 MB (69.6 us; 189 MB read by each pass): 391 us, three passes and two
+//     launches of r x r products; the passes wait for loads, for taking floats apart and for their
+//     Gram matrices, which leave tile by tile (sums of two tiles in tensor memory: 349 us and five
+//     times the error, 1e-6 against 2e-7 in p; one tile a block: 406 us)
 #include <algorithm>
 #include <cmath>
 #include <cstring>
@@ -63,7 +64,7 @@ struct Mat {
     int32_t r, n;
     int32_t tall;                        // stored [n, r] (else [r, n])
     int32_t vec;                         // 16-byte accesses (aligned; r % 4 == 0 of a tall one, n % 4 == 0 of a wide one)
-    int32_t block0, ctas;                // first block of this matrix, and (clusters) how many
+    int32_t block0, ctas;                // first block of this matrix; (clusters) how many, (passes) partial Gram matrices
     float lr, lr_scale;                  // lr lr_mult, and times scale
 };
 
@@ -848,8 +849,8 @@ __global__ void __launch_bounds__(NT, tc_ctas<SOURCE, SINK>()) muon_tc_pass_kern
     for (int t = t0; t < t1; ++t, ++done) {
         const int j0 = t * kTcJ, jn = min(kTcJ, a.n - j0);
         float *y = p.ws + a.y + int64_t(t) * 64 * kTcJ;      // this tile of Y: [64][128]
-        if (SINK != kParam && done > 0) mbar_wait(&bar_g, (done - 1) & 1, p.status, 40u);   // the planes are read
-        if (jn < kTcJ) {                                     // columns past the last count as 0
+        // columns past the last count as 0, and so do rows past r where sums lay in the planes
+        if (jn < kTcJ || (SINK != kParam && done > 0 && a.r < 64)) {
             clear();
             __syncthreads();
         }
@@ -953,39 +954,39 @@ __global__ void __launch_bounds__(NT, tc_ctas<SOURCE, SINK>()) muon_tc_pass_kern
                                  sw128_desc(planes + tb * kXPlane + off) + 2 * (k & 3), idesc, first | uint32_t(k > 0));
                     }
                 };
-                const uint32_t add = done > 0 ? 1u : 0u;
-                gram(td1, 1, 1, add);
+                gram(td1, 1, 1, 0u);
                 gram(td1, 0, 0, 1u);
-                gram(td2, 0, 2, add);
+                gram(td2, 0, 2, 0u);
                 gram(td2, 0, 1, 1u);
                 mma_commit(&bar_g);
             }
-        }
-    }
-    if constexpr (SINK != kParam) {
-        if (done > 0) mbar_wait(&bar_g, (done - 1) & 1, p.status, 42u);
-        __syncwarp();
-        tc_fence_after();
-        float *s1 = reinterpret_cast<float *>(planes), *s2 = s1 + 64 * 65;    // in the planes' place
-        if (q < 2) {
-            uint32_t v[32], w[32];
-            const uint32_t at = (uint32_t(q * 32) << 16) + uint32_t(half * 32);
-            tmem_ld32(td1 + at, v);
-            tmem_ld32(td2 + at, w);
-            tmem_wait_ld();
+            // Every tile's sums go out by themselves: tensor memory cuts a sum after every MMA, and
+            // a second tile's 16 onto a whole sum would cost five times the error
+            mbar_wait(&bar_g, done & 1, p.status, 42u);
+            __syncwarp();
+            tc_fence_after();
+            float *s1 = reinterpret_cast<float *>(planes), *s2 = s1 + 64 * 65;    // in the planes' place
+            if (q < 2) {
+                uint32_t v[32], w[32];
+                const uint32_t at = (uint32_t(q * 32) << 16) + uint32_t(half * 32);
+                tmem_ld32(td1 + at, v);
+                tmem_ld32(td2 + at, w);
+                tmem_wait_ld();
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-                s1[(q * 32 + lane) * 65 + half * 32 + c] = __uint_as_float(v[c]);
-                s2[(q * 32 + lane) * 65 + half * 32 + c] = __uint_as_float(w[c]);
+                for (int c = 0; c < 32; ++c) {
+                    s1[(q * 32 + lane) * 65 + half * 32 + c] = __uint_as_float(v[c]);
+                    s2[(q * 32 + lane) * 65 + half * 32 + c] = __uint_as_float(w[c]);
+                }
             }
-        }
-        tc_fence_before();
-        __syncthreads();
-        float *out = p.ws + a.part + int64_t(bl) * T::GSIZE;
-        for (int e = tid; e < T::GSIZE; e += NT) {
-            int i, k;
-            gram_place<64>(e, i, k);
-            out[e] = s1[i * 65 + k] + (s2[i * 65 + k] + s2[k * 65 + i]);
+            tc_fence_before();
+            __syncthreads();
+            float *out = p.ws + a.part + int64_t(t) * T::GSIZE;
+            for (int e = tid; e < T::GSIZE; e += NT) {
+                int i, k;
+                gram_place<64>(e, i, k);
+                out[e] = s1[i * 65 + k] + (s2[i * 65 + k] + s2[k * 65 + i]);
+            }
+            if (t + 1 < t1) __syncthreads();                 // the planes are free again
         }
     }
     __syncthreads();
@@ -1154,9 +1155,10 @@ int group(const tlb_muon_mat *mats, int *idx, int n, bool clusters, const tlb_mu
             a.ctas = ctas[k];
             a.block0 = block0[k];
         } else {
-            a.ctas = int(ceil_div(tiles_of<RP>(a.n), p.tiles_per_block));
+            const int64_t t = tiles_of<RP>(a.n), nb = ceil_div(t, p.tiles_per_block);
+            a.ctas = int(RP == 64 ? t : nb);                 // partial Gram matrices
             a.block0 = int(blocks);
-            blocks += a.ctas;
+            blocks += nb;
         }
         a.y = off;
         off += tiles_of<RP>(a.n) * RP * pass_columns<RP>();

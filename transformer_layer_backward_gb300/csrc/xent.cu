@@ -319,8 +319,6 @@ struct Shape {
     static constexpr int BH = PAIR ? BN / 2 : BN;            // columns' operand rows that a CTA stages
     static constexpr int A_BYTES = kBM * kBK * 2, B_BYTES = BH * kBK * 2, STAGE = A_BYTES + B_BYTES;
 };
-// CONV: a stage holds the three terms of both operands.
-constexpr int kConvStage = 3 * (kBM * kBK * 2 + 128 * kBK * 2);
 // Ring depth: what shared memory leaves beside the epilogue's buffers (8 x 4 KB boxes of dz, 8 x
 // 4.2 KB for the turn of kOut, none for kStats).
 template <int MODE>
@@ -329,7 +327,7 @@ constexpr int epi_bytes() {
 }
 template <int BN, bool PAIR, int MODE, bool CONV>
 constexpr int stages_of() {
-    const int n = (226 * 1024 - 1024 - epi_bytes<MODE>()) / (CONV ? kConvStage : Shape<BN, PAIR>::STAGE);
+    const int n = (226 * 1024 - 1024 - epi_bytes<MODE>()) / ((CONV ? 3 : 1) * Shape<BN, PAIR>::STAGE);   // CONV: all terms
     return n > 6 ? 6 : n;
 }
 
@@ -363,28 +361,22 @@ __device__ __forceinline__ void conv_load(const XParams &p, int row0, int col0, 
     if (row0 + 64 <= p.b_rows && col0 + 64 <= p.b_cols) conv_fetch<true>(p, row0, col0, cw, lane, v);
     else conv_fetch<false>(p, row0, col0, cw, lane, v);
 }
-// A block's lines on their way to L2: 64 x 128 floats (MN) or 128 x 64, a line a thread.
+// A k block's lines on their way to L2, a line a thread: 128 x 64 floats, or 64 x 128 (MN).
 template <bool B_MN>
 __device__ __forceinline__ void conv_prefetch(const XParams &p, int row0, int col0, int t) {
     static_assert(kConvWarps == 8, "256 lines");
     const int r = row0 + (B_MN ? t >> 2 : t >> 1), c = col0 + 32 * (B_MN ? t & 3 : t & 1);
     if (r < p.b_rows && c < p.b_cols) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.bw + int64_t(r) * p.b_cols + c));
 }
-// Two neighbours' next terms as a word, removed from them.
-template <bool FINITE>
-__device__ __forceinline__ uint32_t next_terms(float &x, float &y) {
-    if constexpr (!FINITE) {
-        const uint32_t a = next_term(x), b = next_term(y);
-        return a | (b << 16);
-    }
+// Two neighbours' next terms as a word, removed from them.  (Infinities and NaN leave NaN.)
+__device__ __forceinline__ uint32_t cut_terms(float &x, float &y) {
     const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
     x -= __uint_as_float(a & 0xFFFF0000u);
     y -= __uint_as_float(b & 0xFFFF0000u);
     return __byte_perm(a, b, 0x7632);
 }
 // ... into the three planes `plane` bytes apart (rows of 128 bytes, 128-byte swizzle).
-template <bool FINITE>
-__device__ __forceinline__ void conv_terms(bool vec, uint8_t *dst, int plane, int cw, int lane, float (&v)[2 * kConvRows]) {
+__device__ __forceinline__ void conv_store(bool vec, uint8_t *dst, int plane, int cw, int lane, float (&v)[2 * kConvRows]) {
     if (vec) {
 #pragma unroll
         for (int u = 0; u < kConvRows / 2; ++u) {
@@ -393,8 +385,8 @@ __device__ __forceinline__ void conv_terms(bool vec, uint8_t *dst, int plane, in
 #pragma unroll
             for (int t = 0; t < 3; ++t) {
                 uint2 w;
-                w.x = next_terms<FINITE>(v[4 * u], v[4 * u + 1]);
-                w.y = next_terms<FINITE>(v[4 * u + 2], v[4 * u + 3]);
+                w.x = cut_terms(v[4 * u], v[4 * u + 1]);
+                w.y = cut_terms(v[4 * u + 2], v[4 * u + 3]);
                 *reinterpret_cast<uint2 *>(at + t * plane) = w;
             }
         }
@@ -404,32 +396,26 @@ __device__ __forceinline__ void conv_terms(bool vec, uint8_t *dst, int plane, in
             const int r = cw * kConvRows + u;
             uint8_t *at = dst + r * 128 + (((lane >> 2) ^ (r & 7)) << 4) + (lane & 3) * 4;
 #pragma unroll
-            for (int t = 0; t < 3; ++t) *reinterpret_cast<uint32_t *>(at + t * plane) = next_terms<FINITE>(v[2 * u], v[2 * u + 1]);
+            for (int t = 0; t < 3; ++t) *reinterpret_cast<uint32_t *>(at + t * plane) = cut_terms(v[2 * u], v[2 * u + 1]);
         }
     }
-}
-__device__ __forceinline__ void conv_store(bool vec, uint8_t *dst, int plane, int cw, int lane, float (&v)[2 * kConvRows]) {
-    uint32_t big = 0;
-#pragma unroll
-    for (int k = 0; k < 2 * kConvRows; ++k) big = max(big, __float_as_uint(v[k]) & 0x7FFFFFFFu);
-    // one branch for all: a test at every value takes longer than the rest
-    if (__all_sync(0xffffffffu, big < 0x7F800000u)) conv_terms<true>(vec, dst, plane, cw, lane, v);
-    else conv_terms<false>(vec, dst, plane, cw, lane, v);
 }
 
 // TERMS: bf16 terms of dz (kGrad; 1 otherwise).  FINE: sums in chunks of k blocks.
 // CONV: the columns' operand is float32 in memory, and 8 more warps take it apart into the three
 // planes of a stage, beside TMA's three of the rows' operand; a k block is then all six term
 // products (24 MMAs, 1536 cycles), and two stages fill shared memory.  It is bound by the
-// converting warps' loads: 32 KB in flight an SM, asked for in L2 two k blocks before (about 2300
-// cycles a k block).  8 warps against 4: 139 against 176 us (128 rows, loss), although the
-// epilogue then spills some registers.
+// converting warps: their loads (32 KB in flight an SM, asked for in L2 two k blocks before) and
+// the cutting, about 2000 cycles a k block.  Loss of 128 rows, 32768 x 2560: 4 warps 176 us, 8
+// warps 139 (although the epilogue then spills some registers), with the prefetch 127, without a
+// test for infinities 115.  CTA pairs that share a k block's rows: slower (333 rows 488 against
+// 300 us).
 template <int BN, bool PAIR, int MODE, int TERMS, bool FINE, bool A_MN, bool B_MN, bool CONV>
 __global__ void __launch_bounds__(CONV ? kConvThreads : kThreads, 1) xent_gemm_kernel(const __grid_constant__ XParams p) {
     using S = Shape<BN, PAIR>;
     static_assert(!CONV || (BN == 128 && !PAIR && FINE && !A_MN), "one form");
     constexpr int kStages = stages_of<BN, PAIR, MODE, CONV>();
-    constexpr int TM = S::TM, BH = S::BH, A_BYTES = (CONV ? 3 : 1) * S::A_BYTES, STAGE = CONV ? kConvStage : S::STAGE;
+    constexpr int TM = S::TM, BH = S::BH, A_BYTES = (CONV ? 3 : 1) * S::A_BYTES, STAGE = (CONV ? 3 : 1) * S::STAGE;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     __shared__ uint64_t full[kStages], empty[kStages], accfull[2], accempty[2], done;
@@ -653,10 +639,8 @@ __global__ void __launch_bounds__(CONV ? kConvThreads : kThreads, 1) xent_gemm_k
                 ++i;
                 return enter();
             };
-            float v[2][2 * kConvRows];                                   // the two halves of the k block that comes next
-            // DRAM takes longer than a k block does: the block after the next is asked for too
+            float v[2][2 * kConvRows];                        // the two halves of the k block that comes next
             auto load = [&](int h) {
-                if (h == 0) conv_prefetch<B_MN>(p, B_MN ? (kb + kAhead) * kBK : n0, B_MN ? n0 : (kb + kAhead) * kBK, cw * 32 + lane);
                 if constexpr (B_MN) conv_load(p, kb * kBK, n0 + 64 * h, cw, lane, v[h]);
                 else conv_load(p, n0 + 64 * h, kb * kBK, cw, lane, v[h]);
             };
@@ -677,6 +661,9 @@ __global__ void __launch_bounds__(CONV ? kConvThreads : kThreads, 1) xent_gemm_k
                 for (int h = 0; h < 2; ++h) {
                     conv_store(p.b_vec != 0, sb + h * 64 * 128, S::B_BYTES, cw, lane, v[h]);
                     if (more) load(h);
+                    // DRAM takes longer than a k block does: later ones are asked for too
+                    if (more && h == 0)
+                        conv_prefetch<B_MN>(p, B_MN ? (kb + kAhead) * kBK : n0, B_MN ? n0 : (kb + kAhead) * kBK, cw * 32 + lane);
                 }
                 fence_proxy_async();
                 __syncwarp();
@@ -1011,7 +998,7 @@ template <int BN, bool PAIR, int MODE, int TERMS, bool FINE, bool A_MN, bool B_M
 int launch(XParams &p, const Mat &a, const Mat &b, cudaStream_t st, bool dependent = false) {
     using S = Shape<BN, PAIR>;
     constexpr int stages = stages_of<BN, PAIR, MODE, CONV>();
-    constexpr int smem = stages * (CONV ? kConvStage : S::STAGE) + epi_bytes<MODE>() + 1024;
+    constexpr int smem = stages * (CONV ? 3 : 1) * S::STAGE + epi_bytes<MODE>() + 1024;
     static_assert(stages >= (CONV ? 2 : 3) && smem <= 227 * 1024 - 512, "shared memory of one CTA");
     for (int t = 0; t < a.terms; ++t)
         TLB_TRY(make_map(&p.a[t], a.p + t * a.plane, a.rows, a.cols, a.ld, A_MN ? kBK : kBM));
@@ -1089,7 +1076,8 @@ template <int MODE, int TERMS>
 int launch_z(XParams &p, const Mat &h, const Mat &w, bool after_targets, cudaStream_t st) {
     constexpr bool fine = MODE == kStats || TERMS > 1;       // the loss is float32 whatever the operands
     if constexpr (MODE == kStats || TERMS == 3)
-        if (w.f32 != nullptr) return launch<128, false, MODE, TERMS, true, false, false, true>(p, h, w, st, after_targets);
+        if (w.f32 != nullptr)
+            return launch<128, false, MODE, TERMS, true, false, false, true>(p, h, w, st, after_targets);
     if constexpr (TERMS != 2)                                // two terms: up to 64 rows
         if (p.M > kBM) return launch<256, true, MODE, TERMS, fine, false, false>(p, h, w, st, after_targets);
     const int64_t n = num_sms(), t256 = ceil_div(p.N, 256), t128 = ceil_div(p.N, 128);
@@ -1101,7 +1089,8 @@ int launch_z(XParams &p, const Mat &h, const Mat &w, bool after_targets, cudaStr
 template <bool A_MN, bool FINE>
 int launch_out(XParams &p, const Mat &a, const Mat &b, cudaStream_t st) {
     if constexpr (FINE && !A_MN)
-        if (b.f32 != nullptr) return launch<128, false, kOut, 1, true, false, true, true>(p, a, b, st);
+        if (b.f32 != nullptr)
+            return launch<128, false, kOut, 1, true, false, true, true>(p, a, b, st);
     if (p.M > kBM) return launch<256, true, kOut, 1, FINE, A_MN, true>(p, a, b, st);
     return launch<256, false, kOut, 1, FINE, A_MN, true>(p, a, b, st);
 }
@@ -1110,9 +1099,9 @@ constexpr int64_t kPieceBytes = int64_t(512) << 20;   // of dz, and of packed he
 constexpr int64_t kFewRows = 64;                      // bf16 rows up to which dz has two terms
 // Rows up to which a float32 head is taken apart by the product itself, once for every 128 rows,
 // instead of being written as three terms (2.5 times its bytes) before.  Loss, gradient in us:
-//   32768 x 2560    128 rows: 127, 259 against 269, 395   333: 319, 677 against 489, 852   512: 387, 867 against 496, 871
-//   50021 x 1001    128 rows:  97, 194 against 207, 297   333: 217, 461 against 309, 564   512: 293, 616 against 315, 578
-// (2048 rows: 1403, 3311 against 1338, 2815: the larger tiles of the other form pay.)
+//   32768 x 2560    128 rows: 115, 248 against 269, 395   333: 300, 656 against 489, 852   512: 356, 827 against 496, 871
+//   50021 x 1001    128 rows:  89, 192 against 207, 297   333: 189, 439 against 309, 564   512: 255, 586 against 315, 578
+// (2048 rows, before the last steps: 1403, 3311 against 1338, 2815: the larger tiles of the other form pay.)
 constexpr int64_t kConvMost = 512;
 constexpr int64_t kRowChunk = 16384;                  // rows of one pass of the loss (its pairs' buffer)
 
@@ -1220,7 +1209,7 @@ int head_operand(const Plan &q, int wtype, const void *W, int64_t v0, int64_t n,
 // in two turns.  Measured, loss and gradient in us, 32768 x 2560 | 110656 x 832, against tensor cores:
 //   bf16                4 rows: 40, 77 against 44, 91 | 1024 wide, 151936: 75, 153 against 78, 154
 //   float32 and bf16    4 rows: 38, 76 against 82, 147 | 56, 114 against 77, 162;   8 rows: 75, 152 | 111, 226
-//   float32             8 rows: 111, 189 | 137, 280;   12: 165, 284 | 204, 419 against 125, 250 | 130, 285
+//   float32             8 rows: 111, 189 | 137, 280;   12: 165, 284 | 204, 419 against 112, 239 | 126, 295
 bool by_tokens(const Plan &q, int64_t rows, int64_t dim, bool grad) {
     const int64_t turns = ceil_div(rows, 4), last = rows - 4 * (turns - 1);
     return turns <= (q.w_terms > 1 ? 2 : 1) && xent_token_supported(std::min<int64_t>(rows, 4), dim, grad) &&
