@@ -42,7 +42,7 @@
 // the read of W.  Measured at 2048 x 2560 x 131072 in bf16 (727 us a product at the rate of a large
 // library product, 1.89 PFLOP/s): loss 771 us, dz 780 us, dz W 784 us each alone, 1.78 PFLOP/s;
 // 862 and 1755 us for the calls back to back, where the power limit sets the clock.  4096 x 2560 x
-// 65536 with d_w: 2.70 ms (2.18).  Float32 rows, 512 x 2560 x 32768: 400 us (273: three products).
+// 65536 with d_w: 2.70 ms (2.18).  Float32 rows, 512 x 2560 x 32768: 388 us (273: three products).
 #include <cuda.h>
 
 #include <algorithm>
@@ -64,9 +64,10 @@ constexpr int kConvWarps = 8;               // ... and those that take a float32
 constexpr int kConvThreads = kThreads + 32 * kConvWarps;
 constexpr int kEpiWarps = 8;                // two per 32 TMEM lanes (rows), each half of the columns
 constexpr int kMaxTerms = 3, kMaxProd = 6;
-// k blocks (4 MMAs each) of one tensor-memory sum of a float32 result.  Reading a sum out takes
-// the tensor pipe about 300 cycles (the loss of 2048 x 2560 x 131072: 812 us at 8 k blocks, 787
-// at 20), and its error grows with its length.
+// k blocks (4 MMAs each) of one tensor-memory sum of a float32 result, of z and of a gradient.
+// Reading a sum out takes the tensor pipe about 300 cycles (the loss of 2048 x 2560 x 131072: 812 us
+// at 8 k blocks, 787 at 20; 512 float32 rows' gradient 400 us with z in tens, 388), and its error
+// grows with its length.
 constexpr int kChunkLoss = 20, kChunkGrad = 10;
 constexpr int kConvLoss = 3, kConvGrad = 2;  // of six term products each
 constexpr int kGroupM = 16;                 // row tiles that share a column tile before the next one
@@ -429,7 +430,7 @@ __global__ void __launch_bounds__(CONV ? kConvThreads : kThreads, 1) xent_gemm_k
     // this unit's segments: its whole tiles, then its share of the split tiles, cut at tiles
     const int KB = p.nprod * p.kb;
     // k blocks of one accumulator
-    const int chunk = !FINE ? KB : MODE == kStats ? (CONV ? kConvLoss : kChunkLoss) : (CONV ? kConvGrad : kChunkGrad);
+    const int chunk = !FINE ? KB : MODE != kOut ? (CONV ? kConvLoss : kChunkLoss) : (CONV ? kConvGrad : kChunkGrad);
     const int nwhole = p.whole > unit ? (p.whole - unit + p.units - 1) / p.units : 0;
     const bool splits = MODE == kOut && p.sk_work > 0 && unit < p.sk_units;
     const int b0 = splits ? int(sk_start(p.sk_work, p.sk_units, unit)) : 0;       // sk_work < units KB < 2^31
