@@ -338,10 +338,11 @@ int tlb_muon(const tlb_muon_mat *mats, int32_t n, const tlb_muon_cfg *cfg, void 
  * (An infinity in a float32 operand counts as NaN.)
  *
  * rows >= 0 (0 rows: no-op, d_w set to 0), vocab >= 1, dim >= 1, of any size up to 2^24,
- * 2^24 and 2^20 (dim % 8 != 0 costs a padded copy of the operands).  The backward pass walks
- * through the vocabulary in pieces whose dz stays in the workspace (512 MB at most; at
- * least 2048 columns).  Same inputs, same bits: no sum depends on timing.  d_hidden may be
- * hidden itself; no other output may overlap an input or another output.
+ * 2^24 and 2^20.  bf16 operands with dim % 8 != 0, bf16 rows where d_w is asked for, float32
+ * rows and, past 512 rows, a float32 head are copied to the workspace (padded, as bf16 terms).
+ * The backward pass walks through the vocabulary in pieces whose dz stays in the workspace
+ * (512 MB at most; at least 2048 columns).  Same inputs, same bits: no sum depends on timing.
+ * d_hidden may be hidden itself; no other output may overlap an input or another output.
  * ws: zero-filled once, 256-byte aligned, tlb_xent_workspace_bytes() bytes (enough for both
  * calls; 0 for sizes or types that the calls refuse).  grad_w: whether d_w will be asked for. */
 size_t tlb_xent_workspace_bytes(int32_t htype, int32_t wtype, int64_t rows, int64_t vocab, int64_t dim, int32_t grad_w);
