@@ -64,13 +64,14 @@ struct Mat {
     int32_t r, n;
     int32_t tall;                        // stored [n, r] (else [r, n])
     int32_t vec;                         // 16-byte accesses (aligned; r % 4 == 0 of a tall one, n % 4 == 0 of a wide one)
-    int32_t block0, ctas;                // first block of this matrix; (clusters) how many, (passes) partial Gram matrices
+    int32_t block0, ctas;                // first block of this matrix, and how many (one a tile for r > 32)
     float lr, lr_scale;                  // lr lr_mult, and times scale
 };
 
 struct Params {
     Mat mat[kMaxMats];
     int nmat, tiles_per_block;
+    int tiles;                           // r > 32: column tiles of all matrices, numbered through (block0: a matrix's first)
     float *ws;
     int64_t mpoly;                       // offset of the products M [nmat][RP * RP]
     uint32_t *status;
@@ -799,6 +800,32 @@ __device__ __forceinline__ void tc_load_update(const Params &p, const Mat &a, ui
     });
 }
 
+// The lines of a pass's next tile on their way to L2 while this one is worked on.
+__device__ __forceinline__ void prefetch_l2(const float *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+__device__ __forceinline__ void prefetch_tile(const Mat &a, const float *x, int j0, int jn) {
+    if (a.tall) {
+        for (int k = threadIdx.x * 32; k < jn * a.r; k += NT * 32) prefetch_l2(x + int64_t(j0) * a.r + k);
+    } else {
+        for (int k = threadIdx.x; k < a.r * (kTcJ / 32); k += NT) {
+            const int c = (k % (kTcJ / 32)) * 32;
+            if (c < jn) prefetch_l2(x + int64_t(k / (kTcJ / 32)) * a.n + j0 + c);
+        }
+    }
+}
+template <int SOURCE, int SINK>
+__device__ __forceinline__ void tc_prefetch(const Params &p, int lo, int g) {
+    if (lo + 1 < p.nmat && p.mat[lo + 1].block0 <= g) ++lo;
+    const Mat &a = p.mat[lo];
+    const int t = g - a.block0, j0 = t * kTcJ, jn = min(kTcJ, a.n - j0);
+    if constexpr (SOURCE == kY) {
+        prefetch_l2(p.ws + a.y + int64_t(t) * 64 * kTcJ + threadIdx.x * 32);
+    } else {
+        prefetch_tile(a, a.g, j0, jn);
+        prefetch_tile(a, a.m, j0, jn);
+    }
+    if constexpr (SINK == kParam) prefetch_tile(a, a.p, j0, jn);
+}
+
 template <int SOURCE, int SINK>
 __global__ void __launch_bounds__(NT, tc_ctas<SOURCE, SINK>()) muon_tc_pass_kernel(const __grid_constant__ Params p) {
     using T = Tile<64>;
@@ -808,15 +835,14 @@ __global__ void __launch_bounds__(NT, tc_ctas<SOURCE, SINK>()) muon_tc_pass_kern
     __shared__ uint64_t bar_y, bar_g;
     __shared__ uint32_t tmem_base;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int lo = 0, hi = p.nmat - 1;                            // this block's matrix
+    // this block's share of all matrices' tiles, and the matrix of the first
+    const int g0 = int(int64_t(p.tiles) * blockIdx.x / gridDim.x), g1 = int(int64_t(p.tiles) * (blockIdx.x + 1) / gridDim.x);
+    int lo = 0, hi = p.nmat - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
-        if (p.mat[mid].block0 <= int(blockIdx.x)) lo = mid;
+        if (p.mat[mid].block0 <= g0) lo = mid;
         else hi = mid - 1;
     }
-    const Mat &a = p.mat[lo];
-    const int bl = blockIdx.x - a.block0, t0 = bl * p.tiles_per_block;
-    const int t1 = min((a.n + kTcJ - 1) / kTcJ, t0 + p.tiles_per_block);
     if (warp == 0) {
         tmem_alloc(&tmem_base, tc_columns<SOURCE, SINK>());
         tmem_relinquish();
@@ -830,15 +856,15 @@ __global__ void __launch_bounds__(NT, tc_ctas<SOURCE, SINK>()) muon_tc_pass_kern
     auto clear = [&] {
         for (int k = tid; k < 3 * kXPlane / 16; k += NT) reinterpret_cast<uint4 *>(planes)[k] = make_uint4(0, 0, 0, 0);
     };
-    clear();                                                 // rows past r stay 0
-    if constexpr (SOURCE != kMomentum) {
+    auto load_m = [&] {
         const float *src = p.ws + p.mpoly + int64_t(lo) * 64 * 64;
         for (int k = tid; k < 64 * 16; k += NT) {
             float v[4];
             load_piece<4>(src + 4 * k, v);
             put_terms<4, 1>(mplanes, kMPlane, k / 16, (k % 16) * 4, v);
         }
-    }
+    };
+    if constexpr (SOURCE != kMomentum) load_m();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = tmem_base, td1 = tmem, td2 = tmem + 64, ty = SINK == kParam ? tmem : tmem + 128;
@@ -846,11 +872,16 @@ __global__ void __launch_bounds__(NT, tc_ctas<SOURCE, SINK>()) muon_tc_pass_kern
     constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(64 >> 3) << 17) | (uint32_t(128 >> 4) << 24);
     const int q = warp & 3, half = warp >> 2;               // TMEM lanes (columns of X), half of the rows
     int done = 0;
-    for (int t = t0; t < t1; ++t, ++done) {
-        const int j0 = t * kTcJ, jn = min(kTcJ, a.n - j0);
+    for (int g = g0; g < g1; ++g, ++done) {
+        if (lo + 1 < p.nmat && p.mat[lo + 1].block0 <= g) {  // the next matrix
+            ++lo;
+            if constexpr (SOURCE != kMomentum) load_m();
+        }
+        const Mat &a = p.mat[lo];
+        const int t = g - a.block0, j0 = t * kTcJ, jn = min(kTcJ, a.n - j0);
         float *y = p.ws + a.y + int64_t(t) * 64 * kTcJ;      // this tile of Y: [64][128]
-        // columns past the last count as 0, and so do rows past r where sums lay in the planes
-        if (jn < kTcJ || (SINK != kParam && done > 0 && a.r < 64)) {
+        // columns past the last count as 0, and so do rows past r (Y has them)
+        if (SOURCE != kY && (jn < kTcJ || a.r < 64)) {
             clear();
             __syncthreads();
         }
@@ -868,6 +899,7 @@ __global__ void __launch_bounds__(NT, tc_ctas<SOURCE, SINK>()) muon_tc_pass_kern
         fence_proxy_async();
         tc_fence_before();
         __syncthreads();
+        if (g + 1 < g1) tc_prefetch<SOURCE, SINK>(p, lo, g + 1);
         if constexpr (SOURCE != kMomentum) {
             if (tid == 0) {
                 tc_fence_after();
@@ -986,7 +1018,7 @@ __global__ void __launch_bounds__(NT, tc_ctas<SOURCE, SINK>()) muon_tc_pass_kern
                 gram_place<64>(e, i, k);
                 out[e] = s1[i * 65 + k] + (s2[i * 65 + k] + s2[k * 65 + i]);
             }
-            if (t + 1 < t1) __syncthreads();                 // the planes are free again
+            __syncthreads();                                 // the planes are free again
         }
     }
     __syncthreads();
@@ -1108,7 +1140,7 @@ int pass(const Params &p, unsigned blocks, cudaStream_t st) {
         auto k = muon_tc_pass_kernel<SOURCE, SINK>;
         constexpr int smem = tc_smem<SOURCE, SINK>();
         TLB_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-        k<<<blocks, NT, smem, st>>>(p);
+        k<<<std::min<int>(p.tiles, tc_ctas<SOURCE, SINK>() * num_sms()), NT, smem, st>>>(p);
         return check_launch("muon_tc_pass");
     } else {
         constexpr int smem = pass_floats<RP>() * 4;
@@ -1127,7 +1159,8 @@ int group(const tlb_muon_mat *mats, int *idx, int n, bool clusters, const tlb_mu
     for (int k = 0; k < n; ++k) tiles += tiles_of<RP>(std::max(mats[idx[k]].rows, mats[idx[k]].cols));
     int32_t ctas[kMaxMats], block0[kMaxMats];
     if (clusters) blocks = place<RP>(mats, idx, n, ctas, block0);
-    p.tiles_per_block = tiles_per_block(tiles);
+    p.tiles_per_block = RP == 64 ? 1 : tiles_per_block(tiles);
+    p.tiles = int(tiles);
     p.nmat = n;
     p.ws = ws;
     p.status = reinterpret_cast<uint32_t *>(reinterpret_cast<char *>(ws) - kStatusBytes);
@@ -1155,10 +1188,9 @@ int group(const tlb_muon_mat *mats, int *idx, int n, bool clusters, const tlb_mu
             a.ctas = ctas[k];
             a.block0 = block0[k];
         } else {
-            const int64_t t = tiles_of<RP>(a.n), nb = ceil_div(t, p.tiles_per_block);
-            a.ctas = int(RP == 64 ? t : nb);                 // partial Gram matrices
+            a.ctas = int(ceil_div(tiles_of<RP>(a.n), p.tiles_per_block));
             a.block0 = int(blocks);
-            blocks += nb;
+            blocks += a.ctas;
         }
         a.y = off;
         off += tiles_of<RP>(a.n) * RP * pass_columns<RP>();
