@@ -694,6 +694,14 @@ constexpr int kXPlane = 64 * kTcJ * 2, kMPlane = 64 * 64 * 2;
 template <int SOURCE, int SINK> constexpr int tc_smem() {
     return 1024 + 3 * kXPlane + (SOURCE == kMomentum ? 64 * 128 : SINK == kParam ? 3 * kMPlane : 84 * 1024 - 1024 - 3 * kXPlane);
 }
+// Partial Gram matrices here: the upper 8 x 8 blocks one after another, each by rows (the place of an
+// element costs a division or two less than in the order of the CUDA-core passes, which took 5000
+// cycles of a tile's 14000).
+__device__ __forceinline__ uchar2 tc_pair(int pair) {
+    int bi, bk;
+    pair_of<8>(pair, bi, bk);
+    return make_uchar2(uint8_t(bi), uint8_t(bk));
+}
 template <int SOURCE, int SINK> constexpr int tc_columns() { return SINK == kParam ? 64 : SOURCE == kMomentum ? 128 : 256; }
 template <int SOURCE, int SINK> constexpr int tc_ctas() { return SOURCE == kMomentum || SINK == kParam ? 3 : 2; }
 
@@ -834,6 +842,8 @@ __global__ void __launch_bounds__(NT, tc_ctas<SOURCE, SINK>()) muon_tc_pass_kern
     uint8_t *mplanes = planes + 3 * kXPlane;
     __shared__ uint64_t bar_y, bar_g;
     __shared__ uint32_t tmem_base;
+    __shared__ uchar2 s_pair[T::PAIRS];
+    if (threadIdx.x < T::PAIRS) s_pair[threadIdx.x] = tc_pair(threadIdx.x);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // this block's share of all matrices' tiles, and the matrix of the first
     const int g0 = int(int64_t(p.tiles) * blockIdx.x / gridDim.x), g1 = int(int64_t(p.tiles) * (blockIdx.x + 1) / gridDim.x);
@@ -1014,8 +1024,7 @@ __global__ void __launch_bounds__(NT, tc_ctas<SOURCE, SINK>()) muon_tc_pass_kern
             __syncthreads();
             float *out = p.ws + a.part + int64_t(t) * T::GSIZE;
             for (int e = tid; e < T::GSIZE; e += NT) {
-                int i, k;
-                gram_place<64>(e, i, k);
+                const int i = s_pair[e >> 6].x * 8 + ((e >> 3) & 7), k = s_pair[e >> 6].y * 8 + (e & 7);
                 out[e] = s1[i * 65 + k] + (s2[i * 65 + k] + s2[k * 65 + i]);
             }
             __syncthreads();                                 // the planes are free again
@@ -1062,7 +1071,13 @@ __global__ void __launch_bounds__(kPolyThreads<RP>) muon_poly_kernel(const __gri
         const int e = threadIdx.x + o * PT;
         if (e < T::GSIZE) {
             int i, k;
-            gram_place<RP>(e, i, k);
+            if constexpr (RP == 64) {
+                const uchar2 b = tc_pair(e >> 6);
+                i = b.x * 8 + ((e >> 3) & 7);
+                k = b.y * 8 + (e & 7);
+            } else {
+                gram_place<RP>(e, i, k);
+            }
             gm[i * LM + k] = g[o];
             gm[k * LM + i] = g[o];
         }
