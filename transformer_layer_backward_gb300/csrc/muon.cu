@@ -128,6 +128,17 @@ __device__ __forceinline__ void pair_of(int q, int &bi, int &bk) {
     bk = bi + q;
 }
 
+// All of them into a table in shared memory (a barrier follows before its use): a search for every
+// element of a Gram matrix would cost more than the rest of its sum.
+template <int RP>
+__device__ __forceinline__ void fill_pairs(uchar2 *pairs) {
+    if (threadIdx.x < Tile<RP>::PAIRS) {
+        int bi, bk;
+        pair_of<Tile<RP>::NB>(threadIdx.x, bi, bk);
+        pairs[threadIdx.x] = make_uchar2(uint8_t(bi), uint8_t(bk));
+    }
+}
+
 // Walks through a tile's elements (columns j0 .. j0 + jn): f(C, S, e, de, at, dat, n) for runs of
 // n pieces of this thread.  A piece is C::value contiguous elements; piece s starts at element
 // e + s de of the matrix and stands at at + s dat of the tile, its elements S::value places
@@ -320,15 +331,15 @@ __device__ __forceinline__ void apply(float *x, const float *mt, int jn) {
 // This thread's share of the tile's Gram matrix: block (bi, bk) over the column
 // quads grp, grp + GROUPS, ...
 template <int RP>
-__device__ __forceinline__ void gram_tile(const float *x, int jn, float (&acc)[Tile<RP>::B][Tile<RP>::B]) {
+__device__ __forceinline__ void gram_tile(const uchar2 *pairs, const float *x, int jn, float (&acc)[Tile<RP>::B][Tile<RP>::B]) {
     using T = Tile<RP>;
     constexpr int B = T::B, NB = T::NB, LD = T::LD;
-    int grp, pair, bi, bk;
+    int grp, pair;
     Gram<RP>::mine(grp, pair);
 #pragma unroll
     for (int k = 0; k < B * B; ++k) acc[k / B][k % B] = 0.f;
     if (grp >= Gram<RP>::GROUPS) return;
-    pair_of<NB>(pair, bi, bk);
+    const int bi = pairs[pair].x, bk = pairs[pair].y;
     const int quads = (jn + 3) / 4;
 #pragma unroll 1
     for (int q = grp; q < quads; q += Gram<RP>::GROUPS) {
@@ -394,13 +405,12 @@ __device__ __forceinline__ void gram_keep(const float (&s)[Gram<RP>::OWN], float
 
 // Element e of [B * B][pair]: its row and column.
 template <int RP>
-__device__ __forceinline__ void gram_place(int e, int &i, int &k) {
+__device__ __forceinline__ void gram_place(const uchar2 *pairs, int e, int &i, int &k) {
     using T = Tile<RP>;
-    int bi, bk;
-    pair_of<T::NB>(e % T::PAIRS, bi, bk);
-    const int q = e / T::PAIRS;
-    i = bi + T::NB * (q / T::B);
-    k = bk + T::NB * (q % T::B);
+    const uint32_t q = uint32_t(e) / T::PAIRS;
+    const uchar2 b = pairs[uint32_t(e) - q * T::PAIRS];
+    i = b.x + T::NB * int(q / T::B);
+    k = b.y + T::NB * int(q % T::B);
 }
 
 // The product of `steps` Newton-Schulz polynomials P of G, times `scale`, in mm.  gm: G
@@ -564,6 +574,8 @@ __global__ void __launch_bounds__(NT, RP <= 16 ? 4 : 1) muon_cluster_kernel(cons
     float *x = sh, *gm = x + T::XF, *sq = gm + RP * LM, *pm = sq + RP * LM, *mm = pm + RP * LM;
     float *part = mm + RP * LM, *red = part + 2 * T::GSIZE;  // part: two, for alternate runs
     __shared__ float s_inv;
+    __shared__ uchar2 pairs[T::PAIRS];
+    fill_pairs<RP>(pairs);
     int lo = 0, hi = p.nmat - 1;                            // this CTA's matrix
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
@@ -587,7 +599,7 @@ __global__ void __launch_bounds__(NT, RP <= 16 ? 4 : 1) muon_cluster_kernel(cons
         float *mine = part + (run & 1) * T::GSIZE;
         {
             float acc[B][B], s[Gram<RP>::OWN] = {};
-            gram_tile<RP>(x, jn, acc);
+            gram_tile<RP>(pairs, x, jn, acc);
             gram_sum<RP>(acc, red, s);
             gram_keep<RP>(s, mine);
         }
@@ -599,7 +611,7 @@ __global__ void __launch_bounds__(NT, RP <= 16 ? 4 : 1) muon_cluster_kernel(cons
 #pragma unroll
             for (int c = 0; c < kCluster; ++c) s += v[c];
             int i, k;
-            gram_place<RP>(e, i, k);
+            gram_place<RP>(pairs, e, i, k);
             gm[i * LM + k] = s;
             gm[k * LM + i] = s;
         }
@@ -628,6 +640,8 @@ __global__ void __launch_bounds__(NT) muon_pass_kernel(const __grid_constant__ P
     constexpr int JT = T::JT, LD = T::LD, LM = T::LM, B = T::B;
     extern __shared__ __align__(16) float sh[];
     float *x = sh, *mt = x + T::XF;
+    __shared__ uchar2 pairs[T::PAIRS];
+    fill_pairs<RP>(pairs);
     int lo = 0, hi = p.nmat - 1;                            // this block's matrix
     while (lo < hi) {
         const int mid = (lo + hi + 1) / 2;
@@ -667,7 +681,7 @@ __global__ void __launch_bounds__(NT) muon_pass_kernel(const __grid_constant__ P
                         *reinterpret_cast<const float4 *>(x + (k / jq) * LD + (k % jq) * 4);
             }
             float acc[B][B];
-            gram_tile<RP>(x, jn, acc);
+            gram_tile<RP>(pairs, x, jn, acc);
             gram_sum<RP>(acc, x, s);       // the tile is used up
         }
     }
@@ -693,14 +707,6 @@ constexpr int kXPlane = 64 * kTcJ * 2, kMPlane = 64 * 64 * 2;
 // of the pass that has all of it.
 template <int SOURCE, int SINK> constexpr int tc_smem() {
     return 1024 + 3 * kXPlane + (SOURCE == kMomentum ? 64 * 128 : SINK == kParam ? 3 * kMPlane : 84 * 1024 - 1024 - 3 * kXPlane);
-}
-// Partial Gram matrices here: the upper 8 x 8 blocks one after another, each by rows (the place of an
-// element costs a division or two less than in the order of the CUDA-core passes, which took 5000
-// cycles of a tile's 14000).
-__device__ __forceinline__ uchar2 tc_pair(int pair) {
-    int bi, bk;
-    pair_of<8>(pair, bi, bk);
-    return make_uchar2(uint8_t(bi), uint8_t(bk));
 }
 template <int SOURCE, int SINK> constexpr int tc_columns() { return SINK == kParam ? 64 : SOURCE == kMomentum ? 128 : 256; }
 template <int SOURCE, int SINK> constexpr int tc_ctas() { return SOURCE == kMomentum || SINK == kParam ? 3 : 2; }
@@ -808,6 +814,14 @@ __device__ __forceinline__ void tc_load_update(const Params &p, const Mat &a, ui
     });
 }
 
+// Partial Gram matrices here are the upper 8 x 8 blocks one after another, each by rows: the row
+// and column of element e.
+__device__ __forceinline__ void block_place(const uchar2 *pairs, int e, int &i, int &k) {
+    const uchar2 b = pairs[e >> 6];
+    i = b.x * 8 + ((e >> 3) & 7);
+    k = b.y * 8 + (e & 7);
+}
+
 // The lines of a pass's next tile on their way to L2 while this one is worked on.
 __device__ __forceinline__ void prefetch_l2(const float *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void prefetch_tile(const Mat &a, const float *x, int j0, int jn) {
@@ -842,8 +856,8 @@ __global__ void __launch_bounds__(NT, tc_ctas<SOURCE, SINK>()) muon_tc_pass_kern
     uint8_t *mplanes = planes + 3 * kXPlane;
     __shared__ uint64_t bar_y, bar_g;
     __shared__ uint32_t tmem_base;
-    __shared__ uchar2 s_pair[T::PAIRS];
-    if (threadIdx.x < T::PAIRS) s_pair[threadIdx.x] = tc_pair(threadIdx.x);
+    __shared__ uchar2 pairs[T::PAIRS];
+    fill_pairs<64>(pairs);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // this block's share of all matrices' tiles, and the matrix of the first
     const int g0 = int(int64_t(p.tiles) * blockIdx.x / gridDim.x), g1 = int(int64_t(p.tiles) * (blockIdx.x + 1) / gridDim.x);
@@ -1024,7 +1038,8 @@ __global__ void __launch_bounds__(NT, tc_ctas<SOURCE, SINK>()) muon_tc_pass_kern
             __syncthreads();
             float *out = p.ws + a.part + int64_t(t) * T::GSIZE;
             for (int e = tid; e < T::GSIZE; e += NT) {
-                const int i = s_pair[e >> 6].x * 8 + ((e >> 3) & 7), k = s_pair[e >> 6].y * 8 + (e & 7);
+                int i, k;
+                block_place(pairs, e, i, k);
                 out[e] = s1[i * 65 + k] + (s2[i * 65 + k] + s2[k * 65 + i]);
             }
             __syncthreads();                                 // the planes are free again
@@ -1047,6 +1062,8 @@ __global__ void __launch_bounds__(kPolyThreads<RP>) muon_poly_kernel(const __gri
     extern __shared__ __align__(16) float sh[];
     float *gm = sh, *sq = gm + RP * LM, *pm = sq + RP * LM, *mm = pm + RP * LM;
     __shared__ float s_inv;
+    __shared__ uchar2 pairs[T::PAIRS];
+    fill_pairs<RP>(pairs);
     const Mat &a = p.mat[blockIdx.x];
     const float *part = p.ws + a.part;
     const int nb = a.ctas;
@@ -1066,18 +1083,14 @@ __global__ void __launch_bounds__(kPolyThreads<RP>) muon_poly_kernel(const __gri
 #pragma unroll
             for (int o = 0; o < OWN; ++o) g[o] += v[u][o];
     }
+    __syncthreads();
 #pragma unroll
     for (int o = 0; o < OWN; ++o) {
         const int e = threadIdx.x + o * PT;
         if (e < T::GSIZE) {
             int i, k;
-            if constexpr (RP == 64) {
-                const uchar2 b = tc_pair(e >> 6);
-                i = b.x * 8 + ((e >> 3) & 7);
-                k = b.y * 8 + (e & 7);
-            } else {
-                gram_place<RP>(e, i, k);
-            }
+            if constexpr (RP == 64) block_place(pairs, e, i, k);
+            else gram_place<RP>(pairs, e, i, k);
             gm[i * LM + k] = g[o];
             gm[k * LM + i] = g[o];
         }
