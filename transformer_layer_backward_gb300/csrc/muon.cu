@@ -293,9 +293,10 @@ __device__ __forceinline__ void move_params(const Params &p, const Mat &a, const
 
 // X <- M X on the shared tile: a thread owns a column pair (for r > 32 half of its rows), so
 // the product goes back in place, past one barrier where two threads share a column.  mt: M's
-// columns as rows; the same for all threads, as x is for the rows of a column.
+// columns as rows; the same for all threads, as x is for the rows of a column.  kr: r rounded up to
+// 8, past which rows are 0.
 template <int RP>
-__device__ __forceinline__ void apply(float *x, const float *mt, int jn) {
+__device__ __forceinline__ void apply(float *x, const float *mt, int jn, int kr) {
     constexpr int LD = Tile<RP>::LD, LM = Tile<RP>::LM;
     constexpr int RH = RP > 32 ? 32 : RP, HALVES = RP / RH, W = NT / HALVES;
     static_assert(HALVES == 1 || 2 * W >= Tile<RP>::JT, "all columns at once where a barrier stands between");
@@ -308,7 +309,7 @@ __device__ __forceinline__ void apply(float *x, const float *mt, int jn) {
         for (int i = 0; i < RH; ++i) y[i] = make_float2(0.f, 0.f);
         if (j < jn) {
 #pragma unroll 2
-            for (int k = 0; k < RP; ++k) {
+            for (int k = 0; k < (RP > 32 ? kr : RP); ++k) {
                 const float2 v = *reinterpret_cast<const float2 *>(x + k * LD + j);
 #pragma unroll
                 for (int i = 0; i < RH; i += 4) {
@@ -424,11 +425,12 @@ __device__ __forceinline__ void polynomial(float *gm, float *sq, float *pm, floa
     constexpr int LM = Tile<RP>::LM;
     constexpr bool WARP = RP <= 16;
     // a thread's DR x DC elements
-    constexpr int DC = RP == 64 ? 1024 / PT : RP == 8 ? 1 : 2, DR = RP == 64 || RP == 16 ? 4 : 2, W = RP / DC;
-    static_assert(W * (RP / DR) <= (WARP ? 32 : PT), "threads of a product");
-    const int tid = threadIdx.x, r0 = (tid / W) * DR, c0 = (tid % W) * DC;
+    constexpr int DC = RP == 64 ? 1024 / PT : RP == 8 ? 1 : 2, DR = RP == 64 || RP == 16 ? 4 : 2;
+    static_assert((RP / DC) * (RP / DR) <= (WARP ? 32 : PT), "threads of a product");
     if constexpr (WARP) kr = RP;                             // unrolled whole
-    const bool on = r0 < kr && c0 < kr;
+    // as few warps as hold the kr x kr elements, so that no scheduler has more of them than another
+    const int tid = threadIdx.x, W = (WARP ? RP : kr) / DC, r0 = (tid / W) * DR, c0 = (tid % W) * DC;
+    const bool on = r0 < kr;
     auto sync = [] {
         if constexpr (WARP) __syncwarp();
         else __syncthreads();
@@ -591,7 +593,7 @@ __global__ void __launch_bounds__(NT, RP <= 16 ? 4 : 1) muon_cluster_kernel(cons
     }
     const int peer0 = int(cluster_rank()) - rank;
     const int w = ((a.n + ctas - 1) / ctas + 3) & ~3;
-    const int j0 = min(a.n, rank * w), jn = min(w, a.n - j0);
+    const int j0 = min(a.n, rank * w), jn = min(w, a.n - j0), kr = (a.r + 7) & ~7;
     load_update<RP, true>(p, a, x, j0, jn);
     float scale = 1.f;
     for (int done = 0, run = 0; done < p.steps; ++run) {
@@ -604,23 +606,33 @@ __global__ void __launch_bounds__(NT, RP <= 16 ? 4 : 1) muon_cluster_kernel(cons
             gram_keep<RP>(s, mine);
         }
         cluster_meet();
-        for (int e = threadIdx.x; e < T::GSIZE; e += NT) {
-            float v[kCluster], s = 0.f;
+        constexpr int EU = Gram<RP>::OWN % 3 == 0 ? 3 : 1;  // elements whose peers' shares are in flight together
+        for (int e0 = threadIdx.x; e0 < T::GSIZE; e0 += EU * NT) {
+            float v[EU][kCluster];
 #pragma unroll
-            for (int c = 0; c < kCluster; ++c) v[c] = c < ctas ? ld_cluster(mine + e, peer0 + c) : 0.f;
+            for (int o = 0; o < EU; ++o)
 #pragma unroll
-            for (int c = 0; c < kCluster; ++c) s += v[c];
-            int i, k;
-            gram_place<RP>(pairs, e, i, k);
-            gm[i * LM + k] = s;
-            gm[k * LM + i] = s;
+                for (int c = 0; c < kCluster; ++c)
+                    v[o][c] = c < ctas && e0 + o * NT < T::GSIZE ? ld_cluster(mine + e0 + o * NT, peer0 + c) : 0.f;
+#pragma unroll
+            for (int o = 0; o < EU; ++o) {
+                const int e = e0 + o * NT;
+                if (e >= T::GSIZE) break;
+                float s = 0.f;
+#pragma unroll
+                for (int c = 0; c < kCluster; ++c) s += v[o][c];
+                int i, k;
+                gram_place<RP>(pairs, e, i, k);
+                gm[i * LM + k] = s;
+                gm[k * LM + i] = s;
+            }
         }
         __syncthreads();
         if (run == 0) scale = normalise<RP>(gm, &s_inv, p.eps);
         const int steps = min(run == 0 ? kFirstRun : kRun, p.steps - done);
-        polynomial<RP>(gm, sq, pm, mm, steps, (a.r + 7) & ~7, p.a, p.b, p.c, run == 0 ? scale : 1.f);
+        polynomial<RP>(gm, sq, pm, mm, steps, kr, p.a, p.b, p.c, run == 0 ? scale : 1.f);
         done += steps;
-        apply<RP>(x, mm, jn);
+        apply<RP>(x, mm, jn, kr);
     }
     __syncthreads();
     move_params<RP>(p, a, x, j0, jn);
@@ -668,7 +680,7 @@ __global__ void __launch_bounds__(NT) muon_pass_kernel(const __grid_constant__ P
         }
         __syncthreads();
         if constexpr (SOURCE != kMomentum) {
-            apply<RP>(x, mt, jn);
+            apply<RP>(x, mt, jn, RP);
             __syncthreads();
         }
         if constexpr (SINK == kParam) {
