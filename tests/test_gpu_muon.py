@@ -191,6 +191,31 @@ def test_muon_beside_others(lib, rows, cols, copies):
         assert all(torch.equal(one[k], x) for x in many[k])
 
 
+@pytest.mark.parametrize("steps", [1, 5])
+def test_muon_mixed_shapes_together(lib, steps):
+    """Long matrices of ranks above 32 share blocks with others of another rank, side or alignment,
+    one of them full of NaN: the same bits as each by itself."""
+    import torch
+    gen = torch.Generator(device="cuda").manual_seed(6)
+    shapes = [(64, 2560), (40, 3001), (2999, 33), (4096, 64), (50, 2100), (3500, 52), (63, 2049)] * 9
+    sets = [[torch.randn(s, generator=gen, device="cuda") * 0.02 for _ in range(3)] for s in shapes]
+    sets[3][1].fill_(float("nan"))
+    cfg = lib.muon_cfg(0.02, 0.95, 0.1, 1e-7, COEF, steps, True)
+    alone = [[x.clone() for x in xs] for xs in sets]
+    for xs in alone:
+        mats = lib.muon_mats(*([x] for x in xs))
+        lib.muon(mats, cfg, lib.muon_workspace(mats))
+    mats = lib.muon_mats(*([xs[k] for xs in sets] for k in range(3)))
+    ws = lib.muon_workspace(mats)
+    ws[256:].fill_(255)                                       # NaN in whatever is read unwritten
+    lib.muon(mats, cfg, ws)
+    for i, (xs, ys) in enumerate(zip(sets, alone)):
+        assert bool(torch.isnan(xs[0]).any()) == (i == 3)
+        for k in (0, 2):
+            assert torch.equal(xs[k].nan_to_num(7.0), ys[k].nan_to_num(7.0)), (i, shapes[i])
+    lib.workspace_status(ws)
+
+
 def test_muon_refusals(lib):
     import torch
     z = lambda *s: torch.zeros(*s, device="cuda")

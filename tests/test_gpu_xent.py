@@ -24,7 +24,7 @@ TYPES = [("bf16", "bf16"), ("f32", "bf16"), ("f32", "f32")]
 HALF = 2.0 ** -8
 SHAPES = [(1, 1, 1), (1, 2, 8), (1, 7, 64), (1, 5000, 2560), (2, 300, 72), (31, 129, 63), (64, 257, 136),
           (127, 1000, 100), (128, 512, 128), (129, 511, 130), (257, 1023, 65), (300, 5003, 1001), (520, 20000, 320), (512, 700, 260), (513, 700, 260), (200, 3001, 3073),
-          (130, 40, 1030), (100, 70000, 36)]
+          (130, 40, 1030), (100, 70000, 36), (20, 5, 1), (40, 1, 3)]
 
 
 def normal(name, shape, std=1.0):

@@ -31,14 +31,14 @@
 //
 // Bounds, and measured (five steps):
 //   one 16 x 2560 matrix: latency of the phases, 16 us in one launch (20 bytes an element are 0.1 us)
-//   144 rank-16 matrices of a 36-layer stack, 118 MB to move (17.4 us): 53 us in one launch.  Its CTAs
+//   144 rank-16 matrices of a 36-layer stack, 118 MB to move (17.4 us): 51 us in one launch.  Its CTAs
 //     go through reading, r x r products and writing in step, so that HBM idles in the middle:
 //     two reads and two Gram sums of X in shared memory, then two chains of r x r products
-//   seven 5 x 1001 and three 999 x 33 matrices: 74 us in two launches, chains of 14 r x r products
-//   144 rank-64 matrices, 472 MB (69.6 us; 189 MB read by each pass): 391 us, three passes and two
-//     launches of r x r products; the passes wait for loads, for taking floats apart and for their
-//     Gram matrices, which leave tile by tile (sums of two tiles in tensor memory: 349 us and five
-//     times the error, 1e-6 against 2e-7 in p; one tile a block: 406 us)
+//   seven 5 x 1001 and three 999 x 33 matrices: 62 us in two launches, chains of 14 r x r products
+//   144 rank-64 matrices, 472 MB (69.6 us; 189 MB read by each pass): 341 us, passes of 75, 115 and
+//     92 us and r x r products of 24 and 33 us; the passes wait for loads, for taking floats apart and
+//     for their Gram matrices, which leave tile by tile (sums of two tiles in tensor memory: five
+//     times the error, 1e-6 against 2e-7 in p)
 #include <algorithm>
 #include <cmath>
 #include <cstring>
