@@ -54,6 +54,11 @@ namespace {
 
 constexpr int kMaxMats = 256;            // matrices of one launch (their table is a kernel parameter)
 constexpr int kFirstRun = 2, kRun = 3;    // steps from the first and from each later Gram matrix
+// Steps of the run after `done`: the later ones as even as they can be (of six steps 2, 2, 2, not 2, 3, 1).
+__host__ __device__ __forceinline__ int run_length(int done, int steps) {
+    const int rest = steps - done, runs = (rest + kRun - 1) / kRun;
+    return done == 0 ? (rest < kFirstRun ? rest : kFirstRun) : (rest + runs - 1) / runs;
+}
 constexpr int kCluster = 8;              // CTAs of a cluster; one to all of them hold one matrix
 constexpr int NT = 256;                  // threads of every kernel
 
@@ -587,7 +592,7 @@ __global__ void __launch_bounds__(NT, RP <= 16 ? 4 : 1) muon_cluster_kernel(cons
     const Mat &a = p.mat[lo];
     const int rank = int(blockIdx.x) - a.block0, ctas = a.ctas;
     if (rank >= ctas) {
-        for (int done = 0; done < p.steps; done += done == 0 ? kFirstRun : kRun) cluster_meet();
+        for (int done = 0; done < p.steps; done += run_length(done, p.steps)) cluster_meet();
         cluster_meet();
         return;
     }
@@ -629,7 +634,7 @@ __global__ void __launch_bounds__(NT, RP <= 16 ? 4 : 1) muon_cluster_kernel(cons
         }
         __syncthreads();
         if (run == 0) scale = normalise<RP>(gm, &s_inv, p.eps);
-        const int steps = min(run == 0 ? kFirstRun : kRun, p.steps - done);
+        const int steps = run_length(done, p.steps);
         polynomial<RP>(gm, sq, pm, mm, steps, kr, p.a, p.b, p.c, run == 0 ? scale : 1.f);
         done += steps;
         apply<RP>(x, mm, jn, kr);
@@ -1262,7 +1267,7 @@ int group(const tlb_muon_mat *mats, int *idx, int n, bool clusters, const tlb_mu
     TLB_TRY((pass<RP, kMomentum, kGram>(p, grid, st)));
     for (int done = 0; done < cfg.steps;) {
         const bool first = done == 0;
-        const int steps = std::min(first ? kFirstRun : kRun, cfg.steps - done);
+        const int steps = run_length(done, cfg.steps);
         muon_poly_kernel<RP><<<unsigned(n), kPolyThreads<RP>, poly_smem, st>>>(p, done, steps);
         TLB_TRY(check_launch("muon_poly"));
         done += steps;
