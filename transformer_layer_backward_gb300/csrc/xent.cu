@@ -186,11 +186,13 @@ __device__ __forceinline__ void stats_row(const XParams &p, float (&z)[BN / 2], 
 #pragma unroll
     for (int c = 4; c < BN / 2; ++c) m[c & 3] = fmaxf(m[c & 3], z[c]);
     const float mx = fmaxf(fmaxf(m[0], m[1]), fmaxf(m[2], m[3]));
-    // nothing but -inf (columns past the last): exponents against 0 give sums of 0
-    const float ref = (mx == -INFINITY ? 0.f : mx) * kLog2e;
+    // nothing but -inf (columns past the last): exponents against 0 give sums of 0.  The maximum's own
+    // exponent is 0 exactly (a product mx log2(e) that is rounded before the difference leaves up to half
+    // a step of it: the lse of a certain row a step below its largest logit, its loss below 0)
+    const float ref = mx == -INFINITY ? 0.f : mx;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int c = 0; c < BN / 2; ++c) sum[c & 3] += ex2(fmaf(z[c], kLog2e, -ref));
+    for (int c = 0; c < BN / 2; ++c) sum[c & 3] += ex2((z[c] - ref) * kLog2e);
     if (row < p.M) p.part[int64_t(slot) * p.ld_part + row] = make_float2(mx, (sum[0] + sum[1]) + (sum[2] + sum[3]));
 }
 
@@ -911,10 +913,12 @@ __global__ void __launch_bounds__(256) xent_join_kernel(const float2 *__restrict
     }
     if (y == 0 && row < rows) {
         const float2 r = sh[threadIdx.x];
-        const float l = r.x + logf(r.y);
+        // the sum is 1 at least, and no logit is above r.x: the loss is not below 0, and keeps digits that
+        // the difference lse - z_t has lost
+        const float l = logf(r.y);
         const int64_t t = targets[row];
-        lse[row] = l;
-        loss[row] = (t >= 0 && t < vocab) ? l - zt[row] : 0.f;
+        lse[row] = r.x + l;
+        loss[row] = (t >= 0 && t < vocab) ? (r.x - zt[row]) + l : 0.f;
     }
 }
 
