@@ -331,8 +331,9 @@ int tlb_muon(const tlb_muon_mat *mats, int32_t n, const tlb_muon_cfg *cfg, void 
  * float32 head) run on a kernel that reads the head once, in fp32 throughout (dim up to a few
  * thousand), more on the tcgen05 tensor cores with fp32 sums.  On the tensor cores:
  * bf16 hidden: dz is rounded to bf16 as the operand of the gradient products, for up to 64
- * rows to two bf16 terms (16 bits); beyond, where d_w is NULL, a factor of each row keeps its
- * target's dz free of rounding.  f32 hidden: every float32 operand, dz included, is taken
+ * rows to two bf16 terms (16 bits); beyond, what the target's dz loses is added to both
+ * gradients in fp32, so that only the other columns' dz (the small ones of a row) are rounded.
+ * f32 hidden: every float32 operand, dz included, is taken
  * apart into three bf16 terms that hold all its 24 bits, for results of float32 precision at
  * a third (W bf16) or a sixth (W f32) of the speed.  The target's own logit is summed in fp32.
  * (An infinity in a float32 operand counts as NaN.)

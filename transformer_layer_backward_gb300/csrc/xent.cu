@@ -22,8 +22,10 @@
 // terms are written to the workspace, or (a float32 head, up to 512 rows) made from the float32
 // values on their way into shared memory.
 // With bf16 operands dz is rounded to bf16 once (2^-8 at most, relative to each dz; the sums
-// of it are in fp32): its error in d_hidden stays below that of d_hidden's rounding to bf16,
-// since the largest dz of most rows, the target's, is kept whole by a factor of the row.
+// of it are in fp32).  What the target's dz, the largest of most rows, loses there is kept
+// aside in fp32, and the epilogues of both gradients add it back, times the target's row of the
+// head to the row's d_hidden, times the hidden row to the target's row of d_w: so the gradients'
+// error stays near that of their own rounding to bf16.
 //
 // The tensor core cuts its fp32 sum after every MMA of 16 products (measured: a sum of 160
 // MMAs comes out about 1.2e-6 of its size short, one of 6144 3e-5).  Results of float32
@@ -46,6 +48,7 @@
 #include <cuda.h>
 
 #include <algorithm>
+#include <cstdint>
 #include <cstring>
 #include <type_traits>
 
@@ -95,8 +98,14 @@ struct XParams {
     int64_t ld_part;
     const float *zt;                         // logit of each row's target, from xent_target_kernel
     const float *lse, *dloss;                // kGrad
-    const float2 *scale;                     // (factor of a row of dz, its inverse), or null
     // kOut
+    // What dz of the targets has lost, times a row of `more` (rows ld_more apart), is added where more is
+    // not null: to row i of d_hidden rest[i] x row targets[i]; with `first`, to row v of d_w rest[i]
+    // x row i for i = order[first[v]] .. order[first[v + 1] - 1]
+    const float *rest;
+    const __nv_bfloat16 *more;
+    int64_t ld_more;
+    const int *first, *order;
     const float *acc;                        // sum of the earlier pieces [M, N], or null
     float *out32;                            // one of the two is written
     __nv_bfloat16 *out16;
@@ -199,11 +208,11 @@ __device__ __forceinline__ void stats_row(const XParams &p, float (&z)[BN / 2], 
 // kGrad: what dz needs of this thread's row; fetched a tile ahead.
 struct GradRow {
     int64_t t;
-    float lse, g, zt;                                      // g with the row's factor
+    float lse, g, zt;
 };
 __device__ __forceinline__ GradRow grad_row(const XParams &p, int row) {
     GradRow r{-1, 0.f, 0.f, 0.f};
-    if (row < p.M) r = GradRow{p.targets[row], p.lse[row], p.dloss[row] * (p.scale != nullptr ? p.scale[row].x : 1.f), p.zt[row]};
+    if (row < p.M) r = GradRow{p.targets[row], p.lse[row], p.dloss[row], p.zt[row]};
     return r;
 }
 
@@ -264,11 +273,6 @@ __device__ __forceinline__ void grad_box(const XParams &p, const GradRow &r, flo
 // Four columns col.. of one row of a result: the earlier pieces' sum is added, the value
 // stored in the result's type.
 __device__ __forceinline__ void store4(const XParams &p, int row, int col, float (&v)[4]) {
-    if (p.scale != nullptr) {
-        const float f = p.scale[row].y;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) v[i] *= f;
-    }
     const int64_t e = int64_t(row) * p.N + col;
     if (p.vec) {
         float4 y = make_float4(v[0], v[1], v[2], v[3]);
@@ -289,15 +293,158 @@ __device__ __forceinline__ void store4(const XParams &p, int row, int col, float
     }
 }
 
+// kOut: what the targets' dz have lost, for this thread's row of a tile; fetched a tile ahead.
+struct MoreRow {
+    int64_t t;                                             // d_hidden: the row of `more`, or -1
+    float rest;
+    int lo, hi;                                            // d_w: entries of `order`; t and rest are the first's
+};
+// (the lines of columns col .. col + cols of that row are asked for in L2)
+template <bool DW>
+__device__ __forceinline__ MoreRow more_row(const XParams &p, int row, int col, int cols) {
+    MoreRow r{-1, 0.f, 0, 0};
+    if (p.more == nullptr || row >= p.M) return r;
+    if constexpr (DW) {
+        r.lo = p.first[row];
+        r.hi = p.first[row + 1];
+        if (r.lo < r.hi) {
+            r.t = p.order[r.lo];
+            r.rest = p.rest[r.t];
+        }
+    } else {
+        const int64_t t = p.targets[row];
+        if (t >= 0 && t < p.vocab) r.t = t;
+        r.rest = p.rest[row];
+    }
+    if (r.t >= 0)
+        for (int c = col; c < min(col + cols, p.N); c += 64)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.more + r.t * p.ld_more + c));
+    return r;
+}
+// d_hidden: rest x columns col .. col + 31 of the target's row onto the thread's row.  Rows of
+// whole 16 bytes are fetched (w) before the tensor memory is read.
+struct Quads {
+    uint4 w[4];
+};
+__device__ __forceinline__ Quads target_quads(const XParams &p, const MoreRow &r, int col) {
+    Quads q;
+    const bool on = r.t >= 0 && p.ld_more % 8 == 0;
+    const __nv_bfloat16 *src = p.more + r.t * p.ld_more + col;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        q.w[k] = on && col + 8 * k < p.N ? *reinterpret_cast<const uint4 *>(src + 8 * k) : make_uint4(0, 0, 0, 0);
+    return q;
+}
+__device__ __forceinline__ void add_target(const XParams &p, const MoreRow &r, const Quads &q, float *y, int col) {
+    if (r.t < 0) return;
+    if (p.ld_more % 8 == 0) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t u[4] = {q.w[k].x, q.w[k].y, q.w[k].z, q.w[k].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                y[8 * k + 2 * i] = fmaf(r.rest, bf16_lo(u[i]), y[8 * k + 2 * i]);
+                y[8 * k + 2 * i + 1] = fmaf(r.rest, bf16_hi(u[i]), y[8 * k + 2 * i + 1]);
+            }
+        }
+    } else {
+        const __nv_bfloat16 *src = p.more + r.t * p.ld_more + col;
+#pragma unroll
+        for (int k = 0; k < 32; ++k)
+            if (col + k < p.N) y[k] = fmaf(r.rest, __bfloat162float(src[k]), y[k]);
+    }
+}
+// d_w: the entries of each of the warp's 32 rows onto its block blk [32][33] of columns col0 .. col0 + 31.
+// Four groups of eight lanes take every fourth entry (a token that many rows have as target has many).
+__device__ __forceinline__ void add_entries(const XParams &p, const MoreRow &m, float *blk, int col0, int lane) {
+    const int c4 = (lane & 7) * 4, rl = lane >> 3;
+    uint32_t rows = __ballot_sync(0xffffffffu, m.hi > m.lo);
+    if (rows == 0) return;
+    for (; rows != 0; rows &= rows - 1) {
+        const int r = __ffs(rows) - 1;
+        const int lo = __shfl_sync(0xffffffffu, m.lo, r), hi = __shfl_sync(0xffffffffu, m.hi, r);
+        const int64_t i0 = __shfl_sync(0xffffffffu, m.t, r);
+        const float f0 = __shfl_sync(0xffffffffu, m.rest, r);
+        float a[4] = {0.f, 0.f, 0.f, 0.f};
+        if (col0 + c4 < p.N) {
+            if (rl == 0) {
+                const uint2 w = *reinterpret_cast<const uint2 *>(p.more + i0 * p.ld_more + col0 + c4);
+                a[0] = f0 * bf16_lo(w.x);
+                a[1] = f0 * bf16_hi(w.x);
+                a[2] = f0 * bf16_lo(w.y);
+                a[3] = f0 * bf16_hi(w.y);
+            }
+#pragma unroll 1
+            for (int e = lo + 1 + rl; e < hi; e += 16) {
+                int i[4];
+                float f[4];
+                uint2 w[4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) i[u] = e + 4 * u < hi ? p.order[e + 4 * u] : -1;
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    f[u] = i[u] >= 0 ? p.rest[i[u]] : 0.f;
+                    w[u] = i[u] >= 0 ? *reinterpret_cast<const uint2 *>(p.more + i[u] * p.ld_more + col0 + c4) : make_uint2(0, 0);
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    a[0] = fmaf(f[u], bf16_lo(w[u].x), a[0]);
+                    a[1] = fmaf(f[u], bf16_hi(w[u].x), a[1]);
+                    a[2] = fmaf(f[u], bf16_lo(w[u].y), a[2]);
+                    a[3] = fmaf(f[u], bf16_hi(w[u].y), a[3]);
+                }
+            }
+        }
+        if (hi - lo > 1) {
+#pragma unroll
+            for (int o = 8; o <= 16; o *= 2)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) a[k] += __shfl_xor_sync(0xffffffffu, a[k], o);
+        }
+        if (rl == 0) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) blk[r * 33 + c4 + k] += a[k];
+        }
+    }
+    __syncwarp();
+}
+
+// Both, for four columns col.. of one row (col % 4 == 0).
+__device__ __forceinline__ void add_rest4(const XParams &p, int row, int col, float (&v)[4]) {
+    auto onto = [&](int64_t i, float f) {
+        const __nv_bfloat16 *src = p.more + i * p.ld_more + col;
+        if (p.ld_more % 4 == 0) {
+            const uint2 w = *reinterpret_cast<const uint2 *>(src);
+            v[0] = fmaf(f, bf16_lo(w.x), v[0]);
+            v[1] = fmaf(f, bf16_hi(w.x), v[1]);
+            v[2] = fmaf(f, bf16_lo(w.y), v[2]);
+            v[3] = fmaf(f, bf16_hi(w.y), v[3]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (col + k < p.N) v[k] = fmaf(f, __bfloat162float(src[k]), v[k]);
+        }
+    };
+    if (p.first != nullptr) {
+#pragma unroll 4
+        for (int e = p.first[row], hi = p.first[row + 1]; e < hi; ++e) onto(p.order[e], p.rest[p.order[e]]);
+    } else {
+        const int64_t t = p.targets[row];
+        if (t >= 0 && t < p.vocab) onto(t, p.rest[row]);
+    }
+}
+
 // kOut: columns col0 .. col0 + 31 of a warp's 32 rows row0.. (one row a thread), turned in
 // shared memory so that lanes run along the columns (8 column quads x 4 rows an access):
 // into the result, or into a partial tile (rows of `ld` floats) where there is one.
-__device__ __forceinline__ void out_block(const XParams &p, const float *z, int row0, int col0, float *partial, int ld,
-                                          float *blk, int lane) {
+template <bool ENTRIES>
+__device__ __forceinline__ void out_block(const XParams &p, const float *z, const MoreRow &m, int row0, int col0,
+                                          float *partial, int ld, float *blk, int lane) {
     if (row0 >= p.M || col0 >= p.N) return;
 #pragma unroll
     for (int t = 0; t < 32; ++t) blk[lane * 33 + t] = z[t];
     __syncwarp();
+    if constexpr (ENTRIES) add_entries(p, m, blk, col0, lane);
     const int c4 = (lane & 7) * 4, rl = lane >> 3;
 #pragma unroll 4
     for (int k = 0; k < 8; ++k) {
@@ -689,26 +836,33 @@ __global__ void __launch_bounds__(CONV ? kConvThreads : kThreads, 1) xent_gemm_k
         bool more = next_seg(0, at, next);
         int m0 = 0, n0 = 0, tn = 0;
         GradRow grn{-1, 0.f, 0.f, 0.f};
-        if (more) {
+        MoreRow mrn{-1, 0.f, 0, 0};
+        auto enter = [&] {
             place(next.tile, m0, n0, tn);
             if constexpr (MODE == kGrad) grn = grad_row(p, m0 + q * 32 + lane);
-        }
+            // (to a split tile the kernel that joins its parts adds it: with many rows at once, where a
+            // part's epilogue, the last of its CTA, would wait for every row's loads)
+            if constexpr (MODE == kOut && !FINE) mrn = next.kb0 == 0 && next.kb1 == KB ? more_row<A_MN>(p, m0 + q * 32 + lane, n0 + half * (BN / 2), BN / 2) : MoreRow{-1, 0.f, 0, 0};
+        };
+        if (more) enter();
         for (int i = 0; ok && more; ++i) {
             sg = next;
             const int row0 = m0 + q * 32, colh = n0 + half * (BN / 2), tile_n = tn;
             const GradRow gr = grn;
+            const MoreRow mr = mrn;
             more = next_seg(i + 1, at, next);
-            if (more) {
-                place(next.tile, m0, n0, tn);
-                if constexpr (MODE == kGrad) grn = grad_row(p, m0 + q * 32 + lane);
-            }
+            if (more) enter();
             float *part = nullptr;                            // kOut: this warp's part of a partial tile
             if (MODE == kOut && (sg.kb0 != 0 || sg.kb1 != KB))
                 part = p.partial + ((int64_t(blockIdx.x) * 2 + sg.slot) * kBM + q * 32) * BN + half * (BN / 2);
             float z[ZN];                                      // this thread's row
+            Quads quads;
             auto block = [&](float *y, int c0) {              // WN columns from colh + c0
                 if constexpr (MODE == kGrad) grad_box<TERMS>(p, gr, y, row0, colh + c0, box, lane);
-                if constexpr (MODE == kOut) out_block(p, y, row0, colh + c0, part != nullptr ? part + c0 : nullptr, BN, blk, lane);
+                if constexpr (MODE == kOut) {
+                    if constexpr (!FINE && !A_MN) add_target(p, mr, quads, y, colh + c0);
+                    out_block<!FINE && A_MN>(p, y, mr, row0, colh + c0, part != nullptr ? part + c0 : nullptr, BN, blk, lane);
+                }
             };
             for (int k0 = sg.kb0; k0 < sg.kb1; k0 += chunk, ++f) {
                 const int b = f & 1;
@@ -734,6 +888,7 @@ __global__ void __launch_bounds__(CONV ? kConvThreads : kThreads, 1) xent_gemm_k
 #pragma unroll 1
                     for (int c0 = 0; c0 < BN / 2; c0 += WN) {
                         uint32_t v[WN / 32][32];
+                        if constexpr (MODE == kOut && !A_MN) quads = target_quads(p, mr, colh + c0);
 #pragma unroll
                         for (int j = 0; j < WN / 32; ++j) tmem_ld32(tm + uint32_t(c0 + j * 32), v[j]);
                         tmem_wait_ld();
@@ -820,27 +975,99 @@ __global__ void __launch_bounds__(256) xent_fixup_kernel(const __grid_constant__
                 }
         }
         float v[4] = {acc.x, acc.y, acc.z, acc.w};
+        if (p.more != nullptr) add_rest4(p, row, col, v);
         store4(p, row, col, v);
     }
 }
 
-// zt[i] = <hidden[i], W[t_i]> in fp32: a warp a row.  scale (dz of one bf16 term): the factor, near
-// 1, that makes the target's dz, the largest of most rows, a bf16 number, and its inverse, which
-// goes onto the row's products: so its rounding drops out of the row's gradient.
+// The rows of every target, in ascending order, for the epilogue of d_w: order[first[v]] ..
+// order[first[v + 1] - 1] are those with target v.  A warp 32 columns of the vocabulary (a block
+// all warps): it goes through all targets twice, to count and to place, so that no order depends
+// on timing.  (V / 32 x N / 128 steps twice, against the products' 6 V N D flops.)  The targets come
+// through shared memory kList at a time, and a step looks at four a lane: 4096 targets of 65536
+// columns 13 us beside the rows' products (11 without lists; one a lane a step 21).
+constexpr int kList = 4096;
+__device__ __forceinline__ void list_targets(const int64_t *targets, int64_t rows, int64_t vocab, int64_t v0, int *sh, int *first,
+                                             int *order) {
+    const int lane = threadIdx.x & 31;
+    int at = 0, mine = 0, less = 0;
+    bool any = false;
+#pragma unroll 1
+    for (int pass = 0; pass < 2; ++pass) {
+#pragma unroll 1
+        for (int64_t i0 = 0; i0 < rows; i0 += kList) {
+            const int n = int(min(int64_t(kList), rows - i0));
+            if (pass == 0 || rows > kList) {                 // else they are still there
+                __syncthreads();
+#pragma unroll 8
+                for (int i = threadIdx.x; i < (n + 127) / 128 * 128; i += 256) {
+                    const int64_t t = i < n ? targets[i0 + i] : -1;
+                    sh[i] = t >= 0 && t < vocab ? int(t) : INT32_MAX;
+                }
+                __syncthreads();
+            }
+            // a lane four neighbours; most steps have none of this warp's targets
+            if (pass == 0 || any)
+#pragma unroll 2
+                for (int i = 4 * lane; i - 4 * lane < n; i += 128) {
+                    const int4 q = *reinterpret_cast<const int4 *>(sh + i);
+                    const int d[4] = {q.x - int(v0), q.y - int(v0), q.z - int(v0), q.w - int(v0)};
+                    bool hit = false;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        less += d[k] < 0;
+                        hit |= uint32_t(d[k]) < 32u;
+                    }
+                    for (uint32_t here = __ballot_sync(0xffffffffu, hit); here != 0; here &= here - 1) {
+                        const int s = __ffs(here) - 1;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if (__shfl_sync(0xffffffffu, d[k], s) != lane) continue;
+                            if (pass == 0) ++mine;
+                            else order[at++] = int(i0) + i + 4 * (s - lane) + k;
+                        }
+                    }
+                }
+        }
+        if (pass == 0) {
+            int sum = mine;                                  // of this lane's and the lower lanes' columns
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const int x = __shfl_up_sync(0xffffffffu, sum, o);
+                if (lane >= o) sum += x;
+            }
+#pragma unroll
+            for (int o = 16; o > 0; o /= 2) less += __shfl_xor_sync(0xffffffffu, less, o);
+            at = less + sum - mine;
+            if (v0 + lane < vocab) first[v0 + lane] = at;
+            if (v0 + lane == vocab - 1) first[vocab] = at + mine;
+            any = __any_sync(0xffffffffu, mine > 0);
+        }
+    }
+}
+
+// zt[i] = <hidden[i], W[t_i]> in fp32: a warp a row.  rest (dz of one bf16 term): what the target's
+// dz loses when it is rounded.  first, order: the blocks past the rows' list the targets.
 template <typename HT, typename WT>
 __global__ void __launch_bounds__(256) xent_target_kernel(const HT *__restrict__ hidden, const WT *__restrict__ W,
                                                           const int64_t *__restrict__ targets, int64_t rows, int64_t vocab,
                                                           int64_t dim, float *__restrict__ zt, const float *__restrict__ lse,
-                                                          const float *__restrict__ dloss, float2 *__restrict__ scale) {
+                                                          const float *__restrict__ dloss, float *__restrict__ rest,
+                                                          int *__restrict__ first, int *__restrict__ order) {
     pdl_trigger();
-    const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+    const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5), row_warps = (rows + 7) / 8 * 8;
     const int lane = threadIdx.x & 31;
+    if (row >= row_warps) {                                  // whole blocks
+        __shared__ __align__(16) int sh[kList];
+        list_targets(targets, rows, vocab, (row - row_warps) * 32, sh, first, order);
+        return;
+    }
     if (row >= rows) return;
     const int64_t t = targets[row];
     if (t < 0 || t >= vocab) {
         if (lane == 0) {
             zt[row] = 0.f;
-            if (scale != nullptr) scale[row] = make_float2(1.f, 1.f);
+            if (rest != nullptr) rest[row] = 0.f;
         }
         return;
     }
@@ -867,10 +1094,9 @@ __global__ void __launch_bounds__(256) xent_target_kernel(const HT *__restrict__
     const float v = warp_sum((s[0] + s[1]) + (s[2] + s[3]));
     if (lane == 0) {
         zt[row] = v;
-        if (scale != nullptr) {
-            const float dz = exp_minus_1(v - lse[row]) * dloss[row], r = __bfloat162float(__float2bfloat16(dz));
-            const float f = r / dz, inv = dz / r;
-            scale[row] = isfinite(f) && isfinite(inv) && f > 0.f ? make_float2(f, inv) : make_float2(1.f, 1.f);
+        if (rest != nullptr) {
+            const float dz = exp_minus_1(v - lse[row]) * dloss[row], lost = dz - __bfloat162float(__float2bfloat16(dz));
+            rest[row] = isfinite(lost) ? lost : 0.f;
         }
     }
 }
@@ -1116,7 +1342,8 @@ struct Plan {
     int64_t dp;                  // packed row length
     int64_t piece;               // vocabulary rows of one piece (multiple of 256)
     int64_t part_ld, slots;
-    size_t h, w, dz, part, zt, scale, acc, partial, total;
+    size_t h, w, dz, part, zt, rest, first, order, acc, partial, total;
+    bool keep_rest, list;        // the targets' dz: what its rounding loses, and the rows of each target (d_w)
 };
 
 Plan plan_of(int htype, int wtype, int64_t N, int64_t V, int64_t D, bool grad, bool grad_w) {
@@ -1138,7 +1365,9 @@ Plan plan_of(int htype, int wtype, int64_t N, int64_t V, int64_t D, bool grad, b
     q.h = q.pack_h ? w.take(size_t(q.h_terms) * N * q.dp * 2) : 0;
     q.w = q.pack_w ? w.take(size_t(q.w_terms) * q.piece * q.dp * 2) : 0;
     q.part_ld = q.slots = 0;
-    q.part = q.zt = q.scale = q.dz = q.acc = q.partial = 0;
+    q.part = q.zt = q.rest = q.first = q.order = q.dz = q.acc = q.partial = 0;
+    q.keep_rest = grad && q.z_terms == 1;
+    q.list = q.keep_rest && grad_w;
     if (!grad) {
         q.part_ld = ceil_div(std::min(N, kRowChunk), 32) * 32;
         // 128-wide tiles: the most slots; four an SM for up to four rows
@@ -1148,7 +1377,11 @@ Plan plan_of(int htype, int wtype, int64_t N, int64_t V, int64_t D, bool grad, b
     } else {
         q.dz = w.take(size_t(q.z_terms) * N * q.piece * 2);
         q.zt = w.take(size_t(N) * 4);
-        q.scale = w.take(size_t(N) * 8);
+        if (q.keep_rest) q.rest = w.take(size_t(N) * 4);
+        if (q.list) {
+            q.first = w.take(size_t(V + 1) * 4);
+            q.order = w.take(size_t(N) * 4);
+        }
         if (htype != TLB_W_F32 && q.piece < V) q.acc = w.take(size_t(N) * D * 4);
         q.partial = w.take(size_t(num_sms() + 1) * 2 * kBM * 256 * 4);
     }
@@ -1222,16 +1455,20 @@ bool by_tokens(const Plan &q, int64_t rows, int64_t dim, bool grad) {
 }
 
 int target_logits(int htype, const void *hidden, int wtype, const void *W, const int64_t *targets, int64_t rows, int64_t vocab,
-                  int64_t dim, float *zt, const float *lse, const float *dloss, float2 *scale, cudaStream_t st) {
-    const unsigned grid = unsigned(ceil_div(rows, 8));
+                  int64_t dim, float *zt, const float *lse, const float *dloss, float *rest, int *first, int *order,
+                  cudaStream_t st) {
+    const unsigned grid = unsigned(ceil_div(rows, 8) + (first != nullptr ? ceil_div(vocab, 256) : 0));
     const float *hf = static_cast<const float *>(hidden);
     const __nv_bfloat16 *hb = static_cast<const __nv_bfloat16 *>(hidden), *wb = static_cast<const __nv_bfloat16 *>(W);
     if (wtype == TLB_W_F32)
-        xent_target_kernel<<<grid, 256, 0, st>>>(hf, static_cast<const float *>(W), targets, rows, vocab, dim, zt, lse, dloss, scale);
+        xent_target_kernel<<<grid, 256, 0, st>>>(hf, static_cast<const float *>(W), targets, rows, vocab, dim, zt, lse, dloss, rest,
+                                                  first, order);
     else if (htype == TLB_W_F32)
-        xent_target_kernel<<<grid, 256, 0, st>>>(hf, wb, targets, rows, vocab, dim, zt, lse, dloss, scale);
+        xent_target_kernel<<<grid, 256, 0, st>>>(hf, wb, targets, rows, vocab, dim, zt, lse, dloss, rest,
+                                                  first, order);
     else
-        xent_target_kernel<<<grid, 256, 0, st>>>(hb, wb, targets, rows, vocab, dim, zt, lse, dloss, scale);
+        xent_target_kernel<<<grid, 256, 0, st>>>(hb, wb, targets, rows, vocab, dim, zt, lse, dloss, rest,
+                                                  first, order);
     return check_launch("xent_target");
 }
 
@@ -1301,7 +1538,7 @@ int tlb_xent_forward(int32_t htype, const void *hidden, int32_t wtype, const voi
             TLB_TRY(head_operand(q, wtype, W, v0, nv, dim, ws, st, w));
             if (v0 == 0)
                 TLB_TRY(target_logits(htype, row_of(hidden, htype, r0, dim), wtype, W, targets + r0, n, vocab, dim,
-                                      ws_at<float>(ws, q.zt) + r0, nullptr, nullptr, nullptr, st));
+                                      ws_at<float>(ws, q.zt) + r0, nullptr, nullptr, nullptr, nullptr, nullptr, st));
             XParams p;
             memset(&p, 0, sizeof(p));
             p.M = int(n);
@@ -1348,15 +1585,15 @@ int tlb_xent_backward(int32_t htype, const void *hidden, int32_t wtype, const vo
     Mat h;
     TLB_TRY(hidden_operand(q, htype, hidden, rows, dim, d_w != nullptr ? targets : nullptr, vocab, ws, st, h));
     const bool wide = htype == TLB_W_F32;
-    // factors of dz's rows would stay in d_w's sums over the rows
-    float2 *scale = q.z_terms == 1 && d_w == nullptr ? ws_at<float2>(ws, q.scale) : nullptr;
+    float *rest = q.keep_rest ? ws_at<float>(ws, q.rest) : nullptr;
+    int *first = q.list ? ws_at<int>(ws, q.first) : nullptr, *order = q.list ? ws_at<int>(ws, q.order) : nullptr;
     for (int64_t v0 = 0; v0 < vocab; v0 += q.piece) {
         const int64_t nv = std::min(q.piece, vocab - v0);
         Mat w;
         TLB_TRY(head_operand(q, wtype, W, v0, nv, dim, ws, st, w));
         if (v0 == 0)
-            TLB_TRY(target_logits(htype, hidden, wtype, W, targets, rows, vocab, dim, ws_at<float>(ws, q.zt), lse, d_loss, scale,
-                                  st));
+            TLB_TRY(target_logits(htype, hidden, wtype, W, targets, rows, vocab, dim, ws_at<float>(ws, q.zt), lse, d_loss, rest,
+                                  first, order, st));
         const Mat dz{ws_at<__nv_bfloat16>(ws, q.dz), rows, nv, q.piece, rows * q.piece, q.z_terms};
         {
             XParams p;
@@ -1369,7 +1606,6 @@ int tlb_xent_backward(int32_t htype, const void *hidden, int32_t wtype, const vo
             p.lse = lse;
             p.dloss = d_loss;
             p.zt = ws_at<float>(ws, q.zt);
-            p.scale = scale;
             for (int t = 0; t < q.z_terms; ++t)
                 TLB_TRY(make_map(&p.d[t], dz.p + t * dz.plane, rows, nv, dz.ld, 32));
             p.status = ws_at<uint32_t>(ws, 0);
@@ -1385,7 +1621,13 @@ int tlb_xent_backward(int32_t htype, const void *hidden, int32_t wtype, const vo
             float *sum = wide ? static_cast<float *>(d_hidden) : ws_at<float>(ws, q.acc);
             const bool last = v0 + nv == vocab;
             p.acc = v0 > 0 ? sum : nullptr;
-            p.scale = scale;
+            if (q.keep_rest && v0 == 0) {                    // once, whatever piece the target is in
+                p.targets = targets;
+                p.vocab = vocab;
+                p.rest = rest;
+                p.more = static_cast<const __nv_bfloat16 *>(W);
+                p.ld_more = dim;
+            }
             if (wide || !last) p.out32 = sum;
             else p.out16 = static_cast<__nv_bfloat16 *>(d_hidden);
             p.vec = dim % 4 == 0 && aligned16(d_hidden);
@@ -1402,6 +1644,13 @@ int tlb_xent_backward(int32_t htype, const void *hidden, int32_t wtype, const vo
             if (wide) p.out32 = reinterpret_cast<float *>(out);
             else p.out16 = reinterpret_cast<__nv_bfloat16 *>(out);
             p.vec = dim % 4 == 0 && aligned16(d_w);
+            if (q.list) {
+                p.rest = rest;
+                p.more = h.p;
+                p.ld_more = h.ld;
+                p.first = first + v0;
+                p.order = order;
+            }
             p.partial = ws_at<float>(ws, q.partial);
             p.status = ws_at<uint32_t>(ws, 0);
             TLB_TRY((wide ? launch_out<true, true>(p, dz, h, st) : launch_out<true, false>(p, dz, h, st)));
