@@ -912,6 +912,10 @@ __global__ void __launch_bounds__(NT, tc_ctas<SOURCE, SINK>()) muon_tc_pass_kern
     // D f32, A and B bf16, 128 x 64; A MN-major for Y
     constexpr uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (uint32_t(64 >> 3) << 17) | (uint32_t(128 >> 4) << 24);
     const int q = warp & 3, half = warp >> 2;               // TMEM lanes (columns of X), half of the rows
+    // After a wait that gives up (ok: of this warp) p stays as it is, and all leave together at the next
+    // barrier; `pending` is then what the last products will still arrive at.
+    bool ok = true;
+    uint64_t *pending = nullptr;
     int done = 0;
     for (int g = g0; g < g1; ++g, ++done) {
         if (lo + 1 < p.nmat && p.mat[lo + 1].block0 <= g) {  // the next matrix
@@ -981,29 +985,28 @@ __global__ void __launch_bounds__(NT, tc_ctas<SOURCE, SINK>()) muon_tc_pass_kern
                     }
                 }
             }
-            mbar_wait(&bar_y, done & 1, p.status, 41u);
-            __syncwarp();                                    // tensor memory is read by whole warps
+            ok = mbar_wait(&bar_y, done & 1, p.status, 41u);
+            ok = __all_sync(0xffffffffu, ok);                // tensor memory is read by whole warps
             tc_fence_after();
             uint32_t v[32];
             tmem_ld32(ty + (uint32_t(q * 32) << 16) + uint32_t(half * 32), v);
             tmem_wait_ld();
             if constexpr (SINK == kParam) {
                 const float decay = a.lr * p.wd, move = a.lr_scale;
+                const int moved = ok ? rows : 0;
 #pragma unroll
                 for (int c = 0; c < 32; ++c) x[c] -= fmaf(move, __uint_as_float(v[c]), __fmul_rn(decay, x[c]));
 #pragma unroll
                 for (int c = 0; c < 32; c += 4) {
                     if (quads) {
-                        if (c < rows) *reinterpret_cast<float4 *>(pp + c) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
+                        if (c < moved) *reinterpret_cast<float4 *>(pp + c) = make_float4(x[c], x[c + 1], x[c + 2], x[c + 3]);
                     } else {
 #pragma unroll
                         for (int d = 0; d < 4; ++d)
-                            if (c + d < rows) pp[(c + d) * step] = x[c + d];
+                            if (c + d < moved) pp[(c + d) * step] = x[c + d];
                     }
                 }
-                tc_fence_before();
-                __syncthreads();                             // the planes and Y are read by all
-            } else {
+            } else {                                         // (workspace only)
 #pragma unroll
                 for (int c = 0; c < 32; ++c) y[(i0 + c) * kTcJ + j] = __uint_as_float(v[c]);
 #pragma unroll
@@ -1012,8 +1015,11 @@ __global__ void __launch_bounds__(NT, tc_ctas<SOURCE, SINK>()) muon_tc_pass_kern
                     put_terms<1, 1>(planes, kXPlane, i0 + c, j, x);
                 }
                 fence_proxy_async();
-                tc_fence_before();
-                __syncthreads();
+            }
+            tc_fence_before();
+            if (__syncthreads_or(!ok)) {                     // (kParam: the planes and Y are read by all)
+                pending = &bar_y;
+                break;
             }
         }
         if constexpr (SINK != kParam) {
@@ -1035,8 +1041,8 @@ __global__ void __launch_bounds__(NT, tc_ctas<SOURCE, SINK>()) muon_tc_pass_kern
             }
             // Every tile's sums go out by themselves: tensor memory cuts a sum after every MMA, and
             // a second tile's 16 onto a whole sum would cost five times the error
-            mbar_wait(&bar_g, done & 1, p.status, 42u);
-            __syncwarp();
+            ok = mbar_wait(&bar_g, done & 1, p.status, 42u);
+            ok = __all_sync(0xffffffffu, ok);
             tc_fence_after();
             float *s1 = reinterpret_cast<float *>(planes), *s2 = s1 + 64 * 65;    // in the planes' place
             if (q < 2) {
@@ -1052,7 +1058,10 @@ __global__ void __launch_bounds__(NT, tc_ctas<SOURCE, SINK>()) muon_tc_pass_kern
                 }
             }
             tc_fence_before();
-            __syncthreads();
+            if (__syncthreads_or(!ok)) {
+                pending = &bar_g;
+                break;
+            }
             float *out = p.ws + a.part + int64_t(t) * T::GSIZE;
             for (int e = tid; e < T::GSIZE; e += NT) {
                 int i, k;
@@ -1062,6 +1071,7 @@ __global__ void __launch_bounds__(NT, tc_ctas<SOURCE, SINK>()) muon_tc_pass_kern
             __syncthreads();                                 // the planes are free again
         }
     }
+    if (pending != nullptr && tid == 0) mbar_wait(pending, done & 1, nullptr, 0u);
     __syncthreads();
     if (warp == 0) {
         tc_fence_after();
