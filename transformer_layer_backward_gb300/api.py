@@ -111,7 +111,7 @@ def linear_backward(wtype, W, dY, scale=1.0, out=None, accumulate=False, ws=None
     if code == A.W_TERNARY_2B:
         out_dim *= 4
     S = dY.shape[0]
-    out = torch.zeros(S, in_dim, device=dY.device) if out is None else out
+    out = torch.zeros(S, in_dim, dtype=torch.float32, device=dY.device) if out is None else out
     ws = linear_workspace(wtype, S, out_dim, in_dim, dY.device) if ws is None else ws
     A.call("tlb_linear_backward", code, _ptr(W, _WDTYPE[code], "W"), float(scale), _ptr(dY, name="dY"),
            S, out_dim, in_dim, _ptr(out, name="out"), 1 if accumulate else 0,
@@ -250,8 +250,8 @@ def xent_forward(hidden, W, targets, loss=None, lse=None, ws=None, stream=None):
     rows, vocab, dim = _xent_shapes(hidden, W, targets, ws, loss=loss, lse=lse)
     ht, wt = _xent_code(hidden.dtype, "hidden"), _xent_code(W.dtype, "W")
     with _queued(hidden, stream):
-        loss = torch.empty(rows, device=hidden.device) if loss is None else loss
-        lse = torch.empty(rows, device=hidden.device) if lse is None else lse
+        loss = torch.empty(rows, dtype=torch.float32, device=hidden.device) if loss is None else loss
+        lse = torch.empty(rows, dtype=torch.float32, device=hidden.device) if lse is None else lse
         ws = xent_workspace(hidden.dtype, W.dtype, rows, vocab, dim, device=hidden.device) if ws is None else ws
         A.call("tlb_xent_forward", ht, _ptr(hidden, None, "hidden"), wt, _ptr(W, None, "W"),
                _ptr(targets, torch.int64, "targets"), rows, vocab, dim, _ptr(loss, name="loss"), _ptr(lse, name="lse"),
