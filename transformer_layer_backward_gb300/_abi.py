@@ -82,6 +82,7 @@ SIGNATURES = {
     "tlb_muon_workspace_bytes": (sz, [P(MuonMat), i32]),
     "tlb_muon": (C.c_int, [P(MuonMat), i32, P(MuonCfg), vp, sz, vp]),
     "tlb_xent_workspace_bytes": (sz, [i32, i32, i64, i64, i64, i32]),
+    "tlb_xent_forward_workspace_bytes": (sz, [i32, i32, i64, i64, i64]),
     "tlb_xent_forward": (C.c_int, [i32, vp, i32, vp, vp, i64, i64, i64, vp, vp, vp, sz, vp]),
     "tlb_xent_backward": (C.c_int, [i32, vp, i32, vp, vp, vp, vp, i64, i64, i64, vp, vp, vp, sz, vp]),
     "tlb_workspace_bytes": (sz, [P(LayerCfg), i64, i64]),

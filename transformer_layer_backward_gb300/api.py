@@ -236,11 +236,12 @@ def _xent_shapes(hidden, W, targets, ws, **per_row):
     return rows, W.shape[0], W.shape[1]
 
 
-def xent_workspace(hidden_dtype, weight_dtype, rows, vocab, dim, grad_w=False, device="cuda"):
+def xent_workspace(hidden_dtype, weight_dtype, rows, vocab, dim, grad_w=False, device="cuda", grad=True):
     """A zeroed workspace tensor for xent_forward and xent_backward (grad_w: with the head's
-    gradient) of these sizes."""
-    n = int(A.load().tlb_xent_workspace_bytes(_xent_code(hidden_dtype, "hidden"), _xent_code(weight_dtype, "W"),
-                                              int(rows), int(vocab), int(dim), 1 if grad_w else 0))
+    gradient) of these sizes; grad=False: for xent_forward alone."""
+    sizes = (_xent_code(hidden_dtype, "hidden"), _xent_code(weight_dtype, "W"), int(rows), int(vocab), int(dim))
+    n = int(A.load().tlb_xent_workspace_bytes(*sizes, 1 if grad_w else 0) if grad or grad_w else
+            A.load().tlb_xent_forward_workspace_bytes(*sizes))
     return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
 
 
@@ -252,7 +253,8 @@ def xent_forward(hidden, W, targets, loss=None, lse=None, ws=None, stream=None):
     with _queued(hidden, stream):
         loss = torch.empty(rows, dtype=torch.float32, device=hidden.device) if loss is None else loss
         lse = torch.empty(rows, dtype=torch.float32, device=hidden.device) if lse is None else lse
-        ws = xent_workspace(hidden.dtype, W.dtype, rows, vocab, dim, device=hidden.device) if ws is None else ws
+        if ws is None:
+            ws = xent_workspace(hidden.dtype, W.dtype, rows, vocab, dim, device=hidden.device, grad=False)
         A.call("tlb_xent_forward", ht, _ptr(hidden, None, "hidden"), wt, _ptr(W, None, "W"),
                _ptr(targets, torch.int64, "targets"), rows, vocab, dim, _ptr(loss, name="loss"), _ptr(lse, name="lse"),
                _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream))

@@ -1501,6 +1501,12 @@ size_t tlb_xent_workspace_bytes(int32_t htype, int32_t wtype, int64_t rows, int6
                     plan_of(htype, wtype, rows, vocab, dim, true, grad_w != 0).total);
 }
 
+size_t tlb_xent_forward_workspace_bytes(int32_t htype, int32_t wtype, int64_t rows, int64_t vocab, int64_t dim) {
+    clear_error();
+    if (check_types("xent_forward_workspace_bytes", htype, wtype, rows, vocab, dim) != TLB_OK) return 0;
+    return plan_of(htype, wtype, rows, vocab, dim, false, false).total;
+}
+
 int tlb_xent_forward(int32_t htype, const void *hidden, int32_t wtype, const void *W, const int64_t *targets, int64_t rows,
                      int64_t vocab, int64_t dim, float *loss, float *lse, void *ws, size_t ws_bytes, void *stream) {
     clear_error();
