@@ -344,7 +344,7 @@ int tlb_muon(const tlb_muon_mat *mats, int32_t n, const tlb_muon_cfg *cfg, void 
  * The backward pass walks through the vocabulary in pieces whose dz stays in the workspace
  * (512 MB at most; at least 2048 columns).  Same inputs, same bits: no sum depends on timing.
  * d_hidden may be hidden itself; no other output may overlap an input or another output.
- * ws: zero-filled once, 256-byte aligned, tlb_xent_workspace_bytes() bytes (enough for both
+ * ws: its first 256 bytes zero-filled once, 256-byte aligned, tlb_xent_workspace_bytes() bytes (enough for both
  * calls; 0 for sizes or types that the calls refuse).  grad_w: whether d_w will be asked for.
  * Where only the loss is wanted (scoring), tlb_xent_forward_workspace_bytes() are enough. */
 size_t tlb_xent_workspace_bytes(int32_t htype, int32_t wtype, int64_t rows, int64_t vocab, int64_t dim, int32_t grad_w);

@@ -21,6 +21,8 @@ _WCODE = {"f32": A.W_F32, "bf16": A.W_BF16, "ternary": A.W_TERNARY_I8, "ternary2
 
 _NO_GUARD = contextlib.nullcontext()
 
+_STATUS_BYTES = 256     # of a workspace, at its start
+
 
 def _queued(t, stream=None):
     """Guard for work on t: its device is the current one, and so is the stream that the work is
@@ -237,33 +239,55 @@ def _xent_shapes(hidden, W, targets, ws, **per_row):
 
 
 def xent_workspace(hidden_dtype, weight_dtype, rows, vocab, dim, grad_w=False, device="cuda", grad=True):
-    """A zeroed workspace tensor for xent_forward and xent_backward (grad_w: with the head's
-    gradient) of these sizes; grad=False: for xent_forward alone."""
+    """A workspace tensor, its status block zeroed, for xent_forward and xent_backward (grad_w:
+    with the head's gradient) of these sizes; grad=False: for xent_forward alone."""
     sizes = (_xent_code(hidden_dtype, "hidden"), _xent_code(weight_dtype, "W"), int(rows), int(vocab), int(dim))
     n = int(A.load().tlb_xent_workspace_bytes(*sizes, 1 if grad_w else 0) if grad or grad_w else
             A.load().tlb_xent_forward_workspace_bytes(*sizes))
-    return torch.zeros(max(n, 256), dtype=torch.uint8, device=device)
+    ws = torch.empty(max(n, _STATUS_BYTES), dtype=torch.uint8, device=device)
+    ws[:_STATUS_BYTES].zero_()
+    return ws
+
+
+# Status words of the workspaces that calls made for themselves, by device and stream.
+_own_status = {}
+
+
+def _keep_status(ws):
+    """Keeps the status words of a workspace that the caller will not see, for workspace_status().
+    (The first call on a stream cannot keep them while it is captured into a graph.)"""
+    words = ws[:_STATUS_BYTES].view(torch.int32)
+    key = ws.device, torch.cuda.current_stream(ws.device).cuda_stream
+    if key in _own_status:
+        torch.maximum(_own_status[key], words, out=_own_status[key])
+    elif not torch.cuda.is_current_stream_capturing():
+        _own_status[key] = words.clone()
 
 
 def xent_forward(hidden, W, targets, loss=None, lse=None, ws=None, stream=None):
     """Per-row cross entropy of the linear head W [vocab, dim] on hidden [rows, dim], without
-    the logits: (loss, lse).  Targets (int64) outside [0, vocab) mark rows without one."""
+    the logits: (loss, lse).  Targets (int64) outside [0, vocab) mark rows without one.
+    Without ws the call makes one of its own, which workspace_status() without one looks after."""
     rows, vocab, dim = _xent_shapes(hidden, W, targets, ws, loss=loss, lse=lse)
     ht, wt = _xent_code(hidden.dtype, "hidden"), _xent_code(W.dtype, "W")
     with _queued(hidden, stream):
         loss = torch.empty(rows, dtype=torch.float32, device=hidden.device) if loss is None else loss
         lse = torch.empty(rows, dtype=torch.float32, device=hidden.device) if lse is None else lse
-        if ws is None:
+        own = ws is None
+        if own:
             ws = xent_workspace(hidden.dtype, W.dtype, rows, vocab, dim, device=hidden.device, grad=False)
         A.call("tlb_xent_forward", ht, _ptr(hidden, None, "hidden"), wt, _ptr(W, None, "W"),
                _ptr(targets, torch.int64, "targets"), rows, vocab, dim, _ptr(loss, name="loss"), _ptr(lse, name="lse"),
                _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream))
+        if own:
+            _keep_status(ws)
     return loss, lse
 
 
 def xent_backward(hidden, W, targets, lse, d_loss, d_hidden=None, d_w=None, grad_w=False, ws=None, stream=None):
     """Gradient of sum(d_loss * loss): (d_hidden, d_w), in hidden's dtype; d_w [vocab, dim] is
-    None unless grad_w is set or a tensor for it is given.  lse as xent_forward returned it."""
+    None unless grad_w is set or a tensor for it is given.  lse as xent_forward returned it; ws
+    as there."""
     rows, vocab, dim = _xent_shapes(hidden, W, targets, ws, lse=lse, d_loss=d_loss)
     ht, wt = _xent_code(hidden.dtype, "hidden"), _xent_code(W.dtype, "W")
     with _queued(hidden, stream):
@@ -273,12 +297,15 @@ def xent_backward(hidden, W, targets, lse, d_loss, d_hidden=None, d_w=None, grad
         for name, t, shape in (("d_hidden", d_hidden, hidden.shape), ("d_w", d_w, W.shape)):
             if t is not None and (t.shape != shape or t.device != hidden.device):
                 raise ValueError("%s must have shape %s on %s" % (name, tuple(shape), hidden.device))
-        if ws is None:
+        own = ws is None
+        if own:
             ws = xent_workspace(hidden.dtype, W.dtype, rows, vocab, dim, d_w is not None, hidden.device)
         A.call("tlb_xent_backward", ht, _ptr(hidden, None, "hidden"), wt, _ptr(W, None, "W"),
                _ptr(targets, torch.int64, "targets"), _ptr(lse, name="lse"), _ptr(d_loss, name="d_loss"), rows, vocab,
                dim, _ptr(d_hidden, hidden.dtype, "d_hidden"), _ptr(d_w, hidden.dtype, "d_w"),
                _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream))
+        if own:
+            _keep_status(ws)
     return d_hidden, d_w
 
 
@@ -336,8 +363,23 @@ def debug_skip_barrier_arrival(block: int):
     A.call("tlb_debug_skip_barrier_arrival", int(block))
 
 
-def workspace_status(ws, stream=None):
-    A.call("tlb_workspace_status", _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream))
+def workspace_status(ws=None, stream=None):
+    """Raises TlbError for an error that a kernel recorded in ws, and clears it (waits for the
+    stream).  Without ws: for errors of calls that made a workspace of their own, on any stream
+    (waits for their devices)."""
+    if ws is not None:
+        A.call("tlb_workspace_status", _ptr(ws, torch.uint8, "ws"), ws.numel(), _stream(stream))
+        return
+    failed = None
+    for (device, _), words in _own_status.items():
+        with torch.cuda.device(device):
+            torch.cuda.synchronize()
+            try:
+                A.call("tlb_workspace_status", _ptr(words, torch.int32, "status"), _STATUS_BYTES, _stream(stream))
+            except A.TlbError as e:
+                failed = failed or e
+    if failed is not None:
+        raise failed
 
 
 def layer_weights(cfg: A.LayerCfg, t: dict):
