@@ -333,16 +333,17 @@ int tlb_muon(const tlb_muon_mat *mats, int32_t n, const tlb_muon_cfg *cfg, void 
  * bf16 hidden: dz is rounded to bf16 as the operand of the gradient products, for up to 64
  * rows to two bf16 terms (16 bits); beyond, what the target's dz loses is added to both
  * gradients in fp32, so that only the other columns' dz (the small ones of a row) are rounded.
- * f32 hidden: every float32 operand, dz included, is taken
- * apart into three bf16 terms that hold all its 24 bits, for results of float32 precision at
- * a third (W bf16) or a sixth (W f32) of the speed.  The target's own logit is summed in fp32.
- * (An infinity in a float32 operand counts as NaN.)
+ * f32 hidden: every float32 operand, dz included, is taken apart into three bf16 terms that
+ * hold all its 24 bits, for results of float32 precision at a third (W bf16) or a sixth (W f32)
+ * of the speed.  The target's own logit is summed in fp32.
+ * (An infinity in a float32 operand counts as NaN; a logit of +infinity makes its row's lse NaN.)
  *
  * rows >= 0 (0 rows: no-op, d_w set to 0), vocab >= 1, dim >= 1, of any size up to 2^24,
  * 2^24 and 2^20.  bf16 operands with dim % 8 != 0, bf16 rows where d_w is asked for, float32
  * rows and, past 512 rows, a float32 head are copied to the workspace (padded, as bf16 terms).
  * The backward pass walks through the vocabulary in pieces whose dz stays in the workspace
- * (512 MB at most; at least 2048 columns).  Same inputs, same bits: no sum depends on timing.
+ * (512 MB at most, or 2048 columns where these are more: past 131072 bf16 rows).  Same
+ * inputs, same bits: no sum depends on timing.
  * d_hidden may be hidden itself; no other output may overlap an input or another output.
  * ws: its first 256 bytes zero-filled once, 256-byte aligned, tlb_xent_workspace_bytes() bytes (enough for both
  * calls; 0 for sizes or types that the calls refuse).  grad_w: whether d_w will be asked for.

@@ -35,8 +35,8 @@
 //     go through reading, r x r products and writing in step, so that HBM idles in the middle:
 //     two reads and two Gram sums of X in shared memory, then two chains of r x r products
 //   seven 5 x 1001 and three 999 x 33 matrices: 62 us in two launches, chains of 14 r x r products
-//   144 rank-64 matrices, 472 MB (69.6 us; 189 MB read by each pass): 341 us, passes of 75, 115 and
-//     92 us and r x r products of 24 and 33 us; the passes wait for loads, for taking floats apart and
+//   144 rank-64 matrices, 472 MB (69.6 us; 189 MB read by each pass): 342 us, passes of 76, 115 and
+//     91 us and r x r products of 24 and 33 us; the passes wait for loads, for taking floats apart and
 //     for their Gram matrices, which leave tile by tile (sums of two tiles in tensor memory: five
 //     times the error, 1e-6 against 2e-7 in p)
 #include <algorithm>

@@ -42,9 +42,10 @@
 //
 // Bounds: N >= 512 rows is bound by the tensor pipe (2 N V D flops a product), few rows by
 // the read of W.  Measured at 2048 x 2560 x 131072 in bf16 (727 us a product at the rate of a large
-// library product, 1.89 PFLOP/s): loss 771 us, dz 780 us, dz W 784 us each alone, 1.78 PFLOP/s;
-// 862 and 1755 us for the calls back to back, where the power limit sets the clock.  4096 x 2560 x
-// 65536 with d_w: 2.70 ms (2.18).  Float32 rows, 512 x 2560 x 32768: 388 us (273: three products).
+// library product, 1.89 PFLOP/s): loss 769 us, dz 793 us, dz W 798 us each alone, 1.72 to 1.79
+// PFLOP/s; 863 and 1766 us for the calls back to back, where the power limit sets the clock.  4096 x
+// 2560 x 65536 with d_w: 2.71 ms (2.18).  Float32 rows, 512 x 2560 x 32768: 391 us (273: three
+// products), at 2048 x 2560 x 131072 2.23 ms the loss (2.18) and 5.30 ms d_hidden (4.36).
 #include <cuda.h>
 
 #include <algorithm>
@@ -68,9 +69,9 @@ constexpr int kConvThreads = kThreads + 32 * kConvWarps;
 constexpr int kEpiWarps = 8;                // two per 32 TMEM lanes (rows), each half of the columns
 constexpr int kMaxTerms = 3, kMaxProd = 6;
 // k blocks (4 MMAs each) of one tensor-memory sum of a float32 result, of z and of a gradient.
-// Reading a sum out takes the tensor pipe about 300 cycles (the loss of 2048 x 2560 x 131072: 812 us
-// at 8 k blocks, 787 at 20; 512 float32 rows' gradient 400 us with z in tens, 388), and its error
-// grows with its length.
+// Reading a sum out takes the tensor pipe about 300 cycles (the loss of 2048 x 2560 x 131072, before its
+// rows' targets were fetched a tile ahead: 812 us at 8 k blocks, 787 at 20, and 769 since; 512 float32
+// rows' gradient 400 us with z in tens, 388), and its error grows with its length.
 constexpr int kChunkLoss = 20, kChunkGrad = 10;
 constexpr int kConvLoss = 3, kConvGrad = 2;  // of six term products each
 constexpr int kGroupM = 16;                 // row tiles that share a column tile before the next one
@@ -1332,7 +1333,8 @@ constexpr int64_t kFewRows = 64;                      // bf16 rows up to which d
 // instead of being written as three terms (2.5 times its bytes) before.  Loss, gradient in us:
 //   32768 x 2560    128 rows: 115, 248 against 269, 395   333: 300, 656 against 489, 852   512: 356, 827 against 496, 871
 //   50021 x 1001    128 rows:  89, 192 against 207, 297   333: 189, 439 against 309, 564   512: 255, 586 against 315, 578
-// (2048 rows, before the last steps: 1403, 3311 against 1338, 2815: the larger tiles of the other form pay.)
+//   32768 x 2560    600 rows: 446, 1004 against 667, 1180   1024: 690, 1545 against 750, 1426   2048: 1308, 3071 against 1345, 2666
+// (the larger tiles of the other form pay for the gradient from about 1000 rows on, for the loss not yet at 2048).
 constexpr int64_t kConvMost = 512;
 constexpr int64_t kRowChunk = 16384;                  // rows of one pass of the loss (its pairs' buffer)
 
