@@ -5,8 +5,8 @@ results, with relative errors of one size u (root mean square) each.  With logit
 p is about 1 / vocab, and a row's dz has a target's of size g beside vocab others that are
 sqrt(vocab) (g / vocab) together.  Where only these are rounded, the squared error of either
 gradient is u^2 (1 + 1 / vocab) of its squared size: at vocab >= 1000 it is that of the
-result's own rounding but for 5e-4 (and a spread of p of exp(0.3^2)).  The fp32 sums add 1e-5,
-5e-5 of u's square.  So 1.02 times the rounding alone; with the targets' dz rounded
+result's own rounding but for 5e-4 (and a spread of p of exp(0.3^2); at 300 for 2e-3).  The
+fp32 sums add 1e-5, 5e-5 of u's square.  So 1.02 times the rounding alone; with the targets' dz rounded
 too it is sqrt(2).
 """
 import numpy as np
@@ -26,6 +26,7 @@ def inputs(rows, vocab, dim, hot=0.0, seed=0):
     t[torch.rand(rows, generator=gen, device="cuda") < 0.1] = -1
     t[torch.rand(rows, generator=gen, device="cuda") < hot] = vocab // 2      # many rows with one target
     t[0], t[1], t[rows - 1] = 0, vocab - 1, vocab
+    t[2], t[3] = 2 ** 40 + 5, -2 ** 32 + 5                   # no column, whatever their low bits say
     g = torch.rand(rows, generator=gen, device="cuda") + 0.5
     return h, w, t, g
 
@@ -45,7 +46,8 @@ def error(x, ref):
 
 
 SHAPES = [(65, 1000, 64, 0.0), (100, 1003, 136, 0.0), (128, 3000, 72, 0.5), (129, 3000, 130, 0.0), (300, 3001, 1001, 0.3),
-          (777, 5000, 1000, 0.0), (1000, 20011, 328, 0.05), (300, 40000, 33, 0.0)]
+          (777, 5000, 1000, 0.0), (1000, 20011, 328, 0.05), (300, 40000, 33, 0.0), (5000, 1000, 64, 0.0), (4100, 300, 520, 0.3),
+          (20000, 2048, 40, 0.0), (2500, 9001, 264, 0.9)]
 
 
 @pytest.mark.parametrize("rows,vocab,dim,hot", SHAPES)

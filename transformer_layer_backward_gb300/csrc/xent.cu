@@ -24,8 +24,8 @@
 // With bf16 operands dz is rounded to bf16 once (2^-8 at most, relative to each dz; the sums
 // of it are in fp32).  What the target's dz, the largest of most rows, loses there is kept
 // aside in fp32, and the epilogues of both gradients add it back, times the target's row of the
-// head to the row's d_hidden, times the hidden row to the target's row of d_w: so the gradients'
-// error stays near that of their own rounding to bf16.
+// head to the row's d_hidden, times the hidden row to the target's row of d_w (summed before over the
+// rows with that target): so the gradients' error stays near that of their own rounding to bf16.
 //
 // The tensor core cuts its fp32 sum after every MMA of 16 products (measured: a sum of 160
 // MMAs comes out about 1.2e-6 of its size short, one of 6144 3e-5).  Results of float32
@@ -100,13 +100,14 @@ struct XParams {
     const float *zt;                         // logit of each row's target, from xent_target_kernel
     const float *lse, *dloss;                // kGrad
     // kOut
-    // What dz of the targets has lost, times a row of `more` (rows ld_more apart), is added where more is
-    // not null: to row i of d_hidden rest[i] x row targets[i]; with `first`, to row v of d_w rest[i]
-    // x row i for i = order[first[v]] .. order[first[v + 1] - 1]
+    // What dz of the targets has lost.  d_hidden (more): rest[i] x row targets[i] of the head (rows ld_more
+    // apart) is added to row i.  d_w (sums): row first[v] of sums, the sum of rest[i] x hidden row i over
+    // the rows with target v, to row v where first[v + 1] > first[v]
     const float *rest;
     const __nv_bfloat16 *more;
-    int64_t ld_more;
-    const int *first, *order;
+    int64_t ld_more;                         // of sums too
+    const float *sums;
+    const int *first;
     const float *acc;                        // sum of the earlier pieces [M, N], or null
     float *out32;                            // one of the two is written
     __nv_bfloat16 *out16;
@@ -294,51 +295,64 @@ __device__ __forceinline__ void store4(const XParams &p, int row, int col, float
     }
 }
 
-// kOut: what the targets' dz have lost, for this thread's row of a tile; fetched a tile ahead.
+// kOut: what the targets' dz have lost, in d_hidden (kTargets) and d_w (kSums).
+enum More { kNone = 0, kTargets = 1, kSums = 2 };
+// ... for this thread's row of a tile; fetched a tile ahead.
 struct MoreRow {
-    int64_t t;                                             // d_hidden: the row of `more`, or -1
+    int64_t row;                                           // of `more` or `sums`, or -1
     float rest;
-    int lo, hi;                                            // d_w: entries of `order`; t and rest are the first's
 };
 // (the lines of columns col .. col + cols of that row are asked for in L2)
-template <bool DW>
+template <int MORE>
 __device__ __forceinline__ MoreRow more_row(const XParams &p, int row, int col, int cols) {
-    MoreRow r{-1, 0.f, 0, 0};
-    if (p.more == nullptr || row >= p.M) return r;
-    if constexpr (DW) {
-        r.lo = p.first[row];
-        r.hi = p.first[row + 1];
-        if (r.lo < r.hi) {
-            r.t = p.order[r.lo];
-            r.rest = p.rest[r.t];
-        }
+    MoreRow r{-1, 0.f};
+    if (row >= p.M) return r;
+    if constexpr (MORE == kSums) {
+        const int at = p.first[row];
+        if (at < p.first[row + 1]) r.row = at;
     } else {
         const int64_t t = p.targets[row];
-        if (t >= 0 && t < p.vocab) r.t = t;
+        if (t >= 0 && t < p.vocab) r.row = t;
         r.rest = p.rest[row];
     }
-    if (r.t >= 0)
-        for (int c = col; c < min(col + cols, p.N); c += 64)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(p.more + r.t * p.ld_more + c));
+    if (r.row >= 0) {
+        constexpr int kLine = MORE == kSums ? 32 : 64;
+        const int64_t e = r.row * p.ld_more;
+        for (int c = col; c < min(col + cols, p.N); c += kLine) {
+            if constexpr (MORE == kSums) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.sums + e + c));
+            else asm volatile("prefetch.global.L2 [%0];" ::"l"(p.more + e + c));
+        }
+    }
     return r;
 }
-// d_hidden: rest x columns col .. col + 31 of the target's row onto the thread's row.  Rows of
-// whole 16 bytes are fetched (w) before the tensor memory is read.
-struct Quads {
-    uint4 w[4];
+// Columns col .. col + 31 of that row, fetched before the tensor memory is read (d_hidden: where the
+// head's rows are whole 16 bytes), and added to the thread's row.
+template <int MORE> struct MoreCols {
+    uint4 w[MORE == kSums ? 8 : MORE == kTargets ? 4 : 1];
 };
-__device__ __forceinline__ Quads target_quads(const XParams &p, const MoreRow &r, int col) {
-    Quads q;
-    const bool on = r.t >= 0 && p.ld_more % 8 == 0;
-    const __nv_bfloat16 *src = p.more + r.t * p.ld_more + col;
+template <int MORE>
+__device__ __forceinline__ void fetch_more(const XParams &p, const MoreRow &r, MoreCols<MORE> &q, int col) {
+    constexpr int C = MORE == kSums ? 4 : 8;
+    const bool on = r.row >= 0 && (MORE == kSums || p.ld_more % 8 == 0);
+    const int64_t e = r.row * p.ld_more + col;
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-        q.w[k] = on && col + 8 * k < p.N ? *reinterpret_cast<const uint4 *>(src + 8 * k) : make_uint4(0, 0, 0, 0);
-    return q;
+    for (int k = 0; k < 32 / C; ++k) {
+        const void *src = MORE == kSums ? static_cast<const void *>(p.sums + e + C * k) : p.more + e + C * k;
+        q.w[k] = on && col + C * k < p.N ? *static_cast<const uint4 *>(src) : make_uint4(0, 0, 0, 0);
+    }
 }
-__device__ __forceinline__ void add_target(const XParams &p, const MoreRow &r, const Quads &q, float *y, int col) {
-    if (r.t < 0) return;
-    if (p.ld_more % 8 == 0) {
+template <int MORE>
+__device__ __forceinline__ void add_more(const XParams &p, const MoreRow &r, const MoreCols<MORE> &q, float *y, int col) {
+    if (r.row < 0) return;
+    if constexpr (MORE == kSums) {
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            y[4 * k] += __uint_as_float(q.w[k].x);
+            y[4 * k + 1] += __uint_as_float(q.w[k].y);
+            y[4 * k + 2] += __uint_as_float(q.w[k].z);
+            y[4 * k + 3] += __uint_as_float(q.w[k].w);
+        }
+    } else if (p.ld_more % 8 == 0) {
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
             const uint32_t u[4] = {q.w[k].x, q.w[k].y, q.w[k].z, q.w[k].w};
@@ -349,71 +363,25 @@ __device__ __forceinline__ void add_target(const XParams &p, const MoreRow &r, c
             }
         }
     } else {
-        const __nv_bfloat16 *src = p.more + r.t * p.ld_more + col;
+        const __nv_bfloat16 *src = p.more + r.row * p.ld_more + col;
 #pragma unroll
         for (int k = 0; k < 32; ++k)
             if (col + k < p.N) y[k] = fmaf(r.rest, __bfloat162float(src[k]), y[k]);
     }
 }
-// d_w: the entries of each of the warp's 32 rows onto its block blk [32][33] of columns col0 .. col0 + 31.
-// Four groups of eight lanes take every fourth entry (a token that many rows have as target has many).
-__device__ __forceinline__ void add_entries(const XParams &p, const MoreRow &m, float *blk, int col0, int lane) {
-    const int c4 = (lane & 7) * 4, rl = lane >> 3;
-    uint32_t rows = __ballot_sync(0xffffffffu, m.hi > m.lo);
-    if (rows == 0) return;
-    for (; rows != 0; rows &= rows - 1) {
-        const int r = __ffs(rows) - 1;
-        const int lo = __shfl_sync(0xffffffffu, m.lo, r), hi = __shfl_sync(0xffffffffu, m.hi, r);
-        const int64_t i0 = __shfl_sync(0xffffffffu, m.t, r);
-        const float f0 = __shfl_sync(0xffffffffu, m.rest, r);
-        float a[4] = {0.f, 0.f, 0.f, 0.f};
-        if (col0 + c4 < p.N) {
-            if (rl == 0) {
-                const uint2 w = *reinterpret_cast<const uint2 *>(p.more + i0 * p.ld_more + col0 + c4);
-                a[0] = f0 * bf16_lo(w.x);
-                a[1] = f0 * bf16_hi(w.x);
-                a[2] = f0 * bf16_lo(w.y);
-                a[3] = f0 * bf16_hi(w.y);
-            }
-#pragma unroll 1
-            for (int e = lo + 1 + rl; e < hi; e += 16) {
-                int i[4];
-                float f[4];
-                uint2 w[4];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) i[u] = e + 4 * u < hi ? p.order[e + 4 * u] : -1;
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    f[u] = i[u] >= 0 ? p.rest[i[u]] : 0.f;
-                    w[u] = i[u] >= 0 ? *reinterpret_cast<const uint2 *>(p.more + i[u] * p.ld_more + col0 + c4) : make_uint2(0, 0);
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    a[0] = fmaf(f[u], bf16_lo(w[u].x), a[0]);
-                    a[1] = fmaf(f[u], bf16_hi(w[u].x), a[1]);
-                    a[2] = fmaf(f[u], bf16_lo(w[u].y), a[2]);
-                    a[3] = fmaf(f[u], bf16_hi(w[u].y), a[3]);
-                }
-            }
-        }
-        if (hi - lo > 1) {
-#pragma unroll
-            for (int o = 8; o <= 16; o *= 2)
-#pragma unroll
-                for (int k = 0; k < 4; ++k) a[k] += __shfl_xor_sync(0xffffffffu, a[k], o);
-        }
-        if (rl == 0) {
-#pragma unroll
-            for (int k = 0; k < 4; ++k) blk[r * 33 + c4 + k] += a[k];
-        }
-    }
-    __syncwarp();
-}
-
-// Both, for four columns col.. of one row (col % 4 == 0).
-__device__ __forceinline__ void add_rest4(const XParams &p, int row, int col, float (&v)[4]) {
-    auto onto = [&](int64_t i, float f) {
-        const __nv_bfloat16 *src = p.more + i * p.ld_more + col;
+// The same for four columns col.. of one row (col % 4 == 0).
+template <int MORE>
+__device__ __forceinline__ void add_more4(const XParams &p, int row, int col, float (&v)[4]) {
+    if constexpr (MORE == kSums) {
+        const int at = p.first[row];
+        if (at >= p.first[row + 1]) return;
+        const float4 c = *reinterpret_cast<const float4 *>(p.sums + at * p.ld_more + col);
+        v[0] += c.x; v[1] += c.y; v[2] += c.z; v[3] += c.w;
+    } else {
+        const int64_t t = p.targets[row];
+        if (t < 0 || t >= p.vocab) return;
+        const float f = p.rest[row];
+        const __nv_bfloat16 *src = p.more + t * p.ld_more + col;
         if (p.ld_more % 4 == 0) {
             const uint2 w = *reinterpret_cast<const uint2 *>(src);
             v[0] = fmaf(f, bf16_lo(w.x), v[0]);
@@ -425,27 +393,18 @@ __device__ __forceinline__ void add_rest4(const XParams &p, int row, int col, fl
             for (int k = 0; k < 4; ++k)
                 if (col + k < p.N) v[k] = fmaf(f, __bfloat162float(src[k]), v[k]);
         }
-    };
-    if (p.first != nullptr) {
-#pragma unroll 4
-        for (int e = p.first[row], hi = p.first[row + 1]; e < hi; ++e) onto(p.order[e], p.rest[p.order[e]]);
-    } else {
-        const int64_t t = p.targets[row];
-        if (t >= 0 && t < p.vocab) onto(t, p.rest[row]);
     }
 }
 
 // kOut: columns col0 .. col0 + 31 of a warp's 32 rows row0.. (one row a thread), turned in
 // shared memory so that lanes run along the columns (8 column quads x 4 rows an access):
 // into the result, or into a partial tile (rows of `ld` floats) where there is one.
-template <bool ENTRIES>
-__device__ __forceinline__ void out_block(const XParams &p, const float *z, const MoreRow &m, int row0, int col0,
-                                          float *partial, int ld, float *blk, int lane) {
+__device__ __forceinline__ void out_block(const XParams &p, const float *z, int row0, int col0, float *partial, int ld,
+                                          float *blk, int lane) {
     if (row0 >= p.M || col0 >= p.N) return;
 #pragma unroll
     for (int t = 0; t < 32; ++t) blk[lane * 33 + t] = z[t];
     __syncwarp();
-    if constexpr (ENTRIES) add_entries(p, m, blk, col0, lane);
     const int c4 = (lane & 7) * 4, rl = lane >> 3;
 #pragma unroll 4
     for (int k = 0; k < 8; ++k) {
@@ -561,7 +520,7 @@ __device__ __forceinline__ void conv_store(bool vec, uint8_t *dst, int plane, in
 // warps 139 (although the epilogue then spills some registers), with the prefetch 127, without a
 // test for infinities 115.  CTA pairs that share a k block's rows: slower (333 rows 488 against
 // 300 us).
-template <int BN, bool PAIR, int MODE, int TERMS, bool FINE, bool A_MN, bool B_MN, bool CONV>
+template <int BN, bool PAIR, int MODE, int TERMS, bool FINE, bool A_MN, bool B_MN, bool CONV, int MORE>
 __global__ void __launch_bounds__(CONV ? kConvThreads : kThreads, 1) xent_gemm_kernel(const __grid_constant__ XParams p) {
     using S = Shape<BN, PAIR>;
     static_assert(!CONV || (BN == 128 && !PAIR && FINE && !A_MN), "one form");
@@ -837,13 +796,14 @@ __global__ void __launch_bounds__(CONV ? kConvThreads : kThreads, 1) xent_gemm_k
         bool more = next_seg(0, at, next);
         int m0 = 0, n0 = 0, tn = 0;
         GradRow grn{-1, 0.f, 0.f, 0.f};
-        MoreRow mrn{-1, 0.f, 0, 0};
+        MoreRow mrn{-1, 0.f};
         auto enter = [&] {
             place(next.tile, m0, n0, tn);
             if constexpr (MODE == kGrad) grn = grad_row(p, m0 + q * 32 + lane);
-            // (to a split tile the kernel that joins its parts adds it: with many rows at once, where a
-            // part's epilogue, the last of its CTA, would wait for every row's loads)
-            if constexpr (MODE == kOut && !FINE) mrn = next.kb0 == 0 && next.kb1 == KB ? more_row<A_MN>(p, m0 + q * 32 + lane, n0 + half * (BN / 2), BN / 2) : MoreRow{-1, 0.f, 0, 0};
+            // (to a split tile the kernel that joins its parts adds it)
+            if constexpr (MORE != kNone)
+                mrn = next.kb0 == 0 && next.kb1 == KB ? more_row<MORE>(p, m0 + q * 32 + lane, n0 + half * (BN / 2), BN / 2)
+                                                      : MoreRow{-1, 0.f};
         };
         if (more) enter();
         for (int i = 0; ok && more; ++i) {
@@ -857,12 +817,12 @@ __global__ void __launch_bounds__(CONV ? kConvThreads : kThreads, 1) xent_gemm_k
             if (MODE == kOut && (sg.kb0 != 0 || sg.kb1 != KB))
                 part = p.partial + ((int64_t(blockIdx.x) * 2 + sg.slot) * kBM + q * 32) * BN + half * (BN / 2);
             float z[ZN];                                      // this thread's row
-            Quads quads;
+            MoreCols<MORE> cols;
             auto block = [&](float *y, int c0) {              // WN columns from colh + c0
                 if constexpr (MODE == kGrad) grad_box<TERMS>(p, gr, y, row0, colh + c0, box, lane);
                 if constexpr (MODE == kOut) {
-                    if constexpr (!FINE && !A_MN) add_target(p, mr, quads, y, colh + c0);
-                    out_block<!FINE && A_MN>(p, y, mr, row0, colh + c0, part != nullptr ? part + c0 : nullptr, BN, blk, lane);
+                    if constexpr (MORE != kNone) add_more<MORE>(p, mr, cols, y, colh + c0);
+                    out_block(p, y, row0, colh + c0, part != nullptr ? part + c0 : nullptr, BN, blk, lane);
                 }
             };
             for (int k0 = sg.kb0; k0 < sg.kb1; k0 += chunk, ++f) {
@@ -889,7 +849,7 @@ __global__ void __launch_bounds__(CONV ? kConvThreads : kThreads, 1) xent_gemm_k
 #pragma unroll 1
                     for (int c0 = 0; c0 < BN / 2; c0 += WN) {
                         uint32_t v[WN / 32][32];
-                        if constexpr (MODE == kOut && !A_MN) quads = target_quads(p, mr, colh + c0);
+                        if constexpr (MORE != kNone) fetch_more<MORE>(p, mr, cols, colh + c0);
 #pragma unroll
                         for (int j = 0; j < WN / 32; ++j) tmem_ld32(tm + uint32_t(c0 + j * 32), v[j]);
                         tmem_wait_ld();
@@ -936,133 +896,232 @@ __global__ void __launch_bounds__(CONV ? kConvThreads : kThreads, 1) xent_gemm_k
     }
 }
 
+// Loads in program order, so that a row of them is in flight together.
+__device__ __forceinline__ float4 ld_ordered(const float *p) {
+    float4 r;
+    asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];" : "=f"(r.x), "=f"(r.y), "=f"(r.z), "=f"(r.w) : "l"(p) : "memory");
+    return r;
+}
+
 // A split tile (number whole + blockIdx.x) is the sum, in unit order, of its units' partial
-// tiles; block y does rows [y TM / gridDim.y, ...).  A tile of one unit was written by it.
-template <int BN, bool PAIR>
+// tiles; block y does fix_rows of its rows.  (A unit's share is less than a tile: none was written by
+// one unit.)  U parts are in flight together: 16 where a tile has more than 24 (200 x 512 x 131072, 38
+// units a tile: d_hidden 95 us, 101 with 8), else 8 (128 x 2560 x 32768, 15 units: 79 us, 81 with 16).
+template <int BN> constexpr int fix_rows() { return 256 * 4 / BN; }
+template <int BN, bool PAIR, int MORE, int U>
 __global__ void __launch_bounds__(256) xent_fixup_kernel(const __grid_constant__ XParams p) {
     constexpr int TM = PAIR ? 2 * kBM : kBM;
     const int64_t KB = int64_t(p.nprod) * p.kb, ta = int64_t(blockIdx.x) * KB, tb = ta + KB;
-    pdl_wait();
     int c0 = int(ta * p.sk_units / p.sk_work);
     while (c0 > 0 && sk_start(p.sk_work, p.sk_units, c0) > ta) --c0;
     while (c0 + 1 < p.sk_units && sk_start(p.sk_work, p.sk_units, c0 + 1) <= ta) ++c0;
     int c1 = c0;
     while (c1 + 1 < p.sk_units && sk_start(p.sk_work, p.sk_units, c1 + 1) < tb) ++c1;
-    if (c1 == c0) return;
     const int s0 = sk_start(p.sk_work, p.sk_units, c0) < ta ? 1 : 0;
     int m, n;
     tile_of(p, uint32_t(p.whole + blockIdx.x), m, n);
-    const int m0 = m * TM, n0 = n * BN;
-    const int rows = TM / gridDim.y, r0 = blockIdx.y * rows;
-    for (int e = threadIdx.x; e < rows * (BN / 4); e += blockDim.x) {
-        const int r = r0 + e / (BN / 4), c4 = (e % (BN / 4)) * 4;
-        const int row = m0 + r, col = n0 + c4;
-        if (row >= p.M || col >= p.N) continue;
-        const int h = r / kBM, lr = r % kBM;
-        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = c0; c <= c1; c += 8) {                  // eight loads in flight
-            float4 v[8];
+    // four columns a thread
+    const int r = int(blockIdx.y) * fix_rows<BN>() + int(threadIdx.x) / (BN / 4), c4 = int(threadIdx.x) % (BN / 4) * 4;
+    const int row = m * TM + r, col = n * BN + c4, h = r / kBM, lr = r % kBM;
+    const bool on = c1 > c0 && row < p.M && col < p.N;
+    float v[4] = {0.f, 0.f, 0.f, 0.f};
+    // (written by kernels before the product: fetched while that still runs)
+    if (MORE != kNone && on) add_more4<MORE>(p, row, col, v);
+    pdl_wait();
+    if (!on) return;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int c = c0; c <= c1; c += U) {
+        float4 x[U];
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (c + u <= c1) {
-                    const int64_t cta = PAIR ? 2 * int64_t(c + u) + h : c + u;
-                    const int slot = c + u == c0 ? s0 : 0;
-                    v[u] = *reinterpret_cast<const float4 *>(p.partial + ((cta * 2 + slot) * kBM + lr) * BN + c4);
-                }
+        for (int u = 0; u < U; ++u)
+            if (c + u <= c1) {
+                const int64_t cta = PAIR ? 2 * int64_t(c + u) + h : c + u;
+                const int slot = c + u == c0 ? s0 : 0;
+                x[u] = ld_ordered(p.partial + ((cta * 2 + slot) * kBM + lr) * BN + c4);
+            }
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
-                if (c + u <= c1) {
-                    acc.x += v[u].x; acc.y += v[u].y; acc.z += v[u].z; acc.w += v[u].w;
-                }
-        }
-        float v[4] = {acc.x, acc.y, acc.z, acc.w};
-        if (p.more != nullptr) add_rest4(p, row, col, v);
-        store4(p, row, col, v);
+        for (int u = 0; u < U; ++u)
+            if (c + u <= c1) {
+                acc.x += x[u].x; acc.y += x[u].y; acc.z += x[u].z; acc.w += x[u].w;
+            }
     }
+    v[0] += acc.x; v[1] += acc.y; v[2] += acc.z; v[3] += acc.w;
+    store4(p, row, col, v);
 }
 
-// The rows of every target, in ascending order, for the epilogue of d_w: order[first[v]] ..
-// order[first[v + 1] - 1] are those with target v.  A warp 32 columns of the vocabulary (a block
-// all warps): it goes through all targets twice, to count and to place, so that no order depends
-// on timing.  (V / 32 x N / 128 steps twice, against the products' 6 V N D flops.)  The targets come
-// through shared memory kList at a time, and a step looks at four a lane: 4096 targets of 65536
-// columns 13 us beside the rows' products (11 without lists; one a lane a step 21).
-constexpr int kList = 4096;
-__device__ __forceinline__ void list_targets(const int64_t *targets, int64_t rows, int64_t vocab, int64_t v0, int *sh, int *first,
-                                             int *order) {
-    const int lane = threadIdx.x & 31;
-    int at = 0, mine = 0, less = 0;
-    bool any = false;
+// The rows of every target, in ascending order: order[first[v]] .. order[first[v + 1] - 1] are those
+// with target v; span of each is (first[v], their number).  A block has 32 columns of the vocabulary, a
+// lane each, and each of its W warps a share of the rows; they go through them twice, to count and to
+// place, so that no order depends on timing.  Launched as a dependent of dz's product: it starts
+// where that runs out of tiles.
+template <int W>
+__global__ void __launch_bounds__(32 * W) xent_list_kernel(const int64_t *__restrict__ targets, int64_t rows, int64_t vocab,
+                                                           int *__restrict__ first, int *__restrict__ order,
+                                                           int2 *__restrict__ span) {
+    __shared__ int cnt[W][32], below[W];
+    const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+    const uint32_t v0 = blockIdx.x * 32u;
+    const int64_t share = (rows + 128 * W - 1) / (128 * W) * 128, i0 = w * share, i1 = min(rows, i0 + share);
+    int less = 0;                                            // targets below the block's columns
+    int at = 0;                                              // rows of this lane's column; then where they go
+    int2 mine;
+    auto scan = [&](auto place) {
+        constexpr bool PLACE = decltype(place)::value;
 #pragma unroll 1
-    for (int pass = 0; pass < 2; ++pass) {
-#pragma unroll 1
-        for (int64_t i0 = 0; i0 < rows; i0 += kList) {
-            const int n = int(min(int64_t(kList), rows - i0));
-            if (pass == 0 || rows > kList) {                 // else they are still there
-                __syncthreads();
-#pragma unroll 8
-                for (int i = threadIdx.x; i < (n + 127) / 128 * 128; i += 256) {
-                    const int64_t t = i < n ? targets[i0 + i] : -1;
-                    sh[i] = t >= 0 && t < vocab ? int(t) : INT32_MAX;
-                }
-                __syncthreads();
+        for (int64_t i = i0; i < i1; i += 128) {
+            int64_t t[4];                                    // without branches, so that all are in flight
+#pragma unroll
+            for (int u = 0; u < 4; ++u) t[u] = targets[min(i + 32 * u + lane, i1 - 1)];
+            uint32_t d[4];                                   // column in the block, or 32 and more
+            bool hit = false;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const bool on = (uint64_t(t[u]) >> 32 == 0) & (i + 32 * u + lane < i1);
+                if (!PLACE) less += on & (uint32_t(t[u]) < v0);
+                d[u] = on ? uint32_t(t[u]) - v0 : ~0u;
+                hit |= d[u] < 32u;
             }
-            // a lane four neighbours; most steps have none of this warp's targets
-            if (pass == 0 || any)
-#pragma unroll 2
-                for (int i = 4 * lane; i - 4 * lane < n; i += 128) {
-                    const int4 q = *reinterpret_cast<const int4 *>(sh + i);
-                    const int d[4] = {q.x - int(v0), q.y - int(v0), q.z - int(v0), q.w - int(v0)};
-                    bool hit = false;
+            if (!__any_sync(0xffffffffu, hit)) continue;     // most steps have none of the block's columns
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        less += d[k] < 0;
-                        hit |= uint32_t(d[k]) < 32u;
+            for (int u = 0; u < 4; ++u)
+                for (uint32_t here = __ballot_sync(0xffffffffu, d[u] < 32u); here != 0; here &= here - 1) {
+                    const int s = __ffs(here) - 1;
+                    if (__shfl_sync(0xffffffffu, d[u], s) != lane) continue;
+                    if constexpr (PLACE) {
+                        order[at] = int(i) + 32 * u + s;
+                        span[at] = mine;
                     }
-                    for (uint32_t here = __ballot_sync(0xffffffffu, hit); here != 0; here &= here - 1) {
-                        const int s = __ffs(here) - 1;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            if (__shfl_sync(0xffffffffu, d[k], s) != lane) continue;
-                            if (pass == 0) ++mine;
-                            else order[at++] = int(i0) + i + 4 * (s - lane) + k;
-                        }
-                    }
+                    ++at;
                 }
         }
-        if (pass == 0) {
-            int sum = mine;                                  // of this lane's and the lower lanes' columns
+    };
+    scan(std::false_type{});
 #pragma unroll
-            for (int o = 1; o < 32; o *= 2) {
-                const int x = __shfl_up_sync(0xffffffffu, sum, o);
-                if (lane >= o) sum += x;
+    for (int o = 16; o > 0; o /= 2) less += __shfl_xor_sync(0xffffffffu, less, o);
+    cnt[w][lane] = at;
+    if (lane == 0) below[w] = less;
+    __syncthreads();
+    int all = 0, before = 0;                                 // of this lane's column; in the warps before
+    less = 0;
+#pragma unroll
+    for (int k = 0; k < W; ++k) {
+        if (k < w) before += cnt[k][lane];
+        all += cnt[k][lane];
+        less += below[k];
+    }
+    int sum = all;                                           // of this lane's and the lower lanes' columns
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int x = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += x;
+    }
+    const bool any = __any_sync(0xffffffffu, at > 0);
+    at = less + sum - all;
+    if (w == 0) {                                            // (columns past the last list targets outside: past first[vocab])
+        if (v0 + lane < vocab) first[v0 + lane] = at;
+        if (v0 + lane == vocab - 1) first[vocab] = at + all;
+    }
+    mine = make_int2(at, all);
+    at += before;
+    if (any) scan(std::true_type{});
+    // The grid is done no earlier than the product before it: one block waits for that.  (All of them would
+    // keep the blocks that find no room beside it from starting before its end.)
+    if (blockIdx.x == 0) pdl_wait();
+}
+
+// What the targets' dz have lost in d_w: row first[v] of sums is the sum of rest[i] x hidden row i over
+// the rows i with target v, in their order.  gridDim.y warps an entry of `order`; the warps of one
+// target's c entries share its row's chunks of columns.  Four entries or more are split over the warp's
+// groups of lanes, four of 64 columns or sixteen of 16; fewer: a chunk of 64 columns a group.  Launched
+// as a dependent of dz W, as the lists of dz's product.
+__global__ void __launch_bounds__(256) xent_sums_kernel(int64_t vocab, const int *__restrict__ first,
+                                                        const int *__restrict__ order, const int2 *__restrict__ span,
+                                                        const float *__restrict__ rest, const __nv_bfloat16 *__restrict__ h,
+                                                        int64_t ld, float *__restrict__ sums) {
+    pdl_trigger();                                           // the fix-up may be scheduled
+    const int e = int(blockIdx.x) * 8 + int(threadIdx.x >> 5), lane = threadIdx.x & 31, rl = lane >> 3;
+    auto add = [](float (&a)[8], float f, uint4 w) {
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            a[2 * q] = fmaf(f, bf16_lo(x[q]), a[2 * q]);
+            a[2 * q + 1] = fmaf(f, bf16_hi(x[q]), a[2 * q + 1]);
+        }
+    };
+    auto put = [](float *out, const float (&a)[8]) {
+        reinterpret_cast<float4 *>(out)[0] = make_float4(a[0], a[1], a[2], a[3]);
+        reinterpret_cast<float4 *>(out)[1] = make_float4(a[4], a[5], a[6], a[7]);
+    };
+    if (e < first[vocab]) {
+        const int lo = span[e].x, c = span[e].y, j = e - lo + c * int(blockIdx.y), warps = c * int(gridDim.y);
+        const int64_t mine = 8 * (lane & 7);                 // first column of eight in a chunk; ld % 8 == 0
+        if (c < 4) {
+            const __nv_bfloat16 *src[3];
+            float f[3];
+#pragma unroll
+            for (int u = 0; u < 3; ++u) {
+                const int i = order[lo + min(u, c - 1)];
+                f[u] = u < c ? rest[i] : 0.f;
+                src[u] = h + i * ld;
             }
+#pragma unroll 2
+            for (int64_t col = (4 * int64_t(j) + rl) * 64 + mine; col < ld; col += 256 * int64_t(warps)) {
+                float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int o = 16; o > 0; o /= 2) less += __shfl_xor_sync(0xffffffffu, less, o);
-            at = less + sum - mine;
-            if (v0 + lane < vocab) first[v0 + lane] = at;
-            if (v0 + lane == vocab - 1) first[vocab] = at + mine;
-            any = __any_sync(0xffffffffu, mine > 0);
+                for (int u = 0; u < 3; ++u)
+                    if (u < c) add(a, f[u], *reinterpret_cast<const uint4 *>(src[u] + col));
+                put(sums + lo * ld + col, a);
+            }
+        } else {
+            // G groups of 32 / G lanes, G entries and 8 x 32 / G columns at a time
+            auto split = [&](auto groups) {
+                constexpr int G = decltype(groups)::value, L = 32 / G, U = 4;
+                const int g = lane / L;
+                for (int64_t k = int64_t(j) * 8 * L; k < ld; k += int64_t(warps) * 8 * L) {
+                    const int64_t col = k + 8 * (lane % L);
+                    const bool on = col < ld;
+                    float a[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+                    for (int s = g; s < c; s += U * G) {
+                        int i[U];
+                        float f[U];
+                        uint4 w[U];
+#pragma unroll
+                        for (int u = 0; u < U; ++u) i[u] = order[lo + min(s + u * G, c - 1)];
+#pragma unroll
+                        for (int u = 0; u < U; ++u) {
+                            f[u] = s + u * G < c ? rest[i[u]] : 0.f;
+                            w[u] = on ? *reinterpret_cast<const uint4 *>(h + i[u] * ld + col) : make_uint4(0, 0, 0, 0);
+                        }
+#pragma unroll
+                        for (int u = 0; u < U; ++u)
+                            if (s + u * G < c) add(a, f[u], w[u]);
+                    }
+#pragma unroll
+                    for (int o = L; o < 32; o *= 2)
+#pragma unroll
+                        for (int q = 0; q < 8; ++q) a[q] += __shfl_xor_sync(0xffffffffu, a[q], o);
+                    if (on && g == 0) put(sums + lo * ld + col, a);
+                }
+            };
+            // a token that many rows have as target
+            if (c >= 32) split(std::integral_constant<int, 16>{});
+            else split(std::integral_constant<int, 4>{});
         }
     }
+    if (blockIdx.x == 0 && blockIdx.y == 0) pdl_wait();      // done no earlier than the product before it
 }
 
 // zt[i] = <hidden[i], W[t_i]> in fp32: a warp a row.  rest (dz of one bf16 term): what the target's
-// dz loses when it is rounded.  first, order: the blocks past the rows' list the targets.
+// dz loses when it is rounded.
 template <typename HT, typename WT>
 __global__ void __launch_bounds__(256) xent_target_kernel(const HT *__restrict__ hidden, const WT *__restrict__ W,
                                                           const int64_t *__restrict__ targets, int64_t rows, int64_t vocab,
                                                           int64_t dim, float *__restrict__ zt, const float *__restrict__ lse,
-                                                          const float *__restrict__ dloss, float *__restrict__ rest,
-                                                          int *__restrict__ first, int *__restrict__ order) {
+                                                          const float *__restrict__ dloss, float *__restrict__ rest) {
     pdl_trigger();
-    const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5), row_warps = (rows + 7) / 8 * 8;
+    const int64_t row = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
     const int lane = threadIdx.x & 31;
-    if (row >= row_warps) {                                  // whole blocks
-        __shared__ __align__(16) int sh[kList];
-        list_targets(targets, rows, vocab, (row - row_warps) * 32, sh, first, order);
-        return;
-    }
     if (row >= rows) return;
     const int64_t t = targets[row];
     if (t < 0 || t >= vocab) {
@@ -1226,8 +1285,12 @@ struct Mat {
     const float *f32 = nullptr;  // instead: the float32 matrix, rows cols apart, taken apart by the product
 };
 
-template <int BN, bool PAIR, int MODE, int TERMS, bool FINE, bool A_MN, bool B_MN, bool CONV = false>
-int launch(XParams &p, const Mat &a, const Mat &b, cudaStream_t st, bool dependent = false) {
+// beside: launches what may run beside the product (and waits for its end).
+struct Nothing {
+    int operator()() const { return TLB_OK; }
+};
+template <int BN, bool PAIR, int MODE, int TERMS, bool FINE, bool A_MN, bool B_MN, bool CONV = false, typename F = Nothing>
+int launch(XParams &p, const Mat &a, const Mat &b, cudaStream_t st, bool dependent = false, F beside = F()) {
     using S = Shape<BN, PAIR>;
     constexpr int stages = stages_of<BN, PAIR, MODE, CONV>();
     constexpr int smem = stages * (CONV ? 3 : 1) * S::STAGE + epi_bytes<MODE>() + 1024;
@@ -1275,7 +1338,12 @@ int launch(XParams &p, const Mat &a, const Mat &b, cudaStream_t st, bool depende
             p.units = p.whole > 0 ? most : p.sk_units;
         }
     }
-    auto k = xent_gemm_kernel<BN, PAIR, MODE, TERMS, FINE, A_MN, B_MN, CONV>;
+    // (a form of its own: the code costs the others 1 to 2 us; split tiles get it from the fix-up)
+    constexpr int MORE = MODE != kOut || FINE ? kNone : A_MN ? kSums : kTargets;
+    const bool more = MORE != kNone && p.rest != nullptr;
+    auto k = xent_gemm_kernel<BN, PAIR, MODE, TERMS, FINE, A_MN, B_MN, CONV, kNone>;
+    if constexpr (MORE != kNone)
+        if (more && p.whole > 0) k = xent_gemm_kernel<BN, PAIR, MODE, TERMS, FINE, A_MN, B_MN, CONV, MORE>;
     TLB_CUDA(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned((PAIR ? 2 : 1) * p.units));
@@ -1292,9 +1360,12 @@ int launch(XParams &p, const Mat &a, const Mat &b, cudaStream_t st, bool depende
     cfg.numAttrs = dependent ? 2 : 1;
     TLB_CUDA(cudaLaunchKernelEx(&cfg, k, p));
     TLB_TRY(check_launch(MODE == kStats ? "xent_stats" : MODE == kGrad ? "xent_grad" : A_MN ? "xent_dw" : "xent_dh"));
+    TLB_TRY(beside());
     if (p.sk_work > 0) {
         const int64_t rest = p.sk_work / KB;
-        TLB_CUDA(launch_dependent(xent_fixup_kernel<BN, PAIR>, dim3(unsigned(rest), PAIR ? 64 : 32), dim3(256), 0, st, p));
+        auto fix = p.sk_units > 24 * rest ? (more ? xent_fixup_kernel<BN, PAIR, MORE, 16> : xent_fixup_kernel<BN, PAIR, kNone, 16>)
+                                         : (more ? xent_fixup_kernel<BN, PAIR, MORE, 8> : xent_fixup_kernel<BN, PAIR, kNone, 8>);
+        TLB_CUDA(launch_dependent(fix, dim3(unsigned(rest), S::TM / fix_rows<BN>()), dim3(256), 0, st, p));
         TLB_TRY(check_launch("xent_fixup"));
     }
     return TLB_OK;
@@ -1318,13 +1389,13 @@ int launch_z(XParams &p, const Mat &h, const Mat &w, bool after_targets, cudaStr
     return launch<128, false, MODE, TERMS, fine, false, false>(p, h, w, st, after_targets);
 }
 
-template <bool A_MN, bool FINE>
-int launch_out(XParams &p, const Mat &a, const Mat &b, cudaStream_t st) {
+template <bool A_MN, bool FINE, typename F = Nothing>
+int launch_out(XParams &p, const Mat &a, const Mat &b, cudaStream_t st, F beside = F()) {
     if constexpr (FINE && !A_MN)
         if (b.f32 != nullptr)
             return launch<128, false, kOut, 1, true, false, true, true>(p, a, b, st);
-    if (p.M > kBM) return launch<256, true, kOut, 1, FINE, A_MN, true>(p, a, b, st);
-    return launch<256, false, kOut, 1, FINE, A_MN, true>(p, a, b, st);
+    if (p.M > kBM) return launch<256, true, kOut, 1, FINE, A_MN, true>(p, a, b, st, false, beside);
+    return launch<256, false, kOut, 1, FINE, A_MN, true>(p, a, b, st, false, beside);
 }
 
 constexpr int64_t kPieceBytes = int64_t(512) << 20;   // of dz, and of packed head rows, in the workspace
@@ -1344,8 +1415,8 @@ struct Plan {
     int64_t dp;                  // packed row length
     int64_t piece;               // vocabulary rows of one piece (multiple of 256)
     int64_t part_ld, slots;
-    size_t h, w, dz, part, zt, rest, first, order, acc, partial, total;
-    bool keep_rest, list;        // the targets' dz: what its rounding loses, and the rows of each target (d_w)
+    size_t h, w, dz, part, zt, rest, first, order, span, sums, acc, partial, total;
+    bool keep_rest, list;        // what the targets' dz lose, and its sums over the rows of each target (d_w)
 };
 
 Plan plan_of(int htype, int wtype, int64_t N, int64_t V, int64_t D, bool grad, bool grad_w) {
@@ -1367,7 +1438,7 @@ Plan plan_of(int htype, int wtype, int64_t N, int64_t V, int64_t D, bool grad, b
     q.h = q.pack_h ? w.take(size_t(q.h_terms) * N * q.dp * 2) : 0;
     q.w = q.pack_w ? w.take(size_t(q.w_terms) * q.piece * q.dp * 2) : 0;
     q.part_ld = q.slots = 0;
-    q.part = q.zt = q.rest = q.first = q.order = q.dz = q.acc = q.partial = 0;
+    q.part = q.zt = q.rest = q.first = q.order = q.span = q.sums = q.dz = q.acc = q.partial = 0;
     q.keep_rest = grad && q.z_terms == 1;
     q.list = q.keep_rest && grad_w;
     if (!grad) {
@@ -1383,6 +1454,8 @@ Plan plan_of(int htype, int wtype, int64_t N, int64_t V, int64_t D, bool grad, b
         if (q.list) {
             q.first = w.take(size_t(V + 1) * 4);
             q.order = w.take(size_t(N) * 4);
+            q.span = w.take(size_t(N) * 8);
+            q.sums = w.take(size_t(N) * q.dp * 4);
         }
         if (htype != TLB_W_F32 && q.piece < V) q.acc = w.take(size_t(N) * D * 4);
         q.partial = w.take(size_t(num_sms() + 1) * 2 * kBM * 256 * 4);
@@ -1457,21 +1530,34 @@ bool by_tokens(const Plan &q, int64_t rows, int64_t dim, bool grad) {
 }
 
 int target_logits(int htype, const void *hidden, int wtype, const void *W, const int64_t *targets, int64_t rows, int64_t vocab,
-                  int64_t dim, float *zt, const float *lse, const float *dloss, float *rest, int *first, int *order,
-                  cudaStream_t st) {
-    const unsigned grid = unsigned(ceil_div(rows, 8) + (first != nullptr ? ceil_div(vocab, 256) : 0));
+                  int64_t dim, float *zt, const float *lse, const float *dloss, float *rest, cudaStream_t st) {
+    const unsigned grid = unsigned(ceil_div(rows, 8));
     const float *hf = static_cast<const float *>(hidden);
     const __nv_bfloat16 *hb = static_cast<const __nv_bfloat16 *>(hidden), *wb = static_cast<const __nv_bfloat16 *>(W);
     if (wtype == TLB_W_F32)
-        xent_target_kernel<<<grid, 256, 0, st>>>(hf, static_cast<const float *>(W), targets, rows, vocab, dim, zt, lse, dloss, rest,
-                                                  first, order);
+        xent_target_kernel<<<grid, 256, 0, st>>>(hf, static_cast<const float *>(W), targets, rows, vocab, dim, zt, lse, dloss, rest);
     else if (htype == TLB_W_F32)
-        xent_target_kernel<<<grid, 256, 0, st>>>(hf, wb, targets, rows, vocab, dim, zt, lse, dloss, rest,
-                                                  first, order);
+        xent_target_kernel<<<grid, 256, 0, st>>>(hf, wb, targets, rows, vocab, dim, zt, lse, dloss, rest);
     else
-        xent_target_kernel<<<grid, 256, 0, st>>>(hb, wb, targets, rows, vocab, dim, zt, lse, dloss, rest,
-                                                  first, order);
+        xent_target_kernel<<<grid, 256, 0, st>>>(hb, wb, targets, rows, vocab, dim, zt, lse, dloss, rest);
     return check_launch("xent_target");
+}
+
+// Which rows have each target, and what their dz lose, summed; both beside a product.
+int list_targets(const Plan &q, void *ws, const int64_t *targets, int64_t rows, int64_t vocab, cudaStream_t st) {
+    const int64_t blocks = ceil_div(vocab, 32);
+    // 32 warps a block where all blocks run at once (both gradients of 4096 x 1024 x 4096 122 us, of 100000 x
+    // 64 x 1000 363, with 8 warps 128 and 570), 8 where there are many
+    const bool wide = blocks <= 2 * num_sms();
+    TLB_CUDA(launch_dependent(wide ? xent_list_kernel<32> : xent_list_kernel<8>, dim3(unsigned(blocks)), dim3(wide ? 1024 : 256), 0,
+                              st, targets, rows, vocab, ws_at<int>(ws, q.first), ws_at<int>(ws, q.order), ws_at<int2>(ws, q.span)));
+    return check_launch("xent_list");
+}
+int sum_rests(const Plan &q, void *ws, int64_t rows, int64_t vocab, const Mat &h, cudaStream_t st) {
+    TLB_CUDA(launch_dependent(xent_sums_kernel, dim3(unsigned(ceil_div(rows, 8)), unsigned(ceil_div(h.ld, 512))), dim3(256), 0, st,
+                              vocab, ws_at<int>(ws, q.first), ws_at<int>(ws, q.order), ws_at<int2>(ws, q.span),
+                              ws_at<float>(ws, q.rest), h.p, h.ld, ws_at<float>(ws, q.sums)));
+    return check_launch("xent_sums");
 }
 
 const void *row_of(const void *x, int type, int64_t r, int64_t dim) {
@@ -1546,7 +1632,7 @@ int tlb_xent_forward(int32_t htype, const void *hidden, int32_t wtype, const voi
             TLB_TRY(head_operand(q, wtype, W, v0, nv, dim, ws, st, w));
             if (v0 == 0)
                 TLB_TRY(target_logits(htype, row_of(hidden, htype, r0, dim), wtype, W, targets + r0, n, vocab, dim,
-                                      ws_at<float>(ws, q.zt) + r0, nullptr, nullptr, nullptr, nullptr, nullptr, st));
+                                      ws_at<float>(ws, q.zt) + r0, nullptr, nullptr, nullptr, st));
             XParams p;
             memset(&p, 0, sizeof(p));
             p.M = int(n);
@@ -1594,14 +1680,12 @@ int tlb_xent_backward(int32_t htype, const void *hidden, int32_t wtype, const vo
     TLB_TRY(hidden_operand(q, htype, hidden, rows, dim, d_w != nullptr ? targets : nullptr, vocab, ws, st, h));
     const bool wide = htype == TLB_W_F32;
     float *rest = q.keep_rest ? ws_at<float>(ws, q.rest) : nullptr;
-    int *first = q.list ? ws_at<int>(ws, q.first) : nullptr, *order = q.list ? ws_at<int>(ws, q.order) : nullptr;
     for (int64_t v0 = 0; v0 < vocab; v0 += q.piece) {
         const int64_t nv = std::min(q.piece, vocab - v0);
         Mat w;
         TLB_TRY(head_operand(q, wtype, W, v0, nv, dim, ws, st, w));
         if (v0 == 0)
-            TLB_TRY(target_logits(htype, hidden, wtype, W, targets, rows, vocab, dim, ws_at<float>(ws, q.zt), lse, d_loss, rest,
-                                  first, order, st));
+            TLB_TRY(target_logits(htype, hidden, wtype, W, targets, rows, vocab, dim, ws_at<float>(ws, q.zt), lse, d_loss, rest, st));
         const Mat dz{ws_at<__nv_bfloat16>(ws, q.dz), rows, nv, q.piece, rows * q.piece, q.z_terms};
         {
             XParams p;
@@ -1620,6 +1704,7 @@ int tlb_xent_backward(int32_t htype, const void *hidden, int32_t wtype, const vo
             if (q.z_terms == 3) TLB_TRY((launch_z<kGrad, 3>(p, h, w, v0 == 0, st)));
             else if (q.z_terms == 2) TLB_TRY((launch_z<kGrad, 2>(p, h, w, v0 == 0, st)));
             else TLB_TRY((launch_z<kGrad, 1>(p, h, w, v0 == 0, st)));
+            if (q.list && v0 == 0) TLB_TRY(list_targets(q, ws, targets, rows, vocab, st));
         }
         {
             XParams p;
@@ -1641,7 +1726,8 @@ int tlb_xent_backward(int32_t htype, const void *hidden, int32_t wtype, const vo
             p.vec = dim % 4 == 0 && aligned16(d_hidden);
             p.partial = ws_at<float>(ws, q.partial);
             p.status = ws_at<uint32_t>(ws, 0);
-            TLB_TRY((wide ? launch_out<false, true>(p, dz, w, st) : launch_out<false, false>(p, dz, w, st)));
+            auto beside = [&] { return q.list && v0 == 0 ? sum_rests(q, ws, rows, vocab, h, st) : TLB_OK; };
+            TLB_TRY((wide ? launch_out<false, true>(p, dz, w, st) : launch_out<false, false>(p, dz, w, st, beside)));
         }
         if (d_w != nullptr) {
             XParams p;
@@ -1654,10 +1740,9 @@ int tlb_xent_backward(int32_t htype, const void *hidden, int32_t wtype, const vo
             p.vec = dim % 4 == 0 && aligned16(d_w);
             if (q.list) {
                 p.rest = rest;
-                p.more = h.p;
+                p.sums = ws_at<float>(ws, q.sums);
                 p.ld_more = h.ld;
-                p.first = first + v0;
-                p.order = order;
+                p.first = ws_at<int>(ws, q.first) + v0;
             }
             p.partial = ws_at<float>(ws, q.partial);
             p.status = ws_at<uint32_t>(ws, 0);
