@@ -327,7 +327,8 @@ int tlb_muon(const tlb_muon_mat *mats, int32_t n, const tlb_muon_cfg *cfg, void 
  * lse hold; its lse is that of its logits all the same.
  *
  * Types (TLB_W_F32, TLB_W_BF16): hidden and W both bf16; hidden f32 with W bf16 or f32.
- * d_hidden and d_w (both overwritten) have hidden's type.  Up to four rows (eight with a
+ * d_hidden and d_w (both overwritten) have hidden's type (the layer calls take a float32 dOut:
+ * bf16 hidden's d_hidden has to be cast for them).  Up to four rows (eight with a
  * float32 head) run on a kernel that reads the head once, in fp32 throughout (dim up to a few
  * thousand), more on the tcgen05 tensor cores with fp32 sums.  On the tensor cores:
  * bf16 hidden: dz is rounded to bf16 as the operand of the gradient products, for up to 64
