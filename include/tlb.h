@@ -357,6 +357,92 @@ int tlb_xent_backward(int32_t htype, const void *hidden, int32_t wtype, const vo
                       const float *lse, const float *d_loss, int64_t rows, int64_t vocab, int64_t dim, void *d_hidden,
                       void *d_w, void *ws, size_t ws_bytes, void *stream);
 
+/* ---------------------------------------------------------------- 8-bit blocks */
+
+/* Frozen weights and cached keys and values in 8 bits.  A block of values is held as e4m3 (4
+ * exponent bits, 3 mantissa bits, no infinity, largest value 448; one byte each) times a float32
+ * scale of the block.  The calls that quantise choose the scale from the block's largest magnitude:
+ * the smallest power of two 2^e, e >= -126, with max|x| <= 448 * 2^e; each value is x / 2^e rounded
+ * once to e4m3 (nearest, ties to even; values below 2^-9 of the scale lose bits).  A block that holds
+ * an infinity or a NaN gets the scale NaN and all its values are NaN.  The calls that read take any
+ * float32 scale.  Float tensors are TLB_W_F32 or TLB_W_BF16 (`type`). */
+
+/* x [rows, cols] in `type` to q [rows, cols] (e4m3) and scales [ceil(rows / block_rows),
+ * ceil(cols / 128)]: blocks of block_rows x 128, where block_rows is 1 (activations and gradients:
+ * a scale for 128 values of a row) or 128 (weights).  Blocks at the edges are smaller.  Any sizes;
+ * rows or cols 0 is a no-op.  Any alignment goes; 16 bytes and cols % 8 == 0 are faster. */
+int tlb_fp8_quantize(int32_t type, const void *x, int64_t rows, int64_t cols, int32_t block_rows, uint8_t *q,
+                     float *scales, void *stream);
+
+/* The Wt product of tlb_linear_backward with both operands in 8-bit blocks:
+ *   dX[s, i] (+)= sum_o dy_scales[s, o / 128] dY[s, o] * w_scales[i / 128, o / 128] W[i, o]
+ * dY [S, out_dim] with dy_scales [S, ceil(out_dim / 128)] and W [in_dim, out_dim] with w_scales
+ * [ceil(in_dim / 128), ceil(out_dim / 128)], as tlb_fp8_quantize lays them out (block_rows 1 and
+ * 128); dX [S, in_dim] in `type`, overwritten, or added to with accumulate = 1 (rounded once).
+ * Products of e4m3 values are exact; the sum over 128 columns and the sum of these, each times the
+ * product of its two scales, are float32.  A product of two scales below 2^-126 loses bits, one above
+ * the float32 range is infinite (and makes a sum of 0 a NaN).  Same inputs, same bits.
+ * S >= 0, in_dim >= 0, out_dim >= 0, up to 2^24 each (S = 0 or in_dim = 0 is a no-op; out_dim = 0 gives
+ * sums of 0).  W, dY and dX 16-byte aligned, dX may not overlap them.
+ * ws: its first 256 bytes zero-filled once, 256-byte aligned, tlb_linear_fp8_workspace_bytes() bytes. */
+size_t tlb_linear_fp8_workspace_bytes(int64_t S, int64_t out_dim, int64_t in_dim);
+int tlb_linear_fp8_backward(const uint8_t *W, const float *w_scales, const uint8_t *dY, const float *dy_scales, int64_t S,
+                            int64_t out_dim, int64_t in_dim, int32_t type, void *dX, int32_t accumulate, void *ws,
+                            size_t ws_bytes, void *stream);
+
+/* A K/V cache in 8 bits: n_slots rows of n_kv_heads x head_dim keys and values (e4m3), with a scale
+ * for each row and head.  A slot holds the key and value of one position of one sequence; which, is
+ * the caller's (pages of slots, or one sequence after the other).  k and v 16-byte aligned. */
+typedef struct {
+    uint8_t *k, *v;          /* [n_slots, n_kv_heads, head_dim] e4m3 */
+    float *k_scale, *v_scale;/* [n_kv_heads, n_slots] */
+    int64_t n_slots;
+    int32_t n_kv_heads;
+    int32_t head_dim;        /* a multiple of 16, <= 256 */
+} tlb_kv8;
+
+/* Quantises `rows` new keys and values into the cache: row i, head h of k is the head_dim values at
+ * k[i * k_stride_row + h * k_stride_head] (strides in elements; v alike with its own), of `type`, and
+ * goes to slot slots[i].  A slot outside [0, n_slots) (padding: -1) is skipped; the others must
+ * differ from one another (of rows with one slot, none is sure to be kept whole). */
+int tlb_kv8_write(const tlb_kv8 *cache, int32_t type, const void *k, int64_t k_stride_row, int64_t k_stride_head,
+                  const void *v, int64_t v_stride_row, int64_t v_stride_head, const int64_t *slots, int64_t rows,
+                  void *stream);
+
+/* The cache back as floats: value d of head h of slot slots[i] goes to k[i * stride_row + h *
+ * stride_head + d] (v alike), the K and V that a layer call takes (tlb_layer_acts).  Rows whose slot is
+ * outside [0, n_slots) are set to 0.  A slot may be read more than once. */
+int tlb_kv8_read(const tlb_kv8 *cache, const int64_t *slots, int64_t rows, int32_t type, void *k, void *v,
+                 int64_t stride_row, int64_t stride_head, void *stream);
+
+/* Attention of single tokens over the cache, one query row for each of n_seq sequences, and its
+ * gradient (the single-token form of tlb_attn_backward, which reads the cache as it is).  Key j of
+ * sequence b, j < lengths[b], is in slot pages[b, j / page] * page + j % page; keys whose slot is outside
+ * [0, n_slots), and keys from max_len or max_pages * page on, are not there.  The newest key
+ * (lengths[b] - 1) is the token's own.  Query head h reads KV head h / (n_heads / n_kv_heads).
+ *   s_j = scale <q, k_j>   lse = log sum_j exp s_j   p_j = exp(s_j - lse)
+ *   forward:   ctx = sum_j p_j v_j
+ *   backward:  dp_j = <d_ctx, v_j>   ds_j = p_j (dp_j - sum_i p_i dp_i)   d_q = scale sum_j ds_j k_j
+ *              and, of the newest key alone (the older ones are constants of the call, as in
+ *              tlb_attn_backward), summed over the heads that share it:
+ *              d_k = scale sum_h ds q   d_v = sum_h p d_ctx
+ * q, ctx, d_ctx, d_q [n_seq, n_heads, head_dim] and d_k, d_v [n_seq, n_kv_heads, head_dim] in `type`,
+ * 16-byte aligned; lse [n_seq, n_heads] float32; pages [n_seq, max_pages] and lengths [n_seq] int32.
+ * A sequence without a key (length <= 0) gives ctx 0, lse -infinity and gradients 0.  backward takes
+ * the lse that forward gave.  All sums are float32; q, d_ctx and the weights of the sums
+ * are taken apart into two halves that hold 22 bits or more of them.  Same inputs, same bits.
+ * max_len bounds the work: set it near the longest length.  n_seq, max_len >= 0, max_len <= 2^30.
+ * ws: its first 256 bytes zero-filled once, 256-byte aligned, tlb_kv8_attn_workspace_bytes() bytes
+ * (grad: enough for both calls, else for forward; 0 for sizes that the calls refuse). */
+size_t tlb_kv8_attn_workspace_bytes(const tlb_kv8 *cache, int64_t n_seq, int32_t n_heads, int64_t max_len, int32_t grad);
+int tlb_kv8_attn_forward(const tlb_kv8 *cache, const int32_t *pages, int64_t max_pages, int32_t page,
+                         const int32_t *lengths, int64_t n_seq, int64_t max_len, int32_t n_heads, float scale, int32_t type,
+                         const void *q, void *ctx, float *lse, void *ws, size_t ws_bytes, void *stream);
+int tlb_kv8_attn_backward(const tlb_kv8 *cache, const int32_t *pages, int64_t max_pages, int32_t page,
+                          const int32_t *lengths, int64_t n_seq, int64_t max_len, int32_t n_heads, float scale, int32_t type,
+                          const void *q, const float *lse, const void *d_ctx, void *d_q, void *d_k, void *d_v, void *ws,
+                          size_t ws_bytes, void *stream);
+
 /* ---------------------------------------------------------------- layer pieces */
 
 /* Workspace bytes needed by tlb_ffn_backward / tlb_attn_backward /

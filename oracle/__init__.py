@@ -6,6 +6,7 @@ the benchmark's CPU-baseline leg may import it; the library itself never does,
 and it shares no code with the library (the two meet only in the seeded input
 generator of the ``synth`` package).
 
+``blocks8`` 8-bit blocks, their product, and attention over an 8-bit K/V cache
 ``ops``     one function per step of the backward, each citing its passage
 ``layer``   the steps composed into ffn / attention / LoRA+AdamW / layer / stack
 ``forward`` a consistent forward used only to pin the backward by finite differences
@@ -13,6 +14,6 @@ generator of the ``synth`` package).
 Every function is pinned by the ``not gpu`` tests (finite differences, closed
 forms, invariants, special cases); none is marked unpinned.
 """
-from . import forward, layer, ops
+from . import blocks8, forward, layer, ops
 
-__all__ = ["forward", "layer", "ops"]
+__all__ = ["blocks8", "forward", "layer", "ops"]

@@ -63,6 +63,11 @@ class MuonCfg(C.Structure):
                 ("a", C.c_double), ("b", C.c_double), ("c", C.c_double), ("steps", i32), ("nesterov", i32)]
 
 
+class Kv8(C.Structure):
+    _fields_ = [("k", vp), ("v", vp), ("k_scale", vp), ("v_scale", vp), ("n_slots", i64), ("n_kv_heads", i32),
+                ("head_dim", i32)]
+
+
 P = C.POINTER
 SIGNATURES = {
     "tlb_last_error": (C.c_char_p, []),
@@ -85,6 +90,14 @@ SIGNATURES = {
     "tlb_xent_forward_workspace_bytes": (sz, [i32, i32, i64, i64, i64]),
     "tlb_xent_forward": (C.c_int, [i32, vp, i32, vp, vp, i64, i64, i64, vp, vp, vp, sz, vp]),
     "tlb_xent_backward": (C.c_int, [i32, vp, i32, vp, vp, vp, vp, i64, i64, i64, vp, vp, vp, sz, vp]),
+    "tlb_fp8_quantize": (C.c_int, [i32, vp, i64, i64, i32, vp, vp, vp]),
+    "tlb_linear_fp8_workspace_bytes": (sz, [i64, i64, i64]),
+    "tlb_linear_fp8_backward": (C.c_int, [vp, vp, vp, vp, i64, i64, i64, i32, vp, i32, vp, sz, vp]),
+    "tlb_kv8_write": (C.c_int, [P(Kv8), i32, vp, i64, i64, vp, i64, i64, vp, i64, vp]),
+    "tlb_kv8_read": (C.c_int, [P(Kv8), vp, i64, i32, vp, vp, i64, i64, vp]),
+    "tlb_kv8_attn_workspace_bytes": (sz, [P(Kv8), i64, i32, i64, i32]),
+    "tlb_kv8_attn_forward": (C.c_int, [P(Kv8), vp, i64, i32, vp, i64, i64, i32, f32, i32, vp, vp, vp, vp, sz, vp]),
+    "tlb_kv8_attn_backward": (C.c_int, [P(Kv8), vp, i64, i32, vp, i64, i64, i32, f32, i32, vp, vp, vp, vp, vp, vp, vp, sz, vp]),
     "tlb_workspace_bytes": (sz, [P(LayerCfg), i64, i64]),
     "tlb_workspace_status": (C.c_int, [vp, sz, vp]),
     "tlb_ffn_backward": (C.c_int, [P(LayerCfg), i64, vp, P(LayerWeights), P(LayerActs), vp, vp,

@@ -309,6 +309,203 @@ def xent_backward(hidden, W, targets, lse, d_loss, d_hidden=None, d_w=None, grad
     return d_hidden, d_w
 
 
+# ------------------------------------------------------------------ 8-bit blocks
+
+_FP8_BLOCK = 128
+_E4M3 = torch.float8_e4m3fn
+
+
+def _at(t, shape, dtype, device, name):
+    """Address of a contiguous tensor of this shape (None: any), type and device."""
+    if t.dtype != dtype:
+        raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
+    if shape is not None and t.shape != shape:
+        raise ValueError("%s must have shape %s, got %s" % (name, tuple(shape), tuple(t.shape)))
+    if t.device != device:
+        raise ValueError("%s is on %s, expected on %s" % (name, t.device, device))
+    if not t.is_cuda:
+        raise ValueError("%s must be on a CUDA device" % name)
+    if not t.is_contiguous():
+        raise ValueError("%s must be contiguous" % name)
+    return t.data_ptr()
+
+
+def _status_cleared(n, device):
+    """A workspace of n bytes, its status block zeroed."""
+    ws = torch.empty(max(n, _STATUS_BYTES), dtype=torch.uint8, device=device)
+    ws[:_STATUS_BYTES].zero_()
+    return ws
+
+
+def fp8_quantize(x, block_rows=1, q=None, scales=None, stream=None):
+    """x [rows, cols] (float32 or bfloat16) in 8-bit blocks of block_rows (1, or 128 for weights) x 128
+    columns: (q, scales), q float8_e4m3fn [rows, cols] and scales float32 [ceil(rows / block_rows),
+    ceil(cols / 128)], powers of two.  x is about q * scales."""
+    code = _xent_code(x.dtype, "x")
+    if x.dim() != 2:
+        raise ValueError("x [rows, cols] expected, got %s" % (tuple(x.shape),))
+    rows, cols = x.shape
+    blocks = (-(-rows // max(int(block_rows), 1)), -(-cols // _FP8_BLOCK))
+    with _queued(x, stream):
+        q = torch.empty(rows, cols, dtype=_E4M3, device=x.device) if q is None else q
+        scales = torch.empty(blocks, dtype=torch.float32, device=x.device) if scales is None else scales
+        A.call("tlb_fp8_quantize", code, _at(x, None, x.dtype, x.device, "x"), rows, cols, int(block_rows),
+               _at(q, x.shape, _E4M3, x.device, "q"), _at(scales, blocks, torch.float32, x.device, "scales"), _stream(stream))
+    return q, scales
+
+
+def linear_fp8_workspace(S, out_dim, in_dim, device="cuda"):
+    """A workspace tensor, its status block zeroed, for linear_fp8_backward of these sizes."""
+    return _status_cleared(int(A.load().tlb_linear_fp8_workspace_bytes(int(S), int(out_dim), int(in_dim))), device)
+
+
+def linear_fp8_backward(W, w_scales, dY, dy_scales, out=None, accumulate=False, dtype=torch.float32, ws=None, stream=None):
+    """dX = dY @ W^T [S, in] of fp8_quantize()d dY [S, out] (block_rows 1) and W [in, out] (block_rows 128),
+    in dtype (float32 or bfloat16; that of out where it is given); accumulate adds into out.
+    Without ws the call makes one of its own, which workspace_status() without one looks after."""
+    if W.dim() != 2 or dY.dim() != 2 or W.shape[1] != dY.shape[1]:
+        raise ValueError("W [in, out] and dY [S, out] expected, got %s and %s" % (tuple(W.shape), tuple(dY.shape)))
+    if accumulate and out is None:
+        raise ValueError("accumulate needs out")
+    (in_dim, out_dim), S, dev = W.shape, dY.shape[0], W.device
+    dtype = dtype if out is None else out.dtype
+    code = _xent_code(dtype, "out")
+    columns = -(-out_dim // _FP8_BLOCK)
+    with _queued(W, stream):
+        out = torch.empty(S, in_dim, dtype=dtype, device=dev) if out is None else out
+        own = ws is None
+        if own:
+            ws = linear_fp8_workspace(S, out_dim, in_dim, dev)
+        A.call("tlb_linear_fp8_backward", _at(W, None, _E4M3, dev, "W"),
+               _at(w_scales, (-(-in_dim // _FP8_BLOCK), columns), torch.float32, dev, "w_scales"),
+               _at(dY, None, _E4M3, dev, "dY"), _at(dy_scales, (S, columns), torch.float32, dev, "dy_scales"), S, out_dim, in_dim,
+               code, _at(out, (S, in_dim), dtype, dev, "out"), 1 if accumulate else 0,
+               _at(ws, None, torch.uint8, dev, "ws"), ws.numel(), _stream(stream))
+        if own:
+            _keep_status(ws)
+    return out
+
+
+def kv8_cache(n_slots, n_kv_heads, head_dim, device="cuda"):
+    """An 8-bit K/V cache of n_slots positions, all 0, for kv8_write, kv8_read and kv8_attn_*."""
+    rows = [torch.zeros(n_slots, n_kv_heads, head_dim, dtype=torch.uint8, device=device).view(_E4M3) for _ in range(2)]
+    scales = [torch.zeros(n_kv_heads, n_slots, dtype=torch.float32, device=device) for _ in range(2)]
+    return kv8_cache_of(rows[0], scales[0], rows[1], scales[1])
+
+
+def kv8_cache_of(k, k_scale, v, v_scale):
+    """An 8-bit K/V cache in these tensors: k, v float8_e4m3fn [n_slots, n_kv_heads, head_dim], k_scale, v_scale
+    float32 [n_kv_heads, n_slots].  Holds them (as .k, .k_scale, .v, .v_scale); their memory must stay where it is."""
+    if k.dim() != 3:
+        raise ValueError("k [n_slots, n_kv_heads, head_dim] expected, got %s" % (tuple(k.shape),))
+    n_slots, n_kv, hd = k.shape
+    at = (_at(k, None, _E4M3, k.device, "k"), _at(v, k.shape, _E4M3, k.device, "v"),
+          _at(k_scale, (n_kv, n_slots), torch.float32, k.device, "k_scale"),
+          _at(v_scale, (n_kv, n_slots), torch.float32, k.device, "v_scale"))
+    cache = A.Kv8(*at, n_slots, n_kv, hd)
+    cache.tensors = k, k_scale, v, v_scale
+    cache.device = k.device
+    return cache
+
+
+def kv8_write(cache, k, v, slots, stream=None):
+    """Quantises new rows k, v [rows, n_kv_heads, head_dim] (float32 or bfloat16; head_dim dense, other strides any)
+    into slots (int64 [rows], distinct; those outside the cache, such as -1, are skipped)."""
+    rows = slots.numel()
+    code = _xent_code(k.dtype, "k")
+    for name, t in (("k", k), ("v", v)):
+        if t.shape != (rows, cache.n_kv_heads, cache.head_dim) or t.dtype != k.dtype or t.device != cache.device:
+            raise ValueError("%s must be %s [%d, %d, %d] on %s" % (name, k.dtype, rows, cache.n_kv_heads, cache.head_dim,
+                                                                 cache.device))
+        if t.numel() and t.stride(2) != 1:
+            raise ValueError("%s: the values of a head must be dense" % name)
+    with _queued(k, stream):
+        A.call("tlb_kv8_write", cache, code, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1),
+               _at(slots, (rows,), torch.int64, cache.device, "slots"), rows, _stream(stream))
+
+
+def kv8_read(cache, slots, dtype=torch.float32, kv_layout="shd", k=None, v=None, stream=None):
+    """The keys and values of slots (int64 [rows]; 0 for those outside the cache) as (k, v) in dtype: [rows, n_kv_heads,
+    head_dim] for kv_layout 'shd', [n_kv_heads, rows, head_dim] for 'hsd', the layouts that layer_acts() takes."""
+    rows, n_kv, hd = slots.numel(), cache.n_kv_heads, cache.head_dim
+    if kv_layout not in ("shd", "hsd"):
+        raise ValueError("kv_layout must be 'shd' or 'hsd', got %r" % (kv_layout,))
+    if (k is None) != (v is None):
+        raise ValueError("k and v are given together or not at all")
+    shape = (rows, n_kv, hd) if kv_layout == "shd" else (n_kv, rows, hd)
+    dtype = dtype if k is None else k.dtype
+    code = _xent_code(dtype, "k")
+    with _queued(slots, stream):
+        k = torch.empty(shape, dtype=dtype, device=cache.device) if k is None else k
+        v = torch.empty(shape, dtype=dtype, device=cache.device) if v is None else v
+        strides = (n_kv * hd, hd) if kv_layout == "shd" else (hd, rows * hd)
+        A.call("tlb_kv8_read", cache, _at(slots, (rows,), torch.int64, cache.device, "slots"), rows, code,
+               _at(k, shape, dtype, cache.device, "k"), _at(v, shape, dtype, cache.device, "v"), *strides, _stream(stream))
+    return k, v
+
+
+def kv8_attn_workspace(cache, n_seq, n_heads, max_len, grad=False):
+    """A workspace tensor, its status block zeroed, for kv8_attn_forward and, with grad, kv8_attn_backward."""
+    n = A.load().tlb_kv8_attn_workspace_bytes(cache, int(n_seq), int(n_heads), int(max_len), 1 if grad else 0)
+    return _status_cleared(int(n), cache.device)
+
+
+def _kv8_over(cache, q, pages, lengths):
+    if q.dim() != 3 or q.shape[2] != cache.head_dim:
+        raise ValueError("q [n_seq, n_heads, %d] expected, got %s" % (cache.head_dim, tuple(q.shape)))
+    n_seq, n_heads = q.shape[:2]
+    if pages.dim() != 2 or pages.shape[0] != n_seq:
+        raise ValueError("pages [%d, max_pages] expected, got %s" % (n_seq, tuple(pages.shape)))
+    return (n_seq, n_heads, _xent_code(q.dtype, "q"), _at(q, None, q.dtype, cache.device, "q"),
+            _at(pages, None, torch.int32, cache.device, "pages"), pages.shape[1],
+            _at(lengths, (n_seq,), torch.int32, cache.device, "lengths"))
+
+
+def kv8_attn_forward(cache, q, pages, page, lengths, max_len, scale=None, ctx=None, lse=None, ws=None, stream=None):
+    """Attention of one query row q [n_seq, n_heads, head_dim] for each sequence over the 8-bit cache: (ctx, lse).
+    Key j < lengths[b] (int32 [n_seq]) of sequence b is in slot pages[b, j // page] * page + j % page (pages int32
+    [n_seq, max_pages]); max_len is at least the longest length; scale 1 / sqrt(head_dim) unless given.
+    Without ws the call makes one of its own, which workspace_status() without one looks after."""
+    n_seq, n_heads, code, at_q, at_pages, max_pages, at_lengths = _kv8_over(cache, q, pages, lengths)
+    dev = cache.device
+    with _queued(q, stream):
+        ctx = torch.empty_like(q) if ctx is None else ctx
+        lse = torch.empty(n_seq, n_heads, dtype=torch.float32, device=dev) if lse is None else lse
+        own = ws is None
+        if own:
+            ws = kv8_attn_workspace(cache, n_seq, n_heads, max_len)
+        A.call("tlb_kv8_attn_forward", cache, at_pages, max_pages, int(page), at_lengths, n_seq, int(max_len), n_heads,
+               1.0 / math.sqrt(cache.head_dim) if scale is None else float(scale), code, at_q,
+               _at(ctx, q.shape, q.dtype, dev, "ctx"), _at(lse, (n_seq, n_heads), torch.float32, dev, "lse"),
+               _at(ws, None, torch.uint8, dev, "ws"), ws.numel(), _stream(stream))
+        if own:
+            _keep_status(ws)
+    return ctx, lse
+
+
+def kv8_attn_backward(cache, q, pages, page, lengths, max_len, lse, d_ctx, scale=None, d_q=None, d_k=None, d_v=None, ws=None,
+                      stream=None):
+    """Gradient of kv8_attn_forward() for d_ctx: (d_q, d_k, d_v) in q's dtype, d_k and d_v [n_seq, n_kv_heads, head_dim]
+    of each sequence's newest key and value.  lse as kv8_attn_forward returned it; ws as there."""
+    n_seq, n_heads, code, at_q, at_pages, max_pages, at_lengths = _kv8_over(cache, q, pages, lengths)
+    dev, newest = cache.device, (n_seq, cache.n_kv_heads, cache.head_dim)
+    with _queued(q, stream):
+        d_q = torch.empty_like(q) if d_q is None else d_q
+        d_k = torch.empty(newest, dtype=q.dtype, device=dev) if d_k is None else d_k
+        d_v = torch.empty(newest, dtype=q.dtype, device=dev) if d_v is None else d_v
+        own = ws is None
+        if own:
+            ws = kv8_attn_workspace(cache, n_seq, n_heads, max_len, grad=True)
+        A.call("tlb_kv8_attn_backward", cache, at_pages, max_pages, int(page), at_lengths, n_seq, int(max_len), n_heads,
+               1.0 / math.sqrt(cache.head_dim) if scale is None else float(scale), code, at_q,
+               _at(lse, (n_seq, n_heads), torch.float32, dev, "lse"), _at(d_ctx, q.shape, q.dtype, dev, "d_ctx"),
+               _at(d_q, q.shape, q.dtype, dev, "d_q"), _at(d_k, newest, q.dtype, dev, "d_k"),
+               _at(d_v, newest, q.dtype, dev, "d_v"), _at(ws, None, torch.uint8, dev, "ws"), ws.numel(), _stream(stream))
+        if own:
+            _keep_status(ws)
+    return d_q, d_k, d_v
+
+
 # ------------------------------------------------------------------ layer pieces
 
 def layer_cfg(dim, ffn_dim, n_heads, n_kv_heads, head_dim, rank, lora_alpha, act="relu2_mul",

@@ -1,0 +1,158 @@
+// Quantising float matrices to e4m3 in blocks of 128 columns.
+#include "common.cuh"
+#include "fp8.cuh"
+
+namespace tlb {
+
+namespace {
+
+// Blocks of 1 x 128: a warp takes kRowBlocks blocks at a time, whose loads are all issued before the
+// first is used; a lane holds four columns of each.  Bound by memory: 5 (float32) or 3 bytes a value.
+constexpr int kRowBlocks = 4;
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) quantize_rows_kernel(const T *__restrict__ x, int64_t cols, int64_t nblk,
+                                                            int64_t items, uint8_t *__restrict__ q,
+                                                            float *__restrict__ scales) {
+    const int lane = threadIdx.x & 31;
+    const int64_t warps = int64_t(gridDim.x) * (blockDim.x >> 5);
+    for (int64_t i0 = (int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5)) * kRowBlocks; i0 < items;
+         i0 += warps * kRowBlocks) {
+        float v[kRowBlocks][4];
+        int64_t at[kRowBlocks];             // element of this lane's first column
+        int left[kRowBlocks];               // columns of the block, 0 past the last
+#pragma unroll
+        for (int u = 0; u < kRowBlocks; ++u) {
+            const int64_t i = i0 + u;
+            const int64_t row = cols == nblk * kFp8Block ? 0 : i / nblk;   // whole blocks: i * 128 is the place
+            const int64_t blk = i - row * nblk;
+            at[u] = row * cols + blk * kFp8Block;
+            left[u] = i < items ? int(min(int64_t(kFp8Block), cols == nblk * kFp8Block ? kFp8Block : cols - blk * kFp8Block)) : 0;
+            if (VEC) {                      // a lane's four columns are there or not (cols % 4 == 0)
+                const float4 f = lane * 4 < left[u] ? load_float4(x + at[u] + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+                v[u][0] = f.x; v[u][1] = f.y; v[u][2] = f.z; v[u][3] = f.w;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) v[u][k] = lane + 32 * k < left[u] ? load_float(x + at[u] + lane + 32 * k) : 0.f;
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kRowBlocks; ++u) {
+            uint32_t top = 0;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) top = max(top, magnitude(v[u][k]));
+            top = __reduce_max_sync(0xffffffffu, top);
+            float inv;
+            const float s = block_scale(top, inv);
+            const uint32_t y = to_e4m3x4(v[u][0] * inv, v[u][1] * inv, v[u][2] * inv, v[u][3] * inv);
+            if (VEC) {
+                if (lane * 4 < left[u]) *reinterpret_cast<uint32_t *>(q + at[u] + lane * 4) = y;
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (lane + 32 * k < left[u]) q[at[u] + lane + 32 * k] = uint8_t(y >> (8 * k));
+            }
+            if (lane == 0 && left[u] > 0) scales[i0 + u] = s;
+        }
+    }
+}
+
+// Blocks of 128 x 128: a CTA of 256 threads holds one in registers, 64 values a thread.
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(256) quantize_tiles_kernel(const T *__restrict__ x, int64_t rows, int64_t cols,
+                                                             int64_t nblk, uint8_t *__restrict__ q,
+                                                             float *__restrict__ scales) {
+    __shared__ uint32_t tops[8];
+    const int64_t rb = blockIdx.x / nblk, cb = blockIdx.x - rb * nblk;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t r0 = rb * kFp8Block, c0 = cb * kFp8Block;
+    const int nc = int(min(int64_t(kFp8Block), cols - c0));
+    float v[16][4];
+    uint32_t top = 0;
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {                       // a warp's row u: eight rows apart
+        const int64_t row = r0 + u * 8 + warp;
+        const T *p = x + row * cols + c0;
+        if (VEC) {
+            const float4 f = row < rows && lane * 4 < nc ? load_float4(p + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[u][0] = f.x; v[u][1] = f.y; v[u][2] = f.z; v[u][3] = f.w;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[u][k] = row < rows && lane + 32 * k < nc ? load_float(p + lane + 32 * k) : 0.f;
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < 16; ++u)
+#pragma unroll
+        for (int k = 0; k < 4; ++k) top = max(top, magnitude(v[u][k]));
+    top = __reduce_max_sync(0xffffffffu, top);
+    if (lane == 0) tops[warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < 8; ++w) top = max(top, tops[w]);
+    float inv;
+    const float s = block_scale(top, inv);
+    if (threadIdx.x == 0) scales[blockIdx.x] = s;
+#pragma unroll
+    for (int u = 0; u < 16; ++u) {
+        const int64_t row = r0 + u * 8 + warp;
+        if (row >= rows) break;
+        uint8_t *p = q + row * cols + c0;
+        const uint32_t y = to_e4m3x4(v[u][0] * inv, v[u][1] * inv, v[u][2] * inv, v[u][3] * inv);
+        if (VEC) {
+            if (lane * 4 < nc) *reinterpret_cast<uint32_t *>(p + lane * 4) = y;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (lane + 32 * k < nc) p[lane + 32 * k] = uint8_t(y >> (8 * k));
+        }
+    }
+}
+
+template <typename T>
+int quantize_launch(const T *x, int64_t rows, int64_t cols, int block_rows, uint8_t *q, float *scales, cudaStream_t st) {
+    const int64_t nblk = ceil_div(cols, kFp8Block);
+    // four columns a lane: every row starts where four elements may be loaded and four bytes stored
+    const bool vec = cols % 4 == 0 && (reinterpret_cast<uintptr_t>(x) % (4 * sizeof(T))) == 0 &&
+                     (reinterpret_cast<uintptr_t>(q) & 3) == 0;
+    if (block_rows == 1) {
+        const int64_t items = rows * nblk;
+        const unsigned grid = stream_grid(ceil_div(items, kRowBlocks) * 32, 256);
+        if (vec) quantize_rows_kernel<T, true><<<grid, 256, 0, st>>>(x, cols, nblk, items, q, scales);
+        else quantize_rows_kernel<T, false><<<grid, 256, 0, st>>>(x, cols, nblk, items, q, scales);
+        return check_launch("fp8_quantize_rows");
+    }
+    const int64_t tiles = ceil_div(rows, kFp8Block) * nblk;
+    TLB_REQUIRE(tiles < (int64_t(1) << 31), TLB_EUNSUPPORTED, "fp8_quantize: more than 2^31 blocks of 128 x 128");
+    if (vec) quantize_tiles_kernel<T, true><<<unsigned(tiles), 256, 0, st>>>(x, rows, cols, nblk, q, scales);
+    else quantize_tiles_kernel<T, false><<<unsigned(tiles), 256, 0, st>>>(x, rows, cols, nblk, q, scales);
+    return check_launch("fp8_quantize_tiles");
+}
+
+}  // namespace
+
+}  // namespace tlb
+
+using namespace tlb;
+
+extern "C" {
+
+int tlb_fp8_quantize(int32_t type, const void *x, int64_t rows, int64_t cols, int32_t block_rows, uint8_t *q,
+                     float *scales, void *stream) {
+    clear_error();
+    TLB_REQUIRE(type == TLB_W_F32 || type == TLB_W_BF16, TLB_EINVAL, "fp8_quantize: type %d is neither f32 nor bf16", type);
+    TLB_REQUIRE(block_rows == 1 || block_rows == kFp8Block, TLB_EINVAL, "fp8_quantize: block_rows must be 1 or 128");
+    TLB_REQUIRE(rows >= 0 && cols >= 0, TLB_EINVAL, "fp8_quantize: negative size");
+    TLB_REQUIRE(rows <= (int64_t(1) << 40) && cols <= (int64_t(1) << 40) && (rows == 0 || cols <= (int64_t(1) << 48) / rows),
+                TLB_EUNSUPPORTED, "fp8_quantize: more than 2^48 values");
+    if (rows == 0 || cols == 0) return TLB_OK;
+    TLB_REQUIRE(x && q && scales, TLB_EINVAL, "fp8_quantize: null pointer");
+    TLB_REQUIRE((reinterpret_cast<uintptr_t>(x) & (type == TLB_W_F32 ? 3 : 1)) == 0 &&
+                    (reinterpret_cast<uintptr_t>(scales) & 3) == 0,
+                TLB_EINVAL, "fp8_quantize: x and scales must be aligned to their elements");
+    if (type == TLB_W_F32)
+        return quantize_launch(static_cast<const float *>(x), rows, cols, block_rows, q, scales, as_stream(stream));
+    return quantize_launch(static_cast<const __nv_bfloat16 *>(x), rows, cols, block_rows, q, scales, as_stream(stream));
+}
+
+}  // extern "C"
