@@ -1,42 +1,663 @@
 // The transposed-weight product of operands in 8-bit blocks:
 //   dX[s, i] (+)= sum_kb dy_scales[s, kb] w_scales[i / 128, kb] sum_{o in block kb} dY[s, o] W[i, o]
+// with both operands K-major e4m3.  The scales change with every 128 columns, so the tensor cores sum 128
+// columns at a time (exact products, float32 sums) and each of these sums is multiplied by its two scales
+// and added up in registers.
+//
+// More than kFewRows rows: tcgen05 (kind::f8f6f4), persistent CTA pairs on 256 x 256 super-tiles:
+//   warp 0      TMA producer: 128 x 128 bytes of dY and of W a stage and CTA (128-byte swizzle: one scale
+//               block is one swizzle row)
+//   warp 1      one thread of the even CTA issues four MMAs (M = N = 256, K = 32) a k block into one of two
+//               accumulators of 256 columns, all of the tensor memory
+//   warps 2..9  a thread has one row and 128 of the columns: it keeps their sums in 128 registers and
+//               adds each k block's accumulator times its scale while the next one is multiplied.
+// Per CTA and k block the MMAs take 512 cycles, the sums 128 float32 additions a thread on two warps a
+// scheduler (256 issue slots as scalars, 128 as pairs) and 128 KB read from tensor memory.
+// Tiles that do not fill a last wave are shared by CTA pairs along K; their parts go to the workspace and
+// are joined in a fixed order by a second kernel.
+//
+// Up to kFewRows rows: bound by the read of W.  A warp multiplies 16 rows of W by up to 8 rows of dY an mma.sync
+// (m16n8k32), straight from global memory: the 128 columns of a block may be summed in any order, so a lane's
+// 16 consecutive bytes of W and of dY serve as the operands' registers as they are.  The warps of a CTA, and
+// the CTAs of a cluster, share the columns of 16 rows and add up through shared memory in a fixed order.
+#include <cuda.h>
+
+#include <algorithm>
+#include <cstring>
+
+#include "async.cuh"
 #include "common.cuh"
 #include "fp8.cuh"
+#include "tc.cuh"
 
 namespace tlb {
 
 namespace {
 
-constexpr int kTile = 16;
+constexpr int kFewRows = 32;
+constexpr int64_t kMost = int64_t(1) << 24;
 
-// One output a thread, 16 x 16 outputs a CTA, 16 columns of both operands in shared memory.
-template <typename T>
-__global__ void __launch_bounds__(kTile *kTile) linear_fp8_simple_kernel(
-    const uint8_t *__restrict__ W, const float *__restrict__ ws, const uint8_t *__restrict__ dY, const float *__restrict__ ys,
-    int64_t S, int64_t out, int64_t in, T *__restrict__ dX, int accumulate) {
-    __shared__ float a[kTile][kTile + 1], b[kTile][kTile + 1];
-    const int64_t nblk = (out + kFp8Block - 1) / kFp8Block;
-    const int tx = threadIdx.x % kTile, ty = threadIdx.x / kTile;
-    const int64_t i0 = int64_t(blockIdx.x) * kTile, s0 = int64_t(blockIdx.y) * kTile;
-    float sum = 0.f;
-    for (int64_t kb = 0; kb < nblk; ++kb) {
-        float part = 0.f;
-        for (int64_t o = kb * kFp8Block; o < min(out, (kb + 1) * kFp8Block); o += kTile) {
-            const bool in_k = o + tx < out;
-            a[ty][tx] = in_k && s0 + ty < S ? e4m3x2_to_float2(dY[(s0 + ty) * out + o + tx]).x : 0.f;
-            b[ty][tx] = in_k && i0 + ty < in ? e4m3x2_to_float2(W[(i0 + ty) * out + o + tx]).x : 0.f;
-            __syncthreads();
-#pragma unroll
-            for (int k = 0; k < kTile; ++k) part = fmaf(a[ty][k], b[tx][k], part);
-            __syncthreads();
+// ------------------------------------------------------------------ results
+
+// Four consecutive values of a row of dX (col % 4 == 0), the last ones past `cols` left out; WIDE: cols % 4 == 0.
+template <typename T, bool WIDE>
+__device__ __forceinline__ void put4(T *p, int col, int cols, float4 y, bool add) {
+    if (WIDE) {
+        if (col >= cols) return;
+        if (add) {
+            const float4 c = load_float4(p);
+            y.x += c.x; y.y += c.y; y.z += c.z; y.w += c.w;
         }
-        if (s0 + ty < S && i0 + tx < in)
-            sum = fmaf(part, ys[(s0 + ty) * nblk + kb] * ws[(i0 + tx) / kFp8Block * nblk + kb], sum);
+        store_float4(p, y);
+        return;
     }
-    if (s0 + ty < S && i0 + tx < in) {
-        T *p = dX + (s0 + ty) * in + i0 + tx;
-        store_float(p, accumulate ? float(*p) + sum : sum);
+    const float v[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (col + k < cols) store_float(p + k, add ? v[k] + load_float(p + k) : v[k]);
+}
+
+// ------------------------------------------------------------------ few rows
+
+constexpr int kRowWarps = 8;
+
+__device__ __forceinline__ void mma_e4m3(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+struct RowsParams {
+    const uint8_t *W, *dY;
+    const float *ws, *ys;
+    int64_t ld_w, ld_y;          // bytes from row to row, multiples of 16
+    int S, out, in, nblk;
+    int add;
+    void *dX;
+};
+
+// 16 bytes of a row at column `col`, zeros past its end (the rows are padded to 16 bytes)
+__device__ __forceinline__ uint4 piece(const uint8_t *row, int col, int out, bool there) {
+    return there && col < out ? ld_stream_u4(row + col) : make_uint4(0, 0, 0, 0);
+}
+
+// NT: n tiles of 8 rows of dY.
+template <typename T, int NT>
+__global__ void __launch_bounds__(kRowWarps * 32) linear_fp8_rows_kernel(const RowsParams p) {
+    __shared__ float part[kRowWarps][16][8 * NT + 1];
+    __shared__ float mine[16][8 * NT];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    uint32_t rank, size;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm("mov.u32 %0, %%cluster_nctaid.x;" : "=r"(size));
+    const int i0 = int(blockIdx.x / size) * 16;
+    const int u = int(rank) * kRowWarps + warp, U = int(size) * kRowWarps;
+    const int kb0 = int(int64_t(p.nblk) * u / U), kb1 = int(int64_t(p.nblk) * (u + 1) / U);
+    const uint8_t *w0 = p.W + int64_t(min(i0 + g, p.in - 1)) * p.ld_w, *w1 = p.W + int64_t(min(i0 + g + 8, p.in - 1)) * p.ld_w;
+    const bool r0 = i0 + g < p.in, r1 = i0 + g + 8 < p.in;
+    const float *wsc = p.ws + int64_t(i0 / kFp8Block) * p.nblk;
+    float acc[NT][4] = {};
+#pragma unroll 2
+    for (int kb = kb0; kb < kb1; ++kb) {
+        const int c = kb * kFp8Block + t * 16;
+        const uint4 a0 = piece(w0, c, p.out, r0), a1 = piece(w1, c, p.out, r1);
+        const uint4 a2 = piece(w0, c + 64, p.out, r0), a3 = piece(w1, c + 64, p.out, r1);
+        const float sw = __ldg(wsc + kb);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int s = n * 8 + g;
+            const bool there = s < p.S;
+            const uint8_t *y = p.dY + int64_t(there ? s : 0) * p.ld_y;
+            uint4 b0 = make_uint4(0, 0, 0, 0), b1 = b0;
+            if (there && c < p.out) b0 = __ldg(reinterpret_cast<const uint4 *>(y + c));
+            if (there && c + 64 < p.out) b1 = __ldg(reinterpret_cast<const uint4 *>(y + c + 64));
+            float d[4] = {0.f, 0.f, 0.f, 0.f};
+            mma_e4m3(d, a0.x, a1.x, a0.y, a1.y, b0.x, b0.y);
+            mma_e4m3(d, a0.z, a1.z, a0.w, a1.w, b0.z, b0.w);
+            mma_e4m3(d, a2.x, a3.x, a2.y, a3.y, b1.x, b1.y);
+            mma_e4m3(d, a2.z, a3.z, a2.w, a3.w, b1.z, b1.w);
+            const int s0 = n * 8 + 2 * t;
+            const float f0 = s0 < p.S ? sw * __ldg(p.ys + int64_t(s0) * p.nblk + kb) : 0.f;
+            const float f1 = s0 + 1 < p.S ? sw * __ldg(p.ys + int64_t(s0 + 1) * p.nblk + kb) : 0.f;
+            acc[n][0] = fmaf(d[0], f0, acc[n][0]);
+            acc[n][1] = fmaf(d[1], f1, acc[n][1]);
+            acc[n][2] = fmaf(d[2], f0, acc[n][2]);
+            acc[n][3] = fmaf(d[3], f1, acc[n][3]);
+        }
     }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        part[warp][g][n * 8 + 2 * t] = acc[n][0];
+        part[warp][g][n * 8 + 2 * t + 1] = acc[n][1];
+        part[warp][g + 8][n * 8 + 2 * t] = acc[n][2];
+        part[warp][g + 8][n * 8 + 2 * t + 1] = acc[n][3];
+    }
+    __syncthreads();
+    for (int e = threadIdx.x; e < 16 * 8 * NT; e += kRowWarps * 32) {
+        const int r = e & 15, s = e >> 4;                     // consecutive threads: consecutive columns of dX
+        float y = 0.f;
+#pragma unroll
+        for (int w = 0; w < kRowWarps; ++w) y += part[w][r][s];
+        mine[r][s] = y;
+    }
+    if (size > 1) cluster_sync();
+    else __syncthreads();
+    if (rank == 0) {
+        for (int e = threadIdx.x; e < 16 * 8 * NT; e += kRowWarps * 32) {
+            const int r = e & 15, s = e >> 4;
+            float y = mine[r][s];
+            for (uint32_t c = 1; c < size; ++c) {
+                float x;
+                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(cluster_addr(&mine[r][s], c)));
+                y += x;
+            }
+            if (s < p.S && i0 + r < p.in) {
+                T *o = static_cast<T *>(p.dX) + int64_t(s) * p.in + i0 + r;
+                store_float(o, p.add ? y + load_float(o) : y);
+            }
+        }
+    }
+    if (size > 1) cluster_sync();                             // no CTA leaves while its sums are read
+}
+
+template <typename T, int NT>
+int rows_launch(const RowsParams &p, cudaStream_t st) {
+    // A CTA takes 16 rows of W; clusters of up to eight share their columns until there are four CTAs an SM, each
+    // warp having a block of 128 columns at least.
+    const int64_t groups = ceil_div(p.in, 16);
+    int c = 1;
+    while (c < 8 && groups * c < int64_t(num_sms()) * 4 && p.nblk >= 2 * c * kRowWarps) c *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(groups * c));
+    cfg.blockDim = dim3(kRowWarps * 32);
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = unsigned(c);
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    TLB_CUDA(cudaLaunchKernelEx(&cfg, linear_fp8_rows_kernel<T, NT>, p));
+    return check_launch("linear_fp8_rows");
+}
+
+// ------------------------------------------------------------------ tcgen05
+
+constexpr int kTM = 256, kTN = 256;      // super-tile of a CTA pair
+constexpr int kHalf = 128;               // rows of dY, and of W, that one CTA stages
+constexpr int kStageBytes = 2 * kHalf * kFp8Block;
+constexpr int kStages = 6;
+constexpr int kThreads = 320;            // producer, MMA, 8 epilogue warps
+constexpr int kEpiWarps = 8;
+constexpr int kTcSmem = kStages * kStageBytes + kEpiWarps * 32 * 33 * 4 + 1024;
+static_assert(kTcSmem <= 227 * 1024, "shared memory of one CTA");
+
+struct TcParams {
+    CUtensorMap y, w;                    // e4m3 [S, out] and [in, out], boxes of 128 x 128
+    const float *ys, *ws;
+    int M, N, KB;
+    int add;
+    void *dX;
+    float *partial;                      // [pairs][2 CTAs][2 slots][128][256]
+    // Pair c first does its share [work c / sk_pairs, work (c + 1) / sk_pairs) of the (tile, k block) units of
+    // the last sk_tiles tiles (c < sk_pairs), cut at the tiles' ends, then the whole tiles c, c + pairs, ...
+    int tiles, sk_tiles, sk_pairs, pairs;
+    uint32_t *status;
+};
+
+__host__ __device__ __forceinline__ int64_t share(int64_t work, int pairs, int c) { return work * c / pairs; }
+
+// The segments of one pair, in order: tile, rows, columns, k blocks [kb0, kb1).  Few registers: the threads
+// that add up have none to spare.
+struct Walk {
+    int at, end, begin;                  // units of the shared tiles still to do (at most 75 tiles of 2^17 k blocks)
+    int whole;                           // next whole tile
+    __device__ __forceinline__ Walk(const TcParams &p, int c) {
+        const int64_t work = int64_t(p.sk_tiles) * p.KB;
+        begin = at = c < p.sk_pairs ? int(share(work, p.sk_pairs, c)) : 0;
+        end = c < p.sk_pairs ? int(share(work, p.sk_pairs, c + 1)) : 0;
+        whole = c;
+    }
+    // false when there is none left; slot: where a part of a tile goes
+    __device__ __forceinline__ bool next(const TcParams &p, int &m, int &n, int &kb0, int &kb1, int &slot) {
+        int tile = p.tiles - p.sk_tiles;
+        if (at < end) {
+            const int t = at / p.KB;
+            slot = at == begin ? 0 : 1;
+            kb0 = at - t * p.KB;
+            kb1 = min(p.KB, end - t * p.KB);
+            at += kb1 - kb0;
+            tile += t;
+        } else {
+            if (whole >= tile) return false;
+            tile = whole;
+            whole += p.pairs;
+            kb0 = 0;
+            kb1 = p.KB;
+            slot = 0;
+        }
+        const int tiles_m = (p.M + kTM - 1) / kTM;
+        m = (tile % tiles_m) * kTM;
+        n = (tile / tiles_m) * kTN;
+        return true;
+    }
+};
+
+__device__ __forceinline__ void mma_e4m3_pair(uint32_t tmem_d, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(tmem_d),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 32 TMEM lanes x 8 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t *v) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+                 : "r"(taddr));
+}
+
+// a += v * s on a pair of floats
+__device__ __forceinline__ void fma2(uint64_t &a, uint32_t v0, uint32_t v1, uint64_t s) {
+    asm volatile("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}" : "+l"(a) : "r"(v0), "r"(v1), "l"(s));
+}
+
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(kThreads, 1) linear_fp8_tc_kernel(const __grid_constant__ TcParams p) {
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    __shared__ uint64_t full[kStages], empty[kStages], accfull[2], accempty[2], done;
+    __shared__ uint32_t tmem_base;
+    __shared__ int s_abort, s_issued, s_consumed;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = int(cluster_rank()), pair = int(blockIdx.x >> 1);
+    const bool leader = rank == 0;
+
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        s_issued = s_consumed = 0;
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(&accfull[b], 1);
+            mbar_init(&accempty[b], 2 * kEpiWarps);          // both CTAs' warps
+        }
+        mbar_init(&done, 1);
+    }
+    if (warp == 1) {
+        tmem_alloc_pair(&tmem_base, 512);
+        tmem_relinquish_pair();
+    }
+    fence_mbar_init();
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base;
+    pdl_trigger();                                            // the join may be scheduled
+    pdl_wait();                                               // padded copies of the operands
+
+    Walk walk(p, pair);
+    int m, n, kb0, kb1, slot;
+    if (warp == 0) {
+        // ------------------------------------------------ TMA producer
+        if (lane == 0) {
+            int g = 0;
+            bool ok = true;
+            while (ok && walk.next(p, m, n, kb0, kb1, slot)) {
+                for (int kb = kb0; kb < kb1; ++kb, ++g) {
+                    const int s = g % kStages;
+                    if (g >= kStages && !mbar_wait(&empty[s], ((g / kStages) - 1) & 1, p.status, 40u)) {
+                        ok = false;
+                        break;
+                    }
+                    uint8_t *sa = smem + s * kStageBytes;
+                    if (leader) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);   // both CTAs' copies count here
+                    const uint32_t fb = cluster_addr(&full[s], 0);
+                    tma_load_2d_pair(sa, &p.y, kb * kFp8Block, m + rank * kHalf, fb);
+                    tma_load_2d_pair(sa + kStageBytes / 2, &p.w, kb * kFp8Block, n + rank * kHalf, fb);
+                    s_issued = g + 1;
+                }
+            }
+            if (!ok) s_abort = 1;
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------ MMA issuer: the accumulators alternate with the k blocks
+        if (lane == 0 && leader) {
+            // D float32, A and B e4m3, both K-major, M = N = 256
+            const uint32_t idesc = (1u << 4) | (uint32_t(kTN >> 3) << 17) | (uint32_t(kTM >> 4) << 24);
+            int g = 0;
+            bool ok = true;
+            while (ok && walk.next(p, m, n, kb0, kb1, slot)) {
+                for (int kb = kb0; kb < kb1; ++kb, ++g) {
+                    const int s = g % kStages, b = g & 1;
+                    if (g >= 2 && !mbar_wait(&accempty[b], ((g >> 1) - 1) & 1, p.status, 43u)) { ok = false; break; }
+                    if (!mbar_wait(&full[s], (g / kStages) & 1, p.status, 41u)) { ok = false; break; }
+                    tc_fence_after();
+                    const uint8_t *sa = smem + s * kStageBytes;
+                    const uint64_t ad = sw128_desc(sa), bd = sw128_desc(sa + kStageBytes / 2);
+#pragma unroll
+                    for (int k = 0; k < kFp8Block / 32; ++k)  // 32 bytes = 2 descriptor units
+                        mma_e4m3_pair(tmem + uint32_t(b * kTN), ad + 2 * k, bd + 2 * k, idesc, k > 0 ? 1u : 0u);
+                    mma_commit_pair(&empty[s], 3);            // frees the stage in both CTAs
+                    mma_commit_pair(&accfull[b], 3);
+                    s_consumed = g + 1;
+                }
+            }
+            if (!ok) s_abort = 1;
+            mma_commit_pair(&done, 1);
+            mbar_wait(&done, 0, nullptr, 0u);
+        }
+    } else {
+        // ------------------------------------------------ sums in registers (warps 2..9)
+        const int q = warp & 3, half = (warp - 2) >> 2;       // this warp's TMEM lanes and columns
+        float *blk = reinterpret_cast<float *>(smem + kStages * kStageBytes) + (warp - 2) * 32 * 33;
+        const uint32_t tbase = tmem + (uint32_t(q * 32) << 16) + uint32_t(half * 128);
+        int g = 0;
+        bool ok = true;
+        while (ok && walk.next(p, m, n, kb0, kb1, slot)) {
+            const int rows0 = m + rank * kHalf + q * 32, cols0 = n + half * 128;
+            const bool any = rows0 < p.M && cols0 < p.N;      // the warp has results to write
+            const int yrow = min(rows0 + lane, p.M - 1), wrow = any ? cols0 / kFp8Block : 0;
+            auto scale_of = [&](const float *scales, int row, int kb) { return __ldg(scales + int64_t(row) * p.KB + kb); };
+            uint64_t acc[64];
+#pragma unroll
+            for (int c = 0; c < 64; ++c) acc[c] = 0;
+            float sy = scale_of(p.ys, yrow, kb0), sw = scale_of(p.ws, wrow, kb0);
+            for (int kb = kb0; kb < kb1; ++kb, ++g) {
+                const int b = g & 1;
+                const float s = sy * sw;
+                uint64_t s2;
+                asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
+                if (kb + 1 < kb1) {
+                    sy = scale_of(p.ys, yrow, kb + 1);
+                    sw = scale_of(p.ws, wrow, kb + 1);
+                }
+                if (!mbar_wait(&accfull[b], (g >> 1) & 1, p.status, 42u)) { ok = false; break; }
+                tc_fence_after();
+                if (any) {
+                    // eight columns on their way while the eight before are added
+                    uint32_t v[2][16];
+                    tmem_ld16(tbase + uint32_t(b * kTN), v[0]);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        tmem_wait_ld();
+                        if (j < 7) tmem_ld16(tbase + uint32_t(b * kTN + (j + 1) * 16), v[(j + 1) & 1]);
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) fma2(acc[j * 8 + c], v[j & 1][2 * c], v[j & 1][2 * c + 1], s2);
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(cluster_addr(&accempty[b], 0));
+            }
+            if (!ok) break;
+            if (!any) continue;
+            // 32 x 32 at a time through shared memory, so that lanes run along columns
+            const bool whole = kb0 == 0 && kb1 == p.KB;
+            const int c4 = (lane & 7) * 4, rl = lane >> 3;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll
+                for (int c = 0; c < 16; ++c) {
+                    uint32_t lo, hi;
+                    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(acc[j * 16 + c]));
+                    blk[lane * 33 + 2 * c] = __uint_as_float(lo);
+                    blk[lane * 33 + 2 * c + 1] = __uint_as_float(hi);
+                }
+                __syncwarp();
+                const int col = cols0 + j * 32 + c4;
+#pragma unroll 1
+                for (int k = 0; k < 8; ++k) {
+                    const int r = 4 * k + rl;
+                    const float *a = blk + r * 33 + c4;
+                    const float4 y = make_float4(a[0], a[1], a[2], a[3]);
+                    if (rows0 + r >= p.M) continue;
+                    if (whole)
+                        put4<T, WIDE>(static_cast<T *>(p.dX) + int64_t(rows0 + r) * p.N + col, col, p.N, y, p.add != 0);
+                    else
+                        *reinterpret_cast<float4 *>(p.partial + ((int64_t(blockIdx.x) * 2 + slot) * kHalf + q * 32 + r) * kTN +
+                                                    half * 128 + j * 32 + c4) = y;
+                }
+                __syncwarp();
+            }
+        }
+        if (!ok) s_abort = 1;
+    }
+    // wind down: the MMA thread waited for its last commit; after an abort also wait (bounded) for the copies
+    // that were issued and never consumed
+    tc_fence_before();
+    __syncthreads();
+    if (s_abort && threadIdx.x == 0 && leader) {
+        for (int g = s_consumed; g < s_issued; ++g) mbar_wait(&full[g % kStages], (g / kStages) & 1, nullptr, 0u);
+    }
+    __syncthreads();
+    cluster_sync();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc_pair(tmem, 512);
+    }
+}
+
+// Joins the parts of the shared tiles in the pairs' order.  Block (tile, y) does rows y, y + gridDim.y, ...
+template <typename T, bool WIDE>
+__global__ void __launch_bounds__(256) linear_fp8_join_kernel(const __grid_constant__ TcParams p) {
+    const int tiles_m = (p.M + kTM - 1) / kTM, tile = p.tiles - p.sk_tiles + int(blockIdx.x);
+    const int m = (tile % tiles_m) * kTM, n = (tile / tiles_m) * kTN;
+    const int64_t work = int64_t(p.sk_tiles) * p.KB, ta = int64_t(blockIdx.x) * p.KB, tb = ta + p.KB;
+    int c0 = int(ta * p.sk_pairs / work);                     // the pair whose share holds unit ta
+    while (share(work, p.sk_pairs, c0 + 1) <= ta) ++c0;
+    int c1 = c0;
+    while (share(work, p.sk_pairs, c1 + 1) < tb) ++c1;
+    pdl_wait();                                               // before any block leaves: what comes next waits for this kernel
+    if (c1 == c0) return;                                     // done whole by one pair
+    const int s0 = share(work, p.sk_pairs, c0) < ta ? 1 : 0;  // that pair began in the tile before
+    const int c4 = (threadIdx.x & 63) * 4;
+    for (int r = int(blockIdx.y) * 4 + (threadIdx.x >> 6); r < min(kTM, p.M - m); r += int(gridDim.y) * 4) {
+        const int h = r / kHalf, lr = r % kHalf;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int c = c0; c <= c1; c += 8) {                   // up to eight loads in flight
+            float4 v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (c + u <= c1)
+                    v[u] = __ldcg(reinterpret_cast<const float4 *>(
+                        p.partial + ((int64_t(2 * (c + u) + h) * 2 + (c + u == c0 ? s0 : 0)) * kHalf + lr) * kTN + c4));
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (c + u <= c1) {
+                    y.x += v[u].x; y.y += v[u].y; y.z += v[u].z; y.w += v[u].w;
+                }
+        }
+        if (n + c4 < p.N)
+            put4<T, WIDE>(static_cast<T *>(p.dX) + int64_t(m + r) * p.N + n + c4, n + c4, p.N, y, p.add != 0);
+    }
+}
+
+// How the tiles are spread over the CTA pairs.
+struct Plan {
+    int tiles, sk_tiles, sk_pairs, pairs;
+};
+
+Plan plan_of(int64_t M, int64_t N, int64_t KB) {
+    const int P = std::max(1, num_sms() / 2);
+    const int64_t tiles = ceil_div(M, kTM) * ceil_div(N, kTN);
+    Plan pl{int(tiles), 0, 0, int(std::min<int64_t>(tiles, P))};
+    const int rest = int(tiles % P);
+    if (rest == 0) return pl;
+    // The tiles of the last wave: whole on `rest` pairs, or shared by more along K, evenly (a multiple of `rest`) or
+    // by all P.  In k blocks of a pair: a part of a tile costs about kPart more (it is written, and read by the join).
+    constexpr double kPart = 6.0;
+    double best = double(KB);
+    auto consider = [&](int pairs) {
+        if (pairs <= rest || pairs > P) return;
+        const int64_t most = ceil_div(int64_t(rest) * KB, pairs);
+        const double cost = double(most) + kPart * (pairs % rest == 0 ? 1 : 2);
+        if (most >= 1 && cost < best) {
+            best = cost;
+            pl.sk_tiles = rest;
+            pl.sk_pairs = pairs;
+            pl.pairs = tiles > P ? P : pairs;
+        }
+    };
+    for (int s = 2; s * rest <= P && s <= KB; ++s) consider(s * rest);
+    if (int64_t(rest) * KB >= P) consider(P);
+    return pl;
+}
+
+int map_of(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int64_t ld) {
+    EncodeTiled enc = encode_fn();
+    TLB_REQUIRE(enc != nullptr, TLB_ECUDA, "linear_fp8_backward: cuTensorMapEncodeTiled unavailable");
+    const cuuint64_t dims[2] = {cuuint64_t(cols), cuuint64_t(rows)};
+    const cuuint64_t strides[1] = {cuuint64_t(ld)};
+    const cuuint32_t box[2] = {cuuint32_t(kFp8Block), cuuint32_t(kHalf)};
+    const cuuint32_t estr[2] = {1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    TLB_REQUIRE(r == CUDA_SUCCESS, TLB_ECUDA, "linear_fp8_backward: tensor map encoding failed (%d)", int(r));
+    return TLB_OK;
+}
+
+template <typename T, bool WIDE>
+int tc_launch(const TcParams &p, cudaStream_t st) {
+    auto kernel = linear_fp8_tc_kernel<T, WIDE>;
+    TLB_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem));
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(unsigned(2 * p.pairs));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = kTcSmem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 2;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    TLB_CUDA(cudaLaunchKernelEx(&cfg, kernel, p));
+    TLB_TRY(check_launch("linear_fp8_tc"));
+    if (p.sk_tiles == 0) return TLB_OK;
+    const int64_t rows = std::min<int64_t>(kTM, p.M);
+    TLB_CUDA(launch_dependent(linear_fp8_join_kernel<T, WIDE>, dim3(unsigned(p.sk_tiles), unsigned(ceil_div(rows, 4))), dim3(256), 0,
+                              st, p));
+    return check_launch("linear_fp8_join");
+}
+
+// ------------------------------------------------------------------ operands whose rows are not multiples of 16 bytes
+
+// [rows, cols] bytes to rows of ld bytes (a multiple of 16), zeros behind each; a thread writes 16.
+__global__ void __launch_bounds__(256) pad_rows_kernel(const uint8_t *__restrict__ a, int64_t a_rows, uint8_t *__restrict__ a_to,
+                                                       const uint8_t *__restrict__ b, int64_t b_rows,
+                                                       uint8_t *__restrict__ b_to, int64_t cols, int64_t ld) {
+    const int64_t per = ld / 16, n = (a_rows + b_rows) * per;
+    for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += int64_t(gridDim.x) * blockDim.x) {
+        int64_t row = i / per;
+        const int64_t c = (i - row * per) * 16;
+        const bool first = row < a_rows;
+        row = first ? row : row - a_rows;
+        const uint8_t *src = first ? a : b;
+        const int64_t at = row * cols + c, total = (first ? a_rows : b_rows) * cols;
+        uint32_t w[4];
+        if (c + 16 <= cols && (at & ~int64_t(3)) + 20 <= total) {
+            // five aligned words, shifted to the row's own alignment (src is 16-byte aligned)
+            const uint32_t *p = reinterpret_cast<const uint32_t *>(src + (at & ~int64_t(3)));
+            uint32_t v[5];
+#pragma unroll
+            for (int k = 0; k < 5; ++k) v[k] = __ldg(p + k);
+            const uint32_t shift = uint32_t(at & 3) * 8;
+#pragma unroll
+            for (int k = 0; k < 4; ++k) w[k] = __funnelshift_r(v[k], v[k + 1], shift);
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                w[k] = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (c + 4 * k + e < cols) w[k] |= uint32_t(__ldg(src + at + 4 * k + e)) << (8 * e);
+            }
+        }
+        *reinterpret_cast<uint4 *>((first ? a_to : b_to) + row * ld + c) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    pdl_trigger();
+}
+
+// ------------------------------------------------------------------ the call
+
+struct Layout {
+    size_t partial, w, y, bytes;
+};
+
+int64_t padded(int64_t out) { return (out + 15) & ~int64_t(15); }
+
+Layout layout_of(int64_t S, int64_t out, int64_t in) {
+    Layout l{};
+    WsPlan ws;
+    if (S > kFewRows && in > 0 && out > 0) {
+        const Plan pl = plan_of(S, in, ceil_div(out, kFp8Block));
+        l.partial = ws.take(pl.sk_tiles ? size_t(pl.sk_pairs) * 4 * kHalf * kTN * sizeof(float) : 0);
+    }
+    if (out % 16 != 0 && S > 0) {
+        l.w = ws.take(size_t(in) * padded(out));
+        l.y = ws.take(size_t(S) * padded(out));
+    }
+    l.bytes = ws.off;
+    return l;
+}
+
+template <typename T>
+int run(const uint8_t *W, const float *w_scales, const uint8_t *dY, const float *dy_scales, int64_t S, int64_t out,
+        int64_t in, T *dX, bool add, void *ws, cudaStream_t st) {
+    const Layout l = layout_of(S, out, in);
+    int64_t ld = out;
+    if (out % 16 != 0) {
+        ld = padded(out);
+        uint8_t *w = ws_at<uint8_t>(ws, l.w), *y = ws_at<uint8_t>(ws, l.y);
+        pad_rows_kernel<<<stream_grid((in + S) * (ld / 16), 256), 256, 0, st>>>(W, in, w, dY, S, y, out, ld);
+        TLB_TRY(check_launch("linear_fp8_pad"));
+        W = w;
+        dY = y;
+    }
+    const int KB = int(ceil_div(out, kFp8Block));
+    if (S <= kFewRows) {
+        const RowsParams p{W, dY, w_scales, dy_scales, ld, ld, int(S), int(out), int(in), KB, add ? 1 : 0, dX};
+        return S <= 8 ? rows_launch<T, 1>(p, st) : S <= 16 ? rows_launch<T, 2>(p, st) : rows_launch<T, 4>(p, st);
+    }
+    TcParams p;
+    memset(&p, 0, sizeof(p));
+    TLB_TRY(map_of(&p.y, dY, S, out, ld));
+    TLB_TRY(map_of(&p.w, W, in, out, ld));
+    const Plan pl = plan_of(S, in, KB);
+    p.ys = dy_scales;
+    p.ws = w_scales;
+    p.M = int(S);
+    p.N = int(in);
+    p.KB = KB;
+    p.add = add ? 1 : 0;
+    p.dX = dX;
+    p.partial = ws_at<float>(ws, l.partial);
+    p.tiles = pl.tiles;
+    p.sk_tiles = pl.sk_tiles;
+    p.sk_pairs = pl.sk_pairs;
+    p.pairs = pl.pairs;
+    p.status = static_cast<uint32_t *>(ws);
+    return in % 4 == 0 ? tc_launch<T, true>(p, st) : tc_launch<T, false>(p, st);
+}
+
+// Sums of nothing.
+template <typename T>
+__global__ void zero_kernel(T *p, int64_t n) {
+    for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += int64_t(gridDim.x) * blockDim.x) store_float(p + i, 0.f);
+}
+
+template <typename T>
+int zero_launch(T *p, int64_t n, cudaStream_t st) {
+    zero_kernel<<<stream_grid(n, 256), 256, 0, st>>>(p, n);
+    return check_launch("linear_fp8_zero");
 }
 
 }  // namespace
@@ -48,19 +669,17 @@ using namespace tlb;
 extern "C" {
 
 size_t tlb_linear_fp8_workspace_bytes(int64_t S, int64_t out_dim, int64_t in_dim) {
-    const int64_t most = int64_t(1) << 24;
-    if (S < 0 || out_dim < 0 || in_dim < 0 || S > most || out_dim > most || in_dim > most) return 0;
-    return kStatusBytes;
+    if (S < 0 || out_dim < 0 || in_dim < 0 || S > kMost || out_dim > kMost || in_dim > kMost) return 0;
+    return layout_of(S, out_dim, in_dim).bytes;
 }
 
 int tlb_linear_fp8_backward(const uint8_t *W, const float *w_scales, const uint8_t *dY, const float *dy_scales, int64_t S,
                             int64_t out_dim, int64_t in_dim, int32_t type, void *dX, int32_t accumulate, void *ws,
                             size_t ws_bytes, void *stream) {
     clear_error();
-    const int64_t most = int64_t(1) << 24;
     TLB_REQUIRE(type == TLB_W_F32 || type == TLB_W_BF16, TLB_EINVAL, "linear_fp8_backward: type %d is neither f32 nor bf16", type);
     TLB_REQUIRE(S >= 0 && out_dim >= 0 && in_dim >= 0, TLB_EINVAL, "linear_fp8_backward: negative size");
-    TLB_REQUIRE(S <= most && out_dim <= most && in_dim <= most, TLB_EUNSUPPORTED, "linear_fp8_backward: a size past 2^24");
+    TLB_REQUIRE(S <= kMost && out_dim <= kMost && in_dim <= kMost, TLB_EUNSUPPORTED, "linear_fp8_backward: a size past 2^24");
     if (S == 0 || in_dim == 0) return TLB_OK;
     TLB_REQUIRE(dX && (out_dim == 0 || (W && w_scales && dY && dy_scales)), TLB_EINVAL, "linear_fp8_backward: null pointer");
     TLB_REQUIRE(aligned16(W) && aligned16(dY) && aligned16(dX), TLB_EINVAL,
@@ -70,15 +689,14 @@ int tlb_linear_fp8_backward(const uint8_t *W, const float *w_scales, const uint8
                 "linear_fp8_backward: workspace of %zu bytes is smaller than the %zu bytes needed", ws_bytes, need);
     TLB_REQUIRE((reinterpret_cast<uintptr_t>(ws) & 255) == 0, TLB_EINVAL, "linear_fp8_backward: workspace must be 256-byte aligned");
     cudaStream_t st = as_stream(stream);
-    const dim3 grid(unsigned(ceil_div(in_dim, kTile)), unsigned(ceil_div(S, kTile)));
-    TLB_REQUIRE(grid.y <= 65535, TLB_EUNSUPPORTED, "linear_fp8_backward: too many rows");
-    if (type == TLB_W_F32)
-        linear_fp8_simple_kernel<<<grid, kTile * kTile, 0, st>>>(W, w_scales, dY, dy_scales, S, out_dim, in_dim,
-                                                                 static_cast<float *>(dX), accumulate);
-    else
-        linear_fp8_simple_kernel<<<grid, kTile * kTile, 0, st>>>(W, w_scales, dY, dy_scales, S, out_dim, in_dim,
-                                                                 static_cast<__nv_bfloat16 *>(dX), accumulate);
-    return check_launch("linear_fp8_simple");
+    if (type == TLB_W_F32) {
+        float *x = static_cast<float *>(dX);
+        if (out_dim == 0) return accumulate ? TLB_OK : zero_launch(x, S * in_dim, st);
+        return run(W, w_scales, dY, dy_scales, S, out_dim, in_dim, x, accumulate != 0, ws, st);
+    }
+    __nv_bfloat16 *x = static_cast<__nv_bfloat16 *>(dX);
+    if (out_dim == 0) return accumulate ? TLB_OK : zero_launch(x, S * in_dim, st);
+    return run(W, w_scales, dY, dy_scales, S, out_dim, in_dim, x, accumulate != 0, ws, st);
 }
 
 }  // extern "C"
