@@ -7,9 +7,9 @@
 // More than kFewRows rows: tcgen05 (kind::f8f6f4), persistent CTA pairs on 256 x 256 super-tiles:
 //   warp 0      TMA producer: 128 x 128 bytes of dY and of W a stage and CTA (128-byte swizzle: one scale
 //               block is one swizzle row)
-//   warp 1      one thread of the even CTA issues four MMAs (M = N = 256, K = 32) a k block into one of two
-//               accumulators of 256 columns, all of the tensor memory
-//   warps 2..9  a thread has one row and 128 of the columns: it keeps their sums in 128 registers and
+//   warps 1, 2  one lane each of the even CTA issues four MMAs (M = 256, N = 128, K = 32) a k block, for one half of
+//               the columns, into two accumulators of 128 columns in turn: all of the tensor memory
+//   warps 4..11 a thread has one row and 128 of the columns: it keeps their sums in 128 registers and
 //               adds each k block's accumulator times its scale while the next one is multiplied.
 // Per CTA and k block the MMAs take 512 cycles, the sums 128 float32 additions a thread on two warps a
 // scheduler (256 issue slots as scalars, 128 as pairs) and 128 KB read from tensor memory.
@@ -188,10 +188,15 @@ int rows_launch(const RowsParams &p, cudaStream_t st) {
 constexpr int kTM = 256, kTN = 256;      // super-tile of a CTA pair
 constexpr int kHalf = 128;               // rows of dY, and of W, that one CTA stages
 constexpr int kStageBytes = 2 * kHalf * kFp8Block;
-constexpr int kStages = 6;
-constexpr int kThreads = 320;            // producer, MMA, 8 epilogue warps
-constexpr int kEpiWarps = 8;
-constexpr int kTcSmem = kStages * kStageBytes + kEpiWarps * 32 * 33 * 4 + 1024;
+constexpr int kStages = 5;
+constexpr int kFirstEpi = 4;             // warps before: producer, two for the MMAs, one that only holds its place
+constexpr int kEpiWarps = 16;              // four for each 32 rows, 64 columns each
+constexpr int kThreads = 32 * (kFirstEpi + kEpiWarps);
+// Registers a thread after the split between the two kinds of warps (setmaxnreg): 128 sums and 64 on their way.
+constexpr int kFewRegs = 64, kManyRegs = 104;
+constexpr int kSplitRegs = 32 * (kFirstEpi * kFewRegs + kEpiWarps * kManyRegs);
+constexpr int kBlkBytes = 32 * 32 * 4;   // a warp's 32 x 32 results on their way out
+constexpr int kTcSmem = kStages * kStageBytes + kEpiWarps * kBlkBytes + 1024;
 static_assert(kTcSmem <= 227 * 1024, "shared memory of one CTA");
 
 struct TcParams {
@@ -201,8 +206,9 @@ struct TcParams {
     int add;
     void *dX;
     float *partial;                      // [pairs][2 CTAs][2 slots][128][256]
-    // Pair c first does its share [work c / sk_pairs, work (c + 1) / sk_pairs) of the (tile, k block) units of
-    // the last sk_tiles tiles (c < sk_pairs), cut at the tiles' ends, then the whole tiles c, c + pairs, ...
+    // Pair c does its share [work c / sk_pairs, work (c + 1) / sk_pairs) of the (tile, k block) units of the last
+    // sk_tiles tiles (c < sk_pairs), cut at the tiles' ends, and the whole tiles c, c + pairs, ...: even pairs the
+    // share first, odd pairs last, so that they do not all write at the same time.
     int tiles, sk_tiles, sk_pairs, pairs;
     uint32_t *status;
 };
@@ -214,16 +220,18 @@ __host__ __device__ __forceinline__ int64_t share(int64_t work, int pairs, int c
 struct Walk {
     int at, end, begin;                  // units of the shared tiles still to do (at most 75 tiles of 2^17 k blocks)
     int whole;                           // next whole tile
+    bool first;                          // the share before the whole tiles
     __device__ __forceinline__ Walk(const TcParams &p, int c) {
         const int64_t work = int64_t(p.sk_tiles) * p.KB;
         begin = at = c < p.sk_pairs ? int(share(work, p.sk_pairs, c)) : 0;
         end = c < p.sk_pairs ? int(share(work, p.sk_pairs, c + 1)) : 0;
         whole = c;
+        first = (c & 1) == 0;
     }
     // false when there is none left; slot: where a part of a tile goes
     __device__ __forceinline__ bool next(const TcParams &p, int &m, int &n, int &kb0, int &kb1, int &slot) {
         int tile = p.tiles - p.sk_tiles;
-        if (at < end) {
+        if (at < end && (first || whole >= tile)) {
             const int t = at / p.KB;
             slot = at == begin ? 0 : 1;
             kb0 = at - t * p.KB;
@@ -253,41 +261,43 @@ __device__ __forceinline__ void mma_e4m3_pair(uint32_t tmem_d, uint64_t adesc, u
         : "memory");
 }
 
-// 32 TMEM lanes x 8 consecutive 32-bit columns.
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, uint32_t *v) {
-    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
-                 : "r"(taddr));
+// One lane of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
 }
 
-// a += v * s on a pair of floats
-__device__ __forceinline__ void fma2(uint64_t &a, uint32_t v0, uint32_t v1, uint64_t s) {
-    asm volatile("{\n\t.reg .b64 v;\n\tmov.b64 v, {%1, %2};\n\tfma.rn.f32x2 %0, v, %3, %0;\n\t}" : "+l"(a) : "r"(v0), "r"(v1), "l"(s));
+// Arrive on an mbarrier of either CTA once this warp's tensor-memory loads are done (tcgen05.wait::ld, and
+// tcgen05.fence::before_thread_sync).  No data goes through other memory, so the arrival orders none: a
+// release waits for the scales' loads as well, and took three quarters of the product's time.
+__device__ __forceinline__ void mbar_arrive_drained(uint32_t bar_cluster) {
+    asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
 }
 
 template <typename T, bool WIDE>
 __global__ void __launch_bounds__(kThreads, 1) linear_fp8_tc_kernel(const __grid_constant__ TcParams p) {
     extern __shared__ uint8_t smem_raw[];
     uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    __shared__ uint64_t full[kStages], empty[kStages], accfull[2], accempty[2], done;
+    __shared__ uint64_t full[kStages], empty[kStages], accfull[2][2], accempty[2][2], done;
     __shared__ uint32_t tmem_base;
-    __shared__ int s_abort, s_issued, s_consumed;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ int s_abort, s_issued, s_consumed[2];
+    const int warp = __shfl_sync(0xffffffffu, int(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
     const int rank = int(cluster_rank()), pair = int(blockIdx.x >> 1);
     const bool leader = rank == 0;
 
     if (threadIdx.x == 0) {
         s_abort = 0;
-        s_issued = s_consumed = 0;
+        s_issued = s_consumed[0] = s_consumed[1] = 0;
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1);
+            mbar_init(&empty[s], 2);                         // both halves of the columns
         }
-        for (int b = 0; b < 2; ++b) {
-            mbar_init(&accfull[b], 1);
-            mbar_init(&accempty[b], 2 * kEpiWarps);          // both CTAs' warps
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&accfull[i >> 1][i & 1], 1);
+            mbar_init(&accempty[i >> 1][i & 1], kEpiWarps);  // half of the warps of both CTAs
         }
-        mbar_init(&done, 1);
+        mbar_init(&done, 2);
     }
     if (warp == 1) {
         tmem_alloc_pair(&tmem_base, 512);
@@ -299,130 +309,142 @@ __global__ void __launch_bounds__(kThreads, 1) linear_fp8_tc_kernel(const __grid
     cluster_sync();
     tc_fence_after();
     const uint32_t tmem = tmem_base;
+    if (threadIdx.x == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&p.y) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&p.w) : "memory");
+    }
     pdl_trigger();                                            // the join may be scheduled
     pdl_wait();                                               // padded copies of the operands
 
     Walk walk(p, pair);
     int m, n, kb0, kb1, slot;
-    if (warp == 0) {
-        // ------------------------------------------------ TMA producer
-        if (lane == 0) {
-            int g = 0;
+    if (warp < kFirstEpi) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFewRegs));
+        // The whole warp goes through the loops and one elected lane issues, so that addresses and descriptors
+        // stay in uniform registers: issued by a lane on its own, the four MMAs and two commits of a k block
+        // took longer than the tensor cores need for them (1160 cycles a k block instead of 512).
+        if (warp == 0) {
+            // -------------------------------------------- TMA producer
+            int g = 0, s = 0, phase = 1;
             bool ok = true;
+            const uint32_t fb = cluster_addr(&full[0], 0);
             while (ok && walk.next(p, m, n, kb0, kb1, slot)) {
                 for (int kb = kb0; kb < kb1; ++kb, ++g) {
-                    const int s = g % kStages;
-                    if (g >= kStages && !mbar_wait(&empty[s], ((g / kStages) - 1) & 1, p.status, 40u)) {
+                    if (g >= kStages && !mbar_wait(&empty[s], phase, p.status, 40u)) {
                         ok = false;
                         break;
                     }
-                    uint8_t *sa = smem + s * kStageBytes;
-                    if (leader) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);   // both CTAs' copies count here
-                    const uint32_t fb = cluster_addr(&full[s], 0);
-                    tma_load_2d_pair(sa, &p.y, kb * kFp8Block, m + rank * kHalf, fb);
-                    tma_load_2d_pair(sa + kStageBytes / 2, &p.w, kb * kFp8Block, n + rank * kHalf, fb);
-                    s_issued = g + 1;
+                    if (elect_one()) {
+                        uint8_t *sa = smem + s * kStageBytes;
+                        if (leader) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);   // both CTAs' copies count here
+                        tma_load_2d_pair(sa, &p.y, kb * kFp8Block, m + rank * kHalf, fb + 8 * s);
+                        tma_load_2d_pair(sa + kStageBytes / 2, &p.w, kb * kFp8Block, n + rank * kHalf, fb + 8 * s);
+                        s_issued = g + 1;
+                    }
+                    if (++s == kStages) { s = 0; phase ^= 1; }
                 }
             }
             if (!ok) s_abort = 1;
-        }
-    } else if (warp == 1) {
-        // ------------------------------------------------ MMA issuer: the accumulators alternate with the k blocks
-        if (lane == 0 && leader) {
-            // D float32, A and B e4m3, both K-major, M = N = 256
-            const uint32_t idesc = (1u << 4) | (uint32_t(kTN >> 3) << 17) | (uint32_t(kTM >> 4) << 24);
-            int g = 0;
+        } else if (warp <= 2 && leader) {
+            // -------------------------------------------- MMA issuers: one for each half of the columns
+            // D float32, A and B e4m3, both K-major, M = 256, N = 128
+            const uint32_t idesc = (1u << 4) | (uint32_t(kTN / 2 >> 3) << 17) | (uint32_t(kTM >> 4) << 24);
+            const int h = warp - 1;
+            // a half takes 64 of the rows of W that each CTA stages
+            const uint64_t ad0 = sw128_desc(smem), bd0 = sw128_desc(smem + kStageBytes / 2 + h * 64 * kFp8Block);
+            int g = 0, s = 0, phase = 0;
             bool ok = true;
             while (ok && walk.next(p, m, n, kb0, kb1, slot)) {
                 for (int kb = kb0; kb < kb1; ++kb, ++g) {
-                    const int s = g % kStages, b = g & 1;
-                    if (g >= 2 && !mbar_wait(&accempty[b], ((g >> 1) - 1) & 1, p.status, 43u)) { ok = false; break; }
-                    if (!mbar_wait(&full[s], (g / kStages) & 1, p.status, 41u)) { ok = false; break; }
+                    const int b = g & 1;
+                    // the copies first, which are mostly there: the accumulator is what the next MMA waits for
+                    if (!mbar_wait(&full[s], phase, p.status, 41u)) { ok = false; break; }
+                    if (!mbar_wait(&accempty[h][b], ((g >> 1) & 1) ^ 1, p.status, 43u)) { ok = false; break; }
                     tc_fence_after();
-                    const uint8_t *sa = smem + s * kStageBytes;
-                    const uint64_t ad = sw128_desc(sa), bd = sw128_desc(sa + kStageBytes / 2);
+                    if (elect_one()) {
+                        const uint64_t ad = ad0 + uint64_t(s * (kStageBytes / 16)), bd = bd0 + uint64_t(s * (kStageBytes / 16));
+                        const uint32_t acc = tmem + uint32_t(h * 256 + b * 128);
 #pragma unroll
-                    for (int k = 0; k < kFp8Block / 32; ++k)  // 32 bytes = 2 descriptor units
-                        mma_e4m3_pair(tmem + uint32_t(b * kTN), ad + 2 * k, bd + 2 * k, idesc, k > 0 ? 1u : 0u);
-                    mma_commit_pair(&empty[s], 3);            // frees the stage in both CTAs
-                    mma_commit_pair(&accfull[b], 3);
-                    s_consumed = g + 1;
+                        for (int k = 0; k < kFp8Block / 32; ++k)  // 32 bytes = 2 descriptor units
+                            mma_e4m3_pair(acc, ad + 2 * k, bd + 2 * k, idesc, k > 0 ? 1u : 0u);
+                        mma_commit_pair(&accfull[h][b], 3);
+                        s_consumed[h] = g + 1;
+                    }
+                    if (++s == kStages) { s = 0; phase ^= 1; }
                 }
             }
             if (!ok) s_abort = 1;
-            mma_commit_pair(&done, 1);
+            if (elect_one()) mma_commit_pair(&done, 1);
             mbar_wait(&done, 0, nullptr, 0u);
         }
     } else {
-        // ------------------------------------------------ sums in registers (warps 2..9)
-        const int q = warp & 3, half = (warp - 2) >> 2;       // this warp's TMEM lanes and columns
-        float *blk = reinterpret_cast<float *>(smem + kStages * kStageBytes) + (warp - 2) * 32 * 33;
-        const uint32_t tbase = tmem + (uint32_t(q * 32) << 16) + uint32_t(half * 128);
-        int g = 0;
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kManyRegs));
+        // ------------------------------------------------ sums in registers
+        const int q = warp & 3, cq = (warp - kFirstEpi) >> 2;     // this warp's TMEM lanes and quarter of the columns
+        const int h = cq >> 1;                                // the half that holds it: columns 64 h.. of each 128
+        float4 *blk = reinterpret_cast<float4 *>(smem + kStages * kStageBytes + (warp - kFirstEpi) * kBlkBytes);
+        const uint32_t tbase = tmem + (uint32_t(q * 32) << 16) + uint32_t(h * 256 + (cq & 1) * 64);
+        int g = 0, st = 0;
         bool ok = true;
         while (ok && walk.next(p, m, n, kb0, kb1, slot)) {
-            const int rows0 = m + rank * kHalf + q * 32, cols0 = n + half * 128;
+            const int rows0 = m + rank * kHalf + q * 32, in_tile = (cq & 1) * 128 + h * 64, cols0 = n + in_tile;
             const bool any = rows0 < p.M && cols0 < p.N;      // the warp has results to write
             const int yrow = min(rows0 + lane, p.M - 1), wrow = any ? cols0 / kFp8Block : 0;
             auto scale_of = [&](const float *scales, int row, int kb) { return __ldg(scales + int64_t(row) * p.KB + kb); };
-            uint64_t acc[64];
+            float acc[64];
 #pragma unroll
-            for (int c = 0; c < 64; ++c) acc[c] = 0;
+            for (int c = 0; c < 64; ++c) acc[c] = 0.f;
             float sy = scale_of(p.ys, yrow, kb0), sw = scale_of(p.ws, wrow, kb0);
             for (int kb = kb0; kb < kb1; ++kb, ++g) {
                 const int b = g & 1;
                 const float s = sy * sw;
-                uint64_t s2;
-                asm("mov.b64 %0, {%1, %1};" : "=l"(s2) : "f"(s));
                 if (kb + 1 < kb1) {
                     sy = scale_of(p.ys, yrow, kb + 1);
                     sw = scale_of(p.ws, wrow, kb + 1);
                 }
-                if (!mbar_wait(&accfull[b], (g >> 1) & 1, p.status, 42u)) { ok = false; break; }
+                if (!mbar_wait(&accfull[h][b], (g >> 1) & 1, p.status, 42u)) { ok = false; break; }
+                // the MMAs that read this stage are done, in both CTAs
+                if (q == 0 && (cq & 1) == 0 && lane == 0) mbar_arrive(&empty[st]);
+                if (++st == kStages) st = 0;
                 tc_fence_after();
                 if (any) {
-                    // eight columns on their way while the eight before are added
-                    uint32_t v[2][16];
-                    tmem_ld16(tbase + uint32_t(b * kTN), v[0]);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t v[16];
+                        tmem_ld16(tbase + uint32_t(b * 128 + j * 16), v);
                         tmem_wait_ld();
-                        if (j < 7) tmem_ld16(tbase + uint32_t(b * kTN + (j + 1) * 16), v[(j + 1) & 1]);
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) fma2(acc[j * 8 + c], v[j & 1][2 * c], v[j & 1][2 * c + 1], s2);
+                        for (int c = 0; c < 16; ++c) acc[j * 16 + c] = fmaf(__uint_as_float(v[c]), s, acc[j * 16 + c]);
                     }
                 }
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive_cluster(cluster_addr(&accempty[b], 0));
+                if (lane == 0) mbar_arrive_drained(cluster_addr(&accempty[h][b], 0));
             }
             if (!ok) break;
             if (!any) continue;
-            // 32 x 32 at a time through shared memory, so that lanes run along columns
+            // 32 x 32 at a time through shared memory, so that lanes run along columns: 16 bytes a lane, whose places in
+            // a row are turned by the row's last three bits (no bank is met twice either way)
             const bool whole = kb0 == 0 && kb1 == p.KB;
-            const int c4 = (lane & 7) * 4, rl = lane >> 3;
+            const int ch = lane & 7, rl = lane >> 3;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
+            for (int j = 0; j < 2; ++j) {
 #pragma unroll
-                for (int c = 0; c < 16; ++c) {
-                    uint32_t lo, hi;
-                    asm("mov.b64 {%0, %1}, %2;" : "=r"(lo), "=r"(hi) : "l"(acc[j * 16 + c]));
-                    blk[lane * 33 + 2 * c] = __uint_as_float(lo);
-                    blk[lane * 33 + 2 * c + 1] = __uint_as_float(hi);
-                }
+                for (int c = 0; c < 8; ++c)
+                    blk[lane * 8 + (c ^ (lane & 7))] =
+                        make_float4(acc[j * 32 + 4 * c], acc[j * 32 + 4 * c + 1], acc[j * 32 + 4 * c + 2], acc[j * 32 + 4 * c + 3]);
                 __syncwarp();
-                const int col = cols0 + j * 32 + c4;
-#pragma unroll 1
+                const int col = cols0 + j * 32 + ch * 4;
+#pragma unroll 2
                 for (int k = 0; k < 8; ++k) {
                     const int r = 4 * k + rl;
-                    const float *a = blk + r * 33 + c4;
-                    const float4 y = make_float4(a[0], a[1], a[2], a[3]);
+                    const float4 y = blk[r * 8 + (ch ^ (r & 7))];
                     if (rows0 + r >= p.M) continue;
                     if (whole)
                         put4<T, WIDE>(static_cast<T *>(p.dX) + int64_t(rows0 + r) * p.N + col, col, p.N, y, p.add != 0);
                     else
                         *reinterpret_cast<float4 *>(p.partial + ((int64_t(blockIdx.x) * 2 + slot) * kHalf + q * 32 + r) * kTN +
-                                                    half * 128 + j * 32 + c4) = y;
+                                                    in_tile + j * 32 + ch * 4) = y;
                 }
                 __syncwarp();
             }
@@ -434,7 +456,7 @@ __global__ void __launch_bounds__(kThreads, 1) linear_fp8_tc_kernel(const __grid
     tc_fence_before();
     __syncthreads();
     if (s_abort && threadIdx.x == 0 && leader) {
-        for (int g = s_consumed; g < s_issued; ++g) mbar_wait(&full[g % kStages], (g / kStages) & 1, nullptr, 0u);
+        for (int g = min(s_consumed[0], s_consumed[1]); g < s_issued; ++g) mbar_wait(&full[g % kStages], (g / kStages) & 1, nullptr, 0u);
     }
     __syncthreads();
     cluster_sync();
@@ -444,9 +466,9 @@ __global__ void __launch_bounds__(kThreads, 1) linear_fp8_tc_kernel(const __grid
     }
 }
 
-// Joins the parts of the shared tiles in the pairs' order.  Block (tile, y) does rows y, y + gridDim.y, ...
+// Joins the parts of the shared tiles in the pairs' order.  Block (tile, y) does rows 2 y and 2 y + 1.
 template <typename T, bool WIDE>
-__global__ void __launch_bounds__(256) linear_fp8_join_kernel(const __grid_constant__ TcParams p) {
+__global__ void __launch_bounds__(128) linear_fp8_join_kernel(const __grid_constant__ TcParams p) {
     const int tiles_m = (p.M + kTM - 1) / kTM, tile = p.tiles - p.sk_tiles + int(blockIdx.x);
     const int m = (tile % tiles_m) * kTM, n = (tile / tiles_m) * kTN;
     const int64_t work = int64_t(p.sk_tiles) * p.KB, ta = int64_t(blockIdx.x) * p.KB, tb = ta + p.KB;
@@ -458,18 +480,19 @@ __global__ void __launch_bounds__(256) linear_fp8_join_kernel(const __grid_const
     if (c1 == c0) return;                                     // done whole by one pair
     const int s0 = share(work, p.sk_pairs, c0) < ta ? 1 : 0;  // that pair began in the tile before
     const int c4 = (threadIdx.x & 63) * 4;
-    for (int r = int(blockIdx.y) * 4 + (threadIdx.x >> 6); r < min(kTM, p.M - m); r += int(gridDim.y) * 4) {
+    for (int r = int(blockIdx.y) * 2 + (threadIdx.x >> 6); r < min(kTM, p.M - m); r += int(gridDim.y) * 2) {
         const int h = r / kHalf, lr = r % kHalf;
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int c = c0; c <= c1; c += 8) {                   // up to eight loads in flight
-            float4 v[8];
+        constexpr int kAhead = 20;                            // loads in flight
+        for (int c = c0; c <= c1; c += kAhead) {
+            float4 v[kAhead];
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
+            for (int u = 0; u < kAhead; ++u)
                 if (c + u <= c1)
                     v[u] = __ldcg(reinterpret_cast<const float4 *>(
                         p.partial + ((int64_t(2 * (c + u) + h) * 2 + (c + u == c0 ? s0 : 0)) * kHalf + lr) * kTN + c4));
 #pragma unroll
-            for (int u = 0; u < 8; ++u)
+            for (int u = 0; u < kAhead; ++u)
                 if (c + u <= c1) {
                     y.x += v[u].x; y.y += v[u].y; y.z += v[u].z; y.w += v[u].w;
                 }
@@ -491,13 +514,13 @@ Plan plan_of(int64_t M, int64_t N, int64_t KB) {
     const int rest = int(tiles % P);
     if (rest == 0) return pl;
     // The tiles of the last wave: whole on `rest` pairs, or shared by more along K, evenly (a multiple of `rest`) or
-    // by all P.  In k blocks of a pair: a part of a tile costs about kPart more (it is written, and read by the join).
-    constexpr double kPart = 6.0;
+    // by all P.  In k blocks of a pair: a part of a tile costs kPart more where it is written, and kJoin where it is read.
+    constexpr double kPart = 6.0, kJoin = 0.2;
     double best = double(KB);
     auto consider = [&](int pairs) {
         if (pairs <= rest || pairs > P) return;
         const int64_t most = ceil_div(int64_t(rest) * KB, pairs);
-        const double cost = double(most) + kPart * (pairs % rest == 0 ? 1 : 2);
+        const double cost = double(most) + kPart * (pairs % rest == 0 ? 1 : 2) + kJoin * pairs;
         if (most >= 1 && cost < best) {
             best = cost;
             pl.sk_tiles = rest;
@@ -528,6 +551,12 @@ template <typename T, bool WIDE>
 int tc_launch(const TcParams &p, cudaStream_t st) {
     auto kernel = linear_fp8_tc_kernel<T, WIDE>;
     TLB_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem));
+    static const int regs = [&] {                             // the split shares out what the block is launched with
+        cudaFuncAttributes a;
+        return cudaFuncGetAttributes(&a, kernel) == cudaSuccess ? a.numRegs : 0;
+    }();
+    TLB_REQUIRE(regs * kThreads >= kSplitRegs, TLB_ECUDA, "linear_fp8_backward: built with %d registers a thread, needs %d", regs,
+                kSplitRegs / kThreads + 1);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(2 * p.pairs));
     cfg.blockDim = dim3(kThreads);
@@ -543,7 +572,7 @@ int tc_launch(const TcParams &p, cudaStream_t st) {
     TLB_TRY(check_launch("linear_fp8_tc"));
     if (p.sk_tiles == 0) return TLB_OK;
     const int64_t rows = std::min<int64_t>(kTM, p.M);
-    TLB_CUDA(launch_dependent(linear_fp8_join_kernel<T, WIDE>, dim3(unsigned(p.sk_tiles), unsigned(ceil_div(rows, 4))), dim3(256), 0,
+    TLB_CUDA(launch_dependent(linear_fp8_join_kernel<T, WIDE>, dim3(unsigned(p.sk_tiles), unsigned(ceil_div(rows, 2))), dim3(128), 0,
                               st, p));
     return check_launch("linear_fp8_join");
 }
