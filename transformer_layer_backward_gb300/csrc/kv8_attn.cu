@@ -1,6 +1,22 @@
 // Attention of single tokens over the 8-bit K/V cache, and its gradient.
+//
+// Bound by the read of the keys and values, once.  What a CTA (four warps) does for a chunk of one sequence's keys, one
+// KV head and a tile of the query heads that share it, 16 keys a warp at a time:
+//   - cp.async brings the keys', values' and scales' bytes to shared memory, two steps ahead; keys that
+//     are not there come as zeros, so that nothing of what a free slot holds is met;
+//   - s = q k and (gradient) dp = d_ctx v are products of mma.sync m16n8k16 with the keys as columns: e4m3 values
+//     are halves exactly, and a query is two of them, the second holding what the first leaves times 2^12 (rows g
+//     and g + 8 of the operand, which meet in one thread).  The 16 bytes of a row that a lane reads serve as
+//     operands as they are, the query's columns being ordered to match;
+//   - the sums over keys (p v; p dp k and p k) take the weights x in the same two halves, scaled by a
+//     power of two of each row that grows with the largest |x| so far, and the rows' bytes transposed
+//     by byte permutes: 23 bits of each weight, 37 below the largest.
+// The gradient uses d_q = scale (sum p dp k - (sum p dp)(sum p k)), so that one pass does.  Rows of the gradient's
+// tile: four heads' s (and p dp) in rows 0..3, their dp (and p) in rows 4..7; of the forward's: eight heads.
+// Warps, then chunks (a second kernel), are joined in a fixed order.
 #include <cmath>
 
+#include "async.cuh"
 #include "kv8.cuh"
 
 namespace tlb {
@@ -8,160 +24,553 @@ namespace tlb {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kDims = 8;                 // 32 lanes x 8 dimensions: head_dim <= 256
+constexpr int kStep = 16;                // keys of a warp's step
+constexpr int kStages = 3;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLow = 4096.f;           // the second half of a value holds what the first leaves, times this
 
-__device__ __forceinline__ void load_row(const uint8_t *rows, int64_t at, int hd, int lane, float (&x)[kDims]) {
-#pragma unroll
-    for (int i = 0; i < kDims; ++i) x[i] = lane + 32 * i < hd ? e4m3x2_to_float2(rows[at + lane + 32 * i]).x : 0.f;
+constexpr int tile_heads(bool grad) { return grad ? 4 : 8; }
+
+// Shared memory: the query's operand (and d_ctx's), then each warp's stages of keys, values and scales.
+template <int HD> constexpr int row_bytes() { return HD; }
+template <int HD> constexpr int stage_bytes() { return 2 * kStep * HD + 3 * kStep * 4; }
+template <int HD, bool GRAD> constexpr int smem_bytes() {
+    return (GRAD ? 2 : 1) * (HD / 16) * 32 * 16 + kWarps * kStages * stage_bytes<HD>();
 }
 
-__device__ __forceinline__ float dot(const float (&a)[kDims], const float (&b)[kDims]) {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < kDims; ++i) s = fmaf(a[i], b[i], s);
-    return warp_sum(s);
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
-// One CTA a query head, its warps taking turns at the keys.
-template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) kv8_attn_forward_simple(tlb_kv8 c, Kv8Pages pg, int n_heads, float scale,
-                                                                       const T *__restrict__ q, T *__restrict__ ctx,
-                                                                       float *__restrict__ lse) {
-    __shared__ float sm[kWarps], sl[kWarps], so[kWarps][256];
-    const int64_t b = blockIdx.x / n_heads;
-    const int h = int(blockIdx.x - b * n_heads), kvh = h / (n_heads / c.n_kv_heads), hd = c.head_dim;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, len = kv8_length(pg, b);
-    float x[kDims], o[kDims] = {}, m = -INFINITY, l = 0.f;
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint4 &a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
+// bytes < 16 or ok false: zeros
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copy4(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
+}
+
+// Place of the 16-byte piece c of row r of a stage: the pieces are turned by the row so that neither the rows n, n + 1
+// that eight lanes read for the logits nor the rows 0, 2, 4, 6 (1, 3, 5, 7) of the sums meet in a bank.
+template <int HD>
+__device__ __forceinline__ int place(int r, int c) {
+    const int turn = HD == 64 ? (r >> 1) & 3 : ((r & 1) << 2) ^ (r & 6);
+    return r * HD + ((c ^ turn) << 4);
+}
+
+// x = hi + lo / 4096, as a pair of each for two values
+__device__ __forceinline__ void halves(float x, float y, uint32_t &hi, uint32_t &lo) {
+    const __half2 h = __floats2half2_rn(x, y);
+    const float2 f = __half22float2(h);
+    const __half2 l = __floats2half2_rn((x - f.x) * kLow, (y - f.y) * kLow);
+    hi = *reinterpret_cast<const uint32_t *>(&h);
+    lo = *reinterpret_cast<const uint32_t *>(&l);
+}
+
+// 2^e, -149 <= e <= 127 (2^128, of a row whose weights are not finite, is infinite)
+__device__ __forceinline__ float pow2(int e) { return e >= -126 ? __uint_as_float(uint32_t(e + 127) << 23) : __uint_as_float(1u << (e + 149)); }
+
+struct AttnParams {
+    tlb_kv8 c;
+    Kv8Pages pg;
+    int n_heads, group, tiles, splits, chunk;    // heads a KV head, tiles of them, chunks of keys
+    float scale;
+    const void *q, *d_ctx;
+    const float *lse;            // gradient
+    void *out;                   // ctx or d_q (one chunk alone)
+    float *out_lse;
+    float *part;                 // [n_seq, n_heads, splits][hd or 2 hd]
+    float2 *sums;                // [n_seq, n_heads, splits]: forward (max, sum), gradient (sum p dp, -)
+    float2 *newest;              // [n_seq, n_heads]: p and dp of the newest key
+    float *D;                    // [n_seq, n_heads]: sum p dp
+};
+
+// Rows of T as the first operand: piece ks of lane (g, t) holds columns 64 (ks / 4) + 16 t + 4 (ks % 4) + {0, 1 | 2, 3} of row
+// g's two halves.  f[g]: the power of two that the row was divided by (its largest value becomes 2^14 .. 2^15).
+template <typename T, int HD>
+__device__ __forceinline__ void stage_rows(const T *rows, int n, int hd, int first, uint4 *to, int *f) {
+    // a warp a row; rows first .. first + n - 1 of the operand, the others zero
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    for (int g = warp; g < 8; g += kWarps) {
+        const bool there = g >= first && g < first + n;
+        const T *p = rows + int64_t(there ? g - first : 0) * hd;
+        uint32_t top = 0;
+        float x[HD / 32];
 #pragma unroll
-    for (int i = 0; i < kDims; ++i) x[i] = lane + 32 * i < hd ? load_float(q + int64_t(blockIdx.x) * hd + lane + 32 * i) * scale : 0.f;
-    for (int j = warp; j < len; j += kWarps) {
-        const int64_t slot = kv8_slot(pg, c.n_slots, b, j);
-        if (slot < 0) continue;
-        float k[kDims], v[kDims];
-        load_row(c.k, (slot * c.n_kv_heads + kvh) * hd, hd, lane, k);
-        load_row(c.v, (slot * c.n_kv_heads + kvh) * hd, hd, lane, v);
-        const float s = dot(x, k) * c.k_scale[int64_t(kvh) * c.n_slots + slot], sv = c.v_scale[int64_t(kvh) * c.n_slots + slot];
-        const float mn = fmaxf(m, s), old = m == -INFINITY ? 0.f : expf(m - mn), p = expf(s - mn);
-        l = l * old + p;
+        for (int i = 0; i < HD / 32; ++i) {
+            x[i] = there && lane + 32 * i < hd ? load_float(p + lane + 32 * i) : 0.f;
+            top = max(top, magnitude(x[i]));
+        }
+        top = __reduce_max_sync(0xffffffffu, top);
+        // rows below 2^-100 keep that power; of infinities and NaN the halves are NaN whatever it is
+        const int e = max(int(top >> 23) - 127, -100) - 14;
+        if (lane == 0) f[g] = e;
+        const float s = pow2(-e);
 #pragma unroll
-        for (int i = 0; i < kDims; ++i) o[i] = o[i] * old + p * sv * v[i];
-        m = mn;
+        for (int i = 0; i < HD / 32; ++i) {
+            const int d = lane + 32 * i;
+            const float y = x[i] * s;
+            const __half hi = __float2half_rn(y);
+            const __half lo = __float2half_rn((y - __half2float(hi)) * kLow);
+            const int ks = (d >> 6) * 4 + ((d >> 2) & 3), t = (d >> 4) & 3;
+            __half *o = reinterpret_cast<__half *>(&to[ks * 32 + g * 4 + t]);   // a0, a1, a2, a3 as pairs
+            o[((d >> 1) & 1) * 4 + (d & 1)] = hi;
+            o[((d >> 1) & 1) * 4 + 2 + (d & 1)] = lo;
+        }
     }
-    if (lane == 0) { sm[warp] = m; sl[warp] = l; }
+}
+
+template <typename T, int HD, bool GRAD>
+__global__ void __launch_bounds__(kWarps * 32) kv8_attn_kernel(const __grid_constant__ AttnParams p) {
+    constexpr int HT = tile_heads(GRAD), KS = HD / 16, NT = HD / 8;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ int s_f[2][8];
+    __shared__ float s_m[kWarps][8], s_l[kWarps][8];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int split = int(blockIdx.x % p.splits);
+    int64_t unit = blockIdx.x / p.splits;
+    const int tile = int(unit % p.tiles);
+    unit /= p.tiles;
+    const int nkv = p.c.n_kv_heads, hd = p.c.head_dim;
+    const int kvh = int(unit % nkv);
+    const int64_t b = unit / nkv;
+    const int len = kv8_length(p.pg, b), k0 = split * p.chunk;
+    if (k0 >= len && !(split == 0 && p.splits == 1)) return;  // the join looks at the chunks below len
+    const int k1 = min(len, k0 + p.chunk), steps = max(0, (k1 - k0 + kStep - 1) / kStep);
+    const int64_t head0 = b * p.n_heads + kvh * p.group + tile * HT;   // first row of q
+    const int heads = min(HT, p.group - tile * HT);
+
+    // ---- copies: step i of this warp is keys k0 + 16 (warp + kWarps i) ..
+    const uint32_t ring = smem_u32(smem) + (GRAD ? 2 : 1) * KS * 512 + warp * kStages * stage_bytes<HD>();
+    const int mine = steps > warp ? (steps - warp + kWarps - 1) / kWarps : 0;
+    auto slot_of = [&](int i) {          // lane's key of step i (its lower four bits), -1 where there is none
+        const int j = k0 + kStep * (warp + kWarps * i) + (lane & 15);
+        return i < mine && j < k1 ? int(kv8_slot(p.pg, p.c.n_slots, b, j)) : -1;
+    };
+    int slot = slot_of(0);
+    auto issue = [&](int i) {
+        if (i < mine) {
+            const uint32_t st = ring + (i % kStages) * stage_bytes<HD>();
+            const int mask = int(__ballot_sync(0xffffffffu, slot >= 0));
 #pragma unroll
-    for (int i = 0; i < kDims; ++i) so[warp][lane + 32 * i] = o[i];
+            for (int c = 0; c < kStep * HD / 16 / 32; ++c) {
+                const int e = c * 32 + lane, r = e / (HD / 16), ch = e % (HD / 16);
+                const int sl = __shfl_sync(0xffffffffu, slot, r);
+                const bool ok = sl >= 0 && ch * 16 < hd;
+                const int64_t at = (int64_t(ok ? sl : 0) * nkv + kvh) * hd + (ok ? ch * 16 : 0);
+                copy16(st + place<HD>(r, ch), p.c.k + at, ok);
+                copy16(st + kStep * HD + place<HD>(r, ch), p.c.v + at, ok);
+            }
+            const int64_t at = int64_t(kvh) * p.c.n_slots + max(slot, 0);
+            copy4(st + 2 * kStep * HD + lane * 4, (lane < 16 ? p.c.k_scale : p.c.v_scale) + at, slot >= 0);
+            if (lane == 0)
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + 2 * kStep * HD + 128), "r"(mask) : "memory");
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        slot = slot_of(i + 1);
+    };
+#pragma unroll
+    for (int i = 0; i < kStages - 1; ++i) issue(i);
+
+    // ---- the queries
+    uint4 *qf = reinterpret_cast<uint4 *>(smem);
+    stage_rows<T, HD>(static_cast<const T *>(p.q) + head0 * hd, heads, hd, 0, qf, s_f[0]);
+    if (GRAD) stage_rows<T, HD>(static_cast<const T *>(p.d_ctx) + head0 * hd, heads, hd, 4, qf + KS * 32, s_f[1]);
     __syncthreads();
-    float top = -INFINITY, total = 0.f;
-    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w]);
-    for (int w = 0; w < kWarps; ++w) total += sl[w] > 0.f || sl[w] != sl[w] ? sl[w] * expf(sm[w] - top) : 0.f;
-    for (int d = threadIdx.x; d < hd; d += blockDim.x) {
+    // this lane's row: the factor of its logits (in powers of two, gradient rows 4..7: of dp)
+    const bool is_dp = GRAD && g >= 4;
+    const float factor = is_dp ? pow2(s_f[1][g]) : p.scale * kLog2e * pow2(s_f[0][g]);
+    const int my_head = is_dp ? g - 4 : g;
+    const float norm = GRAD && my_head < heads ? __ldg(p.lse + head0 + my_head) * kLog2e : 0.f;
+
+    float acc[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) acc[i][0] = acc[i][1] = acc[i][2] = acc[i][3] = 0.f;
+    float m = -INFINITY, l = 0.f;        // forward: the row's largest logit, sum of exp; gradient: l = sum p dp (rows 0..3)
+    int ex = -120;                       // the sums are of x / 2^ex
+    for (int i = 0; i < mine; ++i) {
+        issue(i + kStages - 1);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        __syncwarp();
+        const uint8_t *st = smem + (GRAD ? 2 : 1) * KS * 512 + (warp * kStages + i % kStages) * stage_bytes<HD>();
+        const uint8_t *sk_rows = st, *sv_rows = st + kStep * HD;
+        const float *scales = reinterpret_cast<const float *>(st + 2 * kStep * HD);
+        const uint32_t mask = *reinterpret_cast<const uint32_t *>(st + 2 * kStep * HD + 128);
+
+        // ---- logits (and dp): columns are keys
+        float cf[2][4] = {};
+#pragma unroll
+        for (int w = 0; w < (GRAD ? 2 : 1); ++w)
+#pragma unroll
+            for (int c = 0; c < HD / 64; ++c) {
+                uint4 kq[2];
+#pragma unroll
+                for (int nt = 0; nt < 2; ++nt)
+                    kq[nt] = *reinterpret_cast<const uint4 *>((w == 0 ? sk_rows : sv_rows) + place<HD>(nt * 8 + g, c * 4 + t));
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const uint4 a = qf[(w * KS + c * 4 + u) * 32 + lane];
+#pragma unroll
+                    for (int nt = 0; nt < 2; ++nt) {
+                        const uint32_t y = u == 0 ? kq[nt].x : u == 1 ? kq[nt].y : u == 2 ? kq[nt].z : kq[nt].w;
+                        mma_f16(cf[nt], a, e4m3x2_to_half2(y & 0xFFFFu), e4m3x2_to_half2(y >> 16));
+                    }
+                }
+            }
+        // ---- the weights x of this lane's row for keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
+        float x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int key = (e >> 1) * 8 + 2 * t + (e & 1);
+            const float raw = fmaf(cf[e >> 1][2 + (e & 1)], 1.f / kLow, cf[e >> 1][e & 1]) * factor;
+            x[e] = raw * scales[is_dp ? 16 + key : key];
+        }
+        auto there = [&](int e) { return (mask >> ((e >> 1) * 8 + 2 * t + (e & 1))) & 1u; };
+        float alpha = 1.f;
+        if (!GRAD) {
+            float top = m;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) top = there(e) ? fmaxf(top, x[e]) : top;
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float ref = top == -INFINITY ? 0.f : top;
+            alpha = ex2(m - ref);
+            m = top;
+            l *= alpha;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int key = (e >> 1) * 8 + 2 * t + (e & 1);
+                const float w = there(e) ? ex2(x[e] - ref) : 0.f;
+                l += w;
+                x[e] = there(e) ? w * scales[16 + key] : 0.f;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int key = (e >> 1) * 8 + 2 * t + (e & 1);
+                const float own = is_dp ? x[e] : ex2(x[e] - norm);
+                const float other = __shfl_xor_sync(0xffffffffu, own, 16);   // dp for the rows of p and the other way round
+                const float w = there(e) ? (is_dp ? other : own * other) : 0.f;
+                if (!is_dp) {
+                    l += w;
+                    if (k0 + kStep * (warp + kWarps * i) + key == len - 1 && my_head < heads)
+                        p.newest[head0 + my_head] = there(e) ? make_float2(own, other) : make_float2(0.f, 0.f);
+                }
+                x[e] = there(e) ? w * scales[key] : 0.f;
+            }
+        }
+        uint32_t top = max(max(magnitude(x[0]), magnitude(x[1])), max(magnitude(x[2]), magnitude(x[3])));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+        top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+        const int grown = max(ex, int(top >> 23) - 127);
+        if (__any_sync(0xffffffffu, grown != ex || alpha != 1.f)) {
+            alpha *= pow2(max(ex - grown, -149));
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                acc[n][0] *= alpha; acc[n][1] *= alpha; acc[n][2] *= alpha; acc[n][3] *= alpha;
+            }
+            ex = grown;
+        }
+        const float down = pow2(-ex);
+        uint4 a;
+        halves(x[0] * down, x[1] * down, a.x, a.y);
+        halves(x[2] * down, x[3] * down, a.z, a.w);
+
+        // ---- sums over keys: the rows' bytes transposed, columns are dimensions
+        const uint8_t *rows = GRAD ? sk_rows : sv_rows;
+#pragma unroll
+        for (int c = 0; c < (HD > 128 ? 2 : 1); ++c) {
+            constexpr int W = HD == 64 ? 2 : 4;                // words a lane takes of a row: dimensions 4 W n ..
+            uint32_t v[4][W];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int r = (e >> 1) * 8 + 2 * t + (e & 1);
+                if (HD == 64) {
+                    const uint2 y = *reinterpret_cast<const uint2 *>(rows + place<HD>(r, g >> 1) + (g & 1) * 8);
+                    v[e][0] = y.x;
+                    v[e][1] = y.y;
+                } else {
+                    const uint4 y = *reinterpret_cast<const uint4 *>(rows + place<HD>(r, c * 8 + g));
+                    v[e][0] = y.x;
+                    v[e][1] = y.y;
+                    v[e][W - 2] = y.z;
+                    v[e][W - 1] = y.w;
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {                  // bytes 2 h, 2 h + 1 of the word
+                    const uint32_t b0 = __byte_perm(v[0][w], v[1][w], h ? 0x7362 : 0x5140);
+                    const uint32_t b1 = __byte_perm(v[2][w], v[3][w], h ? 0x7362 : 0x5140);
+                    const int n = c * 16 + w * 4 + h * 2;
+                    mma_f16(acc[n], a, e4m3x2_to_half2(b0 & 0xFFFFu), e4m3x2_to_half2(b1 & 0xFFFFu));
+                    mma_f16(acc[n + 1], a, e4m3x2_to_half2(b0 >> 16), e4m3x2_to_half2(b1 >> 16));
+                }
+        }
+        __syncwarp();                                          // before this stage is copied over
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
+
+    // ---- the warps' sums join in shared memory: [warp][row][hd]
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+    __syncthreads();
+    if (t == 0) {
+        s_m[warp][g] = m;
+        s_l[warp][g] = l;
+    }
+    float *all = reinterpret_cast<float *>(smem);
+    const float up = pow2(ex);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            // column 2 t + e of tile n: the byte that lane group 2 t + e took
+            const int d = HD == 64 ? (2 * t + e) * 8 + n : (n >> 4) * 128 + (2 * t + e) * 16 + (n & 15);
+            all[(warp * 8 + g) * HD + d] = fmaf(acc[n][2 + e], 1.f / kLow, acc[n][e]) * up;
+        }
+    __syncthreads();
+    const int64_t row0 = head0 * p.splits + split;             // of the first head's part
+    for (int e = threadIdx.x; e < 8 * HD; e += kWarps * 32) {
+        const int r = e / HD, d = e % HD;
+        const int h = GRAD ? r & 3 : r;
+        if (h >= heads || d >= hd) continue;
         float y = 0.f;
-        for (int w = 0; w < kWarps; ++w) y += sl[w] > 0.f || sl[w] != sl[w] ? so[w][d] * expf(sm[w] - top) : 0.f;
-        store_float(ctx + int64_t(blockIdx.x) * hd + d, total == 0.f ? 0.f : y / total);
-    }
-    if (threadIdx.x == 0) lse[blockIdx.x] = total == 0.f ? -INFINITY : top + logf(total);
-}
-
-// d_q = scale (sum p dp k - (sum p dp) (sum p k)); leaves D = sum p dp for the newest key's gradients.
-template <typename T>
-__global__ void __launch_bounds__(kWarps * 32) kv8_attn_backward_simple(tlb_kv8 c, Kv8Pages pg, int n_heads, float scale,
-                                                                        const T *__restrict__ q, const float *__restrict__ lse,
-                                                                        const T *__restrict__ d_ctx, T *__restrict__ d_q,
-                                                                        float *__restrict__ D) {
-    __shared__ float sd[kWarps], su[kWarps][256], sw[kWarps][256];
-    const int64_t b = blockIdx.x / n_heads;
-    const int h = int(blockIdx.x - b * n_heads), kvh = h / (n_heads / c.n_kv_heads), hd = c.head_dim;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, len = kv8_length(pg, b);
-    const float norm = lse[blockIdx.x];
-    float x[kDims], g[kDims], u[kDims] = {}, w[kDims] = {}, sum = 0.f;
+        if (!GRAD) {
+            float top = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < kDims; ++i) {
-        x[i] = lane + 32 * i < hd ? load_float(q + int64_t(blockIdx.x) * hd + lane + 32 * i) * scale : 0.f;
-        g[i] = lane + 32 * i < hd ? load_float(d_ctx + int64_t(blockIdx.x) * hd + lane + 32 * i) : 0.f;
-    }
-    for (int j = warp; j < len; j += kWarps) {
-        const int64_t slot = kv8_slot(pg, c.n_slots, b, j);
-        if (slot < 0) continue;
-        float k[kDims], v[kDims];
-        load_row(c.k, (slot * c.n_kv_heads + kvh) * hd, hd, lane, k);
-        load_row(c.v, (slot * c.n_kv_heads + kvh) * hd, hd, lane, v);
-        const float sk = c.k_scale[int64_t(kvh) * c.n_slots + slot], sv = c.v_scale[int64_t(kvh) * c.n_slots + slot];
-        const float p = expf(dot(x, k) * sk - norm), dp = dot(g, v) * sv;
-        sum += p * dp;
+            for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_m[w][r]);
+            const float ref = top == -INFINITY ? 0.f : top;
+            float total = 0.f;
 #pragma unroll
-        for (int i = 0; i < kDims; ++i) {
-            u[i] = fmaf(p * dp * sk, k[i], u[i]);
-            w[i] = fmaf(p * sk, k[i], w[i]);
+            for (int w = 0; w < kWarps; ++w) {
+                const float f = ex2(s_m[w][r] - ref);
+                y = fmaf(all[(w * 8 + r) * HD + d], f, y);
+                total = fmaf(s_l[w][r], f, total);
+            }
+            if (p.splits == 1) {
+                store_float(static_cast<T *>(p.out) + (head0 + h) * hd + d, total == 0.f ? 0.f : y / total);
+                if (d == 0) p.out_lse[head0 + h] = total == 0.f ? -INFINITY : fmaf(log2f(total), kLn2, top * kLn2);
+            } else {
+                p.part[(row0 + int64_t(h) * p.splits) * hd + d] = y;
+                if (d == 0) p.sums[row0 + int64_t(h) * p.splits] = make_float2(top, total);
+            }
+        } else {
+            float D = 0.f, z = 0.f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                y += all[(w * 8 + r) * HD + d];
+                D += s_l[w][h];
+            }
+            if (p.splits == 1) {
+                if (r >= 4) continue;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) z += all[(w * 8 + r + 4) * HD + d];
+                store_float(static_cast<T *>(p.out) + (head0 + h) * hd + d, p.scale * fmaf(-D, z, y));
+                if (d == 0) p.D[head0 + h] = D;
+            } else {
+                p.part[((row0 + int64_t(h) * p.splits) * 2 + (r >> 2)) * hd + d] = y;
+                if (d == 0 && r < 4) p.sums[row0 + int64_t(h) * p.splits] = make_float2(D, 0.f);
+            }
         }
     }
-    if (lane == 0) sd[warp] = sum;
+}
+
+// Joins the chunks of one query head, in order: groups of hd / 4 threads take every kJoinGroups-th.
+constexpr int kJoinThreads = 512;
+
+template <typename T, bool GRAD>
+__global__ void __launch_bounds__(kJoinThreads) kv8_attn_join_kernel(const __grid_constant__ AttnParams p) {
+    __shared__ __align__(16) float sum[kJoinThreads * 4 * (GRAD ? 2 : 1)];
+    __shared__ float red[32];
+    pdl_wait();
+    const int64_t row = blockIdx.x;
+    const int hd = p.c.head_dim, per = hd / 4, groups = kJoinThreads / per;
+    const int n = (kv8_length(p.pg, row / p.n_heads) + p.chunk - 1) / p.chunk;
+    const float2 *sums = p.sums + row * p.splits;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // the largest logit and the sum (gradient: D) of all chunks, the same in every thread
+    float top = -INFINITY, total = 0.f;
+    if (!GRAD) {
+        for (int s = threadIdx.x; s < n; s += kJoinThreads) top = fmaxf(top, __ldcg(sums + s).x);
 #pragma unroll
-    for (int i = 0; i < kDims; ++i) {
-        su[warp][lane + 32 * i] = u[i];
-        sw[warp][lane + 32 * i] = w[i];
+        for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        if (lane == 0) red[warp] = top;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, red[w]);
+    }
+    const float ref = top == -INFINITY ? 0.f : top;
+    for (int s = threadIdx.x; s < n; s += kJoinThreads) {
+        const float2 v = __ldcg(sums + s);
+        total += GRAD ? v.x : v.y * ex2(v.x - ref);
+    }
+    total = block_sum(total, red);
+
+    const int grp = threadIdx.x / per, d4 = (threadIdx.x - grp * per) * 4;
+    float4 y = make_float4(0.f, 0.f, 0.f, 0.f), z = y;
+    if (grp < groups) {
+        const float *part = p.part + row * p.splits * int64_t(hd) * (GRAD ? 2 : 1);
+#pragma unroll 4
+        for (int s = grp; s < n; s += groups) {
+            const float4 a = __ldcg(reinterpret_cast<const float4 *>(part + int64_t(s) * hd * (GRAD ? 2 : 1) + d4));
+            if (GRAD) {
+                const float4 c = __ldcg(reinterpret_cast<const float4 *>(part + (int64_t(s) * 2 + 1) * hd + d4));
+                y.x += a.x; y.y += a.y; y.z += a.z; y.w += a.w;
+                z.x += c.x; z.y += c.y; z.z += c.z; z.w += c.w;
+            } else {
+                const float f = ex2(__ldcg(sums + s).x - ref);
+                y.x = fmaf(a.x, f, y.x); y.y = fmaf(a.y, f, y.y); y.z = fmaf(a.z, f, y.z); y.w = fmaf(a.w, f, y.w);
+            }
+        }
+        reinterpret_cast<float4 *>(sum)[threadIdx.x] = y;
+        if (GRAD) reinterpret_cast<float4 *>(sum)[kJoinThreads + threadIdx.x] = z;
     }
     __syncthreads();
-    sum = 0.f;
-    for (int i = 0; i < kWarps; ++i) sum += sd[i];
-    for (int d = threadIdx.x; d < hd; d += blockDim.x) {
-        float a = 0.f, e = 0.f;
-        for (int i = 0; i < kWarps; ++i) { a += su[i][d]; e += sw[i][d]; }
-        store_float(d_q + int64_t(blockIdx.x) * hd + d, scale * (a - sum * e));
+    for (int d = threadIdx.x; d < hd; d += kJoinThreads) {
+        float a = 0.f, c = 0.f;
+        for (int i = 0; i < groups; ++i) {
+            a += sum[i * hd + d];
+            if (GRAD) c += sum[kJoinThreads * 4 + i * hd + d];
+        }
+        store_float(static_cast<T *>(p.out) + row * hd + d,
+                    GRAD ? p.scale * fmaf(-total, c, a) : total == 0.f ? 0.f : a / total);
     }
-    if (threadIdx.x == 0) D[blockIdx.x] = sum;
+    if (threadIdx.x == 0) {
+        if (GRAD) p.D[row] = total;
+        else p.out_lse[row] = total == 0.f ? -INFINITY : fmaf(log2f(total), kLn2, top * kLn2);
+    }
 }
 
-// Gradients of the newest key and value: a warp for each (sequence, KV head).
+// Gradients of the newest key and value from what the pass left of it: a CTA a (sequence, KV head).
 template <typename T>
-__global__ void __launch_bounds__(32) kv8_attn_newest_simple(tlb_kv8 c, Kv8Pages pg, int n_heads, float scale,
-                                                             const T *__restrict__ q, const float *__restrict__ lse,
-                                                             const T *__restrict__ d_ctx, const float *__restrict__ D,
-                                                             T *__restrict__ d_k, T *__restrict__ d_v) {
-    const int64_t b = blockIdx.x / c.n_kv_heads;
-    const int kvh = int(blockIdx.x - b * c.n_kv_heads), hd = c.head_dim, group = n_heads / c.n_kv_heads;
-    const int lane = threadIdx.x, len = kv8_length(pg, b);
-    const int64_t slot = len > 0 ? kv8_slot(pg, c.n_slots, b, len - 1) : -1;
-    float dk[kDims] = {}, dv[kDims] = {};
-    if (slot >= 0) {
-        float k[kDims], v[kDims];
-        load_row(c.k, (slot * c.n_kv_heads + kvh) * hd, hd, lane, k);
-        load_row(c.v, (slot * c.n_kv_heads + kvh) * hd, hd, lane, v);
-        const float sk = c.k_scale[int64_t(kvh) * c.n_slots + slot], sv = c.v_scale[int64_t(kvh) * c.n_slots + slot];
-        for (int e = 0; e < group; ++e) {
-            const int64_t row = b * n_heads + kvh * group + e;
-            float x[kDims], g[kDims];
-#pragma unroll
-            for (int i = 0; i < kDims; ++i) {
-                x[i] = lane + 32 * i < hd ? load_float(q + row * hd + lane + 32 * i) * scale : 0.f;
-                g[i] = lane + 32 * i < hd ? load_float(d_ctx + row * hd + lane + 32 * i) : 0.f;
+__global__ void __launch_bounds__(128) kv8_attn_newest_kernel(const __grid_constant__ AttnParams p, T *__restrict__ d_k,
+                                                              T *__restrict__ d_v) {
+    pdl_wait();
+    const int hd = p.c.head_dim, nkv = p.c.n_kv_heads;
+    const int64_t b = blockIdx.x / nkv, row0 = b * p.n_heads + int64_t(blockIdx.x - b * nkv) * p.group;
+    const bool any = kv8_length(p.pg, b) > 0;
+    for (int d = threadIdx.x; d < hd; d += blockDim.x) {
+        float dk = 0.f, dv = 0.f;
+        if (any)
+            for (int e = 0; e < p.group; ++e) {
+                const float2 w = __ldcg(p.newest + row0 + e);
+                const float ds = w.x * (w.y - __ldcg(p.D + row0 + e)) * p.scale;
+                // a weight of 0 adds nothing (a newest key that is not there)
+                if (ds != 0.f) dk = fmaf(ds, load_float(static_cast<const T *>(p.q) + (row0 + e) * hd + d), dk);
+                if (w.x != 0.f) dv = fmaf(w.x, load_float(static_cast<const T *>(p.d_ctx) + (row0 + e) * hd + d), dv);
             }
-            const float p = expf(dot(x, k) * sk - lse[row]), ds = p * (dot(g, v) * sv - D[row]);
-#pragma unroll
-            for (int i = 0; i < kDims; ++i) {
-                dk[i] = fmaf(ds, x[i], dk[i]);
-                dv[i] = fmaf(p, g[i], dv[i]);
-            }
-        }
+        store_float(d_k + int64_t(blockIdx.x) * hd + d, dk);
+        store_float(d_v + int64_t(blockIdx.x) * hd + d, dv);
     }
-#pragma unroll
-    for (int i = 0; i < kDims; ++i)
-        if (lane + 32 * i < hd) {
-            store_float(d_k + int64_t(blockIdx.x) * hd + lane + 32 * i, dk[i]);
-            store_float(d_v + int64_t(blockIdx.x) * hd + lane + 32 * i, dv[i]);
-        }
 }
 
 bool sizes_ok(const tlb_kv8 *c, int64_t n_seq, int32_t n_heads, int64_t max_len) {
     return c != nullptr && n_seq >= 0 && max_len >= 0 && max_len <= (int64_t(1) << 30) && n_heads >= 1 && c->n_kv_heads >= 1 &&
            n_heads % c->n_kv_heads == 0 && n_heads <= 65535 && n_seq <= (int64_t(1) << 30) / n_heads && c->head_dim >= 1 &&
-           c->head_dim % 16 == 0 && c->head_dim <= 256;
+           c->head_dim % 16 == 0 && c->head_dim <= 256 && c->n_slots < (int64_t(1) << 31);
+}
+
+// Chunks of keys.  Four for each of three CTAs an SM where there are keys enough, so that the last ones end together,
+// but of 64 keys at least (a step of each warp) and 512 at most: lengths are only known on the device, and a
+// long sequence among short ones has to be spread.  65536 CTAs at most, which bounds the workspace.
+struct Split {
+    int tiles, splits, chunk;
+    int64_t units;
+};
+
+Split split_of(const tlb_kv8 &c, int64_t n_seq, int n_heads, int64_t max_len, bool grad) {
+    const int group = n_heads / c.n_kv_heads;
+    Split s;
+    s.tiles = int(ceil_div(group, tile_heads(grad)));
+    s.units = n_seq * c.n_kv_heads * s.tiles;
+    const int64_t keys = s.units * max_len, per = int64_t(kStep) * kWarps;
+    int64_t chunk = ceil_div(keys, int64_t(num_sms()) * 12);
+    chunk = chunk < per ? per : chunk > 512 ? 512 : chunk;
+    const int64_t least = ceil_div(keys, 65536);
+    chunk = ceil_div(chunk > least ? chunk : least, per) * per;
+    const int64_t all = ceil_div(max_len > 1 ? max_len : 1, per) * per;
+    if (chunk > all) chunk = all;
+    s.chunk = int(chunk);
+    s.splits = int(ceil_div(max_len > 1 ? max_len : 1, chunk));
+    return s;
+}
+
+struct Layout {
+    size_t part, sums, newest, D, bytes;
+};
+
+Layout layout_of(const tlb_kv8 &c, int64_t n_seq, int n_heads, int64_t max_len, bool grad) {
+    const Split s = split_of(c, n_seq, n_heads, max_len, grad);
+    WsPlan p;
+    Layout l{};
+    const size_t rows = size_t(n_seq) * n_heads;
+    if (s.splits > 1) {
+        l.part = p.take(rows * s.splits * c.head_dim * (grad ? 2 : 1) * sizeof(float));
+        l.sums = p.take(rows * s.splits * sizeof(float2));
+    }
+    if (grad) {
+        l.newest = p.take(rows * sizeof(float2));
+        l.D = p.take(rows * sizeof(float));
+    }
+    l.bytes = p.off;
+    return l;
 }
 
 size_t ws_bytes_of(const tlb_kv8 *c, int64_t n_seq, int32_t n_heads, int64_t max_len, bool grad) {
     if (!sizes_ok(c, n_seq, n_heads, max_len)) return 0;
-    WsPlan p;
-    if (grad) p.take(size_t(n_seq) * n_heads * 4);
-    return p.off;
+    const size_t fwd = layout_of(*c, n_seq, n_heads, max_len, false).bytes;
+    const size_t bwd = grad ? layout_of(*c, n_seq, n_heads, max_len, true).bytes : 0;
+    return fwd > bwd ? fwd : bwd;
+}
+
+template <typename T, int HD, bool GRAD>
+int attn_launch(const AttnParams &p, int64_t n_seq, const Split &s, cudaStream_t st) {
+    auto kernel = kv8_attn_kernel<T, HD, GRAD>;
+    constexpr int smem = smem_bytes<HD, GRAD>();
+    static_assert(smem >= kWarps * 8 * HD * 4, "the warps' sums fit where the stages were");
+    TLB_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    kernel<<<unsigned(s.units * s.splits), kWarps * 32, smem, st>>>(p);
+    TLB_TRY(check_launch(GRAD ? "kv8_attn_backward" : "kv8_attn_forward"));
+    if (s.splits == 1) return TLB_OK;
+    TLB_CUDA(launch_dependent(kv8_attn_join_kernel<T, GRAD>, dim3(unsigned(n_seq * p.n_heads)), dim3(kJoinThreads), 0, st, p));
+    return check_launch("kv8_attn_join");
+}
+
+template <typename T, bool GRAD>
+int attn_run(const AttnParams &p, int64_t n_seq, const Split &s, cudaStream_t st) {
+    return p.c.head_dim <= 64 ? attn_launch<T, 64, GRAD>(p, n_seq, s, st)
+           : p.c.head_dim <= 128 ? attn_launch<T, 128, GRAD>(p, n_seq, s, st)
+                                 : attn_launch<T, 256, GRAD>(p, n_seq, s, st);
+}
+
+AttnParams params_of(const tlb_kv8 &c, const Kv8Pages &pg, int n_heads, const Split &s, const Layout &l, float scale, const void *q,
+                     void *ws) {
+    AttnParams p{};
+    p.c = c;
+    p.pg = pg;
+    p.n_heads = n_heads;
+    p.group = n_heads / c.n_kv_heads;
+    p.tiles = s.tiles;
+    p.splits = s.splits;
+    p.chunk = s.chunk;
+    p.scale = scale;
+    p.q = q;
+    p.part = ws_at<float>(ws, l.part);
+    p.sums = ws_at<float2>(ws, l.sums);
+    p.newest = ws_at<float2>(ws, l.newest);
+    p.D = ws_at<float>(ws, l.D);
+    return p;
 }
 
 // Checks that both calls share; fills pg.
@@ -211,15 +620,12 @@ int tlb_kv8_attn_forward(const tlb_kv8 *cache, const int32_t *pages, int64_t max
     if (n_seq == 0) return TLB_OK;
     TLB_REQUIRE(ctx && lse, TLB_EINVAL, "kv8_attn_forward: null pointer");
     TLB_REQUIRE(aligned16(ctx), TLB_EINVAL, "kv8_attn_forward: ctx must be 16-byte aligned");
-    cudaStream_t st = as_stream(stream);
-    const unsigned grid = unsigned(n_seq * n_heads);
-    if (type == TLB_W_F32)
-        kv8_attn_forward_simple<<<grid, kWarps * 32, 0, st>>>(*cache, pg, n_heads, scale, static_cast<const float *>(q),
-                                                              static_cast<float *>(ctx), lse);
-    else
-        kv8_attn_forward_simple<<<grid, kWarps * 32, 0, st>>>(*cache, pg, n_heads, scale, static_cast<const __nv_bfloat16 *>(q),
-                                                              static_cast<__nv_bfloat16 *>(ctx), lse);
-    return check_launch("kv8_attn_forward");
+    const Split sp = split_of(*cache, n_seq, n_heads, max_len, false);
+    AttnParams p = params_of(*cache, pg, n_heads, sp, layout_of(*cache, n_seq, n_heads, max_len, false), scale, q, ws);
+    p.out = ctx;
+    p.out_lse = lse;
+    return type == TLB_W_F32 ? attn_run<float, false>(p, n_seq, sp, as_stream(stream))
+                             : attn_run<__nv_bfloat16, false>(p, n_seq, sp, as_stream(stream));
 }
 
 int tlb_kv8_attn_backward(const tlb_kv8 *cache, const int32_t *pages, int64_t max_pages, int32_t page,
@@ -234,20 +640,23 @@ int tlb_kv8_attn_backward(const tlb_kv8 *cache, const int32_t *pages, int64_t ma
     TLB_REQUIRE(lse && d_ctx && d_q && d_k && d_v, TLB_EINVAL, "kv8_attn_backward: null pointer");
     TLB_REQUIRE(aligned16(d_ctx) && aligned16(d_q) && aligned16(d_k) && aligned16(d_v), TLB_EINVAL,
                 "kv8_attn_backward: d_ctx, d_q, d_k and d_v must be 16-byte aligned");
+    const Split sp = split_of(*cache, n_seq, n_heads, max_len, true);
+    AttnParams p = params_of(*cache, pg, n_heads, sp, layout_of(*cache, n_seq, n_heads, max_len, true), scale, q, ws);
+    p.lse = lse;
+    p.d_ctx = d_ctx;
+    p.out = d_q;
     cudaStream_t st = as_stream(stream);
-    float *D = ws_at<float>(ws, kStatusBytes);
-    auto run = [&](auto t) {
-        using T = decltype(t);
-        kv8_attn_backward_simple<T><<<unsigned(n_seq * n_heads), kWarps * 32, 0, st>>>(
-            *cache, pg, n_heads, scale, static_cast<const T *>(q), lse, static_cast<const T *>(d_ctx), static_cast<T *>(d_q), D);
-        const int rc = check_launch("kv8_attn_backward");
-        if (rc != TLB_OK) return rc;
-        kv8_attn_newest_simple<T><<<unsigned(n_seq * cache->n_kv_heads), 32, 0, st>>>(
-            *cache, pg, n_heads, scale, static_cast<const T *>(q), lse, static_cast<const T *>(d_ctx), D, static_cast<T *>(d_k),
-            static_cast<T *>(d_v));
-        return check_launch("kv8_attn_newest");
-    };
-    return type == TLB_W_F32 ? run(float()) : run(__nv_bfloat16());
+    const dim3 grid(unsigned(n_seq * cache->n_kv_heads));
+    if (type == TLB_W_F32) {
+        TLB_TRY((attn_run<float, true>(p, n_seq, sp, st)));
+        TLB_CUDA(launch_dependent(kv8_attn_newest_kernel<float>, grid, dim3(128), 0, st, p, static_cast<float *>(d_k),
+                                  static_cast<float *>(d_v)));
+    } else {
+        TLB_TRY((attn_run<__nv_bfloat16, true>(p, n_seq, sp, st)));
+        TLB_CUDA(launch_dependent(kv8_attn_newest_kernel<__nv_bfloat16>, grid, dim3(128), 0, st, p,
+                                  static_cast<__nv_bfloat16 *>(d_k), static_cast<__nv_bfloat16 *>(d_v)));
+    }
+    return check_launch("kv8_attn_newest");
 }
 
 }  // extern "C"
