@@ -44,6 +44,12 @@ __device__ __forceinline__ uint32_t e4m3x2_to_half2(uint32_t v) {
     asm("{\n\t.reg .b16 h;\n\tcvt.u16.u32 h, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, h;\n\t}" : "=r"(r) : "r"(v));
     return r;
 }
+// Four e4m3 values as two pairs of halves: the lower two, the upper two.
+__device__ __forceinline__ void e4m3x4_to_half2(uint32_t v, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(v));
+}
 __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t v) {
     const uint32_t h = e4m3x2_to_half2(v);
     return __half22float2(*reinterpret_cast<const __half2 *>(&h));

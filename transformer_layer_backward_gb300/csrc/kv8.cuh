@@ -16,6 +16,7 @@ struct Kv8Pages {
     int64_t max_pages;
     int32_t page;
     int32_t max_len;             // min(max_len, max_pages * page): no key from here on
+    int32_t shift;               // page = 2^shift, or -1
 };
 
 // Keys of sequence b.
@@ -23,7 +24,7 @@ __device__ __forceinline__ int kv8_length(const Kv8Pages &p, int64_t b) { return
 
 // Slot of key j of sequence b, or -1 where the cache has none.
 __device__ __forceinline__ int64_t kv8_slot(const Kv8Pages &p, int64_t n_slots, int64_t b, int j) {
-    const int at = j / p.page;
+    const int at = p.shift >= 0 ? j >> p.shift : j / p.page;
     const int64_t slot = int64_t(__ldg(p.pages + b * p.max_pages + at)) * p.page + (j - at * p.page);
     return slot >= 0 && slot < n_slots ? slot : -1;
 }

@@ -2,7 +2,7 @@
 //
 // Bound by the read of the keys and values, once.  What a CTA (four warps) does for a chunk of one sequence's keys, one
 // KV head and a tile of the query heads that share it, 16 keys a warp at a time:
-//   - cp.async brings the keys', values' and scales' bytes to shared memory, two steps ahead; keys that
+//   - cp.async brings the keys', values' and scales' bytes to shared memory, a step ahead; keys that
 //     are not there come as zeros, so that nothing of what a free slot holds is met;
 //   - s = q k and (gradient) dp = d_ctx v are products of mma.sync m16n8k16 with the keys as columns: e4m3 values
 //     are halves exactly, and a query is two of them, the second holding what the first leaves times 2^12 (rows g
@@ -10,7 +10,7 @@
 //     operands as they are, the query's columns being ordered to match;
 //   - the sums over keys (p v; p dp k and p k) take the weights x in the same two halves, scaled by a
 //     power of two of each row that grows with the largest |x| so far, and the rows' bytes transposed
-//     by byte permutes: 23 bits of each weight, 37 below the largest.
+//     by byte permutes: 23 bits of each weight, 34 below the largest at least.
 // The gradient uses d_q = scale (sum p dp k - (sum p dp)(sum p k)), so that one pass does.  Rows of the gradient's
 // tile: four heads' s (and p dp) in rows 0..3, their dp (and p) in rows 4..7; of the forward's: eight heads.
 // Warps, then chunks (a second kernel), are joined in a fixed order.
@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kStep = 16;                // keys of a warp's step
-constexpr int kStages = 3;
+constexpr int kStages = 2;               // one step ahead: four CTAs an SM keep 70 KB on their way (three stages and three CTAs: slower)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kLow = 4096.f;           // the second half of a value holds what the first leaves, times this
 
@@ -130,7 +130,7 @@ __device__ __forceinline__ void stage_rows(const T *rows, int n, int hd, int fir
 }
 
 template <typename T, int HD, bool GRAD>
-__global__ void __launch_bounds__(kWarps * 32) kv8_attn_kernel(const __grid_constant__ AttnParams p) {
+__global__ void __launch_bounds__(kWarps * 32, HD <= 128 ? 4 : 2) kv8_attn_kernel(const __grid_constant__ AttnParams p) {
     constexpr int HT = tile_heads(GRAD), KS = HD / 16, NT = HD / 8;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ int s_f[2][8];
@@ -157,21 +157,27 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attn_kernel(const __grid_cons
         return i < mine && j < k1 ? int(kv8_slot(p.pg, p.c.n_slots, b, j)) : -1;
     };
     int slot = slot_of(0);
+    // this lane's piece of a row, and the rows r0, r0 + 512 / HD, .. of a step
+    constexpr int PER = HD / 16;
+    const int ch = lane % PER, r0 = lane / PER;
+    const bool in_row = ch * 16 < hd;
+    const int64_t first = int64_t(kvh) * hd + (in_row ? ch * 16 : 0);
+    const uint8_t *kb = p.c.k + first, *vb = p.c.v + first;
+    const int row_stride = nkv * hd;
+    const float *sb = (lane < 16 ? p.c.k_scale : p.c.v_scale) + int64_t(kvh) * p.c.n_slots;
     auto issue = [&](int i) {
         if (i < mine) {
             const uint32_t st = ring + (i % kStages) * stage_bytes<HD>();
             const int mask = int(__ballot_sync(0xffffffffu, slot >= 0));
 #pragma unroll
-            for (int c = 0; c < kStep * HD / 16 / 32; ++c) {
-                const int e = c * 32 + lane, r = e / (HD / 16), ch = e % (HD / 16);
-                const int sl = __shfl_sync(0xffffffffu, slot, r);
-                const bool ok = sl >= 0 && ch * 16 < hd;
-                const int64_t at = (int64_t(ok ? sl : 0) * nkv + kvh) * hd + (ok ? ch * 16 : 0);
-                copy16(st + place<HD>(r, ch), p.c.k + at, ok);
-                copy16(st + kStep * HD + place<HD>(r, ch), p.c.v + at, ok);
+            for (int c = 0; c < kStep * PER / 32; ++c) {
+                const int r = c * (32 / PER) + r0, sl = __shfl_sync(0xffffffffu, slot, r);
+                const bool ok = sl >= 0 && in_row;
+                const int64_t at = int64_t(max(sl, 0)) * row_stride;
+                copy16(st + place<HD>(r, ch), kb + at, ok);
+                copy16(st + kStep * HD + place<HD>(r, ch), vb + at, ok);
             }
-            const int64_t at = int64_t(kvh) * p.c.n_slots + max(slot, 0);
-            copy4(st + 2 * kStep * HD + lane * 4, (lane < 16 ? p.c.k_scale : p.c.v_scale) + at, slot >= 0);
+            copy4(st + 2 * kStep * HD + lane * 4, sb + max(slot, 0), slot >= 0);
             if (lane == 0)
                 asm volatile("st.shared.u32 [%0], %1;" ::"r"(st + 2 * kStep * HD + 128), "r"(mask) : "memory");
         }
@@ -207,7 +213,7 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attn_kernel(const __grid_cons
         const uint32_t mask = *reinterpret_cast<const uint32_t *>(st + 2 * kStep * HD + 128);
 
         // ---- logits (and dp): columns are keys
-        float cf[2][4] = {};
+        float cf[2][4], part[2][2][4] = {};                    // [chain][tile of 8 keys]: two chains of products at least
 #pragma unroll
         for (int w = 0; w < (GRAD ? 2 : 1); ++w)
 #pragma unroll
@@ -221,11 +227,16 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attn_kernel(const __grid_cons
                     const uint4 a = qf[(w * KS + c * 4 + u) * 32 + lane];
 #pragma unroll
                     for (int nt = 0; nt < 2; ++nt) {
-                        const uint32_t y = u == 0 ? kq[nt].x : u == 1 ? kq[nt].y : u == 2 ? kq[nt].z : kq[nt].w;
-                        mma_f16(cf[nt], a, e4m3x2_to_half2(y & 0xFFFFu), e4m3x2_to_half2(y >> 16));
+                        uint32_t b0, b1;
+                        e4m3x4_to_half2(u == 0 ? kq[nt].x : u == 1 ? kq[nt].y : u == 2 ? kq[nt].z : kq[nt].w, b0, b1);
+                        mma_f16(part[u & 1][nt], a, b0, b1);
                     }
                 }
             }
+#pragma unroll
+        for (int nt = 0; nt < 2; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) cf[nt][e] = part[0][nt][e] + part[1][nt][e];
         // ---- the weights x of this lane's row for keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
         float x[4];
 #pragma unroll
@@ -242,10 +253,13 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attn_kernel(const __grid_cons
             for (int e = 0; e < 4; ++e) top = there(e) ? fmaxf(top, x[e]) : top;
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float ref = top == -INFINITY ? 0.f : top;
-            alpha = ex2(m - ref);
-            m = top;
-            l *= alpha;
+            // the reference follows the largest logit when that is 2^8 beyond it: until then weights are up to 2^8
+            if (top > m + 8.f || m == -INFINITY) {
+                alpha = top == -INFINITY ? 1.f : ex2(m - top);
+                m = top;
+                l *= alpha;
+            }
+            const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int key = (e >> 1) * 8 + 2 * t + (e & 1);
@@ -271,7 +285,8 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attn_kernel(const __grid_cons
         uint32_t top = max(max(magnitude(x[0]), magnitude(x[1])), max(magnitude(x[2]), magnitude(x[3])));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        const int grown = max(ex, int(top >> 23) - 127);
+        // with room for weights of eight times the size, so that the sums are seldom turned to a new power
+        const int grown = int(top >> 23) - 127 > ex ? int(top >> 23) - 124 : ex;
         if (__any_sync(0xffffffffu, grown != ex || alpha != 1.f)) {
             alpha *= pow2(max(ex - grown, -149));
 #pragma unroll
@@ -313,8 +328,11 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attn_kernel(const __grid_cons
                     const uint32_t b0 = __byte_perm(v[0][w], v[1][w], h ? 0x7362 : 0x5140);
                     const uint32_t b1 = __byte_perm(v[2][w], v[3][w], h ? 0x7362 : 0x5140);
                     const int n = c * 16 + w * 4 + h * 2;
-                    mma_f16(acc[n], a, e4m3x2_to_half2(b0 & 0xFFFFu), e4m3x2_to_half2(b1 & 0xFFFFu));
-                    mma_f16(acc[n + 1], a, e4m3x2_to_half2(b0 >> 16), e4m3x2_to_half2(b1 >> 16));
+                    uint32_t lo0, hi0, lo1, hi1;
+                    e4m3x4_to_half2(b0, lo0, hi0);
+                    e4m3x4_to_half2(b1, lo1, hi1);
+                    mma_f16(acc[n], a, lo0, lo1);
+                    mma_f16(acc[n + 1], a, hi0, hi1);
                 }
         }
         __syncwarp();                                          // before this stage is copied over
@@ -386,18 +404,20 @@ __global__ void __launch_bounds__(kWarps * 32) kv8_attn_kernel(const __grid_cons
     }
 }
 
-// Joins the chunks of one query head, in order: groups of hd / 4 threads take every kJoinGroups-th.
-constexpr int kJoinThreads = 512;
+// Joins the chunks of 32 dimensions of one query head, in a fixed order: 16 groups of eight lanes take every 16th.
+constexpr int kJoinThreads = 128, kJoinDims = 32;
 
 template <typename T, bool GRAD>
 __global__ void __launch_bounds__(kJoinThreads) kv8_attn_join_kernel(const __grid_constant__ AttnParams p) {
-    __shared__ __align__(16) float sum[kJoinThreads * 4 * (GRAD ? 2 : 1)];
+    constexpr int kGroups = kJoinThreads / 8;
+    __shared__ float sum[GRAD ? 2 : 1][kGroups][kJoinDims];
     __shared__ float red[32];
     pdl_wait();
     const int64_t row = blockIdx.x;
-    const int hd = p.c.head_dim, per = hd / 4, groups = kJoinThreads / per;
+    const int hd = p.c.head_dim;
     const int n = (kv8_length(p.pg, row / p.n_heads) + p.chunk - 1) / p.chunk;
     const float2 *sums = p.sums + row * p.splits;
+    const int grp = threadIdx.x >> 3, dim = int(blockIdx.y) * kJoinDims + (threadIdx.x & 7) * 4;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // the largest logit and the sum (gradient: D) of all chunks, the same in every thread
     float top = -INFINITY, total = 0.f;
@@ -415,38 +435,41 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_attn_join_kernel(const __gri
         const float2 v = __ldcg(sums + s);
         total += GRAD ? v.x : v.y * ex2(v.x - ref);
     }
-    total = block_sum(total, red);
-
-    const int grp = threadIdx.x / per, d4 = (threadIdx.x - grp * per) * 4;
     float4 y = make_float4(0.f, 0.f, 0.f, 0.f), z = y;
-    if (grp < groups) {
-        const float *part = p.part + row * p.splits * int64_t(hd) * (GRAD ? 2 : 1);
-#pragma unroll 4
-        for (int s = grp; s < n; s += groups) {
-            const float4 a = __ldcg(reinterpret_cast<const float4 *>(part + int64_t(s) * hd * (GRAD ? 2 : 1) + d4));
+    if (dim < hd) {
+        const float *part = p.part + row * p.splits * int64_t(hd) * (GRAD ? 2 : 1) + dim;
+#pragma unroll 8
+        for (int s = grp; s < n; s += kGroups) {
+            const float4 a = __ldcg(reinterpret_cast<const float4 *>(part + int64_t(s) * hd * (GRAD ? 2 : 1)));
             if (GRAD) {
-                const float4 c = __ldcg(reinterpret_cast<const float4 *>(part + (int64_t(s) * 2 + 1) * hd + d4));
+                const float4 c = __ldcg(reinterpret_cast<const float4 *>(part + (int64_t(s) * 2 + 1) * hd));
                 y.x += a.x; y.y += a.y; y.z += a.z; y.w += a.w;
                 z.x += c.x; z.y += c.y; z.z += c.z; z.w += c.w;
             } else {
-                const float f = ex2(__ldcg(sums + s).x - ref);
+                const float f = ex2(__ldcg(&sums[s].x) - ref);
                 y.x = fmaf(a.x, f, y.x); y.y = fmaf(a.y, f, y.y); y.z = fmaf(a.z, f, y.z); y.w = fmaf(a.w, f, y.w);
             }
         }
-        reinterpret_cast<float4 *>(sum)[threadIdx.x] = y;
-        if (GRAD) reinterpret_cast<float4 *>(sum)[kJoinThreads + threadIdx.x] = z;
     }
-    __syncthreads();
-    for (int d = threadIdx.x; d < hd; d += kJoinThreads) {
+    const int at = (threadIdx.x & 7) * 4;
+    sum[0][grp][at] = y.x; sum[0][grp][at + 1] = y.y; sum[0][grp][at + 2] = y.z; sum[0][grp][at + 3] = y.w;
+    if (GRAD) {
+        constexpr int w = GRAD ? 1 : 0;
+        sum[w][grp][at] = z.x; sum[w][grp][at + 1] = z.y; sum[w][grp][at + 2] = z.z; sum[w][grp][at + 3] = z.w;
+    }
+    total = block_sum(total, red);                            // (and every thread's sums are there)
+    const int d = int(blockIdx.y) * kJoinDims + threadIdx.x;
+    if (threadIdx.x < kJoinDims && d < hd) {
         float a = 0.f, c = 0.f;
-        for (int i = 0; i < groups; ++i) {
-            a += sum[i * hd + d];
-            if (GRAD) c += sum[kJoinThreads * 4 + i * hd + d];
+#pragma unroll
+        for (int i = 0; i < kGroups; ++i) {
+            a += sum[0][i][threadIdx.x];
+            if (GRAD) c += sum[GRAD ? 1 : 0][i][threadIdx.x];
         }
         store_float(static_cast<T *>(p.out) + row * hd + d,
                     GRAD ? p.scale * fmaf(-total, c, a) : total == 0.f ? 0.f : a / total);
     }
-    if (threadIdx.x == 0) {
+    if (threadIdx.x == 0 && blockIdx.y == 0) {
         if (GRAD) p.D[row] = total;
         else p.out_lse[row] = total == 0.f ? -INFINITY : fmaf(log2f(total), kLn2, top * kLn2);
     }
@@ -481,9 +504,9 @@ bool sizes_ok(const tlb_kv8 *c, int64_t n_seq, int32_t n_heads, int64_t max_len)
            c->head_dim % 16 == 0 && c->head_dim <= 256 && c->n_slots < (int64_t(1) << 31);
 }
 
-// Chunks of keys.  Four for each of three CTAs an SM where there are keys enough, so that the last ones end together,
-// but of 64 keys at least (a step of each warp) and 512 at most: lengths are only known on the device, and a
-// long sequence among short ones has to be spread.  65536 CTAs at most, which bounds the workspace.
+// Chunks of keys.  One sequence: as long as gives four CTAs an SM (their queries and sums cost as much as some steps).
+// More: 512 keys at most, since lengths are only known on the device, and a long sequence among short ones has to
+// be spread.  64 keys at least (a step of each warp), and 65536 CTAs at most, which bounds the workspace.
 struct Split {
     int tiles, splits, chunk;
     int64_t units;
@@ -495,8 +518,9 @@ Split split_of(const tlb_kv8 &c, int64_t n_seq, int n_heads, int64_t max_len, bo
     s.tiles = int(ceil_div(group, tile_heads(grad)));
     s.units = n_seq * c.n_kv_heads * s.tiles;
     const int64_t keys = s.units * max_len, per = int64_t(kStep) * kWarps;
-    int64_t chunk = ceil_div(keys, int64_t(num_sms()) * 12);
-    chunk = chunk < per ? per : chunk > 512 ? 512 : chunk;
+    int64_t chunk = ceil_div(keys, int64_t(num_sms()) * 4);
+    if (n_seq > 1 && chunk > 512) chunk = 512;
+    if (chunk < per) chunk = per;
     const int64_t least = ceil_div(keys, 65536);
     chunk = ceil_div(chunk > least ? chunk : least, per) * per;
     const int64_t all = ceil_div(max_len > 1 ? max_len : 1, per) * per;
@@ -543,7 +567,8 @@ int attn_launch(const AttnParams &p, int64_t n_seq, const Split &s, cudaStream_t
     kernel<<<unsigned(s.units * s.splits), kWarps * 32, smem, st>>>(p);
     TLB_TRY(check_launch(GRAD ? "kv8_attn_backward" : "kv8_attn_forward"));
     if (s.splits == 1) return TLB_OK;
-    TLB_CUDA(launch_dependent(kv8_attn_join_kernel<T, GRAD>, dim3(unsigned(n_seq * p.n_heads)), dim3(kJoinThreads), 0, st, p));
+    const dim3 grid(unsigned(n_seq * p.n_heads), unsigned(ceil_div(p.c.head_dim, kJoinDims)));
+    TLB_CUDA(launch_dependent(kv8_attn_join_kernel<T, GRAD>, grid, dim3(kJoinThreads), 0, st, p));
     return check_launch("kv8_attn_join");
 }
 
@@ -594,7 +619,10 @@ int check_call(const char *what, const tlb_kv8 *cache, const int32_t *pages, int
     TLB_REQUIRE((reinterpret_cast<uintptr_t>(ws) & 255) == 0, TLB_EINVAL, "%s: workspace must be 256-byte aligned", what);
     int64_t most = max_len;
     if (max_pages < (int64_t(1) << 31)) most = most < max_pages * page ? most : max_pages * page;
-    pg = Kv8Pages{pages, lengths, max_pages, page, int32_t(most)};
+    int shift = -1;
+    if ((page & (page - 1)) == 0)
+        for (shift = 0; (1 << shift) < page;) ++shift;
+    pg = Kv8Pages{pages, lengths, max_pages, page, int32_t(most), shift};
     return TLB_OK;
 }
 
