@@ -142,7 +142,7 @@ class TlbError(RuntimeError):
 
 
 def call(name: str, *args) -> int:
-    lib = load()
+    lib = _lib or load()
     rc = getattr(lib, name)(*args)
     if rc != TLB_OK:
         raise TlbError(rc, name, lib.tlb_last_error().decode())

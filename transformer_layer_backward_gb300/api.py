@@ -29,6 +29,8 @@ def _queued(t, stream=None):
     queued on, to which what is allocated meanwhile then belongs."""
     if not t.is_cuda:
         return _NO_GUARD
+    if stream is None and t.device.index == torch._C._cuda_getDevice():
+        return _NO_GUARD
     if isinstance(stream, torch.cuda.Stream):
         if stream.device != t.device:
             raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, t.device))
@@ -315,8 +317,15 @@ _FP8_BLOCK = 128
 _E4M3 = torch.float8_e4m3fn
 
 
+def _raw_stream(stream, device):
+    """The stream's address, the current one of the device where none is given (a guard of _queued() set it)."""
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
+
+
 def _at(t, shape, dtype, device, name):
     """Address of a contiguous tensor of this shape (None: any), type and device."""
+    if t.dtype is dtype and t.is_contiguous() and t.device == device and (shape is None or t.shape == shape) and t.is_cuda:
+        return t.data_ptr()
     if t.dtype != dtype:
         raise TypeError("%s must be %s, got %s" % (name, dtype, t.dtype))
     if shape is not None and t.shape != shape:
@@ -350,7 +359,7 @@ def fp8_quantize(x, block_rows=1, q=None, scales=None, stream=None):
         q = torch.empty(rows, cols, dtype=_E4M3, device=x.device) if q is None else q
         scales = torch.empty(blocks, dtype=torch.float32, device=x.device) if scales is None else scales
         A.call("tlb_fp8_quantize", code, _at(x, None, x.dtype, x.device, "x"), rows, cols, int(block_rows),
-               _at(q, x.shape, _E4M3, x.device, "q"), _at(scales, blocks, torch.float32, x.device, "scales"), _stream(stream))
+               _at(q, x.shape, _E4M3, x.device, "q"), _at(scales, blocks, torch.float32, x.device, "scales"), _raw_stream(stream, x.device))
     return q, scales
 
 
@@ -380,7 +389,7 @@ def linear_fp8_backward(W, w_scales, dY, dy_scales, out=None, accumulate=False, 
                _at(w_scales, (-(-in_dim // _FP8_BLOCK), columns), torch.float32, dev, "w_scales"),
                _at(dY, None, _E4M3, dev, "dY"), _at(dy_scales, (S, columns), torch.float32, dev, "dy_scales"), S, out_dim, in_dim,
                code, _at(out, (S, in_dim), dtype, dev, "out"), 1 if accumulate else 0,
-               _at(ws, None, torch.uint8, dev, "ws"), ws.numel(), _stream(stream))
+               _at(ws, None, torch.uint8, dev, "ws"), ws.numel(), _raw_stream(stream, dev))
         if own:
             _keep_status(ws)
     return out
@@ -421,7 +430,7 @@ def kv8_write(cache, k, v, slots, stream=None):
             raise ValueError("%s: the values of a head must be dense" % name)
     with _queued(k, stream):
         A.call("tlb_kv8_write", cache, code, k.data_ptr(), k.stride(0), k.stride(1), v.data_ptr(), v.stride(0), v.stride(1),
-               _at(slots, (rows,), torch.int64, cache.device, "slots"), rows, _stream(stream))
+               _at(slots, (rows,), torch.int64, cache.device, "slots"), rows, _raw_stream(stream, cache.device))
 
 
 def kv8_read(cache, slots, dtype=torch.float32, kv_layout="shd", k=None, v=None, stream=None):
@@ -440,7 +449,7 @@ def kv8_read(cache, slots, dtype=torch.float32, kv_layout="shd", k=None, v=None,
         v = torch.empty(shape, dtype=dtype, device=cache.device) if v is None else v
         strides = (n_kv * hd, hd) if kv_layout == "shd" else (hd, rows * hd)
         A.call("tlb_kv8_read", cache, _at(slots, (rows,), torch.int64, cache.device, "slots"), rows, code,
-               _at(k, shape, dtype, cache.device, "k"), _at(v, shape, dtype, cache.device, "v"), *strides, _stream(stream))
+               _at(k, shape, dtype, cache.device, "k"), _at(v, shape, dtype, cache.device, "v"), *strides, _raw_stream(stream, cache.device))
     return k, v
 
 
@@ -477,7 +486,7 @@ def kv8_attn_forward(cache, q, pages, page, lengths, max_len, scale=None, ctx=No
         A.call("tlb_kv8_attn_forward", cache, at_pages, max_pages, int(page), at_lengths, n_seq, int(max_len), n_heads,
                1.0 / math.sqrt(cache.head_dim) if scale is None else float(scale), code, at_q,
                _at(ctx, q.shape, q.dtype, dev, "ctx"), _at(lse, (n_seq, n_heads), torch.float32, dev, "lse"),
-               _at(ws, None, torch.uint8, dev, "ws"), ws.numel(), _stream(stream))
+               _at(ws, None, torch.uint8, dev, "ws"), ws.numel(), _raw_stream(stream, dev))
         if own:
             _keep_status(ws)
     return ctx, lse
@@ -500,7 +509,7 @@ def kv8_attn_backward(cache, q, pages, page, lengths, max_len, lse, d_ctx, scale
                1.0 / math.sqrt(cache.head_dim) if scale is None else float(scale), code, at_q,
                _at(lse, (n_seq, n_heads), torch.float32, dev, "lse"), _at(d_ctx, q.shape, q.dtype, dev, "d_ctx"),
                _at(d_q, q.shape, q.dtype, dev, "d_q"), _at(d_k, newest, q.dtype, dev, "d_k"),
-               _at(d_v, newest, q.dtype, dev, "d_v"), _at(ws, None, torch.uint8, dev, "ws"), ws.numel(), _stream(stream))
+               _at(d_v, newest, q.dtype, dev, "d_v"), _at(ws, None, torch.uint8, dev, "ws"), ws.numel(), _raw_stream(stream, dev))
         if own:
             _keep_status(ws)
     return d_q, d_k, d_v

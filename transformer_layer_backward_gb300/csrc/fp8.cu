@@ -57,54 +57,71 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *__restrict_
     }
 }
 
-// Blocks of 128 x 128: a CTA of 256 threads holds one in registers, 64 values a thread.
+// Eight consecutive elements.
+__device__ __forceinline__ void load_float8(const float *p, float (&v)[8]) {
+    const float4 a = load_float4(p), b = load_float4(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void load_float8(const __nv_bfloat16 *p, float (&v)[8]) {
+    const uint4 a = ld_stream_u4(p);
+    v[0] = bf16_lo(a.x); v[1] = bf16_hi(a.x); v[2] = bf16_lo(a.y); v[3] = bf16_hi(a.y);
+    v[4] = bf16_lo(a.z); v[5] = bf16_hi(a.z); v[6] = bf16_lo(a.w); v[7] = bf16_hi(a.w);
+}
+
+// Blocks of 128 x 128: a CTA of 512 threads holds one in registers, 32 values a thread, 16 lanes a row.
+constexpr int kTileThreads = 512, kTileRows = kFp8Block * 16 / kTileThreads;   // rows a thread
+
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) quantize_tiles_kernel(const T *__restrict__ x, int64_t rows, int64_t cols,
-                                                             int64_t nblk, uint8_t *__restrict__ q,
-                                                             float *__restrict__ scales) {
-    __shared__ uint32_t tops[8];
-    const int64_t rb = blockIdx.x / nblk, cb = blockIdx.x - rb * nblk;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t r0 = rb * kFp8Block, c0 = cb * kFp8Block;
-    const int nc = int(min(int64_t(kFp8Block), cols - c0));
-    float v[16][4];
+__global__ void __launch_bounds__(kTileThreads) quantize_tiles_kernel(const T *__restrict__ x, int64_t rows, int64_t cols,
+                                                                      int nblk, uint8_t *__restrict__ q,
+                                                                      float *__restrict__ scales) {
+    __shared__ uint32_t tops[kTileThreads / 32];
+    const int64_t r0 = int64_t(blockIdx.x / unsigned(nblk)) * kFp8Block, c0 = int64_t(blockIdx.x % unsigned(nblk)) * kFp8Block;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = threadIdx.x >> 4, part = threadIdx.x & 15;
+    const int nc = int(min(int64_t(kFp8Block), cols - c0)), nr = int(min(int64_t(kFp8Block), rows - r0));
+    const int64_t at = (r0 + row) * cols + c0;
+    float v[kTileRows][8];
     uint32_t top = 0;
 #pragma unroll
-    for (int u = 0; u < 16; ++u) {                       // a warp's row u: eight rows apart
-        const int64_t row = r0 + u * 8 + warp;
-        const T *p = x + row * cols + c0;
+    for (int u = 0; u < kTileRows; ++u) {
+        const T *p = x + at + u * (kTileThreads / 16) * cols;
+        const bool there = row + u * (kTileThreads / 16) < nr;
         if (VEC) {
-            const float4 f = row < rows && lane * 4 < nc ? load_float4(p + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
-            v[u][0] = f.x; v[u][1] = f.y; v[u][2] = f.z; v[u][3] = f.w;
+            if (there && part * 8 < nc) {
+                load_float8(p + part * 8, v[u]);
+            } else {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) v[u][k] = 0.f;
+            }
         } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k) v[u][k] = row < rows && lane + 32 * k < nc ? load_float(p + lane + 32 * k) : 0.f;
+            for (int k = 0; k < 8; ++k) v[u][k] = there && part + 16 * k < nc ? load_float(p + part + 16 * k) : 0.f;
         }
     }
 #pragma unroll
-    for (int u = 0; u < 16; ++u)
+    for (int u = 0; u < kTileRows; ++u)
 #pragma unroll
-        for (int k = 0; k < 4; ++k) top = max(top, magnitude(v[u][k]));
+        for (int k = 0; k < 8; ++k) top = max(top, magnitude(v[u][k]));
     top = __reduce_max_sync(0xffffffffu, top);
     if (lane == 0) tops[warp] = top;
     __syncthreads();
-#pragma unroll
-    for (int w = 0; w < 8; ++w) top = max(top, tops[w]);
+    top = __reduce_max_sync(0xffffffffu, tops[lane & 15]);
     float inv;
     const float s = block_scale(top, inv);
     if (threadIdx.x == 0) scales[blockIdx.x] = s;
 #pragma unroll
-    for (int u = 0; u < 16; ++u) {
-        const int64_t row = r0 + u * 8 + warp;
-        if (row >= rows) break;
-        uint8_t *p = q + row * cols + c0;
-        const uint32_t y = to_e4m3x4(v[u][0] * inv, v[u][1] * inv, v[u][2] * inv, v[u][3] * inv);
+    for (int u = 0; u < kTileRows; ++u) {
+        if (row + u * (kTileThreads / 16) >= nr) break;
+        uint8_t *p = q + at + u * (kTileThreads / 16) * cols;
+        const uint32_t lo = to_e4m3x4(v[u][0] * inv, v[u][1] * inv, v[u][2] * inv, v[u][3] * inv);
+        const uint32_t hi = to_e4m3x4(v[u][4] * inv, v[u][5] * inv, v[u][6] * inv, v[u][7] * inv);
         if (VEC) {
-            if (lane * 4 < nc) *reinterpret_cast<uint32_t *>(p + lane * 4) = y;
+            if (part * 8 < nc) *reinterpret_cast<uint2 *>(p + part * 8) = make_uint2(lo, hi);
         } else {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-                if (lane + 32 * k < nc) p[lane + 32 * k] = uint8_t(y >> (8 * k));
+            for (int k = 0; k < 8; ++k)
+                if (part + 16 * k < nc) p[part + 16 * k] = uint8_t((k < 4 ? lo : hi) >> (8 * (k & 3)));
         }
     }
 }
@@ -124,8 +141,10 @@ int quantize_launch(const T *x, int64_t rows, int64_t cols, int block_rows, uint
     }
     const int64_t tiles = ceil_div(rows, kFp8Block) * nblk;
     TLB_REQUIRE(tiles < (int64_t(1) << 31), TLB_EUNSUPPORTED, "fp8_quantize: more than 2^31 blocks of 128 x 128");
-    if (vec) quantize_tiles_kernel<T, true><<<unsigned(tiles), 256, 0, st>>>(x, rows, cols, nblk, q, scales);
-    else quantize_tiles_kernel<T, false><<<unsigned(tiles), 256, 0, st>>>(x, rows, cols, nblk, q, scales);
+    // eight columns a thread: 16 bytes loaded, 8 stored
+    const bool vec8 = cols % 8 == 0 && aligned16(x) && (reinterpret_cast<uintptr_t>(q) & 7) == 0;
+    if (vec8) quantize_tiles_kernel<T, true><<<unsigned(tiles), kTileThreads, 0, st>>>(x, rows, cols, int(nblk), q, scales);
+    else quantize_tiles_kernel<T, false><<<unsigned(tiles), kTileThreads, 0, st>>>(x, rows, cols, int(nblk), q, scales);
     return check_launch("fp8_quantize_tiles");
 }
 

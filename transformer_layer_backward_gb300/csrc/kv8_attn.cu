@@ -82,16 +82,17 @@ __device__ __forceinline__ float pow2(int e) { return e >= -126 ? __uint_as_floa
 struct AttnParams {
     tlb_kv8 c;
     Kv8Pages pg;
+    int64_t rows;                // n_seq * n_heads
     int n_heads, group, tiles, splits, chunk;    // heads a KV head, tiles of them, chunks of keys
     float scale;
     const void *q, *d_ctx;
     const float *lse;            // gradient
-    void *out;                   // ctx or d_q (one chunk alone)
+    void *out;                   // ctx or d_q
+    void *d_k, *d_v;             // gradient
     float *out_lse;
     float *part;                 // [n_seq, n_heads, splits][hd or 2 hd]
     float2 *sums;                // [n_seq, n_heads, splits]: forward (max, sum), gradient (sum p dp, -)
     float2 *newest;              // [n_seq, n_heads]: p and dp of the newest key
-    float *D;                    // [n_seq, n_heads]: sum p dp
 };
 
 // Rows of T as the first operand: piece ks of lane (g, t) holds columns 64 (ks / 4) + 16 t + 4 (ks % 4) + {0, 1 | 2, 3} of row
@@ -144,7 +145,7 @@ __global__ void __launch_bounds__(kWarps * 32, HD <= 128 ? 4 : 2) kv8_attn_kerne
     const int kvh = int(unit % nkv);
     const int64_t b = unit / nkv;
     const int len = kv8_length(p.pg, b), k0 = split * p.chunk;
-    if (k0 >= len && !(split == 0 && p.splits == 1)) return;  // the join looks at the chunks below len
+    if (k0 >= len && (GRAD || p.splits > 1)) return;          // the join looks at the chunks below len
     const int k1 = min(len, k0 + p.chunk), steps = max(0, (k1 - k0 + kStep - 1) / kStep);
     const int64_t head0 = b * p.n_heads + kvh * p.group + tile * HT;   // first row of q
     const int heads = min(HT, p.group - tile * HT);
@@ -384,35 +385,72 @@ __global__ void __launch_bounds__(kWarps * 32, HD <= 128 ? 4 : 2) kv8_attn_kerne
                 if (d == 0) p.sums[row0 + int64_t(h) * p.splits] = make_float2(top, total);
             }
         } else {
-            float D = 0.f, z = 0.f;
+            float D = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 y += all[(w * 8 + r) * HD + d];
                 D += s_l[w][h];
             }
-            if (p.splits == 1) {
-                if (r >= 4) continue;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) z += all[(w * 8 + r + 4) * HD + d];
-                store_float(static_cast<T *>(p.out) + (head0 + h) * hd + d, p.scale * fmaf(-D, z, y));
-                if (d == 0) p.D[head0 + h] = D;
-            } else {
-                p.part[((row0 + int64_t(h) * p.splits) * 2 + (r >> 2)) * hd + d] = y;
-                if (d == 0 && r < 4) p.sums[row0 + int64_t(h) * p.splits] = make_float2(D, 0.f);
-            }
+            p.part[((row0 + int64_t(h) * p.splits) * 2 + (r >> 2)) * hd + d] = y;
+            if (d == 0 && r < 4) p.sums[row0 + int64_t(h) * p.splits] = make_float2(D, 0.f);
         }
     }
 }
 
-// Joins the chunks of 32 dimensions of one query head, in a fixed order: 16 groups of eight lanes take every 16th.
 constexpr int kJoinThreads = 128, kJoinDims = 32;
 
+// Gradients of the newest key and value of one (sequence, KV head) from what the pass left of it.
+template <typename T>
+__device__ __forceinline__ void newest_rows(const AttnParams &p, int64_t unit) {
+    const int hd = p.c.head_dim, nkv = p.c.n_kv_heads, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t b = unit / nkv, row0 = b * p.n_heads + (unit - b * nkv) * p.group;
+    const int len = kv8_length(p.pg, b), n = (len + p.chunk - 1) / p.chunk;
+    __shared__ float2 s_w[kJoinThreads / 32];                 // ds and p of a warp's head
+    float dk[256 / kJoinThreads] = {}, dv[256 / kJoinThreads] = {};
+    for (int e0 = 0; e0 < p.group && n > 0; e0 += kJoinThreads / 32) {
+        const int e = e0 + warp;
+        if (e < p.group) {
+            const float2 *sums = p.sums + (row0 + e) * p.splits;
+            float D = 0.f;
+            for (int s = lane; s < n; s += 32) D += __ldcg(&sums[s].x);
+            D = warp_sum(D);
+            const float2 w = __ldcg(p.newest + row0 + e);
+            if (lane == 0) s_w[warp] = make_float2(w.x * (w.y - D) * p.scale, w.x);
+        }
+        __syncthreads();
+        for (int i = 0; i < kJoinThreads / 32 && e0 + i < p.group; ++i)
+#pragma unroll
+            for (int k = 0; k < 256 / kJoinThreads; ++k) {
+                const int d = threadIdx.x + k * kJoinThreads;
+                if (d >= hd) continue;
+                const int64_t at = (row0 + e0 + i) * hd + d;
+                // a weight of 0 adds nothing (a newest key that is not there)
+                if (s_w[i].x != 0.f) dk[k] = fmaf(s_w[i].x, load_float(static_cast<const T *>(p.q) + at), dk[k]);
+                if (s_w[i].y != 0.f) dv[k] = fmaf(s_w[i].y, load_float(static_cast<const T *>(p.d_ctx) + at), dv[k]);
+            }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < 256 / kJoinThreads; ++k) {
+        const int d = threadIdx.x + k * kJoinThreads;
+        if (d >= hd) continue;
+        store_float(static_cast<T *>(p.d_k) + unit * hd + d, dk[k]);
+        store_float(static_cast<T *>(p.d_v) + unit * hd + d, dv[k]);
+    }
+}
+
+// Joins the chunks of 32 dimensions of one query head, in a fixed order: 16 groups of eight lanes take every 16th.  The
+// gradient's last row of CTAs does the newest keys.
 template <typename T, bool GRAD>
 __global__ void __launch_bounds__(kJoinThreads) kv8_attn_join_kernel(const __grid_constant__ AttnParams p) {
     constexpr int kGroups = kJoinThreads / 8;
     __shared__ float sum[GRAD ? 2 : 1][kGroups][kJoinDims];
     __shared__ float red[32];
     pdl_wait();
+    if (GRAD && int(blockIdx.y) * kJoinDims >= p.c.head_dim) {
+        if (blockIdx.x < p.rows / p.group) newest_rows<T>(p, blockIdx.x);
+        return;
+    }
     const int64_t row = blockIdx.x;
     const int hd = p.c.head_dim;
     const int n = (kv8_length(p.pg, row / p.n_heads) + p.chunk - 1) / p.chunk;
@@ -469,33 +507,8 @@ __global__ void __launch_bounds__(kJoinThreads) kv8_attn_join_kernel(const __gri
         store_float(static_cast<T *>(p.out) + row * hd + d,
                     GRAD ? p.scale * fmaf(-total, c, a) : total == 0.f ? 0.f : a / total);
     }
-    if (threadIdx.x == 0 && blockIdx.y == 0) {
-        if (GRAD) p.D[row] = total;
-        else p.out_lse[row] = total == 0.f ? -INFINITY : fmaf(log2f(total), kLn2, top * kLn2);
-    }
-}
-
-// Gradients of the newest key and value from what the pass left of it: a CTA a (sequence, KV head).
-template <typename T>
-__global__ void __launch_bounds__(128) kv8_attn_newest_kernel(const __grid_constant__ AttnParams p, T *__restrict__ d_k,
-                                                              T *__restrict__ d_v) {
-    pdl_wait();
-    const int hd = p.c.head_dim, nkv = p.c.n_kv_heads;
-    const int64_t b = blockIdx.x / nkv, row0 = b * p.n_heads + int64_t(blockIdx.x - b * nkv) * p.group;
-    const bool any = kv8_length(p.pg, b) > 0;
-    for (int d = threadIdx.x; d < hd; d += blockDim.x) {
-        float dk = 0.f, dv = 0.f;
-        if (any)
-            for (int e = 0; e < p.group; ++e) {
-                const float2 w = __ldcg(p.newest + row0 + e);
-                const float ds = w.x * (w.y - __ldcg(p.D + row0 + e)) * p.scale;
-                // a weight of 0 adds nothing (a newest key that is not there)
-                if (ds != 0.f) dk = fmaf(ds, load_float(static_cast<const T *>(p.q) + (row0 + e) * hd + d), dk);
-                if (w.x != 0.f) dv = fmaf(w.x, load_float(static_cast<const T *>(p.d_ctx) + (row0 + e) * hd + d), dv);
-            }
-        store_float(d_k + int64_t(blockIdx.x) * hd + d, dk);
-        store_float(d_v + int64_t(blockIdx.x) * hd + d, dv);
-    }
+    if (!GRAD && threadIdx.x == 0 && blockIdx.y == 0)
+        p.out_lse[row] = total == 0.f ? -INFINITY : fmaf(log2f(total), kLn2, top * kLn2);
 }
 
 bool sizes_ok(const tlb_kv8 *c, int64_t n_seq, int32_t n_heads, int64_t max_len) {
@@ -531,7 +544,7 @@ Split split_of(const tlb_kv8 &c, int64_t n_seq, int n_heads, int64_t max_len, bo
 }
 
 struct Layout {
-    size_t part, sums, newest, D, bytes;
+    size_t part, sums, newest, bytes;
 };
 
 Layout layout_of(const tlb_kv8 &c, int64_t n_seq, int n_heads, int64_t max_len, bool grad) {
@@ -539,14 +552,11 @@ Layout layout_of(const tlb_kv8 &c, int64_t n_seq, int n_heads, int64_t max_len, 
     WsPlan p;
     Layout l{};
     const size_t rows = size_t(n_seq) * n_heads;
-    if (s.splits > 1) {
+    if (grad || s.splits > 1) {
         l.part = p.take(rows * s.splits * c.head_dim * (grad ? 2 : 1) * sizeof(float));
         l.sums = p.take(rows * s.splits * sizeof(float2));
     }
-    if (grad) {
-        l.newest = p.take(rows * sizeof(float2));
-        l.D = p.take(rows * sizeof(float));
-    }
+    if (grad) l.newest = p.take(rows * sizeof(float2));
     l.bytes = p.off;
     return l;
 }
@@ -559,31 +569,32 @@ size_t ws_bytes_of(const tlb_kv8 *c, int64_t n_seq, int32_t n_heads, int64_t max
 }
 
 template <typename T, int HD, bool GRAD>
-int attn_launch(const AttnParams &p, int64_t n_seq, const Split &s, cudaStream_t st) {
+int attn_launch(const AttnParams &p, const Split &s, cudaStream_t st) {
     auto kernel = kv8_attn_kernel<T, HD, GRAD>;
     constexpr int smem = smem_bytes<HD, GRAD>();
     static_assert(smem >= kWarps * 8 * HD * 4, "the warps' sums fit where the stages were");
     TLB_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     kernel<<<unsigned(s.units * s.splits), kWarps * 32, smem, st>>>(p);
     TLB_TRY(check_launch(GRAD ? "kv8_attn_backward" : "kv8_attn_forward"));
-    if (s.splits == 1) return TLB_OK;
-    const dim3 grid(unsigned(n_seq * p.n_heads), unsigned(ceil_div(p.c.head_dim, kJoinDims)));
+    if (!GRAD && s.splits == 1) return TLB_OK;
+    const dim3 grid(unsigned(p.rows), unsigned(ceil_div(p.c.head_dim, kJoinDims)) + (GRAD ? 1 : 0));
     TLB_CUDA(launch_dependent(kv8_attn_join_kernel<T, GRAD>, grid, dim3(kJoinThreads), 0, st, p));
     return check_launch("kv8_attn_join");
 }
 
 template <typename T, bool GRAD>
-int attn_run(const AttnParams &p, int64_t n_seq, const Split &s, cudaStream_t st) {
-    return p.c.head_dim <= 64 ? attn_launch<T, 64, GRAD>(p, n_seq, s, st)
-           : p.c.head_dim <= 128 ? attn_launch<T, 128, GRAD>(p, n_seq, s, st)
-                                 : attn_launch<T, 256, GRAD>(p, n_seq, s, st);
+int attn_run(const AttnParams &p, const Split &s, cudaStream_t st) {
+    return p.c.head_dim <= 64 ? attn_launch<T, 64, GRAD>(p, s, st)
+           : p.c.head_dim <= 128 ? attn_launch<T, 128, GRAD>(p, s, st)
+                                 : attn_launch<T, 256, GRAD>(p, s, st);
 }
 
-AttnParams params_of(const tlb_kv8 &c, const Kv8Pages &pg, int n_heads, const Split &s, const Layout &l, float scale, const void *q,
+AttnParams params_of(const tlb_kv8 &c, const Kv8Pages &pg, int64_t n_seq, int n_heads, const Split &s, const Layout &l, float scale, const void *q,
                      void *ws) {
     AttnParams p{};
     p.c = c;
     p.pg = pg;
+    p.rows = n_seq * n_heads;
     p.n_heads = n_heads;
     p.group = n_heads / c.n_kv_heads;
     p.tiles = s.tiles;
@@ -594,7 +605,6 @@ AttnParams params_of(const tlb_kv8 &c, const Kv8Pages &pg, int n_heads, const Sp
     p.part = ws_at<float>(ws, l.part);
     p.sums = ws_at<float2>(ws, l.sums);
     p.newest = ws_at<float2>(ws, l.newest);
-    p.D = ws_at<float>(ws, l.D);
     return p;
 }
 
@@ -649,11 +659,11 @@ int tlb_kv8_attn_forward(const tlb_kv8 *cache, const int32_t *pages, int64_t max
     TLB_REQUIRE(ctx && lse, TLB_EINVAL, "kv8_attn_forward: null pointer");
     TLB_REQUIRE(aligned16(ctx), TLB_EINVAL, "kv8_attn_forward: ctx must be 16-byte aligned");
     const Split sp = split_of(*cache, n_seq, n_heads, max_len, false);
-    AttnParams p = params_of(*cache, pg, n_heads, sp, layout_of(*cache, n_seq, n_heads, max_len, false), scale, q, ws);
+    AttnParams p = params_of(*cache, pg, n_seq, n_heads, sp, layout_of(*cache, n_seq, n_heads, max_len, false), scale, q, ws);
     p.out = ctx;
     p.out_lse = lse;
-    return type == TLB_W_F32 ? attn_run<float, false>(p, n_seq, sp, as_stream(stream))
-                             : attn_run<__nv_bfloat16, false>(p, n_seq, sp, as_stream(stream));
+    return type == TLB_W_F32 ? attn_run<float, false>(p, sp, as_stream(stream))
+                             : attn_run<__nv_bfloat16, false>(p, sp, as_stream(stream));
 }
 
 int tlb_kv8_attn_backward(const tlb_kv8 *cache, const int32_t *pages, int64_t max_pages, int32_t page,
@@ -669,22 +679,14 @@ int tlb_kv8_attn_backward(const tlb_kv8 *cache, const int32_t *pages, int64_t ma
     TLB_REQUIRE(aligned16(d_ctx) && aligned16(d_q) && aligned16(d_k) && aligned16(d_v), TLB_EINVAL,
                 "kv8_attn_backward: d_ctx, d_q, d_k and d_v must be 16-byte aligned");
     const Split sp = split_of(*cache, n_seq, n_heads, max_len, true);
-    AttnParams p = params_of(*cache, pg, n_heads, sp, layout_of(*cache, n_seq, n_heads, max_len, true), scale, q, ws);
+    AttnParams p = params_of(*cache, pg, n_seq, n_heads, sp, layout_of(*cache, n_seq, n_heads, max_len, true), scale, q, ws);
     p.lse = lse;
     p.d_ctx = d_ctx;
     p.out = d_q;
-    cudaStream_t st = as_stream(stream);
-    const dim3 grid(unsigned(n_seq * cache->n_kv_heads));
-    if (type == TLB_W_F32) {
-        TLB_TRY((attn_run<float, true>(p, n_seq, sp, st)));
-        TLB_CUDA(launch_dependent(kv8_attn_newest_kernel<float>, grid, dim3(128), 0, st, p, static_cast<float *>(d_k),
-                                  static_cast<float *>(d_v)));
-    } else {
-        TLB_TRY((attn_run<__nv_bfloat16, true>(p, n_seq, sp, st)));
-        TLB_CUDA(launch_dependent(kv8_attn_newest_kernel<__nv_bfloat16>, grid, dim3(128), 0, st, p,
-                                  static_cast<__nv_bfloat16 *>(d_k), static_cast<__nv_bfloat16 *>(d_v)));
-    }
-    return check_launch("kv8_attn_newest");
+    p.d_k = d_k;
+    p.d_v = d_v;
+    return type == TLB_W_F32 ? attn_run<float, true>(p, sp, as_stream(stream))
+                             : attn_run<__nv_bfloat16, true>(p, sp, as_stream(stream));
 }
 
 }  // extern "C"
