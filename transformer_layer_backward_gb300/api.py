@@ -478,15 +478,20 @@ def kv8_attn_forward(cache, q, pages, page, lengths, max_len, scale=None, ctx=No
     n_seq, n_heads, code, at_q, at_pages, max_pages, at_lengths = _kv8_over(cache, q, pages, lengths)
     dev = cache.device
     with _queued(q, stream):
-        ctx = torch.empty_like(q) if ctx is None else ctx
-        lse = torch.empty(n_seq, n_heads, dtype=torch.float32, device=dev) if lse is None else lse
+        if ctx is None:
+            ctx = torch.empty_like(q)
+        else:
+            _at(ctx, q.shape, q.dtype, dev, "ctx")
+        if lse is None:
+            lse = torch.empty((n_seq, n_heads), dtype=torch.float32, device=dev)
+        else:
+            _at(lse, (n_seq, n_heads), torch.float32, dev, "lse")
         own = ws is None
         if own:
             ws = kv8_attn_workspace(cache, n_seq, n_heads, max_len)
         A.call("tlb_kv8_attn_forward", cache, at_pages, max_pages, int(page), at_lengths, n_seq, int(max_len), n_heads,
                1.0 / math.sqrt(cache.head_dim) if scale is None else float(scale), code, at_q,
-               _at(ctx, q.shape, q.dtype, dev, "ctx"), _at(lse, (n_seq, n_heads), torch.float32, dev, "lse"),
-               _at(ws, None, torch.uint8, dev, "ws"), ws.numel(), _raw_stream(stream, dev))
+               ctx.data_ptr(), lse.data_ptr(), _at(ws, None, torch.uint8, dev, "ws"), ws.numel(), _raw_stream(stream, dev))
         if own:
             _keep_status(ws)
     return ctx, lse
@@ -499,17 +504,25 @@ def kv8_attn_backward(cache, q, pages, page, lengths, max_len, lse, d_ctx, scale
     n_seq, n_heads, code, at_q, at_pages, max_pages, at_lengths = _kv8_over(cache, q, pages, lengths)
     dev, newest = cache.device, (n_seq, cache.n_kv_heads, cache.head_dim)
     with _queued(q, stream):
-        d_q = torch.empty_like(q) if d_q is None else d_q
-        d_k = torch.empty(newest, dtype=q.dtype, device=dev) if d_k is None else d_k
-        d_v = torch.empty(newest, dtype=q.dtype, device=dev) if d_v is None else d_v
+        if d_q is None:
+            d_q = torch.empty_like(q)
+        else:
+            _at(d_q, q.shape, q.dtype, dev, "d_q")
+        if d_k is None:
+            d_k = torch.empty(newest, dtype=q.dtype, device=dev)
+        else:
+            _at(d_k, newest, q.dtype, dev, "d_k")
+        if d_v is None:
+            d_v = torch.empty(newest, dtype=q.dtype, device=dev)
+        else:
+            _at(d_v, newest, q.dtype, dev, "d_v")
         own = ws is None
         if own:
             ws = kv8_attn_workspace(cache, n_seq, n_heads, max_len, grad=True)
         A.call("tlb_kv8_attn_backward", cache, at_pages, max_pages, int(page), at_lengths, n_seq, int(max_len), n_heads,
                1.0 / math.sqrt(cache.head_dim) if scale is None else float(scale), code, at_q,
                _at(lse, (n_seq, n_heads), torch.float32, dev, "lse"), _at(d_ctx, q.shape, q.dtype, dev, "d_ctx"),
-               _at(d_q, q.shape, q.dtype, dev, "d_q"), _at(d_k, newest, q.dtype, dev, "d_k"),
-               _at(d_v, newest, q.dtype, dev, "d_v"), _at(ws, None, torch.uint8, dev, "ws"), ws.numel(), _raw_stream(stream, dev))
+               d_q.data_ptr(), d_k.data_ptr(), d_v.data_ptr(), _at(ws, None, torch.uint8, dev, "ws"), ws.numel(), _raw_stream(stream, dev))
         if own:
             _keep_status(ws)
     return d_q, d_k, d_v

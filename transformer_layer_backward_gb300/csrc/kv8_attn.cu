@@ -573,7 +573,7 @@ int attn_launch(const AttnParams &p, const Split &s, cudaStream_t st) {
     auto kernel = kv8_attn_kernel<T, HD, GRAD>;
     constexpr int smem = smem_bytes<HD, GRAD>();
     static_assert(smem >= kWarps * 8 * HD * 4, "the warps' sums fit where the stages were");
-    TLB_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+    if (smem > 48 * 1024) TLB_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
     kernel<<<unsigned(s.units * s.splits), kWarps * 32, smem, st>>>(p);
     TLB_TRY(check_launch(GRAD ? "kv8_attn_backward" : "kv8_attn_forward"));
     if (!GRAD && s.splits == 1) return TLB_OK;

@@ -57,6 +57,50 @@ __device__ __forceinline__ void put4(T *p, int col, int cols, float4 y, bool add
         if (col + k < cols) store_float(p + k, add ? v[k] + load_float(p + k) : v[k]);
 }
 
+// A warp's 32 x 32 results out of shared memory (16-byte pieces turned by their row's last three bits), four rows of
+// eight lanes at a time; what they are added to is loaded kAhead rows ahead.
+template <typename T>
+__device__ __forceinline__ void put_rows4(T *dX, int row0, int rows, int col, int cols, const float4 *blk, int ch, int rl, bool add) {
+    constexpr int kAhead = 4;
+    if (col >= cols) return;
+    T *p = dX + int64_t(row0 + rl) * cols + col;
+#pragma unroll 1
+    for (int k0 = 0; k0 < 8; k0 += kAhead) {
+        float4 old[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k)
+            old[k] = add && row0 + 4 * (k0 + k) + rl < rows ? load_float4(p + int64_t(4 * (k0 + k)) * cols) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int r = 4 * (k0 + k) + rl;
+            float4 y = blk[r * 8 + (ch ^ (r & 7))];
+            if (row0 + r >= rows) continue;
+            if (add) { y.x += old[k].x; y.y += old[k].y; y.z += old[k].z; y.w += old[k].w; }
+            store_float4(p + int64_t(4 * (k0 + k)) * cols, y);
+        }
+    }
+}
+
+// The same where rows do not start at multiples of four elements: a row of 32 lanes at a time.
+template <typename T>
+__device__ __forceinline__ void put_rows1(T *dX, int row0, int rows, int col, int cols, const float *blk, int lane, bool add) {
+    constexpr int kAhead = 8;
+    if (col >= cols) return;
+    T *p = dX + int64_t(row0) * cols + col;
+#pragma unroll 1
+    for (int r0 = 0; r0 < 32 && row0 + r0 < rows; r0 += kAhead) {
+        float old[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) old[k] = add && row0 + r0 + k < rows ? load_float(p + int64_t(r0 + k) * cols) : 0.f;
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int r = r0 + k;
+            const float y = blk[r * 32 + (((lane >> 2) ^ (r & 7)) << 2) + (lane & 3)];
+            if (row0 + r < rows) store_float(p + int64_t(r) * cols, add ? y + old[k] : y);
+        }
+    }
+}
+
 // ------------------------------------------------------------------ few rows
 
 constexpr int kRowWarps = 8;
@@ -85,7 +129,7 @@ __device__ __forceinline__ uint4 piece(const uint8_t *row, int col, int out, boo
 
 // NT: n tiles of 8 rows of dY.
 template <typename T, int NT>
-__global__ void __launch_bounds__(kRowWarps * 32) linear_fp8_rows_kernel(const RowsParams p) {
+__global__ void __launch_bounds__(kRowWarps * 32, NT == 1 ? 5 : 1) linear_fp8_rows_kernel(const RowsParams p) {
     __shared__ float part[kRowWarps][16][8 * NT + 1];
     __shared__ float mine[16][8 * NT];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -434,17 +478,19 @@ __global__ void __launch_bounds__(kThreads, 1) linear_fp8_tc_kernel(const __grid
                     blk[lane * 8 + (c ^ (lane & 7))] =
                         make_float4(acc[j * 32 + 4 * c], acc[j * 32 + 4 * c + 1], acc[j * 32 + 4 * c + 2], acc[j * 32 + 4 * c + 3]);
                 __syncwarp();
-                const int col = cols0 + j * 32 + ch * 4;
+                if (!whole) {
 #pragma unroll 2
-                for (int k = 0; k < 8; ++k) {
-                    const int r = 4 * k + rl;
-                    const float4 y = blk[r * 8 + (ch ^ (r & 7))];
-                    if (rows0 + r >= p.M) continue;
-                    if (whole)
-                        put4<T, WIDE>(static_cast<T *>(p.dX) + int64_t(rows0 + r) * p.N + col, col, p.N, y, p.add != 0);
-                    else
-                        *reinterpret_cast<float4 *>(p.partial + ((int64_t(blockIdx.x) * 2 + slot) * kHalf + q * 32 + r) * kTN +
-                                                    in_tile + j * 32 + ch * 4) = y;
+                    for (int k = 0; k < 8; ++k) {
+                        const int r = 4 * k + rl;
+                        if (rows0 + r < p.M)
+                            *reinterpret_cast<float4 *>(p.partial + ((int64_t(blockIdx.x) * 2 + slot) * kHalf + q * 32 + r) * kTN +
+                                                        in_tile + j * 32 + ch * 4) = blk[r * 8 + (ch ^ (r & 7))];
+                    }
+                } else if (WIDE) {
+                    put_rows4(static_cast<T *>(p.dX), rows0, p.M, cols0 + j * 32 + ch * 4, p.N, blk, ch, rl, p.add != 0);
+                } else {
+                    put_rows1(static_cast<T *>(p.dX), rows0, p.M, cols0 + j * 32 + lane, p.N, reinterpret_cast<const float *>(blk),
+                              lane, p.add != 0);
                 }
                 __syncwarp();
             }
