@@ -1,6 +1,6 @@
 // Attention of single tokens over the 8-bit K/V cache, and its gradient.
 //
-// Bound by the read of the keys and values, once.  What a CTA (four warps) does for a chunk of one sequence's keys, one
+// Bound by the read of the keys and values, once.  What a CTA (four warps) does for a run of one sequence's keys, one
 // KV head and a tile of the query heads that share it, 16 keys a warp at a time:
 //   - cp.async brings the keys', values' and scales' bytes to shared memory, a step ahead; keys that
 //     are not there come as zeros, so that nothing of what a free slot holds is met;
@@ -13,7 +13,7 @@
 //     by byte permutes: 23 bits of each weight, 34 below the largest at least.
 // The gradient uses d_q = scale (sum p dp k - (sum p dp)(sum p k)), so that one pass does.  Rows of the gradient's
 // tile: four heads' s (and p dp) in rows 0..3, their dp (and p) in rows 4..7; of the forward's: eight heads.
-// Warps, then chunks (a second kernel), are joined in a fixed order.
+// Warps, then the CTAs that share a unit (a second kernel), are joined in a fixed order.
 #include <cmath>
 
 #include "async.cuh"
@@ -82,17 +82,35 @@ __device__ __forceinline__ float pow2(int e) { return e >= -126 ? __uint_as_floa
 struct AttnParams {
     tlb_kv8 c;
     Kv8Pages pg;
-    int64_t rows;                // n_seq * n_heads
-    int n_heads, group, tiles, splits, chunk;    // heads a KV head, tiles of them, chunks of keys
+    int64_t n_seq;
+    int n_heads, group, tiles, ctas;     // heads a KV head, tiles of them
     float scale;
     const void *q, *d_ctx;
     const float *lse;            // gradient
     void *out;                   // ctx or d_q
     void *d_k, *d_v;             // gradient
     float *out_lse;
-    float *part;                 // [n_seq, n_heads, splits][hd or 2 hd]
-    float2 *sums;                // [n_seq, n_heads, splits]: forward (max, sum), gradient (sum p dp, -)
+    float *part;                 // [ctas][2][8 rows][head_dim]: sums of a CTA's first and last unit, where these are shared
+    float2 *sums;                // [ctas][2][8]: forward (max, sum of exp), gradient (sum p dp, -)
+    int2 *parts;                 // [n_seq, units]: the first CTA of a unit (times 2, plus its slot) and the last
     float2 *newest;              // [n_seq, n_heads]: p and dp of the newest key
+    float *D;                    // [n_seq, n_heads]: sum p dp of a unit that one CTA did
+};
+
+// The work is laid out in a line: sequence by sequence, unit by unit (a KV head and a tile of its query heads), a unit
+// of S steps of 16 keys weighing kFixed + S, since its start and its end cost as much as some steps.  CTA c of n takes
+// [total c / n, total (c + 1) / n) of that line: as many CTAs as are on the GPU at a time, each with the same
+// weight whatever the lengths, which only the device knows.  The first kFixed of a unit are no steps.
+constexpr int kFixed = 12, kLeast = 4;    // kLeast: the weight that is worth a CTA (a step of each warp)
+
+__device__ __forceinline__ int64_t steps_of(int len) { return (len + kStep - 1) / kStep; }
+__device__ __forceinline__ int cta_count(int64_t total, int most) { return int(max(int64_t(1), min(int64_t(most), total / kLeast))); }
+__device__ __forceinline__ int64_t share(int64_t total, int n, int64_t c) { return total / n * c + total % n * c / n; }
+// What a CTA does next.
+struct Segment {
+    int64_t pos, end, base;      // places of the line: next, the CTA's last, the sequence's first
+    int64_t b;
+    int unit, len, s0, s1, slot, run;
 };
 
 // Rows of T as the first operand: piece ks of lane (g, t) holds columns 64 (ks / 4) + 16 t + 4 (ks % 4) + {0, 1 | 2, 3} of row
@@ -137,16 +155,80 @@ __global__ void __launch_bounds__(kWarps * 32, HD <= 128 ? 4 : 2) kv8_attn_kerne
     __shared__ int s_f[2][8];
     __shared__ float s_m[kWarps][8], s_l[kWarps][8];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int split = int(blockIdx.x % p.splits);
-    int64_t unit = blockIdx.x / p.splits;
-    const int tile = int(unit % p.tiles);
-    unit /= p.tiles;
-    const int nkv = p.c.n_kv_heads, hd = p.c.head_dim;
-    const int kvh = int(unit % nkv);
-    const int64_t b = unit / nkv;
-    const int len = kv8_length(p.pg, b), k0 = split * p.chunk;
-    if (k0 >= len && (GRAD || p.splits > 1)) return;          // the join looks at the chunks below len
-    const int k1 = min(len, k0 + p.chunk), steps = max(0, (k1 - k0 + kStep - 1) / kStep);
+    __shared__ Segment sg;
+    __shared__ int64_t s_scan[kWarps];
+    const int nkv = p.c.n_kv_heads, hd = p.c.head_dim, units = nkv * p.tiles;
+
+    // ---- this CTA's part of the line: a scan of the sequences' weights, a run of them a thread
+    {
+        const int64_t per = (p.n_seq + kWarps * 32 - 1) / (kWarps * 32), b0 = min(p.n_seq, threadIdx.x * per), b1 = min(p.n_seq, b0 + per);
+        int64_t mine = 0;
+        for (int64_t i = b0; i < b1; ++i) mine += kFixed + steps_of(kv8_length(p.pg, i));
+        int64_t upto = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t v = __shfl_up_sync(0xffffffffu, upto, o);
+            if (lane >= o) upto += v;
+        }
+        if (lane == 31) s_scan[warp] = upto;
+        __syncthreads();
+        int64_t total = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) upto += s_scan[w];
+            total += s_scan[w];
+        }
+        int64_t base = upto - mine;
+        total *= units;
+        const int n = cta_count(total, p.ctas);
+        if (int(blockIdx.x) >= n) return;
+        const int64_t lo = share(total, n, blockIdx.x);
+        if (lo >= base * units && lo < upto * units) {
+            for (int64_t i = b0; i < b1; ++i) {
+                const int len = kv8_length(p.pg, i);
+                const int64_t next = base + kFixed + steps_of(len);
+                if (lo < next * units) {
+                    sg.pos = lo;
+                    sg.end = share(total, n, int64_t(blockIdx.x) + 1);
+                    sg.base = base * units;
+                    sg.b = i;
+                    sg.len = len;
+                    sg.slot = 0;
+                    break;
+                }
+                base = next;
+            }
+        }
+        __syncthreads();
+    }
+  for (;;) {
+    if (threadIdx.x == 0) {
+        // the next segment that has something to do: steps [s0, s1) of a unit
+        sg.run = 0;
+        while (!sg.run && sg.pos < sg.end) {
+            const int64_t S = steps_of(sg.len), weight = kFixed + S, unit = (sg.pos - sg.base) / weight;
+            const int64_t from = sg.base + unit * weight, to = min(sg.end, from + weight);
+            sg.unit = int(unit);
+            sg.s0 = int(max(sg.pos - from - kFixed, int64_t(0)));
+            sg.s1 = int(max(to - from - kFixed, int64_t(0)));
+            if (sg.s1 > sg.s0 || (S == 0 && to == from + weight)) {
+                sg.run = 1;
+                break;
+            }
+            sg.slot = 1;
+            sg.pos = to;
+            if (to == from + weight && unit == units - 1) {
+                sg.base = to;
+                if (sg.pos < sg.end) sg.len = kv8_length(p.pg, ++sg.b);
+            }
+        }
+    }
+    __syncthreads();
+    if (!sg.run) break;
+    const int64_t b = sg.b;
+    const int kvh = sg.unit / p.tiles, tile = sg.unit % p.tiles, len = sg.len;
+    const int k0 = sg.s0 * kStep, k1 = min(len, sg.s1 * kStep), steps = sg.s1 - sg.s0;
+    const bool whole = sg.s0 == 0 && sg.s1 == steps_of(len);
     const int64_t head0 = b * p.n_heads + kvh * p.group + tile * HT;   // first row of q
     const int heads = min(HT, p.group - tile * HT);
 
@@ -359,7 +441,7 @@ __global__ void __launch_bounds__(kWarps * 32, HD <= 128 ? 4 : 2) kv8_attn_kerne
             all[(warp * 8 + g) * HD + d] = fmaf(acc[n][2 + e], 1.f / kLow, acc[n][e]) * up;
         }
     __syncthreads();
-    const int64_t row0 = head0 * p.splits + split;             // of the first head's part
+    const int64_t row0 = (int64_t(blockIdx.x) * 2 + sg.slot) * 8;      // where a part of a unit goes
     for (int e = threadIdx.x; e < 8 * HD; e += kWarps * 32) {
         const int r = e / HD, d = e % HD;
         const int h = GRAD ? r & 3 : r;
@@ -377,48 +459,88 @@ __global__ void __launch_bounds__(kWarps * 32, HD <= 128 ? 4 : 2) kv8_attn_kerne
                 y = fmaf(all[(w * 8 + r) * HD + d], f, y);
                 total = fmaf(s_l[w][r], f, total);
             }
-            if (p.splits == 1) {
+            if (whole) {
                 store_float(static_cast<T *>(p.out) + (head0 + h) * hd + d, total == 0.f ? 0.f : y / total);
                 if (d == 0) p.out_lse[head0 + h] = total == 0.f ? -INFINITY : fmaf(log2f(total), kLn2, top * kLn2);
             } else {
-                p.part[(row0 + int64_t(h) * p.splits) * hd + d] = y;
-                if (d == 0) p.sums[row0 + int64_t(h) * p.splits] = make_float2(top, total);
+                p.part[(row0 + r) * hd + d] = y;
+                if (d == 0) p.sums[row0 + r] = make_float2(top, total);
             }
         } else {
-            float D = 0.f;
+            float D = 0.f, z = 0.f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 y += all[(w * 8 + r) * HD + d];
                 D += s_l[w][h];
             }
-            p.part[((row0 + int64_t(h) * p.splits) * 2 + (r >> 2)) * hd + d] = y;
-            if (d == 0 && r < 4) p.sums[row0 + int64_t(h) * p.splits] = make_float2(D, 0.f);
+            if (!whole) {
+                p.part[(row0 + r) * hd + d] = y;
+                if (d == 0 && r < 4) p.sums[row0 + r] = make_float2(D, 0.f);
+            } else if (r < 4) {
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) z += all[(w * 8 + r + 4) * HD + d];
+                store_float(static_cast<T *>(p.out) + (head0 + h) * hd + d, p.scale * fmaf(-D, z, y));
+                if (d == 0) p.D[head0 + h] = D;
+            }
         }
     }
+    __syncthreads();                                           // before the next segment's queries and keys
+    if (threadIdx.x == 0) {
+        int2 *parts = p.parts + b * units + sg.unit;           // for the join
+        if (sg.s0 == 0) parts->x = int(blockIdx.x) * 2 + sg.slot;
+        if (sg.s1 == steps_of(len)) parts->y = int(blockIdx.x);
+        const int64_t weight = kFixed + steps_of(len), from = sg.base + sg.unit * weight, to = min(sg.end, from + weight);
+        sg.slot = 1;
+        sg.pos = to;
+        if (to == from + weight && sg.unit == units - 1) {
+            sg.base = to;
+            if (sg.pos < sg.end) sg.len = kv8_length(p.pg, ++sg.b);
+        }
+    }
+  }
 }
 
-constexpr int kJoinThreads = 128, kJoinDims = 32;
+// Where the parts of a unit are: CTAs c0 .. c1, in their slot 0 but for c0's.
+struct Parts {
+    int c0, c1, slot0;
+    __device__ __forceinline__ Parts(const AttnParams &p, int64_t b, int unit) {
+        const int2 v = __ldcg(p.parts + b * p.c.n_kv_heads * p.tiles + unit);
+        c0 = v.x >> 1;
+        slot0 = v.x & 1;
+        c1 = v.y;
+    }
+    __device__ __forceinline__ bool whole() const { return c0 == c1; }
+    __device__ __forceinline__ int64_t row(int c, int r) const { return (int64_t(c) * 2 + (c == c0 ? slot0 : 0)) * 8 + r; }
+};
+
+constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32;
 
 // Gradients of the newest key and value of one (sequence, KV head) from what the pass left of it.
 template <typename T>
 __device__ __forceinline__ void newest_rows(const AttnParams &p, int64_t unit) {
     const int hd = p.c.head_dim, nkv = p.c.n_kv_heads, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int64_t b = unit / nkv, row0 = b * p.n_heads + (unit - b * nkv) * p.group;
-    const int len = kv8_length(p.pg, b), n = (len + p.chunk - 1) / p.chunk;
-    __shared__ float2 s_w[kJoinThreads / 32];                 // ds and p of a warp's head
+    const int64_t b = unit / nkv;
+    const int kvh = int(unit - b * nkv);
+    const int64_t row0 = b * p.n_heads + int64_t(kvh) * p.group;
+    const bool any = kv8_length(p.pg, b) > 0;
+    __shared__ float2 s_w[kJoinWarps];                        // ds and p of a warp's head
     float dk[256 / kJoinThreads] = {}, dv[256 / kJoinThreads] = {};
-    for (int e0 = 0; e0 < p.group && n > 0; e0 += kJoinThreads / 32) {
+    for (int e0 = 0; e0 < p.group && any; e0 += kJoinWarps) {
         const int e = e0 + warp;
         if (e < p.group) {
-            const float2 *sums = p.sums + (row0 + e) * p.splits;
+            const Parts at(p, b, kvh * p.tiles + e / tile_heads(true));
             float D = 0.f;
-            for (int s = lane; s < n; s += 32) D += __ldcg(&sums[s].x);
-            D = warp_sum(D);
+            if (at.whole()) {
+                D = __ldcg(p.D + row0 + e);
+            } else {
+                for (int c = at.c0 + lane; c <= at.c1; c += 32) D += __ldcg(&p.sums[at.row(c, e % tile_heads(true))].x);
+                D = warp_sum(D);
+            }
             const float2 w = __ldcg(p.newest + row0 + e);
             if (lane == 0) s_w[warp] = make_float2(w.x * (w.y - D) * p.scale, w.x);
         }
         __syncthreads();
-        for (int i = 0; i < kJoinThreads / 32 && e0 + i < p.group; ++i)
+        for (int i = 0; i < kJoinWarps && e0 + i < p.group; ++i)
 #pragma unroll
             for (int k = 0; k < 256 / kJoinThreads; ++k) {
                 const int d = threadIdx.x + k * kJoinThreads;
@@ -439,76 +561,68 @@ __device__ __forceinline__ void newest_rows(const AttnParams &p, int64_t unit) {
     }
 }
 
-// Joins the chunks of 32 dimensions of one query head, in a fixed order: 16 groups of eight lanes take every 16th.  The
-// gradient's last row of CTAs does the newest keys.
+// Joins the parts of one query head, where its unit has more than one, in a fixed order: warps take every fourth, a
+// lane four dimensions (and four from 128 on).  The gradient's last CTAs do the newest keys.
 template <typename T, bool GRAD>
 __global__ void __launch_bounds__(kJoinThreads) kv8_attn_join_kernel(const __grid_constant__ AttnParams p) {
-    constexpr int kGroups = kJoinThreads / 8;
-    __shared__ float sum[GRAD ? 2 : 1][kGroups][kJoinDims];
-    __shared__ float red[32];
+    __shared__ float4 sum[GRAD ? 2 : 1][kJoinWarps][64];
     pdl_wait();
-    if (GRAD && int(blockIdx.y) * kJoinDims >= p.c.head_dim) {
-        if (blockIdx.x < p.rows / p.group) newest_rows<T>(p, blockIdx.x);
+    const int64_t row = blockIdx.x;
+    if (GRAD && row >= p.n_seq * p.n_heads) {
+        newest_rows<T>(p, row - p.n_seq * p.n_heads);
         return;
     }
-    const int64_t row = blockIdx.x;
-    const int hd = p.c.head_dim;
-    const int n = (kv8_length(p.pg, row / p.n_heads) + p.chunk - 1) / p.chunk;
-    const float2 *sums = p.sums + row * p.splits;
-    const int grp = threadIdx.x >> 3, dim = int(blockIdx.y) * kJoinDims + (threadIdx.x & 7) * 4;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    // the largest logit and the sum (gradient: D) of all chunks, the same in every thread
+    const int hd = p.c.head_dim, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t b = row / p.n_heads;
+    const int h = int(row - b * p.n_heads), kvh = h / p.group, e = h - kvh * p.group;
+    constexpr int HT = tile_heads(GRAD);
+    const Parts at(p, b, kvh * p.tiles + e / HT);
+    if (at.whole()) return;
+    const int r = e % HT;
+    // the largest logit and the sum (gradient: D) of all parts, the same in every warp
     float top = -INFINITY, total = 0.f;
     if (!GRAD) {
-        for (int s = threadIdx.x; s < n; s += kJoinThreads) top = fmaxf(top, __ldcg(sums + s).x);
+        for (int c = at.c0 + lane; c <= at.c1; c += 32) top = fmaxf(top, __ldcg(&p.sums[at.row(c, r)].x));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        if (lane == 0) red[warp] = top;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < kJoinThreads / 32; ++w) top = fmaxf(top, red[w]);
     }
     const float ref = top == -INFINITY ? 0.f : top;
-    for (int s = threadIdx.x; s < n; s += kJoinThreads) {
-        const float2 v = __ldcg(sums + s);
+    for (int c = at.c0 + lane; c <= at.c1; c += 32) {
+        const float2 v = __ldcg(p.sums + at.row(c, r));
         total += GRAD ? v.x : v.y * ex2(v.x - ref);
     }
-    float4 y = make_float4(0.f, 0.f, 0.f, 0.f), z = y;
-    if (dim < hd) {
-        const float *part = p.part + row * p.splits * int64_t(hd) * (GRAD ? 2 : 1) + dim;
+    total = warp_sum(total);
+    for (int d = lane * 4, k = 0; k < 2; d += 128, ++k) {
+        if (d >= hd) break;
+        float4 y = make_float4(0.f, 0.f, 0.f, 0.f), z = y;
 #pragma unroll 8
-        for (int s = grp; s < n; s += kGroups) {
-            const float4 a = __ldcg(reinterpret_cast<const float4 *>(part + int64_t(s) * hd * (GRAD ? 2 : 1)));
+        for (int c = at.c0 + warp; c <= at.c1; c += kJoinWarps) {
+            const int64_t from = at.row(c, r);
+            const float4 v = __ldcg(reinterpret_cast<const float4 *>(p.part + from * hd + d));
             if (GRAD) {
-                const float4 c = __ldcg(reinterpret_cast<const float4 *>(part + (int64_t(s) * 2 + 1) * hd));
-                y.x += a.x; y.y += a.y; y.z += a.z; y.w += a.w;
-                z.x += c.x; z.y += c.y; z.z += c.z; z.w += c.w;
+                const float4 w = __ldcg(reinterpret_cast<const float4 *>(p.part + (from + 4) * hd + d));
+                y.x += v.x; y.y += v.y; y.z += v.z; y.w += v.w;
+                z.x += w.x; z.y += w.y; z.z += w.z; z.w += w.w;
             } else {
-                const float f = ex2(__ldcg(&sums[s].x) - ref);
-                y.x = fmaf(a.x, f, y.x); y.y = fmaf(a.y, f, y.y); y.z = fmaf(a.z, f, y.z); y.w = fmaf(a.w, f, y.w);
+                const float f = ex2(__ldcg(&p.sums[from].x) - ref);
+                y.x = fmaf(v.x, f, y.x); y.y = fmaf(v.y, f, y.y); y.z = fmaf(v.z, f, y.z); y.w = fmaf(v.w, f, y.w);
             }
         }
+        sum[0][warp][k * 32 + lane] = y;
+        if (GRAD) sum[GRAD ? 1 : 0][warp][k * 32 + lane] = z;
     }
-    const int at = (threadIdx.x & 7) * 4;
-    sum[0][grp][at] = y.x; sum[0][grp][at + 1] = y.y; sum[0][grp][at + 2] = y.z; sum[0][grp][at + 3] = y.w;
-    if (GRAD) {
-        constexpr int w = GRAD ? 1 : 0;
-        sum[w][grp][at] = z.x; sum[w][grp][at + 1] = z.y; sum[w][grp][at + 2] = z.z; sum[w][grp][at + 3] = z.w;
-    }
-    total = block_sum(total, red);                            // (and every thread's sums are there)
-    const int d = int(blockIdx.y) * kJoinDims + threadIdx.x;
-    if (threadIdx.x < kJoinDims && d < hd) {
+    __syncthreads();
+    for (int d = threadIdx.x; d < hd; d += kJoinThreads) {
         float a = 0.f, c = 0.f;
 #pragma unroll
-        for (int i = 0; i < kGroups; ++i) {
-            a += sum[0][i][threadIdx.x];
-            if (GRAD) c += sum[GRAD ? 1 : 0][i][threadIdx.x];
+        for (int w = 0; w < kJoinWarps; ++w) {
+            a += reinterpret_cast<const float *>(sum[0][w])[d];
+            if (GRAD) c += reinterpret_cast<const float *>(sum[GRAD ? 1 : 0][w])[d];
         }
         store_float(static_cast<T *>(p.out) + row * hd + d,
                     GRAD ? p.scale * fmaf(-total, c, a) : total == 0.f ? 0.f : a / total);
     }
-    if (!GRAD && threadIdx.x == 0 && blockIdx.y == 0)
-        p.out_lse[row] = total == 0.f ? -INFINITY : fmaf(log2f(total), kLn2, top * kLn2);
+    if (!GRAD && threadIdx.x == 0) p.out_lse[row] = total == 0.f ? -INFINITY : fmaf(log2f(total), kLn2, top * kLn2);
 }
 
 bool sizes_ok(const tlb_kv8 *c, int64_t n_seq, int32_t n_heads, int64_t max_len) {
@@ -517,94 +631,74 @@ bool sizes_ok(const tlb_kv8 *c, int64_t n_seq, int32_t n_heads, int64_t max_len)
            c->head_dim % 16 == 0 && c->head_dim <= 256 && c->n_slots < (int64_t(1) << 31);
 }
 
-// Chunks of keys.  One sequence: as long as gives four CTAs an SM (their queries and sums cost as much as some steps).
-// More: 512 keys at most, since lengths are only known on the device, and a long sequence among short ones has to
-// be spread.  64 keys at least (a step of each warp), and 65536 CTAs at most, which bounds the workspace.
-struct Split {
-    int tiles, splits, chunk;
-    int64_t units;
-};
-
-Split split_of(const tlb_kv8 &c, int64_t n_seq, int n_heads, int64_t max_len, bool grad) {
-    const int group = n_heads / c.n_kv_heads;
-    Split s;
-    s.tiles = int(ceil_div(group, tile_heads(grad)));
-    s.units = n_seq * c.n_kv_heads * s.tiles;
-    const int64_t keys = s.units * max_len, per = int64_t(kStep) * kWarps;
-    int64_t chunk = ceil_div(keys, int64_t(num_sms()) * 4);
-    if (n_seq > 1 && chunk > 512) chunk = 512;
-    if (chunk < per) chunk = per;
-    const int64_t least = ceil_div(keys, 65536);
-    chunk = ceil_div(chunk > least ? chunk : least, per) * per;
-    const int64_t all = ceil_div(max_len > 1 ? max_len : 1, per) * per;
-    if (chunk > all) chunk = all;
-    s.chunk = int(chunk);
-    s.splits = int(ceil_div(max_len > 1 ? max_len : 1, chunk));
-    return s;
-}
-
 struct Layout {
-    size_t part, sums, newest, bytes;
+    size_t part, sums, parts, newest, D, bytes;
 };
 
-Layout layout_of(const tlb_kv8 &c, int64_t n_seq, int n_heads, int64_t max_len, bool grad) {
-    const Split s = split_of(c, n_seq, n_heads, max_len, grad);
+// CTAs at a time: four an SM (two with heads of more than 128 values).
+int cta_most(const tlb_kv8 &c) { return num_sms() * (c.head_dim <= 128 ? 4 : 2); }
+
+Layout layout_of(const tlb_kv8 &c, int64_t n_seq, int n_heads, bool grad) {
     WsPlan p;
     Layout l{};
-    const size_t rows = size_t(n_seq) * n_heads;
-    if (grad || s.splits > 1) {
-        l.part = p.take(rows * s.splits * c.head_dim * (grad ? 2 : 1) * sizeof(float));
-        l.sums = p.take(rows * s.splits * sizeof(float2));
+    const size_t rows = size_t(n_seq) * n_heads, parts = size_t(cta_most(c)) * 2 * 8;
+    l.part = p.take(parts * c.head_dim * sizeof(float));
+    l.sums = p.take(parts * sizeof(float2));
+    l.parts = p.take(size_t(n_seq) * c.n_kv_heads * size_t(ceil_div(n_heads / c.n_kv_heads, tile_heads(grad))) * sizeof(int2));
+    if (grad) {
+        l.newest = p.take(rows * sizeof(float2));
+        l.D = p.take(rows * sizeof(float));
     }
-    if (grad) l.newest = p.take(rows * sizeof(float2));
     l.bytes = p.off;
     return l;
 }
 
 size_t ws_bytes_of(const tlb_kv8 *c, int64_t n_seq, int32_t n_heads, int64_t max_len, bool grad) {
     if (!sizes_ok(c, n_seq, n_heads, max_len)) return 0;
-    const size_t fwd = layout_of(*c, n_seq, n_heads, max_len, false).bytes;
-    const size_t bwd = grad ? layout_of(*c, n_seq, n_heads, max_len, true).bytes : 0;
-    return fwd > bwd ? fwd : bwd;
+    const size_t fwd = layout_of(*c, n_seq, n_heads, false).bytes, bwd = layout_of(*c, n_seq, n_heads, true).bytes;
+    return grad && bwd > fwd ? bwd : fwd;
 }
 
 template <typename T, int HD, bool GRAD>
-int attn_launch(const AttnParams &p, const Split &s, cudaStream_t st) {
+int attn_launch(const AttnParams &p, cudaStream_t st) {
     auto kernel = kv8_attn_kernel<T, HD, GRAD>;
     constexpr int smem = smem_bytes<HD, GRAD>();
     static_assert(smem >= kWarps * 8 * HD * 4, "the warps' sums fit where the stages were");
     if (smem > 48 * 1024) TLB_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
-    kernel<<<unsigned(s.units * s.splits), kWarps * 32, smem, st>>>(p);
+    kernel<<<unsigned(p.ctas), kWarps * 32, smem, st>>>(p);
     TLB_TRY(check_launch(GRAD ? "kv8_attn_backward" : "kv8_attn_forward"));
-    if (!GRAD && s.splits == 1) return TLB_OK;
-    const dim3 grid(unsigned(p.rows), unsigned(ceil_div(p.c.head_dim, kJoinDims)) + (GRAD ? 1 : 0));
-    TLB_CUDA(launch_dependent(kv8_attn_join_kernel<T, GRAD>, grid, dim3(kJoinThreads), 0, st, p));
+    const int64_t rows = p.n_seq * p.n_heads + (GRAD ? p.n_seq * p.c.n_kv_heads : 0);
+    TLB_CUDA(launch_dependent(kv8_attn_join_kernel<T, GRAD>, dim3(unsigned(rows)), dim3(kJoinThreads), 0, st, p));
     return check_launch("kv8_attn_join");
 }
 
 template <typename T, bool GRAD>
-int attn_run(const AttnParams &p, const Split &s, cudaStream_t st) {
-    return p.c.head_dim <= 64 ? attn_launch<T, 64, GRAD>(p, s, st)
-           : p.c.head_dim <= 128 ? attn_launch<T, 128, GRAD>(p, s, st)
-                                 : attn_launch<T, 256, GRAD>(p, s, st);
+int attn_run(const AttnParams &p, cudaStream_t st) {
+    return p.c.head_dim <= 64 ? attn_launch<T, 64, GRAD>(p, st)
+           : p.c.head_dim <= 128 ? attn_launch<T, 128, GRAD>(p, st)
+                                 : attn_launch<T, 256, GRAD>(p, st);
 }
 
-AttnParams params_of(const tlb_kv8 &c, const Kv8Pages &pg, int64_t n_seq, int n_heads, const Split &s, const Layout &l, float scale, const void *q,
+AttnParams params_of(const tlb_kv8 &c, const Kv8Pages &pg, int64_t n_seq, int n_heads, bool grad, float scale, const void *q,
                      void *ws) {
+    const Layout l = layout_of(c, n_seq, n_heads, grad);
     AttnParams p{};
     p.c = c;
     p.pg = pg;
-    p.rows = n_seq * n_heads;
+    p.n_seq = n_seq;
     p.n_heads = n_heads;
     p.group = n_heads / c.n_kv_heads;
-    p.tiles = s.tiles;
-    p.splits = s.splits;
-    p.chunk = s.chunk;
+    p.tiles = int(ceil_div(p.group, tile_heads(grad)));
+    // no more than the longest sequences could fill (max_len bounds them)
+    const int64_t most = (n_seq * c.n_kv_heads * p.tiles * (kFixed + ceil_div(pg.max_len, kStep))) / kLeast;
+    p.ctas = int(most < cta_most(c) ? (most > 1 ? most : 1) : cta_most(c));
     p.scale = scale;
     p.q = q;
     p.part = ws_at<float>(ws, l.part);
     p.sums = ws_at<float2>(ws, l.sums);
+    p.parts = ws_at<int2>(ws, l.parts);
     p.newest = ws_at<float2>(ws, l.newest);
+    p.D = ws_at<float>(ws, l.D);
     return p;
 }
 
@@ -658,12 +752,10 @@ int tlb_kv8_attn_forward(const tlb_kv8 *cache, const int32_t *pages, int64_t max
     if (n_seq == 0) return TLB_OK;
     TLB_REQUIRE(ctx && lse, TLB_EINVAL, "kv8_attn_forward: null pointer");
     TLB_REQUIRE(aligned16(ctx), TLB_EINVAL, "kv8_attn_forward: ctx must be 16-byte aligned");
-    const Split sp = split_of(*cache, n_seq, n_heads, max_len, false);
-    AttnParams p = params_of(*cache, pg, n_seq, n_heads, sp, layout_of(*cache, n_seq, n_heads, max_len, false), scale, q, ws);
+    AttnParams p = params_of(*cache, pg, n_seq, n_heads, false, scale, q, ws);
     p.out = ctx;
     p.out_lse = lse;
-    return type == TLB_W_F32 ? attn_run<float, false>(p, sp, as_stream(stream))
-                             : attn_run<__nv_bfloat16, false>(p, sp, as_stream(stream));
+    return type == TLB_W_F32 ? attn_run<float, false>(p, as_stream(stream)) : attn_run<__nv_bfloat16, false>(p, as_stream(stream));
 }
 
 int tlb_kv8_attn_backward(const tlb_kv8 *cache, const int32_t *pages, int64_t max_pages, int32_t page,
@@ -678,15 +770,13 @@ int tlb_kv8_attn_backward(const tlb_kv8 *cache, const int32_t *pages, int64_t ma
     TLB_REQUIRE(lse && d_ctx && d_q && d_k && d_v, TLB_EINVAL, "kv8_attn_backward: null pointer");
     TLB_REQUIRE(aligned16(d_ctx) && aligned16(d_q) && aligned16(d_k) && aligned16(d_v), TLB_EINVAL,
                 "kv8_attn_backward: d_ctx, d_q, d_k and d_v must be 16-byte aligned");
-    const Split sp = split_of(*cache, n_seq, n_heads, max_len, true);
-    AttnParams p = params_of(*cache, pg, n_seq, n_heads, sp, layout_of(*cache, n_seq, n_heads, max_len, true), scale, q, ws);
+    AttnParams p = params_of(*cache, pg, n_seq, n_heads, true, scale, q, ws);
     p.lse = lse;
     p.d_ctx = d_ctx;
     p.out = d_q;
     p.d_k = d_k;
     p.d_v = d_v;
-    return type == TLB_W_F32 ? attn_run<float, true>(p, sp, as_stream(stream))
-                             : attn_run<__nv_bfloat16, true>(p, sp, as_stream(stream));
+    return type == TLB_W_F32 ? attn_run<float, true>(p, as_stream(stream)) : attn_run<__nv_bfloat16, true>(p, as_stream(stream));
 }
 
 }  // extern "C"
