@@ -105,7 +105,15 @@ constexpr int kFixed = 12, kLeast = 4;    // kLeast: the weight that is worth a 
 
 __device__ __forceinline__ int64_t steps_of(int len) { return (len + kStep - 1) / kStep; }
 __device__ __forceinline__ int cta_count(int64_t total, int most) { return int(max(int64_t(1), min(int64_t(most), total / kLeast))); }
-__device__ __forceinline__ int64_t share(int64_t total, int n, int64_t c) { return total / n * c + total % n * c / n; }
+// a / b for b below 2^31; places of the line seldom need more than 32 bits, whose division is a few times shorter
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    return uint64_t(a) >> 32 ? a / b : int64_t(uint32_t(a) / uint32_t(b));
+}
+// total c / n, by parts so that no product overflows
+__device__ __forceinline__ int64_t share(int64_t total, int n, int c) {
+    const int64_t q = quotient(total, n);
+    return q * c + int(total - q * n) * c / n;
+}
 // What a CTA does next.
 struct Segment {
     int64_t pos, end, base;      // places of the line: next, the CTA's last, the sequence's first
@@ -182,14 +190,14 @@ __global__ void __launch_bounds__(kWarps * 32, HD <= 128 ? 4 : 2) kv8_attn_kerne
         total *= units;
         const int n = cta_count(total, p.ctas);
         if (int(blockIdx.x) >= n) return;
-        const int64_t lo = share(total, n, blockIdx.x);
+        const int64_t lo = share(total, n, int(blockIdx.x));
         if (lo >= base * units && lo < upto * units) {
             for (int64_t i = b0; i < b1; ++i) {
                 const int len = kv8_length(p.pg, i);
                 const int64_t next = base + kFixed + steps_of(len);
                 if (lo < next * units) {
                     sg.pos = lo;
-                    sg.end = share(total, n, int64_t(blockIdx.x) + 1);
+                    sg.end = share(total, n, int(blockIdx.x) + 1);
                     sg.base = base * units;
                     sg.b = i;
                     sg.len = len;
@@ -206,7 +214,7 @@ __global__ void __launch_bounds__(kWarps * 32, HD <= 128 ? 4 : 2) kv8_attn_kerne
         // the next segment that has something to do: steps [s0, s1) of a unit
         sg.run = 0;
         while (!sg.run && sg.pos < sg.end) {
-            const int64_t S = steps_of(sg.len), weight = kFixed + S, unit = (sg.pos - sg.base) / weight;
+            const int64_t S = steps_of(sg.len), weight = kFixed + S, unit = quotient(sg.pos - sg.base, weight);
             const int64_t from = sg.base + unit * weight, to = min(sg.end, from + weight);
             sg.unit = int(unit);
             sg.s0 = int(max(sg.pos - from - kFixed, int64_t(0)));
