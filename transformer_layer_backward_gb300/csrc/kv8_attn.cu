@@ -27,6 +27,7 @@ constexpr int kWarps = 4;
 constexpr int kStep = 16;                // keys of a warp's step
 constexpr int kStages = 2;               // one step ahead: four CTAs an SM keep 70 KB on their way (three stages and three CTAs: slower)
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kLog2eLow = 1.925963033500e-8f;      // log2(e) - float(log2(e))
 constexpr float kLow = 4096.f;           // the second half of a value holds what the first leaves, times this
 
 constexpr int tile_heads(bool grad) { return grad ? 4 : 8; }
@@ -287,7 +288,16 @@ __global__ void __launch_bounds__(kWarps * 32, HD <= 128 ? 4 : 2) kv8_attn_kerne
     const bool is_dp = GRAD && g >= 4;
     const float factor = is_dp ? pow2(s_f[1][g]) : p.scale * kLog2e * pow2(s_f[0][g]);
     const int my_head = is_dp ? g - 4 : g;
-    const float norm = GRAD && my_head < heads ? __ldg(p.lse + head0 + my_head) * kLog2e : 0.f;
+    // p = 2^(x - lse), x and lse over ln 2.  Of an lse between 0 and 100 the whole part goes into a factor, so that the
+    // difference is of x's size and keeps x's bits; the rest keeps the product's rounding
+    float norm = 0.f, p_scale = 1.f;
+    if (GRAD && my_head < heads) {
+        const float lse = __ldg(p.lse + head0 + my_head), hi = lse * kLog2e;
+        const float part = hi > 0.f && hi < 100.f ? rintf(hi) : 0.f;
+        const float lo = fmaf(lse, kLog2e, -hi) + lse * kLog2eLow;
+        norm = (hi - part) + (isfinite(lo) ? lo : 0.f);
+        p_scale = pow2(-int(part));
+    }
 
     float acc[NT][4];
 #pragma unroll
@@ -362,7 +372,7 @@ __global__ void __launch_bounds__(kWarps * 32, HD <= 128 ? 4 : 2) kv8_attn_kerne
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int key = (e >> 1) * 8 + 2 * t + (e & 1);
-                const float own = is_dp ? x[e] : ex2(x[e] - norm);
+                const float own = is_dp ? x[e] : ex2(x[e] - norm) * p_scale;
                 const float other = __shfl_xor_sync(0xffffffffu, own, 16);   // dp for the rows of p and the other way round
                 const float w = there(e) ? (is_dp ? other : own * other) : 0.f;
                 if (!is_dp) {
