@@ -383,7 +383,8 @@ int tlb_fp8_quantize(int32_t type, const void *x, int64_t rows, int64_t cols, in
  * product of its two scales, are float32.  A product of two scales below 2^-126 loses bits, one above
  * the float32 range is infinite (and makes a sum of 0 a NaN).  Same inputs, same bits.
  * S >= 0, in_dim >= 0, out_dim >= 0, up to 2^24 each (S = 0 or in_dim = 0 is a no-op; out_dim = 0 gives
- * sums of 0).  W, dY and dX 16-byte aligned, dX may not overlap them.
+ * sums of 0).  W, dY and dX 16-byte aligned, dX may not overlap them.  Up to 32 rows read W once through mma.sync,
+ * more run on the tcgen05 tensor cores; with out_dim % 16 != 0 both operands are copied to the workspace first, padded.
  * ws: its first 256 bytes zero-filled once, 256-byte aligned, tlb_linear_fp8_workspace_bytes() bytes. */
 size_t tlb_linear_fp8_workspace_bytes(int64_t S, int64_t out_dim, int64_t in_dim);
 int tlb_linear_fp8_backward(const uint8_t *W, const float *w_scales, const uint8_t *dY, const float *dy_scales, int64_t S,
@@ -431,7 +432,9 @@ int tlb_kv8_read(const tlb_kv8 *cache, const int64_t *slots, int64_t rows, int32
  * A sequence without a key (length <= 0) gives ctx 0, lse -infinity and gradients 0.  backward takes
  * the lse that forward gave.  All sums are float32; q, d_ctx and the weights of the sums
  * are taken apart into two halves that hold 22 bits or more of them.  Same inputs, same bits.
- * max_len bounds the work: set it near the longest length.  n_seq, max_len >= 0, max_len <= 2^30.
+ * The work goes by the lengths, which only the device reads: a captured call follows them.  max_len bounds
+ * them (a longer one counts as max_len).  0 <= n_seq, max_len <= 2^30, n_heads <= 65535, n_seq n_heads <= 2^30,
+ * n_slots < 2^31.
  * ws: its first 256 bytes zero-filled once, 256-byte aligned, tlb_kv8_attn_workspace_bytes() bytes
  * (grad: enough for both calls, else for forward; 0 for sizes that the calls refuse). */
 size_t tlb_kv8_attn_workspace_bytes(const tlb_kv8 *cache, int64_t n_seq, int32_t n_heads, int64_t max_len, int32_t grad);

@@ -356,10 +356,17 @@ def fp8_quantize(x, block_rows=1, q=None, scales=None, stream=None):
     rows, cols = x.shape
     blocks = (-(-rows // max(int(block_rows), 1)), -(-cols // _FP8_BLOCK))
     with _queued(x, stream):
-        q = torch.empty(rows, cols, dtype=_E4M3, device=x.device) if q is None else q
-        scales = torch.empty(blocks, dtype=torch.float32, device=x.device) if scales is None else scales
-        A.call("tlb_fp8_quantize", code, _at(x, None, x.dtype, x.device, "x"), rows, cols, int(block_rows),
-               _at(q, x.shape, _E4M3, x.device, "q"), _at(scales, blocks, torch.float32, x.device, "scales"), _raw_stream(stream, x.device))
+        at_x = _at(x, None, x.dtype, x.device, "x")
+        if q is None:
+            q = torch.empty((rows, cols), dtype=_E4M3, device=x.device)
+        else:
+            _at(q, x.shape, _E4M3, x.device, "q")
+        if scales is None:
+            scales = torch.empty(blocks, dtype=torch.float32, device=x.device)
+        else:
+            _at(scales, blocks, torch.float32, x.device, "scales")
+        A.call("tlb_fp8_quantize", code, at_x, rows, cols, int(block_rows), q.data_ptr(), scales.data_ptr(),
+               _raw_stream(stream, x.device))
     return q, scales
 
 
@@ -381,14 +388,17 @@ def linear_fp8_backward(W, w_scales, dY, dy_scales, out=None, accumulate=False, 
     code = _xent_code(dtype, "out")
     columns = -(-out_dim // _FP8_BLOCK)
     with _queued(W, stream):
-        out = torch.empty(S, in_dim, dtype=dtype, device=dev) if out is None else out
+        if out is None:
+            out = torch.empty((S, in_dim), dtype=dtype, device=dev)
+        else:
+            _at(out, (S, in_dim), dtype, dev, "out")
         own = ws is None
         if own:
             ws = linear_fp8_workspace(S, out_dim, in_dim, dev)
         A.call("tlb_linear_fp8_backward", _at(W, None, _E4M3, dev, "W"),
                _at(w_scales, (-(-in_dim // _FP8_BLOCK), columns), torch.float32, dev, "w_scales"),
                _at(dY, None, _E4M3, dev, "dY"), _at(dy_scales, (S, columns), torch.float32, dev, "dy_scales"), S, out_dim, in_dim,
-               code, _at(out, (S, in_dim), dtype, dev, "out"), 1 if accumulate else 0,
+               code, out.data_ptr(), 1 if accumulate else 0,
                _at(ws, None, torch.uint8, dev, "ws"), ws.numel(), _raw_stream(stream, dev))
         if own:
             _keep_status(ws)
@@ -445,11 +455,14 @@ def kv8_read(cache, slots, dtype=torch.float32, kv_layout="shd", k=None, v=None,
     dtype = dtype if k is None else k.dtype
     code = _xent_code(dtype, "k")
     with _queued(slots, stream):
-        k = torch.empty(shape, dtype=dtype, device=cache.device) if k is None else k
-        v = torch.empty(shape, dtype=dtype, device=cache.device) if v is None else v
+        if k is None:
+            k, v = (torch.empty(shape, dtype=dtype, device=cache.device) for _ in range(2))
+        else:
+            _at(k, shape, dtype, cache.device, "k")
+            _at(v, shape, dtype, cache.device, "v")
         strides = (n_kv * hd, hd) if kv_layout == "shd" else (hd, rows * hd)
-        A.call("tlb_kv8_read", cache, _at(slots, (rows,), torch.int64, cache.device, "slots"), rows, code,
-               _at(k, shape, dtype, cache.device, "k"), _at(v, shape, dtype, cache.device, "v"), *strides, _raw_stream(stream, cache.device))
+        A.call("tlb_kv8_read", cache, _at(slots, (rows,), torch.int64, cache.device, "slots"), rows, code, k.data_ptr(),
+               v.data_ptr(), *strides, _raw_stream(stream, cache.device))
     return k, v
 
 

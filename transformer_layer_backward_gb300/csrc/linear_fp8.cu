@@ -5,21 +5,27 @@
 // and added up in registers.
 //
 // More than kFewRows rows: tcgen05 (kind::f8f6f4), persistent CTA pairs on 256 x 256 super-tiles:
-//   warp 0      TMA producer: 128 x 128 bytes of dY and of W a stage and CTA (128-byte swizzle: one scale
-//               block is one swizzle row)
-//   warps 1, 2  one lane each of the even CTA issues four MMAs (M = 256, N = 128, K = 32) a k block, for one half of
-//               the columns, into two accumulators of 128 columns in turn: all of the tensor memory
-//   warps 4..11 a thread has one row and 128 of the columns: it keeps their sums in 128 registers and
-//               adds each k block's accumulator times its scale while the next one is multiplied.
-// Per CTA and k block the MMAs take 512 cycles, the sums 128 float32 additions a thread on two warps a
-// scheduler (256 issue slots as scalars, 128 as pairs) and 128 KB read from tensor memory.
+//   warp 0       TMA producer: 128 x 128 bytes of dY and of W a stage and CTA (128-byte swizzle: one scale
+//                block is one swizzle row)
+//   warps 1, 2   of the even CTA, one elected lane each, issue four MMAs (M = 256, N = 128, K = 32) a k block for
+//                one half of the columns, into two accumulators of 128 columns in turn: all of the tensor memory
+//   warps 4..19  a thread has one row and 64 of the columns: it keeps their sums in registers and adds each
+//                k block's accumulator times its scale while the next one is multiplied
 // Tiles that do not fill a last wave are shared by CTA pairs along K; their parts go to the workspace and
 // are joined in a fixed order by a second kernel.
+// What bounds it: an accumulator is in use from its MMA's start until both CTAs have read it out, about 1700 cycles
+// (MMA 260 to 400, commit to the readers 400, reading 350, arrival to the next MMA 500), and two k blocks fill the
+// tensor memory: 830 cycles a k block where the MMAs need 512.  2048 x 9728 x 2560: 56 us (1.8 PFLOP/s), of which 33 us
+// are the 76 k blocks of the whole tiles, 5 us the start and first blocks, 5 us the results' way out, 7 us the shared tiles' join.
+// Measured on the way there, same sizes: MMAs issued by a lane on its own 108 us and a release arrival of cluster scope
+// (it waits for the scales' loads) on top; one issuer and two accumulators of 256 columns 57 us; eight warps for the
+// sums with 128 columns each 62 to 71 us; waits that spin 71 us.
 //
 // Up to kFewRows rows: bound by the read of W.  A warp multiplies 16 rows of W by up to 8 rows of dY an mma.sync
 // (m16n8k32), straight from global memory: the 128 columns of a block may be summed in any order, so a lane's
 // 16 consecutive bytes of W and of dY serve as the operands' registers as they are.  The warps of a CTA, and
 // the CTAs of a cluster, share the columns of 16 rows and add up through shared memory in a fixed order.
+// 1 x 9728 x 2560: 9.1 us (25 MB: 2.7 TB/s; launch, one round of loads, the sums through the cluster).
 #include <cuda.h>
 
 #include <algorithm>
@@ -452,13 +458,15 @@ __global__ void __launch_bounds__(kThreads, 1) linear_fp8_tc_kernel(const __grid
                 if (++st == kStages) st = 0;
                 tc_fence_after();
                 if (any) {
+                    uint32_t v[2][16];
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
-                        uint32_t v[16];
-                        tmem_ld16(tbase + uint32_t(b * 128 + j * 16), v);
+                        // 16 columns on their way while the 16 before are added
+                        if (j == 0) tmem_ld16(tbase + uint32_t(b * 128), v[0]);
                         tmem_wait_ld();
+                        if (j < 3) tmem_ld16(tbase + uint32_t(b * 128 + (j + 1) * 16), v[(j + 1) & 1]);
 #pragma unroll
-                        for (int c = 0; c < 16; ++c) acc[j * 16 + c] = fmaf(__uint_as_float(v[c]), s, acc[j * 16 + c]);
+                        for (int c = 0; c < 16; ++c) acc[j * 16 + c] = fmaf(__uint_as_float(v[j & 1][c]), s, acc[j * 16 + c]);
                     }
                 }
                 tc_fence_before();
@@ -594,7 +602,7 @@ int map_of(CUtensorMap *map, const void *base, int64_t rows, int64_t cols, int64
 }
 
 template <typename T, bool WIDE>
-int tc_launch(const TcParams &p, cudaStream_t st) {
+int tc_launch(const TcParams &p, bool after_copies, cudaStream_t st) {
     auto kernel = linear_fp8_tc_kernel<T, WIDE>;
     TLB_CUDA(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kTcSmem));
     static const int regs = [&] {                             // the split shares out what the block is launched with
@@ -612,8 +620,10 @@ int tc_launch(const TcParams &p, cudaStream_t st) {
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;   // behind the copies of padded operands
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = after_copies ? 2 : 1;
     TLB_CUDA(cudaLaunchKernelEx(&cfg, kernel, p));
     TLB_TRY(check_launch("linear_fp8_tc"));
     if (p.sk_tiles == 0) return TLB_OK;
@@ -629,6 +639,7 @@ int tc_launch(const TcParams &p, cudaStream_t st) {
 __global__ void __launch_bounds__(256) pad_rows_kernel(const uint8_t *__restrict__ a, int64_t a_rows, uint8_t *__restrict__ a_to,
                                                        const uint8_t *__restrict__ b, int64_t b_rows,
                                                        uint8_t *__restrict__ b_to, int64_t cols, int64_t ld) {
+    pdl_trigger();                                            // the product's CTAs may be set up meanwhile
     const int64_t per = ld / 16, n = (a_rows + b_rows) * per;
     for (int64_t i = int64_t(blockIdx.x) * blockDim.x + threadIdx.x; i < n; i += int64_t(gridDim.x) * blockDim.x) {
         int64_t row = i / per;
@@ -658,7 +669,6 @@ __global__ void __launch_bounds__(256) pad_rows_kernel(const uint8_t *__restrict
         }
         *reinterpret_cast<uint4 *>((first ? a_to : b_to) + row * ld + c) = make_uint4(w[0], w[1], w[2], w[3]);
     }
-    pdl_trigger();
 }
 
 // ------------------------------------------------------------------ the call
@@ -720,7 +730,7 @@ int run(const uint8_t *W, const float *w_scales, const uint8_t *dY, const float 
     p.sk_pairs = pl.sk_pairs;
     p.pairs = pl.pairs;
     p.status = static_cast<uint32_t *>(ws);
-    return in % 4 == 0 ? tc_launch<T, true>(p, st) : tc_launch<T, false>(p, st);
+    return in % 4 == 0 ? tc_launch<T, true>(p, ld != out, st) : tc_launch<T, false>(p, ld != out, st);
 }
 
 // Sums of nothing.
@@ -755,6 +765,7 @@ int tlb_linear_fp8_backward(const uint8_t *W, const float *w_scales, const uint8
     TLB_REQUIRE(type == TLB_W_F32 || type == TLB_W_BF16, TLB_EINVAL, "linear_fp8_backward: type %d is neither f32 nor bf16", type);
     TLB_REQUIRE(S >= 0 && out_dim >= 0 && in_dim >= 0, TLB_EINVAL, "linear_fp8_backward: negative size");
     TLB_REQUIRE(S <= kMost && out_dim <= kMost && in_dim <= kMost, TLB_EUNSUPPORTED, "linear_fp8_backward: a size past 2^24");
+    TLB_REQUIRE(ceil_div(S, kTM) * ceil_div(in_dim, kTN) < (int64_t(1) << 31), TLB_EUNSUPPORTED, "linear_fp8_backward: dX is too large");
     if (S == 0 || in_dim == 0) return TLB_OK;
     TLB_REQUIRE(dX && (out_dim == 0 || (W && w_scales && dY && dy_scales)), TLB_EINVAL, "linear_fp8_backward: null pointer");
     TLB_REQUIRE(aligned16(W) && aligned16(dY) && aligned16(dX), TLB_EINVAL,
