@@ -36,8 +36,7 @@ constexpr float kLow = 4096.f;           // the second half of a value holds wha
 
 constexpr int tile_heads(bool grad) { return grad ? 4 : 8; }
 
-// Shared memory: the query's operand (and d_ctx's), then each warp's stages of keys, values and scales.
-template <int HD> constexpr int row_bytes() { return HD; }
+// Shared memory: the query's operand (and d_ctx's), then each warp's stages of keys, values, scales and a mask.
 template <int HD> constexpr int stage_bytes() { return 2 * kStep * HD + 3 * kStep * 4; }
 template <int HD, bool GRAD> constexpr int smem_bytes() {
     return (GRAD ? 2 : 1) * (HD / 16) * 32 * 16 + kWarps * kStages * stage_bytes<HD>();
@@ -535,7 +534,7 @@ struct Parts {
     __device__ __forceinline__ int64_t row(int c, int r) const { return (int64_t(c) * 2 + (c == c0 ? slot0 : 0)) * 8 + r; }
 };
 
-constexpr int kJoinThreads = 128, kJoinWarps = kJoinThreads / 32;
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 
 // Gradients of the newest key and value of one (sequence, KV head) from what the pass left of it.
 template <typename T>
@@ -583,7 +582,7 @@ __device__ __forceinline__ void newest_rows(const AttnParams &p, int64_t unit) {
     }
 }
 
-// Joins the parts of one query head, where its unit has more than one, in a fixed order: warps take every fourth, a
+// Joins the parts of one query head, where its unit has more than one, in a fixed order: warps take every eighth, a
 // lane four dimensions (and four from 128 on).  The gradient's last CTAs do the newest keys.
 template <typename T, bool GRAD>
 __global__ void __launch_bounds__(kJoinThreads) kv8_attn_join_kernel(const __grid_constant__ AttnParams p) {

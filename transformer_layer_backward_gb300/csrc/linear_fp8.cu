@@ -67,7 +67,7 @@ __device__ __forceinline__ void put4(T *p, int col, int cols, float4 y, bool add
 // eight lanes at a time; what they are added to is loaded kAhead rows ahead.
 template <typename T>
 __device__ __forceinline__ void put_rows4(T *dX, int row0, int rows, int col, int cols, const float4 *blk, int ch, int rl, bool add) {
-    constexpr int kAhead = 4;
+    constexpr int kAhead = 8;
     if (col >= cols) return;
     T *p = dX + int64_t(row0 + rl) * cols + col;
 #pragma unroll 1
@@ -90,7 +90,7 @@ __device__ __forceinline__ void put_rows4(T *dX, int row0, int rows, int col, in
 // The same where rows do not start at multiples of four elements: a row of 32 lanes at a time.
 template <typename T>
 __device__ __forceinline__ void put_rows1(T *dX, int row0, int rows, int col, int cols, const float *blk, int lane, bool add) {
-    constexpr int kAhead = 8;
+    constexpr int kAhead = 16;
     if (col >= cols) return;
     T *p = dX + int64_t(row0) * cols + col;
 #pragma unroll 1
