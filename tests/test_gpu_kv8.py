@@ -211,6 +211,16 @@ def test_attention(lib, lengths, heads, kv, hd, page, bf16):
     run(lib, lengths, heads, kv, hd, page, bf16, seed=len(lengths) + hd)
 
 
+def test_one_key_has_no_gradient(lib):
+    """Of a sequence of one key d_q and d_k are 0 exactly, and its value's gradient is d_ctx summed over the heads."""
+    import torch
+    cache, q, g, pages, lens, longest, K, V = problem(lib, [1, 1, 40], 8, 2, 64, 16, seed=8)
+    ctx, lse = lib.kv8_attn_forward(cache, q, pages, 16, lens, longest)
+    d_q, d_k, d_v = lib.kv8_attn_backward(cache, q, pages, 16, lens, longest, lse, g)
+    assert torch.count_nonzero(d_q[:2]) == 0 and torch.count_nonzero(d_k[:2]) == 0 and torch.count_nonzero(d_q[2]) > 0
+    compare("d_v", d_v[:2], list(host(g)[:2].reshape(2, 2, 4, 64).sum(2)), False)
+
+
 def test_attention_of_a_long_sequence(lib):
     run(lib, [20011], 8, 2, 128, 64, seed=3)
 

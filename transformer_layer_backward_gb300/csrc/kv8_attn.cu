@@ -500,7 +500,8 @@ __global__ void __launch_bounds__(kWarps * 32, HD <= 128 ? 4 : 2) kv8_attn_kerne
             } else if (r < 4) {
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) z += all[(w * 8 + r + 4) * HD + d];
-                store_float(static_cast<T *>(p.out) + (head0 + h) * hd + d, p.scale * fmaf(-D, z, y));
+                // (of one key there is no gradient, whatever its weight came to)
+                store_float(static_cast<T *>(p.out) + (head0 + h) * hd + d, len == 1 ? 0.f : p.scale * fmaf(-D, z, y));
                 if (d == 0) p.D[head0 + h] = D;
             }
         }
@@ -543,7 +544,8 @@ __device__ __forceinline__ void newest_rows(const AttnParams &p, int64_t unit) {
     const int64_t b = unit / nkv;
     const int kvh = int(unit - b * nkv);
     const int64_t row0 = b * p.n_heads + int64_t(kvh) * p.group;
-    const bool any = kv8_length(p.pg, b) > 0;
+    const int len = kv8_length(p.pg, b);
+    const bool any = len > 0;
     __shared__ float2 s_w[kJoinWarps];                        // ds and p of a warp's head
     float dk[256 / kJoinThreads] = {}, dv[256 / kJoinThreads] = {};
     for (int e0 = 0; e0 < p.group && any; e0 += kJoinWarps) {
@@ -558,7 +560,7 @@ __device__ __forceinline__ void newest_rows(const AttnParams &p, int64_t unit) {
                 D = warp_sum(D);
             }
             const float2 w = __ldcg(p.newest + row0 + e);
-            if (lane == 0) s_w[warp] = make_float2(w.x * (w.y - D) * p.scale, w.x);
+            if (lane == 0) s_w[warp] = make_float2(len == 1 ? 0.f : w.x * (w.y - D) * p.scale, w.x);
         }
         __syncthreads();
         for (int i = 0; i < kJoinWarps && e0 + i < p.group; ++i)
