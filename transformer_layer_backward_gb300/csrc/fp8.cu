@@ -6,6 +6,18 @@ namespace tlb {
 
 namespace {
 
+// Eight consecutive elements.
+__device__ __forceinline__ void load_float8(const float *p, float (&v)[8]) {
+    const float4 a = load_float4(p), b = load_float4(p + 4);
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ void load_float8(const __nv_bfloat16 *p, float (&v)[8]) {
+    const uint4 a = ld_stream_u4(p);
+    v[0] = bf16_lo(a.x); v[1] = bf16_hi(a.x); v[2] = bf16_lo(a.y); v[3] = bf16_hi(a.y);
+    v[4] = bf16_lo(a.z); v[5] = bf16_hi(a.z); v[6] = bf16_lo(a.w); v[7] = bf16_hi(a.w);
+}
+
 // Blocks of 1 x 128: a warp takes kRowBlocks blocks at a time, whose loads are all issued before the
 // first is used; a lane holds four columns of each.  Bound by memory: 5 (float32) or 3 bytes a value.
 // 2048 x 9728 float32: 17.7 us, 5.7 TB/s.
@@ -58,16 +70,47 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *__restrict_
     }
 }
 
-// Eight consecutive elements.
-__device__ __forceinline__ void load_float8(const float *p, float (&v)[8]) {
-    const float4 a = load_float4(p), b = load_float4(p + 4);
-    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void load_float8(const __nv_bfloat16 *p, float (&v)[8]) {
-    const uint4 a = ld_stream_u4(p);
-    v[0] = bf16_lo(a.x); v[1] = bf16_hi(a.x); v[2] = bf16_lo(a.y); v[3] = bf16_hi(a.y);
-    v[4] = bf16_lo(a.z); v[5] = bf16_hi(a.z); v[6] = bf16_lo(a.w); v[7] = bf16_hi(a.w);
+// The same with 16 lanes a block and eight columns a lane, for bf16 (16 bytes loaded a lane, 8 stored): a warp takes
+// kRowPairs pairs of blocks at a time.  The maximum is taken of the 16-bit magnitudes, two at a time.  4096 x 9728:
+// 21.5 us, 5.6 TB/s (four columns a lane, 8-byte loads: 61 us; the maximum of floats by shuffles: 29 us).
+constexpr int kRowPairs = 4;
+
+__global__ void __launch_bounds__(256, 4) quantize_rows8_kernel(const __nv_bfloat16 *__restrict__ x, int64_t cols, int64_t nblk,
+                                                                int64_t items, uint8_t *__restrict__ q,
+                                                                float *__restrict__ scales) {
+    const int lane = threadIdx.x & 31, part = lane & 15;
+    const bool upper = lane >= 16;
+    const int64_t warps = int64_t(gridDim.x) * (blockDim.x >> 5);
+    for (int64_t i0 = (int64_t(blockIdx.x) * (blockDim.x >> 5) + (threadIdx.x >> 5)) * (2 * kRowPairs); i0 < items;
+         i0 += warps * (2 * kRowPairs)) {
+        uint4 v[kRowPairs];
+        int64_t at[kRowPairs];
+        bool there[kRowPairs];
+#pragma unroll
+        for (int u = 0; u < kRowPairs; ++u) {
+            const int64_t i = i0 + 2 * u + (upper ? 1 : 0);
+            const int64_t row = cols == nblk * kFp8Block ? 0 : i / nblk;
+            const int64_t blk = i - row * nblk;
+            at[u] = row * cols + blk * kFp8Block + part * 8;
+            there[u] = i < items && (cols == nblk * kFp8Block || blk * kFp8Block + part * 8 < cols);
+            v[u] = there[u] ? ld_stream_u4(x + at[u]) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int u = 0; u < kRowPairs; ++u) {
+            const uint32_t two = __vmaxu2(__vmaxu2(v[u].x & 0x7FFF7FFFu, v[u].y & 0x7FFF7FFFu),
+                                          __vmaxu2(v[u].z & 0x7FFF7FFFu, v[u].w & 0x7FFF7FFFu));
+            const uint32_t mine = max(two & 0xFFFFu, two >> 16) << 16;            // as float bits
+            const uint32_t lo = __reduce_max_sync(0xffffffffu, upper ? 0u : mine), hi = __reduce_max_sync(0xffffffffu, upper ? mine : 0u);
+            float inv;
+            const float s = block_scale(upper ? hi : lo, inv);
+            if (there[u]) {
+                *reinterpret_cast<uint2 *>(q + at[u]) =
+                    make_uint2(to_e4m3x4(bf16_lo(v[u].x) * inv, bf16_hi(v[u].x) * inv, bf16_lo(v[u].y) * inv, bf16_hi(v[u].y) * inv),
+                               to_e4m3x4(bf16_lo(v[u].z) * inv, bf16_hi(v[u].z) * inv, bf16_lo(v[u].w) * inv, bf16_hi(v[u].w) * inv));
+                if (part == 0) scales[i0 + 2 * u + (upper ? 1 : 0)] = s;
+            }
+        }
+    }
 }
 
 // Blocks of 128 x 128: a CTA of 512 threads holds one in registers, 32 values a thread, 16 lanes a row (16 bytes of bf16
@@ -136,6 +179,12 @@ int quantize_launch(const T *x, int64_t rows, int64_t cols, int block_rows, uint
                      (reinterpret_cast<uintptr_t>(q) & 3) == 0;
     if (block_rows == 1) {
         const int64_t items = rows * nblk;
+        if constexpr (sizeof(T) == 2)
+            if (cols % 8 == 0 && aligned16(x) && (reinterpret_cast<uintptr_t>(q) & 7) == 0) {
+                quantize_rows8_kernel<<<stream_grid(ceil_div(items, 2 * kRowPairs) * 32, 256), 256, 0, st>>>(x, cols, nblk, items, q,
+                                                                                                         scales);
+                return check_launch("fp8_quantize_rows");
+            }
         const unsigned grid = stream_grid(ceil_div(items, kRowBlocks) * 32, 256);
         if (vec) quantize_rows_kernel<T, true><<<grid, 256, 0, st>>>(x, cols, nblk, items, q, scales);
         else quantize_rows_kernel<T, false><<<grid, 256, 0, st>>>(x, cols, nblk, items, q, scales);

@@ -64,7 +64,8 @@ template <> __device__ __forceinline__ float load_float<__nv_bfloat16>(const __n
 // Four consecutive elements, aligned to their size.
 __device__ __forceinline__ float4 load_float4(const float *p) { return ld_stream(reinterpret_cast<const float4 *>(p)); }
 __device__ __forceinline__ float4 load_float4(const __nv_bfloat16 *p) {
-    const uint2 v = __ldg(reinterpret_cast<const uint2 *>(p));
+    uint2 v;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
     return make_float4(bf16_lo(v.x), bf16_hi(v.x), bf16_lo(v.y), bf16_hi(v.y));
 }
 __device__ __forceinline__ void store_float4(float *p, float4 v) { *reinterpret_cast<float4 *>(p) = v; }
