@@ -383,7 +383,7 @@ int tlb_fp8_quantize(int32_t type, const void *x, int64_t rows, int64_t cols, in
  * product of its two scales, are float32.  A product of two scales below 2^-126 loses bits, one above
  * the float32 range is infinite (and makes a sum of 0 a NaN).  Same inputs, same bits.
  * S >= 0, in_dim >= 0, out_dim >= 0, up to 2^24 each (S = 0 or in_dim = 0 is a no-op; out_dim = 0 gives
- * sums of 0).  W, dY and dX 16-byte aligned, dX may not overlap them.  Up to 32 rows read W once through mma.sync,
+ * sums of 0).  W, dY and dX 16-byte aligned, dX may not overlap them.  Up to 8 rows read W once through mma.sync,
  * more run on the tcgen05 tensor cores; with out_dim % 16 != 0 both operands are copied to the workspace first, padded.
  * ws: its first 256 bytes zero-filled once, 256-byte aligned, tlb_linear_fp8_workspace_bytes() bytes. */
 size_t tlb_linear_fp8_workspace_bytes(int64_t S, int64_t out_dim, int64_t in_dim);

@@ -130,12 +130,12 @@ def test_sequence_cached_in_8_bits_and_its_gradient_through_8_bit_weights(lib):
     q, s = lib.fp8_quantize(g)
     first = lib.launch_count()
     all_rows = lib.linear_fp8_backward(W, w_s, q, s)
-    few = lib.linear_fp8_backward(W, w_s, q[:20], s[:20])
+    few = lib.linear_fp8_backward(W, w_s, q[:7], s[:7])
     names = lib.launch_names(first)
     assert "linear_fp8_tc" in names and "linear_fp8_rows" in names
     ref = blocks8.linear_backward(host(W.float()), host(w_s), host(q.float()), host(s))
     check("all rows", host(all_rows), ref)
-    check("few rows", host(few), ref[:20])
+    check("few rows", host(few), ref[:7])
     lib.workspace_status()
     k, v = dev(rows_of(S, 2, 64, 8)), dev(rows_of(S, 2, 64, 9))
     cache = lib.kv8_cache(S, 2, 64)

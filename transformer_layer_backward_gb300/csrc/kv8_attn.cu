@@ -16,7 +16,7 @@
 // Warps, then the CTAs that share a unit (a second kernel), are joined in a fixed order.
 // Of the time of a step (600 instructions for 16 keys in the gradient, a quarter of them conversions to halves)
 // half is latency: 16 warps an SM, since a warp's sums take 64 registers a thread.  131072 keys of 8 KV heads and 32 query
-// heads of 128: gradient 76 us (277 MB, 3.6 TB/s); a batch of 32 sequences up to 16384 keys: forward 38 us (124 MB).
+// heads of 128: gradient 73 us (277 MB, 3.8 TB/s); a batch of 32 sequences up to 16384 keys: forward 38 us (124 MB).
 // Slower: 32 keys a step (82 us: three CTAs an SM), the sums of the step before beside a step's logits (81 us).
 #include <cmath>
 
@@ -105,7 +105,9 @@ struct AttnParams {
 // of S steps of 16 keys weighing kFixed + S, since its start and its end cost as much as some steps.  CTA c of n takes
 // [total c / n, total (c + 1) / n) of that line: as many CTAs as are on the GPU at a time, each with the same
 // weight whatever the lengths, which only the device knows.  The first kFixed of a unit are no steps.
-constexpr int kFixed = 12, kLeast = 4;    // kLeast: the weight that is worth a CTA (a step of each warp)
+// kLeast: the weight that is worth a CTA (a step of each warp).  kMostParts: CTAs a unit, on average, since one CTA of
+// the join reads all its parts (65536 keys of one KV head: 608 parts 41 us, 128 19 us).
+constexpr int kFixed = 12, kLeast = 4, kMostParts = 128;
 
 __device__ __forceinline__ int64_t steps_of(int len) { return (len + kStep - 1) / kStep; }
 __device__ __forceinline__ int cta_count(int64_t total, int most) { return int(max(int64_t(1), min(int64_t(most), total / kLeast))); }
@@ -541,13 +543,14 @@ constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 template <typename T>
 __device__ __forceinline__ void newest_rows(const AttnParams &p, int64_t unit) {
     const int hd = p.c.head_dim, nkv = p.c.n_kv_heads, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int d = threadIdx.x;                                // head_dim <= 256
     const int64_t b = unit / nkv;
     const int kvh = int(unit - b * nkv);
     const int64_t row0 = b * p.n_heads + int64_t(kvh) * p.group;
     const int len = kv8_length(p.pg, b);
     const bool any = len > 0;
     __shared__ float2 s_w[kJoinWarps];                        // ds and p of a warp's head
-    float dk[256 / kJoinThreads] = {}, dv[256 / kJoinThreads] = {};
+    float dk = 0.f, dv = 0.f;
     for (int e0 = 0; e0 < p.group && any; e0 += kJoinWarps) {
         const int e = e0 + warp;
         if (e < p.group) {
@@ -563,24 +566,17 @@ __device__ __forceinline__ void newest_rows(const AttnParams &p, int64_t unit) {
             if (lane == 0) s_w[warp] = make_float2(len == 1 ? 0.f : w.x * (w.y - D) * p.scale, w.x);
         }
         __syncthreads();
-        for (int i = 0; i < kJoinWarps && e0 + i < p.group; ++i)
-#pragma unroll
-            for (int k = 0; k < 256 / kJoinThreads; ++k) {
-                const int d = threadIdx.x + k * kJoinThreads;
-                if (d >= hd) continue;
-                const int64_t at = (row0 + e0 + i) * hd + d;
-                // a weight of 0 adds nothing (a newest key that is not there)
-                if (s_w[i].x != 0.f) dk[k] = fmaf(s_w[i].x, load_float(static_cast<const T *>(p.q) + at), dk[k]);
-                if (s_w[i].y != 0.f) dv[k] = fmaf(s_w[i].y, load_float(static_cast<const T *>(p.d_ctx) + at), dv[k]);
-            }
+        for (int i = 0; i < kJoinWarps && e0 + i < p.group && d < hd; ++i) {
+            const int64_t at = (row0 + e0 + i) * hd + d;
+            // a weight of 0 adds nothing (a newest key that is not there)
+            if (s_w[i].x != 0.f) dk = fmaf(s_w[i].x, load_float(static_cast<const T *>(p.q) + at), dk);
+            if (s_w[i].y != 0.f) dv = fmaf(s_w[i].y, load_float(static_cast<const T *>(p.d_ctx) + at), dv);
+        }
         __syncthreads();
     }
-#pragma unroll
-    for (int k = 0; k < 256 / kJoinThreads; ++k) {
-        const int d = threadIdx.x + k * kJoinThreads;
-        if (d >= hd) continue;
-        store_float(static_cast<T *>(p.d_k) + unit * hd + d, dk[k]);
-        store_float(static_cast<T *>(p.d_v) + unit * hd + d, dv[k]);
+    if (d < hd) {
+        store_float(static_cast<T *>(p.d_k) + unit * hd + d, dk);
+        store_float(static_cast<T *>(p.d_v) + unit * hd + d, dv);
     }
 }
 
@@ -713,7 +709,8 @@ AttnParams params_of(const tlb_kv8 &c, const Kv8Pages &pg, int64_t n_seq, int n_
     p.group = n_heads / c.n_kv_heads;
     p.tiles = int(ceil_div(p.group, tile_heads(grad)));
     // no more than the longest sequences could fill (max_len bounds them)
-    const int64_t most = (n_seq * c.n_kv_heads * p.tiles * (kFixed + ceil_div(pg.max_len, kStep))) / kLeast;
+    const int64_t units = n_seq * c.n_kv_heads * p.tiles, full = units * (kFixed + ceil_div(pg.max_len, kStep)) / kLeast;
+    const int64_t parts = units * kMostParts, most = full < parts ? full : parts;
     p.ctas = int(most < cta_most(c) ? (most > 1 ? most : 1) : cta_most(c));
     p.scale = scale;
     p.q = q;

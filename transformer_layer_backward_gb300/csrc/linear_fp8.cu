@@ -40,7 +40,7 @@ namespace tlb {
 
 namespace {
 
-constexpr int kFewRows = 32;
+constexpr int kFewRows = 8;             // from nine on the tensor cores win: 2560 x 9728, 16 rows 15 us against 22
 constexpr int64_t kMost = int64_t(1) << 24;
 
 // ------------------------------------------------------------------ results
@@ -133,11 +133,10 @@ __device__ __forceinline__ uint4 piece(const uint8_t *row, int col, int out, boo
     return there && col < out ? ld_stream_u4(row + col) : make_uint4(0, 0, 0, 0);
 }
 
-// NT: n tiles of 8 rows of dY.
-template <typename T, int NT>
-__global__ void __launch_bounds__(kRowWarps * 32, NT == 1 ? 5 : 1) linear_fp8_rows_kernel(const RowsParams p) {
-    __shared__ float part[kRowWarps][16][8 * NT + 1];
-    __shared__ float mine[16][8 * NT];
+template <typename T>
+__global__ void __launch_bounds__(kRowWarps * 32, 5) linear_fp8_rows_kernel(const RowsParams p) {
+    __shared__ float part[kRowWarps][16][kFewRows + 1];
+    __shared__ float mine[16][kFewRows];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     uint32_t rank, size;
     asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
@@ -146,73 +145,60 @@ __global__ void __launch_bounds__(kRowWarps * 32, NT == 1 ? 5 : 1) linear_fp8_ro
     const int u = int(rank) * kRowWarps + warp, U = int(size) * kRowWarps;
     const int kb0 = int(int64_t(p.nblk) * u / U), kb1 = int(int64_t(p.nblk) * (u + 1) / U);
     const uint8_t *w0 = p.W + int64_t(min(i0 + g, p.in - 1)) * p.ld_w, *w1 = p.W + int64_t(min(i0 + g + 8, p.in - 1)) * p.ld_w;
-    const bool r0 = i0 + g < p.in, r1 = i0 + g + 8 < p.in;
+    const bool r0 = i0 + g < p.in, r1 = i0 + g + 8 < p.in, there = g < p.S;
     const float *wsc = p.ws + int64_t(i0 / kFp8Block) * p.nblk;
-    float acc[NT][4] = {};
+    const uint8_t *y = p.dY + int64_t(there ? g : 0) * p.ld_y;
+    float acc[4] = {};
 #pragma unroll 2
     for (int kb = kb0; kb < kb1; ++kb) {
         const int c = kb * kFp8Block + t * 16;
         const uint4 a0 = piece(w0, c, p.out, r0), a1 = piece(w1, c, p.out, r1);
         const uint4 a2 = piece(w0, c + 64, p.out, r0), a3 = piece(w1, c + 64, p.out, r1);
         const float sw = __ldg(wsc + kb);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int s = n * 8 + g;
-            const bool there = s < p.S;
-            const uint8_t *y = p.dY + int64_t(there ? s : 0) * p.ld_y;
-            uint4 b0 = make_uint4(0, 0, 0, 0), b1 = b0;
-            if (there && c < p.out) b0 = __ldg(reinterpret_cast<const uint4 *>(y + c));
-            if (there && c + 64 < p.out) b1 = __ldg(reinterpret_cast<const uint4 *>(y + c + 64));
-            float d[4] = {0.f, 0.f, 0.f, 0.f};
-            mma_e4m3(d, a0.x, a1.x, a0.y, a1.y, b0.x, b0.y);
-            mma_e4m3(d, a0.z, a1.z, a0.w, a1.w, b0.z, b0.w);
-            mma_e4m3(d, a2.x, a3.x, a2.y, a3.y, b1.x, b1.y);
-            mma_e4m3(d, a2.z, a3.z, a2.w, a3.w, b1.z, b1.w);
-            const int s0 = n * 8 + 2 * t;
-            const float f0 = s0 < p.S ? sw * __ldg(p.ys + int64_t(s0) * p.nblk + kb) : 0.f;
-            const float f1 = s0 + 1 < p.S ? sw * __ldg(p.ys + int64_t(s0 + 1) * p.nblk + kb) : 0.f;
-            acc[n][0] = fmaf(d[0], f0, acc[n][0]);
-            acc[n][1] = fmaf(d[1], f1, acc[n][1]);
-            acc[n][2] = fmaf(d[2], f0, acc[n][2]);
-            acc[n][3] = fmaf(d[3], f1, acc[n][3]);
-        }
+        uint4 b0 = make_uint4(0, 0, 0, 0), b1 = b0;
+        if (there && c < p.out) b0 = __ldg(reinterpret_cast<const uint4 *>(y + c));
+        if (there && c + 64 < p.out) b1 = __ldg(reinterpret_cast<const uint4 *>(y + c + 64));
+        float d[4] = {0.f, 0.f, 0.f, 0.f};
+        mma_e4m3(d, a0.x, a1.x, a0.y, a1.y, b0.x, b0.y);
+        mma_e4m3(d, a0.z, a1.z, a0.w, a1.w, b0.z, b0.w);
+        mma_e4m3(d, a2.x, a3.x, a2.y, a3.y, b1.x, b1.y);
+        mma_e4m3(d, a2.z, a3.z, a2.w, a3.w, b1.z, b1.w);
+        const int s0 = 2 * t;
+        const float f0 = s0 < p.S ? sw * __ldg(p.ys + int64_t(s0) * p.nblk + kb) : 0.f;
+        const float f1 = s0 + 1 < p.S ? sw * __ldg(p.ys + int64_t(s0 + 1) * p.nblk + kb) : 0.f;
+        acc[0] = fmaf(d[0], f0, acc[0]);
+        acc[1] = fmaf(d[1], f1, acc[1]);
+        acc[2] = fmaf(d[2], f0, acc[2]);
+        acc[3] = fmaf(d[3], f1, acc[3]);
     }
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        part[warp][g][n * 8 + 2 * t] = acc[n][0];
-        part[warp][g][n * 8 + 2 * t + 1] = acc[n][1];
-        part[warp][g + 8][n * 8 + 2 * t] = acc[n][2];
-        part[warp][g + 8][n * 8 + 2 * t + 1] = acc[n][3];
-    }
+    part[warp][g][2 * t] = acc[0];
+    part[warp][g][2 * t + 1] = acc[1];
+    part[warp][g + 8][2 * t] = acc[2];
+    part[warp][g + 8][2 * t + 1] = acc[3];
     __syncthreads();
-    for (int e = threadIdx.x; e < 16 * 8 * NT; e += kRowWarps * 32) {
-        const int r = e & 15, s = e >> 4;                     // consecutive threads: consecutive columns of dX
-        float y = 0.f;
+    const int r = threadIdx.x & 15, s = threadIdx.x >> 4;      // consecutive threads: consecutive columns of dX
+    if (s < kFewRows) {
+        float sum = 0.f;
 #pragma unroll
-        for (int w = 0; w < kRowWarps; ++w) y += part[w][r][s];
-        mine[r][s] = y;
+        for (int w = 0; w < kRowWarps; ++w) sum += part[w][r][s];
+        mine[r][s] = sum;
     }
     if (size > 1) cluster_sync();
     else __syncthreads();
-    if (rank == 0) {
-        for (int e = threadIdx.x; e < 16 * 8 * NT; e += kRowWarps * 32) {
-            const int r = e & 15, s = e >> 4;
-            float y = mine[r][s];
-            for (uint32_t c = 1; c < size; ++c) {
-                float x;
-                asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(cluster_addr(&mine[r][s], c)));
-                y += x;
-            }
-            if (s < p.S && i0 + r < p.in) {
-                T *o = static_cast<T *>(p.dX) + int64_t(s) * p.in + i0 + r;
-                store_float(o, p.add ? y + load_float(o) : y);
-            }
+    if (rank == 0 && s < p.S && i0 + r < p.in) {
+        float sum = mine[r][s];
+        for (uint32_t c = 1; c < size; ++c) {
+            float x;
+            asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(cluster_addr(&mine[r][s], c)));
+            sum += x;
         }
+        T *o = static_cast<T *>(p.dX) + int64_t(s) * p.in + i0 + r;
+        store_float(o, p.add ? sum + load_float(o) : sum);
     }
     if (size > 1) cluster_sync();                             // no CTA leaves while its sums are read
 }
 
-template <typename T, int NT>
+template <typename T>
 int rows_launch(const RowsParams &p, cudaStream_t st) {
     // A CTA takes 16 rows of W; clusters of up to eight share their columns until there are four CTAs an SM, each
     // warp having a block of 128 columns at least.
@@ -229,7 +215,7 @@ int rows_launch(const RowsParams &p, cudaStream_t st) {
     attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    TLB_CUDA(cudaLaunchKernelEx(&cfg, linear_fp8_rows_kernel<T, NT>, p));
+    TLB_CUDA(cudaLaunchKernelEx(&cfg, linear_fp8_rows_kernel<T>, p));
     return check_launch("linear_fp8_rows");
 }
 
@@ -710,7 +696,7 @@ int run(const uint8_t *W, const float *w_scales, const uint8_t *dY, const float 
     const int KB = int(ceil_div(out, kFp8Block));
     if (S <= kFewRows) {
         const RowsParams p{W, dY, w_scales, dy_scales, ld, ld, int(S), int(out), int(in), KB, add ? 1 : 0, dX};
-        return S <= 8 ? rows_launch<T, 1>(p, st) : S <= 16 ? rows_launch<T, 2>(p, st) : rows_launch<T, 4>(p, st);
+        return rows_launch<T>(p, st);
     }
     TcParams p;
     memset(&p, 0, sizeof(p));
