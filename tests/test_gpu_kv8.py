@@ -321,6 +321,19 @@ def test_weights_of_very_different_size(lib):
     compare("d_v", d_v, [back[2]], False, rel=rel)
 
 
+@pytest.mark.parametrize("power", [-110, 110, 118])
+def test_values_of_extreme_scales(lib, power):
+    """Values whose scales are near the ends of float32: results are those of ordinary ones times the power."""
+    import torch
+    cache, q, g, pages, lens, longest, K, V = problem(lib, [150, 20], 8, 2, 64, 16, seed=11)
+    ctx, lse = lib.kv8_attn_forward(cache, q, pages, 16, lens, longest)
+    cache.tensors[3].mul_(2.0 ** power)
+    far, lse2 = lib.kv8_attn_forward(cache, q, pages, 16, lens, longest)
+    assert torch.equal(lse, lse2) and torch.all(far.isfinite())
+    # products with a power of two are exact; sums are held to the same number of bits at any of them
+    check("ctx", host(far * 2.0 ** -power), host(ctx), rel_l2=2 * F32_REL_L2, max_abs=None)
+
+
 def test_only_the_status_block_is_cleared(lib):
     import torch
     cache, q, g, pages, lens, longest, K, V = problem(lib, [900, 33, 0], 8, 2, 128, 16)

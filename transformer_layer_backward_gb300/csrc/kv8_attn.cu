@@ -80,7 +80,7 @@ __device__ __forceinline__ void halves(float x, float y, uint32_t &hi, uint32_t 
     lo = *reinterpret_cast<const uint32_t *>(&l);
 }
 
-// 2^e, -149 <= e <= 127 (2^128, of a row whose weights are not finite, is infinite)
+// 2^e, -149 <= e <= 127
 __device__ __forceinline__ float pow2(int e) { return e >= -126 ? __uint_as_float(uint32_t(e + 127) << 23) : __uint_as_float(1u << (e + 149)); }
 
 struct AttnParams {
@@ -391,8 +391,9 @@ __global__ void __launch_bounds__(kWarps * 32, HD <= 128 ? 4 : 2) kv8_attn_kerne
         uint32_t top = max(max(magnitude(x[0]), magnitude(x[1])), max(magnitude(x[2]), magnitude(x[3])));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-        // with room for weights of eight times the size, so that the sums are seldom turned to a new power
-        const int grown = int(top >> 23) - 127 > ex ? int(top >> 23) - 124 : ex;
+        // with room for weights of eight times the size, so that the sums are seldom turned to a new power (2^127 holds
+        // every float; of weights that are not finite the sums are NaN whatever it is)
+        const int grown = int(top >> 23) - 127 > ex ? min(int(top >> 23) - 124, 127) : ex;
         if (__any_sync(0xffffffffu, grown != ex || alpha != 1.f)) {
             alpha *= pow2(max(ex - grown, -149));
 #pragma unroll
