@@ -554,13 +554,17 @@ Plan plan_of(int64_t M, int64_t N, int64_t KB) {
     const int rest = int(tiles % P);
     if (rest == 0) return pl;
     // The tiles of the last wave: whole on `rest` pairs, or shared by more along K, evenly (a multiple of `rest`) or
-    // by all P.  In k blocks of a pair: a part of a tile costs kPart more where it is written, and kJoin where it is read.
-    constexpr double kPart = 6.0, kJoin = 0.2;
+    // by all P.  In k blocks of a pair: a part of a tile costs kPart more where it is written, and kJoin (for 256 rows)
+    // where it is read.  Fitted to 40 tiles of 76 k blocks (whole 42 us, shared by 76 pairs 55), 20 of 32 beyond a wave
+    // (whole 41 us, by 60 pairs 45), four of 20 (29, by 20 pairs 27) and of 76 (76 pairs 60 us, 24 to 44 pairs 56).
+    constexpr double kPart = 6.0, kJoin = 0.35;
+    const double join = kJoin * double(std::min<int64_t>(M, kTM)) / kTM;
     double best = double(KB);
     auto consider = [&](int pairs) {
         if (pairs <= rest || pairs > P) return;
         const int64_t most = ceil_div(int64_t(rest) * KB, pairs);
-        const double cost = double(most) + kPart * (pairs % rest == 0 ? 1 : 2) + kJoin * pairs;
+        const int parts = pairs % rest == 0 ? 1 : 2;          // of a pair
+        const double cost = double(most) + parts * (kPart + join * pairs);
         if (most >= 1 && cost < best) {
             best = cost;
             pl.sk_tiles = rest;
