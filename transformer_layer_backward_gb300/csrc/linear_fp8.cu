@@ -15,8 +15,8 @@
 // are joined in a fixed order by a second kernel.
 // What bounds it: an accumulator is in use from its MMA's start until both CTAs have read it out, about 1700 cycles
 // (MMA 260 to 400, commit to the readers 400, reading 350, arrival to the next MMA 500), and two k blocks fill the
-// tensor memory: 830 cycles a k block where the MMAs need 512.  2048 x 9728 x 2560: 56 us (1.8 PFLOP/s), of which 33 us
-// are the 76 k blocks of the whole tiles, 5 us the start and first blocks, 5 us the results' way out, 7 us the shared tiles' join.
+// tensor memory: 830 cycles a k block where the MMAs need 512.  2048 x 9728 x 2560: 54.5 us (1.87 PFLOP/s), of which 33 us
+// are the 76 k blocks of the whole tiles, 5 us the start and first blocks, 5 us the results' way out, 6 us the shared tiles' join.
 // Measured on the way there, same sizes: MMAs issued by a lane on its own 108 us and a release arrival of cluster scope
 // (it waits for the scales' loads) on top; one issuer and two accumulators of 256 columns 57 us; eight warps for the
 // sums with 128 columns each 62 to 71 us; waits that spin 71 us.
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(128) linear_fp8_join_kernel(const __grid_const
     for (int r = int(blockIdx.y) * 2 + (threadIdx.x >> 6); r < min(kTM, p.M - m); r += int(gridDim.y) * 2) {
         const int h = r / kHalf, lr = r % kHalf;
         float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
-        constexpr int kAhead = 20;                            // loads in flight
+        constexpr int kAhead = 8;                             // loads in flight (20 took registers: 512 x 9728 x 2560 32 us, 8: 26)
         for (int c = c0; c <= c1; c += kAhead) {
             float4 v[kAhead];
 #pragma unroll
@@ -555,9 +555,10 @@ Plan plan_of(int64_t M, int64_t N, int64_t KB) {
     if (rest == 0) return pl;
     // The tiles of the last wave: whole on `rest` pairs, or shared by more along K, evenly (a multiple of `rest`) or
     // by all P.  In k blocks of a pair: a part of a tile costs kPart more where it is written, and kJoin (for 256 rows)
-    // where it is read.  Fitted to 40 tiles of 76 k blocks (whole 42 us, shared by 76 pairs 55), 20 of 32 beyond a wave
-    // (whole 41 us, by 60 pairs 45), four of 20 (29, by 20 pairs 27) and of 76 (76 pairs 60 us, 24 to 44 pairs 56).
-    constexpr double kPart = 6.0, kJoin = 0.35;
+    // where it is read.  Fitted to 1000 x 9728 x 2560 (40 tiles of 76 k blocks: whole 42 us, by 76 pairs 55),
+    // 1500 x 4096 x 4096 (20 of 32 beyond a wave: whole 41, by 60 pairs 39), 2048 x 2560 x 2560 (four of 20: whole 29, by 20
+    // and more 25) and 2048 x 9728 x 2560 (four of 76: by 76 pairs 60, by 24 to 44 55).
+    constexpr double kPart = 6.0, kJoin = 0.22;
     const double join = kJoin * double(std::min<int64_t>(M, kTM)) / kTM;
     double best = double(KB);
     auto consider = [&](int pairs) {
