@@ -92,6 +92,24 @@ def test_cache(lib):
     assert 256 <= size(cache()) <= size(cache(), grad=1)
 
 
+def test_pointers_off_their_elements(lib):
+    from transformer_layer_backward_gb300 import _abi as A
+    off, off4 = C.c_void_p(258), C.c_void_p(260)
+    c = C.byref(A.Kv8(256, 256, 256, 256, 64, 2, 64))
+    bad = C.byref(A.Kv8(256, 256, 258, 256, 64, 2, 64))
+    for k, v, slots in ((off, p, p), (p, off, p), (p, p, off4)):
+        assert lib.tlb_kv8_write(c, A.W_F32, k, 128, 64, v, 128, 64, slots, 3, None) == A.TLB_EINVAL
+        assert lib.tlb_kv8_read(c, slots, 3, A.W_F32, k, v, 128, 64, None) == A.TLB_EINVAL
+    assert lib.tlb_kv8_write(c, A.W_BF16, C.c_void_p(257), 128, 64, p, 128, 64, p, 3, None) == A.TLB_EINVAL
+    assert lib.tlb_kv8_write(bad, A.W_F32, p, 128, 64, p, 128, 64, p, 3, None) == A.TLB_EINVAL
+    for pages, lengths, lse in ((off, p, p), (p, off, p), (p, p, off)):
+        assert lib.tlb_kv8_attn_forward(c, pages, 4, 16, lengths, 2, 64, 4, 0.1, A.W_F32, p, p, lse, p, 1 << 40, None) == A.TLB_EINVAL
+        assert lib.tlb_kv8_attn_backward(c, pages, 4, 16, lengths, 2, 64, 4, 0.1, A.W_F32, p, lse, p, p, p, p, p, 1 << 40,
+                                         None) == A.TLB_EINVAL
+    for ws, ys in ((off, p), (p, off)):
+        assert lib.tlb_linear_fp8_backward(p, ws, p, ys, 4, 32, 48, A.W_F32, p, 0, p, 1 << 40, None) == A.TLB_EINVAL
+
+
 def test_binding_refuses(lib):
     """Wrong types, shapes and places are refused before the library is called."""
     import torch

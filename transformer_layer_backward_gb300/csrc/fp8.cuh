@@ -10,6 +10,9 @@ namespace tlb {
 
 constexpr int kFp8Block = 128;      // columns that share a scale
 
+// Whether a pointer is aligned to elements of this many bytes.
+inline bool aligned_to(const void *p, size_t bytes) { return reinterpret_cast<uintptr_t>(p) % bytes == 0; }
+
 // Magnitude of x as an integer that orders as the floats do, NaN above infinity: the largest of a
 // block is an integer maximum, which keeps a NaN (a float maximum drops it).
 __device__ __forceinline__ uint32_t magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }

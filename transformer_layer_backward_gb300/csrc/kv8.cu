@@ -143,6 +143,7 @@ int kv8_check(const tlb_kv8 *c, const char *what) {
     if (c->n_slots == 0) return TLB_OK;
     TLB_REQUIRE(c->k && c->v && c->k_scale && c->v_scale, TLB_EINVAL, "%s: null pointer in the cache", what);
     TLB_REQUIRE(aligned16(c->k) && aligned16(c->v), TLB_EINVAL, "%s: the cache's k and v must be 16-byte aligned", what);
+    TLB_REQUIRE(aligned_to(c->k_scale, 4) && aligned_to(c->v_scale, 4), TLB_EINVAL, "%s: the cache's scales must be aligned", what);
     return TLB_OK;
 }
 
@@ -162,6 +163,9 @@ int tlb_kv8_write(const tlb_kv8 *cache, int32_t type, const void *k, int64_t k_s
     TLB_REQUIRE(rows <= (int64_t(1) << 32) / cache->n_kv_heads, TLB_EUNSUPPORTED, "kv8_write: more than 2^32 rows of heads");
     if (rows == 0 || cache->n_slots == 0) return TLB_OK;
     TLB_REQUIRE(k && v && slots, TLB_EINVAL, "kv8_write: null pointer");
+    const size_t wide = type == TLB_W_F32 ? 4 : 2;
+    TLB_REQUIRE(aligned_to(k, wide) && aligned_to(v, wide) && aligned_to(slots, 8), TLB_EINVAL,
+                "kv8_write: k, v and slots must be aligned to their elements");
     if (type == TLB_W_F32)
         return write_launch(*cache, static_cast<const float *>(k), k_stride_row, k_stride_head, static_cast<const float *>(v),
                             v_stride_row, v_stride_head, slots, rows, as_stream(stream));
@@ -178,6 +182,9 @@ int tlb_kv8_read(const tlb_kv8 *cache, const int64_t *slots, int64_t rows, int32
     TLB_REQUIRE(rows <= (int64_t(1) << 32) / cache->n_kv_heads, TLB_EUNSUPPORTED, "kv8_read: more than 2^32 rows of heads");
     if (rows == 0) return TLB_OK;
     TLB_REQUIRE(k && v && slots, TLB_EINVAL, "kv8_read: null pointer");
+    const size_t wide = type == TLB_W_F32 ? 4 : 2;
+    TLB_REQUIRE(aligned_to(k, wide) && aligned_to(v, wide) && aligned_to(slots, 8), TLB_EINVAL,
+                "kv8_read: k, v and slots must be aligned to their elements");
     if (type == TLB_W_F32)
         return read_launch(*cache, slots, rows, static_cast<float *>(k), static_cast<float *>(v), stride_row, stride_head,
                            as_stream(stream));

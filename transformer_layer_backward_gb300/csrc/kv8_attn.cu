@@ -738,6 +738,7 @@ int check_call(const char *what, const tlb_kv8 *cache, const int32_t *pages, int
     if (n_seq == 0) return TLB_OK;
     TLB_REQUIRE(lengths && q && (pages || max_pages == 0), TLB_EINVAL, "%s: null pointer", what);
     TLB_REQUIRE(aligned16(q), TLB_EINVAL, "%s: q must be 16-byte aligned", what);
+    TLB_REQUIRE(aligned_to(pages, 4) && aligned_to(lengths, 4), TLB_EINVAL, "%s: pages and lengths must be aligned", what);
     const size_t need = ws_bytes_of(cache, n_seq, n_heads, max_len, grad);
     TLB_REQUIRE(ws != nullptr && ws_bytes >= need, TLB_EINVAL, "%s: workspace of %zu bytes is smaller than the %zu bytes needed",
                 what, ws_bytes, need);
@@ -772,7 +773,7 @@ int tlb_kv8_attn_forward(const tlb_kv8 *cache, const int32_t *pages, int64_t max
                        ws_bytes, false, pg));
     if (n_seq == 0) return TLB_OK;
     TLB_REQUIRE(ctx && lse, TLB_EINVAL, "kv8_attn_forward: null pointer");
-    TLB_REQUIRE(aligned16(ctx), TLB_EINVAL, "kv8_attn_forward: ctx must be 16-byte aligned");
+    TLB_REQUIRE(aligned16(ctx) && aligned_to(lse, 4), TLB_EINVAL, "kv8_attn_forward: ctx must be 16-byte aligned, lse to its elements");
     AttnParams p = params_of(*cache, pg, n_seq, n_heads, false, scale, q, ws);
     p.out = ctx;
     p.out_lse = lse;
@@ -789,8 +790,8 @@ int tlb_kv8_attn_backward(const tlb_kv8 *cache, const int32_t *pages, int64_t ma
                        ws_bytes, true, pg));
     if (n_seq == 0) return TLB_OK;
     TLB_REQUIRE(lse && d_ctx && d_q && d_k && d_v, TLB_EINVAL, "kv8_attn_backward: null pointer");
-    TLB_REQUIRE(aligned16(d_ctx) && aligned16(d_q) && aligned16(d_k) && aligned16(d_v), TLB_EINVAL,
-                "kv8_attn_backward: d_ctx, d_q, d_k and d_v must be 16-byte aligned");
+    TLB_REQUIRE(aligned16(d_ctx) && aligned16(d_q) && aligned16(d_k) && aligned16(d_v) && aligned_to(lse, 4), TLB_EINVAL,
+                "kv8_attn_backward: d_ctx, d_q, d_k and d_v must be 16-byte aligned, lse to its elements");
     AttnParams p = params_of(*cache, pg, n_seq, n_heads, true, scale, q, ws);
     p.lse = lse;
     p.d_ctx = d_ctx;

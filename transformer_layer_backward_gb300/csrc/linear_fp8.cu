@@ -761,6 +761,7 @@ int tlb_linear_fp8_backward(const uint8_t *W, const float *w_scales, const uint8
     TLB_REQUIRE(dX && (out_dim == 0 || (W && w_scales && dY && dy_scales)), TLB_EINVAL, "linear_fp8_backward: null pointer");
     TLB_REQUIRE(aligned16(W) && aligned16(dY) && aligned16(dX), TLB_EINVAL,
                 "linear_fp8_backward: W, dY and dX must be 16-byte aligned");
+    TLB_REQUIRE(aligned_to(w_scales, 4) && aligned_to(dy_scales, 4), TLB_EINVAL, "linear_fp8_backward: the scales must be aligned");
     const size_t need = tlb_linear_fp8_workspace_bytes(S, out_dim, in_dim);
     TLB_REQUIRE(ws != nullptr && ws_bytes >= need, TLB_EINVAL,
                 "linear_fp8_backward: workspace of %zu bytes is smaller than the %zu bytes needed", ws_bytes, need);
