@@ -16,7 +16,7 @@
 // Warps, then the CTAs that share a unit (a second kernel), are joined in a fixed order.
 // Of the time of a step (600 instructions for 16 keys in the gradient, a quarter of them conversions to halves)
 // half is latency: 16 warps an SM, since a warp's sums take 64 registers a thread.  131072 keys of 8 KV heads and 32 query
-// heads of 128: gradient 73 us (277 MB, 3.8 TB/s); a batch of 32 sequences up to 16384 keys: forward 38 us (124 MB).
+// heads of 128: gradient 73 us (277 MB, 3.8 TB/s); a batch of 32 sequences up to 16384 keys: forward 34.5 us (124 MB).
 // Slower: 32 keys a step (82 us: three CTAs an SM), the sums of the step before beside a step's logits (81 us).
 #include <cmath>
 
@@ -104,10 +104,11 @@ struct AttnParams {
 // The work is laid out in a line: sequence by sequence, unit by unit (a KV head and a tile of its query heads), a unit
 // of S steps of 16 keys weighing kFixed + S, since its start and its end cost as much as some steps.  CTA c of n takes
 // [total c / n, total (c + 1) / n) of that line: as many CTAs as are on the GPU at a time, each with the same
-// weight whatever the lengths, which only the device knows.  The first kFixed of a unit are no steps.
+// weight whatever the lengths, which only the device knows.  The first kFixed of a unit are no steps (a batch of 32
+// sequences up to 16384 keys: kFixed 6 50 us, 12 38, 20 34.5, 30 35.7).
 // kLeast: the weight that is worth a CTA (a step of each warp).  kMostParts: CTAs a unit, on average, since one CTA of
 // the join reads all its parts (65536 keys of one KV head: 608 parts 41 us, 128 19 us).
-constexpr int kFixed = 12, kLeast = 4, kMostParts = 128;
+constexpr int kFixed = 20, kLeast = 4, kMostParts = 128;
 
 __device__ __forceinline__ int64_t steps_of(int len) { return (len + kStep - 1) / kStep; }
 __device__ __forceinline__ int cta_count(int64_t total, int most) { return int(max(int64_t(1), min(int64_t(most), total / kLeast))); }
