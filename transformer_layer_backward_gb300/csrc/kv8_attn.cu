@@ -9,8 +9,9 @@
 //     and g + 8 of the operand, which meet in one thread).  The 16 bytes of a row that a lane reads serve as
 //     operands as they are, the query's columns being ordered to match;
 //   - the sums over keys (p v; p dp k and p k) take the weights x in the same two halves, scaled by a
-//     power of two of each row that grows with the largest |x| so far, and the rows' bytes transposed
-//     by byte permutes: 23 bits of each weight, 34 below the largest at least.
+//     power of two of each row that follows the largest |x| so far (as it counts now: it grows with |x| and falls
+//     when the forward's reference rises), and the rows' bytes transposed by byte permutes: 23 bits of each weight,
+//     34 below the largest at least.
 // The gradient uses d_q = scale (sum p dp k - (sum p dp)(sum p k)), so that one pass does.  Rows of the gradient's
 // tile: four heads' s (and p dp) in rows 0..3, their dp (and p) in rows 4..7; of the forward's: eight heads.
 // Warps, then the CTAs that share a unit (a second kernel), are joined in a fixed order.
@@ -353,18 +354,21 @@ __global__ void __launch_bounds__(kWarps * 32, HD <= 128 ? 4 : 2) kv8_attn_kerne
             x[e] = raw * scales[is_dp ? 16 + key : key];
         }
         auto there = [&](int e) { return (mask >> ((e >> 1) * 8 + 2 * t + (e & 1))) & 1u; };
-        float alpha = 1.f;
+        int fall = 0;                    // powers of two that the reference rose by, and the sums fell by
         if (!GRAD) {
             float top = m;
 #pragma unroll
             for (int e = 0; e < 4; ++e) top = there(e) ? fmaxf(top, x[e]) : top;
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            // the reference follows the largest logit when that is 2^8 beyond it: until then weights are up to 2^8
-            if (top > m + 8.f || m == -INFINITY) {
-                alpha = top == -INFINITY ? 1.f : ex2(m - top);
-                m = top;
-                l *= alpha;
+            // the reference, a whole number, follows the largest logit when that is 2^8 beyond it: until then weights are
+            // up to 2^8.  The sums' power falls by as much as the reference rises: weights of now are held to the
+            // bits of what counts now, however large the values of keys were that have lost their weight
+            if (top > m + 8.f || (m == -INFINITY && top > m)) {
+                const float to = floorf(top);
+                l *= ex2(m - to);
+                fall = int(fminf(to - m, 4096.f));
+                m = to;
             }
             const float ref = m == -INFINITY ? 0.f : m;
 #pragma unroll
@@ -394,14 +398,15 @@ __global__ void __launch_bounds__(kWarps * 32, HD <= 128 ? 4 : 2) kv8_attn_kerne
         top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
         // with room for weights of eight times the size, so that the sums are seldom turned to a new power (2^127 holds
         // every float; of weights that are not finite the sums are NaN whatever it is)
-        const int grown = int(top >> 23) - 127 > ex ? min(int(top >> 23) - 124, 127) : ex;
-        if (__any_sync(0xffffffffu, grown != ex || alpha != 1.f)) {
-            alpha *= pow2(max(ex - grown, -149));
+        const int low = max(ex - fall, -120), grown = int(top >> 23) - 127 > low ? min(int(top >> 23) - 124, 127) : low;
+        const int turn = ex - fall - grown;
+        ex = grown;
+        if (__any_sync(0xffffffffu, turn != 0)) {
+            const float alpha = pow2(max(turn, -149));
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 acc[n][0] *= alpha; acc[n][1] *= alpha; acc[n][2] *= alpha; acc[n][3] *= alpha;
             }
-            ex = grown;
         }
         const float down = pow2(-ex);
         uint4 a;
