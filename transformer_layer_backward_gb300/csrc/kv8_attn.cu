@@ -321,11 +321,13 @@ __global__ void __launch_bounds__(kWarps * 32, HD <= 128 ? 4 : 2) kv8_attn_kerne
         const uint32_t mask = *reinterpret_cast<const uint32_t *>(st + 2 * kStep * HD + 128);
 
         // ---- logits (and dp): columns are keys
+        // (the gradient's rows of q and of d_ctx have sums of their own: 0 times a value that is NaN is NaN, and the
+        // logits do not depend on the values)
         float cf[2][4], part[2][2][4] = {};                    // [chain][tile of 8 keys]: two chains of products at least
 #pragma unroll
-        for (int w = 0; w < (GRAD ? 2 : 1); ++w)
+        for (int c = 0; c < HD / 64; ++c)
 #pragma unroll
-            for (int c = 0; c < HD / 64; ++c) {
+            for (int w = 0; w < (GRAD ? 2 : 1); ++w) {
                 uint4 kq[2];
 #pragma unroll
                 for (int nt = 0; nt < 2; ++nt)
@@ -337,14 +339,15 @@ __global__ void __launch_bounds__(kWarps * 32, HD <= 128 ? 4 : 2) kv8_attn_kerne
                     for (int nt = 0; nt < 2; ++nt) {
                         uint32_t b0, b1;
                         e4m3x4_to_half2(u == 0 ? kq[nt].x : u == 1 ? kq[nt].y : u == 2 ? kq[nt].z : kq[nt].w, b0, b1);
-                        mma_f16(part[u & 1][nt], a, b0, b1);
+                        mma_f16(part[GRAD ? w : u & 1][nt], a, b0, b1);
                     }
                 }
             }
 #pragma unroll
         for (int nt = 0; nt < 2; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) cf[nt][e] = part[0][nt][e] + part[1][nt][e];
+            for (int e = 0; e < 4; ++e)
+                cf[nt][e] = GRAD ? (is_dp ? part[1][nt][e] : part[0][nt][e]) : part[0][nt][e] + part[1][nt][e];
         // ---- the weights x of this lane's row for keys 2 t, 2 t + 1, 2 t + 8, 2 t + 9
         float x[4];
 #pragma unroll
