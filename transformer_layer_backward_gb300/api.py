@@ -322,6 +322,14 @@ def _raw_stream(stream, device):
     return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
+def _int32(n, name):
+    """n for a 32-bit argument, of which ctypes would pass the low 32 bits."""
+    n = int(n)
+    if not -1 << 31 <= n < 1 << 31:
+        raise ValueError("%s does not fit 32 bits: %d" % (name, n))
+    return n
+
+
 def _at(t, shape, dtype, device, name):
     """Address of a contiguous tensor of this shape (None: any), type and device."""
     if t.dtype is dtype and t.is_contiguous() and t.device == device and (shape is None or t.shape == shape) and t.is_cuda:
@@ -354,7 +362,8 @@ def fp8_quantize(x, block_rows=1, q=None, scales=None, stream=None):
     if x.dim() != 2:
         raise ValueError("x [rows, cols] expected, got %s" % (tuple(x.shape),))
     rows, cols = x.shape
-    blocks = (-(-rows // max(int(block_rows), 1)), -(-cols // _FP8_BLOCK))
+    block_rows = _int32(block_rows, "block_rows")
+    blocks = (-(-rows // max(block_rows, 1)), -(-cols // _FP8_BLOCK))
     with _queued(x, stream):
         at_x = _at(x, None, x.dtype, x.device, "x")
         if q is None:
@@ -365,7 +374,7 @@ def fp8_quantize(x, block_rows=1, q=None, scales=None, stream=None):
             scales = torch.empty(blocks, dtype=torch.float32, device=x.device)
         else:
             _at(scales, blocks, torch.float32, x.device, "scales")
-        A.call("tlb_fp8_quantize", code, at_x, rows, cols, int(block_rows), q.data_ptr(), scales.data_ptr(),
+        A.call("tlb_fp8_quantize", code, at_x, rows, cols, block_rows, q.data_ptr(), scales.data_ptr(),
                _raw_stream(stream, x.device))
     return q, scales
 
@@ -472,14 +481,15 @@ def kv8_attn_workspace(cache, n_seq, n_heads, max_len, grad=False):
     return _status_cleared(int(n), cache.device)
 
 
-def _kv8_over(cache, q, pages, lengths):
+def _kv8_over(cache, q, pages, page, lengths):
+    page = _int32(page, "page")
     if q.dim() != 3 or q.shape[2] != cache.head_dim:
         raise ValueError("q [n_seq, n_heads, %d] expected, got %s" % (cache.head_dim, tuple(q.shape)))
     n_seq, n_heads = q.shape[:2]
     if pages.dim() != 2 or pages.shape[0] != n_seq:
         raise ValueError("pages [%d, max_pages] expected, got %s" % (n_seq, tuple(pages.shape)))
     return (n_seq, n_heads, _xent_code(q.dtype, "q"), _at(q, None, q.dtype, cache.device, "q"),
-            _at(pages, None, torch.int32, cache.device, "pages"), pages.shape[1],
+            _at(pages, None, torch.int32, cache.device, "pages"), pages.shape[1], page,
             _at(lengths, (n_seq,), torch.int32, cache.device, "lengths"))
 
 
@@ -488,7 +498,7 @@ def kv8_attn_forward(cache, q, pages, page, lengths, max_len, scale=None, ctx=No
     Key j < lengths[b] (int32 [n_seq]) of sequence b is in slot pages[b, j // page] * page + j % page (pages int32
     [n_seq, max_pages]); max_len is at least the longest length; scale 1 / sqrt(head_dim) unless given.
     Without ws the call makes one of its own, which workspace_status() without one looks after."""
-    n_seq, n_heads, code, at_q, at_pages, max_pages, at_lengths = _kv8_over(cache, q, pages, lengths)
+    n_seq, n_heads, code, at_q, at_pages, max_pages, page, at_lengths = _kv8_over(cache, q, pages, page, lengths)
     dev = cache.device
     with _queued(q, stream):
         if ctx is None:
@@ -502,7 +512,7 @@ def kv8_attn_forward(cache, q, pages, page, lengths, max_len, scale=None, ctx=No
         own = ws is None
         if own:
             ws = kv8_attn_workspace(cache, n_seq, n_heads, max_len)
-        A.call("tlb_kv8_attn_forward", cache, at_pages, max_pages, int(page), at_lengths, n_seq, int(max_len), n_heads,
+        A.call("tlb_kv8_attn_forward", cache, at_pages, max_pages, page, at_lengths, n_seq, int(max_len), n_heads,
                1.0 / math.sqrt(cache.head_dim) if scale is None else float(scale), code, at_q,
                ctx.data_ptr(), lse.data_ptr(), _at(ws, None, torch.uint8, dev, "ws"), ws.numel(), _raw_stream(stream, dev))
         if own:
@@ -514,7 +524,7 @@ def kv8_attn_backward(cache, q, pages, page, lengths, max_len, lse, d_ctx, scale
                       stream=None):
     """Gradient of kv8_attn_forward() for d_ctx: (d_q, d_k, d_v) in q's dtype, d_k and d_v [n_seq, n_kv_heads, head_dim]
     of each sequence's newest key and value.  lse as kv8_attn_forward returned it; ws as there."""
-    n_seq, n_heads, code, at_q, at_pages, max_pages, at_lengths = _kv8_over(cache, q, pages, lengths)
+    n_seq, n_heads, code, at_q, at_pages, max_pages, page, at_lengths = _kv8_over(cache, q, pages, page, lengths)
     dev, newest = cache.device, (n_seq, cache.n_kv_heads, cache.head_dim)
     with _queued(q, stream):
         if d_q is None:
@@ -532,7 +542,7 @@ def kv8_attn_backward(cache, q, pages, page, lengths, max_len, lse, d_ctx, scale
         own = ws is None
         if own:
             ws = kv8_attn_workspace(cache, n_seq, n_heads, max_len, grad=True)
-        A.call("tlb_kv8_attn_backward", cache, at_pages, max_pages, int(page), at_lengths, n_seq, int(max_len), n_heads,
+        A.call("tlb_kv8_attn_backward", cache, at_pages, max_pages, page, at_lengths, n_seq, int(max_len), n_heads,
                1.0 / math.sqrt(cache.head_dim) if scale is None else float(scale), code, at_q,
                _at(lse, (n_seq, n_heads), torch.float32, dev, "lse"), _at(d_ctx, q.shape, q.dtype, dev, "d_ctx"),
                d_q.data_ptr(), d_k.data_ptr(), d_v.data_ptr(), _at(ws, None, torch.uint8, dev, "ws"), ws.numel(), _raw_stream(stream, dev))
