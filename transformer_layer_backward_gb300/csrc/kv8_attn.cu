@@ -754,6 +754,7 @@ int check_call(const char *what, const tlb_kv8 *cache, const int32_t *pages, int
     TLB_REQUIRE((reinterpret_cast<uintptr_t>(ws) & 255) == 0, TLB_EINVAL, "%s: workspace must be 256-byte aligned", what);
     int64_t most = max_len;
     if (max_pages < (int64_t(1) << 31)) most = most < max_pages * page ? most : max_pages * page;
+    if (cache->n_slots == 0) most = 0;                        // no key is there, and no address is made of the null pointers
     int shift = -1;
     if ((page & (page - 1)) == 0)
         for (shift = 0; (1 << shift) < page;) ++shift;
