@@ -29,8 +29,6 @@ def _queued(t, stream=None):
     queued on, to which what is allocated meanwhile then belongs."""
     if not t.is_cuda:
         return _NO_GUARD
-    if stream is None and t.device.index == torch._C._cuda_getDevice():
-        return _NO_GUARD
     if isinstance(stream, torch.cuda.Stream):
         if stream.device != t.device:
             raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, t.device))
