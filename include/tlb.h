@@ -363,14 +363,15 @@ int tlb_xent_backward(int32_t htype, const void *hidden, int32_t wtype, const vo
  * exponent bits, 3 mantissa bits, no infinity, largest value 448; one byte each) times a float32
  * scale of the block.  The calls that quantise choose the scale from the block's largest magnitude:
  * the smallest power of two 2^e, e >= -126, with max|x| <= 448 * 2^e; each value is x / 2^e rounded
- * once to e4m3 (nearest, ties to even; values below 2^-9 of the scale lose bits).  A block that holds
- * an infinity or a NaN gets the scale NaN and all its values are NaN.  The calls that read take any
- * float32 scale.  Float tensors are TLB_W_F32 or TLB_W_BF16 (`type`). */
+ * once to e4m3 (nearest, ties to even; values below 2^-6 of the scale lose bits, up to 2^-10 of it they
+ * become 0).  A block that holds an infinity or a NaN gets the scale NaN and all its values are NaN.
+ * The calls that read take any float32 scale.  Float tensors are TLB_W_F32 or TLB_W_BF16 (`type`). */
 
 /* x [rows, cols] in `type` to q [rows, cols] (e4m3) and scales [ceil(rows / block_rows),
  * ceil(cols / 128)]: blocks of block_rows x 128, where block_rows is 1 (activations and gradients:
  * a scale for 128 values of a row) or 128 (weights).  Blocks at the edges are smaller.  Any sizes;
- * rows or cols 0 is a no-op.  Any alignment goes; 16 bytes and cols % 8 == 0 are faster. */
+ * rows or cols 0 is a no-op.  x and scales are aligned to their elements, q starts anywhere; 16 bytes
+ * and cols % 8 == 0 are faster. */
 int tlb_fp8_quantize(int32_t type, const void *x, int64_t rows, int64_t cols, int32_t block_rows, uint8_t *q,
                      float *scales, void *stream);
 
@@ -430,8 +431,12 @@ int tlb_kv8_read(const tlb_kv8 *cache, const int64_t *slots, int64_t rows, int32
  * q, ctx, d_ctx, d_q [n_seq, n_heads, head_dim] and d_k, d_v [n_seq, n_kv_heads, head_dim] in `type`,
  * 16-byte aligned; lse [n_seq, n_heads] float32; pages [n_seq, max_pages] and lengths [n_seq] int32.
  * A sequence without a key (length <= 0) gives ctx 0, lse -infinity and gradients 0.  backward takes
- * the lse that forward gave.  All sums are float32; q, d_ctx and the weights of the sums
- * are taken apart into two halves that hold 22 bits or more of them.  Same inputs, same bits.
+ * the lse that forward gave; d_v does not depend on the values, not on one that is NaN either.  All sums
+ * are float32, in the forward before they are divided by the sum of the weights.  What the tensor cores
+ * multiply is taken apart into two 16-bit halves: q and d_ctx to 2^-23 of each value or 2^-51 of its row's
+ * largest, whichever is more; the weights of the sums (p times the scale of the value, in the gradient p or
+ * p dp times that of the key) to 2^-23 of each or 2^-34 of the largest that counts among the keys summed
+ * with it (as they stand to one another, whatever order they come in).  Same inputs, same bits.
  * The work goes by the lengths, which only the device reads: a captured call follows them.  max_len bounds
  * them (a longer one counts as max_len).  0 <= n_seq, max_len <= 2^30, n_heads <= 65535, n_seq n_heads <= 2^30,
  * n_slots < 2^31.

@@ -20,7 +20,7 @@ __device__ __forceinline__ void load_float8(const __nv_bfloat16 *p, float (&v)[8
 
 // Blocks of 1 x 128: a warp takes kRowBlocks blocks at a time, whose loads are all issued before the
 // first is used; a lane holds four columns of each.  Bound by memory: 5 (float32) or 3 bytes a value.
-// 2048 x 9728 float32: 17.7 us, 5.7 TB/s.
+// 2048 x 9728 float32: 17.7 us, 5.7 TB/s; 2048 x 9727 (an element at a time): 23.4 us.
 constexpr int kRowBlocks = 4;
 
 template <typename T, bool VEC>
@@ -72,7 +72,7 @@ __global__ void __launch_bounds__(256) quantize_rows_kernel(const T *__restrict_
 
 // The same with 16 lanes a block and eight columns a lane, for bf16 (16 bytes loaded a lane, 8 stored): a warp takes
 // kRowPairs pairs of blocks at a time.  The maximum is taken of the 16-bit magnitudes, two at a time.  4096 x 9728:
-// 21.5 us, 5.6 TB/s (four columns a lane, 8-byte loads: 61 us; the maximum of floats by shuffles: 29 us).
+// 20.8 us, 5.8 TB/s (four columns a lane, 8-byte loads: 61 us; the maximum of floats by shuffles: 29 us).
 constexpr int kRowPairs = 4;
 
 __global__ void __launch_bounds__(256, 4) quantize_rows8_kernel(const __nv_bfloat16 *__restrict__ x, int64_t cols, int64_t nblk,
@@ -114,7 +114,8 @@ __global__ void __launch_bounds__(256, 4) quantize_rows8_kernel(const __nv_bfloa
 }
 
 // Blocks of 128 x 128: a CTA of 512 threads holds one in registers, 32 values a thread, 16 lanes a row (16 bytes of bf16
-// loaded a lane and 8 stored).  2560 x 9728 bf16: 13.9 us, 5.4 TB/s; 256 threads with 8-byte loads took 49 us.
+// loaded a lane and 8 stored).  2560 x 9728 bf16: 13.9 us, 5.4 TB/s, float32 18.5 us, 6.7 TB/s; 256 threads with 8-byte
+// loads took 49 us (bf16).  2560 x 9727 bf16 (an element at a time): 42.6 us.
 constexpr int kTileThreads = 512, kTileRows = kFp8Block * 16 / kTileThreads;   // rows a thread
 
 template <typename T, bool VEC>

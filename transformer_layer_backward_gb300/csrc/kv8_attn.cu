@@ -1,6 +1,7 @@
 // Attention of single tokens over the 8-bit K/V cache, and its gradient.
 //
-// Bound by the read of the keys and values, once.  What a CTA (four warps) does for a run of one sequence's keys, one
+// Bound by the read of the keys and values (once for up to eight query heads a KV head, four in the gradient; a
+// larger group reads and multiplies them again for each tile of as many).  What a CTA (four warps) does for a run of one sequence's keys, one
 // KV head and a tile of the query heads that share it, 16 keys a warp at a time:
 //   - cp.async brings the keys', values' and scales' bytes to shared memory, a step ahead; keys that
 //     are not there come as zeros, so that nothing of what a free slot holds is met;
@@ -17,7 +18,8 @@
 // Warps, then the CTAs that share a unit (a second kernel), are joined in a fixed order.
 // Of the time of a step (600 instructions for 16 keys in the gradient, a quarter of them conversions to halves)
 // half is latency: 16 warps an SM, since a warp's sums take 64 registers a thread.  131072 keys of 8 KV heads and 32 query
-// heads of 128: gradient 73 us (277 MB, 3.8 TB/s); a batch of 32 sequences up to 16384 keys: forward 34.5 us (124 MB).
+// heads of 128: gradient 73.8 us (277 MB, 3.8 TB/s); a batch of 32 sequences up to 16384 keys: forward 34.6 us (116 MB,
+// 3.4 TB/s).  65536 keys of 8 KV heads: gradient of 32 heads 47 us, of 64 (two tiles) 75 us.
 // Slower: 32 keys a step (82 us: three CTAs an SM), the sums of the step before beside a step's logits (81 us).
 #include <cmath>
 
@@ -105,10 +107,15 @@ struct AttnParams {
 // The work is laid out in a line: sequence by sequence, unit by unit (a KV head and a tile of its query heads), a unit
 // of S steps of 16 keys weighing kFixed + S, since its start and its end cost as much as some steps.  CTA c of n takes
 // [total c / n, total (c + 1) / n) of that line: as many CTAs as are on the GPU at a time, each with the same
-// weight whatever the lengths, which only the device knows.  The first kFixed of a unit are no steps (a batch of 32
-// sequences up to 16384 keys: kFixed 6 50 us, 12 38, 20 34.5, 30 35.7).
-// kLeast: the weight that is worth a CTA (a step of each warp).  kMostParts: CTAs a unit, on average, since one CTA of
-// the join reads all its parts (65536 keys of one KV head: 608 parts 41 us, 128 19 us).
+// weight whatever the lengths, which only the device knows.  The first kFixed of a unit are no steps.  A batch of 32
+// sequences of 64 to 16384 keys (120895 in all), us with kFixed 6 / 12 / 20 / 30:
+//   heads of 64 (32 / 8)   bf16 forward 50.0 41.1 40.4 40.6   gradient 64.9 52.5 51.3 51.8
+//   heads of 128 (32 / 8)  float32 forward 71.4 59.2 57.5 57.4   gradient 89.9 76.3 74.0 76.5
+//   heads of 256 (16 / 4)  float32 forward 76.5 64.0 55.1 55.4   gradient 94.0 79.5 68.6 70.3   bf16 forward 93.4 76.7 63.1 57.8
+// kLeast: the weight that is worth a CTA; where it lies in a unit's first kFixed that CTA has nothing to do (1024 keys:
+// weight 84, 21 CTAs, 16 of them with steps).  kMostParts: CTAs a unit, on average over the units, since one CTA of the join
+// reads all its parts (65536 keys of one KV head: 608 parts 41 us, 128 19.6 us).  Among shorter sequences a long one of
+// few KV heads still gets more than that (beside four of 200 keys: 40 us).
 constexpr int kFixed = 20, kLeast = 4, kMostParts = 128;
 
 __device__ __forceinline__ int64_t steps_of(int len) { return (len + kStep - 1) / kStep; }
@@ -320,9 +327,8 @@ __global__ void __launch_bounds__(kWarps * 32, HD <= 128 ? 4 : 2) kv8_attn_kerne
         const float *scales = reinterpret_cast<const float *>(st + 2 * kStep * HD);
         const uint32_t mask = *reinterpret_cast<const uint32_t *>(st + 2 * kStep * HD + 128);
 
-        // ---- logits (and dp): columns are keys
-        // (the gradient's rows of q and of d_ctx have sums of their own: 0 times a value that is NaN is NaN, and the
-        // logits do not depend on the values)
+        // ---- logits (and dp): columns are keys.  The gradient's rows of q and of d_ctx have sums of their own: 0 times a
+        // value that is NaN is NaN, and the logits do not depend on the values
         float cf[2][4], part[2][2][4] = {};                    // [chain][tile of 8 keys]: two chains of products at least
 #pragma unroll
         for (int c = 0; c < HD / 64; ++c)

@@ -15,8 +15,9 @@
 // are joined in a fixed order by a second kernel.
 // What bounds it: an accumulator is in use from its MMA's start until both CTAs have read it out, about 1700 cycles
 // (MMA 260 to 400, commit to the readers 400, reading 350, arrival to the next MMA 500), and two k blocks fill the
-// tensor memory: 830 cycles a k block where the MMAs need 512.  2048 x 9728 x 2560: 54.5 us (1.87 PFLOP/s), of which 33 us
-// are the 76 k blocks of the whole tiles, 5 us the start and first blocks, 5 us the results' way out, 6 us the shared tiles' join.
+// tensor memory: 830 cycles a k block where the MMAs need 512.  2048 x 9728 x 2560: 54.3 us (1.88 PFLOP/s), of which
+// about 33 us are the 76 k blocks of the whole tiles, 5 us the start and first blocks, 5 us the results' way out, 6 us the
+// shared tiles' join; the rest is not told apart.
 // Measured on the way there, same sizes: MMAs issued by a lane on its own 108 us and a release arrival of cluster scope
 // (it waits for the scales' loads) on top; one issuer and two accumulators of 256 columns 57 us; eight warps for the
 // sums with 128 columns each 62 to 71 us; waits that spin 71 us.
@@ -25,7 +26,8 @@
 // (m16n8k32), straight from global memory: the 128 columns of a block may be summed in any order, so a lane's
 // 16 consecutive bytes of W and of dY serve as the operands' registers as they are.  The warps of a CTA, and
 // the CTAs of a cluster, share the columns of 16 rows and add up through shared memory in a fixed order.
-// 1 x 9728 x 2560: 9.1 us (25 MB: 2.7 TB/s; launch, one round of loads, the sums through the cluster).
+// 1 x 9728 x 2560: 8.9 us (25 MB: 2.8 TB/s; launch, one or two rounds of loads, the sums through the cluster).  Five CTAs an
+// SM leave 48 registers, of which 112 bytes a thread go to local memory.  8 x 9728 x 2560: 10.0 us.
 #include <cuda.h>
 
 #include <algorithm>
@@ -40,7 +42,7 @@ namespace tlb {
 
 namespace {
 
-constexpr int kFewRows = 8;             // from nine on the tensor cores win: 2560 x 9728, 16 rows 15 us against 22
+constexpr int kFewRows = 8;             // from nine on the tensor cores win: 2560 x 9728, 16 rows 14 us against 22
 constexpr int64_t kMost = int64_t(1) << 24;
 
 // ------------------------------------------------------------------ results
